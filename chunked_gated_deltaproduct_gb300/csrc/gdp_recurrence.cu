@@ -1,0 +1,248 @@
+// gdp_recurrence.cu -- the gated linear recurrence: packed sequences, backward pass, one-token step
+// (gdp_layer.h).
+//
+// h_t = a_t h_{t-1} + b_t per channel.  One thread walks one channel of one sequence; neighbouring
+// threads hold neighbouring channels, so every row access is one run of memory.
+#include "gdp_layer.cuh"
+
+namespace gdp {
+namespace layer {
+namespace {
+
+constexpr int kThreads = 128;
+
+struct RecProblem {
+  const void *x, *g;
+  int64_t x_st, g_st;
+  void *h;
+  const void *cu;
+  int cu64;
+  int64_t T, N, C;
+  const float *init;
+  float *fin;
+  float *cache;
+  const int32_t *slots;
+  int64_t num_slots;
+  uint32_t *status;
+  int x_type, g_type, gate;
+};
+
+struct RecBwdProblem {
+  const void *g, *x, *h, *dout;
+  int64_t g_st, x_st, h_st, dout_st;
+  const int8_t *codes;
+  const float *scales;
+  int64_t group;
+  const void *cu;
+  int cu64;
+  int64_t T, N, C;
+  const float *init, *dfin;
+  void *dx, *dg;
+  float *dinit;
+  uint32_t *status;
+  int x_type, g_type, gate;
+};
+
+__device__ __forceinline__ float load_any(const void *p, int64_t i, int type) {
+  if (type == GDP_DTYPE_F32) return static_cast<const float *>(p)[i];
+  if (type == GDP_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+  return __half2float(static_cast<const __half *>(p)[i]);
+}
+__device__ __forceinline__ void store_any(void *p, int64_t i, int type, float v) {
+  if (type == GDP_DTYPE_F32) static_cast<float *>(p)[i] = v;
+  else if (type == GDP_DTYPE_BF16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+  else static_cast<__half *>(p)[i] = __float2half_rn(v);
+}
+__device__ __forceinline__ void gate_any(int gate, float g, float *a, float *f) {
+  if (gate == GDP_GATE_LOG) gate_eval<GDP_GATE_LOG>(g, a, f);
+  else if (gate == GDP_GATE_ALPHA) gate_eval<GDP_GATE_ALPHA>(g, a, f);
+  else gate_eval<GDP_GATE_SIGMOID>(g, a, f);
+}
+
+// The state row of sequence i: where it is read (NULL: zero) and written (NULL: nowhere).
+__device__ __forceinline__ void state_rows(const RecProblem &p, int64_t i, bool report, const float **src, float **dst) {
+  *src = p.init ? p.init + i * p.C : nullptr;
+  *dst = p.fin ? p.fin + i * p.C : nullptr;
+  if (p.cache) {
+    int64_t slot = p.slots[i];
+    if (slot < -1 || slot >= p.num_slots) {
+      if (report) set_status(p.status, GDP_DEV_ERR_SLOT);
+      slot = -1;
+    }
+    *src = *dst = slot >= 0 ? p.cache + slot * p.C : nullptr;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) gdp_rec_fwd_kernel(RecProblem p, int step) {
+  const int64_t i = blockIdx.x, c = (int64_t)blockIdx.y * kThreads + threadIdx.x;
+  int64_t bos = i, len = 1;
+  if (!step && (!seq_bounds(p.cu, p.cu64, p.T, i, &bos, &len) || (i == 0 && bos != 0)) && threadIdx.x == 0)
+    set_status(p.status, GDP_DEV_ERR_CU_SEQLENS);
+  if (c >= p.C) return;
+  const float *src;
+  float *dst;
+  state_rows(p, i, c == 0, &src, &dst);
+  float h = src ? src[c] : 0.f;
+  for (int64_t t = bos; t < bos + len; ++t) {
+    float a, f;
+    gate_any(p.gate, load_any(p.g, t * p.g_st + c, p.g_type), &a, &f);
+    h = fmaf(a, h, f * load_any(p.x, t * p.x_st + c, p.x_type));
+    store_any(p.h, t * p.C + c, p.x_type, h);
+  }
+  if (dst) dst[c] = h;
+}
+
+__global__ void __launch_bounds__(kThreads) gdp_rec_bwd_kernel(RecBwdProblem p) {
+  const int64_t i = blockIdx.x, c = (int64_t)blockIdx.y * kThreads + threadIdx.x;
+  int64_t bos, len;
+  if ((!seq_bounds(p.cu, p.cu64, p.T, i, &bos, &len) || (i == 0 && bos != 0)) && threadIdx.x == 0)
+    set_status(p.status, GDP_DEV_ERR_CU_SEQLENS);
+  if (c >= p.C) return;
+  const int64_t blocks = (p.group + kBlock - 1) / kBlock, per_row = p.codes ? p.C / p.group * blocks : 0;
+  const int64_t block = p.codes ? c / p.group * blocks + c % p.group / kBlock : 0;
+  float e = p.dfin ? p.dfin[i * p.C + c] : 0.f;  // a_{t+1} D_{t+1}
+  for (int64_t t = bos + len - 1; t >= bos; --t) {
+    float a, f, prev;
+    gate_any(p.gate, load_any(p.g, t * p.g_st + c, p.g_type), &a, &f);
+    if (t == bos) prev = p.init ? p.init[i * p.C + c] : 0.f;
+    else if (p.codes) prev = p.codes[(t - 1) * p.C + c] * p.scales[(t - 1) * per_row + block];
+    else prev = load_any(p.h, (t - 1) * p.h_st + c, p.x_type);
+    const float d = load_any(p.dout, t * p.dout_st + c, p.x_type) + e;
+    e = a * d;
+    float dg = d * prev;
+    if (p.gate == GDP_GATE_LOG) dg = e * prev;
+    if (p.gate == GDP_GATE_SIGMOID) dg = f * e * (prev - load_any(p.x, t * p.x_st + c, p.x_type));
+    store_any(p.dx, t * p.C + c, p.x_type, f * d);
+    store_any(p.dg, t * p.C + c, p.g_type, dg);
+  }
+  if (p.dinit) p.dinit[i * p.C + c] = e;
+}
+
+gdp_status check_shape(int64_t T, int64_t N, int64_t C, int x_type, int g_type, int gate) {
+  if (T < 0 || N < 0 || C < 1) return fail(GDP_ERR_INVALID_ARG, "T >= 0, N >= 0 and C >= 1 are required");
+  if (T > INT32_MAX || N > INT32_MAX || C > (1 << 20)) return fail(GDP_ERR_UNSUPPORTED, "T and N below 2^31, C up to 2^20");
+  if (!dtype_ok(x_type)) return fail(GDP_ERR_UNSUPPORTED, "x_dtype must be GDP_DTYPE_BF16, GDP_DTYPE_F16 or GDP_DTYPE_F32");
+  if (g_type != x_type && g_type != GDP_DTYPE_F32) return fail(GDP_ERR_UNSUPPORTED, "g_dtype must be x_dtype or GDP_DTYPE_F32");
+  if (gate != GDP_GATE_LOG && gate != GDP_GATE_ALPHA && gate != GDP_GATE_SIGMOID)
+    return fail(GDP_ERR_INVALID_ARG, "gate must be GDP_GATE_LOG, GDP_GATE_ALPHA or GDP_GATE_SIGMOID");
+  return GDP_OK;
+}
+
+// A [T, C] tensor: given where it has elements, aligned to its elements, rows at least C apart.
+gdp_status check_rows(const void *p, int64_t stride, int64_t T, int64_t C, int type, const char *name) {
+  const size_t es = dtype_size(type);
+  if (T > 0 && !p) {
+    set_last_error("%s is required", name);
+    return GDP_ERR_INVALID_ARG;
+  }
+  if (!aligned(p, es) || (T > 1 && stride < C)) {
+    set_last_error("%s must be aligned to its elements, its rows at least C elements apart", name);
+    return GDP_ERR_INVALID_ARG;
+  }
+  return GDP_OK;
+}
+
+gdp_status check_workspace(const void *ws, size_t given, int64_t T, int64_t C) {
+  const size_t need = gdp_linear_recurrence_workspace_bytes(T, C);
+  if (need && (!ws || !aligned(ws, 256) || given < need))
+    return fail(GDP_ERR_WORKSPACE, "workspace missing, not 256-byte aligned or smaller than gdp_linear_recurrence_workspace_bytes");
+  return GDP_OK;
+}
+
+gdp_status resolve(const gdp_recurrence_args *a, bool step, RecProblem *p) {
+  set_last_error("");
+  if (!a) return fail(GDP_ERR_INVALID_ARG, "args is NULL");
+  gdp_status st = check_shape(a->T, a->N, a->C, a->x_dtype, a->g_dtype, a->gate);
+  if (st != GDP_OK) return st;
+  if (step && a->T != a->N) return fail(GDP_ERR_INVALID_ARG, "decode takes one token per sequence: T == N");
+  if ((st = check_rows(a->x, a->x_stride_t, a->T, a->C, a->x_dtype, "x")) != GDP_OK) return st;
+  if ((st = check_rows(a->g, a->g_stride_t, a->T, a->C, a->g_dtype, "g")) != GDP_OK) return st;
+  if ((st = check_rows(a->output, a->C, a->T, a->C, a->x_dtype, "output")) != GDP_OK) return st;
+  if (!step && !a->cu_seqlens) return fail(GDP_ERR_INVALID_ARG, "cu_seqlens is required");
+  if (!aligned(a->initial_state, 4) || !aligned(a->output_state, 4) || !aligned(a->state, 4) || !aligned(a->state_indices, 4))
+    return fail(GDP_ERR_INVALID_ARG, "state buffers must be 4-byte aligned");
+  if (a->state && (a->initial_state || a->output_state))
+    return fail(GDP_ERR_INVALID_ARG, "the state cache excludes initial_state and output_state");
+  if (a->state && (!a->state_indices || a->num_slots < 1))
+    return fail(GDP_ERR_INVALID_ARG, "the state cache needs state_indices and num_slots >= 1");
+  if (partly_overlap(a->initial_state, a->output_state, sizeof(float) * (size_t)a->N * (size_t)a->C))
+    return fail(GDP_ERR_ALIAS, "output_state partly overlaps initial_state");
+  *p = RecProblem{a->x, a->g, a->x_stride_t, a->g_stride_t, a->output, a->cu_seqlens, a->cu_seqlens_int64 != 0, a->T, a->N, a->C,
+                  a->initial_state, a->output_state, a->state, a->state_indices, a->num_slots, a->device_status,
+                  a->x_dtype, a->g_dtype, a->gate};
+  return GDP_OK;
+}
+
+}  // namespace
+}  // namespace layer
+}  // namespace gdp
+
+GDP_EXPORT size_t gdp_linear_recurrence_workspace_bytes(int64_t T, int64_t C) {
+  if (T < 0 || C < 1 || T > INT32_MAX || C > (1 << 20)) return 0;
+  return 256;
+}
+
+GDP_EXPORT gdp_status gdp_linear_recurrence(const gdp_recurrence_args *args, void *stream) {
+  using namespace gdp::layer;
+  RecProblem p;
+  gdp_status st = resolve(args, false, &p);
+  if (st == GDP_OK) st = check_workspace(args->workspace, args->workspace_bytes, p.T, p.C);
+  if (st != GDP_OK || p.N == 0) return st;
+  const dim3 grid((unsigned)p.N, (unsigned)((p.C + kThreads - 1) / kThreads));
+  gdp_rec_fwd_kernel<<<grid, kThreads, 0, (cudaStream_t)stream>>>(p, 0);
+  return launch_status("recurrence kernel");
+}
+
+GDP_EXPORT gdp_status gdp_linear_recurrence_decode(const gdp_recurrence_args *args, void *stream) {
+  using namespace gdp::layer;
+  RecProblem p;
+  const gdp_status st = resolve(args, true, &p);
+  if (st != GDP_OK || p.N == 0) return st;
+  const dim3 grid((unsigned)p.N, (unsigned)((p.C + kThreads - 1) / kThreads));
+  gdp_rec_fwd_kernel<<<grid, kThreads, 0, (cudaStream_t)stream>>>(p, 1);
+  return launch_status("recurrence step kernel");
+}
+
+GDP_EXPORT gdp_status gdp_linear_recurrence_backward(const gdp_recurrence_backward_args *a, void *stream) {
+  using namespace gdp::layer;
+  gdp::set_last_error("");
+  if (!a) return fail(GDP_ERR_INVALID_ARG, "args is NULL");
+  gdp_status st = check_shape(a->T, a->N, a->C, a->x_dtype, a->g_dtype, a->gate);
+  if (st != GDP_OK) return st;
+  if ((st = check_rows(a->g, a->g_stride_t, a->T, a->C, a->g_dtype, "g")) != GDP_OK) return st;
+  if ((st = check_rows(a->d_output, a->d_output_stride_t, a->T, a->C, a->x_dtype, "d_output")) != GDP_OK) return st;
+  if (a->gate == GDP_GATE_SIGMOID && (st = check_rows(a->x, a->x_stride_t, a->T, a->C, a->x_dtype, "x")) != GDP_OK) return st;
+  if ((st = check_rows(a->dx, a->C, a->T, a->C, a->x_dtype, "dx")) != GDP_OK) return st;
+  if ((st = check_rows(a->dg, a->C, a->T, a->C, a->g_dtype, "dg")) != GDP_OK) return st;
+  if (a->T > 0 && (a->h != nullptr) == (a->h_codes != nullptr))
+    return fail(GDP_ERR_INVALID_ARG, "exactly one of h and h_codes is required");
+  if (a->h && (st = check_rows(a->h, a->h_stride_t, a->T, a->C, a->x_dtype, "h")) != GDP_OK) return st;
+  if (a->h_codes && (!a->h_scales || !aligned(a->h_scales, 4) || a->h_group < 1 || a->C % a->h_group != 0))
+    return fail(GDP_ERR_INVALID_ARG, "h_codes needs h_scales and an h_group that divides C");
+  if (!a->cu_seqlens) return fail(GDP_ERR_INVALID_ARG, "cu_seqlens is required");
+  if (!aligned(a->initial_state, 4) || !aligned(a->d_final_state, 4) || !aligned(a->d_initial_state, 4))
+    return fail(GDP_ERR_INVALID_ARG, "state buffers must be 4-byte aligned");
+  const size_t bytes = sizeof(float) * (size_t)a->N * (size_t)a->C;
+  if (partly_overlap(a->d_final_state, a->d_initial_state, bytes) || partly_overlap(a->initial_state, a->d_initial_state, bytes) ||
+      (a->initial_state && a->initial_state == a->d_initial_state))
+    return fail(GDP_ERR_ALIAS, "d_initial_state overlaps initial_state or partly overlaps d_final_state");
+  if ((st = check_workspace(a->workspace, a->workspace_bytes, a->T, a->C)) != GDP_OK) return st;
+  if (a->N == 0) return GDP_OK;
+  RecBwdProblem p{a->g, a->x, a->h, a->d_output, a->g_stride_t, a->x_stride_t, a->h_stride_t, a->d_output_stride_t,
+                  a->h_codes, a->h_scales, a->h_group, a->cu_seqlens, a->cu_seqlens_int64 != 0, a->T, a->N, a->C,
+                  a->initial_state, a->d_final_state, a->dx, a->dg, a->d_initial_state, a->device_status,
+                  a->x_dtype, a->g_dtype, a->gate};
+  const dim3 grid((unsigned)p.N, (unsigned)((p.C + kThreads - 1) / kThreads));
+  gdp_rec_bwd_kernel<<<grid, kThreads, 0, (cudaStream_t)stream>>>(p);
+  return launch_status("recurrence backward kernel");
+}
+
+GDP_EXPORT size_t gdp_layer_args_size(int which) {
+  switch (which) {
+    case 0: return sizeof(gdp_recurrence_args);
+    case 1: return sizeof(gdp_recurrence_backward_args);
+    case 2: return sizeof(gdp_group_norm_args);
+    case 3: return sizeof(gdp_group_norm_backward_args);
+    default: return 0;
+  }
+}
