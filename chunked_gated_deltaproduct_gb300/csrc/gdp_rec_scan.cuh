@@ -1,0 +1,407 @@
+// gdp_rec_scan.cuh -- what the forward and the backward kernel of the gated linear recurrence share.
+//
+// A run of tokens maps the entering state h to A h + B (A the product of its decays, B its end state
+// from zero), so tiles of time are worked on side by side.  The packed rows [0, T) are cut into tiles
+// of 8 S tokens x 64 channels whatever the sequences' lengths (a sequence's first token simply
+// replaces the state).  A cluster of CTAs owns 64 channels for all of time: in step n its CTA k works
+// on tile n * cluster + k.  In a CTA,
+//   - a loading warp brings tiles ahead into a ring of shared-memory stages (TMA, or word-wise
+//     asynchronous copies for rows that are not 16-byte aligned) and finds the sequences in them;
+//   - eight warps of S tokens each run tile n + 1 from zero, which gives each warp's (A, B), and then
+//     tile n from its entering states, which gives the outputs;
+//   - a posting warp folds the eight (A, B) and writes the tile's (A, B) into every CTA of the
+//     cluster (distributed shared memory, completing on the reader's barrier);
+//   - a folding warp takes the cluster's tiles in order of time from the state it carries: the eight
+//     warps' entering states, and the state that enters the next step.
+// Every value comes from the same operations in the same order on every run.  Nothing of it passes
+// through global memory: a chain through flags there took 5 us a hop, which 6.8 TB/s would have to
+// cover with 34 MB of waiting tiles (measured 1.97 ms at 65536 x 4096; see the kernels for now).
+// Every wait is bounded.
+#pragma once
+
+#include <cuda.h>
+
+#include "gdp_layer.cuh"
+#include "gdp_sm100.cuh"
+
+namespace gdp {
+namespace layer {
+
+constexpr int kSlice = 64;        // channels of a tile: two per lane
+constexpr int kScanWarps = 8;     // warps that compute
+constexpr int kLoadWarp = kScanWarps, kPostWarp = kScanWarps + 1, kFoldWarp = kScanWarps + 2;
+constexpr int kScanThreads = 32 * (kScanWarps + 3);
+constexpr int kMailSlots = 4;     // steps whose posts may be under way at once (see fold_steps)
+
+struct ScanShape {
+  const void *cu;
+  int cu64;
+  int64_t T, N, C;
+  int rows, slices;  // tiles in time and in channels
+  int raw;           // word-wise copies instead of TMA
+  const int32_t *slots;
+  int64_t num_slots;
+  uint32_t *status;
+  int cluster;       // CTAs that share a slice's channels
+  uint64_t limit_ns;
+  int withhold;      // test of the failure path: the first tile's (A, B) is not posted
+};
+
+// Sequences of one tile, found by the loading warp.
+template <int S>
+struct TileMeta {
+  int lo, hi;                     // rows of the tile that belong to sequences
+  uint32_t starts[kScanWarps], ends[kScanWarps];  // per warp: its tokens that begin / end a sequence
+  int start_row[kScanWarps * S], end_row[kScanWarps * S];  // state row of that sequence, -1: none
+};
+
+template <typename T>
+constexpr int tile_pitch(bool raw) { return kSlice * (int)sizeof(T) + (raw && sizeof(T) < 4 ? 4 : 0); }
+// Bytes a tensor's tile takes in a stage.
+template <typename T>
+constexpr int tile_bytes(int rows, bool raw) { return (rows * tile_pitch<T>(raw) + 127) / 128 * 128; }
+
+// One input tensor [T][C]: its address for the word-wise copies.
+struct RowSource {
+  const void *base;
+  int64_t stride;  // elements
+};
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(sm100::smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+// Rows [t0, t0 + rows) x channels [c0, c0 + 64) of src by 4-byte copies: the words that hold a wanted
+// byte.  A row that does not start on a word keeps its offset within the word (raw_offset); bytes past
+// the row's last channel are not read.  Rows outside [0, T) become zeros.
+template <typename T>
+__device__ __forceinline__ void load_words(unsigned char *tile, const RowSource &src, int64_t t0, int rows, int64_t T_, int64_t c0,
+                                           int64_t C, int lane) {
+  constexpr int kWords = tile_pitch<T>(true) / 4;
+  const int wanted = (int)min((int64_t)kSlice, C - c0) * (int)sizeof(T);
+  for (int i = lane; i < rows * kWords; i += 32) {
+    const int r = i / kWords, w = i % kWords;
+    const int64_t t = t0 + r;
+    const bool in = t >= 0 && t < T_;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(src.base) + (uintptr_t)(((in ? t : 0) * src.stride + c0) * (int64_t)sizeof(T));
+    const int off = (int)(at & 3u), left = in ? off + wanted - 4 * w : 0;
+    const uintptr_t word = (at & ~(uintptr_t)3) + (left > 0 ? 4u * w : 0u);
+    cp_async4(sm100::smem_u32(tile + r * tile_pitch<T>(true) + 4 * w), reinterpret_cast<const void *>(word),
+              (uint32_t)max(0, min(4, left)));
+  }
+}
+// Offset of row t's first channel within its word.
+template <typename T>
+__device__ __forceinline__ int raw_offset(const RowSource &src, int64_t t, int64_t c0) {
+  return sizeof(T) < 4 ? (int)((reinterpret_cast<uintptr_t>(src.base) + (uintptr_t)((t * src.stride + c0) * (int64_t)sizeof(T))) & 3u) : 0;
+}
+
+// The lane's two channels of tile row r, as fp32.
+template <typename T, bool RAW>
+__device__ __forceinline__ float2 read_pair(const unsigned char *tile, int r, int lane, int offset) {
+  if constexpr (sizeof(T) == 4) {
+    return *reinterpret_cast<const float2 *>(tile + r * tile_pitch<T>(false) + lane * 8);
+  } else {
+    T v[2];
+    if constexpr (RAW) {
+      const T *p = reinterpret_cast<const T *>(tile + r * tile_pitch<T>(true) + offset) + 2 * lane;
+      v[0] = p[0];
+      v[1] = p[1];
+    } else {
+      *reinterpret_cast<uint32_t *>(v) = *reinterpret_cast<const uint32_t *>(tile + r * tile_pitch<T>(false) + lane * 4);
+    }
+    return make_float2(to_f32(v[0]), to_f32(v[1]));
+  }
+}
+
+// Keeps two fp32 values of the lane in the place of its pairs of two tensors' tiles (each lane only
+// ever reads its own pairs), and reads them back.
+template <typename T, bool RAW>
+__device__ __forceinline__ void put_bits(unsigned char *tile, int r, int lane, int offset, float v) {
+  unsigned char *p = tile + r * tile_pitch<T>(RAW) + offset + lane * 2 * (int)sizeof(T);
+  const uint32_t b = __float_as_uint(v);
+  if constexpr (RAW && sizeof(T) < 4) {
+    reinterpret_cast<uint16_t *>(p)[0] = (uint16_t)b;
+    reinterpret_cast<uint16_t *>(p)[1] = (uint16_t)(b >> 16);
+  } else {
+    *reinterpret_cast<uint32_t *>(p) = b;
+  }
+}
+template <typename T, bool RAW>
+__device__ __forceinline__ float get_bits(const unsigned char *tile, int r, int lane, int offset) {
+  const unsigned char *p = tile + r * tile_pitch<T>(RAW) + offset + lane * 2 * (int)sizeof(T);
+  if constexpr (RAW && sizeof(T) < 4)
+    return __uint_as_float(reinterpret_cast<const uint16_t *>(p)[0] | ((uint32_t) reinterpret_cast<const uint16_t *>(p)[1] << 16));
+  return *reinterpret_cast<const float *>(p);
+}
+
+template <typename T>
+__device__ __forceinline__ void write_pair(T *p, float2 v, bool both, bool vec) {
+  if (vec) {  // even channel count, aligned base: one store
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float2 *>(p) = v;
+    } else {
+      T o[2] = {from_f32<T>(v.x), from_f32<T>(v.y)};
+      *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<const uint32_t *>(o);
+    }
+  } else {
+    p[0] = from_f32<T>(v.x);
+    if (both) p[1] = from_f32<T>(v.y);
+  }
+}
+// The lane's two channels of a state row (channels past C read as zero / are not written).
+__device__ __forceinline__ float2 read_state(const float *p, int row, int64_t C, int64_t c) {
+  if (!p || row < 0) return make_float2(0.f, 0.f);
+  const float *q = p + (int64_t)row * C + c;
+  return make_float2(c < C ? q[0] : 0.f, c + 1 < C ? q[1] : 0.f);
+}
+__device__ __forceinline__ void write_state(float *p, int row, int64_t C, int64_t c, float2 v) {
+  if (!p || row < 0) return;
+  float *q = p + (int64_t)row * C + c;
+  if (c < C) q[0] = v.x;
+  if (c + 1 < C) q[1] = v.y;
+}
+
+// Whole warp: the sequences that begin or end in tile rows [t0, t0 + 8 S), into m; those without
+// tokens at a position in the tile (or at T, for the last tile in time) pass their state from `from`
+// to `to` right away.
+template <int S>
+__device__ void find_sequences(const ScanShape &p, TileMeta<S> &m, int64_t t0, bool last, int64_t c0, const float *from, float *to,
+                               int lane) {
+  constexpr int kTile = kScanWarps * S;
+  const int64_t t1 = t0 + kTile;
+  if (lane < kScanWarps) m.starts[lane] = m.ends[lane] = 0u;
+  __syncwarp();
+  // the first sequence that ends at or after t0, 32 probes a round
+  int64_t lo = 0, hi = p.N;
+  while (lo < hi) {
+    const int64_t chunk = (hi - lo + 31) / 32, at = lo + (lane + 1) * chunk - 1;
+    const uint32_t hit = __ballot_sync(0xffffffffu, at >= hi || load_cu(p.cu, p.cu64, at + 1) >= t0);
+    const int f = hit ? __ffs(hit) - 1 : 32;
+    hi = min(hi, lo + (f + 1) * chunk - 1);
+    lo = min(hi, lo + f * chunk);
+  }
+  for (int64_t base = lo; base < p.N; base += 32) {
+    const int64_t s = base + lane;
+    int64_t b = 0, e = 0;
+    bool ok = false;
+    if (s < p.N) {
+      b = load_cu(p.cu, p.cu64, s);
+      e = load_cu(p.cu, p.cu64, s + 1);
+      ok = b >= 0 && b <= e && e <= p.T;
+    }
+    const bool begins = ok && b < e && b >= t0 && b < t1, ends = ok && b < e && e > t0 && e <= t1;
+    const bool none = ok && b == e && b >= t0 && (b < t1 || last);
+    int row = (int)s;
+    if (p.slots && (begins || ends)) {
+      row = p.slots[s];
+      if (row < -1 || row >= p.num_slots) {
+        if (c0 == 0) set_status(p.status, GDP_DEV_ERR_SLOT);
+        row = -1;
+      }
+    }
+    if (begins) {
+      m.start_row[b - t0] = row;
+      atomicOr(&m.starts[(b - t0) / S], 1u << ((b - t0) % S));
+    }
+    if (ends) {
+      m.end_row[e - 1 - t0] = row;
+      atomicOr(&m.ends[(e - 1 - t0) / S], 1u << ((e - 1 - t0) % S));
+    }
+    if (to) {
+      for (uint32_t left = __ballot_sync(0xffffffffu, none); left; left &= left - 1) {
+        const int at = (int)(base + __ffs(left) - 1);
+        write_state(to, at, p.C, c0 + 2 * lane, read_state(from, at, p.C, c0 + 2 * lane));
+      }
+    }
+    if (__any_sync(0xffffffffu, s < p.N && b >= t1)) break;
+  }
+}
+
+// cu_seqlens ascending from 0 to at most T (any number of threads, `first` of `step`).
+__device__ __forceinline__ void check_sequences(const void *cu, int cu64, int64_t N, int64_t T, uint32_t *status, int64_t first,
+                                                int64_t step) {
+  for (int64_t s = first; s < N; s += step) {
+    const int64_t b = load_cu(cu, cu64, s), e = load_cu(cu, cu64, s + 1);
+    if (b > e || b < 0 || e > T || (s == 0 && b != 0)) set_status(status, GDP_DEV_ERR_CU_SEQLENS);
+  }
+}
+
+// ---- the chain through the cluster ----
+// Per-CTA shared memory of the chain: parts (A0, A1, B0, B1 of a lane's two channels) and entering
+// states per warp, two tiles of each; mail, four steps of one part per CTA of the cluster.
+struct Chain {
+  float4 *parts;    // [2][kScanWarps][32]
+  float2 *enter;    // [2][kScanWarps][32]
+  float4 *mail;     // [kMailSlots][cluster][32]
+  uint64_t *parts_full, *enter_full, *mail_full;  // [2], [2], [kMailSlots]
+  static constexpr int parts_bytes = 2 * kScanWarps * 32 * 16, enter_bytes = 2 * kScanWarps * 32 * 8;
+  __host__ __device__ static constexpr int mail_bytes(int cluster) { return kMailSlots * cluster * 32 * 16; }
+  static constexpr int bars = 2 + 2 + kMailSlots;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t in_rank(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void post16(uint32_t addr, float4 v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+               "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)), "r"(__float_as_uint(v.w)), "r"(bar)
+               : "memory");
+}
+// In the place of A where a sequence begins in the tile, so that its end state is B whatever enters
+// (arithmetic never gives this NaN: its own has the sign bit clear).
+constexpr uint32_t kCut = 0xffffffffu;
+
+// A wait on a full or empty barrier: bounded; once one ran out in the CTA the others return at once
+// and the kernel runs to its end with undefined outputs (every copy it issued is still waited for).
+__device__ __forceinline__ void ring_wait(uint64_t *bar, uint32_t parity, volatile int *gave_up, uint32_t *status, uint64_t limit_ns) {
+  if (!sm100::mbar_wait_or_abort(bar, parity, gave_up, limit_ns)) set_status(status, GDP_DEV_ERR_TIMEOUT);
+}
+
+// The posting warp: after the eight warps left tile n's parts.
+template <int S, int META>
+__device__ __forceinline__ void post_steps(const ScanShape &p, const Chain &ch, const TileMeta<S> *metas, int steps, int lane,
+                                           volatile int *gave_up) {
+  const uint32_t rank = cluster_rank();
+  for (int n = 0; n < steps; ++n) {
+    ring_wait(&ch.parts_full[n & 1], (n >> 1) & 1, gave_up, p.status, p.limit_ns);
+    const TileMeta<S> &m = metas[n % META];
+    const float4 *parts = ch.parts + (n & 1) * kScanWarps * 32;
+    float4 own = make_float4(1.f, 1.f, 0.f, 0.f);
+    bool cut = false;
+#pragma unroll
+    for (int w = 0; w < kScanWarps; ++w) {
+      const float4 q = parts[w * 32 + lane];
+      const bool fresh = m.starts[w] != 0u;
+      cut |= fresh;
+      own = make_float4(own.x * q.x, own.y * q.y, fresh ? q.z : fmaf(q.x, own.z, q.z), fresh ? q.w : fmaf(q.y, own.w, q.w));
+    }
+    if (cut) own.x = __uint_as_float(kCut);
+    const uint32_t slot = n % kMailSlots, to = sm100::smem_u32(ch.mail + ((int)slot * p.cluster + (int)rank) * 32 + lane);
+    const uint32_t bar = sm100::smem_u32(&ch.mail_full[slot]);
+    if (p.withhold && n == 0 && rank == 0) continue;
+    for (int k = 0; k < p.cluster; ++k) post16(in_rank(to, k), own, in_rank(bar, k));
+  }
+}
+
+// The folding warp.  Mail slots: a CTA posts step n + 4 only after its own step n + 2 came through,
+// hence after this CTA posted n + 2, hence (its warps run tile n before tile n + 2 from zero) after
+// this warp has read step n: four slots suffice.
+template <int S, int META>
+__device__ __forceinline__ void fold_steps(const ScanShape &p, const Chain &ch, const TileMeta<S> *metas, int steps, int lane,
+                                           volatile int *gave_up) {
+  const int rank = (int)cluster_rank();
+  const uint32_t bytes = (uint32_t)p.cluster * 512u;
+  if (lane == 0)
+    for (int i = 0; i < kMailSlots; ++i) sm100::mbar_arrive_expect_tx(&ch.mail_full[i], bytes);
+  float2 h = make_float2(0.f, 0.f);  // the state entering the step
+  for (int n = 0; n < steps; ++n) {
+    const int slot = n % kMailSlots;
+    ring_wait(&ch.mail_full[slot], (n / kMailSlots) & 1, gave_up, p.status, p.limit_ns);
+    const float4 *mail = ch.mail + slot * p.cluster * 32;
+    float2 e = h;
+    for (int k = 0; k < p.cluster; ++k) {
+      const float4 q = mail[k * 32 + lane];
+      if (k == rank) e = h;
+      h = __float_as_uint(q.x) == kCut ? make_float2(q.z, q.w) : make_float2(fmaf(q.x, h.x, q.z), fmaf(q.y, h.y, q.w));
+    }
+    __syncwarp();
+    if (lane == 0) sm100::mbar_arrive_expect_tx(&ch.mail_full[slot], bytes);  // for step n + 4
+    const TileMeta<S> &m = metas[n % META];
+    const float4 *parts = ch.parts + (n & 1) * kScanWarps * 32;
+    float2 *enter = ch.enter + (n & 1) * kScanWarps * 32;
+#pragma unroll
+    for (int w = 0; w < kScanWarps; ++w) {
+      enter[w * 32 + lane] = e;
+      const float4 q = parts[w * 32 + lane];
+      e = m.starts[w] ? make_float2(q.z, q.w) : make_float2(fmaf(q.x, e.x, q.z), fmaf(q.y, e.y, q.w));
+    }
+    __syncwarp();
+    if (lane == 0) sm100::mbar_arrive(&ch.enter_full[n & 1]);
+  }
+}
+
+struct RecFwd {
+  ScanShape s;
+  RowSource x, g;
+  void *h;
+  const float *from;  // state rows read (initial state or cache)
+  float *to;          // state rows written (final state or cache)
+  int vec_out;
+};
+struct RecBwd {
+  ScanShape s;
+  RowSource g, x, h, dout;
+  RowSource codes;     // int8
+  const float *scales;
+  int64_t group;       // channels of a checkpoint row
+  const float *init, *dfin;
+  void *dx, *dg;
+  float *dinit;
+  int vec_dx, vec_dg;
+};
+
+// Fills s.rows, s.slices, s.cluster and s.raw and launches (gdp_rec_*.cu, by x's type).
+cudaError_t launch_rec_fwd_bf16(RecFwd &p, int g_f32, int gate, cudaStream_t stream);
+cudaError_t launch_rec_fwd_f16(RecFwd &p, int g_f32, int gate, cudaStream_t stream);
+cudaError_t launch_rec_fwd_f32(RecFwd &p, int g_f32, int gate, cudaStream_t stream);
+cudaError_t launch_rec_bwd_bf16(RecBwd &p, int g_f32, int gate, cudaStream_t stream);
+cudaError_t launch_rec_bwd_f16(RecBwd &p, int g_f32, int gate, cudaStream_t stream);
+cudaError_t launch_rec_bwd_f32(RecBwd &p, int g_f32, int gate, cudaStream_t stream);
+
+// CTAs per slice: enough for `per_sm` on every SM, at most one per tile in time and 16 (the largest
+// cluster there is).
+inline int cluster_size(int slices, int rows, int sms, int per_sm) {
+  int k = sms * per_sm / (slices > 0 ? slices : 1);
+  if (k > 16) k = 16;
+  if (k > rows) k = rows;
+  if (k < 1) k = 1;
+  int pow = 1;
+  while (2 * pow <= k) pow *= 2;
+  return pow;
+}
+// Launches slices x cluster CTAs in clusters.
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters(void (*kern)(Params...), int slices, int cluster, int smem, cudaStream_t stream, Args &&...args) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && cluster > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(slices * cluster));
+  cfg.blockDim = dim3(kScanThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<Args &&>(args)...);
+}
+// SMs of the current device.
+int sm_count();
+
+}  // namespace layer
+
+// TMA map of a row-major matrix of 1-, 2- or 4-byte elements, unswizzled boxes of box_cols x box_rows
+// (gdp_tmap.cu; `map` points at a 64-byte aligned CUtensorMap).
+cudaError_t tmap_matrix(void *map, const void *base, int64_t rows, int64_t cols, int64_t stride_bytes, int elem_bytes, int box_cols,
+                        int box_rows);
+}  // namespace gdp

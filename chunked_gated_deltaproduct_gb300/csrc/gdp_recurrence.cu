@@ -3,7 +3,7 @@
 //
 // h_t = a_t h_{t-1} + b_t per channel.  One thread walks one channel of one sequence; neighbouring
 // threads hold neighbouring channels, so every row access is one run of memory.
-#include "gdp_layer.cuh"
+#include "gdp_rec_scan.cuh"
 
 namespace gdp {
 namespace layer {
@@ -142,13 +142,6 @@ gdp_status check_rows(const void *p, int64_t stride, int64_t T, int64_t C, int t
   return GDP_OK;
 }
 
-gdp_status check_workspace(const void *ws, size_t given, int64_t T, int64_t C) {
-  const size_t need = gdp_linear_recurrence_workspace_bytes(T, C);
-  if (need && (!ws || !aligned(ws, 256) || given < need))
-    return fail(GDP_ERR_WORKSPACE, "workspace missing, not 256-byte aligned or smaller than gdp_linear_recurrence_workspace_bytes");
-  return GDP_OK;
-}
-
 gdp_status resolve(const gdp_recurrence_args *a, bool step, RecProblem *p) {
   set_last_error("");
   if (!a) return fail(GDP_ERR_INVALID_ARG, "args is NULL");
@@ -174,23 +167,38 @@ gdp_status resolve(const gdp_recurrence_args *a, bool step, RecProblem *p) {
 }
 
 }  // namespace
+
+int sm_count() {
+  static int counts[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  if (counts[dev] == 0 && cudaDeviceGetAttribute(&counts[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+  return counts[dev];
+}
+
 }  // namespace layer
 }  // namespace gdp
-
-GDP_EXPORT size_t gdp_linear_recurrence_workspace_bytes(int64_t T, int64_t C) {
-  if (T < 0 || C < 1 || T > INT32_MAX || C > (1 << 20)) return 0;
-  return 256;
-}
 
 GDP_EXPORT gdp_status gdp_linear_recurrence(const gdp_recurrence_args *args, void *stream) {
   using namespace gdp::layer;
   RecProblem p;
-  gdp_status st = resolve(args, false, &p);
-  if (st == GDP_OK) st = check_workspace(args->workspace, args->workspace_bytes, p.T, p.C);
+  const gdp_status st = resolve(args, false, &p);
   if (st != GDP_OK || p.N == 0) return st;
-  const dim3 grid((unsigned)p.N, (unsigned)((p.C + kThreads - 1) / kThreads));
-  gdp_rec_fwd_kernel<<<grid, kThreads, 0, (cudaStream_t)stream>>>(p, 0);
-  return launch_status("recurrence kernel");
+  RecFwd f{};
+  f.s.cu = p.cu; f.s.cu64 = p.cu64; f.s.T = p.T; f.s.N = p.N; f.s.C = p.C;
+  f.s.slots = p.cache ? p.slots : nullptr; f.s.num_slots = p.num_slots; f.s.status = p.status;
+  f.s.limit_ns = gdp::sm100::kWaitLimitNs;
+  f.x = {p.x, p.x_st}; f.g = {p.g, p.g_st}; f.h = p.h;
+  f.from = p.cache ? p.cache : p.init;
+  f.to = p.cache ? p.cache : p.fin;
+  f.vec_out = p.C % 2 == 0 && aligned(p.h, 2 * dtype_size(p.x_type));
+  const auto launch = p.x_type == GDP_DTYPE_BF16 ? launch_rec_fwd_bf16 : p.x_type == GDP_DTYPE_F16 ? launch_rec_fwd_f16 : launch_rec_fwd_f32;
+  const cudaError_t e = launch(f, p.g_type == GDP_DTYPE_F32, p.gate, (cudaStream_t)stream);
+  if (e != cudaSuccess) {
+    gdp::set_last_error("recurrence kernel: %s", cudaGetErrorString(e));
+    return GDP_ERR_CUDA;
+  }
+  return GDP_OK;
 }
 
 GDP_EXPORT gdp_status gdp_linear_recurrence_decode(const gdp_recurrence_args *args, void *stream) {
@@ -226,7 +234,6 @@ GDP_EXPORT gdp_status gdp_linear_recurrence_backward(const gdp_recurrence_backwa
   if (partly_overlap(a->d_final_state, a->d_initial_state, bytes) || partly_overlap(a->initial_state, a->d_initial_state, bytes) ||
       (a->initial_state && a->initial_state == a->d_initial_state))
     return fail(GDP_ERR_ALIAS, "d_initial_state overlaps initial_state or partly overlaps d_final_state");
-  if ((st = check_workspace(a->workspace, a->workspace_bytes, a->T, a->C)) != GDP_OK) return st;
   if (a->N == 0) return GDP_OK;
   RecBwdProblem p{a->g, a->x, a->h, a->d_output, a->g_stride_t, a->x_stride_t, a->h_stride_t, a->d_output_stride_t,
                   a->h_codes, a->h_scales, a->h_group, a->cu_seqlens, a->cu_seqlens_int64 != 0, a->T, a->N, a->C,

@@ -71,4 +71,16 @@ cudaError_t tmap_out_rows(void *map, void *base, int64_t T, int H, int V, int bo
                 CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+cudaError_t tmap_matrix(void *map, const void *base, int64_t rows, int64_t cols, int64_t stride_bytes, int elem_bytes, int box_cols,
+                        int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)stride_bytes};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  const CUtensorMapDataType type = elem_bytes == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  return encode(static_cast<CUtensorMap *>(map), type, 2, const_cast<void *>(base), dims, strides, box,
+                CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 }  // namespace gdp

@@ -28,8 +28,7 @@ class GdpRecurrenceArgs(ctypes.Structure):
     _fields_ = [
         ("x", _vp), ("x_stride_t", _i64), ("g", _vp), ("g_stride_t", _i64), ("output", _vp), ("cu_seqlens", _vp),
         ("T", _i64), ("N", _i64), ("C", _i64), ("initial_state", _vp), ("output_state", _vp), ("state", _vp),
-        ("state_indices", _vp), ("num_slots", _i64), ("workspace", _vp), ("workspace_bytes", _sz),
-        ("device_status", _vp), ("cu_seqlens_int64", _int), ("x_dtype", _int), ("g_dtype", _int), ("gate", _int),
+        ("state_indices", _vp), ("num_slots", _i64), ("device_status", _vp), ("cu_seqlens_int64", _int), ("x_dtype", _int), ("g_dtype", _int), ("gate", _int),
     ]
 
 
@@ -39,8 +38,7 @@ class GdpRecurrenceBackwardArgs(ctypes.Structure):
         ("g", _vp), ("g_stride_t", _i64), ("x", _vp), ("x_stride_t", _i64), ("h", _vp), ("h_stride_t", _i64),
         ("h_codes", _vp), ("h_scales", _vp), ("h_group", _i64), ("d_output", _vp), ("d_output_stride_t", _i64),
         ("cu_seqlens", _vp), ("T", _i64), ("N", _i64), ("C", _i64), ("initial_state", _vp), ("d_final_state", _vp),
-        ("dx", _vp), ("dg", _vp), ("d_initial_state", _vp), ("workspace", _vp), ("workspace_bytes", _sz),
-        ("device_status", _vp), ("cu_seqlens_int64", _int), ("x_dtype", _int), ("g_dtype", _int), ("gate", _int),
+        ("dx", _vp), ("dg", _vp), ("d_initial_state", _vp), ("device_status", _vp), ("cu_seqlens_int64", _int), ("x_dtype", _int), ("g_dtype", _int), ("gate", _int),
     ]
 
 
@@ -97,8 +95,6 @@ def _library():
                            ("gdp_group_norm_backward", GdpGroupNormBackwardArgs)):
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = _int, [ctypes.POINTER(args), _vp]
-        lib.gdp_linear_recurrence_workspace_bytes.restype = _sz
-        lib.gdp_linear_recurrence_workspace_bytes.argtypes = [_i64, _i64]
         lib.gdp_group_norm_workspace_bytes.restype = _sz
         lib.gdp_group_norm_workspace_bytes.argtypes = [_i64, _i64, _i64, _int]
         lib.gdp_layer_args_size.restype = _sz
@@ -109,10 +105,6 @@ def _library():
                 raise RuntimeError(f"{args.__name__} layout mismatch between the binding and the library")
         _lib = lib
     return _lib
-
-
-def gdp_linear_recurrence_workspace_bytes(T: int, C: int) -> int:
-    return int(_library().gdp_linear_recurrence_workspace_bytes(T, C))
 
 
 def gdp_group_norm_workspace_bytes(T: int, H: int, D: int, per_head: bool = False) -> int:
@@ -212,8 +204,7 @@ def _state_args(initial_state, output_state, state, state_indices, N, C, dev):
 
 
 def gated_linear_recurrence(x, g, cu_seqlens, gate="log", initial_state=None, output_final_state=False, state=None,
-                            state_indices=None, output=None, output_state=None, workspace=None, device_status=None,
-                            stream=None):
+                            state_indices=None, output=None, output_state=None, device_status=None, stream=None):
     """h_t = a_t h_{t-1} + b_t along every packed sequence, per channel (gdp_linear_recurrence).
 
     x [T, C] bf16, f16 or fp32; g [T, C] fp32 or x's type; rows may be strided (slices of a wider
@@ -235,10 +226,9 @@ def gated_linear_recurrence(x, g, cu_seqlens, gate="log", initial_state=None, ou
     if output_final_state and state is None and output_state is None:
         output_state = torch.empty((N, C), dtype=torch.float32, device=dev)
     init, fin, cache, slots, num = _state_args(initial_state, output_state, state, state_indices, N, C, dev)
-    ws, ws_bytes = _workspace(workspace, gdp_linear_recurrence_workspace_bytes(T, C), dev, stream)
     a = GdpRecurrenceArgs(x.data_ptr(), x.stride(0), g.data_ptr(), g.stride(0),
                           _dense("output", output, (T, C), x.dtype, dev), cu, T, N, C, init, fin, cache, slots, num,
-                          ws.data_ptr(), ws_bytes, _status(device_status, dev), cu64, xt, gt, _gate_code(gate))
+                          _status(device_status, dev), cu64, xt, gt, _gate_code(gate))
     _call("gdp_linear_recurrence", a, stream)
     return (output, output_state) if output_final_state else output
 
@@ -262,13 +252,13 @@ def gated_linear_recurrence_decode(x, g, gate="log", initial_state=None, output_
     init, fin, cache, slots, num = _state_args(initial_state, output_state, state, state_indices, N, C, dev)
     a = GdpRecurrenceArgs(x.data_ptr(), x.stride(0), g.data_ptr(), g.stride(0),
                           _dense("output", output, (N, C), x.dtype, dev), None, N, N, C, init, fin, cache, slots, num,
-                          None, 0, _status(device_status, dev), 0, xt, gt, _gate_code(gate))
+                          _status(device_status, dev), 0, xt, gt, _gate_code(gate))
     _call("gdp_linear_recurrence_decode", a, stream)
     return (output, output_state) if output_final_state else output
 
 
 def gated_linear_recurrence_backward(g, h, d_output, cu_seqlens, gate="log", x=None, initial_state=None,
-                                     d_final_state=None, workspace=None, device_status=None, stream=None):
+                                     d_final_state=None, device_status=None, stream=None):
     """Gradients of gated_linear_recurrence for dL/dh = ``d_output`` [T, C] and dL/dfinal =
     ``d_final_state`` [N, C] fp32 (or None).  ``h``: the forward's output [T, C] in d_output's type, or
     the ActivationCheckpoint of it that gated_group_norm kept ([T, H, D] with H D = C).  ``x`` is needed
@@ -303,12 +293,11 @@ def gated_linear_recurrence_backward(g, h, d_output, cu_seqlens, gate="log", x=N
            "dg": torch.empty((T, C), dtype=g.dtype, device=dev),
            "d_initial_state": (torch.empty((N, C), dtype=torch.float32, device=dev)
                                if initial_state is not None else None)}
-    ws, ws_bytes = _workspace(workspace, gdp_linear_recurrence_workspace_bytes(T, C), dev, stream)
     dinit = out["d_initial_state"]
     a = GdpRecurrenceBackwardArgs(
         g.data_ptr(), g.stride(0), xp, xs, hp, hs, codes, scales, group, d_output.data_ptr(), d_output.stride(0), cu,
         T, N, C, init, dfin, out["dx"].data_ptr(), out["dg"].data_ptr(), None if dinit is None else dinit.data_ptr(),
-        ws.data_ptr(), ws_bytes, _status(device_status, dev), cu64, xt, gt, gate)
+        _status(device_status, dev), cu64, xt, gt, gate)
     _call("gdp_linear_recurrence_backward", a, stream)
     return out
 

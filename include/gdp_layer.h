@@ -44,7 +44,7 @@ typedef enum gdp_gate {
  * every value is formed by the same operations in the same order.
  *
  * gdp_linear_recurrence_decode: one token per sequence (T == N, token i belongs to sequence i);
- * cu_seqlens and the workspace are ignored.
+ * cu_seqlens is ignored.
  *
  * State modes as for the prefill: the cache `state` [num_slots, C] is read and written in place at
  * state_indices[i] (-1: start from zero, write nothing; any other value outside [0, num_slots) sets
@@ -65,8 +65,6 @@ typedef struct gdp_recurrence_args {
   float *state;
   const int32_t *state_indices;
   int64_t num_slots;
-  void *workspace; /* >= gdp_linear_recurrence_workspace_bytes(T, C), 256-byte aligned */
-  size_t workspace_bytes;
   uint32_t *device_status; /* optional */
   int cu_seqlens_int64;
   int x_dtype; /* GDP_DTYPE_BF16, _F16 or _F32 */
@@ -76,9 +74,6 @@ typedef struct gdp_recurrence_args {
 
 gdp_status gdp_linear_recurrence(const gdp_recurrence_args *args, void *stream);
 gdp_status gdp_linear_recurrence_decode(const gdp_recurrence_args *args, void *stream);
-
-/* Workspace bytes of gdp_linear_recurrence and its backward pass (0 for an invalid shape). */
-size_t gdp_linear_recurrence_workspace_bytes(int64_t T, int64_t C);
 
 /*
  * gdp_linear_recurrence_backward: for a loss with dL/dh = d_output and dL/dfinal = d_final_state,
@@ -112,8 +107,6 @@ typedef struct gdp_recurrence_backward_args {
   const float *d_final_state; /* [N, C] or NULL (zero) */
   void *dx, *dg;
   float *d_initial_state;
-  void *workspace;
-  size_t workspace_bytes;
   uint32_t *device_status;
   int cu_seqlens_int64;
   int x_dtype; /* type of x, h, d_output and dx */

@@ -536,7 +536,6 @@ def test_wrapper_refusals(cuda_device):
             (lambda: pkg.gated_linear_recurrence(x, x, cu, state=f32), "state_indices"),
             (lambda: pkg.gated_linear_recurrence(x, x, cu, state=f32, initial_state=f32, state_indices=cu[:1]), "excludes"),
             (lambda: pkg.gated_linear_recurrence(x, x, cu, output=x.float()), "output"),
-            (lambda: pkg.gated_linear_recurrence(x, x, cu, workspace=torch.empty(8, dtype=torch.uint8, device=dev)), "workspace"),
             (lambda: pkg.gated_linear_recurrence(x.expand(8, 16)[:1].expand(8, 16), x, cu), "rows at least C"),
             (lambda: pkg.gated_linear_recurrence_decode(x, x, state=f32, state_indices=cu), "state_indices"),
             (lambda: pkg.gated_linear_recurrence_backward(x, x, x, cu, gate="sigmoid"), "needs x"),

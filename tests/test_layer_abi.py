@@ -23,9 +23,6 @@ def test_layouts_and_queries(lib):
                            pkg.GdpGroupNormBackwardArgs)):
         assert lib.gdp_layer_args_size(i) == ctypes.sizeof(s)
     assert lib.gdp_layer_args_size(4) == 0
-    ws = pkg.gdp_linear_recurrence_workspace_bytes
-    assert ws(65536, 4096) >= ws(1, 1) > 0 and ws(65536, 4096) % 256 == 0
-    assert ws(-1, 4) == 0 and ws(4, 0) == 0
     nw = pkg.gdp_group_norm_workspace_bytes
     assert nw(100, 4, 128) > 0 and nw(100, 4, 0) == 0 and nw(100, 4, 8193) == 0
 
@@ -33,8 +30,7 @@ def test_layouts_and_queries(lib):
 def _rec(**over):
     T, C = 8, 16
     a = pkg.GdpRecurrenceArgs(x=FAKE, x_stride_t=C, g=FAKE, g_stride_t=C, output=FAKE, cu_seqlens=FAKE, T=T, N=2, C=C,
-                              workspace=FAKE, workspace_bytes=1 << 20, x_dtype=pkg.GDP_DTYPE_BF16,
-                              g_dtype=pkg.GDP_DTYPE_BF16, gate=0)
+                              x_dtype=pkg.GDP_DTYPE_BF16, g_dtype=pkg.GDP_DTYPE_BF16, gate=0)
     for k, v in over.items():
         setattr(a, k, v)
     return a
@@ -58,8 +54,6 @@ STATE = dict(state=1 << 22, state_indices=1 << 23, num_slots=4)
     (dict(STATE, initial_state=1 << 24), pkg.GDP_ERR_INVALID_ARG),
     (dict(STATE, output_state=1 << 24), pkg.GDP_ERR_INVALID_ARG),
     (dict(initial_state=1 << 24, output_state=(1 << 24) + 64), pkg.GDP_ERR_ALIAS),
-    (dict(workspace=None), pkg.GDP_ERR_WORKSPACE), (dict(workspace=FAKE + 16), pkg.GDP_ERR_WORKSPACE),
-    (dict(workspace_bytes=8), pkg.GDP_ERR_WORKSPACE),
 ])
 def test_recurrence_refusals(lib, over, status):
     a = _rec(**over)
@@ -82,7 +76,7 @@ def _bwd(**over):
     T, C = 8, 16
     a = pkg.GdpRecurrenceBackwardArgs(
         g=FAKE, g_stride_t=C, h=FAKE, h_stride_t=C, d_output=FAKE, d_output_stride_t=C, cu_seqlens=FAKE, T=T, N=2, C=C,
-        dx=FAKE, dg=FAKE, workspace=FAKE, workspace_bytes=1 << 20, x_dtype=pkg.GDP_DTYPE_BF16,
+        dx=FAKE, dg=FAKE, x_dtype=pkg.GDP_DTYPE_BF16,
         g_dtype=pkg.GDP_DTYPE_F32, gate=0)
     for k, v in over.items():
         setattr(a, k, v)
@@ -99,7 +93,6 @@ def _bwd(**over):
     (dict(dg=FAKE + 2), pkg.GDP_ERR_INVALID_ARG), (dict(h_stride_t=8), pkg.GDP_ERR_INVALID_ARG),
     (dict(initial_state=1 << 24, d_initial_state=1 << 24), pkg.GDP_ERR_ALIAS),
     (dict(d_final_state=1 << 24, d_initial_state=(1 << 24) + 64), pkg.GDP_ERR_ALIAS),
-    (dict(workspace=None), pkg.GDP_ERR_WORKSPACE),
 ])
 def test_recurrence_backward_refusals(lib, over, status):
     a = _bwd(**over)
