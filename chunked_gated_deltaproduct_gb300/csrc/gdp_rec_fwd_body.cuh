@@ -1,6 +1,8 @@
 // gdp_rec_fwd_body.cuh -- the forward scan of the gated linear recurrence (see gdp_rec_scan.cuh).
 #pragma once
 
+#include <type_traits>
+
 #include "gdp_rec_scan.cuh"
 
 namespace gdp {
@@ -9,12 +11,15 @@ namespace {
 
 constexpr int kFwdCtas = 2;  // resident CTAs per SM
 
-template <typename TX, typename TG, bool RAW>
+template <typename TX, typename TG, int GATE, bool RAW>
 struct FwdLayout {
-  static constexpr int S = 8;  // tokens per warp
+  // tokens per warp: as many as the registers hold decays and inputs of (sixteen when the input is
+  // kept packed in 16 bits, eight where it needs 32)
+  static constexpr bool kPacked = sizeof(TX) == 2 && GATE != GDP_GATE_SIGMOID;
+  static constexpr int S = kPacked ? 16 : 8;
   static constexpr int kTile = kScanWarps * S;
   static constexpr int x_off = 0, g_off = tile_bytes<TX>(kTile, RAW), stage = g_off + tile_bytes<TG>(kTile, RAW);
-  static constexpr int kStages = stage <= 18000 ? 4 : stage <= 26000 ? 3 : 2;
+  static constexpr int kStages = stage <= 18000 ? 5 : stage <= 36000 ? 3 : 2;
   static constexpr int kMeta = kStages + 1;
   static constexpr int parts = kStages * stage, enter = parts + Chain::parts_bytes, meta = enter + Chain::enter_bytes;
   static constexpr int bars = (meta + kMeta * (int)sizeof(TileMeta<S>) + 15) / 16 * 16;
@@ -24,7 +29,7 @@ struct FwdLayout {
 template <typename TX, typename TG, int GATE, bool RAW>
 __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
     gdp_rec_fwd_scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g, const RecFwd p) {
-  using L = FwdLayout<TX, TG, RAW>;
+  using L = FwdLayout<TX, TG, GATE, RAW>;
   constexpr int S = L::S;
   extern __shared__ __align__(128) unsigned char smem[];
   TileMeta<S> *metas = reinterpret_cast<TileMeta<S> *>(smem + L::meta);
@@ -34,8 +39,8 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
   ch.enter = reinterpret_cast<float2 *>(smem + L::enter);
   ch.mail = reinterpret_cast<float4 *>(smem + L::mail);
   ch.parts_full = empty + L::kStages;
-  ch.enter_full = ch.parts_full + 2;
-  ch.mail_full = ch.enter_full + 2;
+  ch.enter_full = ch.parts_full + 1;
+  ch.mail_full = ch.enter_full + 1;
   volatile int *gave_up = reinterpret_cast<volatile int *>(ch.mail_full + kMailSlots);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const ScanShape &s = p.s;
@@ -46,10 +51,8 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
       sm100::mbar_init(&full[i], RAW ? 33 : 1);
       sm100::mbar_init(&empty[i], kScanWarps);
     }
-    for (int i = 0; i < 2; ++i) {
-      sm100::mbar_init(&ch.parts_full[i], kScanWarps);
-      sm100::mbar_init(&ch.enter_full[i], 1);
-    }
+    sm100::mbar_init(ch.parts_full, kScanWarps);
+    sm100::mbar_init(ch.enter_full, 1);
     for (int i = 0; i < kMailSlots; ++i) sm100::mbar_init(&ch.mail_full[i], 1);
     *gave_up = 0;
     sm100::mbar_init_fence();
@@ -59,6 +62,8 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
 
   if (warp == kLoadWarp) {
     const int64_t first = load_cu(s.cu, s.cu64, 0), end = min(load_cu(s.cu, s.cu64, s.N), s.T);
+    SeqWindow win;
+    win.load(s, 0, lane);
     for (int n = 0; n < steps; ++n) {
       const int st = n % L::kStages, r = n * s.cluster + rank;
       const int64_t t0 = (int64_t)r * L::kTile;
@@ -73,7 +78,7 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
         sm100::tma_load_2d(base + L::x_off, &map_x, (int)c0, (int)t0, &full[st]);
         sm100::tma_load_2d(base + L::g_off, &map_g, (int)c0, (int)t0, &full[st]);
       }
-      find_sequences<S>(s, m, t0, r + 1 == s.rows, c0, p.from, s.slots ? nullptr : p.to, lane);
+      find_sequences<S, false>(s, m, win, t0, r + 1 == s.rows, c0, p.from, s.slots ? nullptr : p.to, lane);
       if (lane == 0) {
         m.lo = (int)max((int64_t)0, min(first - t0, (int64_t)L::kTile));
         m.hi = (int)max((int64_t)0, min(end - t0, (int64_t)L::kTile));
@@ -83,79 +88,72 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
       if (lane == 0) sm100::mbar_arrive(&full[st]);
     }
     if (blockIdx.x == 0) check_sequences(s.cu, s.cu64, s.N, s.T, s.status, lane, 32);
-  } else if (warp == kPostWarp) {
-    post_steps<S, L::kMeta>(s, ch, metas, steps, lane, gave_up);
-  } else if (warp == kFoldWarp) {
-    fold_steps<S, L::kMeta>(s, ch, metas, steps, lane, gave_up);
+  } else if (warp == kChainWarp) {
+    chain_steps<S, L::kMeta>(s, ch, metas, steps, lane, gave_up);
   } else {
     const int64_t c = c0 + 2 * lane;
-    // decay and input of token i (of this warp's S) of the tile in stage st
-    auto token = [&](int st, int64_t t0, int i, float2 *a, float2 *b) {
-      const unsigned char *base = smem + st * L::stage;
-      const float2 x = read_pair<TX, RAW>(base + L::x_off, warp * S + i, lane, RAW ? raw_offset<TX>(p.x, t0 + i, c0) : 0);
-      const float2 g = read_pair<TG, RAW>(base + L::g_off, warp * S + i, lane, RAW ? raw_offset<TG>(p.g, t0 + i, c0) : 0);
-      float2 f;
-      gate_eval<GATE>(g.x, &a->x, &f.x);
-      gate_eval<GATE>(g.y, &a->y, &f.y);
-      *b = GATE == GDP_GATE_SIGMOID ? make_float2(f.x * x.x, f.y * x.y) : x;
-    };
-    auto x_offset = [&](int64_t t0, int i) { return RAW ? raw_offset<TX>(p.x, t0 + i, c0) : 0; };
-    auto g_offset = [&](int64_t t0, int i) { return RAW ? raw_offset<TG>(p.g, t0 + i, c0) : 0; };
-    auto keep = [&](int st, int64_t t0, int i, float2 v) {
-      put_bits<TX, RAW>(smem + st * L::stage + L::x_off, warp * S + i, lane, x_offset(t0, i), v.x);
-      put_bits<TG, RAW>(smem + st * L::stage + L::g_off, warp * S + i, lane, g_offset(t0, i), v.y);
-    };
-    auto kept = [&](int st, int64_t t0, int i) {
-      return make_float2(get_bits<TX, RAW>(smem + st * L::stage + L::x_off, warp * S + i, lane, x_offset(t0, i)),
-                         get_bits<TG, RAW>(smem + st * L::stage + L::g_off, warp * S + i, lane, g_offset(t0, i)));
-    };
-    for (int n = 0; n <= steps; ++n) {
-      if (n < steps) {  // tile n from zero
-        const int st = n % L::kStages;
-        ring_wait(&full[st], (n / L::kStages) & 1, gave_up, s.status, s.limit_ns);
-        const TileMeta<S> &m = metas[n % L::kMeta];
-        const int64_t t0 = ((int64_t)n * s.cluster + rank) * L::kTile + warp * S;
-        const uint32_t starts = m.starts[warp];
-        float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
+    const bool all_channels = c0 + kSlice <= s.C && p.vec_out;
+    for (int n = 0; n < steps; ++n) {
+      const int st = n % L::kStages;
+      const unsigned char *xs = smem + st * L::stage + L::x_off, *gs = smem + st * L::stage + L::g_off;
+      const int64_t t0 = ((int64_t)n * s.cluster + rank) * L::kTile + warp * S;
+      ring_wait(&full[st], (n / L::kStages) & 1, gave_up, s.status, s.limit_ns);
+      const TileMeta<S> &m = metas[n % L::kMeta];
+      const uint32_t starts = m.starts[warp], ends = m.ends[warp];
+      const int lo = m.lo - warp * S, hi = m.hi - warp * S;
+      // ---- from zero: decays and inputs stay in registers.  Where a sequence begins, the decay's
+      // place takes the state after that token.
+      float2 a[S];
+      typename std::conditional<L::kPacked, uint32_t, float2>::type b[S];
+      float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
+      auto input = [&](int i) {
+        if constexpr (L::kPacked) return unpack<TX>(b[i]);
+        else return b[i];
+      };
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-          float2 a, b;
-          token(st, t0, i, &a, &b);
-          const bool start = starts >> i & 1u;
-          if (start) B = read_state(p.from, m.start_row[warp * S + i], s.C, c);
-          B = make_float2(fmaf(a.x, B.x, b.x), fmaf(a.y, B.y, b.y));
-          // the state after a sequence's first token takes the place of that token's x and g: its
-          // incoming state may be overwritten (in place, by the warp that ends the sequence) before
-          // this warp comes back to the tile
-          if (start) keep(st, t0, i, B);
-          A = make_float2(A.x * a.x, A.y * a.y);
-        }
-        ch.parts[((n & 1) * kScanWarps + warp) * 32 + lane] = make_float4(A.x, A.y, B.x, B.y);
-        __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(&ch.parts_full[n & 1]);
+      for (int i = 0; i < S; ++i) {
+        float2 f;
+        gate_pair<GATE>(unpack<TG>(read_packed<TG, RAW>(gs, warp * S + i, lane, RAW ? raw_offset<TG>(p.g, t0 + i, c0) : 0)), &a[i], &f);
+        const auto x = read_packed<TX, RAW>(xs, warp * S + i, lane, RAW ? raw_offset<TX>(p.x, t0 + i, c0) : 0);
+        if constexpr (L::kPacked) b[i] = x;
+        else if constexpr (GATE == GDP_GATE_SIGMOID) b[i] = mul2(f, unpack<TX>(x));
+        else b[i] = unpack<TX>(x);
+        A = mul2(A, a[i]);
+        B = fma2(a[i], B, input(i));
       }
-      if (n > 0) {  // tile n - 1 from its entering state
-        const int q = n - 1, st = q % L::kStages;
-        const TileMeta<S> &m = metas[q % L::kMeta];
-        const int64_t t0 = ((int64_t)q * s.cluster + rank) * L::kTile + warp * S;
-        const uint32_t starts = m.starts[warp], ends = m.ends[warp];
-        const int lo = m.lo - warp * S, hi = m.hi - warp * S;
-        ring_wait(&ch.enter_full[q & 1], (q >> 1) & 1, gave_up, s.status, s.limit_ns);
-        float2 h = ch.enter[((q & 1) * kScanWarps + warp) * 32 + lane];
-        TX *out = static_cast<TX *>(p.h) + t0 * s.C + c;
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&empty[st]);
+      if (starts) {  // again, token by token
+        B = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-          float2 a, b;
-          token(st, t0, i, &a, &b);
-          h = make_float2(fmaf(a.x, h.x, b.x), fmaf(a.y, h.y, b.y));
-          if (starts >> i & 1u) h = kept(st, t0, i);
+          if (starts >> i & 1u) B = read_state(p.from, m.start_row[warp * S + i], s.C, c);
+          B = fma2(a[i], B, input(i));
+          if (starts >> i & 1u) a[i] = B;
+        }
+      }
+      ch.parts[warp * 32 + lane] = make_float4(A.x, A.y, B.x, B.y);
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(ch.parts_full);
+      ring_wait(ch.enter_full, n & 1, gave_up, s.status, s.limit_ns);
+      // ---- from the entering state
+      float2 h = ch.enter[warp * 32 + lane];
+      TX *out = static_cast<TX *>(p.h) + t0 * s.C + c;
+      if (!(starts | ends) && lo <= 0 && hi >= S && all_channels) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          h = fma2(a[i], h, input(i));
+          write_pair(out, h, true, true);
+          out += s.C;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          h = (starts >> i & 1u) ? a[i] : fma2(a[i], h, input(i));
           if (i >= lo && i < hi && c < s.C) write_pair(out, h, c + 1 < s.C, p.vec_out);
           if (ends >> i & 1u) write_state(p.to, m.end_row[warp * S + i], s.C, c, h);
           out += s.C;
         }
-        if (starts) sm100::fence_async_smem();  // what keep() wrote, before the next tile's copy
-        __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(&empty[st]);
       }
     }
   }
@@ -166,12 +164,12 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
 template <typename TX, typename TG, int GATE, bool RAW>
 cudaError_t run_fwd_as(RecFwd &p, const CUtensorMap *maps, cudaStream_t stream) {
   return launch_clusters(gdp_rec_fwd_scan_kernel<TX, TG, GATE, RAW>, p.s.slices, p.s.cluster,
-                         FwdLayout<TX, TG, RAW>::mail + Chain::mail_bytes(p.s.cluster), stream, maps[0], maps[1], p);
+                         FwdLayout<TX, TG, GATE, RAW>::mail + Chain::mail_bytes(p.s.cluster), stream, maps[0], maps[1], p);
 }
 
 template <typename TX, typename TG, int GATE>
 cudaError_t run_fwd(RecFwd &p, cudaStream_t stream) {
-  using L = FwdLayout<TX, TG, false>;
+  using L = FwdLayout<TX, TG, GATE, false>;
   ScanShape &s = p.s;
   const int64_t rows = (s.T + L::kTile - 1) / L::kTile;
   s.rows = rows > 0 ? (int)rows : 1;

@@ -7,12 +7,12 @@
 // on tile n * cluster + k.  In a CTA,
 //   - a loading warp brings tiles ahead into a ring of shared-memory stages (TMA, or word-wise
 //     asynchronous copies for rows that are not 16-byte aligned) and finds the sequences in them;
-//   - eight warps of S tokens each run tile n + 1 from zero, which gives each warp's (A, B), and then
-//     tile n from its entering states, which gives the outputs;
-//   - a posting warp folds the eight (A, B) and writes the tile's (A, B) into every CTA of the
-//     cluster (distributed shared memory, completing on the reader's barrier);
-//   - a folding warp takes the cluster's tiles in order of time from the state it carries: the eight
-//     warps' entering states, and the state that enters the next step.
+//   - eight warps of S tokens each run the tile from zero, which gives each warp's (A, B), keep their
+//     decays and inputs in registers, and run it again from their entering states for the outputs;
+//   - a chaining warp folds the eight (A, B) in between, writes the tile's (A, B) into every CTA of the
+//     cluster (distributed shared memory, completing on the reader's barrier) and takes the cluster's
+//     tiles in order of time from the state it carries: the eight entering states, and the state that
+//     enters the next step.
 // Every value comes from the same operations in the same order on every run.  Nothing of it passes
 // through global memory: a chain through flags there took 5 us a hop, which 6.8 TB/s would have to
 // cover with 34 MB of waiting tiles (measured 1.97 ms at 65536 x 4096; see the kernels for now).
@@ -29,9 +29,9 @@ namespace layer {
 
 constexpr int kSlice = 64;        // channels of a tile: two per lane
 constexpr int kScanWarps = 8;     // warps that compute
-constexpr int kLoadWarp = kScanWarps, kPostWarp = kScanWarps + 1, kFoldWarp = kScanWarps + 2;
-constexpr int kScanThreads = 32 * (kScanWarps + 3);
-constexpr int kMailSlots = 4;     // steps whose posts may be under way at once (see fold_steps)
+constexpr int kLoadWarp = kScanWarps, kChainWarp = kScanWarps + 1;
+constexpr int kScanThreads = 32 * (kScanWarps + 2);
+constexpr int kMailSlots = 2;     // steps whose posts may be under way at once (see chain_steps)
 
 struct ScanShape {
   const void *cu;
@@ -120,25 +120,65 @@ __device__ __forceinline__ float2 read_pair(const unsigned char *tile, int r, in
   }
 }
 
-// Keeps two fp32 values of the lane in the place of its pairs of two tensors' tiles (each lane only
-// ever reads its own pairs), and reads them back.
+// The pair as it is stored: 16-bit types packed in one register.
+template <typename T>
+struct Packed {
+  using type = uint32_t;
+};
+template <>
+struct Packed<float> {
+  using type = float2;
+};
 template <typename T, bool RAW>
-__device__ __forceinline__ void put_bits(unsigned char *tile, int r, int lane, int offset, float v) {
-  unsigned char *p = tile + r * tile_pitch<T>(RAW) + offset + lane * 2 * (int)sizeof(T);
-  const uint32_t b = __float_as_uint(v);
-  if constexpr (RAW && sizeof(T) < 4) {
-    reinterpret_cast<uint16_t *>(p)[0] = (uint16_t)b;
-    reinterpret_cast<uint16_t *>(p)[1] = (uint16_t)(b >> 16);
+__device__ __forceinline__ typename Packed<T>::type read_packed(const unsigned char *tile, int r, int lane, int offset) {
+  if constexpr (sizeof(T) == 4) {
+    return *reinterpret_cast<const float2 *>(tile + r * tile_pitch<T>(false) + lane * 8);
+  } else if constexpr (RAW) {
+    const uint16_t *p = reinterpret_cast<const uint16_t *>(tile + r * tile_pitch<T>(true) + offset) + 2 * lane;
+    return (uint32_t)p[0] | (uint32_t)p[1] << 16;
   } else {
-    *reinterpret_cast<uint32_t *>(p) = b;
+    return *reinterpret_cast<const uint32_t *>(tile + r * tile_pitch<T>(false) + lane * 4);
   }
 }
-template <typename T, bool RAW>
-__device__ __forceinline__ float get_bits(const unsigned char *tile, int r, int lane, int offset) {
-  const unsigned char *p = tile + r * tile_pitch<T>(RAW) + offset + lane * 2 * (int)sizeof(T);
-  if constexpr (RAW && sizeof(T) < 4)
-    return __uint_as_float(reinterpret_cast<const uint16_t *>(p)[0] | ((uint32_t) reinterpret_cast<const uint16_t *>(p)[1] << 16));
-  return *reinterpret_cast<const float *>(p);
+template <typename T>
+__device__ __forceinline__ float2 unpack(typename Packed<T>::type v) {
+  if constexpr (sizeof(T) == 4) {
+    return v;
+  } else if constexpr (sizeof(T) == 2) {
+    T e[2];
+    *reinterpret_cast<uint32_t *>(e) = v;
+    return make_float2(to_f32(e[0]), to_f32(e[1]));
+  }
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n.reg .b64 x, y, z, w;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\n"
+      "fma.rn.f32x2 w, x, y, z;\nmov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n.reg .b64 x, y, w;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmul.rn.f32x2 w, x, y;\nmov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// Both channels' decay and input factor.
+template <int GATE>
+__device__ __forceinline__ void gate_pair(float2 g, float2 *a, float2 *f) {
+  if constexpr (GATE == GDP_GATE_LOG) {
+    g = mul2(g, make_float2(kLog2e, kLog2e));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a->x) : "f"(g.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a->y) : "f"(g.y));
+    *f = make_float2(1.f, 1.f);
+  } else {
+    gate_eval<GATE>(g.x, &a->x, &f->x);
+    gate_eval<GATE>(g.y, &a->y, &f->y);
+  }
 }
 
 template <typename T>
@@ -168,59 +208,86 @@ __device__ __forceinline__ void write_state(float *p, int row, int64_t C, int64_
   if (c + 1 < C) q[1] = v.y;
 }
 
-// Whole warp: the sequences that begin or end in tile rows [t0, t0 + 8 S), into m; those without
-// tokens at a position in the tile (or at T, for the last tile in time) pass their state from `from`
-// to `to` right away.
-template <int S>
-__device__ void find_sequences(const ScanShape &p, TileMeta<S> &m, int64_t t0, bool last, int64_t c0, const float *from, float *to,
-                               int lane) {
-  constexpr int kTile = kScanWarps * S;
-  const int64_t t1 = t0 + kTile;
-  if (lane < kScanWarps) m.starts[lane] = m.ends[lane] = 0u;
-  __syncwarp();
-  // the first sequence that ends at or after t0, 32 probes a round
-  int64_t lo = 0, hi = p.N;
+// 32 consecutive sequences, one per lane of the loading warp, kept from tile to tile (a CTA's tiles
+// go one way in time), so that a tile inside a long sequence costs no access to cu_seqlens.
+struct SeqWindow {
+  int64_t base, b, e;  // lane: bounds of sequence base + lane (past N: both beyond any row)
+  bool ok;
+  __device__ __forceinline__ void load(const ScanShape &p, int64_t at, int lane) {
+    base = at;
+    b = e = INT64_MAX;
+    ok = false;
+    if (base + lane < p.N) {
+      b = load_cu(p.cu, p.cu64, base + lane);
+      e = load_cu(p.cu, p.cu64, base + lane + 1);
+      ok = b >= 0 && b <= e && e <= p.T;
+    }
+  }
+  __device__ __forceinline__ int64_t first_begin() const { return __shfl_sync(0xffffffffu, b, 0); }
+  __device__ __forceinline__ int64_t last_end() const { return __shfl_sync(0xffffffffu, e, 31); }
+};
+
+// Whole warp: the first i in [lo, hi] with i == hi or cu[i] >= t, 32 probes a round.
+__device__ __forceinline__ int64_t first_at_least(const ScanShape &p, int64_t lo, int64_t hi, int64_t t, int lane) {
   while (lo < hi) {
     const int64_t chunk = (hi - lo + 31) / 32, at = lo + (lane + 1) * chunk - 1;
-    const uint32_t hit = __ballot_sync(0xffffffffu, at >= hi || load_cu(p.cu, p.cu64, at + 1) >= t0);
+    const uint32_t hit = __ballot_sync(0xffffffffu, at >= hi || load_cu(p.cu, p.cu64, at) >= t);
     const int f = hit ? __ffs(hit) - 1 : 32;
     hi = min(hi, lo + (f + 1) * chunk - 1);
     lo = min(hi, lo + f * chunk);
   }
-  for (int64_t base = lo; base < p.N; base += 32) {
-    const int64_t s = base + lane;
-    int64_t b = 0, e = 0;
-    bool ok = false;
-    if (s < p.N) {
-      b = load_cu(p.cu, p.cu64, s);
-      e = load_cu(p.cu, p.cu64, s + 1);
-      ok = b >= 0 && b <= e && e <= p.T;
-    }
-    const bool begins = ok && b < e && b >= t0 && b < t1, ends = ok && b < e && e > t0 && e <= t1;
-    const bool none = ok && b == e && b >= t0 && (b < t1 || last);
-    int row = (int)s;
-    if (p.slots && (begins || ends)) {
-      row = p.slots[s];
-      if (row < -1 || row >= p.num_slots) {
-        if (c0 == 0) set_status(p.status, GDP_DEV_ERR_SLOT);
-        row = -1;
+  return lo;
+}
+
+// Whole warp: the sequences that begin or end in tile rows [t0, t0 + 8 S), into m; those without
+// tokens at a position in the tile (or at T, for the last tile in time) pass their state from `from`
+// to `to` right away.  REV: the CTA's tiles go back in time.
+template <int S, bool REV>
+__device__ __forceinline__ void find_sequences(const ScanShape &p, TileMeta<S> &m, SeqWindow &win, int64_t t0, bool last, int64_t c0,
+                                               const float *from, float *to, int lane) {
+  constexpr int kTile = kScanWarps * S;
+  const int64_t t1 = t0 + kTile;
+  if (lane < kScanWarps) m.starts[lane] = m.ends[lane] = 0u;
+  __syncwarp();
+  if (!REV && win.base + 32 < p.N && win.last_end() < t0)  // on to the first sequence that ends at or after t0
+    win.load(p, first_at_least(p, win.base + 32, p.N, t0, lane) - 1, lane);
+  if (REV && win.base > 0 && win.first_begin() >= t1)  // back to the last ones that begin before t1
+    win.load(p, max((int64_t)0, first_at_least(p, 0, win.base, t1, lane) - 32), lane);
+  for (;;) {
+    const int64_t b = win.b, e = win.e;
+    const bool begins = win.ok && b < e && b >= t0 && b < t1, ends = win.ok && b < e && e > t0 && e <= t1;
+    const bool none = win.ok && b == e && b >= t0 && (b < t1 || last);
+    if (__any_sync(0xffffffffu, begins || ends || none)) {
+      int row = (int)win.base + lane;
+      if (p.slots && (begins || ends)) {
+        row = p.slots[win.base + lane];
+        if (row < -1 || row >= p.num_slots) {
+          if (c0 == 0) set_status(p.status, GDP_DEV_ERR_SLOT);
+          row = -1;
+        }
+      }
+      if (begins) {
+        m.start_row[b - t0] = row;
+        atomicOr(&m.starts[(b - t0) / S], 1u << ((b - t0) % S));
+      }
+      if (ends) {
+        m.end_row[e - 1 - t0] = row;
+        atomicOr(&m.ends[(e - 1 - t0) / S], 1u << ((e - 1 - t0) % S));
+      }
+      if (to) {
+        for (uint32_t left = __ballot_sync(0xffffffffu, none); left; left &= left - 1) {
+          const int at = (int)win.base + __ffs(left) - 1;
+          write_state(to, at, p.C, c0 + 2 * lane, read_state(from, at, p.C, c0 + 2 * lane));
+        }
       }
     }
-    if (begins) {
-      m.start_row[b - t0] = row;
-      atomicOr(&m.starts[(b - t0) / S], 1u << ((b - t0) % S));
+    if (!REV) {
+      if (win.base + 32 >= p.N || (!last && win.last_end() >= t1)) break;
+      win.load(p, win.base + 32, lane);
+    } else {
+      if (win.base == 0 || win.first_begin() < t0) break;
+      win.load(p, max((int64_t)0, win.base - 32), lane);
     }
-    if (ends) {
-      m.end_row[e - 1 - t0] = row;
-      atomicOr(&m.ends[(e - 1 - t0) / S], 1u << ((e - 1 - t0) % S));
-    }
-    if (to) {
-      for (uint32_t left = __ballot_sync(0xffffffffu, none); left; left &= left - 1) {
-        const int at = (int)(base + __ffs(left) - 1);
-        write_state(to, at, p.C, c0 + 2 * lane, read_state(from, at, p.C, c0 + 2 * lane));
-      }
-    }
-    if (__any_sync(0xffffffffu, s < p.N && b >= t1)) break;
   }
 }
 
@@ -235,15 +302,15 @@ __device__ __forceinline__ void check_sequences(const void *cu, int cu64, int64_
 
 // ---- the chain through the cluster ----
 // Per-CTA shared memory of the chain: parts (A0, A1, B0, B1 of a lane's two channels) and entering
-// states per warp, two tiles of each; mail, four steps of one part per CTA of the cluster.
+// states per warp; mail, two steps of one part per CTA of the cluster.
 struct Chain {
-  float4 *parts;    // [2][kScanWarps][32]
-  float2 *enter;    // [2][kScanWarps][32]
+  float4 *parts;    // [kScanWarps][32]
+  float2 *enter;    // [kScanWarps][32]
   float4 *mail;     // [kMailSlots][cluster][32]
-  uint64_t *parts_full, *enter_full, *mail_full;  // [2], [2], [kMailSlots]
-  static constexpr int parts_bytes = 2 * kScanWarps * 32 * 16, enter_bytes = 2 * kScanWarps * 32 * 8;
+  uint64_t *parts_full, *enter_full, *mail_full;  // the last: [kMailSlots]
+  static constexpr int parts_bytes = kScanWarps * 32 * 16, enter_bytes = kScanWarps * 32 * 8;
   __host__ __device__ static constexpr int mail_bytes(int cluster) { return kMailSlots * cluster * 32 * 16; }
-  static constexpr int bars = 2 + 2 + kMailSlots;
+  static constexpr int bars = 2 + kMailSlots;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -274,66 +341,65 @@ __device__ __forceinline__ void ring_wait(uint64_t *bar, uint32_t parity, volati
   if (!sm100::mbar_wait_or_abort(bar, parity, gave_up, limit_ns)) set_status(status, GDP_DEV_ERR_TIMEOUT);
 }
 
-// The posting warp: after the eight warps left tile n's parts.
+// The chaining warp.  Mail slots: a CTA posts step n + 2 only after it has read the mail of step n + 1,
+// which holds this CTA's post of n + 1, which this warp sent after it had read step n: two suffice.
+// parts: a warp writes tile n + 1's after its entering state of tile n, which was formed from tile n's.
 template <int S, int META>
-__device__ __forceinline__ void post_steps(const ScanShape &p, const Chain &ch, const TileMeta<S> *metas, int steps, int lane,
-                                           volatile int *gave_up) {
-  const uint32_t rank = cluster_rank();
-  for (int n = 0; n < steps; ++n) {
-    ring_wait(&ch.parts_full[n & 1], (n >> 1) & 1, gave_up, p.status, p.limit_ns);
-    const TileMeta<S> &m = metas[n % META];
-    const float4 *parts = ch.parts + (n & 1) * kScanWarps * 32;
-    float4 own = make_float4(1.f, 1.f, 0.f, 0.f);
-    bool cut = false;
-#pragma unroll
-    for (int w = 0; w < kScanWarps; ++w) {
-      const float4 q = parts[w * 32 + lane];
-      const bool fresh = m.starts[w] != 0u;
-      cut |= fresh;
-      own = make_float4(own.x * q.x, own.y * q.y, fresh ? q.z : fmaf(q.x, own.z, q.z), fresh ? q.w : fmaf(q.y, own.w, q.w));
-    }
-    if (cut) own.x = __uint_as_float(kCut);
-    const uint32_t slot = n % kMailSlots, to = sm100::smem_u32(ch.mail + ((int)slot * p.cluster + (int)rank) * 32 + lane);
-    const uint32_t bar = sm100::smem_u32(&ch.mail_full[slot]);
-    if (p.withhold && n == 0 && rank == 0) continue;
-    for (int k = 0; k < p.cluster; ++k) post16(in_rank(to, k), own, in_rank(bar, k));
-  }
-}
-
-// The folding warp.  Mail slots: a CTA posts step n + 4 only after its own step n + 2 came through,
-// hence after this CTA posted n + 2, hence (its warps run tile n before tile n + 2 from zero) after
-// this warp has read step n: four slots suffice.
-template <int S, int META>
-__device__ __forceinline__ void fold_steps(const ScanShape &p, const Chain &ch, const TileMeta<S> *metas, int steps, int lane,
-                                           volatile int *gave_up) {
-  const int rank = (int)cluster_rank();
-  const uint32_t bytes = (uint32_t)p.cluster * 512u;
+__device__ __forceinline__ void chain_steps(const ScanShape &p, const Chain &ch, const TileMeta<S> *metas, int steps, int lane,
+                                            volatile int *gave_up) {
+  const uint32_t rank = cluster_rank(), bytes = (uint32_t)p.cluster * 512u;
   if (lane == 0)
     for (int i = 0; i < kMailSlots; ++i) sm100::mbar_arrive_expect_tx(&ch.mail_full[i], bytes);
   float2 h = make_float2(0.f, 0.f);  // the state entering the step
   for (int n = 0; n < steps; ++n) {
+    ring_wait(ch.parts_full, n & 1, gave_up, p.status, p.limit_ns);
+    const TileMeta<S> &m = metas[n % META];
+    uint32_t fresh = 0;  // bit w: a sequence begins among warp w's tokens
+    float4 q[kScanWarps];
+#pragma unroll
+    for (int w = 0; w < kScanWarps; ++w) {
+      q[w] = ch.parts[w * 32 + lane];
+      fresh |= (m.starts[w] != 0u ? 1u : 0u) << w;
+    }
+    float4 own = q[0];
+#pragma unroll
+    for (int w = 1; w < kScanWarps; ++w) {
+      const bool f = fresh >> w & 1u;
+      own = make_float4(own.x * q[w].x, own.y * q[w].y, f ? q[w].z : fmaf(q[w].x, own.z, q[w].z), f ? q[w].w : fmaf(q[w].y, own.w, q[w].w));
+    }
+    if (fresh) own.x = __uint_as_float(kCut);
     const int slot = n % kMailSlots;
+    const uint32_t to = sm100::smem_u32(ch.mail + (slot * p.cluster + (int)rank) * 32 + lane);
+    const uint32_t bar = sm100::smem_u32(&ch.mail_full[slot]);
+    if (!(p.withhold && n == 0 && rank == 0)) {
+#pragma unroll 4
+      for (int k = 0; k < p.cluster; ++k) post16(in_rank(to, k), own, in_rank(bar, k));
+    }
     ring_wait(&ch.mail_full[slot], (n / kMailSlots) & 1, gave_up, p.status, p.limit_ns);
     const float4 *mail = ch.mail + slot * p.cluster * 32;
     float2 e = h;
-    for (int k = 0; k < p.cluster; ++k) {
-      const float4 q = mail[k * 32 + lane];
-      if (k == rank) e = h;
-      h = __float_as_uint(q.x) == kCut ? make_float2(q.z, q.w) : make_float2(fmaf(q.x, h.x, q.z), fmaf(q.y, h.y, q.w));
+    for (int k0 = 0; k0 < p.cluster; k0 += 4) {
+      float4 t[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (k0 + u < p.cluster) t[u] = mail[(k0 + u) * 32 + lane];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (k0 + u >= p.cluster) break;
+        if (k0 + u == (int)rank) e = h;
+        h = __float_as_uint(t[u].x) == kCut ? make_float2(t[u].z, t[u].w) : make_float2(fmaf(t[u].x, h.x, t[u].z), fmaf(t[u].y, h.y, t[u].w));
+      }
     }
-    __syncwarp();
-    if (lane == 0) sm100::mbar_arrive_expect_tx(&ch.mail_full[slot], bytes);  // for step n + 4
-    const TileMeta<S> &m = metas[n % META];
-    const float4 *parts = ch.parts + (n & 1) * kScanWarps * 32;
-    float2 *enter = ch.enter + (n & 1) * kScanWarps * 32;
 #pragma unroll
     for (int w = 0; w < kScanWarps; ++w) {
-      enter[w * 32 + lane] = e;
-      const float4 q = parts[w * 32 + lane];
-      e = m.starts[w] ? make_float2(q.z, q.w) : make_float2(fmaf(q.x, e.x, q.z), fmaf(q.y, e.y, q.w));
+      ch.enter[w * 32 + lane] = e;
+      e = (fresh >> w & 1u) ? make_float2(q[w].z, q[w].w) : make_float2(fmaf(q[w].x, e.x, q[w].z), fmaf(q[w].y, e.y, q[w].w));
     }
     __syncwarp();
-    if (lane == 0) sm100::mbar_arrive(&ch.enter_full[n & 1]);
+    if (lane == 0) {
+      sm100::mbar_arrive(ch.enter_full);
+      sm100::mbar_arrive_expect_tx(&ch.mail_full[slot], bytes);  // for step n + 2
+    }
   }
 }
 
