@@ -92,10 +92,13 @@ inline gdp_status launch_status(const char *what) {
   return GDP_ERR_CUDA;
 }
 inline bool aligned(const void *p, size_t bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
+inline bool overlap(const void *a, const void *b, size_t bytes) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && x < y + bytes && y < x + bytes;
+}
 // Neither the same range nor disjoint.
 inline bool partly_overlap(const void *a, const void *b, size_t bytes) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return a && b && x != y && x < y + bytes && y < x + bytes;
+  return a != b && overlap(a, b, bytes);
 }
 
 }  // namespace layer

@@ -1,0 +1,6 @@
+// gdp_rec_bf16_f32.cu -- the recurrence's scans: bf16 inputs, fp32 gates.
+#include "gdp_rec_bwd_body.cuh"
+#include "gdp_rec_fwd_body.cuh"
+
+template cudaError_t gdp::layer::launch_rec_fwd<__nv_bfloat16, float>(RecFwd &, int, cudaStream_t);
+template cudaError_t gdp::layer::launch_rec_bwd<__nv_bfloat16, float>(RecBwd &, int, cudaStream_t);

@@ -1,6 +1,6 @@
-// gdp_rec_f16.cu -- the recurrence's scans over f16 inputs.
+// gdp_rec_f16.cu -- the recurrence's scans: f16 inputs, f16 gates.
+#include "gdp_rec_bwd_body.cuh"
 #include "gdp_rec_fwd_body.cuh"
 
-cudaError_t gdp::layer::launch_rec_fwd_f16(RecFwd &p, int g_f32, int gate, cudaStream_t stream) {
-  return g_f32 ? run_fwd_gate<__half, float>(p, gate, stream) : run_fwd_gate<__half, __half>(p, gate, stream);
-}
+template cudaError_t gdp::layer::launch_rec_fwd<__half, __half>(RecFwd &, int, cudaStream_t);
+template cudaError_t gdp::layer::launch_rec_bwd<__half, __half>(RecBwd &, int, cudaStream_t);

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
     }
     if (blockIdx.x == 0) check_sequences(s.cu, s.cu64, s.N, s.T, s.status, lane, 32);
   } else if (warp == kChainWarp) {
-    chain_steps<S, L::kMeta>(s, ch, metas, steps, lane, gave_up);
+    chain_steps<S, L::kMeta, false>(s, ch, metas, steps, lane, gave_up);
   } else {
     const int64_t c = c0 + 2 * lane;
     const bool all_channels = c0 + kSlice <= s.C && p.vec_out;
@@ -177,23 +177,21 @@ cudaError_t run_fwd(RecFwd &p, cudaStream_t stream) {
   s.cluster = cluster_size(s.slices, s.rows, sm_count(), kFwdCtas);
   CUtensorMap maps[2];
   memset(maps, 0, sizeof(maps));
-  auto fits = [&](const RowSource &src, size_t es) { return s.T > 0 && s.C >= kSlice && aligned(src.base, 16) && src.stride * es % 16 == 0; };
-  s.raw = !(fits(p.x, sizeof(TX)) && fits(p.g, sizeof(TG)));
-  cudaError_t e = cudaSuccess;
-  if (!s.raw) {
-    if ((e = tmap_matrix(&maps[0], p.x.base, s.T, s.C, p.x.stride * sizeof(TX), sizeof(TX), kSlice, L::kTile)) != cudaSuccess) return e;
-    if ((e = tmap_matrix(&maps[1], p.g.base, s.T, s.C, p.g.stride * sizeof(TG), sizeof(TG), kSlice, L::kTile)) != cudaSuccess) return e;
-  }
-  return s.raw ? run_fwd_as<TX, TG, GATE, true>(p, maps, stream) : run_fwd_as<TX, TG, GATE, false>(p, maps, stream);
+  if (!tma_rows(p.x, sizeof(TX), s.T, s.C) || !tma_rows(p.g, sizeof(TG), s.T, s.C)) return run_fwd_as<TX, TG, GATE, true>(p, maps, stream);
+  cudaError_t e;
+  if ((e = tmap_matrix(&maps[0], p.x.base, s.T, s.C, p.x.stride * sizeof(TX), sizeof(TX), kSlice, L::kTile)) != cudaSuccess) return e;
+  if ((e = tmap_matrix(&maps[1], p.g.base, s.T, s.C, p.g.stride * sizeof(TG), sizeof(TG), kSlice, L::kTile)) != cudaSuccess) return e;
+  return run_fwd_as<TX, TG, GATE, false>(p, maps, stream);
 }
 
+}  // namespace
+
 template <typename TX, typename TG>
-cudaError_t run_fwd_gate(RecFwd &p, int gate, cudaStream_t stream) {
+cudaError_t launch_rec_fwd(RecFwd &p, int gate, cudaStream_t stream) {
   if (gate == GDP_GATE_LOG) return run_fwd<TX, TG, GDP_GATE_LOG>(p, stream);
   if (gate == GDP_GATE_ALPHA) return run_fwd<TX, TG, GDP_GATE_ALPHA>(p, stream);
   return run_fwd<TX, TG, GDP_GATE_SIGMOID>(p, stream);
 }
 
-}  // namespace
 }  // namespace layer
 }  // namespace gdp

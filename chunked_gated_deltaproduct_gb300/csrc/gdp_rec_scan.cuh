@@ -57,15 +57,18 @@ struct TileMeta {
 
 template <typename T>
 constexpr int tile_pitch(bool raw) { return kSlice * (int)sizeof(T) + (raw && sizeof(T) < 4 ? 4 : 0); }
-// Bytes a tensor's tile takes in a stage.
-template <typename T>
-constexpr int tile_bytes(int rows, bool raw) { return (rows * tile_pitch<T>(raw) + 127) / 128 * 128; }
-
 // One input tensor [T][C]: its address for the word-wise copies.
 struct RowSource {
   const void *base;
   int64_t stride;  // elements
 };
+// Whether TMA can fetch its tiles.
+inline bool tma_rows(const RowSource &src, size_t elem, int64_t T, int64_t C) {
+  return T > 0 && C >= kSlice && aligned(src.base, 16) && src.stride * elem % 16 == 0;
+}
+// Bytes a tensor's tile takes in a stage.
+template <typename T>
+constexpr int tile_bytes(int rows, bool raw) { return (rows * tile_pitch<T>(raw) + 127) / 128 * 128; }
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -344,7 +347,8 @@ __device__ __forceinline__ void ring_wait(uint64_t *bar, uint32_t parity, volati
 // The chaining warp.  Mail slots: a CTA posts step n + 2 only after it has read the mail of step n + 1,
 // which holds this CTA's post of n + 1, which this warp sent after it had read step n: two suffice.
 // parts: a warp writes tile n + 1's after its entering state of tile n, which was formed from tile n's.
-template <int S, int META>
+// REV: the tiles and the tokens in them go back in time, and the ends of sequences cut the chain.
+template <int S, int META, bool REV>
 __device__ __forceinline__ void chain_steps(const ScanShape &p, const Chain &ch, const TileMeta<S> *metas, int steps, int lane,
                                             volatile int *gave_up) {
   const uint32_t rank = cluster_rank(), bytes = (uint32_t)p.cluster * 512u;
@@ -354,12 +358,12 @@ __device__ __forceinline__ void chain_steps(const ScanShape &p, const Chain &ch,
   for (int n = 0; n < steps; ++n) {
     ring_wait(ch.parts_full, n & 1, gave_up, p.status, p.limit_ns);
     const TileMeta<S> &m = metas[n % META];
-    uint32_t fresh = 0;  // bit w: a sequence begins among warp w's tokens
+    uint32_t fresh = 0;  // bit w: a sequence begins (REV: ends) among warp w's tokens
     float4 q[kScanWarps];
 #pragma unroll
     for (int w = 0; w < kScanWarps; ++w) {
       q[w] = ch.parts[w * 32 + lane];
-      fresh |= (m.starts[w] != 0u ? 1u : 0u) << w;
+      fresh |= ((REV ? m.ends[kScanWarps - 1 - w] : m.starts[w]) != 0u ? 1u : 0u) << w;
     }
     float4 own = q[0];
 #pragma unroll
@@ -417,20 +421,18 @@ struct RecBwd {
   RowSource codes;     // int8
   const float *scales;
   int64_t group;       // channels of a checkpoint row
+  int64_t blocks;      // scales of a checkpoint row
   const float *init, *dfin;
   void *dx, *dg;
   float *dinit;
   int vec_dx, vec_dg;
 };
 
-// Fills s.rows, s.slices, s.cluster and s.raw and launches (gdp_rec_*.cu, by x's type).
-cudaError_t launch_rec_fwd_bf16(RecFwd &p, int g_f32, int gate, cudaStream_t stream);
-cudaError_t launch_rec_fwd_f16(RecFwd &p, int g_f32, int gate, cudaStream_t stream);
-cudaError_t launch_rec_fwd_f32(RecFwd &p, int g_f32, int gate, cudaStream_t stream);
-cudaError_t launch_rec_bwd_bf16(RecBwd &p, int g_f32, int gate, cudaStream_t stream);
-cudaError_t launch_rec_bwd_f16(RecBwd &p, int g_f32, int gate, cudaStream_t stream);
-cudaError_t launch_rec_bwd_f32(RecBwd &p, int g_f32, int gate, cudaStream_t stream);
-
+// Fills s.rows, s.slices and s.cluster and launches (instantiated in gdp_rec_*.cu).
+template <typename TX, typename TG>
+cudaError_t launch_rec_fwd(RecFwd &p, int gate, cudaStream_t stream);
+template <typename TX, typename TG>
+cudaError_t launch_rec_bwd(RecBwd &p, int gate, cudaStream_t stream);
 // CTAs per slice: enough for `per_sm` on every SM, at most one per tile in time and 16 (the largest
 // cluster there is).
 inline int cluster_size(int slices, int rows, int sms, int per_sm) {

@@ -27,22 +27,6 @@ struct RecProblem {
   int x_type, g_type, gate;
 };
 
-struct RecBwdProblem {
-  const void *g, *x, *h, *dout;
-  int64_t g_st, x_st, h_st, dout_st;
-  const int8_t *codes;
-  const float *scales;
-  int64_t group;
-  const void *cu;
-  int cu64;
-  int64_t T, N, C;
-  const float *init, *dfin;
-  void *dx, *dg;
-  float *dinit;
-  uint32_t *status;
-  int x_type, g_type, gate;
-};
-
 __device__ __forceinline__ float load_any(const void *p, int64_t i, int type) {
   if (type == GDP_DTYPE_F32) return static_cast<const float *>(p)[i];
   if (type == GDP_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
@@ -90,32 +74,6 @@ __global__ void __launch_bounds__(kThreads) gdp_rec_fwd_kernel(RecProblem p, int
     store_any(p.h, t * p.C + c, p.x_type, h);
   }
   if (dst) dst[c] = h;
-}
-
-__global__ void __launch_bounds__(kThreads) gdp_rec_bwd_kernel(RecBwdProblem p) {
-  const int64_t i = blockIdx.x, c = (int64_t)blockIdx.y * kThreads + threadIdx.x;
-  int64_t bos, len;
-  if ((!seq_bounds(p.cu, p.cu64, p.T, i, &bos, &len) || (i == 0 && bos != 0)) && threadIdx.x == 0)
-    set_status(p.status, GDP_DEV_ERR_CU_SEQLENS);
-  if (c >= p.C) return;
-  const int64_t blocks = (p.group + kBlock - 1) / kBlock, per_row = p.codes ? p.C / p.group * blocks : 0;
-  const int64_t block = p.codes ? c / p.group * blocks + c % p.group / kBlock : 0;
-  float e = p.dfin ? p.dfin[i * p.C + c] : 0.f;  // a_{t+1} D_{t+1}
-  for (int64_t t = bos + len - 1; t >= bos; --t) {
-    float a, f, prev;
-    gate_any(p.gate, load_any(p.g, t * p.g_st + c, p.g_type), &a, &f);
-    if (t == bos) prev = p.init ? p.init[i * p.C + c] : 0.f;
-    else if (p.codes) prev = p.codes[(t - 1) * p.C + c] * p.scales[(t - 1) * per_row + block];
-    else prev = load_any(p.h, (t - 1) * p.h_st + c, p.x_type);
-    const float d = load_any(p.dout, t * p.dout_st + c, p.x_type) + e;
-    e = a * d;
-    float dg = d * prev;
-    if (p.gate == GDP_GATE_LOG) dg = e * prev;
-    if (p.gate == GDP_GATE_SIGMOID) dg = f * e * (prev - load_any(p.x, t * p.x_st + c, p.x_type));
-    store_any(p.dx, t * p.C + c, p.x_type, f * d);
-    store_any(p.dg, t * p.C + c, p.g_type, dg);
-  }
-  if (p.dinit) p.dinit[i * p.C + c] = e;
 }
 
 gdp_status check_shape(int64_t T, int64_t N, int64_t C, int x_type, int g_type, int gate) {
@@ -166,6 +124,26 @@ gdp_status resolve(const gdp_recurrence_args *a, bool step, RecProblem *p) {
   return GDP_OK;
 }
 
+cudaError_t run(RecFwd &p, int gate, cudaStream_t stream, bool bf16, bool wide) {
+  if (bf16) return wide ? launch_rec_fwd<__nv_bfloat16, float>(p, gate, stream) : launch_rec_fwd<__nv_bfloat16, __nv_bfloat16>(p, gate, stream);
+  return wide ? launch_rec_fwd<__half, float>(p, gate, stream) : launch_rec_fwd<__half, __half>(p, gate, stream);
+}
+cudaError_t run(RecBwd &p, int gate, cudaStream_t stream, bool bf16, bool wide) {
+  if (bf16) return wide ? launch_rec_bwd<__nv_bfloat16, float>(p, gate, stream) : launch_rec_bwd<__nv_bfloat16, __nv_bfloat16>(p, gate, stream);
+  return wide ? launch_rec_bwd<__half, float>(p, gate, stream) : launch_rec_bwd<__half, __half>(p, gate, stream);
+}
+cudaError_t run_f32(RecFwd &p, int gate, cudaStream_t stream) { return launch_rec_fwd<float, float>(p, gate, stream); }
+cudaError_t run_f32(RecBwd &p, int gate, cudaStream_t stream) { return launch_rec_bwd<float, float>(p, gate, stream); }
+
+template <typename P>
+gdp_status dispatch(int x_type, int g_type, P &p, int gate, cudaStream_t stream) {
+  const cudaError_t e = x_type == GDP_DTYPE_F32 ? run_f32(p, gate, stream)
+                                                : run(p, gate, stream, x_type == GDP_DTYPE_BF16, g_type == GDP_DTYPE_F32);
+  if (e == cudaSuccess) return GDP_OK;
+  set_last_error("recurrence kernel: %s", cudaGetErrorString(e));
+  return GDP_ERR_CUDA;
+}
+
 }  // namespace
 
 int sm_count() {
@@ -192,13 +170,7 @@ GDP_EXPORT gdp_status gdp_linear_recurrence(const gdp_recurrence_args *args, voi
   f.from = p.cache ? p.cache : p.init;
   f.to = p.cache ? p.cache : p.fin;
   f.vec_out = p.C % 2 == 0 && aligned(p.h, 2 * dtype_size(p.x_type));
-  const auto launch = p.x_type == GDP_DTYPE_BF16 ? launch_rec_fwd_bf16 : p.x_type == GDP_DTYPE_F16 ? launch_rec_fwd_f16 : launch_rec_fwd_f32;
-  const cudaError_t e = launch(f, p.g_type == GDP_DTYPE_F32, p.gate, (cudaStream_t)stream);
-  if (e != cudaSuccess) {
-    gdp::set_last_error("recurrence kernel: %s", cudaGetErrorString(e));
-    return GDP_ERR_CUDA;
-  }
-  return GDP_OK;
+  return dispatch(p.x_type, p.g_type, f, p.gate, (cudaStream_t)stream);
 }
 
 GDP_EXPORT gdp_status gdp_linear_recurrence_decode(const gdp_recurrence_args *args, void *stream) {
@@ -231,17 +203,23 @@ GDP_EXPORT gdp_status gdp_linear_recurrence_backward(const gdp_recurrence_backwa
   if (!aligned(a->initial_state, 4) || !aligned(a->d_final_state, 4) || !aligned(a->d_initial_state, 4))
     return fail(GDP_ERR_INVALID_ARG, "state buffers must be 4-byte aligned");
   const size_t bytes = sizeof(float) * (size_t)a->N * (size_t)a->C;
-  if (partly_overlap(a->d_final_state, a->d_initial_state, bytes) || partly_overlap(a->initial_state, a->d_initial_state, bytes) ||
-      (a->initial_state && a->initial_state == a->d_initial_state))
-    return fail(GDP_ERR_ALIAS, "d_initial_state overlaps initial_state or partly overlaps d_final_state");
+  if (overlap(a->d_final_state, a->d_initial_state, bytes) || overlap(a->initial_state, a->d_initial_state, bytes))
+    return fail(GDP_ERR_ALIAS, "d_initial_state overlaps initial_state or d_final_state");
   if (a->N == 0) return GDP_OK;
-  RecBwdProblem p{a->g, a->x, a->h, a->d_output, a->g_stride_t, a->x_stride_t, a->h_stride_t, a->d_output_stride_t,
-                  a->h_codes, a->h_scales, a->h_group, a->cu_seqlens, a->cu_seqlens_int64 != 0, a->T, a->N, a->C,
-                  a->initial_state, a->d_final_state, a->dx, a->dg, a->d_initial_state, a->device_status,
-                  a->x_dtype, a->g_dtype, a->gate};
-  const dim3 grid((unsigned)p.N, (unsigned)((p.C + kThreads - 1) / kThreads));
-  gdp_rec_bwd_kernel<<<grid, kThreads, 0, (cudaStream_t)stream>>>(p);
-  return launch_status("recurrence backward kernel");
+  RecBwd p{};
+  p.s.cu = a->cu_seqlens; p.s.cu64 = a->cu_seqlens_int64 != 0; p.s.T = a->T; p.s.N = a->N; p.s.C = a->C;
+  p.s.status = a->device_status;
+  p.s.limit_ns = gdp::sm100::kWaitLimitNs;
+  p.g = {a->g, a->g_stride_t}; p.x = {a->x, a->x_stride_t}; p.h = {a->h, a->h_stride_t}; p.dout = {a->d_output, a->d_output_stride_t};
+  p.codes = {a->h_codes, a->C};
+  p.scales = a->h_scales;
+  p.group = a->h_codes ? a->h_group : 1;
+  p.blocks = (p.group + kBlock - 1) / kBlock;
+  p.init = a->initial_state; p.dfin = a->d_final_state;
+  p.dx = a->dx; p.dg = a->dg; p.dinit = a->d_initial_state;
+  p.vec_dx = a->C % 2 == 0 && aligned(a->dx, 2 * dtype_size(a->x_dtype));
+  p.vec_dg = a->C % 2 == 0 && aligned(a->dg, 2 * dtype_size(a->g_dtype));
+  return dispatch(a->x_dtype, a->g_dtype, p, a->gate, (cudaStream_t)stream);
 }
 
 GDP_EXPORT size_t gdp_layer_args_size(int which) {
