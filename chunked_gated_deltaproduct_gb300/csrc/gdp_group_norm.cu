@@ -1,206 +1,44 @@
-// gdp_group_norm.cu -- the grouped norm with an activated gate, its 8-bit checkpoints and its
-// backward pass (gdp_layer.h).
-//
-// One warp per (token, head) row of D channels.  The sums over rows of the backward pass (dweight,
-// dbias) run in a fixed order: column sums of a slab of rows into the workspace, then the slabs in turn.
-#include "gdp_layer.cuh"
+// gdp_group_norm.cu -- the grouped norm's C entries, argument checks and column-sum kernel
+// (gdp_layer.h; the kernels over rows are in gdp_norm_body.cuh).
+#include "gdp_norm.cuh"
 
 namespace gdp {
 namespace layer {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kSlabs = 256;  // row slabs of the column sums
-
-struct NormProblem {
-  const void *o, *z;
-  int64_t o_st, o_sh, z_st, z_sh;
-  const int8_t *o_codes_in, *z_codes_in;  // backward: read instead of o and z
-  const float *o_scales_in, *z_scales_in;
-  const float *w, *b;
-  void *y;
-  int8_t *o_codes, *z_codes;
-  float *o_scales, *z_scales;
-  const void *dy;
-  int64_t dy_st, dy_sh;
-  void *d_o, *d_z;
-  float *dw, *db, *stats, *partial;
-  int64_t T, H, D;
-  float eps;
-  int type, center, per_head, act;
-};
-
-__device__ __forceinline__ float load_any(const void *p, int64_t i, int type) {
-  if (type == GDP_DTYPE_F32) return static_cast<const float *>(p)[i];
-  if (type == GDP_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-  return __half2float(static_cast<const __half *>(p)[i]);
-}
-__device__ __forceinline__ void store_any(void *p, int64_t i, int type, float v) {
-  if (type == GDP_DTYPE_F32) static_cast<float *>(p)[i] = v;
-  else if (type == GDP_DTYPE_BF16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
-  else static_cast<__half *>(p)[i] = __float2half_rn(v);
-}
-__device__ __forceinline__ float warp_sum(float v) {
-  for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-  return v;
-}
-
-// Element d of row (t, h) of o or z, from the tensor or its checkpoint.
-struct RowReader {
-  const void *p;
-  const int8_t *codes;
-  const float *scales;
-  int64_t at, row, D;
-  int type;
-  __device__ float operator()(int64_t d) const {
-    if (codes) return codes[row * D + d] * scales[row * ((D + kBlock - 1) / kBlock) + d / kBlock];
-    return load_any(p, at + d, type);
+// Adds up the parts of every column in a fixed order: 32 columns per CTA, each warp a stride of the
+// parts, then the warps' sums in turn.
+constexpr int kFinishWarps = 16;
+__global__ void __launch_bounds__(32 * kFinishWarps) gdp_norm_finish_kernel(const float *partial, int64_t parts, int64_t cols, float *dw,
+                                                                            float *db) {
+  __shared__ float sums[kFinishWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t col = (int64_t)blockIdx.x * 32 + lane;
+  const float *from = partial + (blockIdx.y ? parts * cols : 0);
+  float s = 0.f;
+  if (col < cols) {
+#pragma unroll 4
+    for (int64_t i = warp; i < parts; i += kFinishWarps) s += from[i * cols + col];
   }
-};
-__device__ __forceinline__ RowReader reader_o(const NormProblem &p, int64_t t, int64_t h) {
-  return {p.o, p.o_codes_in, p.o_scales_in, t * p.o_st + h * p.o_sh, t * p.H + h, p.D, p.type};
-}
-__device__ __forceinline__ RowReader reader_z(const NormProblem &p, int64_t t, int64_t h) {
-  return {p.z, p.z_codes_in, p.z_scales_in, t * p.z_st + h * p.z_sh, t * p.H + h, p.D, p.type};
-}
-__device__ __forceinline__ bool has_z(const NormProblem &p) { return p.z || p.z_codes_in; }
-
-__device__ __forceinline__ void row_stats(const NormProblem &p, const RowReader &o, int lane, float *mean, float *rstd) {
-  float s = 0.f, m = 0.f;
-  if (p.center) {
-    for (int64_t d = lane; d < p.D; d += 32) s += o(d);
-    m = warp_sum(s) / (float)p.D;
-  }
-  s = 0.f;
-  for (int64_t d = lane; d < p.D; d += 32) s += (o(d) - m) * (o(d) - m);
-  *mean = m;
-  *rstd = rsqrtf(warp_sum(s) / (float)p.D + p.eps);
-}
-
-// act(t) and its slope at t.
-__device__ __forceinline__ void activation(int act, float t, float *v, float *slope) {
-  float q, r;  // sigmoid(t) and 1 - sigmoid(t), each to its own relative precision
-  gate_eval<GDP_GATE_SIGMOID>(t, &q, &r);
-  *v = act == GDP_ACT_SILU ? t * q : q;
-  *slope = act == GDP_ACT_SILU ? q * (1.f + t * r) : q * r;
-}
-
-__device__ __forceinline__ void save_row(const RowReader &v, int64_t row, int64_t D, int8_t *codes, float *scales, int lane) {
-  const int64_t nb = (D + kBlock - 1) / kBlock;
-  for (int64_t b = 0; b < nb; ++b) {
-    const int64_t lo = b * kBlock, hi = min(lo + kBlock, D);
-    uint32_t amax = 0;
-    for (int64_t d = lo + lane; d < hi; d += 32) amax = max(amax, abs_bits(v(d)));
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    const float inv = block_inverse(amax);
-    for (int64_t d = lo + lane; d < hi; d += 32) codes[row * D + d] = (int8_t)block_code(v(d), inv);
-    if (lane == 0) scales[row * nb + b] = block_scale(amax, inv);
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && col < cols) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kFinishWarps; ++i) s += sums[i][lane];
+    (blockIdx.y ? db : dw)[col] = s;
   }
 }
 
-__global__ void __launch_bounds__(kWarps * 32) gdp_norm_fwd_kernel(NormProblem p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (row >= p.T * p.H) return;
-  const int64_t t = row / p.H, h = row % p.H;
-  const RowReader o = reader_o(p, t, h), z = reader_z(p, t, h);
-  float mean, rstd;
-  row_stats(p, o, lane, &mean, &rstd);
-  const float *w = p.w + (p.per_head ? h * p.D : 0), *b = p.b ? p.b + (p.per_head ? h * p.D : 0) : nullptr;
-  for (int64_t d = lane; d < p.D; d += 32) {
-    const float u = (o(d) - mean) * rstd * w[d] + (b ? b[d] : 0.f);
-    float v = 1.f, slope;
-    if (has_z(p)) {
-      activation(p.act, z(d), &v, &slope);
-      if (p.act == GDP_ACT_NONE) v = 1.f;
-    } else if (p.act == GDP_ACT_SILU) {
-      v = sigmoid(u);
-    }
-    store_any(p.y, row * p.D + d, p.type, u * v);
-  }
-  if (p.o_codes) save_row(o, row, p.D, p.o_codes, p.o_scales, lane);
-  if (p.z_codes) save_row(z, row, p.D, p.z_codes, p.z_scales, lane);
+// Eight channels at a time: whole chunks of 16 bytes in every tensor.
+bool vec_ok(const void *p, int64_t st, int64_t sh, int64_t T, int64_t H, int type) {
+  return aligned(p, 16) && (T <= 1 || st * dtype_size(type) % 16 == 0) && (H <= 1 || sh * dtype_size(type) % 16 == 0);
 }
 
-// du and dz of one element from u, z and dy.
-__device__ __forceinline__ void through_gate(const NormProblem &p, float u, float z, float dy, float *du, float *dz) {
-  float v, slope;
-  *du = dy;
-  *dz = 0.f;
-  if (p.act == GDP_ACT_NONE) return;
-  activation(p.act, has_z(p) ? z : u, &v, &slope);
-  if (has_z(p)) {
-    *du = dy * v;
-    *dz = dy * u * slope;
-  } else {
-    *du = dy * slope;
-  }
-}
-
-__global__ void __launch_bounds__(kWarps * 32) gdp_norm_bwd_kernel(NormProblem p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (row >= p.T * p.H) return;
-  const int64_t t = row / p.H, h = row % p.H;
-  const RowReader o = reader_o(p, t, h), z = reader_z(p, t, h);
-  const bool zed = has_z(p);
-  float mean, rstd;
-  row_stats(p, o, lane, &mean, &rstd);
-  if (lane == 0) {
-    p.stats[2 * row] = mean;
-    p.stats[2 * row + 1] = rstd;
-  }
-  const float *w = p.w + (p.per_head ? h * p.D : 0), *b = p.b ? p.b + (p.per_head ? h * p.D : 0) : nullptr;
-  const int64_t at = t * p.dy_st + h * p.dy_sh;
-  float s1 = 0.f, s2 = 0.f;
-  for (int64_t d = lane; d < p.D; d += 32) {
-    const float n = (o(d) - mean) * rstd;
-    float du, dz;
-    through_gate(p, n * w[d] + (b ? b[d] : 0.f), zed ? z(d) : 0.f, load_any(p.dy, at + d, p.type), &du, &dz);
-    if (zed) store_any(p.d_z, row * p.D + d, p.type, dz);
-    s1 += du * w[d];
-    s2 += du * w[d] * n;
-  }
-  s1 = p.center ? warp_sum(s1) / (float)p.D : 0.f;
-  s2 = warp_sum(s2) / (float)p.D;
-  for (int64_t d = lane; d < p.D; d += 32) {
-    const float n = (o(d) - mean) * rstd;
-    float du, dz;
-    through_gate(p, n * w[d] + (b ? b[d] : 0.f), zed ? z(d) : 0.f, load_any(p.dy, at + d, p.type), &du, &dz);
-    store_any(p.d_o, row * p.D + d, p.type, rstd * (du * w[d] - s1 - n * s2));
-  }
-}
-
-// Column sums of slab blockIdx.y: partial[slab][0] = sum du n, [1] = sum du.
-__global__ void __launch_bounds__(128) gdp_norm_columns_kernel(NormProblem p) {
-  const int64_t cols = p.per_head ? p.H * p.D : p.D, col = (int64_t)blockIdx.x * 128 + threadIdx.x;
-  if (col >= cols) return;
-  const int64_t h0 = p.per_head ? col / p.D : 0, d = col % p.D, step = p.per_head ? p.H : 1;
-  const int64_t rows = p.per_head ? p.T : p.T * p.H, lo = rows * blockIdx.y / kSlabs, hi = rows * (blockIdx.y + 1) / kSlabs;
-  float sw = 0.f, sb = 0.f;
-  for (int64_t r = lo; r < hi; ++r) {
-    const int64_t row = r * step + h0, t = row / p.H, h = row % p.H;
-    const float n = (reader_o(p, t, h)(d) - p.stats[2 * row]) * p.stats[2 * row + 1];
-    float du, dz;
-    through_gate(p, n * p.w[col] + (p.b ? p.b[col] : 0.f), has_z(p) ? reader_z(p, t, h)(d) : 0.f,
-                 load_any(p.dy, t * p.dy_st + h * p.dy_sh + d, p.type), &du, &dz);
-    sw += du * n;
-    sb += du;
-  }
-  p.partial[(2 * blockIdx.y) * cols + col] = sw;
-  p.partial[(2 * blockIdx.y + 1) * cols + col] = sb;
-}
-
-__global__ void __launch_bounds__(128) gdp_norm_finish_kernel(NormProblem p) {
-  const int64_t cols = p.per_head ? p.H * p.D : p.D, col = (int64_t)blockIdx.x * 128 + threadIdx.x;
-  if (col >= cols) return;
-  float sw = 0.f, sb = 0.f;
-  for (int s = 0; s < kSlabs; ++s) {
-    sw += p.partial[(2 * s) * cols + col];
-    sb += p.partial[(2 * s + 1) * cols + col];
-  }
-  p.dw[col] = sw;
-  if (p.db) p.db[col] = sb;
+gdp_status norm_status(cudaError_t e, const char *what) {
+  if (e == cudaSuccess) return GDP_OK;
+  set_last_error("%s: %s", what, cudaGetErrorString(e));
+  return GDP_ERR_CUDA;
 }
 
 gdp_status check_norm(int64_t T, int64_t H, int64_t D, float eps, int type, int act, bool has_gate, const float *w) {
@@ -253,18 +91,25 @@ GDP_EXPORT gdp_status gdp_group_norm(const gdp_group_norm_args *a, void *stream)
   p.w = a->weight; p.b = a->bias; p.y = a->y;
   p.o_codes = a->o_codes; p.o_scales = a->o_scales; p.z_codes = a->z_codes; p.z_scales = a->z_scales;
   p.T = a->T; p.H = a->H; p.D = a->D; p.eps = a->eps;
-  p.type = a->dtype; p.center = a->center != 0; p.per_head = a->per_head != 0; p.act = a->activation;
-  const int64_t blocks = (p.T * p.H + kWarps - 1) / kWarps;
-  if (blocks > INT32_MAX) return fail(GDP_ERR_UNSUPPORTED, "too many rows for one launch");
-  gdp_norm_fwd_kernel<<<(unsigned)blocks, kWarps * 32, 0, (cudaStream_t)stream>>>(p);
-  return launch_status("group norm kernel");
+  p.inv_d = 1.f / (float)p.D;
+  p.center = a->center != 0; p.per_head = a->per_head != 0; p.act = a->activation;
+  const int vec = p.D % 8 == 0 && vec_ok(p.o, p.o_st, p.o_sh, p.T, p.H, a->dtype) && (!p.z || vec_ok(p.z, p.z_st, p.z_sh, p.T, p.H, a->dtype)) &&
+                  aligned(p.y, 16) && aligned(p.o_codes, 8) && aligned(p.z_codes, 8);
+  const NormPlan n = norm_plan(p.T, p.H, p.D, p.per_head, vec, sm_count());
+  p.heads = n.heads; p.groups = n.groups; p.parts = n.parts;
+  cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e = a->dtype == GDP_DTYPE_BF16  ? launch_norm_fwd<__nv_bfloat16>(p, n, s)
+                        : a->dtype == GDP_DTYPE_F16 ? launch_norm_fwd<__half>(p, n, s)
+                                                    : launch_norm_fwd<float>(p, n, s);
+  return norm_status(e, "group norm kernel");
 }
 
 GDP_EXPORT size_t gdp_group_norm_workspace_bytes(int64_t T, int64_t H, int64_t D, int per_head) {
   using namespace gdp::layer;
   if (T < 0 || H < 1 || D < 1 || D > 8192 || H > (1 << 20) || T > INT32_MAX) return 0;
   const size_t cols = per_head ? (size_t)(H * D) : (size_t)D;
-  return ((size_t)(T * H) * 8 + 255) / 256 * 256 + (size_t)kSlabs * 2 * cols * 4 + 256;
+  const int64_t a = norm_plan(T, H, D, per_head, 0, sm_count()).parts, b = norm_plan(T, H, D, per_head, 1, sm_count()).parts;
+  return ((size_t)(a > b ? a : b) * 2 * cols * 4 + 255) / 256 * 256;
 }
 
 GDP_EXPORT gdp_status gdp_group_norm_backward(const gdp_group_norm_backward_args *a, void *stream) {
@@ -301,15 +146,22 @@ GDP_EXPORT gdp_status gdp_group_norm_backward(const gdp_group_norm_backward_args
   p.dy = a->d_y; p.dy_st = a->d_y_stride_t; p.dy_sh = a->d_y_stride_h;
   p.d_o = a->d_o; p.d_z = a->d_z; p.dw = a->d_weight; p.db = a->d_bias;
   p.T = a->T; p.H = a->H; p.D = a->D; p.eps = a->eps;
-  p.type = a->dtype; p.center = a->center != 0; p.per_head = a->per_head != 0; p.act = a->activation;
-  p.stats = static_cast<float *>(a->workspace);
-  p.partial = p.stats + ((size_t)(p.T * p.H) * 2 + 63) / 64 * 64;
+  p.inv_d = 1.f / (float)p.D;
+  p.center = a->center != 0; p.per_head = a->per_head != 0; p.act = a->activation;
+  p.partial = static_cast<float *>(a->workspace);
   cudaStream_t s = (cudaStream_t)stream;
-  const int64_t blocks = (p.T * p.H + kWarps - 1) / kWarps, cols = p.per_head ? p.H * p.D : p.D;
-  if (blocks > INT32_MAX) return fail(GDP_ERR_UNSUPPORTED, "too many rows for one launch");
-  if (blocks > 0) gdp_norm_bwd_kernel<<<(unsigned)blocks, kWarps * 32, 0, s>>>(p);
-  const dim3 grid((unsigned)((cols + 127) / 128), kSlabs);
-  gdp_norm_columns_kernel<<<grid, 128, 0, s>>>(p);
-  gdp_norm_finish_kernel<<<grid.x, 128, 0, s>>>(p);
-  return launch_status("group norm backward kernels");
+  const int vec = p.D % 8 == 0 && vec_ok(p.dy, p.dy_st, p.dy_sh, p.T, p.H, a->dtype) &&
+                  (!p.o || vec_ok(p.o, p.o_st, p.o_sh, p.T, p.H, a->dtype)) && (!p.z || vec_ok(p.z, p.z_st, p.z_sh, p.T, p.H, a->dtype)) &&
+                  aligned(p.o_codes_in, 8) && aligned(p.z_codes_in, 8) && aligned(p.d_o, 16) && aligned(p.d_z, 16);
+  const NormPlan n = norm_plan(p.T, p.H, p.D, p.per_head, vec, sm_count());
+  p.heads = n.heads; p.groups = n.groups; p.parts = n.parts;
+  cudaError_t e = a->dtype == GDP_DTYPE_BF16  ? launch_norm_bwd<__nv_bfloat16>(p, n, s)
+                  : a->dtype == GDP_DTYPE_F16 ? launch_norm_bwd<__half>(p, n, s)
+                                              : launch_norm_bwd<float>(p, n, s);
+  if (e == cudaSuccess) {
+    const int64_t cols = p.per_head ? p.H * p.D : p.D;
+    gdp_norm_finish_kernel<<<dim3((unsigned)((cols + 31) / 32), p.db ? 2 : 1), 32 * kFinishWarps, 0, s>>>(p.partial, n.parts, cols, p.dw, p.db);
+    e = cudaGetLastError();
+  }
+  return norm_status(e, "group norm backward kernels");
 }

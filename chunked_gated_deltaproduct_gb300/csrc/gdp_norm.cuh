@@ -1,0 +1,87 @@
+// gdp_norm.cuh -- the grouped norm's problem, launch plan and launchers.
+#pragma once
+
+#include <type_traits>
+
+#include "gdp_layer.cuh"
+
+namespace gdp {
+namespace layer {
+
+struct NormProblem {
+  const void *o, *z;
+  int64_t o_st, o_sh, z_st, z_sh;
+  const int8_t *o_codes_in, *z_codes_in;  // backward: read instead of o and z
+  const float *o_scales_in, *z_scales_in;
+  const float *w, *b;
+  void *y;
+  int8_t *o_codes, *z_codes;
+  float *o_scales, *z_scales;
+  const void *dy;
+  int64_t dy_st, dy_sh;
+  void *d_o, *d_z;
+  float *dw, *db, *partial;
+  int64_t T, H, D;
+  int64_t heads, groups, parts;  // see NormPlan
+  float eps, inv_d;
+  int center, per_head, act;
+};
+
+// Threads of a CTA: groups of L lanes (L > 0), or one group (L = 0: up to 512 threads).
+template <int L>
+constexpr int kNormThreads = L > 0 ? 256 : 512;
+
+// How a call runs: groups of `lanes` threads (0: a CTA of `threads`), `chunks` of eight channels each.
+// The groups number grid * (groups per CTA), a multiple of `heads`; group i keeps head i % heads (none
+// when that is H or more), and there are `parts` column sums to add up.
+struct NormPlan {
+  int vec, lanes, chunks, threads;
+  int64_t grid, heads, groups, parts;
+};
+
+inline NormPlan norm_plan(int64_t T, int64_t H, int64_t D, int per_head, int vec, int sms) {
+  NormPlan n{};
+  n.vec = vec;
+  n.chunks = 1;
+  n.threads = 256;
+  if (D <= 256) {
+    n.lanes = !vec || D > 128 ? 32 : D > 64 ? 16 : 8;
+  } else {
+    const int64_t eights = (D + 7) / 8;
+    n.chunks = eights > 512 ? 2 : 1;
+    n.threads = (int)((eights + 32 * n.chunks - 1) / (32 * n.chunks) * 32);
+  }
+  const int64_t per_cta = n.lanes ? n.threads / n.lanes : 1;
+  // CTAs must come in multiples of m for every group to keep its head; where that is too coarse, heads
+  // are rounded up to whole CTAs and the last groups have none
+  int64_t a = H, b = per_cta;
+  while (b) {
+    const int64_t c = a % b;
+    a = b;
+    b = c;
+  }
+  int64_t m = H / a;
+  n.heads = H;
+  if (m > 32) {
+    n.heads = (H + per_cta - 1) / per_cta * per_cta;
+    m = n.heads / per_cta;
+  }
+  const int64_t resident = (int64_t)sms * (2048 / n.threads < 8 ? 2048 / n.threads : 8) / 2;
+  const int64_t need = (T * n.heads + per_cta - 1) / per_cta;
+  n.grid = (need + m - 1) / m * m;
+  if (n.grid > resident) n.grid = resident / m * m;
+  if (n.grid < m) n.grid = m;
+  n.groups = n.grid * per_cta;
+  n.parts = per_head ? n.groups / n.heads : n.grid;
+  return n;
+}
+
+template <typename T>
+cudaError_t launch_norm_fwd(const NormProblem &p, const NormPlan &n, cudaStream_t stream);
+template <typename T>
+cudaError_t launch_norm_bwd(const NormProblem &p, const NormPlan &n, cudaStream_t stream);
+
+int sm_count();  // of the current device (gdp_recurrence.cu)
+
+}  // namespace layer
+}  // namespace gdp
