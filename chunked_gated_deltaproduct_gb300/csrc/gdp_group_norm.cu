@@ -8,7 +8,7 @@ namespace {
 
 // Adds up the parts of every column in a fixed order: 32 columns per CTA, each warp a stride of the
 // parts, then the warps' sums in turn.
-constexpr int kFinishWarps = 16;
+constexpr int kFinishWarps = 32;
 __global__ void __launch_bounds__(32 * kFinishWarps) gdp_norm_finish_kernel(const float *partial, int64_t parts, int64_t cols, float *dw,
                                                                             float *db) {
   __shared__ float sums[kFinishWarps][32];
@@ -17,7 +17,7 @@ __global__ void __launch_bounds__(32 * kFinishWarps) gdp_norm_finish_kernel(cons
   const float *from = partial + (blockIdx.y ? parts * cols : 0);
   float s = 0.f;
   if (col < cols) {
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t i = warp; i < parts; i += kFinishWarps) s += from[i * cols + col];
   }
   sums[warp][lane] = s;

@@ -29,6 +29,64 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n.reg .b64 x, y, z, w;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\n"
+      "fma.rn.f32x2 w, x, y, z;\nmov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n.reg .b64 x, y, w;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmul.rn.f32x2 w, x, y;\nmov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n.reg .b64 x, y, w;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 w, x, y;\nmov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two stored values in one register (16-bit types), widened, and back.
+template <typename T>
+__device__ __forceinline__ float2 widen(uint32_t v);
+template <>
+__device__ __forceinline__ float2 widen<__nv_bfloat16>(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 widen<__half>(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+template <typename T>
+__device__ __forceinline__ uint32_t narrow(float2 v);
+template <>
+__device__ __forceinline__ uint32_t narrow<__nv_bfloat16>(float2 v) {
+  const __nv_bfloat162 h = __float22bfloat162_rn(v);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t narrow<__half>(float2 v) {
+  const __half2 h = __float22half2_rn(v);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 // e^x by the hardware's base-2 exponential: relative error about 2^-22 + |x| 2^-24, 0 below 2^-126.
 __device__ __forceinline__ float exp_fast(float x) {
   float y;
@@ -61,21 +119,24 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 
 // Inverse scale of a checkpoint block from its largest absolute value: 127 / amax cut to four
 // significant bits (its product with a 16-bit value is exact in fp32, so the codes do not depend on
-// the arithmetic), 0 for a block of zeros or next to it.
+// the arithmetic), 0 for a block of zeros or next to it.  T: the type the value came from.  Of the
+// 16-bit types' values, 127 / amax is a four-bit number only where amax is 127 times a power of two,
+// and otherwise at least 2^-15 relative away from one (amax times the number is an integer of at most
+// 15 bits); so the approximate reciprocal (2^-22), raised by 2^-20, is cut to the same four bits.
+template <typename T>
 __device__ __forceinline__ float block_inverse(uint32_t amax_bits) {
-  if (amax_bits >= 0x7f800000u) return 0.f;
   const float amax = __uint_as_float(amax_bits);
-  if (amax < kTinyAmax) return 0.f;
-  return __uint_as_float(__float_as_uint(__fdiv_rn(127.f, amax)) & 0xfff00000u);
+  // (amax / 256, so that the largest values' reciprocals are not flushed to zero)
+  const float quotient = sizeof(T) == 4 ? __fdiv_rn(127.f, amax) : rcp(amax * 0x1p-8f) * (127.f * 0x1p-8f * (1.f + 0x1p-20f));
+  const bool plain = amax >= kTinyAmax && amax_bits < 0x7f800000u;
+  return plain ? __uint_as_float(__float_as_uint(quotient) & 0xfff00000u) : 0.f;
 }
+// 1 / inverse, correctly rounded: the inverse is (8 + i) / 8 times a power of two.
+__constant__ const float kEighths[8] = {8.f / 8.f, 8.f / 9.f, 8.f / 10.f, 8.f / 11.f, 8.f / 12.f, 8.f / 13.f, 8.f / 14.f, 8.f / 15.f};
 __device__ __forceinline__ float block_scale(uint32_t amax_bits, float inverse) {
-  if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
-  return inverse > 0.f ? __fdiv_rn(1.f, inverse) : 0.f;
-}
-// round-to-even(v k) as a signed byte: v k + 1.5 2^23 in one rounding leaves the integer in the low
-// bits.  A zero inverse gives code 0 whatever v is (0 times an infinity would be NaN).
-__device__ __forceinline__ uint32_t block_code(float v, float inverse) {
-  return inverse > 0.f ? (__float_as_uint(fmaf(v, inverse, 12582912.f)) & 0xffu) : 0u;
+  const uint32_t b = __float_as_uint(inverse);
+  const float s = kEighths[b >> 20 & 7u] * __uint_as_float((254u << 23) - (b & 0x7f800000u));
+  return amax_bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : b == 0u ? 0.f : s;
 }
 
 // ---- host side ----

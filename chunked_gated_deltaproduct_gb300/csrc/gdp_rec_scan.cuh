@@ -105,24 +105,6 @@ __device__ __forceinline__ int raw_offset(const RowSource &src, int64_t t, int64
   return sizeof(T) < 4 ? (int)((reinterpret_cast<uintptr_t>(src.base) + (uintptr_t)((t * src.stride + c0) * (int64_t)sizeof(T))) & 3u) : 0;
 }
 
-// The lane's two channels of tile row r, as fp32.
-template <typename T, bool RAW>
-__device__ __forceinline__ float2 read_pair(const unsigned char *tile, int r, int lane, int offset) {
-  if constexpr (sizeof(T) == 4) {
-    return *reinterpret_cast<const float2 *>(tile + r * tile_pitch<T>(false) + lane * 8);
-  } else {
-    T v[2];
-    if constexpr (RAW) {
-      const T *p = reinterpret_cast<const T *>(tile + r * tile_pitch<T>(true) + offset) + 2 * lane;
-      v[0] = p[0];
-      v[1] = p[1];
-    } else {
-      *reinterpret_cast<uint32_t *>(v) = *reinterpret_cast<const uint32_t *>(tile + r * tile_pitch<T>(false) + lane * 4);
-    }
-    return make_float2(to_f32(v[0]), to_f32(v[1]));
-  }
-}
-
 // The pair as it is stored: 16-bit types packed in one register.
 template <typename T>
 struct Packed {
@@ -148,35 +130,16 @@ __device__ __forceinline__ float2 unpack(typename Packed<T>::type v) {
   if constexpr (sizeof(T) == 4) {
     return v;
   } else if constexpr (sizeof(T) == 2) {
-    T e[2];
-    *reinterpret_cast<uint32_t *>(e) = v;
-    return make_float2(to_f32(e[0]), to_f32(e[1]));
+    return widen<T>(v);
   }
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n.reg .b64 x, y, z, w;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\n"
-      "fma.rn.f32x2 w, x, y, z;\nmov.b64 {%0, %1}, w;\n}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n.reg .b64 x, y, w;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmul.rn.f32x2 w, x, y;\nmov.b64 {%0, %1}, w;\n}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
 // Both channels' decay and input factor.
 template <int GATE>
 __device__ __forceinline__ void gate_pair(float2 g, float2 *a, float2 *f) {
   if constexpr (GATE == GDP_GATE_LOG) {
-    g = mul2(g, make_float2(kLog2e, kLog2e));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a->x) : "f"(g.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a->y) : "f"(g.y));
+    g = mul2(g, both(kLog2e));
+    *a = make_float2(ex2(g.x), ex2(g.y));
     *f = make_float2(1.f, 1.f);
   } else {
     gate_eval<GATE>(g.x, &a->x, &f->x);
@@ -190,8 +153,7 @@ __device__ __forceinline__ void write_pair(T *p, float2 v, bool both, bool vec) 
     if constexpr (sizeof(T) == 4) {
       *reinterpret_cast<float2 *>(p) = v;
     } else {
-      T o[2] = {from_f32<T>(v.x), from_f32<T>(v.y)};
-      *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<const uint32_t *>(o);
+      *reinterpret_cast<uint32_t *>(p) = narrow<T>(v);
     }
   } else {
     p[0] = from_f32<T>(v.x);
