@@ -96,6 +96,7 @@ GDP_EXPORT gdp_status gdp_group_norm(const gdp_group_norm_args *a, void *stream)
   const int vec = p.D % 8 == 0 && vec_ok(p.o, p.o_st, p.o_sh, p.T, p.H, a->dtype) && (!p.z || vec_ok(p.z, p.z_st, p.z_sh, p.T, p.H, a->dtype)) &&
                   aligned(p.y, 16) && aligned(p.o_codes, 8) && aligned(p.z_codes, 8);
   const NormPlan n = norm_plan(p.T, p.H, p.D, p.per_head, vec, sm_count());
+  p.vec_cols = p.D % 8 == 0 && aligned(p.w, 16) && aligned(p.b, 16);
   p.heads = n.heads; p.groups = n.groups; p.parts = n.parts;
   cudaStream_t s = (cudaStream_t)stream;
   const cudaError_t e = a->dtype == GDP_DTYPE_BF16  ? launch_norm_fwd<__nv_bfloat16>(p, n, s)
@@ -154,6 +155,7 @@ GDP_EXPORT gdp_status gdp_group_norm_backward(const gdp_group_norm_backward_args
                   (!p.o || vec_ok(p.o, p.o_st, p.o_sh, p.T, p.H, a->dtype)) && (!p.z || vec_ok(p.z, p.z_st, p.z_sh, p.T, p.H, a->dtype)) &&
                   aligned(p.o_codes_in, 8) && aligned(p.z_codes_in, 8) && aligned(p.d_o, 16) && aligned(p.d_z, 16);
   const NormPlan n = norm_plan(p.T, p.H, p.D, p.per_head, vec, sm_count());
+  p.vec_cols = p.D % 8 == 0 && aligned(p.w, 16) && aligned(p.b, 16);
   p.heads = n.heads; p.groups = n.groups; p.parts = n.parts;
   cudaError_t e = a->dtype == GDP_DTYPE_BF16  ? launch_norm_bwd<__nv_bfloat16>(p, n, s)
                   : a->dtype == GDP_DTYPE_F16 ? launch_norm_bwd<__half>(p, n, s)

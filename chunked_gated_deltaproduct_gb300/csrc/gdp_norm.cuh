@@ -25,32 +25,35 @@ struct NormProblem {
   int64_t heads, groups, parts;  // see NormPlan
   float eps, inv_d;
   int center, per_head, act;
+  int vec_cols;  // weight and bias rows start on 16-byte boundaries
 };
 
 // Threads of a CTA: groups of L lanes (L > 0), or one group (L = 0: up to 512 threads).
 template <int L>
 constexpr int kNormThreads = L > 0 ? 256 : 512;
 
-// How a call runs: groups of `lanes` threads (0: a CTA of `threads`), `chunks` of eight channels each.
+#ifndef FWDB
+#define FWDB 3
+#define BWDB 2
+#define GRIDM 4
+#endif
+// How a call runs: groups of `lanes` threads (0: a CTA of `threads`), sixteen channels each.
 // The groups number grid * (groups per CTA), a multiple of `heads`; group i keeps head i % heads (none
 // when that is H or more), and there are `parts` column sums to add up.
 struct NormPlan {
-  int vec, lanes, chunks, threads;
+  int vec, lanes, threads;
   int64_t grid, heads, groups, parts;
 };
 
 inline NormPlan norm_plan(int64_t T, int64_t H, int64_t D, int per_head, int vec, int sms) {
   NormPlan n{};
   n.vec = vec;
-  n.chunks = 1;
   n.threads = 256;
-  if (D <= 256) {
-    n.lanes = !vec || D > 128 ? 32 : D > 64 ? 16 : 8;
-  } else {
-    const int64_t eights = (D + 7) / 8;
-    n.chunks = eights > 512 ? 2 : 1;
-    n.threads = (int)((eights + 32 * n.chunks - 1) / (32 * n.chunks) * 32);
-  }
+  if (D <= 64 && vec) n.lanes = 4;
+  else if (D <= 128) n.lanes = 8;
+  else if (D <= 256 && vec) n.lanes = 16;
+  else if (D <= 512) n.lanes = 32;
+  else n.threads = (int)((D + 511) / 512 * 32);
   const int64_t per_cta = n.lanes ? n.threads / n.lanes : 1;
   // CTAs must come in multiples of m for every group to keep its head; where that is too coarse, heads
   // are rounded up to whole CTAs and the last groups have none
@@ -66,7 +69,8 @@ inline NormPlan norm_plan(int64_t T, int64_t H, int64_t D, int per_head, int vec
     n.heads = (H + per_cta - 1) / per_cta * per_cta;
     m = n.heads / per_cta;
   }
-  const int64_t resident = (int64_t)sms * (2048 / n.threads < 8 ? 2048 / n.threads : 8) / 2;
+  // CTAs of 256 threads: a few per SM; smaller ones: as many threads
+  const int64_t resident = (int64_t)sms * (n.threads >= 256 ? GRIDM : GRIDM * 256 / n.threads);
   const int64_t need = (T * n.heads + per_cta - 1) / per_cta;
   n.grid = (need + m - 1) / m * m;
   if (n.grid > resident) n.grid = resident / m * m;

@@ -1,27 +1,42 @@
 // gdp_norm_body.cuh -- the grouped norm with an activated gate: forward (with 8-bit checkpoints) and
 // backward kernels (gdp_layer.h).
 //
-// A row (token, head) is held by a group of threads, eight channels per thread and chunk: 8, 16 or 32
-// lanes of a warp (D up to 64, 128, 256), or a whole CTA.  A group keeps one head, so that its weights
-// stay in registers and the backward's sums over tokens (dweight, dbias) accumulate there; it walks
-// over tokens with the next row's loads in flight.  Those sums leave once per CTA (or per group where
-// every head has its own weights) and a second kernel adds them up in a fixed order.
+// A row (token, head) is held by a group of threads, sixteen channels per thread: 4, 8, 16 or 32 lanes
+// of a warp (D up to 64, 128, 256, 512), or a whole CTA.  A group keeps one head, so that the backward's
+// sums over tokens (dweight, dbias) accumulate in registers; it walks over tokens with the next row's
+// loads in flight.  Those sums leave once per CTA (or per group where every head has its own weights)
+// and a second kernel adds them up in a fixed order.
 #pragma once
 
 #include "gdp_norm.cuh"
 
-#ifndef FWDB
-#define FWDB 4
-#define BWDB 3
-#endif
 namespace gdp {
 namespace layer {
 namespace {
 
-// Eight values of a row as they lie in memory.
+constexpr int kPer = 16;  // channels of a thread: 8 cost 42 instructions per channel in the reductions and
+                          // addresses alone (966 us for the training step of 65536 x 32 x 128)
+
+// Where a thread's channels lie in its row.  VEC: sixteen consecutive ones; else strided by the width of
+// a run of lanes, so that the lanes' accesses are runs of memory.  Either way a checkpoint block of 128
+// channels lies in eight lanes (a shorter row in its four).
+template <bool VEC, int L>
+struct Place {
+  static constexpr int kRun = L == 4 ? 4 : 8;
+  int id, first;  // thread of the group, its first channel
+  __device__ __forceinline__ Place() {
+    id = L > 0 ? (int)threadIdx.x % (L > 0 ? L : 1) : (int)threadIdx.x;
+    first = VEC ? id * kPer : id / kRun * (kRun * kPer) + id % kRun;
+  }
+  __device__ __forceinline__ int at(int j) const { return first + (VEC ? j : kRun * j); }
+  __device__ __forceinline__ bool leads_block() const { return id % kRun == 0; }
+  __device__ __forceinline__ int block() const { return first / kBlock; }
+};
+
+// Sixteen values of a row as they lie in memory.
 template <typename T>
-struct alignas(8 * sizeof(T) > 16 ? 16 : 8 * sizeof(T)) Eight {
-  T v[8];
+struct alignas(16) Sixteen {
+  T v[kPer];
   __device__ __forceinline__ uint32_t word(int i) const { return reinterpret_cast<const uint32_t *>(v)[i]; }
   __device__ __forceinline__ float2 pair(int i) const {
     if constexpr (sizeof(T) == 4) return make_float2(v[2 * i], v[2 * i + 1]);
@@ -36,144 +51,153 @@ struct alignas(8 * sizeof(T) > 16 ? 16 : 8 * sizeof(T)) Eight {
     }
   }
 };
-// Source of o and z: a tensor, or codes with the scales of the (one or two) blocks the eight lie in.
-template <typename T, bool Q8, bool VEC>
+
+// VEC: 16 bytes at a time, eight channels (of codes: sixteen) at least, D a multiple of eight.
+template <typename T, bool VEC, int L>
+__device__ __forceinline__ void load_row(Sixteen<T> &e, const T *row, const Place<VEC, L> &pl, int D, bool on) {
+  if constexpr (VEC && sizeof(T) == 1) {
+    uint2 *to = reinterpret_cast<uint2 *>(e.v);
+    const uint2 *from = reinterpret_cast<const uint2 *>(row + pl.first);
+    to[0] = on && pl.first < D ? __ldcs(from) : make_uint2(0u, 0u);
+    to[1] = on && pl.first + 8 < D ? __ldcs(from + 1) : make_uint2(0u, 0u);
+  } else if constexpr (VEC) {
+    uint4 *to = reinterpret_cast<uint4 *>(e.v);
+    const uint4 *from = reinterpret_cast<const uint4 *>(row + pl.first);
+    constexpr int n = (int)sizeof(T);  // 16-byte words
+#pragma unroll
+    for (int i = 0; i < n; ++i) to[i] = on && pl.first + i / (n / 2) * 8 < D ? __ldcs(from + i) : make_uint4(0u, 0u, 0u, 0u);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if constexpr (sizeof(T) == 1) e.v[j] = on && pl.at(j) < D ? row[pl.at(j)] : (T)0;
+      else e.v[j] = on && pl.at(j) < D ? row[pl.at(j)] : from_f32<T>(0.f);
+    }
+  }
+}
+template <typename T, bool VEC, int L>
+__device__ __forceinline__ void store_row(T *row, const Sixteen<T> &e, const Place<VEC, L> &pl, int D) {
+  if constexpr (VEC && sizeof(T) == 1) {
+    const uint2 *from = reinterpret_cast<const uint2 *>(e.v);
+    uint2 *to = reinterpret_cast<uint2 *>(row + pl.first);
+    if (pl.first < D) __stcs(to, from[0]);
+    if (pl.first + 8 < D) __stcs(to + 1, from[1]);
+  } else if constexpr (VEC) {
+    const uint4 *from = reinterpret_cast<const uint4 *>(e.v);
+    uint4 *to = reinterpret_cast<uint4 *>(row + pl.first);
+    constexpr int n = (int)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      if (pl.first + i / (n / 2) * 8 < D) __stcs(to + i, from[i]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (pl.at(j) < D) row[pl.at(j)] = e.v[j];
+  }
+}
+
+// Source of the backward's o and z: a tensor, or codes with the scale of the block they lie in.
+template <typename T, bool Q8>
 struct Source {
-  Eight<typename std::conditional<Q8, int8_t, T>::type> e;
-  float scale[Q8 ? (VEC ? 1 : 2) : 1];
+  Sixteen<typename std::conditional<Q8, int8_t, T>::type> e;
+  float scale;
   __device__ __forceinline__ float2 pair(int i) const {
     if constexpr (Q8) {
       // a byte plus 128 under the exponent of 2^23 is 2^23 + 128 + code
       const uint32_t w = e.word(i >> 1) ^ 0x80808080u;
       const float2 m = make_float2(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + (i & 1) * 2)),
                                    __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441 + (i & 1) * 2)));
-      return mul2(add2(m, both(-8388736.f)), both(scale[VEC ? 0 : i >> 1]));
+      return mul2(add2(m, both(-8388736.f)), both(scale));
     } else {
       return e.pair(i);
     }
   }
 };
-
-// Where a thread's channels lie in its row.  VEC: eight consecutive ones; else eight 32 apart, so that a
-// warp's accesses stay one run of memory.  Either way a checkpoint block of 128 channels lies in one warp:
-// in 16 lanes (VEC), or in four of the eight of all 32.
-template <bool VEC, int L>
-struct Place {
-  int id, first, width;  // thread of the group, first channel of chunk 0, channels of a chunk of the whole group
-  __device__ __forceinline__ Place() {
-    id = L > 0 ? (int)threadIdx.x % (L > 0 ? L : 1) : (int)threadIdx.x;
-    width = (L > 0 ? L : (int)blockDim.x) * 8;
-    first = VEC ? id * 8 : (id >> 5) * 256 + (id & 31);
-  }
-  __device__ __forceinline__ int at(int k, int j) const { return k * width + first + (VEC ? j : 32 * j); }
-};
-
-template <typename T, bool VEC, int L>
-__device__ __forceinline__ void load_eight(Eight<T> &e, const T *row, const Place<VEC, L> &pl, int k, int D, bool on) {
-  if constexpr (VEC) {
-    using V = typename std::conditional<sizeof(T) == 1, uint2, uint4>::type;
-    constexpr int n = (int)(8 * sizeof(T) / sizeof(V));
-    V *to = reinterpret_cast<V *>(e.v);
-    const bool in = on && pl.at(k, 0) < D;
-#pragma unroll
-    for (int i = 0; i < n; ++i) to[i] = in ? __ldcs(reinterpret_cast<const V *>(row + pl.at(k, 0)) + i) : V{};
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const bool in = on && pl.at(k, j) < D;
-      if constexpr (sizeof(T) == 1) e.v[j] = in ? row[pl.at(k, j)] : (T)0;
-      else e.v[j] = in ? row[pl.at(k, j)] : from_f32<T>(0.f);
-    }
-  }
-}
-template <typename T, bool VEC, int L>
-__device__ __forceinline__ void store_eight(T *row, const Eight<T> &e, const Place<VEC, L> &pl, int k, int D) {
-  if constexpr (VEC) {
-    using V = typename std::conditional<sizeof(T) == 1, uint2, uint4>::type;
-    constexpr int n = (int)(8 * sizeof(T) / sizeof(V));
-    if (pl.at(k, 0) < D) {
-#pragma unroll
-      for (int i = 0; i < n; ++i) __stcs(reinterpret_cast<V *>(row + pl.at(k, 0)) + i, reinterpret_cast<const V *>(e.v)[i]);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (pl.at(k, j) < D) row[pl.at(k, j)] = e.v[j];
-  }
-}
-
 template <typename T, bool Q8, bool VEC, int L>
-__device__ __forceinline__ void load_source(Source<T, Q8, VEC> &s, const void *base, int64_t at, const float *scales, const Place<VEC, L> &pl,
-                                            int k, int D, bool on) {
-  using E = typename std::conditional<Q8, int8_t, T>::type;
-  load_eight<E, VEC, L>(s.e, static_cast<const E *>(base) + at, pl, k, D, on);
+__device__ __forceinline__ void load_source(Source<T, Q8> &s, const void *tensor, int64_t at, const int8_t *codes, const float *scales,
+                                            int64_t row, int D, int blocks, const Place<VEC, L> &pl, bool on) {
   if constexpr (Q8) {
-#pragma unroll
-    for (int i = 0; i < (VEC ? 1 : 2); ++i) s.scale[i] = on && pl.at(k, 4 * i) < D ? scales[pl.at(k, 4 * i) / kBlock] : 0.f;
-  }
-}
-
-// Sums over the group's threads.  `turn` alternates the CTA-wide buffers, so that one barrier per sum is
-// enough (a warp writes a buffer again only after the barrier of the sum between).
-template <int L>
-__device__ __forceinline__ float group_sum(float v, float (*red)[32], int &turn) {
-  constexpr int kLanes = L > 0 ? L : 32;
-#pragma unroll
-  for (int s = kLanes / 2; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-  if constexpr (L == 0) {
-    float *buf = red[turn & 1];
-    ++turn;
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    const int warps = (int)blockDim.x >> 5;
-    v = (int)(threadIdx.x & 31) < warps ? buf[threadIdx.x & 31] : 0.f;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-  }
-  return v;
-}
-
-// The two sums at once.
-template <int L>
-__device__ __forceinline__ float2 group_sum2(float2 v, float2 (*red)[32], int &turn) {
-  constexpr int kLanes = L > 0 ? L : 32;
-#pragma unroll
-  for (int s = kLanes / 2; s > 0; s >>= 1)
-    v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, s), __shfl_xor_sync(0xffffffffu, v.y, s)));
-  if constexpr (L == 0) {
-    float2 *buf = red[turn & 1];
-    ++turn;
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    const int warps = (int)blockDim.x >> 5;
-    v = (int)(threadIdx.x & 31) < warps ? buf[threadIdx.x & 31] : both(0.f);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1)
-      v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, s), __shfl_xor_sync(0xffffffffu, v.y, s)));
-  }
-  return v;
-}
-
-// Absolute values' largest bits: of 16-bit types as 16-bit patterns, two at a time.
-template <typename T>
-__device__ __forceinline__ uint32_t top_bits(uint32_t top, const Eight<T> &e, int word) {
-  if constexpr (sizeof(T) == 4) {
-    return max(top, abs_bits(e.v[word]));
+    load_row<int8_t, VEC, L>(s.e, codes + row * D, pl, D, on);
+    s.scale = on && pl.first < D ? __ldcs(scales + row * blocks + pl.block()) : 0.f;
   } else {
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(top), "r"(e.word(word) & 0x7fff7fffu));
-    return r;
+    load_row<T, VEC, L>(s.e, static_cast<const T *>(tensor) + at, pl, D, on);
   }
 }
-template <typename T>
-__device__ __forceinline__ uint32_t top_one(uint32_t top) {
-  if constexpr (sizeof(T) == 4) return top;
-  else return max(top & 0xffffu, top >> 16);
+
+// The group's weights (or biases) at pairs i and i + 1 of the thread's channels: read for every row (a few
+// KB that stay in L1), so that they take no registers meanwhile.
+template <bool VEC, int L>
+__device__ __forceinline__ void load_columns(float2 *to, const float *from, int i, const Place<VEC, L> &pl, int D, int vec) {
+  if (VEC && vec) {
+    const float4 q = pl.first + i / 4 * 8 < D ? __ldg(reinterpret_cast<const float4 *>(from + pl.first) + i / 2) : make_float4(0.f, 0.f, 0.f, 0.f);
+    to[0] = make_float2(q.x, q.y);
+    to[1] = make_float2(q.z, q.w);
+  } else {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int d0 = pl.at(2 * (i + u)), d1 = pl.at(2 * (i + u) + 1);
+      to[u] = make_float2(d0 < D ? __ldg(from + d0) : 0.f, d1 < D ? __ldg(from + d1) : 0.f);
+    }
+  }
 }
+
+// Sums over the group's threads, one or two at once.  `turn` alternates the CTA-wide buffers, so that one
+// barrier per sum is enough (a warp writes a buffer again only after the barrier of the sum between).
+__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 plus(float2 a, float2 b) { return add2(a, b); }
+__device__ __forceinline__ float from_lane(float v, int s) { return __shfl_xor_sync(0xffffffffu, v, s); }
+__device__ __forceinline__ float2 from_lane(float2 v, int s) { return make_float2(from_lane(v.x, s), from_lane(v.y, s)); }
+template <int L, typename V>
+__device__ __forceinline__ V group_sum(V v, float2 (*red)[32], int &turn) {
+  constexpr int kLanes = L > 0 ? L : 32;
+#pragma unroll
+  for (int s = kLanes / 2; s > 0; s >>= 1) v = plus(v, from_lane(v, s));
+  if constexpr (L == 0) {
+    V *buf = reinterpret_cast<V *>(red[turn & 1]);
+    ++turn;
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = buf[0];
+    const int warps = (int)blockDim.x >> 5;
+    for (int w = 1; w < warps; ++w) v = plus(v, buf[w]);
+  }
+  return v;
+}
+
+// ---- checkpoints ----
+// Largest absolute value of the sixteen: bits of the type itself (NaN above all).
 template <typename T>
-__device__ __forceinline__ uint32_t top_as_f32(uint32_t top) {
-  if constexpr (sizeof(T) == 4) return top;
-  else return __float_as_uint(widen<T>(top).x);
+__device__ __forceinline__ uint32_t top_bits(const Sixteen<T> &e) {
+  uint32_t top = 0;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) top = max(top, abs_bits(e.v[i]));
+    return top;
+  } else {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    T2 m = __habs2(*reinterpret_cast<const T2 *>(&e.v[0]));
+#pragma unroll
+    for (int i = 1; i < kPer / 2; ++i) m = __hmax2_nan(__habs2(*reinterpret_cast<const T2 *>(&e.v[2 * i])), m);
+    top = *reinterpret_cast<const uint32_t *>(&m);
+    return max(top & 0xffffu, top >> 16);
+  }
+}
+// Of the block: two tensors' at once.
+template <typename T, int L>
+__device__ __forceinline__ void block_tops(uint32_t &a, uint32_t &b) {
+  constexpr int kRun = L == 4 ? 4 : 8;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int s = kRun / 2; s > 0; s >>= 1) {
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, s));
+      b = max(b, __shfl_xor_sync(0xffffffffu, b, s));
+    }
+  } else {
+    uint32_t t = a | b << 16;
+#pragma unroll
+    for (int s = kRun / 2; s > 0; s >>= 1) t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, s));
+    a = __float_as_uint(widen<T>(t).x);
+    b = __float_as_uint(widen<T>(t).y);
+  }
 }
 // Codes of two pairs in a word: v k + 1.5 2^23 in one rounding leaves the integer in the low byte.
 __device__ __forceinline__ uint32_t code_word(float2 a, float2 b, float inv) {
@@ -182,69 +206,17 @@ __device__ __forceinline__ uint32_t code_word(float2 a, float2 b, float inv) {
   return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
                      __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
 }
-// 8-bit codes of the eight values of a chunk (v: the same as fp32 pairs), and the scale of their
-// block(s) by its first thread.
 template <typename T, bool VEC, int L>
-__device__ __forceinline__ void save_eight(const Eight<T> &raw, const float2 *v, int8_t *codes, float *scales, const Place<VEC, L> &pl, int k,
-                                           int D, bool on) {
-  constexpr int kWords = sizeof(T) == 4 ? 8 : 4;  // of a chunk
-  Eight<int8_t> e;
-  if constexpr (VEC) {
-    uint32_t top = 0;
+__device__ __forceinline__ void save_row(const Sixteen<T> &v, uint32_t top, int8_t *codes, float *scales, const Place<VEC, L> &pl, int D) {
+  const float inv = block_inverse<T>(top);
+  Sixteen<int8_t> e;
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) top = top_bits<T>(top, raw, i);
-    top = top_one<T>(top);
-    constexpr int kLanes = L > 0 && L < 16 ? L : 16;
-#pragma unroll
-    for (int s = kLanes / 2; s > 0; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
-    top = top_as_f32<T>(top);
-    const float inv = block_inverse<T>(top);
-    uint2 w;
-    w.x = code_word(v[0], v[1], inv);
-    w.y = code_word(v[2], v[3], inv);
-    *reinterpret_cast<uint2 *>(e.v) = w;
-    if (on && pl.id % 16 == 0 && pl.at(k, 0) < D) scales[pl.at(k, 0) / kBlock] = block_scale(top, inv);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int j = 0; j < kWords / 2; ++j) top = top_bits<T>(top, raw, i * kWords / 2 + j);
-      top = top_as_f32<T>(__reduce_max_sync(0xffffffffu, top_one<T>(top)));
-      const float inv = block_inverse<T>(top);
-      reinterpret_cast<uint32_t *>(e.v)[i] = code_word(v[2 * i], v[2 * i + 1], inv);
-      if (on && (threadIdx.x & 31) == 0 && pl.at(k, 4 * i) < D) scales[pl.at(k, 4 * i) / kBlock] = block_scale(top, inv);
-    }
-  }
-  if (on) store_eight<int8_t, VEC, L>(codes, e, pl, k, D);
+  for (int i = 0; i < kPer / 4; ++i) reinterpret_cast<uint32_t *>(e.v)[i] = code_word(v.pair(2 * i), v.pair(2 * i + 1), inv);
+  store_row<int8_t, VEC, L>(codes, e, pl, D);
+  if (pl.leads_block() && pl.first < D) scales[pl.block()] = block_scale(top, inv);
 }
 
-// The rows of a group: one head, tokens `first`, `first + step`, ...
-struct RowWalk {
-  int64_t h, t, step, part;  // part: index among the groups of this head
-  bool any;                  // the group has a head
-  __device__ __forceinline__ RowWalk(const NormProblem &p, int per_cta, int L) {
-    const int64_t gid = (int64_t)blockIdx.x * per_cta + (L > 0 ? threadIdx.x / L : 0);
-    h = gid % p.heads;
-    part = t = gid / p.heads;
-    step = p.groups / p.heads;
-    any = h < p.H;
-  }
-};
-
-// The group's weights (or biases) at pair i of the thread's channels.
-template <bool VEC, int L>
-__device__ __forceinline__ float2 load_columns(const float *from, const RowWalk &rw, const NormProblem &p, const Place<VEC, L> &pl, int i) {
-  const int d0 = pl.at(i / 4, i % 4 * 2), d1 = pl.at(i / 4, i % 4 * 2 + 1);
-  from += p.per_head && rw.any ? rw.h * p.D : 0;
-  return make_float2(d0 < p.D ? from[d0] : 0.f, d1 < p.D ? from[d1] : 0.f);
-}
-// v - m, zero past the row's end.
-template <bool VEC, int L>
-__device__ __forceinline__ float2 off_mean(float2 v, float m, const Place<VEC, L> &pl, int i, int D) {
-  v = add2(v, both(-m));
-  return make_float2(pl.at(i / 4, i % 4 * 2) < D ? v.x : 0.f, pl.at(i / 4, i % 4 * 2 + 1) < D ? v.y : 0.f);
-}
+// ---- arithmetic of a row ----
 __device__ __forceinline__ float2 sigmoid2(float2 x) {
   const float2 t = mul2(x, both(-kLog2e)), d = add2(make_float2(ex2(t.x), ex2(t.y)), both(1.f));
   return make_float2(rcp(d.x), rcp(d.y));
@@ -259,278 +231,266 @@ __device__ __forceinline__ void sigmoid_halves(float2 x, float2 *q, float2 *rest
   *q = make_float2(rcp(d.x), rcp(d.y));
   *rest = mul2(e, *q);
 }
-__device__ __forceinline__ float one_of(const float2 *v, int i) { return i & 1 ? v[i >> 1].y : v[i >> 1].x; }
-
-template <typename T, bool VEC, int L, int K>
-__global__ void __launch_bounds__(kNormThreads<L>, K == 1 && L > 0 ? FWDB : 1) gdp_norm_fwd_kernel(const NormProblem p) {
-  __shared__ float red[2][32];
-  int turn = 0;
-  const Place<VEC, L> pl;
-  const int D = (int)p.D;
-  RowWalk rw(p, L > 0 ? (int)blockDim.x / (L > 0 ? L : 1) : 1, L);
-  // the tokens of the warp's (or CTA's) first group: all its threads take part while that one has rows
-  int64_t lead = L > 0 ? ((int64_t)blockIdx.x * blockDim.x + (threadIdx.x & ~31u)) / (L > 0 ? L : 1) / p.heads : rw.t;
-  const int64_t blocks = (p.D + kBlock - 1) / kBlock;
-  float2 w[4 * K], b[4 * K];
+// v less its mean where centred (zero past the row's end), and the reciprocal root of its mean square.
+template <bool VEC, int L>
+__device__ __forceinline__ float row_stats(float2 *v, const NormProblem &p, const Place<VEC, L> &pl, int D, float2 (*red)[32], int &turn) {
+  constexpr int P = kPer / 2;
+  if (p.center) {
+    float2 s = v[0];
 #pragma unroll
-  for (int i = 0; i < 4 * K; ++i) {
-    w[i] = load_columns<VEC, L>(p.w, rw, p, pl, i);
-    b[i] = p.b ? load_columns<VEC, L>(p.b, rw, p, pl, i) : both(0.f);
-  }
-  Eight<T> o[K], z[K];
-  auto load = [&](int64_t t) {
-    const bool on = rw.any && t < p.T;
+    for (int i = 1; i < P; ++i) s = add2(s, v[i]);
+    const float m = group_sum<L>(s.x + s.y, red, turn) * p.inv_d;
+    const bool whole = pl.at(kPer - 1) < D;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      load_eight<T, VEC, L>(o[k], static_cast<const T *>(p.o) + t * p.o_st + rw.h * p.o_sh, pl, k, D, on);
-      if (p.z) load_eight<T, VEC, L>(z[k], static_cast<const T *>(p.z) + t * p.z_st + rw.h * p.z_sh, pl, k, D, on);
-    }
-  };
-  load(rw.t);
-  int64_t row = rw.t * p.H + rw.h;
-  for (; lead < p.T; lead += rw.step, rw.t += rw.step, row += rw.step * p.H) {
-    const bool on = rw.any && rw.t < p.T;
-    float2 v[4 * K], g[4 * K];
-#pragma unroll
-    for (int i = 0; i < 4 * K; ++i) v[i] = o[i / 4].pair(i % 4);
-    if (p.z) {
-#pragma unroll
-      for (int i = 0; i < 4 * K; ++i) g[i] = z[i / 4].pair(i % 4);
-    }
-    if (p.o_codes) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) save_eight<T, VEC, L>(o[k], v + 4 * k, p.o_codes + row * p.D, p.o_scales + row * blocks, pl, k, D, on);
-      if (p.z) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) save_eight<T, VEC, L>(z[k], g + 4 * k, p.z_codes + row * p.D, p.z_scales + row * blocks, pl, k, D, on);
-      }
-    }
-    load(rw.t + rw.step);
-    float2 s = both(0.f);
-    if (p.center) {
-#pragma unroll
-      for (int i = 0; i < 4 * K; ++i) s = add2(s, v[i]);
-      const float m = group_sum<L>(s.x + s.y, red, turn) * p.inv_d;
-#pragma unroll
-      for (int i = 0; i < 4 * K; ++i) v[i] = off_mean<VEC, L>(v[i], m, pl, i, D);
-      s = both(0.f);
-    }
-#pragma unroll
-    for (int i = 0; i < 4 * K; ++i) s = fma2(v[i], v[i], s);
-    const float r = rsqrtf(group_sum<L>(s.x + s.y, red, turn) * p.inv_d + p.eps);
-#pragma unroll
-    for (int i = 0; i < 4 * K; ++i) v[i] = fma2(mul2(v[i], both(r)), w[i], b[i]);
-    if (p.z) {
-      if (p.act == GDP_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < 4 * K; ++i) v[i] = mul2(mul2(v[i], g[i]), sigmoid2(g[i]));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4 * K; ++i) v[i] = mul2(v[i], sigmoid2(g[i]));
-      }
-    } else if (p.act == GDP_ACT_SILU) {
-#pragma unroll
-      for (int i = 0; i < 4 * K; ++i) v[i] = mul2(v[i], sigmoid2(v[i]));
-    }
-    if (on) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        Eight<T> e;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e.set(i, v[4 * k + i]);
-        store_eight<T, VEC, L>(static_cast<T *>(p.y) + row * p.D, e, pl, k, D);
-      }
+    for (int i = 0; i < P; ++i) {
+      v[i] = add2(v[i], both(-m));
+      if (!whole) v[i] = make_float2(pl.at(2 * i) < D ? v[i].x : 0.f, pl.at(2 * i + 1) < D ? v[i].y : 0.f);
     }
   }
+  float2 s = mul2(v[0], v[0]);
+#pragma unroll
+  for (int i = 1; i < P; ++i) s = fma2(v[i], v[i], s);
+  return rsqrtf(group_sum<L>(s.x + s.y, red, turn) * p.inv_d + p.eps);
 }
 
-template <typename T, bool Q8, bool VEC, int L, int K>
-__global__ void __launch_bounds__(kNormThreads<L>, K == 1 && L > 0 ? BWDB : 1) gdp_norm_bwd_kernel(const NormProblem p) {
-  __shared__ float red[2][32];
-  __shared__ float2 red2[2][32];
-  __shared__ float cols[L > 0 ? 2 * 8 * kNormThreads<L> : 1];
-  int turn = 0, turn2 = 0;
-  const Place<VEC, L> pl;
-  const int D = (int)p.D;
-  RowWalk rw(p, L > 0 ? (int)blockDim.x / (L > 0 ? L : 1) : 1, L);
-  int64_t lead = L > 0 ? ((int64_t)blockIdx.x * blockDim.x + (threadIdx.x & ~31u)) / (L > 0 ? L : 1) / p.heads : rw.t;
-  const int64_t blocks = (p.D + kBlock - 1) / kBlock;
-  const bool zed = Q8 ? p.z_codes_in != nullptr : p.z != nullptr;
-  float2 w[4 * K], sw[4 * K], sb[4 * K];
-#pragma unroll
-  for (int i = 0; i < 4 * K; ++i) {
-    w[i] = load_columns<VEC, L>(p.w, rw, p, pl, i);
-    sw[i] = sb[i] = both(0.f);
+// The rows of a group: one head, tokens t, t + step, ...
+struct RowWalk {
+  int64_t h, t, step, part;  // part: index among the groups of this head
+  int64_t lead;              // token of the warp's (or CTA's) first group: its threads go on together while that one has rows
+  bool any;                  // the group has a head
+  __device__ __forceinline__ RowWalk(const NormProblem &p, int L) {
+    const int64_t per_cta = L > 0 ? blockDim.x / L : 1, gid = blockIdx.x * per_cta + (L > 0 ? threadIdx.x / L : 0);
+    h = gid % p.heads;
+    part = t = gid / p.heads;
+    step = p.groups / p.heads;
+    any = h < p.H;
+    lead = L > 0 ? (blockIdx.x * per_cta + (threadIdx.x & ~31u) / L) / p.heads : t;
   }
-  Source<T, Q8, VEC> o[K], z[K];
-  Eight<T> y[K];
-  auto load = [&](int64_t t) {
-    const bool on = rw.any && t < p.T;
-    const int64_t row = t * p.H + rw.h;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      load_eight<T, VEC, L>(y[k], static_cast<const T *>(p.dy) + t * p.dy_st + rw.h * p.dy_sh, pl, k, D, on);
-      if constexpr (Q8) {
-        load_source<T, true, VEC, L>(o[k], p.o_codes_in, row * p.D, p.o_scales_in + row * blocks, pl, k, D, on);
-        if (zed) load_source<T, true, VEC, L>(z[k], p.z_codes_in, row * p.D, p.z_scales_in + row * blocks, pl, k, D, on);
-      } else {
-        load_source<T, false, VEC, L>(o[k], p.o, t * p.o_st + rw.h * p.o_sh, nullptr, pl, k, D, on);
-        if (zed) load_source<T, false, VEC, L>(z[k], p.z, t * p.z_st + rw.h * p.z_sh, nullptr, pl, k, D, on);
+};
+
+template <typename T, bool VEC, int L>
+__global__ void __launch_bounds__(kNormThreads<L>, L > 0 ? FWDB : 1) gdp_norm_fwd_kernel(const NormProblem p) {
+  constexpr int P = kPer / 2;
+  __shared__ float2 red[2][32];
+  int turn = 0;
+  const Place<VEC, L> pl;
+  const int D = (int)p.D, blocks = (D + kBlock - 1) / kBlock;
+  RowWalk rw(p, L);
+  const float *w = p.w + (p.per_head && rw.any ? rw.h * D : 0), *b = p.b ? p.b + (p.per_head && rw.any ? rw.h * D : 0) : nullptr;
+  const T *o_at = static_cast<const T *>(p.o) + rw.t * p.o_st + rw.h * p.o_sh, *z_at = static_cast<const T *>(p.z) + rw.t * p.z_st + rw.h * p.z_sh;
+  Sixteen<T> next_o, next_z;
+  auto load = [&](bool on) {
+    load_row<T, VEC, L>(next_o, o_at, pl, D, on);
+    if (p.z) load_row<T, VEC, L>(next_z, z_at, pl, D, on);
+    o_at += rw.step * p.o_st;
+    z_at += rw.step * p.z_st;
+  };
+  load(rw.any && rw.t < p.T);
+  int64_t row = rw.t * p.H + rw.h;
+  for (; rw.lead < p.T; rw.lead += rw.step, rw.t += rw.step, row += rw.step * p.H) {
+    const bool on = rw.any && rw.t < p.T;
+    Sixteen<T> e = next_o;
+    const Sixteen<T> z = next_z;
+    load(rw.any && rw.t + rw.step < p.T);
+    if (p.o_codes) {
+      uint32_t a = top_bits<T>(e), c = p.z ? top_bits<T>(z) : 0u;
+      block_tops<T, L>(a, c);
+      if (on) {
+        save_row<T, VEC, L>(e, a, p.o_codes + row * D, p.o_scales + row * blocks, pl, D);
+        if (p.z) save_row<T, VEC, L>(z, c, p.z_codes + row * D, p.z_scales + row * blocks, pl, D);
       }
     }
-  };
-  load(rw.t);
-  int64_t row = rw.t * p.H + rw.h;
-  for (; lead < p.T; lead += rw.step, rw.t += rw.step, row += rw.step * p.H) {
-    const bool on = rw.any && rw.t < p.T;
-    float2 n[4 * K], g[4 * K], dn[4 * K];
+    float2 v[P];
 #pragma unroll
-    for (int i = 0; i < 4 * K; ++i) {
-      n[i] = o[i / 4].pair(i % 4);
-      dn[i] = y[i / 4].pair(i % 4);
-    }
-    if (zed) {
+    for (int i = 0; i < P; ++i) v[i] = e.pair(i);
+    const float r = row_stats<VEC, L>(v, p, pl, D, red, turn);
+    auto finish = [&](auto zed_, auto act_) {
+      constexpr bool kZed = decltype(zed_)::value;
+      constexpr int kAct = decltype(act_)::value;
 #pragma unroll
-      for (int i = 0; i < 4 * K; ++i) g[i] = z[i / 4].pair(i % 4);
-    }
-    load(rw.t + rw.step);
-    float2 s = both(0.f);
-    if (p.center) {
+      for (int i = 0; i < P; i += 2) {
+        float2 cw[2], cb[2] = {both(0.f), both(0.f)};
+        load_columns<VEC, L>(cw, w, i, pl, D, p.vec_cols);
+        if (b) load_columns<VEC, L>(cb, b, i, pl, D, p.vec_cols);
 #pragma unroll
-      for (int i = 0; i < 4 * K; ++i) s = add2(s, n[i]);
-      const float m = group_sum<L>(s.x + s.y, red, turn) * p.inv_d;
-#pragma unroll
-      for (int i = 0; i < 4 * K; ++i) n[i] = off_mean<VEC, L>(n[i], m, pl, i, D);
-      s = both(0.f);
-    }
-#pragma unroll
-    for (int i = 0; i < 4 * K; ++i) s = fma2(n[i], n[i], s);
-    float r = rsqrtf(group_sum<L>(s.x + s.y, red, turn) * p.inv_d + p.eps);
-    if (!on) r = 0.f;  // a group without a row adds zeros to its sums
-#pragma unroll
-    for (int i = 0; i < 4 * K; ++i) n[i] = mul2(n[i], both(r));
-    // through the activation: dn from dy to du = dL/du, g from z to dz
-    auto gate = [&](auto zed_, auto silu_) {
-      constexpr bool kZed = decltype(zed_)::value, kSilu = decltype(silu_)::value;
-#pragma unroll
-      for (int i = 0; i < 4 * K; ++i) {
-        float2 u = mul2(n[i], w[i]);
-        if (p.b) u = add2(u, load_columns<VEC, L>(p.b, rw, p, pl, i));
-        const float2 x = kZed ? g[i] : u;
-        float2 q, rest;
-        sigmoid_halves(x, &q, &rest);
-        const float2 slope = kSilu ? mul2(q, fma2(x, rest, both(1.f))) : mul2(q, rest);
-        if (kZed) {
-          g[i] = mul2(mul2(dn[i], u), slope);
-          dn[i] = mul2(dn[i], kSilu ? mul2(x, q) : q);
-        } else {
-          dn[i] = mul2(dn[i], slope);
+        for (int u = i; u < i + 2; ++u) {
+          float2 x = fma2(mul2(v[u], both(r)), cw[u - i], cb[u - i]);
+          if constexpr (kZed) {
+            const float2 g = z.pair(u);
+            x = mul2(kAct == GDP_ACT_SILU ? mul2(x, g) : x, sigmoid2(g));
+          } else if constexpr (kAct == GDP_ACT_SILU) {
+            x = mul2(x, sigmoid2(x));
+          }
+          e.set(u, x);
         }
       }
     };
-    if (zed) {
-      if (p.act == GDP_ACT_SILU) gate(std::true_type{}, std::true_type{});
-      else gate(std::true_type{}, std::false_type{});
-      if (on) {
+    using Silu = std::integral_constant<int, GDP_ACT_SILU>;
+    if (p.z) {
+      if (p.act == GDP_ACT_SILU) finish(std::true_type{}, Silu{});
+      else finish(std::true_type{}, std::integral_constant<int, GDP_ACT_SIGMOID>{});
+    } else if (p.act == GDP_ACT_SILU) {
+      finish(std::false_type{}, Silu{});
+    } else {
+      finish(std::false_type{}, std::integral_constant<int, GDP_ACT_NONE>{});
+    }
+    if (on) store_row<T, VEC, L>(static_cast<T *>(p.y) + row * D, e, pl, D);
+  }
+}
+
+template <typename T, bool Q8, bool VEC, int L>
+__global__ void __launch_bounds__(kNormThreads<L>, L > 0 ? BWDB : 1) gdp_norm_bwd_kernel(const NormProblem p) {
+  constexpr int P = kPer / 2;
+  __shared__ float2 red[2][32];
+  int turn = 0;
+  const Place<VEC, L> pl;
+  const int D = (int)p.D, blocks = (D + kBlock - 1) / kBlock;
+  RowWalk rw(p, L);
+  const bool zed = Q8 ? p.z_codes_in != nullptr : p.z != nullptr;
+  const float *w = p.w + (p.per_head && rw.any ? rw.h * D : 0), *b = p.b ? p.b + (p.per_head && rw.any ? rw.h * D : 0) : nullptr;
+  // sums over tokens: dweight's in registers, dbias's (fewer calls have one) in shared memory
+  __shared__ float4 side[kPer / 4][kNormThreads<L>];
+  float2 sw[P];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          Eight<T> e;
+  for (int i = 0; i < P; ++i) sw[i] = both(0.f);
+  if (b) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e.set(i, g[4 * k + i]);
-          store_eight<T, VEC, L>(static_cast<T *>(p.d_z) + row * p.D, e, pl, k, D);
+    for (int i = 0; i < kPer / 4; ++i) side[i][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  Source<T, Q8> next_o, next_z;
+  Sixteen<T> next_y;
+  auto load = [&](int64_t t, int64_t row) {
+    const bool on = rw.any && t < p.T;
+    load_row<T, VEC, L>(next_y, static_cast<const T *>(p.dy) + t * p.dy_st + rw.h * p.dy_sh, pl, D, on);
+    load_source<T, Q8, VEC, L>(next_o, p.o, t * p.o_st + rw.h * p.o_sh, p.o_codes_in, p.o_scales_in, row, D, blocks, pl, on);
+    if (zed) load_source<T, Q8, VEC, L>(next_z, p.z, t * p.z_st + rw.h * p.z_sh, p.z_codes_in, p.z_scales_in, row, D, blocks, pl, on);
+  };
+  int64_t row = rw.t * p.H + rw.h;
+  load(rw.t, row);
+  for (; rw.lead < p.T; rw.lead += rw.step, rw.t += rw.step, row += rw.step * p.H) {
+    const bool on = rw.any && rw.t < p.T;
+    const Source<T, Q8> z = next_z;
+    Sixteen<T> e = next_y;  // dy, then dz in its place
+    float2 n[P], dn[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) n[i] = next_o.pair(i);
+    load(rw.t + rw.step, row + rw.step * p.H);
+    float r = row_stats<VEC, L>(n, p, pl, D, red, turn);
+    if (!on) r = 0.f;  // a group without a row adds zeros to its sums
+    float2 s1 = both(0.f), s2 = both(0.f);
+    // through the activation: du = dL/du and dz; then dn = du w
+    auto gate = [&](auto zed_, auto act_) {
+      constexpr bool kZed = decltype(zed_)::value;
+      constexpr int kAct = decltype(act_)::value;
+#pragma unroll
+      for (int i = 0; i < P; i += 2) {
+        float2 cw[2], cb[2] = {both(0.f), both(0.f)}, du[2];
+        load_columns<VEC, L>(cw, w, i, pl, D, p.vec_cols);
+        if (b && kAct != GDP_ACT_NONE) load_columns<VEC, L>(cb, b, i, pl, D, p.vec_cols);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          n[i + k] = mul2(n[i + k], both(r));
+          du[k] = e.pair(i + k);
+          if constexpr (kAct != GDP_ACT_NONE) {
+            const float2 u = fma2(n[i + k], cw[k], cb[k]), x = kZed ? z.pair(i + k) : u;
+            float2 q, rest;
+            sigmoid_halves(x, &q, &rest);
+            const float2 slope = kAct == GDP_ACT_SILU ? mul2(q, fma2(x, rest, both(1.f))) : mul2(q, rest);
+            if constexpr (kZed) {
+              e.set(i + k, mul2(mul2(du[k], u), slope));
+              du[k] = mul2(du[k], kAct == GDP_ACT_SILU ? mul2(x, q) : q);
+            } else {
+              du[k] = mul2(du[k], slope);
+            }
+          }
+          sw[i + k] = fma2(du[k], n[i + k], sw[i + k]);
+          dn[i + k] = mul2(du[k], cw[k]);
+          s1 = add2(s1, dn[i + k]);
+          s2 = fma2(dn[i + k], n[i + k], s2);
+        }
+        if (b) {
+          float4 t = side[i / 2][threadIdx.x];
+          side[i / 2][threadIdx.x] = make_float4(t.x + du[0].x, t.y + du[0].y, t.z + du[1].x, t.w + du[1].y);
         }
       }
+    };
+    using Silu = std::integral_constant<int, GDP_ACT_SILU>;
+    if (zed) {
+      if (p.act == GDP_ACT_SILU) gate(std::true_type{}, Silu{});
+      else gate(std::true_type{}, std::integral_constant<int, GDP_ACT_SIGMOID>{});
+      if (on) store_row<T, VEC, L>(static_cast<T *>(p.d_z) + row * D, e, pl, D);
     } else if (p.act == GDP_ACT_SILU) {
-      gate(std::false_type{}, std::true_type{});
-    }
-    float2 s1 = both(0.f), s2 = both(0.f);
-    if (p.b) {
-#pragma unroll
-      for (int i = 0; i < 4 * K; ++i) sb[i] = add2(sb[i], dn[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4 * K; ++i) {
-      sw[i] = fma2(dn[i], n[i], sw[i]);
-      dn[i] = mul2(dn[i], w[i]);
-      s2 = fma2(dn[i], n[i], s2);
-    }
-    float m1 = 0.f, m2;
-    if (p.center) {
-#pragma unroll
-      for (int i = 0; i < 4 * K; ++i) s1 = add2(s1, dn[i]);
-      const float2 t = group_sum2<L>(make_float2(s1.x + s1.y, s2.x + s2.y), red2, turn2);
-      m1 = t.x * p.inv_d;
-      m2 = t.y * p.inv_d;
+      gate(std::false_type{}, Silu{});
     } else {
-      m2 = group_sum<L>(s2.x + s2.y, red, turn) * p.inv_d;
+      gate(std::false_type{}, std::integral_constant<int, GDP_ACT_NONE>{});
     }
+    const float2 t = group_sum<L>(make_float2(s1.x + s1.y, s2.x + s2.y), red, turn);
+    const float m1 = p.center ? t.x * p.inv_d : 0.f, m2 = t.y * p.inv_d;
     if (on) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        Eight<T> e;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e.set(i, mul2(fma2(n[4 * k + i], both(-m2), add2(dn[4 * k + i], both(-m1))), both(r)));
-        store_eight<T, VEC, L>(static_cast<T *>(p.d_o) + row * p.D, e, pl, k, D);
-      }
+      for (int i = 0; i < P; ++i) e.set(i, mul2(fma2(n[i], both(-m2), add2(dn[i], both(-m1))), both(r)));
+      store_row<T, VEC, L>(static_cast<T *>(p.d_o) + row * D, e, pl, D);
     }
   }
   // column sums: [part][columns], all dweight parts before all dbias parts
   const int64_t ncols = p.per_head ? p.H * p.D : p.D;
-  if (L == 0 || p.per_head) {
-    const int64_t part = p.per_head ? rw.part : blockIdx.x, off = p.per_head ? rw.h * p.D : 0;
+  for (int which = 0; which < (b ? 2 : 1); ++which) {
+    if (which) {
 #pragma unroll
-    for (int i = 0; i < 8 * K; ++i) {
-      const int d = pl.at(i / 8, i % 8);
-      if (rw.any && d < D) {
-        p.partial[part * ncols + off + d] = one_of(sw, i);
-        if (p.b) p.partial[(p.parts + part) * ncols + off + d] = one_of(sb, i);
+      for (int i = 0; i < kPer / 4; ++i) {
+        const float4 t = side[i][threadIdx.x];
+        sw[2 * i] = make_float2(t.x, t.y);
+        sw[2 * i + 1] = make_float2(t.z, t.w);
       }
     }
-  } else if constexpr (L > 0) {  // one part per CTA: the groups' sums in turn
-    constexpr int kGroups = kNormThreads<L> / L;
-    const int group = (int)threadIdx.x / L;
+    float *to = p.partial + which * p.parts * ncols;
+    if (L == 0 || p.per_head) {
+      to += (p.per_head ? rw.part : (int64_t)blockIdx.x) * ncols + (p.per_head ? rw.h * p.D : 0);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      cols[group * 8 * L + pl.at(0, j)] = rw.any ? one_of(sw, j) : 0.f;
-      cols[(kGroups + group) * 8 * L + pl.at(0, j)] = rw.any ? one_of(sb, j) : 0.f;
-    }
-    __syncthreads();
-    for (int d = (int)threadIdx.x; d < 2 * D; d += (int)blockDim.x) {
-      const int which = d >= D, c = d - which * D;
-      if (which && !p.b) break;
-      float s = 0.f;
-#pragma unroll 4
-      for (int i = 0; i < kGroups; ++i) s += cols[(which * kGroups + i) * 8 * L + c];
-      p.partial[(which * p.parts + blockIdx.x) * ncols + c] = s;
+      for (int j = 0; j < kPer; ++j)
+        if (rw.any && pl.at(j) < D) to[pl.at(j)] = j & 1 ? sw[j >> 1].y : sw[j >> 1].x;
+    } else if constexpr (L > 0) {  // one part per CTA: the groups' sums in turn
+      constexpr int kGroups = kNormThreads<L> / L, kWide = kPer * L;
+      __shared__ float cols[kGroups * kWide];
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) cols[(int)threadIdx.x / L * kWide + pl.at(j)] = rw.any ? (j & 1 ? sw[j >> 1].y : sw[j >> 1].x) : 0.f;
+      __syncthreads();
+      for (int d = (int)threadIdx.x; d < D; d += (int)blockDim.x) {
+        float t = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < kGroups; ++i) t += cols[i * kWide + d];
+        to[blockIdx.x * ncols + d] = t;
+      }
     }
   }
 }
 
-template <typename T, bool VEC, int L, int K>
+template <typename T, bool VEC, int L>
 cudaError_t run_norm_fwd(const NormProblem &p, const NormPlan &n, cudaStream_t stream) {
-  gdp_norm_fwd_kernel<T, VEC, L, K><<<(unsigned)n.grid, n.threads, 0, stream>>>(p);
+  gdp_norm_fwd_kernel<T, VEC, L><<<(unsigned)n.grid, n.threads, 0, stream>>>(p);
   return cudaGetLastError();
 }
-template <typename T, bool VEC, int L, int K>
+template <typename T, bool VEC, int L>
 cudaError_t run_norm_bwd(const NormProblem &p, const NormPlan &n, cudaStream_t stream) {
-  if (p.o_codes_in) gdp_norm_bwd_kernel<T, true, VEC, L, K><<<(unsigned)n.grid, n.threads, 0, stream>>>(p);
-  else gdp_norm_bwd_kernel<T, false, VEC, L, K><<<(unsigned)n.grid, n.threads, 0, stream>>>(p);
+  if (p.o_codes_in) gdp_norm_bwd_kernel<T, true, VEC, L><<<(unsigned)n.grid, n.threads, 0, stream>>>(p);
+  else gdp_norm_bwd_kernel<T, false, VEC, L><<<(unsigned)n.grid, n.threads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-#define GDP_NORM_CASES(RUN)                                              \
-  if (n.vec) {                                                           \
-    if (n.lanes == 8) return RUN<T, true, 8, 1>(p, n, stream);           \
-    if (n.lanes == 16) return RUN<T, true, 16, 1>(p, n, stream);         \
-    if (n.lanes == 32) return RUN<T, true, 32, 1>(p, n, stream);         \
-    if (n.chunks == 1) return RUN<T, true, 0, 1>(p, n, stream);          \
-    return RUN<T, true, 0, 2>(p, n, stream);                             \
-  }                                                                      \
-  if (n.lanes == 32) return RUN<T, false, 32, 1>(p, n, stream);          \
-  if (n.chunks == 1) return RUN<T, false, 0, 1>(p, n, stream);           \
-  return RUN<T, false, 0, 2>(p, n, stream);
+#define GDP_NORM_CASES(RUN)                                   \
+  if (n.vec) {                                                \
+    if (n.lanes == 4) return RUN<T, true, 4>(p, n, stream);   \
+    if (n.lanes == 8) return RUN<T, true, 8>(p, n, stream);   \
+    if (n.lanes == 16) return RUN<T, true, 16>(p, n, stream); \
+    if (n.lanes == 32) return RUN<T, true, 32>(p, n, stream); \
+    return RUN<T, true, 0>(p, n, stream);                     \
+  }                                                           \
+  if (n.lanes == 8) return RUN<T, false, 8>(p, n, stream);    \
+  if (n.lanes == 32) return RUN<T, false, 32>(p, n, stream);  \
+  return RUN<T, false, 0>(p, n, stream);
 
 template <typename T>
 cudaError_t launch_norm_fwd(const NormProblem &p, const NormPlan &n, cudaStream_t stream) {
