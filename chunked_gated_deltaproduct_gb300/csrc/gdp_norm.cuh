@@ -35,7 +35,8 @@ constexpr int kNormThreads = L > 0 ? 256 : 512;
 #ifndef FWDB
 #define FWDB 3
 #define BWDB 2
-#define GRIDM 4
+#define GRIDF 6
+#define GRIDB 4
 #endif
 // How a call runs: groups of `lanes` threads (0: a CTA of `threads`), sixteen channels each.
 // The groups number grid * (groups per CTA), a multiple of `heads`; group i keeps head i % heads (none
@@ -45,7 +46,7 @@ struct NormPlan {
   int64_t grid, heads, groups, parts;
 };
 
-inline NormPlan norm_plan(int64_t T, int64_t H, int64_t D, int per_head, int vec, int sms) {
+inline NormPlan norm_plan(int64_t T, int64_t H, int64_t D, int per_head, int vec, int sms, int per_sm) {
   NormPlan n{};
   n.vec = vec;
   n.threads = 256;
@@ -70,7 +71,7 @@ inline NormPlan norm_plan(int64_t T, int64_t H, int64_t D, int per_head, int vec
     m = n.heads / per_cta;
   }
   // CTAs of 256 threads: a few per SM; smaller ones: as many threads
-  const int64_t resident = (int64_t)sms * (n.threads >= 256 ? GRIDM : GRIDM * 256 / n.threads);
+  const int64_t resident = (int64_t)sms * (n.threads >= 256 ? per_sm : per_sm * 256 / n.threads);
   const int64_t need = (T * n.heads + per_cta - 1) / per_cta;
   n.grid = (need + m - 1) / m * m;
   if (n.grid > resident) n.grid = resident / m * m;

@@ -6,6 +6,7 @@ the current stream, and there is no fallback: without the library every call rai
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -64,6 +65,17 @@ class GdpGroupNormBackwardArgs(ctypes.Structure):
     ]
 
 
+def _packer(args):
+    """The argument struct's bytes from its fields' values in order: a tenth of the time of filling a
+    ctypes structure, which a one-token step would notice.  (The fields need no padding between them.)"""
+    codes = {_vp: "Q", _i64: "q", _sz: "Q", _int: "i", _f32: "f"}
+    return struct.Struct("@" + "".join(codes[t] for _, t in args._fields_) + "0q").pack
+
+
+_pack_recurrence, _pack_recurrence_backward = _packer(GdpRecurrenceArgs), _packer(GdpRecurrenceBackwardArgs)
+_pack_norm, _pack_norm_backward = _packer(GdpGroupNormArgs), _packer(GdpGroupNormBackwardArgs)
+
+
 class ActivationCheckpoint(NamedTuple):
     """8-bit codes [T, H, D] of an activation and the scales [T, H, ceil(D / 128)] of their blocks."""
     codes: torch.Tensor
@@ -94,14 +106,14 @@ def _library():
                            ("gdp_group_norm", GdpGroupNormArgs),
                            ("gdp_group_norm_backward", GdpGroupNormBackwardArgs)):
             fn = getattr(lib, name)
-            fn.restype, fn.argtypes = _int, [ctypes.POINTER(args), _vp]
+            fn.restype, fn.argtypes = _int, [_vp, _vp]
         lib.gdp_group_norm_workspace_bytes.restype = _sz
         lib.gdp_group_norm_workspace_bytes.argtypes = [_i64, _i64, _i64, _int]
         lib.gdp_layer_args_size.restype = _sz
         lib.gdp_layer_args_size.argtypes = [_int]
         for i, args in enumerate((GdpRecurrenceArgs, GdpRecurrenceBackwardArgs, GdpGroupNormArgs,
                                   GdpGroupNormBackwardArgs)):
-            if lib.gdp_layer_args_size(i) != ctypes.sizeof(args):
+            if not lib.gdp_layer_args_size(i) == ctypes.sizeof(args) == len(_packer(args)(*[0] * len(args._fields_))):
                 raise RuntimeError(f"{args.__name__} layout mismatch between the binding and the library")
         _lib = lib
     return _lib
@@ -111,96 +123,127 @@ def gdp_group_norm_workspace_bytes(T: int, H: int, D: int, per_head: bool = Fals
     return int(_library().gdp_group_norm_workspace_bytes(T, H, D, int(per_head)))
 
 
-def _call(name, args, stream):
-    lib = _library()
-    st = getattr(lib, name)(ctypes.byref(args), ctypes.c_void_p(binding._stream(stream)))
-    if st != GDP_OK:
-        raise GdpError(st, lib.gdp_last_error().decode())
-
+# ---- checks.  A one-token step costs a few microseconds of host time, so each tensor's are one
+# expression, and the wording of a refusal is worked out only once it fails.
 
 def _invalid(msg):
     raise GdpError(GDP_ERR_INVALID_ARG, msg)
 
 
-def _rows(name, t, shape, dtype, dev):
-    """A [T, C] or [T, H, D] tensor whose last dimension is contiguous."""
-    if t.shape != shape:
-        _invalid(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    if t.dtype != dtype:
-        raise GdpError(GDP_ERR_UNSUPPORTED, f"{name} must be {dtype} (got {t.dtype})")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+def _finish(status, lib):
+    if status != GDP_OK:
+        raise GdpError(status, lib.gdp_last_error().decode())
+
+
+def _current(stream, dev):
+    """The stream handle of a call: the caller's, or torch's current one on the device."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream
+
+
+def _first(name, t, dims):
+    """(shape, type code, device index) of the tensor that sets them for the call."""
+    if t.dim() != len(dims):
+        _invalid(f"{name} must be [{', '.join(dims)}]")
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise GdpError(GDP_ERR_UNSUPPORTED, f"{name} must be bfloat16, float16 or float32 (got {t.dtype})")
+    if not t.is_cuda:
+        _invalid("the tensors must be on a CUDA device")
+    shape = t.shape
+    if shape[-1] > 1 and t.stride(-1) != 1:
         _invalid(f"{name} must be contiguous in its last dimension")
-    if t.device != dev:
-        _invalid(f"{name} must be on {dev}")
+    return shape, code, t.get_device()
 
 
-def _dense(name, t, shape, dtype, dev):
-    if t is None:
-        return None
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.device != dev:
-        _invalid(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+def _rows(name, t, shape, dtype, dev):
+    """Address of a tensor of that shape, type and device whose last dimension is contiguous."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or (t.stride(-1) != 1 and shape[-1] > 1):
+        if t.shape != shape:
+            _invalid(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+        if t.dtype != dtype:
+            raise GdpError(GDP_ERR_UNSUPPORTED, f"{name} must be {dtype} (got {t.dtype})")
+        if t.get_device() != dev:
+            _invalid(f"{name} must be on the device of the other tensors")
+        _invalid(f"{name} must be contiguous in its last dimension")
     return t.data_ptr()
 
 
-def _device(t):
-    if not t.is_cuda:
-        _invalid("the tensors must be on a CUDA device")
-    return t.device
+def _dense(name, t, shape, dtype, dev):
+    """Address of a contiguous tensor of that shape, type and device (None: 0)."""
+    if t is None:
+        return 0
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != dev:
+        _invalid(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the device of the other tensors")
+    return t.data_ptr()
 
 
-def _types(x, g):
-    if x.dtype not in _TYPES:
-        raise GdpError(GDP_ERR_UNSUPPORTED, f"x must be bfloat16, float16 or float32 (got {x.dtype})")
-    if g.dtype != x.dtype and g.dtype != torch.float32:
-        raise GdpError(GDP_ERR_UNSUPPORTED, f"g must be float32 or of x's type (got {g.dtype})")
-    return _TYPES[x.dtype], _TYPES[g.dtype]
+def _gate_type(x, g):
+    """g's type code: x's or fp32."""
+    dtype = g.dtype
+    if dtype != x.dtype and dtype != torch.float32:
+        raise GdpError(GDP_ERR_UNSUPPORTED, f"g must be float32 or of x's type (got {dtype})")
+    return _TYPES[dtype]
 
 
 def _cu(cu_seqlens, dev):
     if cu_seqlens is None:
         _invalid("cu_seqlens is required (packed input only)")
-    if (cu_seqlens.dtype not in (torch.int32, torch.int64) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1
-            or not cu_seqlens.is_contiguous() or cu_seqlens.device != dev):
+    wide = cu_seqlens.dtype == torch.int64
+    if (not (wide or cu_seqlens.dtype == torch.int32) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1
+            or not cu_seqlens.is_contiguous() or cu_seqlens.get_device() != dev):
         _invalid("cu_seqlens must be a contiguous int32 or int64 vector of N + 1 entries on the tensors' device")
-    return cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, int(cu_seqlens.dtype == torch.int64)
+    return cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, int(wide)
 
 
 def _status(t, dev):
     if t is None:
-        return None
-    if t.numel() < 1 or t.element_size() != 4 or t.device != dev:
+        return 0
+    if t.numel() < 1 or t.element_size() != 4 or t.get_device() != dev:
         _invalid("device_status must be a 32-bit word on the tensors' device")
     return t.data_ptr()
 
 
-def _workspace(ws, nbytes, dev, stream):
-    """The caller's workspace, or a new one (kept from reuse until `stream` has passed the call)."""
-    if ws is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            ws.record_stream(torch.cuda.ExternalStream(stream, device=dev))
-    elif ws.device != dev or not ws.is_contiguous():
-        _invalid("workspace must be contiguous and on the tensors' device")
-    return ws, ws.numel() * ws.element_size()
-
-
 def _gate_code(gate):
-    if gate not in _GATES:
+    code = _GATES.get(gate)
+    if code is None:
         _invalid(f"gate must be one of {sorted(_GATES)} (got {gate!r})")
-    return _GATES[gate]
+    return code
 
 
 def _state_args(initial_state, output_state, state, state_indices, N, C, dev):
-    f32 = torch.float32
     if state is None:
-        return (_dense("initial_state", initial_state, (N, C), f32, dev),
-                _dense("output_state", output_state, (N, C), f32, dev), None, None, 0)
+        if initial_state is None and output_state is None:
+            return 0, 0, 0, 0, 0
+        return (_dense("initial_state", initial_state, (N, C), torch.float32, dev),
+                _dense("output_state", output_state, (N, C), torch.float32, dev), 0, 0, 0)
     if initial_state is not None or output_state is not None:
         _invalid("the state cache excludes initial_state and output_state")
     if state_indices is None or state.dim() != 2:
         _invalid("the state cache is [num_slots, C] and needs state_indices")
-    return (None, None, _dense("state", state, (state.shape[0], C), f32, dev),
-            _dense("state_indices", state_indices, (N,), torch.int32, dev), state.shape[0])
+    slots = state.shape[0]
+    return (0, 0, _dense("state", state, (slots, C), torch.float32, dev),
+            _dense("state_indices", state_indices, (N,), torch.int32, dev), slots)
+
+
+def _recurrence(x, g, gate, cu, N, cu64, entry, first, initial_state, output_final_state, state, state_indices, output,
+                output_state, device_status, stream):
+    """The common part of the packed and the one-token call."""
+    shape, xt, dev = first
+    T, C = shape
+    gp, gt = _rows("g", g, shape, g.dtype, dev), _gate_type(x, g)
+    if output is None:
+        output = torch.empty_like(x, memory_format=torch.contiguous_format)
+        op = output.data_ptr()
+    else:
+        op = _dense("output", output, shape, x.dtype, dev)
+    if output_final_state and state is None and output_state is None:
+        output_state = torch.empty((N, C), dtype=torch.float32, device=x.device)
+    lib = _library()
+    a = _pack_recurrence(x.data_ptr(), x.stride(0), gp, g.stride(0), op, cu, T, N, C,
+                          *_state_args(initial_state, output_state, state, state_indices, N, C, dev),
+                          _status(device_status, dev), cu64, xt, gt, _gate_code(gate))
+    _finish(getattr(lib, entry)(a, _current(stream, dev)), lib)
+    return (output, output_state) if output_final_state else output
 
 
 def gated_linear_recurrence(x, g, cu_seqlens, gate="log", initial_state=None, output_final_state=False, state=None,
@@ -213,24 +256,10 @@ def gated_linear_recurrence(x, g, cu_seqlens, gate="log", initial_state=None, ou
     cache ``state`` [num_slots, C] fp32 read and written in place at ``state_indices`` [N] int32 (-1:
     from zero, nothing written).  Returns ``h`` [T, C] in x's type, or ``(h, final_state)`` when
     output_final_state (dense mode; None in cache mode)."""
-    if x.dim() != 2:
-        _invalid("x must be [T, C]")
-    T, C = x.shape
-    dev = _device(x)
-    xt, gt = _types(x, g)
-    _rows("x", x, x.shape, x.dtype, dev)
-    _rows("g", g, x.shape, g.dtype, dev)
-    cu, N, cu64 = _cu(cu_seqlens, dev)
-    if output is None:
-        output = torch.empty((T, C), dtype=x.dtype, device=dev)
-    if output_final_state and state is None and output_state is None:
-        output_state = torch.empty((N, C), dtype=torch.float32, device=dev)
-    init, fin, cache, slots, num = _state_args(initial_state, output_state, state, state_indices, N, C, dev)
-    a = GdpRecurrenceArgs(x.data_ptr(), x.stride(0), g.data_ptr(), g.stride(0),
-                          _dense("output", output, (T, C), x.dtype, dev), cu, T, N, C, init, fin, cache, slots, num,
-                          _status(device_status, dev), cu64, xt, gt, _gate_code(gate))
-    _call("gdp_linear_recurrence", a, stream)
-    return (output, output_state) if output_final_state else output
+    first = _first("x", x, ("T", "C"))
+    cu, N, cu64 = _cu(cu_seqlens, first[2])
+    return _recurrence(x, g, gate, cu, N, cu64, "gdp_linear_recurrence", first, initial_state, output_final_state, state,
+                       state_indices, output, output_state, device_status, stream)
 
 
 def gated_linear_recurrence_decode(x, g, gate="log", initial_state=None, output_final_state=False, state=None,
@@ -238,23 +267,9 @@ def gated_linear_recurrence_decode(x, g, gate="log", initial_state=None, output_
                                    stream=None):
     """One token per sequence: x, g [N, C]; the state modes, types and gates of gated_linear_recurrence.
     Returns ``h`` [N, C], or ``(h, final_state)`` when output_final_state (dense mode)."""
-    if x.dim() != 2:
-        _invalid("x must be [N, C]")
-    N, C = x.shape
-    dev = _device(x)
-    xt, gt = _types(x, g)
-    _rows("x", x, x.shape, x.dtype, dev)
-    _rows("g", g, x.shape, g.dtype, dev)
-    if output is None:
-        output = torch.empty((N, C), dtype=x.dtype, device=dev)
-    if output_final_state and state is None and output_state is None:
-        output_state = torch.empty((N, C), dtype=torch.float32, device=dev)
-    init, fin, cache, slots, num = _state_args(initial_state, output_state, state, state_indices, N, C, dev)
-    a = GdpRecurrenceArgs(x.data_ptr(), x.stride(0), g.data_ptr(), g.stride(0),
-                          _dense("output", output, (N, C), x.dtype, dev), None, N, N, C, init, fin, cache, slots, num,
-                          _status(device_status, dev), 0, xt, gt, _gate_code(gate))
-    _call("gdp_linear_recurrence_decode", a, stream)
-    return (output, output_state) if output_final_state else output
+    first = _first("x", x, ("N", "C"))
+    return _recurrence(x, g, gate, 0, first[0][0], 0, "gdp_linear_recurrence_decode", first, initial_state,
+                       output_final_state, state, state_indices, output, output_state, device_status, stream)
 
 
 def gated_linear_recurrence_backward(g, h, d_output, cu_seqlens, gate="log", x=None, initial_state=None,
@@ -264,72 +279,64 @@ def gated_linear_recurrence_backward(g, h, d_output, cu_seqlens, gate="log", x=N
     the ActivationCheckpoint of it that gated_group_norm kept ([T, H, D] with H D = C).  ``x`` is needed
     for the sigmoid gate only.  Returns a dict: dx in d_output's type, dg in g's type, d_initial_state
     fp32 (None without an initial state)."""
-    if d_output.dim() != 2:
-        _invalid("d_output must be [T, C]")
-    T, C = d_output.shape
-    dev = _device(d_output)
-    xt, gt = _types(d_output, g)
-    _rows("d_output", d_output, d_output.shape, d_output.dtype, dev)
-    _rows("g", g, d_output.shape, g.dtype, dev)
+    shape, xt, dev = _first("d_output", d_output, ("T", "C"))
+    T, C = shape
+    dtype, where = d_output.dtype, d_output.device
+    gp, gt = _rows("g", g, shape, g.dtype, dev), _gate_type(d_output, g)
     gate = _gate_code(gate)
-    xp = xs = 0
+    xp = xs = hp = hs = codes = scales = group = 0
     if gate == GDP_GATE_SIGMOID:
         if x is None:
             _invalid("the sigmoid gate's gradient needs x")
-        _rows("x", x, d_output.shape, d_output.dtype, dev)
-        xp, xs = x.data_ptr(), x.stride(0)
-    hp = hs = codes = scales = group = 0
+        xp, xs = _rows("x", x, shape, dtype, dev), x.stride(0)
     if isinstance(h, ActivationCheckpoint):
         if h.codes.dim() != 3 or h.codes.shape[0] != T or h.codes.shape[1] * h.codes.shape[2] != C:
             _invalid("the checkpoint of h must be [T, H, D] with H D = C")
-        codes, scales, group = _checkpoint("h", h, h.codes.shape, dev) + (h.codes.shape[2],)
+        group = h.codes.shape[2]
+        codes, scales = _checkpoint("h", h, h.codes.shape, dev)
     else:
-        _rows("h", h, d_output.shape, d_output.dtype, dev)
-        hp, hs = h.data_ptr(), h.stride(0)
+        hp, hs = _rows("h", h, shape, dtype, dev), h.stride(0)
     cu, N, cu64 = _cu(cu_seqlens, dev)
     init = _dense("initial_state", initial_state, (N, C), torch.float32, dev)
     dfin = _dense("d_final_state", d_final_state, (N, C), torch.float32, dev)
-    out = {"dx": torch.empty((T, C), dtype=d_output.dtype, device=dev),
-           "dg": torch.empty((T, C), dtype=g.dtype, device=dev),
-           "d_initial_state": (torch.empty((N, C), dtype=torch.float32, device=dev)
-                               if initial_state is not None else None)}
-    dinit = out["d_initial_state"]
-    a = GdpRecurrenceBackwardArgs(
-        g.data_ptr(), g.stride(0), xp, xs, hp, hs, codes, scales, group, d_output.data_ptr(), d_output.stride(0), cu,
-        T, N, C, init, dfin, out["dx"].data_ptr(), out["dg"].data_ptr(), None if dinit is None else dinit.data_ptr(),
-        _status(device_status, dev), cu64, xt, gt, gate)
-    _call("gdp_linear_recurrence_backward", a, stream)
-    return out
+    dx, dg = torch.empty(shape, dtype=dtype, device=where), torch.empty(shape, dtype=g.dtype, device=where)
+    dinit = torch.empty((N, C), dtype=torch.float32, device=where) if initial_state is not None else None
+    lib = _library()
+    a = _pack_recurrence_backward(
+        gp, g.stride(0), xp, xs, hp, hs, codes, scales, group, d_output.data_ptr(), d_output.stride(0), cu, T, N, C, init,
+        dfin, dx.data_ptr(), dg.data_ptr(), 0 if dinit is None else dinit.data_ptr(), _status(device_status, dev), cu64,
+        xt, gt, gate)
+    _finish(lib.gdp_linear_recurrence_backward(a, _current(stream, dev)), lib)
+    return {"dx": dx, "dg": dg, "d_initial_state": dinit}
 
 
 def _checkpoint(name, c, shape, dev):
     """Addresses of a checkpoint's codes and scales for an activation of `shape` [T, H, D]."""
     T, H, D = shape
-    return (_dense(f"{name}'s codes", c.codes, (T, H, D), torch.int8, dev),
-            _dense(f"{name}'s scales", c.scales, (T, H, -(-D // CHECKPOINT_BLOCK)), torch.float32, dev))
+    return (_dense(name + "'s codes", c.codes, shape, torch.int8, dev),
+            _dense(name + "'s scales", c.scales, (T, H, -(-D // CHECKPOINT_BLOCK)), torch.float32, dev))
 
 
-def _new_checkpoint(T, H, D, dev):
-    return ActivationCheckpoint(torch.empty((T, H, D), dtype=torch.int8, device=dev),
-                                torch.empty((T, H, -(-D // CHECKPOINT_BLOCK)), dtype=torch.float32, device=dev))
+def _new_checkpoint(T, H, D, where):
+    return ActivationCheckpoint(torch.empty((T, H, D), dtype=torch.int8, device=where),
+                                torch.empty((T, H, -(-D // CHECKPOINT_BLOCK)), dtype=torch.float32, device=where))
 
 
 def _affine(weight, bias, H, D, dev):
     """(weight, bias, per_head): fp32 [D] or [H, D]."""
-    if weight.dim() == 2 and weight.shape == (H, D):
-        per_head = 1
-    elif weight.shape == (D,):
-        per_head = 0
-    else:
-        _invalid(f"weight must be [{D}] or [{H}, {D}] (got {tuple(weight.shape)})")
-    return (_dense("weight", weight, weight.shape, torch.float32, dev),
-            _dense("bias", bias, weight.shape, torch.float32, dev), per_head)
+    shape = weight.shape
+    per_head = len(shape) == 2 and shape == (H, D)
+    if not per_head and shape != (D,):
+        _invalid(f"weight must be [{D}] or [{H}, {D}] (got {tuple(shape)})")
+    return (_dense("weight", weight, shape, torch.float32, dev), _dense("bias", bias, shape, torch.float32, dev),
+            int(per_head))
 
 
 def _act_code(activation):
-    if activation not in _ACTS:
+    code = _ACTS.get(activation)
+    if code is None:
         _invalid(f"activation must be 'silu', 'sigmoid' or None (got {activation!r})")
-    return _ACTS[activation]
+    return code
 
 
 def gated_group_norm(o, weight, z=None, bias=None, eps=1e-5, center=False, activation="silu", save_checkpoint=False,
@@ -341,29 +348,30 @@ def gated_group_norm(o, weight, z=None, bias=None, eps=1e-5, center=False, activ
 
     Returns ``y`` [T, H, D] in o's type, or ``(y, checkpoint)`` with the GroupNormCheckpoint (8-bit
     codes of o and z) that gated_group_norm_backward takes when ``save_checkpoint``."""
-    if o.dim() != 3:
-        _invalid("o must be [T, H, D]")
-    T, H, D = o.shape
-    dev = _device(o)
-    if o.dtype not in _TYPES:
-        raise GdpError(GDP_ERR_UNSUPPORTED, f"o must be bfloat16, float16 or float32 (got {o.dtype})")
-    _rows("o", o, o.shape, o.dtype, dev)
+    shape, dt, dev = _first("o", o, ("T", "H", "D"))
+    T, H, D = shape
+    where = o.device
+    ot, oh, _ = o.stride()
     zp = zt = zh = 0
     if z is not None:
-        _rows("z", z, o.shape, o.dtype, dev)
-        zp, zt, zh = z.data_ptr(), z.stride(0), z.stride(1)
+        zp = _rows("z", z, shape, o.dtype, dev)
+        zt, zh, _ = z.stride()
     w, b, per_head = _affine(weight, bias, H, D, dev)
     if output is None:
-        output = torch.empty((T, H, D), dtype=o.dtype, device=dev)
-    kept, ptrs = None, (None, None, None, None)
+        output = torch.empty_like(o, memory_format=torch.contiguous_format)
+        yp = output.data_ptr()
+    else:
+        yp = _dense("output", output, shape, o.dtype, dev)
+    kept, ptrs = None, (0, 0, 0, 0)
     if save_checkpoint:
-        kept = GroupNormCheckpoint(_new_checkpoint(T, H, D, dev), _new_checkpoint(T, H, D, dev) if z is not None else None)
-        ptrs = (kept.o.codes.data_ptr(), kept.o.scales.data_ptr())
-        ptrs += (kept.z.codes.data_ptr(), kept.z.scales.data_ptr()) if z is not None else (None, None)
-    a = GdpGroupNormArgs(o.data_ptr(), o.stride(0), o.stride(1), zp, zt, zh, w, b,
-                         _dense("output", output, (T, H, D), o.dtype, dev), *ptrs, T, H, D, eps, _TYPES[o.dtype],
-                         int(bool(center)), per_head, _act_code(activation))
-    _call("gdp_group_norm", a, stream)
+        ko, kz = _new_checkpoint(T, H, D, where), _new_checkpoint(T, H, D, where) if z is not None else None
+        kept = GroupNormCheckpoint(ko, kz)
+        ptrs = (ko.codes.data_ptr(), ko.scales.data_ptr(), *((kz.codes.data_ptr(), kz.scales.data_ptr()) if kz is not None
+                                                             else (0, 0)))
+    lib = _library()
+    a = _pack_norm(o.data_ptr(), ot, oh, zp, zt, zh, w, b, yp, *ptrs, T, H, D, eps, dt, int(bool(center)), per_head,
+                         _act_code(activation))
+    _finish(lib.gdp_group_norm(a, _current(stream, dev)), lib)
     return (output, kept) if save_checkpoint else output
 
 
@@ -373,33 +381,35 @@ def gated_group_norm_backward(d_output, saved, weight, bias=None, eps=1e-5, cent
     GroupNormCheckpoint of the forward call, or the pair ``(o, z)`` of tensors (z None without a gate).
     Returns a dict: do and dz in d_output's type (dz None without z), dweight and dbias fp32 (None
     without a bias)."""
-    if d_output.dim() != 3:
-        _invalid("d_output must be [T, H, D]")
-    T, H, D = d_output.shape
-    dev = _device(d_output)
-    if d_output.dtype not in _TYPES:
-        raise GdpError(GDP_ERR_UNSUPPORTED, f"d_output must be bfloat16, float16 or float32 (got {d_output.dtype})")
-    _rows("d_output", d_output, d_output.shape, d_output.dtype, dev)
+    shape, dt, dev = _first("d_output", d_output, ("T", "H", "D"))
+    T, H, D = shape
+    dtype, where = d_output.dtype, d_output.device
+    dt_t, dt_h, _ = d_output.stride()
     o, z = saved
-    tensors, codes = [0] * 6, [None] * 4
+    op = ot = oh = zp = zt = zh = 0
+    codes = (0, 0, 0, 0)
     if isinstance(saved, GroupNormCheckpoint):
-        codes[:2] = _checkpoint("o", o, d_output.shape, dev)
-        if z is not None:
-            codes[2:] = _checkpoint("z", z, d_output.shape, dev)
+        codes = _checkpoint("o", o, shape, dev) + (_checkpoint("z", z, shape, dev) if z is not None else (0, 0))
     else:
-        for i, (name, t) in enumerate((("o", o), ("z", z))):
-            if t is not None:
-                _rows(name, t, d_output.shape, d_output.dtype, dev)
-                tensors[3 * i:3 * i + 3] = t.data_ptr(), t.stride(0), t.stride(1)
+        op = _rows("o", o, shape, dtype, dev)
+        ot, oh, _ = o.stride()
+        if z is not None:
+            zp = _rows("z", z, shape, dtype, dev)
+            zt, zh, _ = z.stride()
     w, b, per_head = _affine(weight, bias, H, D, dev)
-    like = dict(dtype=d_output.dtype, device=dev)
-    out = {"do": torch.empty((T, H, D), **like), "dz": torch.empty((T, H, D), **like) if z is not None else None,
-           "dweight": torch.empty_like(weight), "dbias": torch.empty_like(bias) if bias is not None else None}
-    ws, ws_bytes = _workspace(workspace, gdp_group_norm_workspace_bytes(T, H, D, per_head), dev, stream)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    a = GdpGroupNormBackwardArgs(
-        d_output.data_ptr(), d_output.stride(0), d_output.stride(1), *tensors, *codes, w, b, ptr(out["do"]),
-        ptr(out["dz"]), ptr(out["dweight"]), ptr(out["dbias"]), ws.data_ptr(), ws_bytes, T, H, D, eps,
-        _TYPES[d_output.dtype], int(bool(center)), per_head, _act_code(activation))
-    _call("gdp_group_norm_backward", a, stream)
-    return out
+    do, dz = torch.empty(shape, dtype=dtype, device=where), torch.empty(shape, dtype=dtype, device=where) if z is not None else None
+    dw, db = torch.empty_like(weight), torch.empty_like(bias) if bias is not None else None
+    lib = _library()
+    need = lib.gdp_group_norm_workspace_bytes(T, H, D, per_head)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=where)
+        if stream is not None:  # not to be reused before that stream has passed this call
+            workspace.record_stream(torch.cuda.ExternalStream(stream, device=where))
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _invalid("workspace must be contiguous and on the tensors' device")
+    a = _pack_norm_backward(
+        d_output.data_ptr(), dt_t, dt_h, op, ot, oh, zp, zt, zh, *codes, w, b, do.data_ptr(),
+        0 if dz is None else dz.data_ptr(), dw.data_ptr(), 0 if db is None else db.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), T, H, D, eps, dt, int(bool(center)), per_head, _act_code(activation))
+    _finish(lib.gdp_group_norm_backward(a, _current(stream, dev)), lib)
+    return {"do": do, "dz": dz, "dweight": dw, "dbias": db}
