@@ -65,6 +65,17 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
+// sigmoid(x) and 1 - sigmoid(x) = e^-x sigmoid(x), each to its own relative precision; the exponent is
+// held to 2^115, where the first is 0 next to any other term and the product is still 1.
+__device__ __forceinline__ void sigmoid_halves(float2 x, float2 *q, float2 *rest) {
+  float2 t = mul2(x, both(-kLog2e));
+  asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(t.x));
+  asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(t.y));
+  const float2 e = make_float2(ex2(t.x), ex2(t.y)), d = add2(e, both(1.f));
+  *q = make_float2(rcp(d.x), rcp(d.y));
+  *rest = mul2(e, *q);
+}
+
 // Two stored values in one register (16-bit types), widened, and back.
 template <typename T>
 __device__ __forceinline__ float2 widen(uint32_t v);

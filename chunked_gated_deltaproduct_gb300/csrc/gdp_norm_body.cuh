@@ -221,16 +221,6 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) {
   const float2 t = mul2(x, both(-kLog2e)), d = add2(make_float2(ex2(t.x), ex2(t.y)), both(1.f));
   return make_float2(rcp(d.x), rcp(d.y));
 }
-// sigmoid(x) and 1 - sigmoid(x) = e^-x sigmoid(x), each to its own relative precision; the exponent is
-// held to 2^115, where the first is 0 next to any other term and the product is still 1.
-__device__ __forceinline__ void sigmoid_halves(float2 x, float2 *q, float2 *rest) {
-  float2 t = mul2(x, both(-kLog2e));
-  asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(t.x));
-  asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(t.y));
-  const float2 e = make_float2(ex2(t.x), ex2(t.y)), d = add2(e, both(1.f));
-  *q = make_float2(rcp(d.x), rcp(d.y));
-  *rest = mul2(e, *q);
-}
 // v less its mean where centred (zero past the row's end), and the reciprocal root of its mean square.
 template <bool VEC, int L>
 __device__ __forceinline__ float row_stats(float2 *v, const NormProblem &p, const Place<VEC, L> &pl, int D, float2 (*red)[32], int &turn) {

@@ -14,17 +14,21 @@ namespace gdp {
 namespace layer {
 namespace {
 
+#ifndef SB8
+#define SB8 0
+#endif
 constexpr int kBwdCtas = 2;  // resident CTAs per SM
 
 template <typename TX, typename TG, int GATE, bool Q8, bool RAW>
 struct BwdLayout {
-  static constexpr int S = 8;  // tokens per warp
+  // tokens per warp: sixteen decays stay in registers, or eight with the input factors
+  static constexpr int S = GATE == GDP_GATE_SIGMOID || sizeof(TX) == 4 || SB8 ? 8 : 16;
   static constexpr int kTile = kScanWarps * S;
   static constexpr bool kX = GATE == GDP_GATE_SIGMOID;
   static constexpr int g_off = 0, d_off = g_off + tile_bytes<TG>(kTile, RAW), h_off = d_off + tile_bytes<TX>(kTile, RAW);
   static constexpr int s_off = h_off + (Q8 ? tile_bytes<int8_t>(kTile, RAW) : tile_bytes<TX>(kTile, RAW));
   static constexpr int x_off = s_off + (Q8 ? kTile * 4 : 0), stage = (x_off + (kX ? tile_bytes<TX>(kTile, RAW) : 0) + 127) / 128 * 128;
-  static constexpr int kStages = stage <= 22000 ? 4 : stage <= 30000 ? 3 : 2;
+  static constexpr int kStages = stage <= 22000 ? 4 : stage <= 34000 ? 3 : 2;
   static constexpr int kMeta = kStages + 1;
   static constexpr int parts = kStages * stage, enter = parts + Chain::parts_bytes, meta = enter + Chain::enter_bytes;
   static constexpr int bars = (meta + kMeta * (int)sizeof(TileMeta<S>) + 15) / 16 * 16;
@@ -118,6 +122,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
   } else {
     const int64_t c = c0 + 2 * lane;
     const bool all_channels = c0 + kSlice <= s.C && p.vec_dx && p.vec_dg;
+    const int64_t scale0 = Q8 ? scale_index(c) : 0, scale1 = Q8 ? scale_index(c + 1) : 0;
     const int block = kScanWarps - 1 - warp;  // this warp's tokens: rows block * S .. + S - 1, last first
     for (int n = 0; n < steps; ++n) {
       const int st = n % L::kStages;
@@ -127,57 +132,27 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
       const TileMeta<S> &m = metas[n % L::kMeta];
       const uint32_t starts = m.starts[block], ends = m.ends[block];
       const int lo = m.lo - block * S, hi = m.hi - block * S;
-      float2 a[S], f[L::kX ? S : 1];
-      typename Packed<TX>::type d[S], x[L::kX ? S : 1];
-      typename std::conditional<Q8, float2, typename Packed<TX>::type>::type before[S];
-      float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
-      auto previous = [&](int i) {
-        if constexpr (Q8) return before[i];
-        else return unpack<TX>(before[i]);
+      auto row_of = [&](int off, int pitch, int i) { return base + off + (block * S + i) * pitch; };
+      auto upstream = [&](int i) {
+        return unpack<TX>(read_packed<TX, RAW>(base + L::d_off, block * S + i, lane, RAW ? raw_offset<TX>(p.dout, t0 + i, c0) : 0));
       };
+      float2 a[S], f[L::kX ? S : 1];
+      float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = S - 1; i >= 0; --i) {
-        const int row = block * S + i;
-        const int64_t t = t0 + i;
         float2 fi;
-        gate_pair<GATE>(unpack<TG>(read_packed<TG, RAW>(base + L::g_off, row, lane, RAW ? raw_offset<TG>(p.g, t, c0) : 0)), &a[i], &fi);
-        d[i] = read_packed<TX, RAW>(base + L::d_off, row, lane, RAW ? raw_offset<TX>(p.dout, t, c0) : 0);
-        if constexpr (L::kX) {
-          f[i] = fi;
-          x[i] = read_packed<TX, RAW>(base + L::x_off, row, lane, RAW ? raw_offset<TX>(p.x, t, c0) : 0);
-        }
-        if constexpr (Q8) {
-          const int8_t *q = reinterpret_cast<const int8_t *>(base + L::h_off) + row * tile_pitch<int8_t>(RAW) +
-                            (RAW ? raw_offset<int8_t>(p.codes, t - 1, c0) : 0) + 2 * lane;
-          float2 sc = make_float2(0.f, 0.f);
-          if (one_scale) {
-            sc.x = sc.y = *reinterpret_cast<const float *>(base + L::s_off + 4 * row);
-          } else if (t >= 1 && t <= s.T) {
-            if (c < s.C) sc.x = p.scales[(t - 1) * scales_per_token + scale_index(c)];
-            if (c + 1 < s.C) sc.y = p.scales[(t - 1) * scales_per_token + scale_index(c + 1)];
-          }
-          if constexpr (RAW) {
-            before[i] = make_float2((float)q[0] * sc.x, (float)q[1] * sc.y);
-          } else {
-            const char2 q2 = *reinterpret_cast<const char2 *>(q);
-            before[i] = mul2(make_float2((float)q2.x, (float)q2.y), sc);
-          }
-        } else {
-          before[i] = read_packed<TX, RAW>(base + L::h_off, row, lane, RAW ? raw_offset<TX>(p.h, t - 1, c0) : 0);
-        }
+        gate_pair<GATE>(unpack<TG>(read_packed<TG, RAW>(base + L::g_off, block * S + i, lane, RAW ? raw_offset<TG>(p.g, t0 + i, c0) : 0)),
+                        &a[i], &fi);
+        if constexpr (L::kX) f[i] = fi;
         A = mul2(A, a[i]);
-        const float2 v = unpack<TX>(d[i]);
-        B = mul2(a[i], make_float2(v.x + B.x, v.y + B.y));
+        B = mul2(a[i], add2(upstream(i), B));
       }
-      __syncwarp();
-      if (lane == 0) sm100::mbar_arrive(&empty[st]);
       if (ends) {  // again, token by token
         B = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = S - 1; i >= 0; --i) {
           if (ends >> i & 1u) B = read_state(p.dfin, m.end_row[block * S + i], s.C, c);
-          const float2 v = unpack<TX>(d[i]);
-          B = mul2(a[i], make_float2(v.x + B.x, v.y + B.y));
+          B = mul2(a[i], add2(upstream(i), B));
         }
       }
       ch.parts[warp * 32 + lane] = make_float4(A.x, A.y, B.x, B.y);
@@ -187,14 +162,34 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
       float2 E = ch.enter[warp * 32 + lane];
       TX *dx = static_cast<TX *>(p.dx) + (t0 + S - 1) * s.C + c;
       TG *dg = static_cast<TG *>(p.dg) + (t0 + S - 1) * s.C + c;
+      // the state before token i
+      auto before = [&](int i) {
+        if constexpr (Q8) {
+          const unsigned char *q = row_of(L::h_off, tile_pitch<int8_t>(RAW), i) + (RAW ? raw_offset<int8_t>(p.codes, t0 + i - 1, c0) : 0) + 2 * lane;
+          // a byte plus 128 under the exponent of 2^23 is 2^23 + 128 + code
+          const uint32_t w = (RAW ? (uint32_t)q[0] | (uint32_t)q[1] << 8 : (uint32_t) * reinterpret_cast<const uint16_t *>(q)) ^ 0x8080u;
+          const float2 v = add2(make_float2(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440)), __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441))),
+                                both(-8388736.f));
+          if (one_scale) return mul2(v, both(*reinterpret_cast<const float *>(row_of(L::s_off, 4, i))));
+          float2 sc = both(0.f);
+          const int64_t t = t0 + i - 1;
+          if (t >= 0 && t < s.T) {
+            if (c < s.C) sc.x = p.scales[t * scales_per_token + scale0];
+            if (c + 1 < s.C) sc.y = p.scales[t * scales_per_token + scale1];
+          }
+          return mul2(v, sc);
+        } else {
+          return unpack<TX>(read_packed<TX, RAW>(base + L::h_off, block * S + i, lane, RAW ? raw_offset<TX>(p.h, t0 + i - 1, c0) : 0));
+        }
+      };
       // D in, dx and dg out; E moves on to this token
       auto token = [&](int i, float2 prev, float2 *ox, float2 *og) {
-        const float2 v = unpack<TX>(d[i]), D = make_float2(v.x + E.x, v.y + E.y);
+        const float2 D = add2(upstream(i), E);
         E = mul2(a[i], D);
         if constexpr (L::kX) {
-          const float2 in = unpack<TX>(x[i]);
+          const float2 in = unpack<TX>(read_packed<TX, RAW>(base + L::x_off, block * S + i, lane, RAW ? raw_offset<TX>(p.x, t0 + i, c0) : 0));
           *ox = mul2(f[i], D);
-          *og = mul2(mul2(f[i], E), make_float2(prev.x - in.x, prev.y - in.y));
+          *og = mul2(mul2(f[i], E), fma2(in, both(-1.f), prev));
         } else {
           *ox = D;
           *og = mul2(GATE == GDP_GATE_LOG ? E : D, prev);
@@ -204,7 +199,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
 #pragma unroll
         for (int i = S - 1; i >= 0; --i) {
           float2 ox, og;
-          token(i, previous(i), &ox, &og);
+          token(i, before(i), &ox, &og);
           write_pair(dx, ox, true, true);
           write_pair(dg, og, true, true);
           dx -= s.C;
@@ -215,7 +210,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
         for (int i = S - 1; i >= 0; --i) {
           if (ends >> i & 1u) E = read_state(p.dfin, m.end_row[block * S + i], s.C, c);
           float2 ox, og;
-          token(i, starts >> i & 1u ? read_state(p.init, m.start_row[block * S + i], s.C, c) : previous(i), &ox, &og);
+          token(i, starts >> i & 1u ? read_state(p.init, m.start_row[block * S + i], s.C, c) : before(i), &ox, &og);
           if (i >= lo && i < hi && c < s.C) {
             write_pair(dx, ox, c + 1 < s.C, p.vec_dx);
             write_pair(dg, og, c + 1 < s.C, p.vec_dg);
@@ -225,6 +220,8 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
           dg -= s.C;
         }
       }
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&empty[st]);
     }
   }
   __syncwarp();

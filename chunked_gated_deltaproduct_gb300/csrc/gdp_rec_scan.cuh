@@ -141,9 +141,11 @@ __device__ __forceinline__ void gate_pair(float2 g, float2 *a, float2 *f) {
     g = mul2(g, both(kLog2e));
     *a = make_float2(ex2(g.x), ex2(g.y));
     *f = make_float2(1.f, 1.f);
+  } else if constexpr (GATE == GDP_GATE_ALPHA) {
+    *a = g;
+    *f = both(1.f);
   } else {
-    gate_eval<GATE>(g.x, &a->x, &f->x);
-    gate_eval<GATE>(g.y, &a->y, &f->y);
+    sigmoid_halves(g, a, f);
   }
 }
 
