@@ -14,29 +14,33 @@ namespace gdp {
 namespace layer {
 namespace {
 
-#ifndef SB8
-#define SB8 0
-#endif
 constexpr int kBwdCtas = 2;  // resident CTAs per SM
 
 template <typename TX, typename TG, int GATE, bool Q8, bool RAW>
 struct BwdLayout {
-  // tokens per warp: sixteen decays stay in registers, or eight with the input factors
-  static constexpr int S = GATE == GDP_GATE_SIGMOID || sizeof(TX) == 4 || SB8 ? 8 : 16;
+  // Bytes of a channel and token; three stages where that leaves ten tokens per warp, else two (65536 x
+  // 4096 from codes: 401 us with three, 448 us with two; 8 x 4096 x 2048 sigmoid: 174 us and 154 us).
+  static constexpr int kBytes = (int)(sizeof(TG) + sizeof(TX) * (GATE == GDP_GATE_SIGMOID ? 2 : 1) + (Q8 ? 1 : sizeof(TX)));
+  static constexpr int kStages = scan_tokens(3 * kBytes) >= 10 ? 3 : 2, S = scan_tokens(kStages * kBytes);
   static constexpr int kTile = kScanWarps * S;
   static constexpr bool kX = GATE == GDP_GATE_SIGMOID;
   static constexpr int g_off = 0, d_off = g_off + tile_bytes<TG>(kTile, RAW), h_off = d_off + tile_bytes<TX>(kTile, RAW);
   static constexpr int s_off = h_off + (Q8 ? tile_bytes<int8_t>(kTile, RAW) : tile_bytes<TX>(kTile, RAW));
-  static constexpr int x_off = s_off + (Q8 ? kTile * 4 : 0), stage = (x_off + (kX ? tile_bytes<TX>(kTile, RAW) : 0) + 127) / 128 * 128;
-  static constexpr int kStages = stage <= 22000 ? 4 : stage <= 34000 ? 3 : 2;
+  static constexpr int x_off = s_off + (Q8 ? (kTile * 4 + 127) / 128 * 128 : 0);
+  static constexpr int stage = x_off + (kX ? tile_bytes<TX>(kTile, RAW) : 0);
   static constexpr int kMeta = kStages + 1;
   static constexpr int parts = kStages * stage, enter = parts + Chain::parts_bytes, meta = enter + Chain::enter_bytes;
   static constexpr int bars = (meta + kMeta * (int)sizeof(TileMeta<S>) + 15) / 16 * 16;
   static constexpr int mail = (bars + (2 * kStages + Chain::bars) * 8 + 16 + 127) / 128 * 128;  // last: its size is the cluster's
+  // TMA destinations, 16-byte arrays, barriers, and the largest cluster's whole
+  static_assert(g_off % 128 == 0 && d_off % 128 == 0 && h_off % 128 == 0 && x_off % 128 == 0 && s_off % 4 == 0 && S * kSlice * sizeof(TX) % 128 == 0 && S * kSlice * sizeof(TG) % 128 == 0 && stage % 128 == 0, "TMA reads and writes at 128-byte boundaries");
+  static_assert(parts % 16 == 0 && enter % 16 == 0 && meta % 4 == 0 && bars % 8 == 0 && mail % 16 == 0, "alignment");
+  static_assert(mail + Chain::mail_bytes(16) <= kScanSmem, "two CTAs per SM");
 };
 
 struct BwdMaps {
   CUtensorMap g, dout, h, x;  // h: of the tensor or of the codes
+  CUtensorMap dx, dg;
 };
 
 template <typename TX, typename TG, int GATE, bool Q8, bool RAW>
@@ -121,7 +125,10 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
     chain_steps<S, L::kMeta, true>(s, ch, metas, steps, lane, gave_up);
   } else {
     const int64_t c = c0 + 2 * lane;
-    const bool all_channels = c0 + kSlice <= s.C && p.vec_dx && p.vec_dg;
+    // dx and dg take the places of d_output and g in the stage and leave by TMA stores (each warp its own
+    // rows), so that a warp does not wait for memory to take them; rows of unaligned outputs, and tiles with
+    // rows of no sequence, do not
+    const bool bulk = !RAW && p.vec_out;
     const int64_t scale0 = Q8 ? scale_index(c) : 0, scale1 = Q8 ? scale_index(c + 1) : 0;
     const int block = kScanWarps - 1 - warp;  // this warp's tokens: rows block * S .. + S - 1, last first
     for (int n = 0; n < steps; ++n) {
@@ -136,32 +143,39 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
       auto upstream = [&](int i) {
         return unpack<TX>(read_packed<TX, RAW>(base + L::d_off, block * S + i, lane, RAW ? raw_offset<TX>(p.dout, t0 + i, c0) : 0));
       };
-      float2 a[S], f[L::kX ? S : 1];
+      float2 kept[S];  // gates
       float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = S - 1; i >= 0; --i) {
-        float2 fi;
-        gate_pair<GATE>(unpack<TG>(read_packed<TG, RAW>(base + L::g_off, block * S + i, lane, RAW ? raw_offset<TG>(p.g, t0 + i, c0) : 0)),
-                        &a[i], &fi);
-        if constexpr (L::kX) f[i] = fi;
-        A = mul2(A, a[i]);
-        B = mul2(a[i], add2(upstream(i), B));
+        kept[i] = gate_kept<GATE>(
+            unpack<TG>(read_packed<TG, RAW>(base + L::g_off, block * S + i, lane, RAW ? raw_offset<TG>(p.g, t0 + i, c0) : 0)));
+        float2 f;
+        const float2 a = gate_decay<GATE>(kept[i], &f);
+        A = mul2(A, a);
+        B = mul2(a, add2(upstream(i), B));
       }
       if (ends) {  // again, token by token
+        keep_only<S>(kept);
         B = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = S - 1; i >= 0; --i) {
           if (ends >> i & 1u) B = read_state(p.dfin, m.end_row[block * S + i], s.C, c);
-          B = mul2(a[i], add2(upstream(i), B));
+          float2 f;
+          B = mul2(gate_decay<GATE>(kept[i], &f), add2(upstream(i), B));
         }
       }
       ch.parts[warp * 32 + lane] = make_float4(A.x, A.y, B.x, B.y);
       __syncwarp();
-      if (lane == 0) sm100::mbar_arrive(ch.parts_full);
+      if (lane == 0) {
+        sm100::mbar_arrive(ch.parts_full);
+        if (n > 0) {  // the last tile's stage, once its stores have read it
+          sm100::bulk_wait_read<0>();
+          sm100::mbar_arrive(&empty[(n - 1) % L::kStages]);
+        }
+      }
       ring_wait(ch.enter_full, n & 1, gave_up, s.status, s.limit_ns);
+      keep_only<S>(kept);
       float2 E = ch.enter[warp * 32 + lane];
-      TX *dx = static_cast<TX *>(p.dx) + (t0 + S - 1) * s.C + c;
-      TG *dg = static_cast<TG *>(p.dg) + (t0 + S - 1) * s.C + c;
       // the state before token i
       auto before = [&](int i) {
         if constexpr (Q8) {
@@ -182,54 +196,78 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
           return unpack<TX>(read_packed<TX, RAW>(base + L::h_off, block * S + i, lane, RAW ? raw_offset<TX>(p.h, t0 + i - 1, c0) : 0));
         }
       };
-      // D in, dx and dg out; E moves on to this token
-      auto token = [&](int i, float2 prev, float2 *ox, float2 *og) {
-        const float2 D = add2(upstream(i), E);
-        E = mul2(a[i], D);
-        if constexpr (L::kX) {
-          const float2 in = unpack<TX>(read_packed<TX, RAW>(base + L::x_off, block * S + i, lane, RAW ? raw_offset<TX>(p.x, t0 + i, c0) : 0));
-          *ox = mul2(f[i], D);
-          *og = mul2(mul2(f[i], E), fma2(in, both(-1.f), prev));
-        } else {
-          *ox = D;
-          *og = mul2(GATE == GDP_GATE_LOG ? E : D, prev);
+      // Four tokens' inputs are read before any of their outputs is written (outputs go to the same shared
+      // memory, so that the compiler keeps the order: token by token the second run took 221 cycles each).
+      // whole: every row belongs to a sequence and the outputs leave by TMA; plain: no sequence begins or ends
+      auto run = [&](auto whole_, auto plain_) {
+        constexpr bool kWhole = decltype(whole_)::value, kPlain = decltype(plain_)::value;
+        TX *dx = static_cast<TX *>(p.dx) + (t0 + S - 1) * s.C + c;
+        TG *dg = static_cast<TG *>(p.dg) + (t0 + S - 1) * s.C + c;
+        TX *dx_rows = reinterpret_cast<TX *>(smem + st * L::stage + L::d_off) + block * S * kSlice + 2 * lane;
+        TG *dg_rows = reinterpret_cast<TG *>(smem + st * L::stage + L::g_off) + block * S * kSlice + 2 * lane;
+#pragma unroll
+        for (int hi4 = S - 1; hi4 >= 0; hi4 -= 4) {
+          float2 up[4], prev[4], in[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int i = hi4 - u;
+            if (i < 0) break;
+            up[u] = upstream(i);
+            prev[u] = !kPlain && (starts >> i & 1u) ? read_state(p.init, m.start_row[block * S + i], s.C, c) : before(i);
+            if constexpr (L::kX)
+              in[u] = unpack<TX>(read_packed<TX, RAW>(base + L::x_off, block * S + i, lane, RAW ? raw_offset<TX>(p.x, t0 + i, c0) : 0));
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int i = hi4 - u;
+            if (i < 0) break;
+            if (!kPlain && (ends >> i & 1u)) E = read_state(p.dfin, m.end_row[block * S + i], s.C, c);
+            float2 f;
+            const float2 a = gate_decay<GATE>(kept[i], &f), D = add2(up[u], E);
+            E = mul2(a, D);
+            float2 ox = D, og;
+            if constexpr (L::kX) {
+              ox = mul2(f, D);
+              og = mul2(mul2(f, E), fma2(in[u], both(-1.f), prev[u]));
+            } else {
+              og = mul2(GATE == GDP_GATE_LOG ? E : D, prev[u]);
+            }
+            if constexpr (kWhole) {
+              write_pair(dx_rows + i * kSlice, ox, true, true);
+              write_pair(dg_rows + i * kSlice, og, true, true);
+            } else if (i >= lo && i < hi && c < s.C) {
+              write_pair(dx, ox, c + 1 < s.C, p.pair_dx);
+              write_pair(dg, og, c + 1 < s.C, p.pair_dg);
+            }
+            dx -= s.C;
+            dg -= s.C;
+            if (!kPlain && (starts >> i & 1u)) write_state(p.dinit, m.start_row[block * S + i], s.C, c, E);
+          }
+        }
+        if constexpr (kWhole) {
+          sm100::fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            sm100::tma_store_2d(&maps.dx, dx_rows, (int)c0, (int)t0);
+            sm100::tma_store_2d(&maps.dg, dg_rows, (int)c0, (int)t0);
+            sm100::bulk_commit();
+          }
         }
       };
-      if (!(starts | ends) && lo <= 0 && hi >= S && all_channels) {
-#pragma unroll
-        for (int i = S - 1; i >= 0; --i) {
-          float2 ox, og;
-          token(i, before(i), &ox, &og);
-          write_pair(dx, ox, true, true);
-          write_pair(dg, og, true, true);
-          dx -= s.C;
-          dg -= s.C;
-        }
-      } else {
-#pragma unroll
-        for (int i = S - 1; i >= 0; --i) {
-          if (ends >> i & 1u) E = read_state(p.dfin, m.end_row[block * S + i], s.C, c);
-          float2 ox, og;
-          token(i, starts >> i & 1u ? read_state(p.init, m.start_row[block * S + i], s.C, c) : before(i), &ox, &og);
-          if (i >= lo && i < hi && c < s.C) {
-            write_pair(dx, ox, c + 1 < s.C, p.vec_dx);
-            write_pair(dg, og, c + 1 < s.C, p.vec_dg);
-          }
-          if (starts >> i & 1u) write_state(p.dinit, m.start_row[block * S + i], s.C, c, E);
-          dx -= s.C;
-          dg -= s.C;
-        }
-      }
+      const bool whole = lo <= 0 && hi >= S && bulk;
+      if (!RAW && whole && !(starts | ends)) run(std::true_type{}, std::true_type{});
+      else if (!RAW && whole) run(std::true_type{}, std::false_type{});
+      else run(std::false_type{}, std::false_type{});
       __syncwarp();
-      if (lane == 0) sm100::mbar_arrive(&empty[st]);
     }
+    if (lane == 0) sm100::bulk_wait_all();
   }
   __syncwarp();
   cluster_sync();  // no CTA leaves while another may still post to it
 }
 
 template <typename TX, typename TG, int GATE, bool Q8, bool RAW>
-cudaError_t run_bwd_as(RecBwd &p, const BwdMaps &maps, cudaStream_t stream) {
+cudaError_t run_bwd_as(const RecBwd &p, const BwdMaps &maps, cudaStream_t stream) {
   return launch_clusters(gdp_rec_bwd_scan_kernel<TX, TG, GATE, Q8, RAW>, p.s.slices, p.s.cluster,
                          BwdLayout<TX, TG, GATE, Q8, RAW>::mail + Chain::mail_bytes(p.s.cluster), stream, maps, p);
 }
@@ -254,6 +292,11 @@ cudaError_t run_bwd(RecBwd &p, cudaStream_t stream) {
   if ((e = tmap_matrix(&m.dout, p.dout.base, s.T, s.C, p.dout.stride * sizeof(TX), sizeof(TX), kSlice, L::kTile)) != cudaSuccess) return e;
   if ((e = tmap_matrix(&m.h, h.base, s.T, s.C, h.stride * hs, hs, kSlice, L::kTile)) != cudaSuccess) return e;
   if (L::kX && (e = tmap_matrix(&m.x, p.x.base, s.T, s.C, p.x.stride * sizeof(TX), sizeof(TX), kSlice, L::kTile)) != cudaSuccess) return e;
+  p.vec_out = tma_rows(RowSource{p.dx, s.C}, sizeof(TX), s.T, s.C) && tma_rows(RowSource{p.dg, s.C}, sizeof(TG), s.T, s.C);
+  if (p.vec_out) {
+    if ((e = tmap_matrix(&m.dx, p.dx, s.T, s.C, s.C * sizeof(TX), sizeof(TX), kSlice, L::S)) != cudaSuccess) return e;
+    if ((e = tmap_matrix(&m.dg, p.dg, s.T, s.C, s.C * sizeof(TG), sizeof(TG), kSlice, L::S)) != cudaSuccess) return e;
+  }
   return run_bwd_as<TX, TG, GATE, Q8, false>(p, m, stream);
 }
 

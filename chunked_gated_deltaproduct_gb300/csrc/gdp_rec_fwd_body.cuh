@@ -13,22 +13,29 @@ constexpr int kFwdCtas = 2;  // resident CTAs per SM
 
 template <typename TX, typename TG, int GATE, bool RAW>
 struct FwdLayout {
-  // tokens per warp: as many as the registers hold decays and inputs of (sixteen when the input is
-  // kept packed in 16 bits, eight where it needs 32)
-  static constexpr bool kPacked = sizeof(TX) == 2 && GATE != GDP_GATE_SIGMOID;
-  static constexpr int S = kPacked ? 16 : 8;
+  // Sigmoid gates: decays and inputs (three special-function operations a channel to form again) stay in
+  // registers, and the stage is free after the first run; else the second run reads the inputs again
+  // (at 65536 x 4096 bf16, 1.61 GB: 262 us; with three stages 322 us).
+  static constexpr bool kKeep = GATE == GDP_GATE_SIGMOID;
+  static constexpr int kStages = 2;
+  static constexpr int S = scan_tokens(kStages * (int)(sizeof(TX) + sizeof(TG)) + (int)sizeof(TX));
   static constexpr int kTile = kScanWarps * S;
   static constexpr int x_off = 0, g_off = tile_bytes<TX>(kTile, RAW), stage = g_off + tile_bytes<TG>(kTile, RAW);
-  static constexpr int kStages = stage <= 18000 ? 5 : stage <= 36000 ? 3 : 2;
   static constexpr int kMeta = kStages + 1;
-  static constexpr int parts = kStages * stage, enter = parts + Chain::parts_bytes, meta = enter + Chain::enter_bytes;
+  static constexpr int out = kStages * stage, out_bytes = RAW ? 0 : kTile * kSlice * (int)sizeof(TX);
+  static constexpr int parts = out + out_bytes, enter = parts + Chain::parts_bytes, meta = enter + Chain::enter_bytes;
   static constexpr int bars = (meta + kMeta * (int)sizeof(TileMeta<S>) + 15) / 16 * 16;
   static constexpr int mail = (bars + (2 * kStages + Chain::bars) * 8 + 16 + 127) / 128 * 128;  // last: its size is the cluster's
+  // TMA destinations, 16-byte arrays, barriers, and the largest cluster's whole
+  static_assert(x_off % 128 == 0 && g_off % 128 == 0 && out % 128 == 0 && S * kSlice * sizeof(TX) % 128 == 0 && stage % 128 == 0, "TMA writes to 128-byte boundaries");
+  static_assert(parts % 16 == 0 && enter % 16 == 0 && meta % 4 == 0 && bars % 8 == 0 && mail % 16 == 0, "alignment");
+  static_assert(mail + Chain::mail_bytes(16) <= kScanSmem, "two CTAs per SM");
 };
 
 template <typename TX, typename TG, int GATE, bool RAW>
 __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
-    gdp_rec_fwd_scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g, const RecFwd p) {
+    gdp_rec_fwd_scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g,
+                            const __grid_constant__ CUtensorMap map_h, const RecFwd p) {
   using L = FwdLayout<TX, TG, GATE, RAW>;
   constexpr int S = L::S;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -92,7 +99,10 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
     chain_steps<S, L::kMeta, false>(s, ch, metas, steps, lane, gave_up);
   } else {
     const int64_t c = c0 + 2 * lane;
-    const bool all_channels = c0 + kSlice <= s.C && p.vec_out;
+    // outputs leave through shared memory and TMA stores (each warp its own rows), so that a warp does not
+    // wait for memory to take them; rows of unaligned outputs, and tiles with rows of no sequence, do not
+    const bool bulk = !RAW && p.vec_out;
+    unsigned char *mine = smem + L::out + warp * S * kSlice * (int)sizeof(TX);
     for (int n = 0; n < steps; ++n) {
       const int st = n % L::kStages;
       const unsigned char *xs = smem + st * L::stage + L::x_off, *gs = smem + st * L::stage + L::g_off;
@@ -101,70 +111,101 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
       const TileMeta<S> &m = metas[n % L::kMeta];
       const uint32_t starts = m.starts[warp], ends = m.ends[warp];
       const int lo = m.lo - warp * S, hi = m.hi - warp * S;
-      // ---- from zero: decays and inputs stay in registers.  Where a sequence begins, the decay's
-      // place takes the state after that token.
-      float2 a[S];
-      typename std::conditional<L::kPacked, uint32_t, float2>::type b[S];
+      // ---- from zero: the decays stay in registers, and the inputs too (kKeep).  Where a sequence begins,
+      // the decay's place takes the state after that token.
+      float2 a[S], b[L::kKeep ? S : 1];
       float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
-      auto input = [&](int i) {
-        if constexpr (L::kPacked) return unpack<TX>(b[i]);
-        else return b[i];
+      auto read_x = [&](int i) {
+        return unpack<TX>(read_packed<TX, RAW>(xs, warp * S + i, lane, RAW ? raw_offset<TX>(p.x, t0 + i, c0) : 0));
       };
 #pragma unroll
       for (int i = 0; i < S; ++i) {
         float2 f;
-        gate_pair<GATE>(unpack<TG>(read_packed<TG, RAW>(gs, warp * S + i, lane, RAW ? raw_offset<TG>(p.g, t0 + i, c0) : 0)), &a[i], &f);
-        const auto x = read_packed<TX, RAW>(xs, warp * S + i, lane, RAW ? raw_offset<TX>(p.x, t0 + i, c0) : 0);
-        if constexpr (L::kPacked) b[i] = x;
-        else if constexpr (GATE == GDP_GATE_SIGMOID) b[i] = mul2(f, unpack<TX>(x));
-        else b[i] = unpack<TX>(x);
+        a[i] = gate_decay<GATE>(
+            gate_kept<GATE>(unpack<TG>(read_packed<TG, RAW>(gs, warp * S + i, lane, RAW ? raw_offset<TG>(p.g, t0 + i, c0) : 0))), &f);
+        const float2 x = GATE == GDP_GATE_SIGMOID ? mul2(f, read_x(i)) : read_x(i);
+        if constexpr (L::kKeep) b[i] = x;
+        B = fma2(a[i], B, x);
         A = mul2(A, a[i]);
-        B = fma2(a[i], B, input(i));
       }
-      __syncwarp();
-      if (lane == 0) sm100::mbar_arrive(&empty[st]);
       if (starts) {  // again, token by token
+        keep_only<S>(a);
         B = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < S; ++i) {
           if (starts >> i & 1u) B = read_state(p.from, m.start_row[warp * S + i], s.C, c);
-          B = fma2(a[i], B, input(i));
+          float2 x;
+          if constexpr (L::kKeep) x = b[i];
+          else x = read_x(i);
+          B = fma2(a[i], B, x);
           if (starts >> i & 1u) a[i] = B;
         }
       }
       ch.parts[warp * 32 + lane] = make_float4(A.x, A.y, B.x, B.y);
       __syncwarp();
-      if (lane == 0) sm100::mbar_arrive(ch.parts_full);
+      if (lane == 0) {
+        sm100::mbar_arrive(ch.parts_full);
+        if (L::kKeep) sm100::mbar_arrive(&empty[st]);
+        sm100::bulk_wait_read<0>();  // the last tile's store has read `mine`
+      }
+      __syncwarp();
       ring_wait(ch.enter_full, n & 1, gave_up, s.status, s.limit_ns);
-      // ---- from the entering state
+      keep_only<S>(a);
+      // ---- from the entering state.  Four tokens' inputs are read before their outputs are written (the
+      // compiler keeps the order of accesses to shared memory).
+      // whole: every row belongs to a sequence and the outputs leave by TMA; plain: no sequence begins or ends
       float2 h = ch.enter[warp * 32 + lane];
-      TX *out = static_cast<TX *>(p.h) + t0 * s.C + c;
-      if (!(starts | ends) && lo <= 0 && hi >= S && all_channels) {
+      auto run = [&](auto whole_, auto plain_) {
+        constexpr bool kWhole = decltype(whole_)::value, kPlain = decltype(plain_)::value;
+        TX *out = static_cast<TX *>(p.h) + t0 * s.C + c, *rows = reinterpret_cast<TX *>(mine) + 2 * lane;
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-          h = fma2(a[i], h, input(i));
-          write_pair(out, h, true, true);
-          out += s.C;
-        }
-      } else {
+        for (int lo4 = 0; lo4 < S; lo4 += 4) {
+          float2 x[4];
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-          h = (starts >> i & 1u) ? a[i] : fma2(a[i], h, input(i));
-          if (i >= lo && i < hi && c < s.C) write_pair(out, h, c + 1 < s.C, p.vec_out);
-          if (ends >> i & 1u) write_state(p.to, m.end_row[warp * S + i], s.C, c, h);
-          out += s.C;
+          for (int u = 0; u < 4; ++u) {
+            if (lo4 + u >= S) break;
+            if constexpr (L::kKeep) x[u] = b[lo4 + u];
+            else x[u] = read_x(lo4 + u);
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int i = lo4 + u;
+            if (i >= S) break;
+            h = !kPlain && (starts >> i & 1u) ? a[i] : fma2(a[i], h, x[u]);
+            if constexpr (kWhole) write_pair(rows + i * kSlice, h, true, true);
+            else if (i >= lo && i < hi && c < s.C) write_pair(out, h, c + 1 < s.C, p.pair_out);
+            out += s.C;
+            if (!kPlain && (ends >> i & 1u)) write_state(p.to, m.end_row[warp * S + i], s.C, c, h);
+          }
         }
+        if constexpr (kWhole) {
+          sm100::fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            sm100::tma_store_2d(&map_h, mine, (int)c0, (int)t0);
+            sm100::bulk_commit();
+          }
+        }
+      };
+      const bool whole = lo <= 0 && hi >= S && bulk;
+      if (!RAW && whole && !(starts | ends)) run(std::true_type{}, std::true_type{});
+      else if (!RAW && whole) run(std::true_type{}, std::false_type{});
+      else run(std::false_type{}, std::false_type{});
+      if (!L::kKeep) {
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&empty[st]);
       }
     }
+    if (lane == 0) sm100::bulk_wait_all();
   }
   __syncwarp();
   cluster_sync();  // no CTA leaves while another may still post to it
 }
 
 template <typename TX, typename TG, int GATE, bool RAW>
-cudaError_t run_fwd_as(RecFwd &p, const CUtensorMap *maps, cudaStream_t stream) {
+cudaError_t run_fwd_as(const RecFwd &p, const CUtensorMap *maps, cudaStream_t stream) {
   return launch_clusters(gdp_rec_fwd_scan_kernel<TX, TG, GATE, RAW>, p.s.slices, p.s.cluster,
-                         FwdLayout<TX, TG, GATE, RAW>::mail + Chain::mail_bytes(p.s.cluster), stream, maps[0], maps[1], p);
+                         FwdLayout<TX, TG, GATE, RAW>::mail + Chain::mail_bytes(p.s.cluster), stream, maps[0], maps[1], maps[2], p);
 }
 
 template <typename TX, typename TG, int GATE>
@@ -175,12 +216,14 @@ cudaError_t run_fwd(RecFwd &p, cudaStream_t stream) {
   s.rows = rows > 0 ? (int)rows : 1;
   s.slices = (int)((s.C + kSlice - 1) / kSlice);
   s.cluster = cluster_size(s.slices, s.rows, sm_count(), kFwdCtas);
-  CUtensorMap maps[2];
+  CUtensorMap maps[3];
   memset(maps, 0, sizeof(maps));
   if (!tma_rows(p.x, sizeof(TX), s.T, s.C) || !tma_rows(p.g, sizeof(TG), s.T, s.C)) return run_fwd_as<TX, TG, GATE, true>(p, maps, stream);
   cudaError_t e;
   if ((e = tmap_matrix(&maps[0], p.x.base, s.T, s.C, p.x.stride * sizeof(TX), sizeof(TX), kSlice, L::kTile)) != cudaSuccess) return e;
   if ((e = tmap_matrix(&maps[1], p.g.base, s.T, s.C, p.g.stride * sizeof(TG), sizeof(TG), kSlice, L::kTile)) != cudaSuccess) return e;
+  p.vec_out = tma_rows(RowSource{p.h, s.C}, sizeof(TX), s.T, s.C);
+  if (p.vec_out && (e = tmap_matrix(&maps[2], p.h, s.T, s.C, s.C * sizeof(TX), sizeof(TX), kSlice, L::S)) != cudaSuccess) return e;
   return run_fwd_as<TX, TG, GATE, false>(p, maps, stream);
 }
 

@@ -134,23 +134,47 @@ __device__ __forceinline__ float2 unpack(typename Packed<T>::type v) {
   }
 }
 
-// Both channels' decay and input factor.
+// Both channels' gates in two steps: what stays in registers between the two runs over a tile (the decay;
+// for the sigmoid e^-g, held to 2^115, from which either half follows to its own relative precision), and
+// decay and input factor from it.
 template <int GATE>
-__device__ __forceinline__ void gate_pair(float2 g, float2 *a, float2 *f) {
-  if constexpr (GATE == GDP_GATE_LOG) {
-    g = mul2(g, both(kLog2e));
-    *a = make_float2(ex2(g.x), ex2(g.y));
-    *f = make_float2(1.f, 1.f);
-  } else if constexpr (GATE == GDP_GATE_ALPHA) {
-    *a = g;
+__device__ __forceinline__ float2 gate_kept(float2 g) {
+  if constexpr (GATE == GDP_GATE_ALPHA) return g;
+  float2 t = mul2(g, both(GATE == GDP_GATE_LOG ? kLog2e : -kLog2e));
+  if constexpr (GATE == GDP_GATE_SIGMOID) {
+    asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(t.x));
+    asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(t.y));
+  }
+  return make_float2(ex2(t.x), ex2(t.y));
+}
+template <int GATE>
+__device__ __forceinline__ float2 gate_decay(float2 kept, float2 *f) {
+  if constexpr (GATE != GDP_GATE_SIGMOID) {
     *f = both(1.f);
+    return kept;
   } else {
-    sigmoid_halves(g, a, f);
+    const float2 d = add2(kept, both(1.f)), a = make_float2(rcp(d.x), rcp(d.y));
+    *f = mul2(kept, a);
+    return a;
   }
 }
+// Makes another run over the tile form decay and factor from these again, and read the tile again (the
+// compiler would keep what the run before formed and read, and spill).
+template <int S>
+__device__ __forceinline__ void keep_only(float2 *kept) {
+#pragma unroll
+  for (int i = 0; i < S; ++i) asm volatile("" : "+f"(kept[i].x), "+f"(kept[i].y)::"memory");
+}
+// Tokens per warp when a channel and token takes `bytes` of shared memory (all stages and the outputs), so
+// that with the chain's part two CTAs share an SM; at most sixteen gates of two channels stay in registers.
+constexpr int scan_tokens(int bytes) {
+  const int n = 160 / bytes / 2 * 2;
+  return n > 16 ? 16 : n;
+}
+constexpr int kScanSmem = 113 * 1024 + 512 - 1024;  // of a CTA, two per SM
 
 template <typename T>
-__device__ __forceinline__ void write_pair(T *p, float2 v, bool both, bool vec) {
+__device__ __forceinline__ void write_pair(T *p, float2 v, bool two, bool vec) {
   if (vec) {  // even channel count, aligned base: one store
     if constexpr (sizeof(T) == 4) {
       *reinterpret_cast<float2 *>(p) = v;
@@ -159,7 +183,7 @@ __device__ __forceinline__ void write_pair(T *p, float2 v, bool both, bool vec) 
     }
   } else {
     p[0] = from_f32<T>(v.x);
-    if (both) p[1] = from_f32<T>(v.y);
+    if (two) p[1] = from_f32<T>(v.y);
   }
 }
 // The lane's two channels of a state row (channels past C read as zero / are not written).
@@ -305,6 +329,10 @@ constexpr uint32_t kCut = 0xffffffffu;
 // A wait on a full or empty barrier: bounded; once one ran out in the CTA the others return at once
 // and the kernel runs to its end with undefined outputs (every copy it issued is still waited for).
 __device__ __forceinline__ void ring_wait(uint64_t *bar, uint32_t parity, volatile int *gave_up, uint32_t *status, uint64_t limit_ns) {
+  // sleeping tries first: the bounded wait begins with a read of the global timer, which takes longer
+  // than most waits here (8 x 4096 x 2048 backward: 235 us with it alone, 150 us so)
+  for (int i = 0; i < 64; ++i)
+    if (sm100::mbar_try_sleep(bar, parity, 1000u)) return;
   if (!sm100::mbar_wait_or_abort(bar, parity, gave_up, limit_ns)) set_status(status, GDP_DEV_ERR_TIMEOUT);
 }
 
@@ -377,7 +405,8 @@ struct RecFwd {
   void *h;
   const float *from;  // state rows read (initial state or cache)
   float *to;          // state rows written (final state or cache)
-  int vec_out;
+  int pair_out;       // two channels of h can be stored at once
+  int vec_out;        // h can be stored by TMA
 };
 struct RecBwd {
   ScanShape s;
@@ -389,7 +418,8 @@ struct RecBwd {
   const float *init, *dfin;
   void *dx, *dg;
   float *dinit;
-  int vec_dx, vec_dg;
+  int pair_dx, pair_dg;  // two channels can be stored at once
+  int vec_out;           // dx and dg can be stored by TMA
 };
 
 // Fills s.rows, s.slices and s.cluster and launches (instantiated in gdp_rec_*.cu).

@@ -169,7 +169,7 @@ GDP_EXPORT gdp_status gdp_linear_recurrence(const gdp_recurrence_args *args, voi
   f.x = {p.x, p.x_st}; f.g = {p.g, p.g_st}; f.h = p.h;
   f.from = p.cache ? p.cache : p.init;
   f.to = p.cache ? p.cache : p.fin;
-  f.vec_out = p.C % 2 == 0 && aligned(p.h, 2 * dtype_size(p.x_type));
+  f.pair_out = p.C % 2 == 0 && aligned(p.h, 2 * dtype_size(p.x_type));
   return dispatch(p.x_type, p.g_type, f, p.gate, (cudaStream_t)stream);
 }
 
@@ -217,8 +217,8 @@ GDP_EXPORT gdp_status gdp_linear_recurrence_backward(const gdp_recurrence_backwa
   p.blocks = (p.group + kBlock - 1) / kBlock;
   p.init = a->initial_state; p.dfin = a->d_final_state;
   p.dx = a->dx; p.dg = a->dg; p.dinit = a->d_initial_state;
-  p.vec_dx = a->C % 2 == 0 && aligned(a->dx, 2 * dtype_size(a->x_dtype));
-  p.vec_dg = a->C % 2 == 0 && aligned(a->dg, 2 * dtype_size(a->g_dtype));
+  p.pair_dx = a->C % 2 == 0 && aligned(a->dx, 2 * dtype_size(a->x_dtype));
+  p.pair_dg = a->C % 2 == 0 && aligned(a->dg, 2 * dtype_size(a->g_dtype));
   return dispatch(a->x_dtype, a->g_dtype, p, a->gate, (cudaStream_t)stream);
 }
 
