@@ -12,6 +12,7 @@ constexpr int kFinishWarps = 32;
 __global__ void __launch_bounds__(32 * kFinishWarps) gdp_norm_finish_kernel(const float *partial, int64_t parts, int64_t cols, float *dw,
                                                                             float *db) {
   __shared__ float sums[kFinishWarps][32];
+  sm100::pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + lane;
   const float *from = partial + (blockIdx.y ? parts * cols : 0);
@@ -95,7 +96,7 @@ GDP_EXPORT gdp_status gdp_group_norm(const gdp_group_norm_args *a, void *stream)
   p.center = a->center != 0; p.per_head = a->per_head != 0; p.act = a->activation;
   const int vec = p.D % 8 == 0 && vec_ok(p.o, p.o_st, p.o_sh, p.T, p.H, a->dtype) && (!p.z || vec_ok(p.z, p.z_st, p.z_sh, p.T, p.H, a->dtype)) &&
                   aligned(p.y, 16) && aligned(p.o_codes, 8) && aligned(p.z_codes, 8);
-  const NormPlan n = norm_plan(p.T, p.H, p.D, p.per_head, vec, sm_count(), GRIDF);
+  const NormPlan n = norm_plan(p.T, p.H, p.D, p.per_head, vec, sm_count(), kNormFwdCtas);
   p.vec_cols = p.D % 8 == 0 && aligned(p.w, 16) && aligned(p.b, 16);
   p.heads = n.heads; p.groups = n.groups; p.parts = n.parts;
   cudaStream_t s = (cudaStream_t)stream;
@@ -109,7 +110,7 @@ GDP_EXPORT size_t gdp_group_norm_workspace_bytes(int64_t T, int64_t H, int64_t D
   using namespace gdp::layer;
   if (T < 0 || H < 1 || D < 1 || D > 8192 || H > (1 << 20) || T > INT32_MAX) return 0;
   const size_t cols = per_head ? (size_t)(H * D) : (size_t)D;
-  const int64_t a = norm_plan(T, H, D, per_head, 0, sm_count(), GRIDB).parts, b = norm_plan(T, H, D, per_head, 1, sm_count(), GRIDB).parts;
+  const int64_t a = norm_plan(T, H, D, per_head, 0, sm_count(), kNormBwdCtas).parts, b = norm_plan(T, H, D, per_head, 1, sm_count(), kNormBwdCtas).parts;
   return ((size_t)(a > b ? a : b) * 2 * cols * 4 + 255) / 256 * 256;
 }
 
@@ -154,7 +155,7 @@ GDP_EXPORT gdp_status gdp_group_norm_backward(const gdp_group_norm_backward_args
   const int vec = p.D % 8 == 0 && vec_ok(p.dy, p.dy_st, p.dy_sh, p.T, p.H, a->dtype) &&
                   (!p.o || vec_ok(p.o, p.o_st, p.o_sh, p.T, p.H, a->dtype)) && (!p.z || vec_ok(p.z, p.z_st, p.z_sh, p.T, p.H, a->dtype)) &&
                   aligned(p.o_codes_in, 8) && aligned(p.z_codes_in, 8) && aligned(p.d_o, 16) && aligned(p.d_z, 16);
-  const NormPlan n = norm_plan(p.T, p.H, p.D, p.per_head, vec, sm_count(), GRIDB);
+  const NormPlan n = norm_plan(p.T, p.H, p.D, p.per_head, vec, sm_count(), kNormBwdCtas);
   p.vec_cols = p.D % 8 == 0 && aligned(p.w, 16) && aligned(p.b, 16);
   p.heads = n.heads; p.groups = n.groups; p.parts = n.parts;
   cudaError_t e = a->dtype == GDP_DTYPE_BF16  ? launch_norm_bwd<__nv_bfloat16>(p, n, s)
@@ -162,8 +163,8 @@ GDP_EXPORT gdp_status gdp_group_norm_backward(const gdp_group_norm_backward_args
                                               : launch_norm_bwd<float>(p, n, s);
   if (e == cudaSuccess) {
     const int64_t cols = p.per_head ? p.H * p.D : p.D;
-    gdp_norm_finish_kernel<<<dim3((unsigned)((cols + 31) / 32), p.db ? 2 : 1), 32 * kFinishWarps, 0, s>>>(p.partial, n.parts, cols, p.dw, p.db);
-    e = cudaGetLastError();
+    e = gdp::launch_kernel(gdp_norm_finish_kernel, dim3((unsigned)((cols + 31) / 32), p.db ? 2 : 1), dim3(32 * kFinishWarps), 0, s, true,
+                           (const float *)p.partial, n.parts, cols, p.dw, p.db);
   }
   return norm_status(e, "group norm backward kernels");
 }

@@ -23,10 +23,13 @@ constexpr int kPer = 16;  // channels of a thread: 8 cost 42 instructions per ch
 template <bool VEC, int L>
 struct Place {
   static constexpr int kRun = L == 4 ? 4 : 8;
-  int id, first;  // thread of the group, its first channel
-  __device__ __forceinline__ Place() {
+  int id, first;     // thread of the group, its first channel
+  bool in[2];        // VEC: its two halves lie in the row
+  __device__ __forceinline__ explicit Place(int D) {
     id = L > 0 ? (int)threadIdx.x % (L > 0 ? L : 1) : (int)threadIdx.x;
     first = VEC ? id * kPer : id / kRun * (kRun * kPer) + id % kRun;
+    in[0] = first < D;
+    in[1] = first + 8 < D;
   }
   __device__ __forceinline__ int at(int j) const { return first + (VEC ? j : kRun * j); }
   __device__ __forceinline__ bool leads_block() const { return id % kRun == 0; }
@@ -52,46 +55,48 @@ struct alignas(16) Sixteen {
   }
 };
 
-// VEC: 16 bytes at a time, eight channels (of codes: sixteen) at least, D a multiple of eight.
+// Loads and stores of a row, `at` pointing to the thread's first channel.  VEC: 16 bytes at a time, eight
+// channels (of codes: eight or sixteen), D a multiple of eight.
 template <typename T, bool VEC, int L>
-__device__ __forceinline__ void load_row(Sixteen<T> &e, const T *row, const Place<VEC, L> &pl, int D, bool on) {
+__device__ __forceinline__ void load_row(Sixteen<T> &e, const T *at, const Place<VEC, L> &pl, int D, bool on) {
   if constexpr (VEC && sizeof(T) == 1) {
     uint2 *to = reinterpret_cast<uint2 *>(e.v);
-    const uint2 *from = reinterpret_cast<const uint2 *>(row + pl.first);
-    to[0] = on && pl.first < D ? __ldcs(from) : make_uint2(0u, 0u);
-    to[1] = on && pl.first + 8 < D ? __ldcs(from + 1) : make_uint2(0u, 0u);
+    const uint2 *from = reinterpret_cast<const uint2 *>(at);
+    to[0] = on && pl.in[0] ? __ldcs(from) : make_uint2(0u, 0u);
+    to[1] = on && pl.in[1] ? __ldcs(from + 1) : make_uint2(0u, 0u);
   } else if constexpr (VEC) {
     uint4 *to = reinterpret_cast<uint4 *>(e.v);
-    const uint4 *from = reinterpret_cast<const uint4 *>(row + pl.first);
+    const uint4 *from = reinterpret_cast<const uint4 *>(at);
     constexpr int n = (int)sizeof(T);  // 16-byte words
 #pragma unroll
-    for (int i = 0; i < n; ++i) to[i] = on && pl.first + i / (n / 2) * 8 < D ? __ldcs(from + i) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < n; ++i) to[i] = on && pl.in[i / (n / 2)] ? __ldcs(from + i) : make_uint4(0u, 0u, 0u, 0u);
   } else {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      if constexpr (sizeof(T) == 1) e.v[j] = on && pl.at(j) < D ? row[pl.at(j)] : (T)0;
-      else e.v[j] = on && pl.at(j) < D ? row[pl.at(j)] : from_f32<T>(0.f);
+      const bool in = on && pl.at(j) < D;
+      if constexpr (sizeof(T) == 1) e.v[j] = in ? at[pl.kRun * j] : (T)0;
+      else e.v[j] = in ? at[pl.kRun * j] : from_f32<T>(0.f);
     }
   }
 }
 template <typename T, bool VEC, int L>
-__device__ __forceinline__ void store_row(T *row, const Sixteen<T> &e, const Place<VEC, L> &pl, int D) {
+__device__ __forceinline__ void store_row(T *at, const Sixteen<T> &e, const Place<VEC, L> &pl, int D, bool on) {
   if constexpr (VEC && sizeof(T) == 1) {
     const uint2 *from = reinterpret_cast<const uint2 *>(e.v);
-    uint2 *to = reinterpret_cast<uint2 *>(row + pl.first);
-    if (pl.first < D) __stcs(to, from[0]);
-    if (pl.first + 8 < D) __stcs(to + 1, from[1]);
+    uint2 *to = reinterpret_cast<uint2 *>(at);
+    if (on && pl.in[0]) __stcs(to, from[0]);
+    if (on && pl.in[1]) __stcs(to + 1, from[1]);
   } else if constexpr (VEC) {
     const uint4 *from = reinterpret_cast<const uint4 *>(e.v);
-    uint4 *to = reinterpret_cast<uint4 *>(row + pl.first);
+    uint4 *to = reinterpret_cast<uint4 *>(at);
     constexpr int n = (int)sizeof(T);
 #pragma unroll
     for (int i = 0; i < n; ++i)
-      if (pl.first + i / (n / 2) * 8 < D) __stcs(to + i, from[i]);
+      if (on && pl.in[i / (n / 2)]) __stcs(to + i, from[i]);
   } else {
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-      if (pl.at(j) < D) row[pl.at(j)] = e.v[j];
+      if (on && pl.at(j) < D) at[pl.kRun * j] = e.v[j];
   }
 }
 
@@ -113,11 +118,11 @@ struct Source {
   }
 };
 template <typename T, bool Q8, bool VEC, int L>
-__device__ __forceinline__ void load_source(Source<T, Q8> &s, const void *tensor, int64_t at, const int8_t *codes, const float *scales,
-                                            int64_t row, int D, int blocks, const Place<VEC, L> &pl, bool on) {
+__device__ __forceinline__ void load_source(Source<T, Q8> &s, const void *tensor, const int8_t *codes, const float *scales, int64_t at,
+                                            int64_t scale_at, const Place<VEC, L> &pl, int D, bool on) {
   if constexpr (Q8) {
-    load_row<int8_t, VEC, L>(s.e, codes + row * D, pl, D, on);
-    s.scale = on && pl.first < D ? __ldcs(scales + row * blocks + pl.block()) : 0.f;
+    load_row<int8_t, VEC, L>(s.e, codes + at, pl, D, on);
+    s.scale = on && pl.in[0] ? __ldcs(scales + scale_at) : 0.f;
   } else {
     load_row<T, VEC, L>(s.e, static_cast<const T *>(tensor) + at, pl, D, on);
   }
@@ -128,14 +133,14 @@ __device__ __forceinline__ void load_source(Source<T, Q8> &s, const void *tensor
 template <bool VEC, int L>
 __device__ __forceinline__ void load_columns(float2 *to, const float *from, int i, const Place<VEC, L> &pl, int D, int vec) {
   if (VEC && vec) {
-    const float4 q = pl.first + i / 4 * 8 < D ? __ldg(reinterpret_cast<const float4 *>(from + pl.first) + i / 2) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 q = pl.in[i / 4] ? __ldg(reinterpret_cast<const float4 *>(from) + i / 2) : make_float4(0.f, 0.f, 0.f, 0.f);
     to[0] = make_float2(q.x, q.y);
     to[1] = make_float2(q.z, q.w);
   } else {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int d0 = pl.at(2 * (i + u)), d1 = pl.at(2 * (i + u) + 1);
-      to[u] = make_float2(d0 < D ? __ldg(from + d0) : 0.f, d1 < D ? __ldg(from + d1) : 0.f);
+      to[u] = make_float2(d0 < D ? __ldg(from + d0 - pl.first) : 0.f, d1 < D ? __ldg(from + d1 - pl.first) : 0.f);
     }
   }
 }
@@ -207,13 +212,13 @@ __device__ __forceinline__ uint32_t code_word(float2 a, float2 b, float inv) {
                      __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
 }
 template <typename T, bool VEC, int L>
-__device__ __forceinline__ void save_row(const Sixteen<T> &v, uint32_t top, int8_t *codes, float *scales, const Place<VEC, L> &pl, int D) {
+__device__ __forceinline__ void save_row(const Sixteen<T> &v, uint32_t top, int8_t *codes, float *scale, const Place<VEC, L> &pl, int D, bool on) {
   const float inv = block_inverse<T>(top);
   Sixteen<int8_t> e;
 #pragma unroll
   for (int i = 0; i < kPer / 4; ++i) reinterpret_cast<uint32_t *>(e.v)[i] = code_word(v.pair(2 * i), v.pair(2 * i + 1), inv);
-  store_row<int8_t, VEC, L>(codes, e, pl, D);
-  if (pl.leads_block() && pl.first < D) scales[pl.block()] = block_scale(top, inv);
+  store_row<int8_t, VEC, L>(codes, e, pl, D, on);
+  if (on && pl.leads_block() && pl.in[0]) *scale = block_scale(top, inv);
 }
 
 // ---- arithmetic of a row ----
@@ -230,7 +235,7 @@ __device__ __forceinline__ float row_stats(float2 *v, const NormProblem &p, cons
 #pragma unroll
     for (int i = 1; i < P; ++i) s = add2(s, v[i]);
     const float m = group_sum<L>(s.x + s.y, red, turn) * p.inv_d;
-    const bool whole = pl.at(kPer - 1) < D;
+    const bool whole = VEC ? pl.in[1] : pl.at(kPer - 1) < D;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       v[i] = add2(v[i], both(-m));
@@ -245,50 +250,53 @@ __device__ __forceinline__ float row_stats(float2 *v, const NormProblem &p, cons
 
 // The rows of a group: one head, tokens t, t + step, ...
 struct RowWalk {
-  int64_t h, t, step, part;  // part: index among the groups of this head
-  int64_t lead;              // token of the warp's (or CTA's) first group: its threads go on together while that one has rows
-  bool any;                  // the group has a head
+  uint32_t t, step;  // T is below 2^31, so that neither passes 2^32
+  uint32_t lead;     // token of the warp's (or CTA's) first group: its threads go on together while that one has rows
+  int h;
+  bool any;          // the group has a head
   __device__ __forceinline__ RowWalk(const NormProblem &p, int L) {
     const int64_t per_cta = L > 0 ? blockDim.x / L : 1, gid = blockIdx.x * per_cta + (L > 0 ? threadIdx.x / L : 0);
-    h = gid % p.heads;
-    part = t = gid / p.heads;
-    step = p.groups / p.heads;
+    h = (int)(gid % p.heads);
+    t = (uint32_t)(gid / p.heads);  // also the group's index among those of its head
+    step = (uint32_t)(p.groups / p.heads);
     any = h < p.H;
-    lead = L > 0 ? (blockIdx.x * per_cta + (threadIdx.x & ~31u) / L) / p.heads : t;
+    lead = L > 0 ? (uint32_t)((blockIdx.x * per_cta + (threadIdx.x & ~31u) / L) / p.heads) : t;
   }
 };
 
 template <typename T, bool VEC, int L>
-__global__ void __launch_bounds__(kNormThreads<L>, L > 0 ? FWDB : 1) gdp_norm_fwd_kernel(const NormProblem p) {
+__global__ void __launch_bounds__(kNormThreads<L>, L > 0 ? kNormFwdCtas : 1) gdp_norm_fwd_kernel(const NormProblem p) {
   constexpr int P = kPer / 2;
   __shared__ float2 red[2][32];
   int turn = 0;
-  const Place<VEC, L> pl;
   const int D = (int)p.D, blocks = (D + kBlock - 1) / kBlock;
+  const Place<VEC, L> pl(D);
   RowWalk rw(p, L);
-  const float *w = p.w + (p.per_head && rw.any ? rw.h * D : 0), *b = p.b ? p.b + (p.per_head && rw.any ? rw.h * D : 0) : nullptr;
-  const T *o_at = static_cast<const T *>(p.o) + rw.t * p.o_st + rw.h * p.o_sh, *z_at = static_cast<const T *>(p.z) + rw.t * p.z_st + rw.h * p.z_sh;
+  const int64_t col = (p.per_head && rw.any ? (int64_t)rw.h * D : 0) + pl.first;
+  const float *w = p.w + col, *b = p.b ? p.b + col : nullptr;
+  const bool zed = p.z != nullptr, save = p.o_codes != nullptr;
+  int64_t o_at = (int64_t)rw.t * p.o_st + rw.h * p.o_sh + pl.first, z_at = (int64_t)rw.t * p.z_st + rw.h * p.z_sh + pl.first;
   Sixteen<T> next_o, next_z;
   auto load = [&](bool on) {
-    load_row<T, VEC, L>(next_o, o_at, pl, D, on);
-    if (p.z) load_row<T, VEC, L>(next_z, z_at, pl, D, on);
+    load_row<T, VEC, L>(next_o, static_cast<const T *>(p.o) + o_at, pl, D, on);
+    if (zed) load_row<T, VEC, L>(next_z, static_cast<const T *>(p.z) + z_at, pl, D, on);
     o_at += rw.step * p.o_st;
     z_at += rw.step * p.z_st;
   };
   load(rw.any && rw.t < p.T);
-  int64_t row = rw.t * p.H + rw.h;
-  for (; rw.lead < p.T; rw.lead += rw.step, rw.t += rw.step, row += rw.step * p.H) {
+  // offset of the thread's channels, and of their block's scale, in the outputs
+  int64_t at = ((int64_t)rw.t * p.H + rw.h) * D + pl.first, scale_at = ((int64_t)rw.t * p.H + rw.h) * blocks + pl.block();
+  const int64_t step = rw.step * p.H * D, scale_step = rw.step * p.H * blocks;
+  for (; rw.lead < p.T; rw.lead += rw.step, rw.t += rw.step, at += step, scale_at += scale_step) {
     const bool on = rw.any && rw.t < p.T;
     Sixteen<T> e = next_o;
     const Sixteen<T> z = next_z;
     load(rw.any && rw.t + rw.step < p.T);
-    if (p.o_codes) {
-      uint32_t a = top_bits<T>(e), c = p.z ? top_bits<T>(z) : 0u;
+    if (save) {
+      uint32_t a = top_bits<T>(e), c = zed ? top_bits<T>(z) : 0u;
       block_tops<T, L>(a, c);
-      if (on) {
-        save_row<T, VEC, L>(e, a, p.o_codes + row * D, p.o_scales + row * blocks, pl, D);
-        if (p.z) save_row<T, VEC, L>(z, c, p.z_codes + row * D, p.z_scales + row * blocks, pl, D);
-      }
+      save_row<T, VEC, L>(e, a, p.o_codes + at, p.o_scales + scale_at, pl, D, on);
+      if (zed) save_row<T, VEC, L>(z, c, p.z_codes + at, p.z_scales + scale_at, pl, D, on);
     }
     float2 v[P];
 #pragma unroll
@@ -316,7 +324,7 @@ __global__ void __launch_bounds__(kNormThreads<L>, L > 0 ? FWDB : 1) gdp_norm_fw
       }
     };
     using Silu = std::integral_constant<int, GDP_ACT_SILU>;
-    if (p.z) {
+    if (zed) {
       if (p.act == GDP_ACT_SILU) finish(std::true_type{}, Silu{});
       else finish(std::true_type{}, std::integral_constant<int, GDP_ACT_SIGMOID>{});
     } else if (p.act == GDP_ACT_SILU) {
@@ -324,20 +332,21 @@ __global__ void __launch_bounds__(kNormThreads<L>, L > 0 ? FWDB : 1) gdp_norm_fw
     } else {
       finish(std::false_type{}, std::integral_constant<int, GDP_ACT_NONE>{});
     }
-    if (on) store_row<T, VEC, L>(static_cast<T *>(p.y) + row * D, e, pl, D);
+    store_row<T, VEC, L>(static_cast<T *>(p.y) + at, e, pl, D, on);
   }
 }
 
 template <typename T, bool Q8, bool VEC, int L>
-__global__ void __launch_bounds__(kNormThreads<L>, L > 0 ? BWDB : 1) gdp_norm_bwd_kernel(const NormProblem p) {
+__global__ void __launch_bounds__(kNormThreads<L>, L > 0 ? kNormBwdCtas : 1) gdp_norm_bwd_kernel(const NormProblem p) {
   constexpr int P = kPer / 2;
   __shared__ float2 red[2][32];
   int turn = 0;
-  const Place<VEC, L> pl;
   const int D = (int)p.D, blocks = (D + kBlock - 1) / kBlock;
+  const Place<VEC, L> pl(D);
   RowWalk rw(p, L);
   const bool zed = Q8 ? p.z_codes_in != nullptr : p.z != nullptr;
-  const float *w = p.w + (p.per_head && rw.any ? rw.h * D : 0), *b = p.b ? p.b + (p.per_head && rw.any ? rw.h * D : 0) : nullptr;
+  const int64_t col = (p.per_head && rw.any ? (int64_t)rw.h * D : 0) + pl.first;
+  const float *w = p.w + col, *b = p.b ? p.b + col : nullptr;
   // sums over tokens: dweight's in registers, dbias's (fewer calls have one) in shared memory
   __shared__ float4 side[kPer / 4][kNormThreads<L>];
   float2 sw[P];
@@ -347,24 +356,35 @@ __global__ void __launch_bounds__(kNormThreads<L>, L > 0 ? BWDB : 1) gdp_norm_bw
 #pragma unroll
     for (int i = 0; i < kPer / 4; ++i) side[i][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  // offsets of the thread's channels: in the outputs and the codes (and of their block's scale), and of the
+  // next row in the strided tensors
+  int64_t at = ((int64_t)rw.t * p.H + rw.h) * D + pl.first, scale_at = ((int64_t)rw.t * p.H + rw.h) * blocks + pl.block();
+  int64_t y_at = (int64_t)rw.t * p.dy_st + rw.h * p.dy_sh + pl.first;
+  int64_t o_at = (int64_t)rw.t * p.o_st + rw.h * p.o_sh + pl.first, z_at = (int64_t)rw.t * p.z_st + rw.h * p.z_sh + pl.first;
+  const int64_t step = rw.step * p.H * D;
   Source<T, Q8> next_o, next_z;
   Sixteen<T> next_y;
-  auto load = [&](int64_t t, int64_t row) {
-    const bool on = rw.any && t < p.T;
-    load_row<T, VEC, L>(next_y, static_cast<const T *>(p.dy) + t * p.dy_st + rw.h * p.dy_sh, pl, D, on);
-    load_source<T, Q8, VEC, L>(next_o, p.o, t * p.o_st + rw.h * p.o_sh, p.o_codes_in, p.o_scales_in, row, D, blocks, pl, on);
-    if (zed) load_source<T, Q8, VEC, L>(next_z, p.z, t * p.z_st + rw.h * p.z_sh, p.z_codes_in, p.z_scales_in, row, D, blocks, pl, on);
+  auto load = [&](int64_t codes_at, bool on) {
+    load_row<T, VEC, L>(next_y, static_cast<const T *>(p.dy) + y_at, pl, D, on);
+    load_source<T, Q8, VEC, L>(next_o, p.o, p.o_codes_in, p.o_scales_in, Q8 ? codes_at : o_at, scale_at, pl, D, on);
+    if (zed) load_source<T, Q8, VEC, L>(next_z, p.z, p.z_codes_in, p.z_scales_in, Q8 ? codes_at : z_at, scale_at, pl, D, on);
+    y_at += rw.step * p.dy_st;
+    if constexpr (Q8) {
+      scale_at += rw.step * p.H * blocks;
+    } else {
+      o_at += rw.step * p.o_st;
+      z_at += rw.step * p.z_st;
+    }
   };
-  int64_t row = rw.t * p.H + rw.h;
-  load(rw.t, row);
-  for (; rw.lead < p.T; rw.lead += rw.step, rw.t += rw.step, row += rw.step * p.H) {
+  load(at, rw.any && rw.t < p.T);
+  for (; rw.lead < p.T; rw.lead += rw.step, rw.t += rw.step, at += step) {
     const bool on = rw.any && rw.t < p.T;
     const Source<T, Q8> z = next_z;
     Sixteen<T> e = next_y;  // dy, then dz in its place
     float2 n[P], dn[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) n[i] = next_o.pair(i);
-    load(rw.t + rw.step, row + rw.step * p.H);
+    load(at + step, rw.any && rw.t + rw.step < p.T);
     float r = row_stats<VEC, L>(n, p, pl, D, red, turn);
     if (!on) r = 0.f;  // a group without a row adds zeros to its sums
     float2 s1 = both(0.f), s2 = both(0.f);
@@ -408,7 +428,7 @@ __global__ void __launch_bounds__(kNormThreads<L>, L > 0 ? BWDB : 1) gdp_norm_bw
     if (zed) {
       if (p.act == GDP_ACT_SILU) gate(std::true_type{}, Silu{});
       else gate(std::true_type{}, std::integral_constant<int, GDP_ACT_SIGMOID>{});
-      if (on) store_row<T, VEC, L>(static_cast<T *>(p.d_z) + row * D, e, pl, D);
+      store_row<T, VEC, L>(static_cast<T *>(p.d_z) + at, e, pl, D, on);
     } else if (p.act == GDP_ACT_SILU) {
       gate(std::false_type{}, Silu{});
     } else {
@@ -416,12 +436,11 @@ __global__ void __launch_bounds__(kNormThreads<L>, L > 0 ? BWDB : 1) gdp_norm_bw
     }
     const float2 t = group_sum<L>(make_float2(s1.x + s1.y, s2.x + s2.y), red, turn);
     const float m1 = p.center ? t.x * p.inv_d : 0.f, m2 = t.y * p.inv_d;
-    if (on) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) e.set(i, mul2(fma2(n[i], both(-m2), add2(dn[i], both(-m1))), both(r)));
-      store_row<T, VEC, L>(static_cast<T *>(p.d_o) + row * D, e, pl, D);
-    }
+    for (int i = 0; i < P; ++i) e.set(i, mul2(fma2(n[i], both(-m2), add2(dn[i], both(-m1))), both(r)));
+    store_row<T, VEC, L>(static_cast<T *>(p.d_o) + at, e, pl, D, on);
   }
+  sm100::pdl_trigger();  // the kernel that adds them up may get ready
   // column sums: [part][columns], all dweight parts before all dbias parts
   const int64_t ncols = p.per_head ? p.H * p.D : p.D;
   for (int which = 0; which < (b ? 2 : 1); ++which) {
@@ -435,7 +454,8 @@ __global__ void __launch_bounds__(kNormThreads<L>, L > 0 ? BWDB : 1) gdp_norm_bw
     }
     float *to = p.partial + which * p.parts * ncols;
     if (L == 0 || p.per_head) {
-      to += (p.per_head ? rw.part : (int64_t)blockIdx.x) * ncols + (p.per_head ? rw.h * p.D : 0);
+      const int64_t gid = (int64_t)blockIdx.x * (L > 0 ? blockDim.x / (L > 0 ? L : 1) : 1) + (L > 0 ? threadIdx.x / (L > 0 ? L : 1) : 0);
+      to += (p.per_head ? gid / p.heads : (int64_t)blockIdx.x) * ncols + (p.per_head ? rw.h * p.D : 0);
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
         if (rw.any && pl.at(j) < D) to[pl.at(j)] = j & 1 ? sw[j >> 1].y : sw[j >> 1].x;
