@@ -17,6 +17,10 @@ namespace {
 constexpr int kPer = 16;  // channels of a thread: 8 cost 42 instructions per channel in the reductions and
                           // addresses alone (966 us for the training step of 65536 x 32 x 128)
 
+// Wide rows' forward CTAs have at most 512 threads; the larger bound holds the compiler to 80 registers, so
+// that three of 256 threads share an SM (1421 x 4096: 13.1 us, with 114 registers 14.9 us).
+constexpr int kWideFwdBound = 768;
+
 // Where a thread's channels lie in its row.  VEC: sixteen consecutive ones; else strided by the width of
 // a run of lanes, so that the lanes' accesses are runs of memory.  Either way a checkpoint block of 128
 // channels lies in eight lanes (a shorter row in its four).
@@ -157,13 +161,21 @@ __device__ __forceinline__ V group_sum(V v, float2 (*red)[32], int &turn) {
 #pragma unroll
   for (int s = kLanes / 2; s > 0; s >>= 1) v = plus(v, from_lane(v, s));
   if constexpr (L == 0) {
-    V *buf = reinterpret_cast<V *>(red[turn & 1]);
+    // up to 16 warps' values: single sums in the first 64 bytes, pairs in the 128 after them
+    V *buf = reinterpret_cast<V *>(red[turn & 1] + (sizeof(V) == 4 ? 0 : 8));
     ++turn;
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = buf[0];
+    // the warps' sums, 16 bytes at a time (the buffers' unused ends are zero)
     const int warps = (int)blockDim.x >> 5;
-    for (int w = 1; w < warps; ++w) v = plus(v, buf[w]);
+    constexpr int kEach = 16 / (int)sizeof(V);
+    float4 sum = *reinterpret_cast<const float4 *>(buf);
+    for (int i = kEach; i < warps; i += kEach) {
+      const float4 q = *reinterpret_cast<const float4 *>(buf + i);
+      sum = make_float4(sum.x + q.x, sum.y + q.y, sum.z + q.z, sum.w + q.w);
+    }
+    if constexpr (sizeof(V) == 4) v = (sum.x + sum.y) + (sum.z + sum.w);
+    else v = make_float2(sum.x + sum.z, sum.y + sum.w);
   }
   return v;
 }
@@ -265,10 +277,14 @@ struct RowWalk {
 };
 
 template <typename T, bool VEC, int L>
-__global__ void __launch_bounds__(kNormThreads<L>, L > 0 ? kNormFwdCtas : 1) gdp_norm_fwd_kernel(const NormProblem p) {
+__global__ void __launch_bounds__(L > 0 ? kNormThreads<L> : kWideFwdBound, L > 0 ? kNormFwdCtas : 1) gdp_norm_fwd_kernel(const NormProblem p) {
   constexpr int P = kPer / 2;
-  __shared__ float2 red[2][32];
+  __shared__ __align__(16) float2 red[2][32];
   int turn = 0;
+  if (L == 0) {
+    if (threadIdx.x < 64) red[threadIdx.x >> 5][threadIdx.x & 31] = both(0.f);
+    __syncthreads();
+  }
   const int D = (int)p.D, blocks = (D + kBlock - 1) / kBlock;
   const Place<VEC, L> pl(D);
   RowWalk rw(p, L);
@@ -339,8 +355,12 @@ __global__ void __launch_bounds__(kNormThreads<L>, L > 0 ? kNormFwdCtas : 1) gdp
 template <typename T, bool Q8, bool VEC, int L>
 __global__ void __launch_bounds__(kNormThreads<L>, L > 0 ? kNormBwdCtas : 1) gdp_norm_bwd_kernel(const NormProblem p) {
   constexpr int P = kPer / 2;
-  __shared__ float2 red[2][32];
+  __shared__ __align__(16) float2 red[2][32];
   int turn = 0;
+  if (L == 0) {
+    if (threadIdx.x < 64) red[threadIdx.x >> 5][threadIdx.x & 31] = both(0.f);
+    __syncthreads();
+  }
   const int D = (int)p.D, blocks = (D + kBlock - 1) / kBlock;
   const Place<VEC, L> pl(D);
   RowWalk rw(p, L);
