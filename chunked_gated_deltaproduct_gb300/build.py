@@ -34,6 +34,15 @@ def nvcc() -> str:
     return cand
 
 
+# Sources without range checks: their objects are the same in both variants, so that the debug-bounds
+# build links those of the normal one.
+UNCHECKED = ("gdp_rec", "gdp_norm_", "gdp_group_norm")
+
+
+def _shared(src: str) -> bool:
+    return os.path.basename(src).startswith(UNCHECKED)
+
+
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
@@ -61,7 +70,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug_boun
     srcs = _sources()
 
     def compile_one(src):
-        obj = os.path.join(folder, os.path.basename(src)[:-3] + ".o")
+        name = os.path.basename(src)[:-3] + ".o"
+        if debug_bounds and _shared(src):
+            obj = os.path.join(BUILD, name)
+            if os.path.exists(obj) and all(os.path.getmtime(d) <= os.path.getmtime(obj) for d in _deps()):
+                return obj
+        obj = os.path.join(folder, name)
         cmd = [cc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
@@ -70,7 +84,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug_boun
             print(r.stdout, r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(os.cpu_count() or 8, 16, len(srcs))) as ex:
         objs = list(ex.map(compile_one, srcs))
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]

@@ -84,12 +84,13 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
     const int64_t first = load_cu(s.cu, s.cu64, 0), end = min(load_cu(s.cu, s.cu64, s.N), s.T);
     SeqWindow win;
     win.load(s, max((int64_t)0, s.N - 32), lane);
-    for (int n = 0; n < steps; ++n) {
+    int n = 0;
+    for (; n < steps; ++n) {
       const int st = n % L::kStages, r = s.rows - 1 - (n * s.cluster + rank);
       const int64_t t0 = (int64_t)r * L::kTile;  // before row 0 in the last step of some CTAs: an empty tile
       TileMeta<S> &m = metas[n % L::kMeta];
       unsigned char *base = smem + st * L::stage;
-      if (n >= L::kStages) ring_wait(&empty[st], (n / L::kStages + 1) & 1, gave_up, s.status, s.limit_ns);
+      if (n >= L::kStages && !ring_wait(&empty[st], (n / L::kStages + 1) & 1, gave_up, s.status, s.limit_ns)) break;
       if (RAW) {
         load_words<TG>(base + L::g_off, p.g, t0, L::kTile, s.T, c0, s.C, lane);
         load_words<TX>(base + L::d_off, p.dout, t0, L::kTile, s.T, c0, s.C, lane);
@@ -120,6 +121,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
       if (RAW || Q8) cp_async_arrive(&full[st]);
       if (lane == 0) sm100::mbar_arrive(&full[st]);
     }
+    if (*gave_up) drain_loads<L::kStages>(full, n, RAW || Q8);
     if (blockIdx.x == 0) check_sequences(s.cu, s.cu64, s.N, s.T, s.status, lane, 32);
   } else if (warp == kChainWarp) {
     chain_steps<S, L::kMeta, true>(s, ch, metas, steps, lane, gave_up);
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
       const int st = n % L::kStages;
       const unsigned char *base = smem + st * L::stage;
       const int64_t t0 = ((int64_t)s.rows - 1 - ((int64_t)n * s.cluster + rank)) * L::kTile + block * S;
-      ring_wait(&full[st], (n / L::kStages) & 1, gave_up, s.status, s.limit_ns);
+      if (!ring_wait(&full[st], (n / L::kStages) & 1, gave_up, s.status, s.limit_ns)) break;
       const TileMeta<S> &m = metas[n % L::kMeta];
       const uint32_t starts = m.starts[block], ends = m.ends[block];
       const int lo = m.lo - block * S, hi = m.hi - block * S;
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
           sm100::mbar_arrive(&empty[(n - 1) % L::kStages]);
         }
       }
-      ring_wait(ch.enter_full, n & 1, gave_up, s.status, s.limit_ns);
+      if (!ring_wait(ch.enter_full, n & 1, gave_up, s.status, s.limit_ns)) break;
       keep_only<S>(kept);
       float2 E = ch.enter[warp * 32 + lane];
       // the state before token i
@@ -262,8 +264,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
     }
     if (lane == 0) sm100::bulk_wait_all();
   }
-  __syncwarp();
-  cluster_sync();  // no CTA leaves while another may still post to it
+  leave_cluster(gave_up);
 }
 
 template <typename TX, typename TG, int GATE, bool Q8, bool RAW>

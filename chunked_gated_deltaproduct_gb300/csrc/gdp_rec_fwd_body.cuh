@@ -71,12 +71,13 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
     const int64_t first = load_cu(s.cu, s.cu64, 0), end = min(load_cu(s.cu, s.cu64, s.N), s.T);
     SeqWindow win;
     win.load(s, 0, lane);
-    for (int n = 0; n < steps; ++n) {
+    int n = 0;
+    for (; n < steps; ++n) {
       const int st = n % L::kStages, r = n * s.cluster + rank;
       const int64_t t0 = (int64_t)r * L::kTile;
       TileMeta<S> &m = metas[n % L::kMeta];
       unsigned char *base = smem + st * L::stage;
-      if (n >= L::kStages) ring_wait(&empty[st], (n / L::kStages + 1) & 1, gave_up, s.status, s.limit_ns);
+      if (n >= L::kStages && !ring_wait(&empty[st], (n / L::kStages + 1) & 1, gave_up, s.status, s.limit_ns)) break;
       if (RAW) {
         load_words<TX>(base + L::x_off, p.x, t0, L::kTile, s.T, c0, s.C, lane);
         load_words<TG>(base + L::g_off, p.g, t0, L::kTile, s.T, c0, s.C, lane);
@@ -94,6 +95,7 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
       if (RAW) cp_async_arrive(&full[st]);
       if (lane == 0) sm100::mbar_arrive(&full[st]);
     }
+    if (*gave_up) drain_loads<L::kStages>(full, n, RAW);
     if (blockIdx.x == 0) check_sequences(s.cu, s.cu64, s.N, s.T, s.status, lane, 32);
   } else if (warp == kChainWarp) {
     chain_steps<S, L::kMeta, false>(s, ch, metas, steps, lane, gave_up);
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
       const int st = n % L::kStages;
       const unsigned char *xs = smem + st * L::stage + L::x_off, *gs = smem + st * L::stage + L::g_off;
       const int64_t t0 = ((int64_t)n * s.cluster + rank) * L::kTile + warp * S;
-      ring_wait(&full[st], (n / L::kStages) & 1, gave_up, s.status, s.limit_ns);
+      if (!ring_wait(&full[st], (n / L::kStages) & 1, gave_up, s.status, s.limit_ns)) break;
       const TileMeta<S> &m = metas[n % L::kMeta];
       const uint32_t starts = m.starts[warp], ends = m.ends[warp];
       const int lo = m.lo - warp * S, hi = m.hi - warp * S;
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
         sm100::bulk_wait_read<0>();  // the last tile's store has read `mine`
       }
       __syncwarp();
-      ring_wait(ch.enter_full, n & 1, gave_up, s.status, s.limit_ns);
+      if (!ring_wait(ch.enter_full, n & 1, gave_up, s.status, s.limit_ns)) break;
       keep_only<S>(a);
       // ---- from the entering state.  Four tokens' inputs are read before their outputs are written (the
       // compiler keeps the order of accesses to shared memory).
@@ -198,8 +200,7 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
     }
     if (lane == 0) sm100::bulk_wait_all();
   }
-  __syncwarp();
-  cluster_sync();  // no CTA leaves while another may still post to it
+  leave_cluster(gave_up);
 }
 
 template <typename TX, typename TG, int GATE, bool RAW>

@@ -326,14 +326,33 @@ __device__ __forceinline__ void post16(uint32_t addr, float4 v, uint32_t bar) {
 // (arithmetic never gives this NaN: its own has the sign bit clear).
 constexpr uint32_t kCut = 0xffffffffu;
 
-// A wait on a full or empty barrier: bounded; once one ran out in the CTA the others return at once
-// and the kernel runs to its end with undefined outputs (every copy it issued is still waited for).
-__device__ __forceinline__ void ring_wait(uint64_t *bar, uint32_t parity, volatile int *gave_up, uint32_t *status, uint64_t limit_ns) {
+// A whole warp's wait on one of the CTA's barriers: bounded, one answer for all lanes.  False once this wait, or any other of the CTA, ran out: the
+// calling role then stops (its outputs are undefined from there on); the other CTAs of the cluster stop
+// likewise, for want of this one's mail.
+__device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, volatile int *gave_up, uint32_t *status, uint64_t limit_ns) {
   // sleeping tries first: the bounded wait begins with a read of the global timer, which takes longer
   // than most waits here (8 x 4096 x 2048 backward: 235 us with it alone, 150 us so)
   for (int i = 0; i < 64; ++i)
-    if (sm100::mbar_try_sleep(bar, parity, 1000u)) return;
-  if (!sm100::mbar_wait_or_abort(bar, parity, gave_up, limit_ns)) set_status(status, GDP_DEV_ERR_TIMEOUT);
+    if (__all_sync(0xffffffffu, sm100::mbar_try_sleep(bar, parity, 1000u))) return true;
+  if (__all_sync(0xffffffffu, sm100::mbar_wait_or_abort(bar, parity, gave_up, limit_ns))) return true;
+  set_status(status, GDP_DEV_ERR_TIMEOUT);
+  return false;
+}
+// The loading warp, stopped before step n after a failed wait: its copies in flight (stages whose last use began before n).
+template <int STAGES>
+__device__ __forceinline__ void drain_loads(uint64_t *full, int n, bool words) {
+  if (words) sm100::cp_async_wait_all();
+  for (int i = n > STAGES ? n - STAGES : 0; i < n; ++i) (void)sm100::mbar_wait(&full[i % STAGES], (i / STAGES) & 1);
+}
+// Leaves the cluster: no CTA exits while another may still post to it.  After a failed wait posts may be
+// under way that nobody waited for: they take microseconds at most.
+__device__ __forceinline__ void leave_cluster(volatile int *gave_up) {
+  __syncwarp();
+  cluster_sync();
+  if (*gave_up) {
+    const uint64_t t0 = sm100::globaltimer_ns();
+    while (sm100::globaltimer_ns() - t0 < 100000ull) __nanosleep(1000);
+  }
 }
 
 // The chaining warp.  Mail slots: a CTA posts step n + 2 only after it has read the mail of step n + 1,
@@ -348,7 +367,7 @@ __device__ __forceinline__ void chain_steps(const ScanShape &p, const Chain &ch,
     for (int i = 0; i < kMailSlots; ++i) sm100::mbar_arrive_expect_tx(&ch.mail_full[i], bytes);
   float2 h = make_float2(0.f, 0.f);  // the state entering the step
   for (int n = 0; n < steps; ++n) {
-    ring_wait(ch.parts_full, n & 1, gave_up, p.status, p.limit_ns);
+    if (!ring_wait(ch.parts_full, n & 1, gave_up, p.status, p.limit_ns)) return;
     const TileMeta<S> &m = metas[n % META];
     uint32_t fresh = 0;  // bit w: a sequence begins (REV: ends) among warp w's tokens
     float4 q[kScanWarps];
@@ -371,7 +390,7 @@ __device__ __forceinline__ void chain_steps(const ScanShape &p, const Chain &ch,
 #pragma unroll 4
       for (int k = 0; k < p.cluster; ++k) post16(in_rank(to, k), own, in_rank(bar, k));
     }
-    ring_wait(&ch.mail_full[slot], (n / kMailSlots) & 1, gave_up, p.status, p.limit_ns);
+    if (!ring_wait(&ch.mail_full[slot], (n / kMailSlots) & 1, gave_up, p.status, p.limit_ns)) return;
     const float4 *mail = ch.mail + slot * p.cluster * 32;
     float2 e = h;
     for (int k0 = 0; k0 < p.cluster; k0 += 4) {

@@ -124,6 +124,15 @@ gdp_status resolve(const gdp_recurrence_args *a, bool step, RecProblem *p) {
   return GDP_OK;
 }
 
+// Set by gdp_arm_recurrence_wait_test for the calling thread's next scan.
+thread_local uint64_t armed_limit_ns = 0;
+
+void set_limits(ScanShape &s) {
+  s.limit_ns = armed_limit_ns ? armed_limit_ns : sm100::kWaitLimitNs;
+  s.withhold = armed_limit_ns != 0;
+  armed_limit_ns = 0;
+}
+
 cudaError_t run(RecFwd &p, int gate, cudaStream_t stream, bool bf16, bool wide) {
   if (bf16) return wide ? launch_rec_fwd<__nv_bfloat16, float>(p, gate, stream) : launch_rec_fwd<__nv_bfloat16, __nv_bfloat16>(p, gate, stream);
   return wide ? launch_rec_fwd<__half, float>(p, gate, stream) : launch_rec_fwd<__half, __half>(p, gate, stream);
@@ -165,7 +174,7 @@ GDP_EXPORT gdp_status gdp_linear_recurrence(const gdp_recurrence_args *args, voi
   RecFwd f{};
   f.s.cu = p.cu; f.s.cu64 = p.cu64; f.s.T = p.T; f.s.N = p.N; f.s.C = p.C;
   f.s.slots = p.cache ? p.slots : nullptr; f.s.num_slots = p.num_slots; f.s.status = p.status;
-  f.s.limit_ns = gdp::sm100::kWaitLimitNs;
+  set_limits(f.s);
   f.x = {p.x, p.x_st}; f.g = {p.g, p.g_st}; f.h = p.h;
   f.from = p.cache ? p.cache : p.init;
   f.to = p.cache ? p.cache : p.fin;
@@ -209,7 +218,7 @@ GDP_EXPORT gdp_status gdp_linear_recurrence_backward(const gdp_recurrence_backwa
   RecBwd p{};
   p.s.cu = a->cu_seqlens; p.s.cu64 = a->cu_seqlens_int64 != 0; p.s.T = a->T; p.s.N = a->N; p.s.C = a->C;
   p.s.status = a->device_status;
-  p.s.limit_ns = gdp::sm100::kWaitLimitNs;
+  set_limits(p.s);
   p.g = {a->g, a->g_stride_t}; p.x = {a->x, a->x_stride_t}; p.h = {a->h, a->h_stride_t}; p.dout = {a->d_output, a->d_output_stride_t};
   p.codes = {a->h_codes, a->C};
   p.scales = a->h_scales;
@@ -220,6 +229,14 @@ GDP_EXPORT gdp_status gdp_linear_recurrence_backward(const gdp_recurrence_backwa
   p.pair_dx = a->C % 2 == 0 && aligned(a->dx, 2 * dtype_size(a->x_dtype));
   p.pair_dg = a->C % 2 == 0 && aligned(a->dg, 2 * dtype_size(a->g_dtype));
   return dispatch(a->x_dtype, a->g_dtype, p, a->gate, (cudaStream_t)stream);
+}
+
+GDP_EXPORT gdp_status gdp_arm_recurrence_wait_test(uint64_t limit_ns) {
+  using namespace gdp::layer;
+  gdp::set_last_error("");
+  if (limit_ns < 100000ull || limit_ns > 1000000000ull) return fail(GDP_ERR_INVALID_ARG, "limit_ns must be between 1e5 and 1e9");
+  armed_limit_ns = limit_ns;
+  return GDP_OK;
 }
 
 GDP_EXPORT size_t gdp_layer_args_size(int which) {

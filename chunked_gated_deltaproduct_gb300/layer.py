@@ -109,6 +109,8 @@ def _library():
             fn.restype, fn.argtypes = _int, [_vp, _vp]
         lib.gdp_group_norm_workspace_bytes.restype = _sz
         lib.gdp_group_norm_workspace_bytes.argtypes = [_i64, _i64, _i64, _int]
+        lib.gdp_arm_recurrence_wait_test.restype = _int
+        lib.gdp_arm_recurrence_wait_test.argtypes = [ctypes.c_uint64]
         lib.gdp_layer_args_size.restype = _sz
         lib.gdp_layer_args_size.argtypes = [_int]
         for i, args in enumerate((GdpRecurrenceArgs, GdpRecurrenceBackwardArgs, GdpGroupNormArgs,
@@ -121,6 +123,13 @@ def _library():
 
 def gdp_group_norm_workspace_bytes(T: int, H: int, D: int, per_head: bool = False) -> int:
     return int(_library().gdp_group_norm_workspace_bytes(T, H, D, int(per_head)))
+
+
+def gdp_arm_recurrence_wait_test(limit_ns: int) -> None:
+    """Arm the calling thread's next packed recurrence (or its backward pass) to exercise the bounded-wait
+    failure path; see the header."""
+    lib = _library()
+    _finish(lib.gdp_arm_recurrence_wait_test(int(limit_ns)), lib)
 
 
 # ---- checks.  A one-token step costs a few microseconds of host time, so each tensor's are one

@@ -116,6 +116,15 @@ typedef struct gdp_recurrence_backward_args {
 
 gdp_status gdp_linear_recurrence_backward(const gdp_recurrence_backward_args *args, void *stream);
 
+/*
+ * gdp_arm_recurrence_wait_test: a test of the failure path, as gdp_arm_wait_expiry_test is for the
+ * prefill.  The waits of the calling thread's next gdp_linear_recurrence or _backward call give up after
+ * limit_ns (1e5 .. 1e9 ns), and the first tile's contribution to the chain is withheld, so that one of
+ * them runs out: GDP_DEV_ERR_TIMEOUT in *device_status, outputs undefined, later calls unaffected.
+ * GDP_ERR_INVALID_ARG for a limit outside the range.
+ */
+gdp_status gdp_arm_recurrence_wait_test(uint64_t limit_ns);
+
 /* What the normed value is multiplied with (z given) or passed through (z NULL). */
 typedef enum gdp_activation {
   GDP_ACT_NONE = 0,    /* y = u */

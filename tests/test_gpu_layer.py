@@ -343,6 +343,27 @@ def test_recurrence_past_32_bit_offsets(cuda_device):
     assert torch.equal(d["dg"][1], (x[1].float() * x[0].float()).to(BF16))
 
 
+@pytest.mark.parametrize("backward", [False, True])
+def test_expired_wait_is_reported(cuda_device, backward):
+    """A wait that runs out sets the status bit and ends the call; the next call is unaffected."""
+    dev, T, C = cuda_device, 5000, 192
+    x, g = _rand((T, C), 1, BF16).to(dev), _gates("log", (T, C), 2, BF16).to(dev)
+    cu, st = _cu([T], dev), torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def call():
+        if backward:
+            return pkg.gated_linear_recurrence_backward(g, x, x, cu, device_status=st)["dx"]
+        return pkg.gated_linear_recurrence(x, g, cu, device_status=st)
+
+    want = call().clone()
+    pkg.gdp_arm_recurrence_wait_test(1_000_000)
+    call()
+    torch.cuda.synchronize()
+    assert int(st) == pkg.GDP_DEV_ERR_TIMEOUT
+    st.zero_()
+    assert torch.equal(call(), want) and int(st) == 0
+
+
 def test_on_another_stream_and_in_a_graph(cuda_device):
     dev = cuda_device
     lengths, C = [3000, 2000], 128

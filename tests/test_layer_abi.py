@@ -27,6 +27,11 @@ def test_layouts_and_queries(lib):
     assert nw(100, 4, 128) > 0 and nw(100, 4, 0) == 0 and nw(100, 4, 8193) == 0
 
 
+@pytest.mark.parametrize("limit", [0, 99_999, 1_000_000_001])
+def test_wait_test_limits(lib, limit):
+    assert lib.gdp_arm_recurrence_wait_test(limit) == pkg.GDP_ERR_INVALID_ARG and pkg.gdp_last_error() != ""
+
+
 def _rec(**over):
     T, C = 8, 16
     a = pkg.GdpRecurrenceArgs(x=FAKE, x_stride_t=C, g=FAKE, g_stride_t=C, output=FAKE, cu_seqlens=FAKE, T=T, N=2, C=C,
