@@ -35,7 +35,7 @@ struct BwdLayout {
   // TMA destinations, 16-byte arrays, barriers, and the largest cluster's whole
   static_assert(g_off % 128 == 0 && d_off % 128 == 0 && h_off % 128 == 0 && x_off % 128 == 0 && s_off % 4 == 0 && S * kSlice * sizeof(TX) % 128 == 0 && S * kSlice * sizeof(TG) % 128 == 0 && stage % 128 == 0, "TMA reads and writes at 128-byte boundaries");
   static_assert(parts % 16 == 0 && enter % 16 == 0 && meta % 4 == 0 && bars % 8 == 0 && mail % 16 == 0, "alignment");
-  static_assert(mail + Chain::mail_bytes(16) <= kScanSmem, "two CTAs per SM");
+  static_assert(mail + Chain::mail_bytes(RAW ? 8 : 16) <= kScanSmem && mail + Chain::mail_bytes(16) <= 227 * 1024, "two CTAs per SM");
 };
 
 struct BwdMaps {
@@ -92,11 +92,13 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
       unsigned char *base = smem + st * L::stage;
       if (n >= L::kStages && !ring_wait(&empty[st], (n / L::kStages + 1) & 1, gave_up, s.status, s.limit_ns)) break;
       if (RAW) {
-        load_words<TG>(base + L::g_off, p.g, t0, L::kTile, s.T, c0, s.C, lane);
-        load_words<TX>(base + L::d_off, p.dout, t0, L::kTile, s.T, c0, s.C, lane);
-        if (Q8) load_words<int8_t>(base + L::h_off, p.codes, t0 - 1, L::kTile, s.T, c0, s.C, lane);
-        else load_words<TX>(base + L::h_off, p.h, t0 - 1, L::kTile, s.T, c0, s.C, lane);
-        if (L::kX) load_words<TX>(base + L::x_off, p.x, t0, L::kTile, s.T, c0, s.C, lane);
+        uint32_t bytes = load_rows<TG>(base + L::g_off, p.g, t0, L::kTile, s.T, c0, s.C, lane, &full[st]) +
+                         load_rows<TX>(base + L::d_off, p.dout, t0, L::kTile, s.T, c0, s.C, lane, &full[st]);
+        if (Q8) bytes += load_rows<int8_t>(base + L::h_off, p.codes, t0 - 1, L::kTile, s.T, c0, s.C, lane, &full[st]);
+        else bytes += load_rows<TX>(base + L::h_off, p.h, t0 - 1, L::kTile, s.T, c0, s.C, lane, &full[st]);
+        if (L::kX) bytes += load_rows<TX>(base + L::x_off, p.x, t0, L::kTile, s.T, c0, s.C, lane, &full[st]);
+        const uint32_t total = warp_total(bytes);
+        if (lane == 0 && total) mbar_expect_tx(&full[st], total);
       } else if (lane == 0) {
         mbar_expect_tx(&full[st], L::kTile * kSlice * (sizeof(TG) + (L::kX ? 2 : 1) * sizeof(TX) + (Q8 ? 1 : sizeof(TX))));
         sm100::tma_load_2d(base + L::g_off, &maps.g, (int)c0, (int)t0, &full[st]);

@@ -29,7 +29,7 @@ struct FwdLayout {
   // TMA destinations, 16-byte arrays, barriers, and the largest cluster's whole
   static_assert(x_off % 128 == 0 && g_off % 128 == 0 && out % 128 == 0 && S * kSlice * sizeof(TX) % 128 == 0 && stage % 128 == 0, "TMA writes to 128-byte boundaries");
   static_assert(parts % 16 == 0 && enter % 16 == 0 && meta % 4 == 0 && bars % 8 == 0 && mail % 16 == 0, "alignment");
-  static_assert(mail + Chain::mail_bytes(16) <= kScanSmem, "two CTAs per SM");
+  static_assert(mail + Chain::mail_bytes(RAW ? 8 : 16) <= kScanSmem && mail + Chain::mail_bytes(16) <= 227 * 1024, "two CTAs per SM");
 };
 
 template <typename TX, typename TG, int GATE, bool RAW>
@@ -79,8 +79,10 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
       unsigned char *base = smem + st * L::stage;
       if (n >= L::kStages && !ring_wait(&empty[st], (n / L::kStages + 1) & 1, gave_up, s.status, s.limit_ns)) break;
       if (RAW) {
-        load_words<TX>(base + L::x_off, p.x, t0, L::kTile, s.T, c0, s.C, lane);
-        load_words<TG>(base + L::g_off, p.g, t0, L::kTile, s.T, c0, s.C, lane);
+        const uint32_t bytes = load_rows<TX>(base + L::x_off, p.x, t0, L::kTile, s.T, c0, s.C, lane, &full[st]) +
+                               load_rows<TG>(base + L::g_off, p.g, t0, L::kTile, s.T, c0, s.C, lane, &full[st]);
+        const uint32_t total = warp_total(bytes);
+        if (lane == 0 && total) mbar_expect_tx(&full[st], total);
       } else if (lane == 0) {
         mbar_expect_tx(&full[st], L::kTile * kSlice * (sizeof(TX) + sizeof(TG)));
         sm100::tma_load_2d(base + L::x_off, &map_x, (int)c0, (int)t0, &full[st]);

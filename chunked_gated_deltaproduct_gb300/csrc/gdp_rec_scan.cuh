@@ -5,8 +5,8 @@
 // of 8 S tokens x 64 channels whatever the sequences' lengths (a sequence's first token simply
 // replaces the state).  A cluster of CTAs owns 64 channels for all of time: in step n its CTA k works
 // on tile n * cluster + k.  In a CTA,
-//   - a loading warp brings tiles ahead into a ring of shared-memory stages (TMA, or word-wise
-//     asynchronous copies for rows that are not 16-byte aligned) and finds the sequences in them;
+//   - a loading warp brings tiles ahead into a ring of shared-memory stages (TMA boxes, or a bulk copy per
+//     row where rows are not 16-byte aligned) and finds the sequences in them;
 //   - eight warps of S tokens each run the tile from zero, which gives each warp's (A, B), keep their
 //     decays and inputs in registers, and run it again from their entering states for the outputs;
 //   - a chaining warp folds the eight (A, B) in between, writes the tile's (A, B) into every CTA of the
@@ -38,7 +38,6 @@ struct ScanShape {
   int cu64;
   int64_t T, N, C;
   int rows, slices;  // tiles in time and in channels
-  int raw;           // word-wise copies instead of TMA
   const int32_t *slots;
   int64_t num_slots;
   uint32_t *status;
@@ -56,7 +55,7 @@ struct TileMeta {
 };
 
 template <typename T>
-constexpr int tile_pitch(bool raw) { return kSlice * (int)sizeof(T) + (raw && sizeof(T) < 4 ? 4 : 0); }
+constexpr int tile_pitch(bool raw) { return kSlice * (int)sizeof(T) + (raw ? 16 : 0); }
 // One input tensor [T][C]: its address for the word-wise copies.
 struct RowSource {
   const void *base;
@@ -80,29 +79,44 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(sm100::smem_u32(bar)), "r"(bytes) : "memory");
 }
 
-// Rows [t0, t0 + rows) x channels [c0, c0 + 64) of src by 4-byte copies: the words that hold a wanted
-// byte.  A row that does not start on a word keeps its offset within the word (raw_offset); bytes past
-// the row's last channel are not read.  Rows outside [0, T) become zeros.
+// Whole warp: rows [t0, t0 + rows) x channels [c0, c0 + 64) of a tensor whose rows start anywhere, one bulk
+// copy per row of the 16-byte words that hold it; a row keeps its offset within its first word (raw_offset).
+// The words' other bytes belong to neighbouring rows; where they could lie outside the tensor (before its
+// first row, after its last) the row comes by 4-byte copies that stop at its end.  Rows outside [0, T)
+// become zeros.  Returns the bulk copies' bytes (of this lane's rows).
 template <typename T>
-__device__ __forceinline__ void load_words(unsigned char *tile, const RowSource &src, int64_t t0, int rows, int64_t T_, int64_t c0,
-                                           int64_t C, int lane) {
-  constexpr int kWords = tile_pitch<T>(true) / 4;
+__device__ __forceinline__ uint32_t load_rows(unsigned char *tile, const RowSource &src, int64_t t0, int rows, int64_t T_, int64_t c0,
+                                              int64_t C, int lane, uint64_t *bar) {
   const int wanted = (int)min((int64_t)kSlice, C - c0) * (int)sizeof(T);
-  for (int i = lane; i < rows * kWords; i += 32) {
-    const int r = i / kWords, w = i % kWords;
+  const uintptr_t base = reinterpret_cast<uintptr_t>(src.base);
+  const uintptr_t end = base + (uintptr_t)(((T_ - 1) * src.stride + C) * (int64_t)sizeof(T));
+  uint32_t bytes = 0;
+  for (int r = lane; r < rows; r += 32) {
     const int64_t t = t0 + r;
-    const bool in = t >= 0 && t < T_;
-    const uintptr_t at = reinterpret_cast<uintptr_t>(src.base) + (uintptr_t)(((in ? t : 0) * src.stride + c0) * (int64_t)sizeof(T));
-    const int off = (int)(at & 3u), left = in ? off + wanted - 4 * w : 0;
-    const uintptr_t word = (at & ~(uintptr_t)3) + (left > 0 ? 4u * w : 0u);
-    cp_async4(sm100::smem_u32(tile + r * tile_pitch<T>(true) + 4 * w), reinterpret_cast<const void *>(word),
-              (uint32_t)max(0, min(4, left)));
+    unsigned char *to = tile + r * tile_pitch<T>(true);
+    if (t < 0 || t >= T_) {
+      for (int b = 0; b < tile_pitch<T>(true); b += 16) *reinterpret_cast<uint4 *>(to + b) = make_uint4(0u, 0u, 0u, 0u);
+      sm100::fence_async_smem();  // before a later bulk copy to the same place
+      continue;
+    }
+    const uintptr_t at = base + (uintptr_t)((t * src.stride + c0) * (int64_t)sizeof(T)), from = at & ~(uintptr_t)15;
+    const uint32_t n = (uint32_t)((at - from) + wanted + 15) & ~15u;
+    if (from >= base && from + n <= end) {
+      sm100::bulk_g2s(to, reinterpret_cast<const void *>(from), n, bar);
+      bytes += n;
+    } else {  // words from the one that holds the row's first byte on
+      const int off = (int)(at & 3u), skip = (int)(at - from) - off;
+      for (int b = 0; b < off + wanted; b += 4)
+        cp_async4(sm100::smem_u32(to + skip + b), reinterpret_cast<const void *>(at - off + b), (uint32_t)min(4, off + wanted - b));
+    }
   }
+  return bytes;
 }
-// Offset of row t's first channel within its word.
+__device__ __forceinline__ uint32_t warp_total(uint32_t v) { return __reduce_add_sync(0xffffffffu, v); }
+// Offset of row t's first channel within its first 16-byte word.
 template <typename T>
 __device__ __forceinline__ int raw_offset(const RowSource &src, int64_t t, int64_t c0) {
-  return sizeof(T) < 4 ? (int)((reinterpret_cast<uintptr_t>(src.base) + (uintptr_t)((t * src.stride + c0) * (int64_t)sizeof(T))) & 3u) : 0;
+  return (int)((reinterpret_cast<uintptr_t>(src.base) + (uintptr_t)((t * src.stride + c0) * (int64_t)sizeof(T))) & 15u);
 }
 
 // The pair as it is stored: 16-bit types packed in one register.
@@ -117,7 +131,9 @@ struct Packed<float> {
 template <typename T, bool RAW>
 __device__ __forceinline__ typename Packed<T>::type read_packed(const unsigned char *tile, int r, int lane, int offset) {
   if constexpr (sizeof(T) == 4) {
-    return *reinterpret_cast<const float2 *>(tile + r * tile_pitch<T>(false) + lane * 8);
+    const float *p = reinterpret_cast<const float *>(tile + r * tile_pitch<T>(RAW) + offset) + 2 * lane;
+    if constexpr (RAW) return make_float2(p[0], p[1]);
+    else return *reinterpret_cast<const float2 *>(p);
   } else if constexpr (RAW) {
     const uint16_t *p = reinterpret_cast<const uint16_t *>(tile + r * tile_pitch<T>(true) + offset) + 2 * lane;
     return (uint32_t)p[0] | (uint32_t)p[1] << 16;
@@ -182,8 +198,12 @@ __device__ __forceinline__ void write_pair(T *p, float2 v, bool two, bool vec) {
       *reinterpret_cast<uint32_t *>(p) = narrow<T>(v);
     }
   } else {
-    p[0] = from_f32<T>(v.x);
-    if (two) p[1] = from_f32<T>(v.y);
+    if (sizeof(T) == 2 && two && (reinterpret_cast<uintptr_t>(p) & 3u) == 0) {
+      *reinterpret_cast<uint32_t *>(p) = narrow<T>(v);
+    } else {
+      p[0] = from_f32<T>(v.x);
+      if (two) p[1] = from_f32<T>(v.y);
+    }
   }
 }
 // The lane's two channels of a state row (channels past C read as zero / are not written).

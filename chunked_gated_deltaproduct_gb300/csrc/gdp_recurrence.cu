@@ -1,8 +1,5 @@
-// gdp_recurrence.cu -- the gated linear recurrence: packed sequences, backward pass, one-token step
-// (gdp_layer.h).
-//
-// h_t = a_t h_{t-1} + b_t per channel.  One thread walks one channel of one sequence; neighbouring
-// threads hold neighbouring channels, so every row access is one run of memory.
+// gdp_recurrence.cu -- the gated linear recurrence (gdp_layer.h): C entries, argument checks, and the
+// one-token step.  The scans over packed sequences are in gdp_rec_fwd_body.cuh and gdp_rec_bwd_body.cuh.
 #include "gdp_rec_scan.cuh"
 
 namespace gdp {
@@ -27,22 +24,6 @@ struct RecProblem {
   int x_type, g_type, gate;
 };
 
-__device__ __forceinline__ float load_any(const void *p, int64_t i, int type) {
-  if (type == GDP_DTYPE_F32) return static_cast<const float *>(p)[i];
-  if (type == GDP_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-  return __half2float(static_cast<const __half *>(p)[i]);
-}
-__device__ __forceinline__ void store_any(void *p, int64_t i, int type, float v) {
-  if (type == GDP_DTYPE_F32) static_cast<float *>(p)[i] = v;
-  else if (type == GDP_DTYPE_BF16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
-  else static_cast<__half *>(p)[i] = __float2half_rn(v);
-}
-__device__ __forceinline__ void gate_any(int gate, float g, float *a, float *f) {
-  if (gate == GDP_GATE_LOG) gate_eval<GDP_GATE_LOG>(g, a, f);
-  else if (gate == GDP_GATE_ALPHA) gate_eval<GDP_GATE_ALPHA>(g, a, f);
-  else gate_eval<GDP_GATE_SIGMOID>(g, a, f);
-}
-
 // The state row of sequence i: where it is read (NULL: zero) and written (NULL: nowhere).
 __device__ __forceinline__ void state_rows(const RecProblem &p, int64_t i, bool report, const float **src, float **dst) {
   *src = p.init ? p.init + i * p.C : nullptr;
@@ -57,23 +38,56 @@ __device__ __forceinline__ void state_rows(const RecProblem &p, int64_t i, bool 
   }
 }
 
-__global__ void __launch_bounds__(kThreads) gdp_rec_fwd_kernel(RecProblem p, int step) {
-  const int64_t i = blockIdx.x, c = (int64_t)blockIdx.y * kThreads + threadIdx.x;
-  int64_t bos = i, len = 1;
-  if (!step && (!seq_bounds(p.cu, p.cu64, p.T, i, &bos, &len) || (i == 0 && bos != 0)) && threadIdx.x == 0)
-    set_status(p.status, GDP_DEV_ERR_CU_SEQLENS);
+// Four values of a row: 16 bytes of fp32, 8 of a 16-bit type.
+template <typename T>
+struct alignas(4 * sizeof(T)) Quad {
+  T v[4];
+};
+
+// The one-token step: every value is touched once, so it is bound by memory, and at serving sizes by its
+// own latency.  VEC channels per thread (4 where rows are aligned, else 1).
+template <typename TX, typename TG, int VEC>
+__global__ void __launch_bounds__(kThreads) gdp_rec_step_kernel(const RecProblem p) {
+  const int64_t i = blockIdx.x, c = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * VEC;
   if (c >= p.C) return;
   const float *src;
   float *dst;
-  state_rows(p, i, c == 0, &src, &dst);
-  float h = src ? src[c] : 0.f;
-  for (int64_t t = bos; t < bos + len; ++t) {
+  const TX *x_at = static_cast<const TX *>(p.x) + i * p.x_st + c;
+  const TG *g_at = static_cast<const TG *>(p.g) + i * p.g_st + c;
+  TX *h_at = static_cast<TX *>(p.h) + i * p.C + c;
+  auto one = [&](float x, float g, float s) {
     float a, f;
-    gate_any(p.gate, load_any(p.g, t * p.g_st + c, p.g_type), &a, &f);
-    h = fmaf(a, h, f * load_any(p.x, t * p.x_st + c, p.x_type));
-    store_any(p.h, t * p.C + c, p.x_type, h);
+    if (p.gate == GDP_GATE_LOG) gate_eval<GDP_GATE_LOG>(g, &a, &f);
+    else if (p.gate == GDP_GATE_ALPHA) gate_eval<GDP_GATE_ALPHA>(g, &a, &f);
+    else gate_eval<GDP_GATE_SIGMOID>(g, &a, &f);
+    return fmaf(a, s, f * x);
+  };
+  if constexpr (VEC == 4) {
+    const Quad<TX> x = *reinterpret_cast<const Quad<TX> *>(x_at);
+    const Quad<TG> g = *reinterpret_cast<const Quad<TG> *>(g_at);
+    state_rows(p, i, c == 0, &src, &dst);
+    const float4 s = src ? *reinterpret_cast<const float4 *>(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 h = make_float4(one(to_f32(x.v[0]), to_f32(g.v[0]), s.x), one(to_f32(x.v[1]), to_f32(g.v[1]), s.y),
+                                 one(to_f32(x.v[2]), to_f32(g.v[2]), s.z), one(to_f32(x.v[3]), to_f32(g.v[3]), s.w));
+    *reinterpret_cast<Quad<TX> *>(h_at) = Quad<TX>{{from_f32<TX>(h.x), from_f32<TX>(h.y), from_f32<TX>(h.z), from_f32<TX>(h.w)}};
+    if (dst) *reinterpret_cast<float4 *>(dst + c) = h;
+  } else {
+    const float x = to_f32(*x_at), g = to_f32(*g_at);
+    state_rows(p, i, c == 0, &src, &dst);
+    const float h = one(x, g, src ? src[c] : 0.f);
+    *h_at = from_f32<TX>(h);
+    if (dst) dst[c] = h;
   }
-  if (dst) dst[c] = h;
+}
+
+template <typename TX, typename TG>
+void launch_step(const RecProblem &p, cudaStream_t stream) {
+  const bool vec = p.C % 4 == 0 && p.x_st % 4 == 0 && p.g_st % 4 == 0 && aligned(p.x, 4 * sizeof(TX)) && aligned(p.g, 4 * sizeof(TG)) &&
+                   aligned(p.h, 4 * sizeof(TX)) && aligned(p.init, 16) && aligned(p.fin, 16) && aligned(p.cache, 16);
+  const int64_t width = vec ? 4 : 1;
+  const dim3 grid((unsigned)p.N, (unsigned)((p.C + kThreads * width - 1) / (kThreads * width)));
+  if (vec) gdp_rec_step_kernel<TX, TG, 4><<<grid, kThreads, 0, stream>>>(p);
+  else gdp_rec_step_kernel<TX, TG, 1><<<grid, kThreads, 0, stream>>>(p);
 }
 
 gdp_status check_shape(int64_t T, int64_t N, int64_t C, int x_type, int g_type, int gate) {
@@ -187,8 +201,13 @@ GDP_EXPORT gdp_status gdp_linear_recurrence_decode(const gdp_recurrence_args *ar
   RecProblem p;
   const gdp_status st = resolve(args, true, &p);
   if (st != GDP_OK || p.N == 0) return st;
-  const dim3 grid((unsigned)p.N, (unsigned)((p.C + kThreads - 1) / kThreads));
-  gdp_rec_fwd_kernel<<<grid, kThreads, 0, (cudaStream_t)stream>>>(p, 1);
+  const bool wide = p.g_type == GDP_DTYPE_F32;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (p.x_type == GDP_DTYPE_F32) launch_step<float, float>(p, s);
+  else if (p.x_type == GDP_DTYPE_BF16 && wide) launch_step<__nv_bfloat16, float>(p, s);
+  else if (p.x_type == GDP_DTYPE_BF16) launch_step<__nv_bfloat16, __nv_bfloat16>(p, s);
+  else if (wide) launch_step<__half, float>(p, s);
+  else launch_step<__half, __half>(p, s);
   return launch_status("recurrence step kernel");
 }
 
