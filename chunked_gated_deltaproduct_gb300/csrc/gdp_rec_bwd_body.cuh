@@ -62,8 +62,8 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
   const ScanShape &s = p.s;
   const int slice = (int)blockIdx.x / s.cluster, rank = (int)cluster_rank(), steps = (s.rows + s.cluster - 1) / s.cluster;
   const int64_t c0 = (int64_t)slice * kSlice;
-  // checkpoint scales: the slice lies in one block of one row when a row is a multiple of 64 channels
-  const bool one_scale = Q8 && p.group % kSlice == 0;
+  // checkpoint scales: the slice lies in one block of one row when a row is a multiple of 64 channels, or all
+  const bool one_scale = Q8 && (p.group % kSlice == 0 || p.group == s.C);
   const int64_t scales_per_token = Q8 ? s.C / p.group * p.blocks : 0;
   auto scale_index = [&](int64_t c) { return c / p.group * p.blocks + c % p.group / kBlock; };
   if (threadIdx.x == 0) {
@@ -92,13 +92,11 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
       unsigned char *base = smem + st * L::stage;
       if (n >= L::kStages && !ring_wait(&empty[st], (n / L::kStages + 1) & 1, gave_up, s.status, s.limit_ns)) break;
       if (RAW) {
-        uint32_t bytes = load_rows<TG>(base + L::g_off, p.g, t0, L::kTile, s.T, c0, s.C, lane, &full[st]) +
-                         load_rows<TX>(base + L::d_off, p.dout, t0, L::kTile, s.T, c0, s.C, lane, &full[st]);
-        if (Q8) bytes += load_rows<int8_t>(base + L::h_off, p.codes, t0 - 1, L::kTile, s.T, c0, s.C, lane, &full[st]);
-        else bytes += load_rows<TX>(base + L::h_off, p.h, t0 - 1, L::kTile, s.T, c0, s.C, lane, &full[st]);
-        if (L::kX) bytes += load_rows<TX>(base + L::x_off, p.x, t0, L::kTile, s.T, c0, s.C, lane, &full[st]);
-        const uint32_t total = warp_total(bytes);
-        if (lane == 0 && total) mbar_expect_tx(&full[st], total);
+        load_rows<TG>(base + L::g_off, p.g, t0, L::kTile, s.T, c0, s.C, lane);
+        load_rows<TX>(base + L::d_off, p.dout, t0, L::kTile, s.T, c0, s.C, lane);
+        if (Q8) load_rows<int8_t>(base + L::h_off, p.codes, t0 - 1, L::kTile, s.T, c0, s.C, lane);
+        else load_rows<TX>(base + L::h_off, p.h, t0 - 1, L::kTile, s.T, c0, s.C, lane);
+        if (L::kX) load_rows<TX>(base + L::x_off, p.x, t0, L::kTile, s.T, c0, s.C, lane);
       } else if (lane == 0) {
         mbar_expect_tx(&full[st], L::kTile * kSlice * (sizeof(TG) + (L::kX ? 2 : 1) * sizeof(TX) + (Q8 ? 1 : sizeof(TX))));
         sm100::tma_load_2d(base + L::g_off, &maps.g, (int)c0, (int)t0, &full[st]);

@@ -79,10 +79,8 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
       unsigned char *base = smem + st * L::stage;
       if (n >= L::kStages && !ring_wait(&empty[st], (n / L::kStages + 1) & 1, gave_up, s.status, s.limit_ns)) break;
       if (RAW) {
-        const uint32_t bytes = load_rows<TX>(base + L::x_off, p.x, t0, L::kTile, s.T, c0, s.C, lane, &full[st]) +
-                               load_rows<TG>(base + L::g_off, p.g, t0, L::kTile, s.T, c0, s.C, lane, &full[st]);
-        const uint32_t total = warp_total(bytes);
-        if (lane == 0 && total) mbar_expect_tx(&full[st], total);
+        load_rows<TX>(base + L::x_off, p.x, t0, L::kTile, s.T, c0, s.C, lane);
+        load_rows<TG>(base + L::g_off, p.g, t0, L::kTile, s.T, c0, s.C, lane);
       } else if (lane == 0) {
         mbar_expect_tx(&full[st], L::kTile * kSlice * (sizeof(TX) + sizeof(TG)));
         sm100::tma_load_2d(base + L::x_off, &map_x, (int)c0, (int)t0, &full[st]);

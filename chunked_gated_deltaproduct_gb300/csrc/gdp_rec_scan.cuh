@@ -5,8 +5,8 @@
 // of 8 S tokens x 64 channels whatever the sequences' lengths (a sequence's first token simply
 // replaces the state).  A cluster of CTAs owns 64 channels for all of time: in step n its CTA k works
 // on tile n * cluster + k.  In a CTA,
-//   - a loading warp brings tiles ahead into a ring of shared-memory stages (TMA boxes, or a bulk copy per
-//     row where rows are not 16-byte aligned) and finds the sequences in them;
+//   - a loading warp brings tiles ahead into a ring of shared-memory stages (TMA boxes, or 16-byte
+//     asynchronous copies where rows are not 16-byte aligned) and finds the sequences in them;
 //   - eight warps of S tokens each run the tile from zero, which gives each warp's (A, B), keep their
 //     decays and inputs in registers, and run it again from their entering states for the outputs;
 //   - a chaining warp folds the eight (A, B) in between, writes the tile's (A, B) into every CTA of the
@@ -79,40 +79,51 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(sm100::smem_u32(bar)), "r"(bytes) : "memory");
 }
 
-// Whole warp: rows [t0, t0 + rows) x channels [c0, c0 + 64) of a tensor whose rows start anywhere, one bulk
-// copy per row of the 16-byte words that hold it; a row keeps its offset within its first word (raw_offset).
-// The words' other bytes belong to neighbouring rows; where they could lie outside the tensor (before its
-// first row, after its last) the row comes by 4-byte copies that stop at its end.  Rows outside [0, T)
-// become zeros.  Returns the bulk copies' bytes (of this lane's rows).
+// Whole warp: rows [t0, t0 + rows) x channels [c0, c0 + 64) of a tensor whose rows start anywhere, by
+// asynchronous copies of the 16-byte words that hold them; a row keeps its offset within its first word
+// (raw_offset).  The words' other bytes belong to neighbouring rows: nothing before the tensor's first
+// element's 4-byte word or after its last element is read.  Rows outside [0, T) become zeros.  Tiles away from
+// the tensor's first and last rows go eight rows at a time without a check per word, the others word by word
+// (everywhere so: 308 us at 16384 x 4095; a bulk copy per row: 298 us).
 template <typename T>
-__device__ __forceinline__ uint32_t load_rows(unsigned char *tile, const RowSource &src, int64_t t0, int rows, int64_t T_, int64_t c0,
-                                              int64_t C, int lane, uint64_t *bar) {
-  const int wanted = (int)min((int64_t)kSlice, C - c0) * (int)sizeof(T);
+__device__ __forceinline__ void load_rows(unsigned char *tile, const RowSource &src, int64_t t0, int rows, int64_t T_, int64_t c0,
+                                          int64_t C, int lane) {
+  constexpr int kWords = tile_pitch<T>(true) / 16;
+  const int64_t pitch = src.stride * (int64_t)sizeof(T);
+  if (t0 >= 1 && t0 + rows < T_ && pitch >= 16 * kWords + 16) {  // every word lies between two rows of the tensor
+    const int q = lane & 3;
+    int r = lane >> 2;
+    uintptr_t at = reinterpret_cast<uintptr_t>(src.base) + (uintptr_t)((t0 + r) * pitch + c0 * (int64_t)sizeof(T));
+    unsigned char *to = tile + r * tile_pitch<T>(true) + 16 * q;
+#pragma unroll 2
+    for (; r < rows; r += 8, at += 8 * pitch, to += 8 * tile_pitch<T>(true)) {
+      const unsigned char *from = reinterpret_cast<const unsigned char *>(at & ~(uintptr_t)15) + 16 * q;
+#pragma unroll
+      for (int k = 0; k < kWords; k += 4)
+        if (k + 4 <= kWords || q < kWords - k) sm100::cp_async16(to + 16 * k, from + 16 * k, 16u);
+    }
+    return;
+  }
+  const uint32_t wanted = (uint32_t)min((int64_t)kSlice, C - c0) * (uint32_t)sizeof(T);
   const uintptr_t base = reinterpret_cast<uintptr_t>(src.base);
   const uintptr_t end = base + (uintptr_t)(((T_ - 1) * src.stride + C) * (int64_t)sizeof(T));
-  uint32_t bytes = 0;
-  for (int r = lane; r < rows; r += 32) {
+  for (int i = lane; i < rows * kWords; i += 32) {
+    const int r = i / kWords, w = i % kWords;
     const int64_t t = t0 + r;
-    unsigned char *to = tile + r * tile_pitch<T>(true);
-    if (t < 0 || t >= T_) {
-      for (int b = 0; b < tile_pitch<T>(true); b += 16) *reinterpret_cast<uint4 *>(to + b) = make_uint4(0u, 0u, 0u, 0u);
-      sm100::fence_async_smem();  // before a later bulk copy to the same place
-      continue;
-    }
-    const uintptr_t at = base + (uintptr_t)((t * src.stride + c0) * (int64_t)sizeof(T)), from = at & ~(uintptr_t)15;
-    const uint32_t n = (uint32_t)((at - from) + wanted + 15) & ~15u;
-    if (from >= base && from + n <= end) {
-      sm100::bulk_g2s(to, reinterpret_cast<const void *>(from), n, bar);
-      bytes += n;
-    } else {  // words from the one that holds the row's first byte on
-      const int off = (int)(at & 3u), skip = (int)(at - from) - off;
-      for (int b = 0; b < off + wanted; b += 4)
-        cp_async4(sm100::smem_u32(to + skip + b), reinterpret_cast<const void *>(at - off + b), (uint32_t)min(4, off + wanted - b));
+    const bool in = t >= 0 && t < T_;
+    const uintptr_t at = base + (uintptr_t)(((in ? t : 0) * src.stride + c0) * (int64_t)sizeof(T));
+    const uintptr_t word = (at & ~(uintptr_t)15) + 16u * w;
+    unsigned char *to = tile + r * tile_pitch<T>(true) + 16 * w;
+    if (!in || word >= at + wanted) {
+      sm100::cp_async16(to, reinterpret_cast<const void *>(base & ~(uintptr_t)15), 0u);  // zeros, nothing is read
+    } else if (word >= base) {
+      sm100::cp_async16(to, reinterpret_cast<const void *>(word), (uint32_t)min((uintptr_t)16, end - word));
+    } else {  // the tensor begins within this word
+      for (uintptr_t b = base & ~(uintptr_t)3; b < word + 16 && b < end; b += 4)
+        cp_async4(sm100::smem_u32(to + (b - word)), reinterpret_cast<const void *>(b), (uint32_t)min((uintptr_t)4, end - b));
     }
   }
-  return bytes;
 }
-__device__ __forceinline__ uint32_t warp_total(uint32_t v) { return __reduce_add_sync(0xffffffffu, v); }
 // Offset of row t's first channel within its first 16-byte word.
 template <typename T>
 __device__ __forceinline__ int raw_offset(const RowSource &src, int64_t t, int64_t c0) {
