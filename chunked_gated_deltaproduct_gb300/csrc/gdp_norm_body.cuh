@@ -216,10 +216,18 @@ __device__ __forceinline__ void block_tops(uint32_t &a, uint32_t &b) {
     b = __float_as_uint(widen<T>(t).y);
   }
 }
-// Codes of two pairs in a word: v k + 1.5 2^23 in one rounding leaves the integer in the low byte.
+// Codes of two pairs in a word: v k + 1.5 2^23 leaves the integer in the low byte.  The product is exact for
+// 16-bit types and rounded to fp32 first for fp32 values, so that the codes are those of plain fp32 arithmetic.
+template <typename T>
+__device__ __forceinline__ float2 code_pair(float2 v, float inv) {
+  // (one by one: the paired operations came out contracted)
+  if constexpr (sizeof(T) == 4) return make_float2(__fadd_rn(__fmul_rn(v.x, inv), 12582912.f), __fadd_rn(__fmul_rn(v.y, inv), 12582912.f));
+  else return fma2(v, both(inv), both(12582912.f));
+}
+template <typename T>
 __device__ __forceinline__ uint32_t code_word(float2 a, float2 b, float inv) {
-  a = fma2(a, both(inv), both(12582912.f));
-  b = fma2(b, both(inv), both(12582912.f));
+  a = code_pair<T>(a, inv);
+  b = code_pair<T>(b, inv);
   return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
                      __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
 }
@@ -228,7 +236,7 @@ __device__ __forceinline__ void save_row(const Sixteen<T> &v, uint32_t top, int8
   const float inv = block_inverse<T>(top);
   Sixteen<int8_t> e;
 #pragma unroll
-  for (int i = 0; i < kPer / 4; ++i) reinterpret_cast<uint32_t *>(e.v)[i] = code_word(v.pair(2 * i), v.pair(2 * i + 1), inv);
+  for (int i = 0; i < kPer / 4; ++i) reinterpret_cast<uint32_t *>(e.v)[i] = code_word<T>(v.pair(2 * i), v.pair(2 * i + 1), inv);
   store_row<int8_t, VEC, L>(codes, e, pl, D, on);
   if (on && pl.leads_block() && pl.in[0]) *scale = block_scale(top, inv);
 }

@@ -144,10 +144,11 @@ typedef enum gdp_activation {
  * [T, H, ceil(D / 128)] fp32, written in the same pass.  Each row is cut into blocks of 128 channels
  * (the last one shorter); k = 127 / amax of the block cut to four significant bits,
  * code = round-to-even(value k), scale = 1 / k, and the code stands for code * scale.  (Four bits, so
- * that value k is exact for 16-bit values: the codes are the same in any arithmetic; at most 1/9 of
- * the code range stays unused.)  A block whose amax is below 2^-100 is all zeros with scale 0; a block
- * holding an infinity or a NaN gets scale NaN, so that its values, and what is computed from them,
- * are NaN.  Both of a pair, or neither; z's only with z.
+ * that value k is exact for 16-bit values and the codes are the same in any arithmetic; of an fp32
+ * value the product is rounded to fp32 first.  At most 1/9 of the code range stays unused.)  A block
+ * whose amax is below 2^-100 is all zeros with scale 0; a block holding an infinity or a NaN gets
+ * scale NaN, so that its values, and what is computed from them, are NaN.  Both of a pair, or neither;
+ * z's only with z.
  */
 typedef struct gdp_group_norm_args {
   const void *o; /* [T, H, D] */

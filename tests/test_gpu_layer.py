@@ -460,6 +460,19 @@ def test_group_norm(cuda_device, case):
             assert torch.equal(c.scales.cpu(), scales.float()), name
 
 
+def test_checkpoint_codes_of_fp32_values(cuda_device):
+    """fp32 values: the codes of plain fp32 arithmetic, product rounded first, bit for bit (a value next to a
+    tie may differ from the 64-bit code)."""
+    for shape in ((3000, 8, 128), (400, 1, 4096), (500, 3, 100)):
+        v = _rand(shape, 1).to(cuda_device)
+        kept = pkg.gated_group_norm(v, torch.ones(shape[-1], device=cuda_device), activation=None, save_checkpoint=True)[1]
+        pad = -shape[-1] % 128
+        amax = torch.nn.functional.pad(v, (0, pad)).view(*shape[:2], -1, 128).abs().amax(-1)
+        inv = ((127.0 / amax).view(torch.int32) & -0x100000).view(torch.float32)
+        codes = torch.round(v * inv.repeat_interleave(128, -1)[..., :shape[-1]])
+        assert torch.equal(kept.o.codes, codes.to(torch.int8)) and torch.equal(kept.o.scales, 1.0 / inv)
+
+
 @pytest.mark.parametrize("saved", ["checkpoint", "tensors"])
 @pytest.mark.parametrize("case", NORMS)
 def test_group_norm_backward(cuda_device, case, saved):
