@@ -6,6 +6,11 @@
 // sums over tokens (dweight, dbias) accumulate in registers; it walks over tokens with the next row's
 // loads in flight.  Those sums leave once per CTA (or per group where every head has its own weights)
 // and a second kernel adds them up in a fixed order.
+//
+// Bound: 65536 x 32 x 128 bf16 with a gate takes 337 us forward with checkpoints (2.16 GB, 6.4 TB/s: memory) and
+// about 435 us backward from them (2.16 GB, 5.0 TB/s).  The backward takes 35 instructions per channel, issues on
+// 55 % of the cycles and draws 54 % of the memory's peak: 128 registers hold the row, its gradient and the
+// column sums, and two CTAs per SM (16 warps) do not hide the loads; three spill (1244 against 834 us).
 #pragma once
 
 #include "gdp_norm.cuh"

@@ -45,7 +45,8 @@ struct alignas(4 * sizeof(T)) Quad {
 };
 
 // The one-token step: every value is touched once, so it is bound by memory, and at serving sizes by its
-// own latency.  VEC channels per thread (4 where rows are aligned, else 1).
+// own latency (64 x 2048 bf16: 1.7 MB in 2.2 us on the device, 0.25 us at the memory's rate).  VEC channels
+// per thread (4 where rows are aligned, else 1).
 template <typename TX, typename TG, int VEC>
 __global__ void __launch_bounds__(kThreads) gdp_rec_step_kernel(const RecProblem p) {
   const int64_t i = blockIdx.x, c = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * VEC;
