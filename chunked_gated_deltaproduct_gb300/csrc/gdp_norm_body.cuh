@@ -10,7 +10,8 @@
 // Bound: 65536 x 32 x 128 bf16 with a gate takes 337 us forward with checkpoints (2.16 GB, 6.4 TB/s: memory) and
 // about 435 us backward from them (2.16 GB, 5.0 TB/s).  The backward takes 35 instructions per channel, issues on
 // 55 % of the cycles and draws 54 % of the memory's peak: 128 registers hold the row, its gradient and the
-// column sums, and two CTAs per SM (16 warps) do not hide the loads; three spill (1244 against 834 us).
+// column sums, and two CTAs per SM (16 warps) do not hide the loads.  More warps spill (three CTAs 1244 against 834 us for
+// the training step), and with dweight's sums in shared memory too (1057 and, two CTAs, 807 against 783 us).
 #pragma once
 
 #include "gdp_norm.cuh"
