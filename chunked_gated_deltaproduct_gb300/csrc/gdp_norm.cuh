@@ -33,8 +33,8 @@ struct NormProblem {
 template <int L>
 constexpr int kNormThreads = L > 0 ? 256 : 512;
 
-// Resident CTAs of 256 threads per SM: what the registers allow without spilling in the loops (forward 80,
-// backward 128 registers; four and three: 915 us and 1240 us for the training step of 65536 x 32 x 128, so:
+// Resident CTAs of 256 threads per SM: what the registers allow with next to no spills (forward 80, backward
+// 128 registers, 8 to 28 bytes spilled; four and three: 915 us and 1240 us for the training step of 65536 x 32 x 128, so:
 // 784 us).
 constexpr int kNormFwdCtas = 3, kNormBwdCtas = 2;
 // How a call runs: groups of `lanes` threads (0: a CTA of `threads`), sixteen channels each.
