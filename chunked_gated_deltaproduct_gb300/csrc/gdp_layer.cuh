@@ -65,13 +65,16 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// sigmoid(x) and 1 - sigmoid(x) = e^-x sigmoid(x), each to its own relative precision; the exponent is
-// held to 2^115, where the first is 0 next to any other term and the product is still 1.
+// sigmoid(x) and 1 - sigmoid(x) = e^-x sigmoid(x), each to its own relative precision.  e^-x is held to the
+// largest fp32 value, so that the second is finite; the first reaches 0 (at x below -87.3, 2^-126), so that its
+// product with any finite x does too.  Where it is 0 the second is 0 as well, and not 1: a caller multiplies it by
+// the first, or by x and then by the first.
 __device__ __forceinline__ void sigmoid_halves(float2 x, float2 *q, float2 *rest) {
-  float2 t = mul2(x, both(-kLog2e));
-  asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(t.x));
-  asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(t.y));
-  const float2 e = make_float2(ex2(t.x), ex2(t.y)), d = add2(e, both(1.f));
+  const float2 t = mul2(x, both(-kLog2e));
+  float2 e = make_float2(ex2(t.x), ex2(t.y));
+  asm("min.NaN.f32 %0, %0, 0f7F7FFFFF;" : "+f"(e.x));
+  asm("min.NaN.f32 %0, %0, 0f7F7FFFFF;" : "+f"(e.y));
+  const float2 d = add2(e, both(1.f));
   *q = make_float2(rcp(d.x), rcp(d.y));
   *rest = mul2(e, *q);
 }
@@ -146,7 +149,9 @@ __device__ __forceinline__ float block_inverse(uint32_t amax_bits) {
 __constant__ const float kEighths[8] = {8.f / 8.f, 8.f / 9.f, 8.f / 10.f, 8.f / 11.f, 8.f / 12.f, 8.f / 13.f, 8.f / 14.f, 8.f / 15.f};
 __device__ __forceinline__ float block_scale(uint32_t amax_bits, float inverse) {
   const uint32_t b = __float_as_uint(inverse);
-  const float s = kEighths[b >> 20 & 7u] * __uint_as_float((254u << 23) - (b & 0x7f800000u));
+  // 127 / amax is at least 1.875 2^-122; a code of 120 times that one's reciprocal would be 2^128, beyond fp32, for
+  // a block whose largest value is the type's: the next number below it makes that the largest fp32 value
+  const float s = fminf(kEighths[b >> 20 & 7u] * __uint_as_float((254u << 23) - (b & 0x7f800000u)), __uint_as_float(0x7c088888u));
   return amax_bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : b == 0u ? 0.f : s;
 }
 

@@ -345,7 +345,8 @@ __global__ void __launch_bounds__(L > 0 ? kNormThreads<L> : kWideFwdBound, L > 0
           float2 x = fma2(mul2(v[u], both(r)), cw[u - i], cb[u - i]);
           if constexpr (kZed) {
             const float2 g = z.pair(u);
-            x = mul2(kAct == GDP_ACT_SILU ? mul2(x, g) : x, sigmoid2(g));
+            // g sigmoid(g) first: for g next to the type's lowest value it is 0, while x g overflows
+            x = mul2(x, kAct == GDP_ACT_SILU ? mul2(g, sigmoid2(g)) : sigmoid2(g));
           } else if constexpr (kAct == GDP_ACT_SILU) {
             x = mul2(x, sigmoid2(x));
           }

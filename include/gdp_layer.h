@@ -147,7 +147,8 @@ typedef enum gdp_activation {
  * that value k is exact for 16-bit values and the codes are the same in any arithmetic; of an fp32
  * value the product is rounded to fp32 first.  At most 1/9 of the code range stays unused.)  A block
  * whose amax is below 2^-100 is all zeros with scale 0; a block holding an infinity or a NaN gets
- * scale NaN, so that its values, and what is computed from them, are NaN.  Both of a pair, or neither;
+ * scale NaN, so that its values, and what is computed from them, are NaN.  (Where 120 scale would be 2^128,
+ * beyond fp32, the scale is the next number below 1 / k: every finite block's values are finite.)  Both of a pair, or neither;
  * z's only with z.
  */
 typedef struct gdp_group_norm_args {

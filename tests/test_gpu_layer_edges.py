@@ -1,0 +1,83 @@
+"""The layer operators at the edges of their types and of what a call may be."""
+import math
+
+import pytest
+import torch
+
+import chunked_gated_deltaproduct_gb300 as pkg
+from tests import _layer_ref as R
+from tests.test_gpu_layer import _as_laid_out, _cu, _gates, _rand
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+# ---- the norm's gate far below zero.  Where sigmoid(z) is below fp32's smallest normal number it counts as zero:
+# 2^-126 off, times what it is multiplied with.
+FLUSH = 2.0 ** -126
+
+
+@pytest.fixture
+def exact_slopes(monkeypatch):
+    """The reference with 1 - sigmoid(t) as sigmoid(-t): the difference cancels to 0 in 64 bits for t above 36."""
+    def act(kind, t):
+        q, rest = torch.sigmoid(t), torch.sigmoid(-t)
+        return (t * q, q * (1 + t * rest)) if kind == "silu" else (q, q * rest)
+    monkeypatch.setattr(R, "_act", act)
+
+
+def _masked_gate(dt, T, H, D):
+    lowest = torch.finfo(dt).min
+    z = _rand((T, H, D), 2, F32, 2.0)
+    values = [lowest, 0.5 * lowest, -1e36, -1e33, -1e30, -1e4, -100.0, -89.0, -88.0, -87.0, -80.0, -40.0, 40.0, 100.0]
+    for i, v in enumerate(values):
+        z[:, :, 3 * i] = max(v, lowest)
+    z[1], z[2, :, ::2] = lowest, lowest  # a whole row masked, and half of one
+    return z.to(dt)
+
+
+@pytest.mark.parametrize("dt,D,act,layout", [(BF16, 128, "silu", "dense"), (BF16, 100, "sigmoid", "odd"), (F32, 128, "silu", "slice"),
+                                             (F32, 1024, "sigmoid", "dense"), (F32, 61, "silu", "odd"), (F16, 64, "silu", "dense"),
+                                             (BF16, 1000, "silu", "dense")])
+def test_group_norm_gate_at_the_lowest_value(cuda_device, exact_slopes, dt, D, act, layout):
+    dev, T, H = cuda_device, 9, 3
+    o, z, dy = _rand((T, H, D), 1, dt, 2.0), _masked_gate(dt, T, H, D), _rand((T, H, D), 5, dt)
+    w, b = 1 + _rand((D,), 3, sigma=0.3), _rand((D,), 4, sigma=0.3)
+    on = lambda t: _as_laid_out(t, layout, dev)  # noqa: E731
+    y, kept = pkg.gated_group_norm(on(o), w.to(dev), on(z), b.to(dev), activation=act, save_checkpoint=True)
+    ref, err = R.group_norm(o, w, z, b, act=act)
+    u = R._normed(o.double(), 1e-5, False)[0] * w + b
+    R.check(y, ref, err + FLUSH * u.abs() * (z.double().abs().clamp(max=128) if act == "silu" else 1.0), "y")
+    for saved in ("tensors", "checkpoint"):
+        if saved == "checkpoint":  # what the codes stand for: finite, however large the block's largest value
+            assert bool(torch.isfinite(kept.z.dequantize()).all())
+            o, z = (c.dequantize().cpu().double() for c in kept)
+        got = pkg.gated_group_norm_backward(on(dy), kept if saved == "checkpoint" else (on(o), on(z)), w.to(dev), b.to(dev),
+                                            activation=act)
+        ref = R.group_norm_backward(dy, o, w, z, b, act=act)
+        n, r = R._normed(o.double(), 1e-5, False)
+        u, size = n * w + b, FLUSH * (1 + z.double().abs().clamp(max=128)) * dy.double().abs()
+        d = size * w.abs()  # of dn
+        extra = {"dz": size * u.abs(), "do": r * (d + n.abs() * (d * n.abs()).mean(-1, keepdim=True)),
+                 "dweight": (size * n.abs()).sum((0, 1)), "dbias": size.sum((0, 1))}
+        for name in ("do", "dz", "dweight", "dbias"):
+            R.check(got[name], ref[name][0], ref[name][1] + extra[name], f"{name} from {saved}")
+
+
+def test_group_norm_of_itself_far_below_zero(cuda_device):
+    """Without z the affine norm gates itself: weights that take it far below zero."""
+    dev, D = cuda_device, 128
+    o, dy, w = _rand((4, 2, D), 1, F32), _rand((4, 2, D), 2, F32), _rand((D,), 3)
+    w[::4] = 1e35
+    y = pkg.gated_group_norm(o.to(dev), w.to(dev))
+    R.check(y, *R.group_norm(o, w), "y")
+    # far below zero the slope is zero, far above it is one; in between (|u| < 128) the reference's bound
+    got = pkg.gated_group_norm_backward(dy.to(dev), (o.to(dev), None), w.to(dev))
+    n = R._normed(o.double(), 1e-5, False)[0]
+    u = n * w
+    slope = R._act("silu", u)[1]
+    far = (u.abs() > 1e3).all(0).all(0)
+    assert bool(far.any())
+    dw = (dy.double() * slope * n).sum((0, 1))
+    assert bool(torch.isfinite(got["do"]).all())
+    # a sum of eight products, each off by a few 2^-22
+    assert bool(((got["dweight"].cpu() - dw).abs() <= 2.0 ** -18 * (dy.double() * n).abs().sum((0, 1)))[far].all())
