@@ -49,8 +49,9 @@ gdp_status check_norm(int64_t T, int64_t H, int64_t D, float eps, int type, int 
   if (!(eps >= 0.f)) return fail(GDP_ERR_INVALID_ARG, "eps must not be negative");
   if (act != GDP_ACT_NONE && act != GDP_ACT_SILU && act != GDP_ACT_SIGMOID)
     return fail(GDP_ERR_INVALID_ARG, "activation must be GDP_ACT_NONE, GDP_ACT_SILU or GDP_ACT_SIGMOID");
-  if (has_gate && act == GDP_ACT_NONE) return fail(GDP_ERR_INVALID_ARG, "z needs an activation");
-  if (!has_gate && act == GDP_ACT_SIGMOID) return fail(GDP_ERR_INVALID_ARG, "the sigmoid activation gates with z");
+  // (of an empty batch the gate may be given and have no address)
+  if (T > 0 && has_gate && act == GDP_ACT_NONE) return fail(GDP_ERR_INVALID_ARG, "z needs an activation");
+  if (T > 0 && !has_gate && act == GDP_ACT_SIGMOID) return fail(GDP_ERR_INVALID_ARG, "the sigmoid activation gates with z");
   if (!w) return fail(GDP_ERR_INVALID_ARG, "weight is required");
   return GDP_OK;
 }

@@ -81,3 +81,17 @@ def test_group_norm_of_itself_far_below_zero(cuda_device):
     assert bool(torch.isfinite(got["do"]).all())
     # a sum of eight products, each off by a few 2^-22
     assert bool(((got["dweight"].cpu() - dw).abs() <= 2.0 ** -18 * (dy.double() * n).abs().sum((0, 1)))[far].all())
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("saved", ["tensors", "checkpoint"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_empty_gated_batch(cuda_device, act, saved, bias):
+    dev = cuda_device
+    o = torch.empty((0, 3, 8), dtype=BF16, device=dev)
+    w = torch.ones(8, device=dev)
+    b = torch.zeros(8, device=dev) if bias else None
+    y, kept = pkg.gated_group_norm(o, w, o.clone(), b, activation=act, save_checkpoint=True)
+    d = pkg.gated_group_norm_backward(y, kept if saved == "checkpoint" else (o, o.clone()), w, b, activation=act)
+    assert y.shape == o.shape and d["do"].shape == o.shape and d["dz"].shape == o.shape
+    assert not bool(d["dweight"].any()) and (b is None or not bool(d["dbias"].any()))

@@ -176,3 +176,10 @@ def test_checkpoint_dequantizes_by_blocks():
     c = pkg.ActivationCheckpoint(torch.full((1, 1, 130), 2, dtype=torch.int8), torch.tensor([[[0.5, 3.0]]]))
     v = c.dequantize()
     assert v.shape == (1, 1, 130) and float(v[0, 0, 127]) == 1.0 and float(v[0, 0, 128]) == 6.0
+
+
+@pytest.mark.parametrize("activation", [0, 1, 2])
+def test_group_norm_of_an_empty_batch(lib, activation):
+    """Its tensors, the gate among them, may have no address."""
+    a = _norm(T=0, o=None, z=None, y=None, activation=activation)
+    assert lib.gdp_group_norm(ctypes.byref(a), None) == pkg.GDP_OK, pkg.gdp_last_error()
