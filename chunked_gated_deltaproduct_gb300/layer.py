@@ -149,8 +149,13 @@ def _current(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream
 
 
+def _current_device():
+    return torch._C._cuda_getDevice()
+
+
 def _first(name, t, dims):
-    """(shape, type code, device index) of the tensor that sets them for the call."""
+    """(shape, type code, device index) of the tensor that sets them for the call.  The library launches on the
+    current device, so the tensors have to be there."""
     if t.dim() != len(dims):
         _invalid(f"{name} must be [{', '.join(dims)}]")
     code = _TYPES.get(t.dtype)
@@ -161,7 +166,10 @@ def _first(name, t, dims):
     shape = t.shape
     if shape[-1] > 1 and t.stride(-1) != 1:
         _invalid(f"{name} must be contiguous in its last dimension")
-    return shape, code, t.get_device()
+    dev = t.get_device()
+    if dev != _current_device():
+        _invalid(f"{name} is on cuda:{dev}, the current device is cuda:{_current_device()}")
+    return shape, code, dev
 
 
 def _rows(name, t, shape, dtype, dev):

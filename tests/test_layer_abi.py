@@ -183,3 +183,31 @@ def test_group_norm_of_an_empty_batch(lib, activation):
     """Its tensors, the gate among them, may have no address."""
     a = _norm(T=0, o=None, z=None, y=None, activation=activation)
     assert lib.gdp_group_norm(ctypes.byref(a), None) == pkg.GDP_OK, pkg.gdp_last_error()
+
+
+class _Elsewhere:
+    """What the checks ask of a CUDA tensor, without one."""
+    is_cuda, dtype = True, torch.bfloat16
+
+    def __init__(self, *shape):
+        self.shape = torch.Size(shape)
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i):
+        return 1
+
+    def get_device(self):
+        return 1
+
+
+def test_wrappers_refuse_tensors_off_the_current_device(lib, monkeypatch):
+    """The library launches on the current device; nothing is launched here."""
+    monkeypatch.setattr(layer, "_current_device", lambda: 0, raising=False)
+    x, o = _Elsewhere(4, 8), _Elsewhere(4, 2, 4)
+    for call in (lambda: pkg.gated_linear_recurrence(x, x, None), lambda: pkg.gated_linear_recurrence_decode(x, x),
+                 lambda: pkg.gated_linear_recurrence_backward(x, x, x, None), lambda: pkg.gated_group_norm(o, None),
+                 lambda: pkg.gated_group_norm_backward(o, (o, None), None)):
+        with pytest.raises(pkg.GdpError, match="is on cuda:1, the current device is cuda:0"):
+            call()
