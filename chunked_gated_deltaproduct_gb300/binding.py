@@ -10,6 +10,10 @@ Megatron-Core API page "core.ssm.ops.gdp.chunk", function
 chunk_gated_delta_product_varlen): torch supplies device memory and the
 current stream, every step of the computation runs in the library's CUDA
 kernels.  There is no fallback: if the library is missing, every call raises.
+
+``stream``, a raw stream handle, says where a call's kernels run; outputs and workspaces that the caller does not
+give are allocated from the current stream's memory all the same, so a caller that gives another stream orders it
+after the current one first (or makes the call under ``torch.cuda.stream``).
 """
 from __future__ import annotations
 

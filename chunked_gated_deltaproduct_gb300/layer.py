@@ -2,6 +2,9 @@
 (packed sequences, backward, one-token step) and the grouped norm with an activated gate, with its
 8-bit activation checkpoints.  Argument checks and marshalling only; torch supplies device memory and
 the current stream, and there is no fallback: without the library every call raises.
+
+``stream``, a raw stream handle, makes a call as under ``torch.cuda.stream`` of it: it runs there and what it
+allocates belongs there, so that the caller orders it after the inputs' stream, and other streams after it.
 """
 from __future__ import annotations
 
@@ -144,9 +147,16 @@ def _finish(status, lib):
         raise GdpError(status, lib.gdp_last_error().decode())
 
 
-def _current(stream, dev):
-    """The stream handle of a call: the caller's, or torch's current one on the device."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream
+def _current(dev):
+    """Handle of torch's current stream on the device."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _on(stream, call, *args):
+    """The call with that stream as torch's current one, its allocations too: a block of another stream's pool may
+    still be in use by work on that one."""
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream)):
+        return call(*args)
 
 
 def _current_device():
@@ -243,7 +253,7 @@ def _state_args(initial_state, output_state, state, state_indices, N, C, dev):
 
 
 def _recurrence(x, g, gate, cu, N, cu64, entry, first, initial_state, output_final_state, state, state_indices, output,
-                output_state, device_status, stream):
+                output_state, device_status):
     """The common part of the packed and the one-token call."""
     shape, xt, dev = first
     T, C = shape
@@ -259,7 +269,7 @@ def _recurrence(x, g, gate, cu, N, cu64, entry, first, initial_state, output_fin
     a = _pack_recurrence(x.data_ptr(), x.stride(0), gp, g.stride(0), op, cu, T, N, C,
                           *_state_args(initial_state, output_state, state, state_indices, N, C, dev),
                           _status(device_status, dev), cu64, xt, gt, _gate_code(gate))
-    _finish(getattr(lib, entry)(a, _current(stream, dev)), lib)
+    _finish(getattr(lib, entry)(a, _current(dev)), lib)
     return (output, output_state) if output_final_state else output
 
 
@@ -273,10 +283,13 @@ def gated_linear_recurrence(x, g, cu_seqlens, gate="log", initial_state=None, ou
     cache ``state`` [num_slots, C] fp32 read and written in place at ``state_indices`` [N] int32 (-1:
     from zero, nothing written).  Returns ``h`` [T, C] in x's type, or ``(h, final_state)`` when
     output_final_state (dense mode; None in cache mode)."""
+    if stream is not None:
+        return _on(stream, gated_linear_recurrence, x, g, cu_seqlens, gate, initial_state, output_final_state, state,
+                   state_indices, output, output_state, device_status)
     first = _first("x", x, ("T", "C"))
     cu, N, cu64 = _cu(cu_seqlens, first[2])
     return _recurrence(x, g, gate, cu, N, cu64, "gdp_linear_recurrence", first, initial_state, output_final_state, state,
-                       state_indices, output, output_state, device_status, stream)
+                       state_indices, output, output_state, device_status)
 
 
 def gated_linear_recurrence_decode(x, g, gate="log", initial_state=None, output_final_state=False, state=None,
@@ -284,9 +297,12 @@ def gated_linear_recurrence_decode(x, g, gate="log", initial_state=None, output_
                                    stream=None):
     """One token per sequence: x, g [N, C]; the state modes, types and gates of gated_linear_recurrence.
     Returns ``h`` [N, C], or ``(h, final_state)`` when output_final_state (dense mode)."""
+    if stream is not None:
+        return _on(stream, gated_linear_recurrence_decode, x, g, gate, initial_state, output_final_state, state, state_indices,
+                   output, output_state, device_status)
     first = _first("x", x, ("N", "C"))
     return _recurrence(x, g, gate, 0, first[0][0], 0, "gdp_linear_recurrence_decode", first, initial_state,
-                       output_final_state, state, state_indices, output, output_state, device_status, stream)
+                       output_final_state, state, state_indices, output, output_state, device_status)
 
 
 def gated_linear_recurrence_backward(g, h, d_output, cu_seqlens, gate="log", x=None, initial_state=None,
@@ -296,6 +312,9 @@ def gated_linear_recurrence_backward(g, h, d_output, cu_seqlens, gate="log", x=N
     the ActivationCheckpoint of it that gated_group_norm kept ([T, H, D] with H D = C).  ``x`` is needed
     for the sigmoid gate only.  Returns a dict: dx in d_output's type, dg in g's type, d_initial_state
     fp32 (None without an initial state)."""
+    if stream is not None:
+        return _on(stream, gated_linear_recurrence_backward, g, h, d_output, cu_seqlens, gate, x, initial_state, d_final_state,
+                   device_status)
     shape, xt, dev = _first("d_output", d_output, ("T", "C"))
     T, C = shape
     dtype, where = d_output.dtype, d_output.device
@@ -323,7 +342,7 @@ def gated_linear_recurrence_backward(g, h, d_output, cu_seqlens, gate="log", x=N
         gp, g.stride(0), xp, xs, hp, hs, codes, scales, group, d_output.data_ptr(), d_output.stride(0), cu, T, N, C, init,
         dfin, dx.data_ptr(), dg.data_ptr(), 0 if dinit is None else dinit.data_ptr(), _status(device_status, dev), cu64,
         xt, gt, gate)
-    _finish(lib.gdp_linear_recurrence_backward(a, _current(stream, dev)), lib)
+    _finish(lib.gdp_linear_recurrence_backward(a, _current(dev)), lib)
     return {"dx": dx, "dg": dg, "d_initial_state": dinit}
 
 
@@ -365,6 +384,8 @@ def gated_group_norm(o, weight, z=None, bias=None, eps=1e-5, center=False, activ
 
     Returns ``y`` [T, H, D] in o's type, or ``(y, checkpoint)`` with the GroupNormCheckpoint (8-bit
     codes of o and z) that gated_group_norm_backward takes when ``save_checkpoint``."""
+    if stream is not None:
+        return _on(stream, gated_group_norm, o, weight, z, bias, eps, center, activation, save_checkpoint, output)
     shape, dt, dev = _first("o", o, ("T", "H", "D"))
     T, H, D = shape
     where = o.device
@@ -388,7 +409,7 @@ def gated_group_norm(o, weight, z=None, bias=None, eps=1e-5, center=False, activ
     lib = _library()
     a = _pack_norm(o.data_ptr(), ot, oh, zp, zt, zh, w, b, yp, *ptrs, T, H, D, eps, dt, int(bool(center)), per_head,
                          _act_code(activation))
-    _finish(lib.gdp_group_norm(a, _current(stream, dev)), lib)
+    _finish(lib.gdp_group_norm(a, _current(dev)), lib)
     return (output, kept) if save_checkpoint else output
 
 
@@ -398,6 +419,8 @@ def gated_group_norm_backward(d_output, saved, weight, bias=None, eps=1e-5, cent
     GroupNormCheckpoint of the forward call, or the pair ``(o, z)`` of tensors (z None without a gate).
     Returns a dict: do and dz in d_output's type (dz None without z), dweight and dbias fp32 (None
     without a bias)."""
+    if stream is not None:
+        return _on(stream, gated_group_norm_backward, d_output, saved, weight, bias, eps, center, activation, workspace)
     shape, dt, dev = _first("d_output", d_output, ("T", "H", "D"))
     T, H, D = shape
     dtype, where = d_output.dtype, d_output.device
@@ -420,13 +443,11 @@ def gated_group_norm_backward(d_output, saved, weight, bias=None, eps=1e-5, cent
     need = lib.gdp_group_norm_workspace_bytes(T, H, D, per_head)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=where)
-        if stream is not None:  # not to be reused before that stream has passed this call
-            workspace.record_stream(torch.cuda.ExternalStream(stream, device=where))
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         _invalid("workspace must be contiguous and on the tensors' device")
     a = _pack_norm_backward(
         d_output.data_ptr(), dt_t, dt_h, op, ot, oh, zp, zt, zh, *codes, w, b, do.data_ptr(),
         0 if dz is None else dz.data_ptr(), dw.data_ptr(), 0 if db is None else db.data_ptr(), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), T, H, D, eps, dt, int(bool(center)), per_head, _act_code(activation))
-    _finish(lib.gdp_group_norm_backward(a, _current(stream, dev)), lib)
+    _finish(lib.gdp_group_norm_backward(a, _current(dev)), lib)
     return {"do": do, "dz": dz, "dweight": dw, "dbias": db}

@@ -95,3 +95,29 @@ def test_empty_gated_batch(cuda_device, act, saved, bias):
     d = pkg.gated_group_norm_backward(y, kept if saved == "checkpoint" else (o, o.clone()), w, b, activation=act)
     assert y.shape == o.shape and d["do"].shape == o.shape and d["dz"].shape == o.shape
     assert not bool(d["dweight"].any()) and (b is None or not bool(d["dbias"].any()))
+
+
+def test_stream_argument_allocates_on_that_stream(cuda_device):
+    """What a call on a given stream allocates is not memory that the current stream has yet to write."""
+    dev, T, C = cuda_device, 2000, 128
+    x, g, cu = _rand((T, C), 1, BF16).to(dev), _gates("log", (T, C), 2, BF16).to(dev), _cu([T], dev)
+    w, z = torch.ones(64, device=dev), _rand((T, 2, 64), 3, BF16).to(dev)
+    side = torch.cuda.Stream()
+
+    def calls(**how):
+        h, fin = pkg.gated_linear_recurrence(x, g, cu, output_final_state=True, **how)
+        y, kept = pkg.gated_group_norm(x.view(T, 2, 64), w, z, save_checkpoint=True, **how)
+        d = pkg.gated_group_norm_backward(z, kept, w, **how)
+        r = pkg.gated_linear_recurrence_backward(g, x, x, cu, initial_state=torch.zeros_like(fin), **how)
+        step = pkg.gated_linear_recurrence_decode(x, g, **how)
+        return [h, fin, y, *kept.o, *kept.z, d["do"], d["dz"], d["dweight"], r["dx"], r["dg"], r["d_initial_state"], step]
+
+    want = calls()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # some 50 ms: the fills below come after the calls on the other stream
+    late = [torch.full_like(t, 77) for t in want for _ in range(3)] + [torch.full((1 << 22,), 77, dtype=torch.uint8, device=dev)]
+    del late
+    got = calls(stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
