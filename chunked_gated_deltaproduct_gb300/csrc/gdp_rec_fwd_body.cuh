@@ -68,7 +68,8 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
   cluster_sync();  // the barriers stand before anyone posts to them
 
   if (warp == kLoadWarp) {
-    const int64_t first = load_cu(s.cu, s.cu64, 0), end = min(load_cu(s.cu, s.cu64, s.N), s.T);
+    // rows [first, end) belong to sequences, whatever cu_seqlens hold: nothing outside [0, T) is written
+    const int64_t first = clamp_row(load_cu(s.cu, s.cu64, 0), s.T), end = clamp_row(load_cu(s.cu, s.cu64, s.N), s.T);
     SeqWindow win;
     win.load(s, 0, lane);
     int n = 0;

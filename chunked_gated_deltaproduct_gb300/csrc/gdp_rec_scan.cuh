@@ -317,6 +317,9 @@ __device__ __forceinline__ void find_sequences(const ScanShape &p, TileMeta<S> &
   }
 }
 
+// An entry of cu_seqlens as a row: within [0, T], so that a tile's place relative to it cannot overflow.
+__device__ __forceinline__ int64_t clamp_row(int64_t v, int64_t T) { return max((int64_t)0, min(v, T)); }
+
 // cu_seqlens ascending from 0 to at most T (any number of threads, `first` of `step`).
 __device__ __forceinline__ void check_sequences(const void *cu, int cu64, int64_t N, int64_t T, uint32_t *status, int64_t first,
                                                 int64_t step) {

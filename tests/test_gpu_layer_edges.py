@@ -1,4 +1,5 @@
 """The layer operators at the edges of their types and of what a call may be."""
+import ctypes
 import math
 
 import pytest
@@ -121,3 +122,30 @@ def test_stream_argument_allocates_on_that_stream(cuda_device):
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("cu", [[0, -2 ** 63], [0, 2 ** 63 - 1], [2 ** 63 - 1, 10], [-2 ** 63, 2 ** 63 - 1], [0, 5, -2 ** 63 + 3],
+                                [2 ** 63 - 5, 2 ** 63 - 1], [0, 300]])
+@pytest.mark.parametrize("C", [64, 61])
+def test_wild_sequence_bounds_write_nothing_outside(cuda_device, cu, C):
+    """Offsets at the ends of 64 bits are reported, and nothing but the outputs' rows is written."""
+    dev, T = cuda_device, 200
+    x = _rand((T, C), 1, BF16).to(dev)
+    cu = torch.tensor(cu, dtype=torch.int64, device=dev)
+    n = cu.numel() - 1
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    pad = 1024 * C
+    fence = {k: torch.full((2 * pad + T * C,), 7.0, dtype=BF16, device=dev) for k in ("h", "dx", "dg")}
+    inner = {k: v[pad:pad + T * C] for k, v in fence.items()}
+    pkg.gated_linear_recurrence(x, x, cu, output=inner["h"].view(T, C), device_status=st)
+    assert int(st) == pkg.GDP_DEV_ERR_CU_SEQLENS
+    st.zero_()
+    a = pkg.GdpRecurrenceBackwardArgs(
+        g=x.data_ptr(), g_stride_t=C, h=x.data_ptr(), h_stride_t=C, d_output=x.data_ptr(), d_output_stride_t=C,
+        cu_seqlens=cu.data_ptr(), T=T, N=n, C=C, dx=inner["dx"].data_ptr(), dg=inner["dg"].data_ptr(), device_status=st.data_ptr(),
+        cu_seqlens_int64=1, x_dtype=pkg.GDP_DTYPE_BF16, g_dtype=pkg.GDP_DTYPE_BF16, gate=0)
+    lib = pkg.layer._library()
+    assert lib.gdp_linear_recurrence_backward(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == pkg.GDP_OK
+    assert int(st) == pkg.GDP_DEV_ERR_CU_SEQLENS
+    for k, v in fence.items():
+        assert bool((v[:pad] == 7.0).all()) and bool((v[pad + T * C:] == 7.0).all()), k
