@@ -118,6 +118,10 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
         m.lo = (int)max((int64_t)0, min(first - t0, (int64_t)L::kTile));
         m.hi = (int)max((int64_t)0, min(end - t0, (int64_t)L::kTile));
       }
+      if (t0 + L::kTile > end && t0 >= 0) {
+        zero_rows_of<TX>(p.dx, max(end, t0), min(s.T, t0 + L::kTile), s.C, c0, lane);
+        zero_rows_of<TG>(p.dg, max(end, t0), min(s.T, t0 + L::kTile), s.C, c0, lane);
+      }
       __syncwarp();
       if (RAW || Q8) cp_async_arrive(&full[st]);
       if (lane == 0) sm100::mbar_arrive(&full[st]);

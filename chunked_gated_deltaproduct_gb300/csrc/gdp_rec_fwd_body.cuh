@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
         m.lo = (int)max((int64_t)0, min(first - t0, (int64_t)L::kTile));
         m.hi = (int)max((int64_t)0, min(end - t0, (int64_t)L::kTile));
       }
+      if (s.zero_pad && t0 + L::kTile > end) zero_rows_of<TX>(p.h, max(end, t0), min(s.T, t0 + L::kTile), s.C, c0, lane);
       __syncwarp();
       if (RAW) cp_async_arrive(&full[st]);
       if (lane == 0) sm100::mbar_arrive(&full[st]);

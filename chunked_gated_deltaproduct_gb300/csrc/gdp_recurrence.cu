@@ -139,6 +139,15 @@ gdp_status resolve(const gdp_recurrence_args *a, bool step, RecProblem *p) {
   return GDP_OK;
 }
 
+// A [T, C] output none of whose rows belongs to a sequence.
+gdp_status zero_rows(void *p, int64_t T, int64_t C, int type, cudaStream_t stream) {
+  if (T == 0) return GDP_OK;
+  const cudaError_t e = cudaMemsetAsync(p, 0, (size_t)T * (size_t)C * dtype_size(type), stream);
+  if (e == cudaSuccess) return GDP_OK;
+  set_last_error("recurrence padding rows: %s", cudaGetErrorString(e));
+  return GDP_ERR_CUDA;
+}
+
 // Set by gdp_arm_recurrence_wait_test for the calling thread's next scan.
 thread_local uint64_t armed_limit_ns = 0;
 
@@ -185,10 +194,12 @@ GDP_EXPORT gdp_status gdp_linear_recurrence(const gdp_recurrence_args *args, voi
   using namespace gdp::layer;
   RecProblem p;
   const gdp_status st = resolve(args, false, &p);
-  if (st != GDP_OK || p.N == 0) return st;
+  if (st != GDP_OK) return st;
+  if (p.N == 0) return args->zero_padding ? zero_rows(p.h, p.T, p.C, p.x_type, (cudaStream_t)stream) : GDP_OK;
   RecFwd f{};
   f.s.cu = p.cu; f.s.cu64 = p.cu64; f.s.T = p.T; f.s.N = p.N; f.s.C = p.C;
   f.s.slots = p.cache ? p.slots : nullptr; f.s.num_slots = p.num_slots; f.s.status = p.status;
+  f.s.zero_pad = args->zero_padding != 0;
   set_limits(f.s);
   f.x = {p.x, p.x_st}; f.g = {p.g, p.g_st}; f.h = p.h;
   f.from = p.cache ? p.cache : p.init;
@@ -234,7 +245,10 @@ GDP_EXPORT gdp_status gdp_linear_recurrence_backward(const gdp_recurrence_backwa
   const size_t bytes = sizeof(float) * (size_t)a->N * (size_t)a->C;
   if (overlap(a->d_final_state, a->d_initial_state, bytes) || overlap(a->initial_state, a->d_initial_state, bytes))
     return fail(GDP_ERR_ALIAS, "d_initial_state overlaps initial_state or d_final_state");
-  if (a->N == 0) return GDP_OK;
+  if (a->N == 0) {  // every row is padding
+    st = zero_rows(a->dx, a->T, a->C, a->x_dtype, (cudaStream_t)stream);
+    return st != GDP_OK ? st : zero_rows(a->dg, a->T, a->C, a->g_dtype, (cudaStream_t)stream);
+  }
   RecBwd p{};
   p.s.cu = a->cu_seqlens; p.s.cu64 = a->cu_seqlens_int64 != 0; p.s.T = a->T; p.s.N = a->N; p.s.C = a->C;
   p.s.status = a->device_status;

@@ -33,6 +33,7 @@ class GdpRecurrenceArgs(ctypes.Structure):
         ("x", _vp), ("x_stride_t", _i64), ("g", _vp), ("g_stride_t", _i64), ("output", _vp), ("cu_seqlens", _vp),
         ("T", _i64), ("N", _i64), ("C", _i64), ("initial_state", _vp), ("output_state", _vp), ("state", _vp),
         ("state_indices", _vp), ("num_slots", _i64), ("device_status", _vp), ("cu_seqlens_int64", _int), ("x_dtype", _int), ("g_dtype", _int), ("gate", _int),
+        ("zero_padding", _int),
     ]
 
 
@@ -258,7 +259,8 @@ def _recurrence(x, g, gate, cu, N, cu64, entry, first, initial_state, output_fin
     shape, xt, dev = first
     T, C = shape
     gp, gt = _rows("g", g, shape, g.dtype, dev), _gate_type(x, g)
-    if output is None:
+    own = output is None
+    if own:
         output = torch.empty_like(x, memory_format=torch.contiguous_format)
         op = output.data_ptr()
     else:
@@ -268,7 +270,7 @@ def _recurrence(x, g, gate, cu, N, cu64, entry, first, initial_state, output_fin
     lib = _library()
     a = _pack_recurrence(x.data_ptr(), x.stride(0), gp, g.stride(0), op, cu, T, N, C,
                           *_state_args(initial_state, output_state, state, state_indices, N, C, dev),
-                          _status(device_status, dev), cu64, xt, gt, _gate_code(gate))
+                          _status(device_status, dev), cu64, xt, gt, _gate_code(gate), own)
     _finish(getattr(lib, entry)(a, _current(dev)), lib)
     return (output, output_state) if output_final_state else output
 
@@ -282,7 +284,8 @@ def gated_linear_recurrence(x, g, cu_seqlens, gate="log", initial_state=None, ou
     b = (1 - a) x.  cu_seqlens [N + 1] int32 / int64.  initial_state [N, C] fp32 (None: zero), or the
     cache ``state`` [num_slots, C] fp32 read and written in place at ``state_indices`` [N] int32 (-1:
     from zero, nothing written).  Returns ``h`` [T, C] in x's type, or ``(h, final_state)`` when
-    output_final_state (dense mode; None in cache mode)."""
+    output_final_state (dense mode; None in cache mode).  Rows at or past cu_seqlens[N] (padding) are zeros;
+    in a buffer given as ``output`` they are left as they are."""
     if stream is not None:
         return _on(stream, gated_linear_recurrence, x, g, cu_seqlens, gate, initial_state, output_final_state, state,
                    state_indices, output, output_state, device_status)
@@ -310,8 +313,8 @@ def gated_linear_recurrence_backward(g, h, d_output, cu_seqlens, gate="log", x=N
     """Gradients of gated_linear_recurrence for dL/dh = ``d_output`` [T, C] and dL/dfinal =
     ``d_final_state`` [N, C] fp32 (or None).  ``h``: the forward's output [T, C] in d_output's type, or
     the ActivationCheckpoint of it that gated_group_norm kept ([T, H, D] with H D = C).  ``x`` is needed
-    for the sigmoid gate only.  Returns a dict: dx in d_output's type, dg in g's type, d_initial_state
-    fp32 (None without an initial state)."""
+    for the sigmoid gate only.  Returns a dict: dx in d_output's type, dg in g's type (both zero in rows at or
+    past cu_seqlens[N]), d_initial_state fp32 (None without an initial state)."""
     if stream is not None:
         return _on(stream, gated_linear_recurrence_backward, g, h, d_output, cu_seqlens, gate, x, initial_state, d_final_state,
                    device_status)

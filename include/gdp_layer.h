@@ -37,8 +37,9 @@ typedef enum gdp_gate {
  *
  *     h_t = a_t h_{t-1} + b_t,   h_{-1} = the incoming state,   final state = h of the last token.
  *
- * An empty sequence's final state is its incoming state.  Rows at or past cu_seqlens[N] are not
- * written.  cu_seqlens that do not ascend from 0 to at most T set GDP_DEV_ERR_CU_SEQLENS; the
+ * An empty sequence's final state is its incoming state.  Rows at or past cu_seqlens[N] (a padded
+ * batch's) are not written, or with zero_padding written as zeros; they are not read into any result.
+ * cu_seqlens that do not ascend from 0 to at most T set GDP_DEV_ERR_CU_SEQLENS; the
  * outputs are then undefined (nothing outside the buffers is touched).  A sequence's values never
  * depend on another sequence's, infinities and NaN included.  Results do not depend on scheduling:
  * every value is formed by the same operations in the same order.
@@ -70,6 +71,7 @@ typedef struct gdp_recurrence_args {
   int x_dtype; /* GDP_DTYPE_BF16, _F16 or _F32 */
   int g_dtype; /* x_dtype or GDP_DTYPE_F32 */
   int gate;    /* gdp_gate */
+  int zero_padding; /* nonzero: output rows at or past cu_seqlens[N] are written as zeros */
 } gdp_recurrence_args;
 
 gdp_status gdp_linear_recurrence(const gdp_recurrence_args *args, void *stream);
@@ -87,7 +89,8 @@ gdp_status gdp_linear_recurrence_decode(const gdp_recurrence_args *args, void *s
  * gdp_group_norm writes them for rows of h_group channels: C a multiple of h_group).  Exactly one of h
  * and h_codes is given.  x is needed for the sigmoid gate only.  The dense state mode only.  dx takes
  * x_dtype, dg g_dtype, both contiguous [T, C]; d_initial_state [N, C] fp32 or NULL (an empty sequence's
- * is its d_final_state).
+ * is its d_final_state).  dx and dg rows at or past cu_seqlens[N] are written as zeros, so that sums over
+ * all rows are those over the sequences'.
  */
 typedef struct gdp_recurrence_backward_args {
   const void *g;

@@ -149,3 +149,40 @@ def test_wild_sequence_bounds_write_nothing_outside(cuda_device, cu, C):
     assert int(st) == pkg.GDP_DEV_ERR_CU_SEQLENS
     for k, v in fence.items():
         assert bool((v[:pad] == 7.0).all()) and bool((v[pad + T * C:] == 7.0).all()), k
+
+
+# ---- rows at or past the last sequence's end (a captured batch's padding)
+def _poison(*shapes):
+    """Fills memory that the allocator will hand out again with NaN."""
+    held = [torch.full(s, math.nan, dtype=t, device="cuda") for s, t in shapes for _ in range(3)]
+    torch.cuda.synchronize()
+    del held
+
+
+@pytest.mark.parametrize("lengths,T", [([130, 77], 400), ([0, 0], 130), ([64], 65), ([], 50), ([200, 0], 200)])
+@pytest.mark.parametrize("C,xt,gt,kind", [(80, BF16, BF16, "log"), (61, F16, F32, "sigmoid"), (128, F32, F32, "log")])
+def test_padding_rows_are_zeros(cuda_device, lengths, T, C, xt, gt, kind):
+    """Of what the wrappers allocate: outputs and gradients of padding rows are zeros, so that sums over all rows
+    stay right; a caller's output buffer keeps its rows."""
+    dev, n = cuda_device, sum(lengths)
+    x, g, dh = _rand((T, C), 1, xt).to(dev), _gates(kind, (T, C), 2, gt).to(dev), _rand((T, C), 3, xt).to(dev)
+    x[n:], g[n:], dh[n:] = math.nan, math.nan, math.nan
+    cu = _cu(lengths, dev)
+    _poison(((T, C), xt), ((T, C), gt))
+    h = pkg.gated_linear_recurrence(x, g, cu, gate=kind)
+    assert not bool(h[n:].any())
+    d = pkg.gated_linear_recurrence_backward(g, h, dh, cu, gate=kind, x=x if kind == "sigmoid" else None)
+    assert not bool(d["dx"][n:].any()) and not bool(d["dg"][n:].any())
+    if n:
+        rh, _, eh, _ = R.recurrence(x.cpu()[:n], g.cpu()[:n], lengths, kind)
+        R.check(h[:n], rh, eh, "h")
+        dx, dg, _, ex, eg, _ = R.recurrence_backward(g.cpu()[:n], h.cpu()[:n], dh.cpu()[:n], lengths, kind, x.cpu()[:n])
+        R.check(d["dx"][:n], dx, ex, "dx")
+        R.check(d["dg"][:n], dg, eg + 2.0 ** -23 * dg.abs(), "dg")
+    out = torch.full((T, C), 9.0, dtype=xt, device=dev)
+    assert pkg.gated_linear_recurrence(x, g, cu, gate=kind, output=out) is out
+    assert bool((out[n:] == 9.0).all()) and torch.equal(out[:n], h[:n])
+    # behind it the norm, whose weight gradient sums over all rows
+    y, kept = pkg.gated_group_norm(h.view(T, 1, C), torch.ones(C, device=dev), save_checkpoint=True)
+    dy = torch.zeros((T, 1, C), dtype=xt, device=dev)
+    assert bool(torch.isfinite(pkg.gated_group_norm_backward(dy, kept, torch.ones(C, device=dev))["dweight"]).all())
