@@ -115,6 +115,9 @@ gdp_status check_rows(const void *p, int64_t stride, int64_t T, int64_t C, int t
   return GDP_OK;
 }
 
+// The stride of a single row means nothing and may be anything in a view (a tensor map refuses 0): one that fits.
+int64_t row_stride(int64_t stride, int64_t T, int64_t C) { return T > 1 ? stride : (C + 15) / 16 * 16; }
+
 gdp_status resolve(const gdp_recurrence_args *a, bool step, RecProblem *p) {
   set_last_error("");
   if (!a) return fail(GDP_ERR_INVALID_ARG, "args is NULL");
@@ -133,7 +136,7 @@ gdp_status resolve(const gdp_recurrence_args *a, bool step, RecProblem *p) {
     return fail(GDP_ERR_INVALID_ARG, "the state cache needs state_indices and num_slots >= 1");
   if (partly_overlap(a->initial_state, a->output_state, sizeof(float) * (size_t)a->N * (size_t)a->C))
     return fail(GDP_ERR_ALIAS, "output_state partly overlaps initial_state");
-  *p = RecProblem{a->x, a->g, a->x_stride_t, a->g_stride_t, a->output, a->cu_seqlens, a->cu_seqlens_int64 != 0, a->T, a->N, a->C,
+  *p = RecProblem{a->x, a->g, row_stride(a->x_stride_t, a->T, a->C), row_stride(a->g_stride_t, a->T, a->C), a->output, a->cu_seqlens, a->cu_seqlens_int64 != 0, a->T, a->N, a->C,
                   a->initial_state, a->output_state, a->state, a->state_indices, a->num_slots, a->device_status,
                   a->x_dtype, a->g_dtype, a->gate};
   return GDP_OK;
@@ -253,7 +256,9 @@ GDP_EXPORT gdp_status gdp_linear_recurrence_backward(const gdp_recurrence_backwa
   p.s.cu = a->cu_seqlens; p.s.cu64 = a->cu_seqlens_int64 != 0; p.s.T = a->T; p.s.N = a->N; p.s.C = a->C;
   p.s.status = a->device_status;
   set_limits(p.s);
-  p.g = {a->g, a->g_stride_t}; p.x = {a->x, a->x_stride_t}; p.h = {a->h, a->h_stride_t}; p.dout = {a->d_output, a->d_output_stride_t};
+  auto rows_of = [&](const void *at, int64_t stride) { return RowSource{at, row_stride(stride, a->T, a->C)}; };
+  p.g = rows_of(a->g, a->g_stride_t); p.x = rows_of(a->x, a->x_stride_t);
+  p.h = rows_of(a->h, a->h_stride_t); p.dout = rows_of(a->d_output, a->d_output_stride_t);
   p.codes = {a->h_codes, a->C};
   p.scales = a->h_scales;
   p.group = a->h_codes ? a->h_group : 1;

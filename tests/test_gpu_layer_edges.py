@@ -186,3 +186,16 @@ def test_padding_rows_are_zeros(cuda_device, lengths, T, C, xt, gt, kind):
     y, kept = pkg.gated_group_norm(h.view(T, 1, C), torch.ones(C, device=dev), save_checkpoint=True)
     dy = torch.zeros((T, 1, C), dtype=xt, device=dev)
     assert bool(torch.isfinite(pkg.gated_group_norm_backward(dy, kept, torch.ones(C, device=dev))["dweight"]).all())
+
+
+def test_one_row_of_any_stride(cuda_device):
+    """A single row's stride means nothing, whatever the view says."""
+    dev, C = cuda_device, 128
+    x, g = _rand((1, C), 1, BF16), _gates("log", (1, C), 2, BF16)
+    rh, rfin, eh, efin = R.recurrence(x, g, [1], "log")
+    for stride in (0, 1, 8, 64, 1 << 40):
+        lay = lambda t: t.to(dev).as_strided((1, C), (stride, 1))  # noqa: E731
+        R.check(pkg.gated_linear_recurrence(lay(x), lay(g), _cu([1], dev)), rh, eh, f"h, stride {stride}")
+        R.check(pkg.gated_linear_recurrence_decode(lay(x), lay(g)), rh, eh, f"step, stride {stride}")
+        d = pkg.gated_linear_recurrence_backward(lay(g), lay(x), lay(x), _cu([1], dev))
+        assert torch.equal(d["dx"].cpu(), x) and not bool(d["dg"].any())
