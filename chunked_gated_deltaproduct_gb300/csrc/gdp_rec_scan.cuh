@@ -167,15 +167,15 @@ __device__ __forceinline__ float2 unpack(typename Packed<T>::type v) {
 }
 
 // Both channels' gates in two steps: what stays in registers between the two runs over a tile (the decay;
-// for the sigmoid e^-g, held to 2^115, from which either half follows to its own relative precision), and
-// decay and input factor from it.
+// for the sigmoid e^-g, held to 2^125, from which either half follows to its own relative precision: the decay
+// stays above 2^-125, next to the end of fp32, and the factor is 1), and decay and input factor from it.
 template <int GATE>
 __device__ __forceinline__ float2 gate_kept(float2 g) {
   if constexpr (GATE == GDP_GATE_ALPHA) return g;
   float2 t = mul2(g, both(GATE == GDP_GATE_LOG ? kLog2e : -kLog2e));
   if constexpr (GATE == GDP_GATE_SIGMOID) {
-    asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(t.x));
-    asm("min.NaN.f32 %0, %0, 0f42E60000;" : "+f"(t.y));
+    asm("min.NaN.f32 %0, %0, 0f42FA0000;" : "+f"(t.x));
+    asm("min.NaN.f32 %0, %0, 0f42FA0000;" : "+f"(t.y));
   }
   return make_float2(ex2(t.x), ex2(t.y));
 }

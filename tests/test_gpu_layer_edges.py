@@ -199,3 +199,28 @@ def test_one_row_of_any_stride(cuda_device):
         R.check(pkg.gated_linear_recurrence_decode(lay(x), lay(g)), rh, eh, f"step, stride {stride}")
         d = pkg.gated_linear_recurrence_backward(lay(g), lay(x), lay(x), _cu([1], dev))
         assert torch.equal(d["dx"].cpu(), x) and not bool(d["dg"].any())
+
+
+# a value below fp32's smallest normal number may be held as zero, at any token
+SMALL = 2.0 ** -125
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("C", [64, 37])
+def test_gate_logits_at_the_lowest_value(cuda_device, dt, C):
+    """A sigmoid gate closed by a mask: the state is dropped, the input taken whole, no gradient to the logit."""
+    dev, T = cuda_device, 300
+    x, dh, s0 = _rand((T, C), 1, dt), _rand((T, C), 4, dt), _rand((1, C), 3)
+    g = _gates("sigmoid", (T, C), 2, dt)
+    for t, v in ((5, torch.finfo(dt).min), (17, -1e4), (18, -90.0), (140, torch.finfo(dt).min), (299, -1e30)):
+        g[t] = v
+        x[t] = 0.0
+    h, fin = pkg.gated_linear_recurrence(x.to(dev), g.to(dev), _cu([T], dev), gate="sigmoid", initial_state=s0.to(dev), output_final_state=True)
+    rh, rfin, eh, efin = R.recurrence(x, g, [T], "sigmoid", s0)
+    # sigmoid(g) below 2^-125 may come out as that
+    R.check(h, rh, eh + SMALL * (1 + rh.abs().max()), "h")
+    R.check(fin, rfin, efin + SMALL * (1 + rh.abs().max()), "final")
+    d = pkg.gated_linear_recurrence_backward(g.to(dev), h, dh.to(dev), _cu([T], dev), gate="sigmoid", x=x.to(dev), initial_state=s0.to(dev))
+    dx, dg, dinit, ex, eg, einit = R.recurrence_backward(g, h.cpu(), dh, [T], "sigmoid", x, s0)
+    R.check(d["dx"], dx, ex + 1e3 * SMALL, "dx")
+    R.check(d["dg"], dg, eg + 2.0 ** -23 * dg.abs() + 1e3 * SMALL * (1 + rh.abs().max()), "dg")
