@@ -29,12 +29,12 @@ struct BwdLayout {
   static constexpr int x_off = s_off + (Q8 ? (kTile * 4 + 127) / 128 * 128 : 0);
   static constexpr int stage = x_off + (kX ? tile_bytes<TX>(kTile, RAW) : 0);
   static constexpr int kMeta = kStages + 1;
-  static constexpr int parts = kStages * stage, enter = parts + Chain::parts_bytes, meta = enter + Chain::enter_bytes;
+  static constexpr int parts = kStages * stage, parts_m = parts + Chain::parts_bytes, parts_e = parts_m + Chain::parts_m_bytes, enter = parts_e + Chain::parts_e_bytes, meta = enter + Chain::enter_bytes;
   static constexpr int bars = (meta + kMeta * (int)sizeof(TileMeta<S>) + 15) / 16 * 16;
   static constexpr int mail = (bars + (2 * kStages + Chain::bars) * 8 + 16 + 127) / 128 * 128;  // last: its size is the cluster's
   // TMA destinations, 16-byte arrays, barriers, and the largest cluster's whole
   static_assert(g_off % 128 == 0 && d_off % 128 == 0 && h_off % 128 == 0 && x_off % 128 == 0 && s_off % 4 == 0 && S * kSlice * sizeof(TX) % 128 == 0 && S * kSlice * sizeof(TG) % 128 == 0 && stage % 128 == 0, "TMA reads and writes at 128-byte boundaries");
-  static_assert(parts % 16 == 0 && enter % 16 == 0 && meta % 4 == 0 && bars % 8 == 0 && mail % 16 == 0, "alignment");
+  static_assert(parts % 16 == 0 && parts_m % 8 == 0 && parts_e % 4 == 0 && enter % 16 == 0 && meta % 4 == 0 && bars % 8 == 0 && mail % 16 == 0, "alignment");
   static_assert(mail + Chain::mail_bytes(RAW ? 8 : 16) <= kScanSmem && mail + Chain::mail_bytes(16) <= 227 * 1024, "two CTAs per SM");
 };
 
@@ -52,11 +52,16 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::bars), *empty = full + L::kStages;
   Chain ch;
   ch.parts = reinterpret_cast<float4 *>(smem + L::parts);
+  ch.parts_m = reinterpret_cast<float2 *>(smem + L::parts_m);
+  ch.parts_e = reinterpret_cast<int *>(smem + L::parts_e);
   ch.enter = reinterpret_cast<float2 *>(smem + L::enter);
   ch.mail = reinterpret_cast<float4 *>(smem + L::mail);
+  ch.wide_mail = reinterpret_cast<int2 *>(ch.mail + kMailSlots * p.s.cluster * 32);
   ch.parts_full = empty + L::kStages;
-  ch.enter_full = ch.parts_full + 1;
-  ch.mail_full = ch.enter_full + 1;
+  ch.products_full = ch.parts_full + 1;
+  ch.enter_full = ch.products_full + 1;
+  ch.wide_full = ch.enter_full + 1;
+  ch.mail_full = ch.wide_full + 1;
   volatile int *gave_up = reinterpret_cast<volatile int *>(ch.mail_full + kMailSlots);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const ScanShape &s = p.s;
@@ -72,7 +77,9 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
       sm100::mbar_init(&empty[i], kScanWarps);
     }
     sm100::mbar_init(ch.parts_full, kScanWarps);
+    sm100::mbar_init(ch.products_full, kScanWarps);
     sm100::mbar_init(ch.enter_full, 1);
+    sm100::mbar_init(ch.wide_full, 1);
     for (int i = 0; i < kMailSlots; ++i) sm100::mbar_init(&ch.mail_full[i], 1);
     *gave_up = 0;
     sm100::mbar_init_fence();
@@ -129,7 +136,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
     if (*gave_up) drain_loads<L::kStages>(full, n, RAW || Q8);
     if (blockIdx.x == 0) check_sequences(s.cu, s.cu64, s.N, s.T, s.status, lane, 32);
   } else if (warp == kChainWarp) {
-    chain_steps<S, L::kMeta, true>(s, ch, metas, steps, lane, gave_up);
+    chain_steps<S, L::kMeta>(s, ch, metas, steps, lane, gave_up);
   } else {
     const int64_t c = c0 + 2 * lane;
     // dx and dg take the places of d_output and g in the stage and leave by TMA stores (each warp its own
@@ -152,10 +159,12 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
       };
       float2 kept[S];  // gates
       float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
+      LargestGate<TG, GATE> largest;
 #pragma unroll
       for (int i = S - 1; i >= 0; --i) {
-        kept[i] = gate_kept<GATE>(
-            unpack<TG>(read_packed<TG, RAW>(base + L::g_off, block * S + i, lane, RAW ? raw_offset<TG>(p.g, t0 + i, c0) : 0)));
+        const auto g = read_packed<TG, RAW>(base + L::g_off, block * S + i, lane, RAW ? raw_offset<TG>(p.g, t0 + i, c0) : 0);
+        largest.see(g);
+        kept[i] = gate_kept<GATE>(unpack<TG>(g));
         float2 f;
         const float2 a = gate_decay<GATE>(kept[i], &f);
         A = mul2(A, a);
@@ -171,7 +180,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
           B = mul2(gate_decay<GATE>(kept[i], &f), add2(upstream(i), B));
         }
       }
-      ch.parts[warp * 32 + lane] = make_float4(A.x, A.y, B.x, B.y);
+      const bool unsafe = write_part(ch, warp * 32 + lane, A, B, largest, ends != 0u || hi <= 0);
       __syncwarp();
       if (lane == 0) {
         sm100::mbar_arrive(ch.parts_full);
@@ -180,6 +189,10 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
           sm100::mbar_arrive(&empty[(n - 1) % L::kStages]);
         }
       }
+      if (unsafe)
+        write_products<TG, GATE, RAW, S>(ch.parts_m + warp * 32 + lane, ch.parts_e + warp * 32 + lane, base + L::g_off, block * S, lane, p.g, t0, c0);
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(ch.products_full);
       if (!ring_wait(ch.enter_full, n & 1, gave_up, s.status, s.limit_ns)) break;
       keep_only<S>(kept);
       float2 E = ch.enter[warp * 32 + lane];

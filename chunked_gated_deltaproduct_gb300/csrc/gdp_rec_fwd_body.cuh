@@ -23,12 +23,12 @@ struct FwdLayout {
   static constexpr int x_off = 0, g_off = tile_bytes<TX>(kTile, RAW), stage = g_off + tile_bytes<TG>(kTile, RAW);
   static constexpr int kMeta = kStages + 1;
   static constexpr int out = kStages * stage, out_bytes = RAW ? 0 : kTile * kSlice * (int)sizeof(TX);
-  static constexpr int parts = out + out_bytes, enter = parts + Chain::parts_bytes, meta = enter + Chain::enter_bytes;
+  static constexpr int parts = out + out_bytes, parts_m = parts + Chain::parts_bytes, parts_e = parts_m + Chain::parts_m_bytes, enter = parts_e + Chain::parts_e_bytes, meta = enter + Chain::enter_bytes;
   static constexpr int bars = (meta + kMeta * (int)sizeof(TileMeta<S>) + 15) / 16 * 16;
   static constexpr int mail = (bars + (2 * kStages + Chain::bars) * 8 + 16 + 127) / 128 * 128;  // last: its size is the cluster's
   // TMA destinations, 16-byte arrays, barriers, and the largest cluster's whole
   static_assert(x_off % 128 == 0 && g_off % 128 == 0 && out % 128 == 0 && S * kSlice * sizeof(TX) % 128 == 0 && stage % 128 == 0, "TMA writes to 128-byte boundaries");
-  static_assert(parts % 16 == 0 && enter % 16 == 0 && meta % 4 == 0 && bars % 8 == 0 && mail % 16 == 0, "alignment");
+  static_assert(parts % 16 == 0 && parts_m % 8 == 0 && parts_e % 4 == 0 && enter % 16 == 0 && meta % 4 == 0 && bars % 8 == 0 && mail % 16 == 0, "alignment");
   static_assert(mail + Chain::mail_bytes(RAW ? 8 : 16) <= kScanSmem && mail + Chain::mail_bytes(16) <= 227 * 1024, "two CTAs per SM");
 };
 
@@ -43,11 +43,16 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::bars), *empty = full + L::kStages;
   Chain ch;
   ch.parts = reinterpret_cast<float4 *>(smem + L::parts);
+  ch.parts_m = reinterpret_cast<float2 *>(smem + L::parts_m);
+  ch.parts_e = reinterpret_cast<int *>(smem + L::parts_e);
   ch.enter = reinterpret_cast<float2 *>(smem + L::enter);
   ch.mail = reinterpret_cast<float4 *>(smem + L::mail);
+  ch.wide_mail = reinterpret_cast<int2 *>(ch.mail + kMailSlots * p.s.cluster * 32);
   ch.parts_full = empty + L::kStages;
-  ch.enter_full = ch.parts_full + 1;
-  ch.mail_full = ch.enter_full + 1;
+  ch.products_full = ch.parts_full + 1;
+  ch.enter_full = ch.products_full + 1;
+  ch.wide_full = ch.enter_full + 1;
+  ch.mail_full = ch.wide_full + 1;
   volatile int *gave_up = reinterpret_cast<volatile int *>(ch.mail_full + kMailSlots);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const ScanShape &s = p.s;
@@ -59,7 +64,9 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
       sm100::mbar_init(&empty[i], kScanWarps);
     }
     sm100::mbar_init(ch.parts_full, kScanWarps);
+    sm100::mbar_init(ch.products_full, kScanWarps);
     sm100::mbar_init(ch.enter_full, 1);
+    sm100::mbar_init(ch.wide_full, 1);
     for (int i = 0; i < kMailSlots; ++i) sm100::mbar_init(&ch.mail_full[i], 1);
     *gave_up = 0;
     sm100::mbar_init_fence();
@@ -100,7 +107,7 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
     if (*gave_up) drain_loads<L::kStages>(full, n, RAW);
     if (blockIdx.x == 0) check_sequences(s.cu, s.cu64, s.N, s.T, s.status, lane, 32);
   } else if (warp == kChainWarp) {
-    chain_steps<S, L::kMeta, false>(s, ch, metas, steps, lane, gave_up);
+    chain_steps<S, L::kMeta>(s, ch, metas, steps, lane, gave_up);
   } else {
     const int64_t c = c0 + 2 * lane;
     // outputs leave through shared memory and TMA stores (each warp its own rows), so that a warp does not
@@ -119,14 +126,16 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
       // the decay's place takes the state after that token.
       float2 a[S], b[L::kKeep ? S : 1];
       float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
+      LargestGate<TG, GATE> largest;
       auto read_x = [&](int i) {
         return unpack<TX>(read_packed<TX, RAW>(xs, warp * S + i, lane, RAW ? raw_offset<TX>(p.x, t0 + i, c0) : 0));
       };
 #pragma unroll
       for (int i = 0; i < S; ++i) {
         float2 f;
-        a[i] = gate_decay<GATE>(
-            gate_kept<GATE>(unpack<TG>(read_packed<TG, RAW>(gs, warp * S + i, lane, RAW ? raw_offset<TG>(p.g, t0 + i, c0) : 0))), &f);
+        const auto g = read_packed<TG, RAW>(gs, warp * S + i, lane, RAW ? raw_offset<TG>(p.g, t0 + i, c0) : 0);
+        largest.see(g);
+        a[i] = gate_decay<GATE>(gate_kept<GATE>(unpack<TG>(g)), &f);
         const float2 x = GATE == GDP_GATE_SIGMOID ? mul2(f, read_x(i)) : read_x(i);
         if constexpr (L::kKeep) b[i] = x;
         B = fma2(a[i], B, x);
@@ -145,14 +154,19 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
           if (starts >> i & 1u) a[i] = B;
         }
       }
-      ch.parts[warp * 32 + lane] = make_float4(A.x, A.y, B.x, B.y);
+      const bool unsafe = write_part(ch, warp * 32 + lane, A, B, largest, starts != 0u || hi <= 0);
       __syncwarp();
       if (lane == 0) {
         sm100::mbar_arrive(ch.parts_full);
-        if (L::kKeep) sm100::mbar_arrive(&empty[st]);
         sm100::bulk_wait_read<0>();  // the last tile's store has read `mine`
       }
+      if (unsafe)
+        write_products<TG, GATE, RAW, S>(ch.parts_m + warp * 32 + lane, ch.parts_e + warp * 32 + lane, gs, warp * S, lane, p.g, t0, c0);
       __syncwarp();
+      if (lane == 0) {
+        sm100::mbar_arrive(ch.products_full);
+        if (L::kKeep) sm100::mbar_arrive(&empty[st]);
+      }
       if (!ring_wait(ch.enter_full, n & 1, gave_up, s.status, s.limit_ns)) break;
       keep_only<S>(a);
       // ---- from the entering state.  Four tokens' inputs are read before their outputs are written (the

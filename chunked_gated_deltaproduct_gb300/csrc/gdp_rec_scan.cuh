@@ -23,6 +23,9 @@
 // where sequences begin and end inside the tiles (64 packed requests x 2048, 83 steps).
 #pragma once
 
+#include <climits>
+#include <type_traits>
+
 #include <cuda.h>
 
 #include "gdp_layer.cuh"
@@ -55,6 +58,7 @@ struct ScanShape {
 template <int S>
 struct TileMeta {
   int lo, hi;                     // rows of the tile that belong to sequences
+  uint32_t fresh;                 // bit w: in the chain's w-th warp a sequence begins (going back in time: ends)
   uint32_t starts[kScanWarps], ends[kScanWarps];  // per warp: its tokens that begin / end a sequence
   int start_row[kScanWarps * S], end_row[kScanWarps * S];  // state row of that sequence, -1: none
 };
@@ -316,6 +320,10 @@ __device__ __forceinline__ void find_sequences(const ScanShape &p, TileMeta<S> &
       win.load(p, max((int64_t)0, win.base - 32), lane);
     }
   }
+  __syncwarp();
+  const uint32_t cuts = lane < kScanWarps ? (REV ? m.ends[kScanWarps - 1 - lane] : m.starts[lane]) : 0u;
+  const uint32_t fresh = __ballot_sync(0xffffffffu, cuts != 0u);
+  if (lane == 0) m.fresh = fresh;
 }
 
 // An entry of cu_seqlens as a row: within [0, T], so that a tile's place relative to it cannot overflow.
@@ -343,17 +351,95 @@ __device__ __forceinline__ void check_sequences(const void *cu, int cu64, int64_
   }
 }
 
+// ---- products of decays beyond fp32 ----
+// A run's product A of decays may leave fp32's range though no state does: decays of 2 over 128 tokens while the
+// state is zero, decays of 0.4 under an infinite state, a rise and its undoing.  The definition never forms such a
+// product.  A plain product is right where no decay is above 2^(1/8), so that a tile's rises by 2^16 at most, and it
+// ends above 2^-110, so that no part of it was below 2^-126; and where it ends below that it is right enough for a
+// state of at most 64 (it is off by 2^16 times 2^-149, the state by less than 2^-126).  Everything else goes as A 2^e:
+// with e = 0 and A plain where the whole is a normal number, else with A in [1, 2) in magnitude (a decay of
+// exactly zero, infinity or NaN: itself, e = 0).  Which form a channel's product takes depends on its own tokens and
+// state, and not on what its neighbours need.
+constexpr float kNormal = 0x1p-126f, kMost = 0x1.fffffep127f;  // fp32's normal numbers
+constexpr float kSafe = 0x1p-110f, kLargeState = 64.f;
+
+// v as m 2^e with 1 <= |m| < 2; zero, infinity and NaN are themselves (e = 0).
+__device__ __forceinline__ float split(float v, int &e) {
+  e = 0;
+  uint32_t b = __float_as_uint(v);
+  if ((b & 0x7fffffffu) == 0u || (b & 0x7f800000u) == 0x7f800000u) return v;
+  if ((b & 0x7f800000u) == 0u) {
+    b = __float_as_uint(v * 0x1p24f);
+    e = -24;
+  }
+  e += (int)(b >> 23 & 255u) - 127;
+  return __uint_as_float((b & 0x807fffffu) | 0x3f800000u);
+}
+__device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 <= e <= 127
+__device__ __forceinline__ bool outside(float A) { return !(fabsf(A) >= kNormal && fabsf(A) <= kMost); }
+struct WideProduct {
+  float m;  // a product of numbers of split (up to 16 before settle)
+  int e;
+  __device__ __forceinline__ void times(float v, int k) {  // by v 2^k
+    int i;
+    m *= split(v, i);
+    e += i + k;
+  }
+  __device__ __forceinline__ void settle() {
+    int i;
+    m = split(m, i);
+    e = outside(m) ? 0 : e + i;
+    if (e >= -126 && e <= 127) {
+      m *= power2(e);
+      e = 0;
+    }
+  }
+};
+__device__ __forceinline__ int pack_exponents(int x, int y) { return (x & 0xffff) | y << 16; }
+__device__ __forceinline__ int low_exponent(int v) { return (int)(short)(v & 0xffff); }
+__device__ __forceinline__ int high_exponent(int v) { return v >> 16; }
+// A 2^e as it is used: two factors, applied one after the other, so that only the result can leave the range (beyond
+// 2^-252 and 2^254 any normal state gives zero or infinity alike).
+struct Factors {
+  float a, b;
+  __device__ __forceinline__ Factors(float A, int e) {
+    e = max(-252, min(e, 254));
+    a = A * power2(e / 2);
+    b = power2(e - e / 2);
+  }
+  __device__ __forceinline__ float apply(float h, float add) const { return b == 1.f ? fmaf(a, h, add) : fmaf(a * h, b, add); }
+};
+// A 2^e in 32 bits, a sign, nine bits of exponent and 22 of fraction: half a unit is 2^-23 of a product that has
+// itself been rounded as often as it has factors.  Only products below 2^-110 or beyond fp32 are read back from it.
+__device__ __forceinline__ uint32_t wide_code(float A, int e) {
+  const uint32_t b = __float_as_uint(A);
+  if (outside(A)) return A == 0.f ? 0u : (b & 0x80000000u) | 511u << 22 | (A != A ? 1u : 0u);
+  return (b & 0x80000000u) | (((uint32_t)(max(-252, min(e + (int)(b >> 23 & 255u) - 127, 253)) + 256) << 22) + (((b & 0x7fffffu) + 1u) >> 1));
+}
+__device__ __forceinline__ Factors wide_factors(uint32_t code) {
+  const int e = (int)(code >> 22 & 511u) - 256;
+  const uint32_t sign = code & 0x80000000u;
+  if (e == 255) return Factors(__uint_as_float(sign | 0x7f800000u | (code & 1u) << 22), 0);
+  if (e == -256) return Factors(__uint_as_float(sign), 0);
+  return Factors(__uint_as_float(sign | 0x3f800000u | (code & 0x3fffffu) << 1), e);
+}
+
 // ---- the chain through the cluster ----
-// Per-CTA shared memory of the chain: parts (A0, A1, B0, B1 of a lane's two channels) and entering
-// states per warp; mail, two steps of one part per CTA of the cluster.
+// Per-CTA shared memory of the chain: parts (A0, A1, B0, B1 of a lane's two channels) and entering states per
+// warp; mail, two steps of one part per CTA of the cluster.  A part whose A0 is a NaN has A0 and A1, and their
+// exponents, in parts_m and parts_e, complete on a barrier of their own.  A second mail brings a tile's products
+// outside fp32, in the steps that need them.
 struct Chain {
   float4 *parts;    // [kScanWarps][32]
+  float2 *parts_m;  // [kScanWarps][32]
+  int *parts_e;     // [kScanWarps][32]
   float2 *enter;    // [kScanWarps][32]
   float4 *mail;     // [kMailSlots][cluster][32]
-  uint64_t *parts_full, *enter_full, *mail_full;  // the last: [kMailSlots]
-  static constexpr int parts_bytes = kScanWarps * 32 * 16, enter_bytes = kScanWarps * 32 * 8;
-  __host__ __device__ static constexpr int mail_bytes(int cluster) { return kMailSlots * cluster * 32 * 16; }
-  static constexpr int bars = 2 + kMailSlots;
+  int2 *wide_mail;  // [cluster][32], behind it
+  uint64_t *parts_full, *products_full, *enter_full, *wide_full, *mail_full;  // the last: [kMailSlots]
+  static constexpr int parts_bytes = kScanWarps * 32 * 16, parts_m_bytes = kScanWarps * 32 * 8, parts_e_bytes = kScanWarps * 32 * 4, enter_bytes = kScanWarps * 32 * 8;
+  __host__ __device__ static constexpr int mail_bytes(int cluster) { return cluster * 32 * (kMailSlots * 16 + 8); }
+  static constexpr int bars = 4 + kMailSlots;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -372,6 +458,10 @@ __device__ __forceinline__ uint32_t in_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void post16(uint32_t addr, float4 v, uint32_t bar) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
                "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)), "r"(__float_as_uint(v.w)), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void post8(uint32_t addr, int2 v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(bar)
                : "memory");
 }
 // In the place of A where a sequence begins in the tile, so that its end state is B whatever enters
@@ -407,60 +497,230 @@ __device__ __forceinline__ void leave_cluster(volatile int *gave_up) {
   }
 }
 
+// Whether some decay of a lane's run is above 2^(1/8) (or a NaN), from the gates as they are stored, compared as
+// integers (log gates: above 0.0866); a sigmoid's never are.
+template <typename TG, int GATE>
+struct LargestGate {
+  static constexpr bool kWord = sizeof(TG) == 2;  // two channels in a word
+  static constexpr bool kHalf = std::is_same<TG, __half>::value;
+  static constexpr int kTop = GATE == GDP_GATE_LOG ? (!kWord ? 0x3db15b57 : kHalf ? 0x2d8b : 0x3db1) : (!kWord ? 0x3f8b95c1 : kHalf ? 0x3c5c : 0x3f8b);
+  static constexpr int kMask = GATE == GDP_GATE_LOG ? -1 : kWord ? 0x7fff7fff : 0x7fffffff;
+  int x = kWord ? (int)0x80008000u : INT_MIN, y = INT_MIN;
+  __device__ __forceinline__ void see(typename Packed<TG>::type v) {
+    if constexpr (GATE != GDP_GATE_SIGMOID) {
+      if constexpr (kWord) {
+        asm("max.s16x2 %0, %0, %1;" : "+r"(x) : "r"((int)v & kMask));
+      } else {
+        x = max(x, __float_as_int(v.x) & kMask);
+        y = max(y, __float_as_int(v.y) & kMask);
+      }
+    }
+  }
+  __device__ __forceinline__ bool rises() const {
+    if constexpr (GATE == GDP_GATE_SIGMOID) return false;
+    else if constexpr (kWord) return max((int)(short)(x & 0xffff), x >> 16) > kTop;
+    else return max(x, y) > kTop;
+  }
+};
+// The products of S decays of a lane that is not safe, read again from the tile (out of line: few tiles come here).
+template <typename TG, int GATE, bool RAW, int S>
+__device__ __noinline__ void write_products(float2 *m, int *e, const unsigned char *gs, int row, int lane, RowSource src, int64_t t0, int64_t c0) {
+  WideProduct x{1.f, 0}, y{1.f, 0};
+#pragma unroll 1
+  for (int i = 0; i < S; ++i) {
+    float2 f;
+    const float2 a = gate_decay<GATE>(gate_kept<GATE>(unpack<TG>(read_packed<TG, RAW>(gs, row + i, lane, RAW ? raw_offset<TG>(src, t0 + i, c0) : 0))), &f);
+    x.times(a.x, 0);
+    y.times(a.y, 0);
+  }
+  x.settle();
+  y.settle();
+  *m = make_float2(x.m, y.m);
+  *e = pack_exponents(x.e, y.e);
+}
+// A computing warp, after its first run: writes its part, and says whether the lane's products have to follow (see
+// write_products).  `cut`: a sequence begins among the tokens, or none of them belongs to one, and A is not used.
+template <typename TG, int GATE>
+__device__ __forceinline__ bool write_part(const Chain &ch, int at, float2 A, float2 B, const LargestGate<TG, GATE> &largest, bool cut) {
+  const bool unsafe = !cut && (largest.rises() || !(fabsf(A.x) >= kSafe && fabsf(A.y) >= kSafe));
+  ch.parts[at] = make_float4(cut ? 1.f : unsafe ? __uint_as_float(0x7fffffffu) : A.x, cut ? 1.f : A.y, B.x, B.y);
+  return unsafe;
+}
+// A part, its exponents brought in.
+__device__ __forceinline__ float4 read_part(const Chain &ch, int at, int &e) {
+  float4 q = ch.parts[at];
+  e = 0;
+  if (q.x != q.x) {
+    const float2 m = ch.parts_m[at];
+    q.x = m.x;
+    q.y = m.y;
+    e = ch.parts_e[at];
+  }
+  return q;
+}
+
+// The cluster's tiles in order of time from the state h that enters the step, by plain products: the states that enter
+// this CTA's tile and the next step, and whether those hold for this lane (every CTA finds the same).
+struct StepStates {
+  float2 enter, next;
+  bool holds;
+};
+__device__ __forceinline__ StepStates plain_states(const float4 *mail, int cluster, int rank, int lane, float2 h) {
+  float2 e = h;
+  float least = kMost, most = 0.f, state = 0.f;
+  for (int k0 = 0; k0 < cluster; k0 += 4) {
+    float4 t[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (k0 + u < cluster) t[u] = mail[(k0 + u) * 32 + lane];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (k0 + u >= cluster) break;
+      if (k0 + u == rank) e = h;
+      least = fminf(least, fminf(fabsf(t[u].x), fabsf(t[u].y)));  // (a cut tile has a NaN and a one)
+      most = fmaxf(most, fmaxf(fabsf(t[u].x), fabsf(t[u].y)));
+      state = fmaxf(state, fmaxf(fabsf(h.x), fabsf(h.y)));
+      h = __float_as_uint(t[u].x) == kCut ? make_float2(t[u].z, t[u].w) : make_float2(fmaf(t[u].x, h.x, t[u].z), fmaf(t[u].y, h.y, t[u].w));
+    }
+  }
+  return StepStates{e, h, most <= kMost && (least >= kSafe || state <= kLargeState)};
+}
+
+// The chaining warp's step where plain products do not hold, out of line: before this CTA's mail is posted, when a part
+// of its tile is not plain, or after (`posted`), when the cluster's mail shows that products outside fp32 matter.  Those
+// come in a second mail, posted once the first has come, so that every CTA has read the step before's.
+struct WideStep {
+  float2 h;
+  uint32_t phase;  // of the second mail
+  bool ok;         // no wait ran out
+};
+static __device__ __noinline__ WideStep wide_step(Chain ch, int cluster, uint32_t *status, uint64_t limit_ns, uint32_t fresh, int n, int lane, float2 h, bool posted,
+                                                  uint32_t phase, volatile int *gave_up) {
+  const int rank = (int)cluster_rank(), slot = n % kMailSlots;
+  if (!ring_wait(ch.products_full, n & 1, gave_up, status, limit_ns)) return WideStep{h, phase, false};
+  WideProduct x{1.f, 0}, y{1.f, 0};
+  float2 B = make_float2(0.f, 0.f), A = both(1.f);  // A: as chain_steps has it
+#pragma unroll 2
+  for (int w = 0; w < kScanWarps; ++w) {
+    int e;
+    const float4 raw = ch.parts[w * 32 + lane], q = read_part(ch, w * 32 + lane, e);
+    A = make_float2(A.x * raw.x, A.y * raw.y);
+    x.times(q.x, low_exponent(e));
+    y.times(q.y, high_exponent(e));
+    B = w == 0 || (fresh >> w & 1u) ? make_float2(q.z, q.w)
+                                    : make_float2(Factors(q.x, low_exponent(e)).apply(B.x, q.z), Factors(q.y, high_exponent(e)).apply(B.y, q.w));
+  }
+  x.settle();
+  y.settle();
+  if (!posted) {
+    auto plain = [](WideProduct v) { return v.e == 0 ? v.m : v.e < 0 ? 0.f : __uint_as_float(0x7f800000u); };
+    if (A.x != A.x) A = make_float2(plain(x), plain(y));
+    const float4 own = make_float4(fresh ? __uint_as_float(kCut) : A.x, fresh ? 1.f : A.y, B.x, B.y);
+    const uint32_t to = sm100::smem_u32(ch.mail + (slot * cluster + rank) * 32 + lane), full = sm100::smem_u32(&ch.mail_full[slot]);
+    for (int k = 0; k < cluster; ++k) post16(in_rank(to, k), own, in_rank(full, k));
+    if (!ring_wait(&ch.mail_full[slot], (n / kMailSlots) & 1, gave_up, status, limit_ns)) return WideStep{h, phase, false};
+  }
+  const float4 *mail = ch.mail + slot * cluster * 32;
+  const StepStates plain = plain_states(mail, cluster, rank, lane, h);
+  float2 e = plain.enter, next = plain.next;
+  if (!__all_sync(0xffffffffu, plain.holds)) {
+    auto suspect = [](float v) { return fabsf(v) < kSafe || fabsf(v) > kMost; };
+    uint32_t which = 0;  // tiles that send a second mail
+    for (int k = 0; k < cluster; ++k) {
+      const float4 t = mail[k * 32 + lane];
+      which |= (__any_sync(0xffffffffu, __float_as_uint(t.x) != kCut && (suspect(t.x) || suspect(t.y))) ? 1u : 0u) << k;
+    }
+    if (which >> rank & 1u) {
+      const uint32_t to = sm100::smem_u32(ch.wide_mail + rank * 32 + lane), full = sm100::smem_u32(ch.wide_full);
+      const int2 codes = make_int2((int)wide_code(x.m, x.e), (int)wide_code(y.m, y.e));
+      for (int k = 0; k < cluster; ++k) post8(in_rank(to, k), codes, in_rank(full, k));
+    }
+    if (lane == 0) sm100::mbar_arrive_expect_tx(ch.wide_full, (uint32_t)__popc(which) * 256u);
+    if (!ring_wait(ch.wide_full, phase, gave_up, status, limit_ns)) return WideStep{h, phase, false};
+    phase ^= 1u;
+    next = h;
+    for (int k = 0; k < cluster; ++k) {
+      const float4 t = mail[k * 32 + lane];
+      if (k == rank) e = next;
+      if (__float_as_uint(t.x) == kCut) {
+        next = make_float2(t.z, t.w);
+      } else {
+        const int2 codes = which >> k & 1u ? ch.wide_mail[k * 32 + lane] : make_int2(0, 0);
+        auto through = [&](float A, int code, float h, float add) {
+          const bool wide = fabsf(A) > kMost || (fabsf(A) < kSafe && fabsf(h) > kLargeState);
+          return wide ? wide_factors((uint32_t)code).apply(h, add) : fmaf(A, h, add);
+        };
+        next = make_float2(through(t.x, codes.x, next.x, t.z), through(t.y, codes.y, next.y, t.w));
+      }
+    }
+  }
+#pragma unroll 2
+  for (int w = 0; w < kScanWarps; ++w) {
+    int qe;
+    const float4 q = read_part(ch, w * 32 + lane, qe);
+    ch.enter[w * 32 + lane] = e;
+    e = (fresh >> w & 1u) ? make_float2(q.z, q.w)
+                          : make_float2(Factors(q.x, low_exponent(qe)).apply(e.x, q.z), Factors(q.y, high_exponent(qe)).apply(e.y, q.w));
+  }
+  return WideStep{next, phase, true};
+}
+
 // The chaining warp.  Mail slots: a CTA posts step n + 2 only after it has read the mail of step n + 1,
 // which holds this CTA's post of n + 1, which this warp sent after it had read step n: two suffice.
 // parts: a warp writes tile n + 1's after its entering state of tile n, which was formed from tile n's.
-// REV: the tiles and the tokens in them go back in time, and the ends of sequences cut the chain.
-template <int S, int META, bool REV>
+// (Backward, the tiles and the tokens in them go back in time, and the ends of sequences cut the chain.)
+template <int S, int META>
 __device__ __forceinline__ void chain_steps(const ScanShape &p, const Chain &ch, const TileMeta<S> *metas, int steps, int lane,
                                             volatile int *gave_up) {
   const uint32_t rank = cluster_rank(), bytes = (uint32_t)p.cluster * 512u;
   if (lane == 0)
     for (int i = 0; i < kMailSlots; ++i) sm100::mbar_arrive_expect_tx(&ch.mail_full[i], bytes);
   float2 h = make_float2(0.f, 0.f);  // the state entering the step
+  uint32_t phase = 0;
   for (int n = 0; n < steps; ++n) {
     if (!ring_wait(ch.parts_full, n & 1, gave_up, p.status, p.limit_ns)) return;
-    const TileMeta<S> &m = metas[n % META];
-    uint32_t fresh = 0;  // bit w: a sequence begins (REV: ends) among warp w's tokens
+    const uint32_t fresh = metas[n % META].fresh;
+    const int slot = n % kMailSlots;
     float4 q[kScanWarps];
 #pragma unroll
-    for (int w = 0; w < kScanWarps; ++w) {
-      q[w] = ch.parts[w * 32 + lane];
-      fresh |= ((REV ? m.ends[kScanWarps - 1 - w] : m.starts[w]) != 0u ? 1u : 0u) << w;
-    }
+    for (int w = 0; w < kScanWarps; ++w) q[w] = ch.parts[w * 32 + lane];
     float4 own = q[0];
 #pragma unroll
     for (int w = 1; w < kScanWarps; ++w) {
       const bool f = fresh >> w & 1u;
       own = make_float4(own.x * q[w].x, own.y * q[w].y, f ? q[w].z : fmaf(q[w].x, own.z, q[w].z), f ? q[w].w : fmaf(q[w].y, own.w, q[w].w));
     }
-    if (fresh) own.x = __uint_as_float(kCut);
-    const int slot = n % kMailSlots;
-    const uint32_t to = sm100::smem_u32(ch.mail + (slot * p.cluster + (int)rank) * 32 + lane);
-    const uint32_t bar = sm100::smem_u32(&ch.mail_full[slot]);
-    if (!(p.withhold && n == 0 && rank == 0)) {
+    bool posted = false, done = false;
+    if (!__any_sync(0xffffffffu, own.x != own.x)) {  // every part is plain
+      if (fresh) {
+        own.x = __uint_as_float(kCut);
+        own.y = 1.f;
+      }
+      const uint32_t to = sm100::smem_u32(ch.mail + (slot * p.cluster + (int)rank) * 32 + lane);
+      const uint32_t bar = sm100::smem_u32(&ch.mail_full[slot]);
+      if (!(p.withhold && n == 0 && rank == 0)) {
 #pragma unroll 4
-      for (int k = 0; k < p.cluster; ++k) post16(in_rank(to, k), own, in_rank(bar, k));
-    }
-    if (!ring_wait(&ch.mail_full[slot], (n / kMailSlots) & 1, gave_up, p.status, p.limit_ns)) return;
-    const float4 *mail = ch.mail + slot * p.cluster * 32;
-    float2 e = h;
-    for (int k0 = 0; k0 < p.cluster; k0 += 4) {
-      float4 t[4];
+        for (int k = 0; k < p.cluster; ++k) post16(in_rank(to, k), own, in_rank(bar, k));
+      }
+      if (!ring_wait(&ch.mail_full[slot], (n / kMailSlots) & 1, gave_up, p.status, p.limit_ns)) return;
+      posted = true;
+      const StepStates states = plain_states(ch.mail + slot * p.cluster * 32, p.cluster, (int)rank, lane, h);
+      done = __all_sync(0xffffffffu, states.holds);
+      if (done) {
+        h = states.next;
+        float2 e = states.enter;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (k0 + u < p.cluster) t[u] = mail[(k0 + u) * 32 + lane];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (k0 + u >= p.cluster) break;
-        if (k0 + u == (int)rank) e = h;
-        h = __float_as_uint(t[u].x) == kCut ? make_float2(t[u].z, t[u].w) : make_float2(fmaf(t[u].x, h.x, t[u].z), fmaf(t[u].y, h.y, t[u].w));
+        for (int w = 0; w < kScanWarps; ++w) {
+          ch.enter[w * 32 + lane] = e;
+          e = (fresh >> w & 1u) ? make_float2(q[w].z, q[w].w) : make_float2(fmaf(q[w].x, e.x, q[w].z), fmaf(q[w].y, e.y, q[w].w));
+        }
       }
     }
-#pragma unroll
-    for (int w = 0; w < kScanWarps; ++w) {
-      ch.enter[w * 32 + lane] = e;
-      e = (fresh >> w & 1u) ? make_float2(q[w].z, q[w].w) : make_float2(fmaf(q[w].x, e.x, q[w].z), fmaf(q[w].y, e.y, q[w].w));
+    if (!done) {
+      const WideStep step = wide_step(ch, p.cluster, p.status, p.limit_ns, fresh, n, lane, h, posted, phase, gave_up);
+      if (!step.ok) return;
+      h = step.h;
+      phase = step.phase;
     }
     __syncwarp();
     if (lane == 0) {

@@ -224,3 +224,100 @@ def test_gate_logits_at_the_lowest_value(cuda_device, dt, C):
     dx, dg, dinit, ex, eg, einit = R.recurrence_backward(g, h.cpu(), dh, [T], "sigmoid", x, s0)
     R.check(d["dx"], dx, ex + 1e3 * SMALL, "dx")
     R.check(d["dg"], dg, eg + 2.0 ** -23 * dg.abs() + 1e3 * SMALL * (1 + rh.abs().max()), "dg")
+
+
+# ---- products of decays beyond fp32's range: the definition never forms them
+def _case(name, T, C, xt, gt):
+    """(x, decays, state, upstream gradient); the strong decays are powers of two."""
+    x, a, s0, dh = _rand((T, C), 1, xt), torch.full((T, C), 0.9), _rand((1, C), 3), _rand((T, C), 4, xt)
+    if name != "infinite state":
+        x[:], dh[:] = 0.0, 0.0
+    if name == "growth of nothing":  # a masked stretch under gates above one
+        a[:] = 64.0
+        s0[:] = 0.0
+        x[T - 20], dh[20] = 1.0, 1.0
+    elif name == "growth from far below":
+        a[:] = 1.0
+        a[130:165] = 64.0  # by 2^210
+        s0[:] = 2.0 ** -120
+        dh[300] = 2.0 ** -120
+    elif name == "growth of nothing, then a reset":
+        a[:250], a[250], s0[:] = 64.0, 0.0, 0.0
+        x[251:] = _rand((T - 251, C), 1, xt)
+        dh[20] = 1.0
+    elif name == "growth and its undoing":  # by 2^132 and back, or by 2^-132 and back
+        a[:] = 1.0
+        for lane, (at, up) in enumerate(((130, True), (130, False), (165, True), (165, False))):
+            a[at:at + 22, lane::4], a[at + 22:at + 44, lane::4] = (64.0, 1 / 64) if up else (1 / 64, 64.0)
+            s0[0, lane::4] = 2.0 ** (-40 if up else 60)
+            dh[400, lane::4] = 2.0 ** (60 if up else -40)
+    elif name == "infinite state":
+        a[:] = 0.1
+        s0[0, ::3], s0[0, 1::3] = math.inf, -math.inf
+    elif name == "large state, strong decays":
+        a[:], s0[:] = 1.0, 2.0 ** 120
+        a[150:166] = 2.0 ** -10
+        dh[T - 5] = 2.0 ** 119
+    elif name == "large state, decays about a half":
+        a[:], s0[:] = 0.5, 2.0 ** 120
+        dh[T - 5] = 2.0 ** 100
+    elif name == "negative decays":
+        a[10:43, ::2], a[200:250, 1::2] = -64.0, -1 / 64
+        s0[0, ::2], s0[0, 1::2] = 2.0 ** -100, 2.0 ** 98
+        dh[150, ::2], dh[390, 1::2] = 2.0 ** -100, 2.0 ** 40
+    return x, a.to(gt), s0, dh
+
+
+CASES = ["growth of nothing", "growth from far below", "growth of nothing, then a reset", "growth and its undoing", "infinite state",
+         "large state, strong decays", "large state, decays about a half", "negative decays"]
+@pytest.mark.parametrize("name", CASES)
+@pytest.mark.parametrize("T,C,dt,gt", [(450, 128, BF16, BF16), (450, 61, F32, F32), (3000, 64, F32, F32), (1300, 1024, BF16, F32),
+                                       (1300, 515, BF16, F32), (2000, 512, BF16, BF16)])
+def test_products_of_decays_beyond_fp32(cuda_device, name, T, C, dt, gt):
+    dev = cuda_device
+    x, a, s0, dh = _case(name, T, C, dt, gt)
+    cu, lengths = _cu([T], dev), [T]
+    h, fin = pkg.gated_linear_recurrence(x.to(dev), a.to(dev), cu, gate="alpha", initial_state=s0.to(dev), output_final_state=True)
+    rh, rfin, eh, efin = R.recurrence(x, a, lengths, "alpha", s0)
+    # values that fp32 does not hold (beyond 2^127 to either side) are left out from there on, as every form's are
+    held = (rh.abs() < 2.0 ** 127).cummin(0)[0].bool() if name != "infinite state" else torch.ones_like(rh, dtype=torch.bool)
+    keep = lambda v, m: torch.where(m, v, torch.zeros_like(v))  # noqa: E731
+    R.check(keep(h.cpu(), held), keep(rh, held), keep(eh, held) + SMALL, "h")
+    R.check(keep(fin.cpu(), held[-1:]), keep(rfin, held[-1:]), keep(efin, held[-1:]) + SMALL, "final")
+    # the one-token step goes the same way
+    state = s0.to(dev).clone()
+    for t in range(min(T, 460)):
+        hs = pkg.gated_linear_recurrence_decode(x[t:t + 1].to(dev), a[t:t + 1].to(dev), gate="alpha", initial_state=state,
+                                                output_state=state)
+        if t % 50 == 49:
+            m = held[t:t + 1]
+            R.check(keep(hs.cpu(), m), keep(rh[t:t + 1], m), keep(eh[t:t + 1], m) + SMALL, f"step {t}")
+    kept = _rand((T, C), 6, dt)
+    got = pkg.gated_linear_recurrence_backward(a.to(dev), kept.to(dev), dh.to(dev), cu, gate="alpha", initial_state=torch.zeros_like(s0).to(dev),
+                                               d_final_state=(s0 if "state" in name else torch.zeros_like(s0)).to(dev))
+    dx, dg, dinit, ex, eg, einit = R.recurrence_backward(a, kept, dh, lengths, "alpha", None, torch.zeros_like(s0),
+                                                         s0 if "state" in name else None)
+    held = (dx.abs() < 2.0 ** 126).flip(0).cummin(0)[0].flip(0) if name != "infinite state" else torch.ones_like(held)
+    small = SMALL * (1 + kept.double().abs())
+    R.check(keep(got["dx"].cpu(), held), keep(dx, held), keep(ex, held) + SMALL, "dx")
+    if name != "infinite state":
+        R.check(keep(got["dg"].cpu(), held), keep(dg, held), keep(eg + 2.0 ** -23 * dg.abs(), held) + small, "dg")
+    R.check(keep(got["d_initial_state"].cpu(), held[:1]), keep(dinit, held[:1]), keep(einit, held[:1]) + SMALL, "d_initial_state")
+
+
+@pytest.mark.parametrize("gate,value", [("log", 3.0), ("log", -9.0), ("sigmoid", -9.0), ("sigmoid", -0.4)])
+@pytest.mark.parametrize("C", [64, 33])
+def test_long_runs_of_one_gate(cuda_device, gate, value, C):
+    """Growth of nothing and strong decays of a large state, by the other gates."""
+    dev, T = cuda_device, 700
+    g = torch.full((T, C), value)
+    x, s0 = torch.zeros((T, C)), torch.zeros((1, C))
+    if value > 0:
+        x[T - 25] = 1.0
+    else:
+        s0[:] = 2.0 ** 120
+        s0[0, 1::2] = math.inf
+    h, fin = pkg.gated_linear_recurrence(x.to(dev), g.to(dev), _cu([T], dev), gate=gate, initial_state=s0.to(dev), output_final_state=True)
+    rh, rfin, eh, efin = R.recurrence(x, g, [T], gate, s0)
+    R.check(h, rh, eh + SMALL, "h")
+    R.check(fin, rfin, efin + SMALL, "final")
