@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
         B = mul2(a, add2(upstream(i), B));
       }
       if (ends) {  // again, token by token
+        A = both(1.f);
         keep_only<S>(kept);
         B = make_float2(0.f, 0.f);
 #pragma unroll
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
           B = mul2(gate_decay<GATE>(kept[i], &f), add2(upstream(i), B));
         }
       }
-      const bool unsafe = write_part(ch, warp * 32 + lane, A, B, largest, ends != 0u || hi <= 0);
+      const bool unsafe = write_part(ch, warp * 32 + lane, A, B, largest, ends != 0u);
       __syncwarp();
       if (lane == 0) {
         sm100::mbar_arrive(ch.parts_full);
@@ -189,8 +190,16 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
           sm100::mbar_arrive(&empty[(n - 1) % L::kStages]);
         }
       }
-      if (unsafe)
-        write_products<TG, GATE, RAW, S>(ch.parts_m + warp * 32 + lane, ch.parts_e + warp * 32 + lane, base + L::g_off, block * S, lane, p.g, t0, c0);
+      if (unsafe) {
+        float2 *products = ch.parts_m + warp * 32 + lane;
+        int *exponents = ch.parts_e + warp * 32 + lane;
+        if (largest.holds(A)) {
+          *products = A;
+          *exponents = 0;
+        } else {
+          write_products<TG, GATE, RAW, S>(products, exponents, base + L::g_off, block * S, lane, p.g, t0, c0);
+        }
+      }
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(ch.products_full);
       if (!ring_wait(ch.enter_full, n & 1, gave_up, s.status, s.limit_ns)) break;

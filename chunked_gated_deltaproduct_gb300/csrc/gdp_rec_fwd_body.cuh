@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
         A = mul2(A, a[i]);
       }
       if (starts) {  // again, token by token
+        A = both(1.f);
         keep_only<S>(a);
         B = make_float2(0.f, 0.f);
 #pragma unroll
@@ -154,14 +155,22 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
           if (starts >> i & 1u) a[i] = B;
         }
       }
-      const bool unsafe = write_part(ch, warp * 32 + lane, A, B, largest, starts != 0u || hi <= 0);
+      const bool unsafe = write_part(ch, warp * 32 + lane, A, B, largest, starts != 0u);
       __syncwarp();
       if (lane == 0) {
         sm100::mbar_arrive(ch.parts_full);
         sm100::bulk_wait_read<0>();  // the last tile's store has read `mine`
       }
-      if (unsafe)
-        write_products<TG, GATE, RAW, S>(ch.parts_m + warp * 32 + lane, ch.parts_e + warp * 32 + lane, gs, warp * S, lane, p.g, t0, c0);
+      if (unsafe) {
+        float2 *products = ch.parts_m + warp * 32 + lane;
+        int *exponents = ch.parts_e + warp * 32 + lane;
+        if (largest.holds(A)) {
+          *products = A;
+          *exponents = 0;
+        } else {
+          write_products<TG, GATE, RAW, S>(products, exponents, gs, warp * S, lane, p.g, t0, c0);
+        }
+      }
       __syncwarp();
       if (lane == 0) {
         sm100::mbar_arrive(ch.products_full);

@@ -354,14 +354,14 @@ __device__ __forceinline__ void check_sequences(const void *cu, int cu64, int64_
 // ---- products of decays beyond fp32 ----
 // A run's product A of decays may leave fp32's range though no state does: decays of 2 over 128 tokens while the
 // state is zero, decays of 0.4 under an infinite state, a rise and its undoing.  The definition never forms such a
-// product.  A plain product is right where no decay is above 2^(1/8), so that a tile's rises by 2^16 at most, and it
-// ends above 2^-110, so that no part of it was below 2^-126; and where it ends below that it is right enough for a
-// state of at most 64 (it is off by 2^16 times 2^-149, the state by less than 2^-126).  Everything else goes as A 2^e:
-// with e = 0 and A plain where the whole is a normal number, else with A in [1, 2) in magnitude (a decay of
-// exactly zero, infinity or NaN: itself, e = 0).  Which form a channel's product takes depends on its own tokens and
-// state, and not on what its neighbours need.
+// product.  A plain product is right where no decay is above 2^(1/16), so that a tile's rises by 2^8 at most, and it
+// ends above 2^-118, so that no part of it was below 2^-126; and where it ends below that it is right enough for a
+// state of at most 2^16 (it is off by 2^8 times 2^-149, the state by 2^-125).  Everything else goes as A 2^e: with
+// e = 0 and A plain where the whole is a normal number, else with A in [1, 2) in magnitude (a decay of exactly
+// zero, infinity or NaN: itself, e = 0).  Which form a channel's product takes depends on its own tokens and state,
+// and not on what its neighbours need.
 constexpr float kNormal = 0x1p-126f, kMost = 0x1.fffffep127f;  // fp32's normal numbers
-constexpr float kSafe = 0x1p-110f, kLargeState = 64.f;
+constexpr float kSafe = 0x1p-118f, kLargeState = 0x1p16f;
 
 // v as m 2^e with 1 <= |m| < 2; zero, infinity and NaN are themselves (e = 0).
 __device__ __forceinline__ float split(float v, int &e) {
@@ -410,7 +410,7 @@ struct Factors {
   __device__ __forceinline__ float apply(float h, float add) const { return b == 1.f ? fmaf(a, h, add) : fmaf(a * h, b, add); }
 };
 // A 2^e in 32 bits, a sign, nine bits of exponent and 22 of fraction: half a unit is 2^-23 of a product that has
-// itself been rounded as often as it has factors.  Only products below 2^-110 or beyond fp32 are read back from it.
+// itself been rounded as often as it has factors.  Only products below 2^-118 or beyond fp32 are read back from it.
 __device__ __forceinline__ uint32_t wide_code(float A, int e) {
   const uint32_t b = __float_as_uint(A);
   if (outside(A)) return A == 0.f ? 0u : (b & 0x80000000u) | 511u << 22 | (A != A ? 1u : 0u);
@@ -497,13 +497,15 @@ __device__ __forceinline__ void leave_cluster(volatile int *gave_up) {
   }
 }
 
-// Whether some decay of a lane's run is above 2^(1/8) (or a NaN), from the gates as they are stored, compared as
-// integers (log gates: above 0.0866); a sigmoid's never are.
+// The largest decay of a lane's run, from the gates as they are stored, compared as integers (a NaN is on top); a
+// sigmoid's decays are below one.
 template <typename TG, int GATE>
 struct LargestGate {
   static constexpr bool kWord = sizeof(TG) == 2;  // two channels in a word
   static constexpr bool kHalf = std::is_same<TG, __half>::value;
-  static constexpr int kTop = GATE == GDP_GATE_LOG ? (!kWord ? 0x3db15b57 : kHalf ? 0x2d8b : 0x3db1) : (!kWord ? 0x3f8b95c1 : kHalf ? 0x3c5c : 0x3f8b);
+  // decays of 2^(1/16) and of 2^7: log gates of 0.0433 and 4.8125
+  static constexpr int kRise = GATE == GDP_GATE_LOG ? (!kWord ? 0x3d317217 : kHalf ? 0x298b : 0x3d31) : (!kWord ? 0x3f85aac3 : kHalf ? 0x3c2d : 0x3f85);
+  static constexpr int kSteep = GATE == GDP_GATE_LOG ? (!kWord ? 0x409a0000 : kHalf ? 0x44d0 : 0x409a) : (!kWord ? 0x43000000 : kHalf ? 0x5800 : 0x4300);
   static constexpr int kMask = GATE == GDP_GATE_LOG ? -1 : kWord ? 0x7fff7fff : 0x7fffffff;
   int x = kWord ? (int)0x80008000u : INT_MIN, y = INT_MIN;
   __device__ __forceinline__ void see(typename Packed<TG>::type v) {
@@ -516,10 +518,15 @@ struct LargestGate {
       }
     }
   }
-  __device__ __forceinline__ bool rises() const {
+  __device__ __forceinline__ bool above(int limit) const {
     if constexpr (GATE == GDP_GATE_SIGMOID) return false;
-    else if constexpr (kWord) return max((int)(short)(x & 0xffff), x >> 16) > kTop;
-    else return max(x, y) > kTop;
+    else if constexpr (kWord) return max((int)(short)(x & 0xffff), x >> 16) > limit;
+    else return max(x, y) > limit;
+  }
+  __device__ __forceinline__ bool rises() const { return above(kRise); }
+  // The plain product holds all the same: up to 15 decays of 2^7 cannot bring back what a part of it had lost.
+  __device__ __forceinline__ bool holds(float2 A) const {
+    return !above(kSteep) && fminf(fabsf(A.x), fabsf(A.y)) >= 0x1p-15f && fmaxf(fabsf(A.x), fabsf(A.y)) <= 0x1p15f;
   }
 };
 // The products of S decays of a lane that is not safe, read again from the tile (out of line: few tiles come here).
@@ -539,11 +546,11 @@ __device__ __noinline__ void write_products(float2 *m, int *e, const unsigned ch
   *e = pack_exponents(x.e, y.e);
 }
 // A computing warp, after its first run: writes its part, and says whether the lane's products have to follow (see
-// write_products).  `cut`: a sequence begins among the tokens, or none of them belongs to one, and A is not used.
+// write_products).  `cut`: a sequence begins among the tokens, A is one and is not used.
 template <typename TG, int GATE>
 __device__ __forceinline__ bool write_part(const Chain &ch, int at, float2 A, float2 B, const LargestGate<TG, GATE> &largest, bool cut) {
   const bool unsafe = !cut && (largest.rises() || !(fabsf(A.x) >= kSafe && fabsf(A.y) >= kSafe));
-  ch.parts[at] = make_float4(cut ? 1.f : unsafe ? __uint_as_float(0x7fffffffu) : A.x, cut ? 1.f : A.y, B.x, B.y);
+  ch.parts[at] = make_float4(unsafe ? __uint_as_float(0x7fffffffu) : A.x, A.y, B.x, B.y);
   return unsafe;
 }
 // A part, its exponents brought in.
@@ -586,9 +593,19 @@ __device__ __forceinline__ StepStates plain_states(const float4 *mail, int clust
   return StepStates{e, h, most <= kMost && (least >= kSafe || state <= kLargeState)};
 }
 
+// The entering states are written; the slot's next mail may come (of step n + 2).
+__device__ __forceinline__ void finish_step(const Chain &ch, int slot, uint32_t bytes, int lane) {
+  __syncwarp();
+  if (lane == 0) {
+    sm100::mbar_arrive(ch.enter_full);
+    sm100::mbar_arrive_expect_tx(&ch.mail_full[slot], bytes);
+  }
+}
+
 // The chaining warp's step where plain products do not hold, out of line: before this CTA's mail is posted, when a part
 // of its tile is not plain, or after (`posted`), when the cluster's mail shows that products outside fp32 matter.  Those
-// come in a second mail, posted once the first has come, so that every CTA has read the step before's.
+// come in a second mail, posted once the first has come, so that every CTA has read the step before's.  Costs 2.5 us a
+// step (65536 x 4096 bf16 with log gates in -0.05 .. 0.05, all of whose steps come here: 583 against 268 us).
 struct WideStep {
   float2 h;
   uint32_t phase;  // of the second mail
@@ -662,6 +679,7 @@ static __device__ __noinline__ WideStep wide_step(Chain ch, int cluster, uint32_
     e = (fresh >> w & 1u) ? make_float2(q.z, q.w)
                           : make_float2(Factors(q.x, low_exponent(qe)).apply(e.x, q.z), Factors(q.y, high_exponent(qe)).apply(e.y, q.w));
   }
+  finish_step(ch, slot, (uint32_t)cluster * 512u, lane);
   return WideStep{next, phase, true};
 }
 
@@ -690,43 +708,40 @@ __device__ __forceinline__ void chain_steps(const ScanShape &p, const Chain &ch,
       const bool f = fresh >> w & 1u;
       own = make_float4(own.x * q[w].x, own.y * q[w].y, f ? q[w].z : fmaf(q[w].x, own.z, q[w].z), f ? q[w].w : fmaf(q[w].y, own.w, q[w].w));
     }
-    bool posted = false, done = false;
-    if (!__any_sync(0xffffffffu, own.x != own.x)) {  // every part is plain
-      if (fresh) {
-        own.x = __uint_as_float(kCut);
-        own.y = 1.f;
-      }
-      const uint32_t to = sm100::smem_u32(ch.mail + (slot * p.cluster + (int)rank) * 32 + lane);
-      const uint32_t bar = sm100::smem_u32(&ch.mail_full[slot]);
-      if (!(p.withhold && n == 0 && rank == 0)) {
-#pragma unroll 4
-        for (int k = 0; k < p.cluster; ++k) post16(in_rank(to, k), own, in_rank(bar, k));
-      }
-      if (!ring_wait(&ch.mail_full[slot], (n / kMailSlots) & 1, gave_up, p.status, p.limit_ns)) return;
-      posted = true;
-      const StepStates states = plain_states(ch.mail + slot * p.cluster * 32, p.cluster, (int)rank, lane, h);
-      done = __all_sync(0xffffffffu, states.holds);
-      if (done) {
-        h = states.next;
-        float2 e = states.enter;
-#pragma unroll
-        for (int w = 0; w < kScanWarps; ++w) {
-          ch.enter[w * 32 + lane] = e;
-          e = (fresh >> w & 1u) ? make_float2(q[w].z, q[w].w) : make_float2(fmaf(q[w].x, e.x, q[w].z), fmaf(q[w].y, e.y, q[w].w));
-        }
-      }
-    }
-    if (!done) {
+    auto wide = [&](bool posted) {
       const WideStep step = wide_step(ch, p.cluster, p.status, p.limit_ns, fresh, n, lane, h, posted, phase, gave_up);
-      if (!step.ok) return;
       h = step.h;
       phase = step.phase;
+      return step.ok;
+    };
+    if (__builtin_expect(__any_sync(0xffffffffu, own.x != own.x), 0)) {  // some part is not plain
+      if (!wide(false)) return;
+      continue;
     }
-    __syncwarp();
-    if (lane == 0) {
-      sm100::mbar_arrive(ch.enter_full);
-      sm100::mbar_arrive_expect_tx(&ch.mail_full[slot], bytes);  // for step n + 2
+    if (fresh) {
+      own.x = __uint_as_float(kCut);
+      own.y = 1.f;
     }
+    const uint32_t to = sm100::smem_u32(ch.mail + (slot * p.cluster + (int)rank) * 32 + lane);
+    const uint32_t bar = sm100::smem_u32(&ch.mail_full[slot]);
+    if (!(p.withhold && n == 0 && rank == 0)) {
+#pragma unroll 4
+      for (int k = 0; k < p.cluster; ++k) post16(in_rank(to, k), own, in_rank(bar, k));
+    }
+    if (!ring_wait(&ch.mail_full[slot], (n / kMailSlots) & 1, gave_up, p.status, p.limit_ns)) return;
+    const StepStates states = plain_states(ch.mail + slot * p.cluster * 32, p.cluster, (int)rank, lane, h);
+    if (__builtin_expect(!__all_sync(0xffffffffu, states.holds), 0)) {
+      if (!wide(true)) return;
+      continue;
+    }
+    h = states.next;
+    float2 e = states.enter;
+#pragma unroll
+    for (int w = 0; w < kScanWarps; ++w) {
+      ch.enter[w * 32 + lane] = e;
+      e = (fresh >> w & 1u) ? make_float2(q[w].z, q[w].w) : make_float2(fmaf(q[w].x, e.x, q[w].z), fmaf(q[w].y, e.y, q[w].w));
+    }
+    finish_step(ch, slot, bytes, lane);
   }
 }
 

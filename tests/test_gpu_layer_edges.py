@@ -321,3 +321,39 @@ def test_long_runs_of_one_gate(cuda_device, gate, value, C):
     rh, rfin, eh, efin = R.recurrence(x, g, [T], gate, s0)
     R.check(h, rh, eh + SMALL, "h")
     R.check(fin, rfin, efin + SMALL, "final")
+
+
+@pytest.mark.parametrize("C", [64, 61])
+@pytest.mark.parametrize("how", ["growth", "large state", "infinite state"])
+def test_neighbours_keep_their_bits(cuda_device, how, C):
+    """A sequence, or a pair of channels, whose products of decays leave fp32's range changes no bit of the others: not
+    where its neighbours' products are tiny (below 2^-126 over a tile) either."""
+    dev, lengths = cuda_device, [700, 900, 500]
+    T, cu = sum(lengths), _cu(lengths, dev)
+    x, dh, s0 = _rand((T, C), 1, F32).to(dev), _rand((T, C), 2, F32).to(dev), _rand((3, C), 3).to(dev)
+    a = (0.3 + 0.2 * torch.rand((T, C), generator=torch.Generator().manual_seed(4))).to(dev)
+    x[100:400], dh[100:400] = 0.0, 0.0  # a stretch where only the products tell
+
+    def run(x, a, s0, dh):
+        h, fin = pkg.gated_linear_recurrence(x, a, cu, gate="alpha", initial_state=s0, output_final_state=True)
+        d = pkg.gated_linear_recurrence_backward(a, x, dh, cu, gate="alpha", initial_state=s0, d_final_state=s0)
+        return h, fin, d["dx"], d["dg"], d["d_initial_state"]
+
+    want = run(x, a, s0, dh)
+    for rows, channels in ((slice(700, 1600), slice(0, C)), (slice(0, T), slice(6, 8))):
+        x2, a2, s2, dh2 = x.clone(), a.clone(), s0.clone(), dh.clone()
+        if how == "growth":
+            x2[rows, channels], dh2[rows, channels] = 0.0, 0.0
+            a2[rows, channels], s2[:, channels] = 8.0, 0.0
+        else:
+            s2[:, channels] = 2.0 ** 100 if how == "large state" else math.inf
+        others = [i for i in range(3) if not (rows.start == 700 and i == 1)]
+        if rows.start == 700:
+            s2[others] = s0[others]
+        free = torch.ones((T, C), dtype=torch.bool, device=dev)
+        free[rows, channels] = False
+        kept = torch.ones((3, C), dtype=torch.bool, device=dev)
+        kept[1 if rows.start == 700 else slice(0, 3), channels] = False
+        for was, now in zip(want, run(x2, a2, s2, dh2)):
+            m = free if was.shape[0] == T else kept
+            assert torch.equal(was[m], now[m])
