@@ -29,6 +29,7 @@ struct BwdLayout {
   static constexpr int x_off = s_off + (Q8 ? (kTile * 4 + 127) / 128 * 128 : 0);
   static constexpr int stage = x_off + (kX ? tile_bytes<TX>(kTile, RAW) : 0);
   static constexpr int kMeta = kStages + 1;
+  static constexpr bool kShortWaits = true;
   static constexpr int parts = kStages * stage, parts_m = parts + Chain::parts_bytes, parts_e = parts_m + Chain::parts_m_bytes, enter = parts_e + Chain::parts_e_bytes, meta = enter + Chain::enter_bytes;
   static constexpr int bars = (meta + kMeta * (int)sizeof(TileMeta<S>) + 15) / 16 * 16;
   static constexpr int mail = (bars + (2 * kStages + Chain::bars) * 8 + 16 + 127) / 128 * 128;  // last: its size is the cluster's
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
       const int64_t t0 = (int64_t)r * L::kTile;  // before row 0 in the last step of some CTAs: an empty tile
       TileMeta<S> &m = metas[n % L::kMeta];
       unsigned char *base = smem + st * L::stage;
-      if (n >= L::kStages && !ring_wait(&empty[st], (n / L::kStages + 1) & 1, gave_up, s.status, s.limit_ns)) break;
+      if (n >= L::kStages && !ring_wait<L::kShortWaits>(&empty[st], (n / L::kStages + 1) & 1, gave_up, s.status, s.limit_ns)) break;
       if (RAW) {
         load_rows<TG>(base + L::g_off, p.g, t0, L::kTile, s.T, c0, s.C, lane);
         load_rows<TX>(base + L::d_off, p.dout, t0, L::kTile, s.T, c0, s.C, lane);
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
     if (*gave_up) drain_loads<L::kStages>(full, n, RAW || Q8);
     if (blockIdx.x == 0) check_sequences(s.cu, s.cu64, s.N, s.T, s.status, lane, 32);
   } else if (warp == kChainWarp) {
-    chain_steps<S, L::kMeta>(s, ch, metas, steps, lane, gave_up);
+    chain_steps<S, L::kMeta, L::kShortWaits>(s, ch, metas, steps, lane, gave_up);
   } else {
     const int64_t c = c0 + 2 * lane;
     // dx and dg take the places of d_output and g in the stage and leave by TMA stores (each warp its own
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
       const int st = n % L::kStages;
       const unsigned char *base = smem + st * L::stage;
       const int64_t t0 = ((int64_t)s.rows - 1 - ((int64_t)n * s.cluster + rank)) * L::kTile + block * S;
-      if (!ring_wait(&full[st], (n / L::kStages) & 1, gave_up, s.status, s.limit_ns)) break;
+      if (!ring_wait<L::kShortWaits>(&full[st], (n / L::kStages) & 1, gave_up, s.status, s.limit_ns)) break;
       const TileMeta<S> &m = metas[n % L::kMeta];
       const uint32_t starts = m.starts[block], ends = m.ends[block];
       const int lo = m.lo - block * S, hi = m.hi - block * S;
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdCtas) gdp_rec_bwd_scan_kerne
       }
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(ch.products_full);
-      if (!ring_wait(ch.enter_full, n & 1, gave_up, s.status, s.limit_ns)) break;
+      if (!ring_wait<L::kShortWaits>(ch.enter_full, n & 1, gave_up, s.status, s.limit_ns)) break;
       keep_only<S>(kept);
       float2 E = ch.enter[warp * 32 + lane];
       // the state before token i

@@ -22,6 +22,7 @@ struct FwdLayout {
   static constexpr int kTile = kScanWarps * S;
   static constexpr int x_off = 0, g_off = tile_bytes<TX>(kTile, RAW), stage = g_off + tile_bytes<TG>(kTile, RAW);
   static constexpr int kMeta = kStages + 1;
+  static constexpr bool kShortWaits = !kKeep;
   static constexpr int out = kStages * stage, out_bytes = RAW ? 0 : kTile * kSlice * (int)sizeof(TX);
   static constexpr int parts = out + out_bytes, parts_m = parts + Chain::parts_bytes, parts_e = parts_m + Chain::parts_m_bytes, enter = parts_e + Chain::parts_e_bytes, meta = enter + Chain::enter_bytes;
   static constexpr int bars = (meta + kMeta * (int)sizeof(TileMeta<S>) + 15) / 16 * 16;
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
       const int64_t t0 = (int64_t)r * L::kTile;
       TileMeta<S> &m = metas[n % L::kMeta];
       unsigned char *base = smem + st * L::stage;
-      if (n >= L::kStages && !ring_wait(&empty[st], (n / L::kStages + 1) & 1, gave_up, s.status, s.limit_ns)) break;
+      if (n >= L::kStages && !ring_wait<L::kShortWaits>(&empty[st], (n / L::kStages + 1) & 1, gave_up, s.status, s.limit_ns)) break;
       if (RAW) {
         load_rows<TX>(base + L::x_off, p.x, t0, L::kTile, s.T, c0, s.C, lane);
         load_rows<TG>(base + L::g_off, p.g, t0, L::kTile, s.T, c0, s.C, lane);
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
     if (*gave_up) drain_loads<L::kStages>(full, n, RAW);
     if (blockIdx.x == 0) check_sequences(s.cu, s.cu64, s.N, s.T, s.status, lane, 32);
   } else if (warp == kChainWarp) {
-    chain_steps<S, L::kMeta>(s, ch, metas, steps, lane, gave_up);
+    chain_steps<S, L::kMeta, L::kShortWaits>(s, ch, metas, steps, lane, gave_up);
   } else {
     const int64_t c = c0 + 2 * lane;
     // outputs leave through shared memory and TMA stores (each warp its own rows), so that a warp does not
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
       const int st = n % L::kStages;
       const unsigned char *xs = smem + st * L::stage + L::x_off, *gs = smem + st * L::stage + L::g_off;
       const int64_t t0 = ((int64_t)n * s.cluster + rank) * L::kTile + warp * S;
-      if (!ring_wait(&full[st], (n / L::kStages) & 1, gave_up, s.status, s.limit_ns)) break;
+      if (!ring_wait<L::kShortWaits>(&full[st], (n / L::kStages) & 1, gave_up, s.status, s.limit_ns)) break;
       const TileMeta<S> &m = metas[n % L::kMeta];
       const uint32_t starts = m.starts[warp], ends = m.ends[warp];
       const int lo = m.lo - warp * S, hi = m.hi - warp * S;
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(kScanThreads, kFwdCtas)
         sm100::mbar_arrive(ch.products_full);
         if (L::kKeep) sm100::mbar_arrive(&empty[st]);
       }
-      if (!ring_wait(ch.enter_full, n & 1, gave_up, s.status, s.limit_ns)) break;
+      if (!ring_wait<L::kShortWaits>(ch.enter_full, n & 1, gave_up, s.status, s.limit_ns)) break;
       keep_only<S>(a);
       // ---- from the entering state.  Four tokens' inputs are read before their outputs are written (the
       // compiler keeps the order of accesses to shared memory).

@@ -471,11 +471,21 @@ constexpr uint32_t kCut = 0xffffffffu;
 // A whole warp's wait on one of the CTA's barriers: bounded, one answer for all lanes.  False once this wait, or any other of the CTA, ran out: the
 // calling role then stops (its outputs are undefined from there on); the other CTAs of the cluster stop
 // likewise, for want of this one's mail.
+// SHORT: the tries in a loop that is not unrolled.  Which is faster goes by the registers that a kernel gets (96, with a
+// few spills): unrolled by the compiler and not, forward with log gates (65536 x 4096) 268 and 266 us, with sigmoid
+// gates (64 packed requests) 210 and 217, backward from codes (65536 x 4096) 443 and 432.
+template <bool SHORT>
 __device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, volatile int *gave_up, uint32_t *status, uint64_t limit_ns) {
   // sleeping tries first: the bounded wait begins with a read of the global timer, which takes longer
   // than most waits here (8 x 4096 x 2048 backward: 235 us with it alone, 150 us so)
-  for (int i = 0; i < 64; ++i)
-    if (__all_sync(0xffffffffu, sm100::mbar_try_sleep(bar, parity, 1000u))) return true;
+  if constexpr (SHORT) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (__all_sync(0xffffffffu, sm100::mbar_try_sleep(bar, parity, 1000u))) return true;
+  } else {
+    for (int i = 0; i < 64; ++i)
+      if (__all_sync(0xffffffffu, sm100::mbar_try_sleep(bar, parity, 1000u))) return true;
+  }
   if (__all_sync(0xffffffffu, sm100::mbar_wait_or_abort(bar, parity, gave_up, limit_ns))) return true;
   set_status(status, GDP_DEV_ERR_TIMEOUT);
   return false;
@@ -605,7 +615,7 @@ __device__ __forceinline__ void finish_step(const Chain &ch, int slot, uint32_t 
 // The chaining warp's step where plain products do not hold, out of line: before this CTA's mail is posted, when a part
 // of its tile is not plain, or after (`posted`), when the cluster's mail shows that products outside fp32 matter.  Those
 // come in a second mail, posted once the first has come, so that every CTA has read the step before's.  Costs 2.5 us a
-// step (65536 x 4096 bf16 with log gates in -0.05 .. 0.05, all of whose steps come here: 583 against 268 us).
+// step (65536 x 4096 bf16 with log gates in -0.05 .. 0.05, all of whose steps come here: 578 against 265 us).
 struct WideStep {
   float2 h;
   uint32_t phase;  // of the second mail
@@ -614,7 +624,7 @@ struct WideStep {
 static __device__ __noinline__ WideStep wide_step(Chain ch, int cluster, uint32_t *status, uint64_t limit_ns, uint32_t fresh, int n, int lane, float2 h, bool posted,
                                                   uint32_t phase, volatile int *gave_up) {
   const int rank = (int)cluster_rank(), slot = n % kMailSlots;
-  if (!ring_wait(ch.products_full, n & 1, gave_up, status, limit_ns)) return WideStep{h, phase, false};
+  if (!ring_wait<false>(ch.products_full, n & 1, gave_up, status, limit_ns)) return WideStep{h, phase, false};
   WideProduct x{1.f, 0}, y{1.f, 0};
   float2 B = make_float2(0.f, 0.f), A = both(1.f);  // A: as chain_steps has it
 #pragma unroll 2
@@ -635,7 +645,7 @@ static __device__ __noinline__ WideStep wide_step(Chain ch, int cluster, uint32_
     const float4 own = make_float4(fresh ? __uint_as_float(kCut) : A.x, fresh ? 1.f : A.y, B.x, B.y);
     const uint32_t to = sm100::smem_u32(ch.mail + (slot * cluster + rank) * 32 + lane), full = sm100::smem_u32(&ch.mail_full[slot]);
     for (int k = 0; k < cluster; ++k) post16(in_rank(to, k), own, in_rank(full, k));
-    if (!ring_wait(&ch.mail_full[slot], (n / kMailSlots) & 1, gave_up, status, limit_ns)) return WideStep{h, phase, false};
+    if (!ring_wait<false>(&ch.mail_full[slot], (n / kMailSlots) & 1, gave_up, status, limit_ns)) return WideStep{h, phase, false};
   }
   const float4 *mail = ch.mail + slot * cluster * 32;
   const StepStates plain = plain_states(mail, cluster, rank, lane, h);
@@ -653,7 +663,7 @@ static __device__ __noinline__ WideStep wide_step(Chain ch, int cluster, uint32_
       for (int k = 0; k < cluster; ++k) post8(in_rank(to, k), codes, in_rank(full, k));
     }
     if (lane == 0) sm100::mbar_arrive_expect_tx(ch.wide_full, (uint32_t)__popc(which) * 256u);
-    if (!ring_wait(ch.wide_full, phase, gave_up, status, limit_ns)) return WideStep{h, phase, false};
+    if (!ring_wait<false>(ch.wide_full, phase, gave_up, status, limit_ns)) return WideStep{h, phase, false};
     phase ^= 1u;
     next = h;
     for (int k = 0; k < cluster; ++k) {
@@ -687,7 +697,7 @@ static __device__ __noinline__ WideStep wide_step(Chain ch, int cluster, uint32_
 // which holds this CTA's post of n + 1, which this warp sent after it had read step n: two suffice.
 // parts: a warp writes tile n + 1's after its entering state of tile n, which was formed from tile n's.
 // (Backward, the tiles and the tokens in them go back in time, and the ends of sequences cut the chain.)
-template <int S, int META>
+template <int S, int META, bool SHORT>
 __device__ __forceinline__ void chain_steps(const ScanShape &p, const Chain &ch, const TileMeta<S> *metas, int steps, int lane,
                                             volatile int *gave_up) {
   const uint32_t rank = cluster_rank(), bytes = (uint32_t)p.cluster * 512u;
@@ -696,7 +706,7 @@ __device__ __forceinline__ void chain_steps(const ScanShape &p, const Chain &ch,
   float2 h = make_float2(0.f, 0.f);  // the state entering the step
   uint32_t phase = 0;
   for (int n = 0; n < steps; ++n) {
-    if (!ring_wait(ch.parts_full, n & 1, gave_up, p.status, p.limit_ns)) return;
+    if (!ring_wait<SHORT>(ch.parts_full, n & 1, gave_up, p.status, p.limit_ns)) return;
     const uint32_t fresh = metas[n % META].fresh;
     const int slot = n % kMailSlots;
     float4 q[kScanWarps];
@@ -728,7 +738,7 @@ __device__ __forceinline__ void chain_steps(const ScanShape &p, const Chain &ch,
 #pragma unroll 4
       for (int k = 0; k < p.cluster; ++k) post16(in_rank(to, k), own, in_rank(bar, k));
     }
-    if (!ring_wait(&ch.mail_full[slot], (n / kMailSlots) & 1, gave_up, p.status, p.limit_ns)) return;
+    if (!ring_wait<SHORT>(&ch.mail_full[slot], (n / kMailSlots) & 1, gave_up, p.status, p.limit_ns)) return;
     const StepStates states = plain_states(ch.mail + slot * p.cluster * 32, p.cluster, (int)rank, lane, h);
     if (__builtin_expect(!__all_sync(0xffffffffu, states.holds), 0)) {
       if (!wide(true)) return;
