@@ -126,8 +126,6 @@ __device__ __forceinline__ void gate_eval(float g, float *a, float *f) {
   }
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + exp_fast(-z)); }
-
 // Largest absolute value as its bits: they order like the values, with infinities and NaN on top.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 

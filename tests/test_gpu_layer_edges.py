@@ -102,14 +102,14 @@ def test_stream_argument_allocates_on_that_stream(cuda_device):
     """What a call on a given stream allocates is not memory that the current stream has yet to write."""
     dev, T, C = cuda_device, 2000, 128
     x, g, cu = _rand((T, C), 1, BF16).to(dev), _gates("log", (T, C), 2, BF16).to(dev), _cu([T], dev)
-    w, z = torch.ones(64, device=dev), _rand((T, 2, 64), 3, BF16).to(dev)
+    w, z, zero = torch.ones(64, device=dev), _rand((T, 2, 64), 3, BF16).to(dev), torch.zeros((1, C), device=dev)
     side = torch.cuda.Stream()
 
     def calls(**how):
         h, fin = pkg.gated_linear_recurrence(x, g, cu, output_final_state=True, **how)
         y, kept = pkg.gated_group_norm(x.view(T, 2, 64), w, z, save_checkpoint=True, **how)
         d = pkg.gated_group_norm_backward(z, kept, w, **how)
-        r = pkg.gated_linear_recurrence_backward(g, x, x, cu, initial_state=torch.zeros_like(fin), **how)
+        r = pkg.gated_linear_recurrence_backward(g, x, x, cu, initial_state=zero, **how)
         step = pkg.gated_linear_recurrence_decode(x, g, **how)
         return [h, fin, y, *kept.o, *kept.z, d["do"], d["dz"], d["dweight"], r["dx"], r["dg"], r["d_initial_state"], step]
 
