@@ -18,8 +18,8 @@ constexpr int kBwdCtas = 2;  // resident CTAs per SM
 
 template <typename TX, typename TG, int GATE, bool Q8, bool RAW>
 struct BwdLayout {
-  // Bytes of a channel and token; three stages where that leaves ten tokens per warp, else two (65536 x
-  // 4096 from codes: 401 us with three, 448 us with two; 8 x 4096 x 2048 sigmoid: 174 us and 154 us).
+  // Bytes of a channel and token; three stages where that leaves ten tokens per warp, else two (when it was
+  // chosen, 65536 x 4096 from codes: 401 us with three, 448 us with two; 8 x 4096 x 2048 sigmoid: 174 us and 154 us).
   static constexpr int kBytes = (int)(sizeof(TG) + sizeof(TX) * (GATE == GDP_GATE_SIGMOID ? 2 : 1) + (Q8 ? 1 : sizeof(TX)));
   static constexpr int kStages = scan_tokens(3 * kBytes) >= 10 ? 3 : 2, S = scan_tokens(kStages * kBytes);
   static constexpr int kTile = kScanWarps * S;

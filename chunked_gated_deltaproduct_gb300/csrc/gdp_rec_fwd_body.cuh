@@ -15,7 +15,7 @@ template <typename TX, typename TG, int GATE, bool RAW>
 struct FwdLayout {
   // Sigmoid gates: decays and inputs (three special-function operations a channel to form again) stay in
   // registers, and the stage is free after the first run; else the second run reads the inputs again
-  // (at 65536 x 4096 bf16, 1.61 GB: 262 us; with three stages 322 us).
+  // (at 65536 x 4096 bf16, when it was chosen: 262 us; with three stages 322 us).
   static constexpr bool kKeep = GATE == GDP_GATE_SIGMOID;
   static constexpr int kStages = 2;
   static constexpr int S = scan_tokens(kStages * (int)(sizeof(TX) + sizeof(TG)) + (int)sizeof(TX));

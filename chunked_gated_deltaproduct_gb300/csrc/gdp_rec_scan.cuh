@@ -15,12 +15,13 @@
 //     enters the next step.
 // Every value comes from the same operations in the same order on every run.  Nothing of the chain passes
 // through global memory: with (A, B) and states published there a hop took 5 us, which 6.8 TB/s would have to
-// cover with 34 MB of waiting tiles (1.97 ms at 65536 x 4096 bf16, now 0.26 ms).  Every wait is bounded.
+// cover with 34 MB of waiting tiles (1.97 ms at 65536 x 4096 bf16, now 0.27 ms).  Every wait is bounded.
 //
 // Bound: memory (a multiply-add and an exponential per element against 6 or 9 bytes).  At 65536 x 4096 bf16 the
-// forward moves 1.61 GB in 261 us (6.2 TB/s), the backward from 8-bit states 2.42 GB in 410 us (5.9 TB/s); at
-// smaller sizes the latency of a step (load, run, chain, run) bounds: 2.0 us at 65536 x 4096 (128 steps), 2.4 us
-// where sequences begin and end inside the tiles (64 packed requests x 2048, 83 steps).
+// forward moves 1.61 GB in 265 us (6.1 TB/s), the backward from 8-bit states 2.42 GB in 432 us (5.6 TB/s); at
+// smaller sizes the latency of a step (load, run, chain, run) bounds: 2.1 us at 65536 x 4096 (128 steps), 2.5 us
+// where sequences begin and end inside the tiles (64 packed requests x 2048, 83 steps).  Of that, keeping products of
+// decays within range (below) costs 2 to 6 % (261, 412 and 201 us without, and with wrong results for some gates).
 #pragma once
 
 #include <climits>
@@ -786,7 +787,7 @@ cudaError_t launch_rec_bwd(RecBwd &p, int gate, cudaStream_t stream);
 // CTAs per slice: a power of two that fills every SM with `per_sm` (9 CTAs per cluster instead of 8 took
 // 458 us instead of 288 us at C = 2048), at most one per tile in time.  Clusters of 16 start slowly and pay
 // only for few channels and many tiles (us with 8 / 16 CTAs: 65536 x 512 106 / 77, 65536 x 1024 128 / 139,
-// 8192 x 512 16.5 / 12.6, 8192 x 1024 19.0 / 22.9, 1421 x 1024 8.1 / 13.3).
+// 8192 x 512 16.5 / 12.6, 8192 x 1024 19.0 / 22.9, 1421 x 1024 8.1 / 13.3, all when this was chosen).
 inline int cluster_size(int slices, int rows, int sms, int per_sm) {
   int k = sms * per_sm / (slices > 0 ? slices : 1);
   if (k > rows) k = rows;

@@ -42,7 +42,10 @@ typedef enum gdp_gate {
  * cu_seqlens that do not ascend from 0 to at most T set GDP_DEV_ERR_CU_SEQLENS; the
  * outputs are then undefined (nothing outside the buffers is touched).  A sequence's values never
  * depend on another sequence's, infinities and NaN included.  Results do not depend on scheduling:
- * every value is formed by the same operations in the same order.
+ * every value is formed by the same operations in the same order.  Gates may be of any size: decays above
+ * one, of zero, and any run of them; only the states, and the states that a run of tokens makes from zero,
+ * have to stay within fp32.  (Values below 2^-125 may come out as zero; a sigmoid gate is never closed
+ * further than 2^-125.)
  *
  * gdp_linear_recurrence_decode: one token per sequence (T == N, token i belongs to sequence i);
  * cu_seqlens is ignored.
