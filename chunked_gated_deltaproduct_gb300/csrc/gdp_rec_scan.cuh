@@ -291,7 +291,7 @@ __device__ __forceinline__ void find_sequences(const ScanShape &p, TileMeta<S> &
     const bool none = win.ok && b == e && b >= t0 && (b < t1 || last);
     if (__any_sync(0xffffffffu, begins || ends || none)) {
       int row = (int)win.base + lane;
-      if (p.slots && (begins || ends)) {
+      if (p.slots && (begins || ends || none)) {
         row = p.slots[win.base + lane];
         if (row < -1 || row >= p.num_slots) {
           if (c0 == 0) set_status(p.status, GDP_DEV_ERR_SLOT);

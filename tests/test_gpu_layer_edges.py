@@ -357,3 +357,22 @@ def test_neighbours_keep_their_bits(cuda_device, how, C):
         for was, now in zip(want, run(x2, a2, s2, dh2)):
             m = free if was.shape[0] == T else kept
             assert torch.equal(was[m], now[m])
+
+
+@pytest.mark.parametrize("lengths,slots", [([4, 0, 6], [0, 7, 1]), ([4, 6, 0], [0, 1, -3]), ([0, 0], [2, 1 << 30])])
+def test_slots_of_empty_sequences_are_checked(cuda_device, lengths, slots):
+    """A slot outside the cache is reported for a sequence without tokens too; nothing of the cache is written for it."""
+    dev, C = cuda_device, 96
+    x = _rand((sum(lengths), C), 1, BF16).to(dev)
+    cache, st = _rand((3, C), 2).to(dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    before = cache.clone()
+    pkg.gated_linear_recurrence(x, x, _cu(lengths, dev), state=cache, state_indices=torch.tensor(slots, dtype=torch.int32, device=dev),
+                                device_status=st)
+    assert int(st) == pkg.GDP_DEV_ERR_SLOT
+    written = [s for s, n in zip(slots, lengths) if n and 0 <= s < 3]
+    rest = [s for s in range(3) if s not in written]
+    assert torch.equal(cache[rest], before[rest])
+    st.zero_()
+    ok = torch.tensor([s if 0 <= s < 3 else -1 for s in slots], dtype=torch.int32, device=dev)
+    pkg.gated_linear_recurrence(x, x, _cu(lengths, dev), state=cache, state_indices=ok, device_status=st)
+    assert int(st) == 0
