@@ -36,7 +36,7 @@ def nvcc() -> str:
 
 # Sources without range checks: their objects are the same in both variants, so that the debug-bounds
 # build links those of the normal one.
-UNCHECKED = ("gdp_rec", "gdp_norm_", "gdp_group_norm")
+UNCHECKED = ("gdp_rec", "gdp_norm_", "gdp_group_norm", "gdp_conv", "gdp_ssm", "gdp_resnorm")
 
 
 def _shared(src: str) -> bool:

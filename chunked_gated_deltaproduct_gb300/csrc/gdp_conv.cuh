@@ -1,0 +1,59 @@
+// gdp_conv.cuh -- the short causal convolution's problem and launchers.
+#pragma once
+
+#include "gdp_block.cuh"
+
+namespace gdp {
+namespace layer {
+
+struct ConvProblem {
+  const void *x;
+  int64_t x_st;
+  const float *w, *b;
+  void *y;
+  Packed p;
+  int64_t C;
+  StateModes s;
+  int act, zero_pad;
+  // backward
+  const void *dy;
+  int64_t dy_st;
+  const void *dfin;
+  void *dx, *dinit;
+  float *partial;  // [parts][W + 1][C]
+  // plan
+  int64_t runs;    // forward: blocks over rows; backward: CTAs over rows
+  int64_t parts, part_rows;
+};
+
+constexpr int kConvThreads = 128;
+// A CTA is `x` vectors of channels by `y` runs of rows.
+inline dim3 conv_block(int64_t vecs) {
+  int x = 1;
+  while (x < 32 && x < vecs) x *= 2;
+  return dim3(x, kConvThreads / x);
+}
+
+template <typename T>
+cudaError_t launch_conv_fwd(ConvProblem &p, int width, int vec, bool states, cudaStream_t stream);
+template <typename T>
+cudaError_t launch_conv_states(const ConvProblem &p, int width, cudaStream_t stream);
+template <typename T>
+cudaError_t launch_conv_step(const ConvProblem &p, int width, cudaStream_t stream);
+template <typename T>
+cudaError_t launch_conv_bwd(ConvProblem &p, int width, int vec, cudaStream_t stream);
+
+// Parts of the rows whose weight gradients are summed apart, by the vectors of channels in a row: enough CTAs for
+// every SM, of 64 rows or more.
+inline int64_t conv_parts(int64_t T, int64_t vecs, int sms) {
+  const int64_t y = conv_block(vecs).y, x = conv_block(vecs).x;
+  const int64_t across = (vecs + x - 1) / x;
+  int64_t ctas = (sms * 6 + across - 1) / across;
+  const int64_t most = (T + 64 * y - 1) / (64 * y);
+  if (ctas > most) ctas = most;
+  if (ctas < 1) ctas = 1;
+  return ctas * y;
+}
+
+}  // namespace layer
+}  // namespace gdp
