@@ -47,9 +47,9 @@ class GdpScanArgs(ctypes.Structure):
         ("B_stride_t", _i64), ("B_stride_g", _i64), ("C_stride_t", _i64), ("C_stride_g", _i64), ("D", _vp),
         ("z", _vp), ("z_stride_t", _i64), ("dt_bias", _vp), ("output", _vp), ("cu_seqlens", _vp), ("T", _i64),
         ("N", _i64), ("C", _i64), ("S", _i64), ("G", _i64), ("initial_state", _vp), ("output_state", _vp),
-        ("state", _vp), ("state_indices", _vp), ("num_slots", _i64), ("chunk_states", _vp), ("device_status", _vp),
-        ("cu_seqlens_int64", _int), ("x_dtype", _int), ("dt_dtype", _int), ("dt_softplus", _int),
-        ("zero_padding", _int),
+        ("state", _vp), ("state_indices", _vp), ("num_slots", _i64), ("chunk_states", _vp), ("workspace", _vp),
+        ("workspace_bytes", _sz), ("device_status", _vp), ("cu_seqlens_int64", _int), ("x_dtype", _int),
+        ("dt_dtype", _int), ("dt_softplus", _int), ("zero_padding", _int),
     ]
 
 
@@ -103,6 +103,7 @@ def _library():
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = _int, [_vp, _vp]
         for name, dims, result in (("gdp_conv_workspace_bytes", 3, _sz), ("gdp_scan_workspace_bytes", 5, _sz),
+                                   ("gdp_scan_forward_workspace_bytes", 5, _sz),
                                    ("gdp_residual_norm_workspace_bytes", 2, _sz), ("gdp_scan_chunk_rows", 2, _i64)):
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = result, [_i64] * dims
@@ -120,6 +121,10 @@ def gdp_conv_workspace_bytes(T: int, C: int, width: int) -> int:
 
 def gdp_scan_workspace_bytes(T: int, N: int, C: int, S: int, G: int = 1) -> int:
     return int(_library().gdp_scan_workspace_bytes(T, N, C, S, G))
+
+
+def gdp_scan_forward_workspace_bytes(T: int, N: int, C: int, S: int, G: int = 1) -> int:
+    return int(_library().gdp_scan_forward_workspace_bytes(T, N, C, S, G))
 
 
 def gdp_scan_chunk_rows(T: int, N: int) -> int:
@@ -291,7 +296,7 @@ def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, first):
 
 
 def _scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, first, cu, N, cu64, entry, initial_state, output_final_state, state,
-          state_indices, save_states, output, output_state, device_status):
+          state_indices, save_states, output, output_state, workspace, device_status):
     """The common part of the packed and the one-token call."""
     shape, dtype, dev = first
     T, channels = shape
@@ -303,9 +308,13 @@ def _scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, first, cu, N, cu64, entry,
     kept = None
     if save_states:
         kept = torch.empty((lib.gdp_scan_chunk_rows(T, N), channels, S), dtype=torch.float32, device=x.device)
+    need = lib.gdp_scan_forward_workspace_bytes(T, N, channels, S, G) if cu else 0
+    wp = wb = 0
+    if need:
+        workspace, wp, wb = _workspace(workspace, need, x, dev)
     a = _pack_scan(*inputs, op, cu, T, N, channels, S, G,
                    *_states(initial_state, output_state, state, state_indices, N, (channels, S), torch.float32, dev), _address(kept),
-                   _status(device_status, dev), cu64, dtype, dt_type, int(bool(dt_softplus)), own)
+                   wp, wb, _status(device_status, dev), cu64, dtype, dt_type, int(bool(dt_softplus)), own)
     _finish(getattr(lib, entry)(a, _current(dev)), lib)
     if not output_final_state:
         return (output, kept) if save_states else output
@@ -314,7 +323,7 @@ def _scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, first, cu, N, cu64, entry,
 
 def selective_scan(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_softplus=True, initial_state=None,
                    output_final_state=False, state=None, state_indices=None, save_states=False, output=None, output_state=None,
-                   device_status=None, stream=None):
+                   workspace=None, device_status=None, stream=None):
     """h_t = exp(e_t A) h_{t-1} + e_t x_t B_t, y_t = (sum_s C_t h_t + D x_t) silu(z_t) along every packed sequence,
     with e = softplus(dt + dt_bias) (or dt + dt_bias): S states per channel (gdp_selective_scan).
 
@@ -330,11 +339,11 @@ def selective_scan(x, dt, A, B, C, cu_seqlens, D=None, z=None, dt_bias=None, dt_
     zeros; in a buffer given as ``output`` they are left as they are."""
     if stream is not None:
         return _on(stream, selective_scan, x, dt, A, B, C, cu_seqlens, D, z, dt_bias, dt_softplus, initial_state, output_final_state,
-                   state, state_indices, save_states, output, output_state, device_status)
+                   state, state_indices, save_states, output, output_state, workspace, device_status)
     first = _first("x", x, ("T", "C"))
     cu, N, cu64 = _cu(cu_seqlens, first[2])
     return _scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, first, cu, N, cu64, "gdp_selective_scan", initial_state,
-                 output_final_state, state, state_indices, save_states, output, output_state, device_status)
+                 output_final_state, state, state_indices, save_states, output, output_state, workspace, device_status)
 
 
 def selective_scan_decode(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, initial_state=None,
@@ -347,7 +356,7 @@ def selective_scan_decode(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softp
                    state_indices, output, output_state, device_status)
     first = _first("x", x, ("N", "C"))
     return _scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, first, 0, first[0][0], 0, "gdp_selective_scan_decode", initial_state,
-                 output_final_state, state, state_indices, False, output, output_state, device_status)
+                 output_final_state, state, state_indices, False, output, output_state, None, device_status)
 
 
 def selective_scan_backward(x, dt, A, B, C, d_output, cu_seqlens, chunk_states, D=None, z=None, dt_bias=None, dt_softplus=True,

@@ -15,7 +15,7 @@ gdp_status common(const Args *a, SsmProblem *p) {
   if (a->S < 1 || a->G < 1 || a->C % a->G != 0) return fail(GDP_ERR_INVALID_ARG, "S >= 1 and a G that divides C are required");
   if (a->S > 64) return fail(GDP_ERR_UNSUPPORTED, "S up to 64");
   const int64_t per = a->C / a->G, tiles = ssm_tiles(per, a->S);
-  if (a->G * tiles > 65535) return fail(GDP_ERR_UNSUPPORTED, "too many groups");
+  if (a->G * tiles > 65535 || (a->N + 1) * a->G * tiles > INT32_MAX) return fail(GDP_ERR_UNSUPPORTED, "too many groups, or sequences by channels");
   if ((st = rows_ok(a->x, a->x_stride_t, a->T, a->C, a->x_dtype, "x")) != GDP_OK) return st;
   if ((st = rows_ok(a->dt, a->dt_stride_t, a->T, a->C, a->dt_dtype, "dt")) != GDP_OK) return st;
   if (a->z && (st = rows_ok(a->z, a->z_stride_t, a->T, a->C, a->x_dtype, "z")) != GDP_OK) return st;
@@ -37,6 +37,14 @@ gdp_status common(const Args *a, SsmProblem *p) {
   p->per = per; p->tiles = tiles;
   p->dt_f32 = a->dt_dtype == GDP_DTYPE_F32;
   p->softplus = a->dt_softplus != 0;
+  p->sms = sm_count();
+  const int es = dtype_size(a->x_dtype), ds = dtype_size(a->dt_dtype);
+  // (a CTA's channels begin at a multiple of eight within their group)
+  p->fast_rows = (a->G == 1 || per * es % 16 == 0) && a->C * es % 16 == 0 && rows_by(p->x, p->x_st, a->T, a->x_dtype, 16) &&
+                 rows_by(p->dt, p->dt_st, a->T, a->dt_dtype, 16) && (ds == es || per * ds % 16 == 0) && rows_by(p->z, p->z_st, a->T, a->x_dtype, 16);
+  p->fast_vectors = a->S * es % 16 == 0 && rows_by(p->B, p->B_st, a->T, a->x_dtype, 16) && rows_by(p->Cm, p->C_st, a->T, a->x_dtype, 16) &&
+                    p->B_sg * es % 16 == 0 && p->C_sg * es % 16 == 0;
+  p->pair_out = a->C % 2 == 0 && per % 2 == 0;
   return GDP_OK;
 }
 
@@ -55,16 +63,28 @@ gdp_status resolve(const gdp_scan_args *a, bool step, SsmProblem *p) {
   p->y = a->output;
   p->s = StateModes{a->initial_state, a->output_state, a->state, a->state_indices, a->num_slots};
   p->chunks = step ? nullptr : a->chunk_states;
+  p->pair_out = p->pair_out && aligned(a->output, 2 * dtype_size(a->x_dtype));
   p->zero_pad = !step && a->zero_padding != 0;
   p->quad_states = a->S % 4 == 0 && aligned(a->initial_state, 16) && aligned(a->output_state, 16) && aligned(a->state, 16) && aligned(a->chunk_states, 16);
   return GDP_OK;
 }
 
+bool scan_shape(int64_t T, int64_t N, int64_t C, int64_t S, int64_t G) {
+  return T >= 0 && N >= 0 && C >= 1 && S >= 1 && S <= 64 && G >= 1 && C % G == 0 && C <= (1 << 20) && T <= INT32_MAX && N < INT32_MAX;
+}
+int64_t enter_bytes(int64_t pieces, int64_t C, int64_t S) { return (pieces * C * S * 4 + 255) / 256 * 256; }
 int64_t over_rows_bytes(int64_t workers, int64_t C, int64_t S) { return (workers * C * (S + 2) * 4 + 255) / 256 * 256; }
 
 }  // namespace
 }  // namespace layer
 }  // namespace gdp
+
+GDP_EXPORT size_t gdp_scan_forward_workspace_bytes(int64_t T, int64_t N, int64_t C, int64_t S, int64_t G) {
+  using namespace gdp::layer;
+  if (!scan_shape(T, N, C, S, G)) return 0;
+  const int64_t piece = ssm_piece(T, N, G * ssm_tiles(C / G, S), sm_count());
+  return piece ? (size_t)enter_bytes(T / piece + N, C, S) + (size_t)(T / piece + N) * (size_t)C * 4 : 0;
+}
 
 GDP_EXPORT gdp_status gdp_selective_scan(const gdp_scan_args *args, void *stream) {
   using namespace gdp::layer;
@@ -73,6 +93,15 @@ GDP_EXPORT gdp_status gdp_selective_scan(const gdp_scan_args *args, void *stream
   if (st != GDP_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
   if (p.p.N == 0) return p.zero_pad ? zero_out(p.y, (size_t)(p.p.T * p.C), args->x_dtype, s) : GDP_OK;
+  const size_t need = gdp_scan_forward_workspace_bytes(args->T, args->N, args->C, args->S, args->G);
+  if (need && (!args->workspace || !aligned(args->workspace, 256) || args->workspace_bytes < need))
+    return fail(GDP_ERR_WORKSPACE, "workspace missing, not 256-byte aligned or smaller than gdp_scan_forward_workspace_bytes");
+  p.piece = ssm_piece(p.p.T, p.p.N, p.G * p.tiles, p.sms);
+  p.pieces = p.piece ? p.p.T / p.piece + p.p.N : p.p.N;
+  if (p.piece) {
+    p.enter = static_cast<float *>(args->workspace);
+    p.spans = p.enter + enter_bytes(p.pieces, p.C, p.S) / 4;
+  }
   return cuda_status(args->x_dtype == GDP_DTYPE_BF16  ? launch_ssm_fwd<__nv_bfloat16>(p, s)
                      : args->x_dtype == GDP_DTYPE_F16 ? launch_ssm_fwd<__half>(p, s)
                                                       : launch_ssm_fwd<float>(p, s),
@@ -95,7 +124,7 @@ GDP_EXPORT int64_t gdp_scan_chunk_rows(int64_t T, int64_t N) { return T < 0 || N
 
 GDP_EXPORT size_t gdp_scan_workspace_bytes(int64_t T, int64_t N, int64_t C, int64_t S, int64_t G) {
   using namespace gdp::layer;
-  if (T < 0 || N < 0 || C < 1 || S < 1 || S > 64 || G < 1 || C % G != 0 || C > (1 << 20) || T > INT32_MAX || N > INT32_MAX - 1) return 0;
+  if (!scan_shape(T, N, C, S, G)) return 0;
   const int64_t tiles = G * ssm_tiles(C / G, S);
   return (size_t)over_rows_bytes(ssm_workers(N, tiles, sm_count()), C, S) + (size_t)tiles * (size_t)T * (size_t)(8 * 4 * ssm_lanes(S));
 }

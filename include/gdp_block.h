@@ -141,6 +141,8 @@ typedef struct gdp_scan_args {
   const int32_t *state_indices;
   int64_t num_slots;
   float *chunk_states;
+  void *workspace; /* >= gdp_scan_forward_workspace_bytes(T, N, C, S, G), 256-byte aligned; NULL where that is 0 */
+  size_t workspace_bytes;
   uint32_t *device_status;
   int cu_seqlens_int64;
   int x_dtype;  /* GDP_DTYPE_BF16, _F16 or _F32 */
@@ -152,6 +154,9 @@ typedef struct gdp_scan_args {
 gdp_status gdp_selective_scan(const gdp_scan_args *args, void *stream);
 gdp_status gdp_selective_scan_decode(const gdp_scan_args *args, void *stream);
 int64_t gdp_scan_chunk_rows(int64_t T, int64_t N);
+/* Few sequences of few channels run in pieces side by side, whose states are joined through this workspace (0: none
+   is needed; decode needs none). */
+size_t gdp_scan_forward_workspace_bytes(int64_t T, int64_t N, int64_t C, int64_t S, int64_t G);
 
 /*
  * gdp_selective_scan_backward: gradients for dL/dy = d_output and dL/dfinal = d_final_state (or NULL), from

@@ -160,6 +160,12 @@ SCAN = [
     ([1] * 100, 36, 16, 1, F32, F32, True, False, True, "dense"), ([1200], 32, 16, 1, BF16, BF16, True, True, True, "dense"),
     ([700, 701], 16, 17, 1, F32, F32, True, True, True, "dense"),
 ]
+# few sequences of few channels: the plan runs them in pieces
+PIECES = [
+    ([1200], 32, 16, 1, BF16, BF16, True, True, True, "dense"), ([600], 20, 5, 2, F32, F32, True, True, True, "odd"),
+    ([100, 0, 300, 64, 1, 1500, 0], 40, 16, 1, BF16, F32, True, False, True, "slice"), ([0, 900, 0], 48, 32, 1, F16, F16, True, True, False, "dense"),
+    ([129, 127, 128, 640], 9, 64, 1, F32, F32, False, True, True, "dense"),
+]
 
 
 def _scan_case(case, init=True):
@@ -184,7 +190,7 @@ def _scan_reference(v, lengths, softplus):
 
 
 @pytest.mark.parametrize("init", [False, True])
-@pytest.mark.parametrize("case", SCAN)
+@pytest.mark.parametrize("case", SCAN + PIECES)
 def test_scan(cuda_device, case, init):
     lengths, softplus, layout, dev = case[0], case[6], case[-1], cuda_device
     v = _scan_case(case, init)
@@ -198,7 +204,7 @@ def test_scan(cuda_device, case, init):
 
 
 @pytest.mark.parametrize("init", [False, True])
-@pytest.mark.parametrize("case", SCAN)
+@pytest.mark.parametrize("case", SCAN + PIECES)
 def test_scan_backward(cuda_device, case, init):
     lengths, softplus, layout, dev = case[0], case[6], case[-1], cuda_device
     v = _scan_case(case, init)
@@ -212,6 +218,12 @@ def test_scan_backward(cuda_device, case, init):
         assert (got[name] is None) == (given is None), name
     assert got["dB"].shape == v["B"].shape and got["ddt"].dtype == v["dt"].dtype
     _close(got, R.scan_backward(*args, v["dy"], lengths, dfin=v["dfin"], **kw))
+
+
+@pytest.mark.parametrize("case", PIECES)
+def test_pieces_are_used(cuda_device, case):
+    lengths, C, S, G = case[:4]
+    assert pkg.gdp_scan_forward_workspace_bytes(sum(lengths), len(lengths), C, S, G) > 0
 
 
 def test_scan_without_groups(cuda_device):
