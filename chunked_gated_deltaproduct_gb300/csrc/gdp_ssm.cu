@@ -73,7 +73,7 @@ bool scan_shape(int64_t T, int64_t N, int64_t C, int64_t S, int64_t G) {
   return T >= 0 && N >= 0 && C >= 1 && S >= 1 && S <= 64 && G >= 1 && C % G == 0 && C <= (1 << 20) && T <= INT32_MAX && N < INT32_MAX;
 }
 int64_t enter_bytes(int64_t pieces, int64_t C, int64_t S) { return (pieces * C * S * 4 + 255) / 256 * 256; }
-int64_t over_rows_bytes(int64_t workers, int64_t C, int64_t S) { return (workers * C * (S + 2) * 4 + 255) / 256 * 256; }
+int64_t over_rows_bytes(int64_t workers, int64_t C, int64_t S) { return (workers * ssm_sum_cols(C, S) * 4 + 255) / 256 * 256; }
 
 }  // namespace
 }  // namespace layer
@@ -125,8 +125,10 @@ GDP_EXPORT int64_t gdp_scan_chunk_rows(int64_t T, int64_t N) { return T < 0 || N
 GDP_EXPORT size_t gdp_scan_workspace_bytes(int64_t T, int64_t N, int64_t C, int64_t S, int64_t G) {
   using namespace gdp::layer;
   if (!scan_shape(T, N, C, S, G)) return 0;
-  const int64_t tiles = G * ssm_tiles(C / G, S);
-  return (size_t)over_rows_bytes(ssm_workers(N, tiles, sm_count()), C, S) + (size_t)tiles * (size_t)T * (size_t)(8 * 4 * ssm_lanes(S));
+  const int64_t tiles = G * ssm_tiles(C / G, S), piece = ssm_piece(T, N, tiles, sm_count()), pieces = piece ? T / piece + N : N;
+  size_t bytes = (size_t)over_rows_bytes(ssm_workers(pieces, tiles, sm_count()), C, S) + (size_t)tiles * (size_t)T * (size_t)(8 * 4 * ssm_lanes(S));
+  if (piece) bytes += (size_t)enter_bytes(pieces, C, S) + (size_t)pieces * (size_t)C * 4;
+  return bytes;
 }
 
 GDP_EXPORT gdp_status gdp_selective_scan_backward(const gdp_scan_backward_args *a, void *stream) {
@@ -168,17 +170,25 @@ GDP_EXPORT gdp_status gdp_selective_scan_backward(const gdp_scan_backward_args *
   p.chunks = const_cast<float *>(a->chunk_states);
   p.dx = a->dx; p.ddt = a->ddt; p.dz = a->z ? a->dz : nullptr; p.dB = a->dB; p.dC = a->dC; p.dinit = a->d_initial_state;
   p.quad_states = a->S % 4 == 0 && aligned(a->chunk_states, 16) && aligned(a->d_final_state, 16) && aligned(a->d_initial_state, 16);
-  p.workers = ssm_workers(p.p.N, p.G * p.tiles, sm_count());
+  p.fast_rows = p.fast_rows && rows_by(p.dy, p.dy_st, p.p.T, a->x_dtype, 16);
+  p.pair_out = p.pair_out && aligned(p.dx, 2 * dtype_size(a->x_dtype)) && aligned(p.dz, 2 * dtype_size(a->x_dtype)) && aligned(p.ddt, 2 * dtype_size(a->dt_dtype));
+  p.piece = ssm_piece(p.p.T, p.p.N, p.G * p.tiles, p.sms);
+  p.pieces = p.piece ? p.p.T / p.piece + p.p.N : p.p.N;
+  p.workers = ssm_workers(p.pieces, p.G * p.tiles, p.sms);
   p.over_rows = static_cast<float *>(a->workspace);
   p.over_channels = p.over_rows + over_rows_bytes(p.workers, p.C, p.S) / 4;
+  if (p.piece) {
+    p.enter = p.over_channels + p.G * p.tiles * p.p.T * 8 * ssm_lanes(p.S);
+    p.spans = p.enter + enter_bytes(p.pieces, p.C, p.S) / 4;
+  }
   cudaError_t e = a->x_dtype == GDP_DTYPE_BF16  ? launch_ssm_bwd<__nv_bfloat16>(p, s)
                   : a->x_dtype == GDP_DTYPE_F16 ? launch_ssm_bwd<__half>(p, s)
                                                 : launch_ssm_bwd<float>(p, s);
   if (e == cudaSuccess) {
     ColumnSums c{};
-    c.from = p.over_rows; c.parts = p.workers; c.cols = p.C * (p.S + 2);
+    c.from = p.over_rows; c.parts = p.workers; c.cols = ssm_sum_cols(p.C, p.S);
     c.to[0] = a->dA; c.to[1] = a->dD; c.to[2] = a->ddt_bias;
-    c.first[1] = p.C * p.S; c.first[2] = p.C * (p.S + 1); c.first[3] = c.cols;
+    c.first[1] = p.C * p.S; c.first[2] = p.C * (p.S + 1); c.first[3] = p.C * (p.S + 2);
     e = launch_column_sums(c, s);
   }
   return cuda_status(e, "selective scan backward kernels");

@@ -32,7 +32,7 @@ struct SsmProblem {
   const float *dfin;
   void *dx, *ddt, *dz, *dB, *dC;
   float *dinit;
-  float *over_rows;      // [workers][C (S + 2)]: sums over a worker's rows for dA, dD, ddt_bias
+  float *over_rows;      // [workers][ssm_sum_cols]: sums over a worker's rows for dA, dD, ddt_bias
   float *over_channels;  // [G tiles][T][2 padded S]: a CTA's channels' sums for dB and dC
   int64_t workers;       // CTAs that share the sequences
 };
@@ -63,6 +63,9 @@ inline int64_t ssm_piece(int64_t T, int64_t N, int64_t tiles, int sms) {
   n = (n + 31) / 32 * 32;
   return n < 128 ? 128 : n;
 }
+
+// Columns of the backward pass's sums over rows: C S, C and C, and up to a multiple of 16 bytes.
+__host__ __device__ inline int64_t ssm_sum_cols(int64_t C, int64_t S) { return (C * (S + 2) + 3) / 4 * 4; }
 
 template <typename T>
 cudaError_t launch_ssm_fwd(const SsmProblem &p, cudaStream_t stream);

@@ -1,0 +1,539 @@
+// gdp_ssm_bwd_body.cuh -- the selective state space scan's backward kernels, instantiated by type in gdp_ssm_bwd_*.cu.
+#pragma once
+
+#include "gdp_ssm_parts.cuh"
+
+namespace gdp {
+namespace layer {
+
+// Chunk by chunk from a piece's end.  As in the forward pass, feeding warps bring rows (and the states entering the
+// chunks), form e, e x and dy, and finish gradients, while running warps hold two channels by four states a lane.  The
+// states before a chunk's tokens are formed again from the entering one: once through for those before every fourth
+// token, then four tokens at a time into registers, with their decays, which the same four tokens going back use.  A
+// token's sums over the CTA's channels (dB, dC) are made by shuffles in each running warp and added up by the feeding ones.
+
+template <typename T, int L>
+struct SsmBack {
+  static constexpr int CH = kSsmThreads / L, SP = L * kQ, K = kSsmChunk, RT = kSsmThreads / 2, W = RT / 32, YP = CH + 8;
+  __host__ __device__ static constexpr int stage(int dt_size, bool gated) {
+    return K * CH * ((int)sizeof(T) * (gated ? 3 : 2) + dt_size) + 2 * K * SP * (int)sizeof(T) + CH * SP * 4;
+  }
+  // two tiles of: e and e x, dy, B and C; u, v and y; the running warps' sums
+  static constexpr int formed = K * CH * 12 + 2 * K * SP * 4, made = 3 * K * YP * 4, sums = W * K * 2 * SP * 4, starts = 4 * RT * 8 * 4;
+  __host__ __device__ static constexpr int bytes(int dt_size, bool gated) { return kSsmStages * stage(dt_size, gated) + 2 * (formed + made + sums) + starts; }
+};
+
+template <typename T, int L, bool FULL, bool LOCAL>
+__global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_kernel(const SsmProblem p) {
+  using Back = SsmBack<T, L>;
+  constexpr int CH = Back::CH, SP = Back::SP, K = Back::K, CP = CH / 2, HT = kSsmFeed, RT = Back::RT, W = Back::W, YP = Back::YP, R = 32 / L;
+  constexpr float kLn2 = 0.69314718055994531f;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int dt_size = p.dt_f32 ? 4 : (int)sizeof(T), stage_bytes = Back::stage(dt_size, p.z != nullptr);
+  float2 *steps = reinterpret_cast<float2 *>(smem);            // [2][K][CH]: e, e x
+  float *gs = reinterpret_cast<float *>(steps + 2 * K * CH);   // [2][K][CH]: dy
+  float *Bs = gs + 2 * K * CH, *Cs = Bs + 2 * K * SP;          // [2][K][SP]
+  float *us = Cs + 2 * K * SP, *vs = us + 2 * K * YP, *ys = vs + 2 * K * YP;  // [2][K][YP]
+  float *sums = ys + 2 * K * YP;                               // [2][W][K][2 SP]
+  float4 *starts = reinterpret_cast<float4 *>(sums + 2 * W * K * 2 * SP);  // [4][2][RT]: a running thread's states before every fourth token
+  unsigned char *ring = reinterpret_cast<unsigned char *>(starts + 4 * 2 * RT);
+  struct Stage {
+    unsigned char *x, *dt, *dy, *z, *B, *C;
+    float *h;  // [CH][S]
+  };
+  auto stage = [&](int k) {
+    Stage s;
+    s.x = ring + (k % kSsmStages) * stage_bytes;
+    s.dy = s.x + K * CH * sizeof(T);
+    s.B = s.dy + K * CH * sizeof(T);
+    s.C = s.B + K * SP * sizeof(T);
+    s.h = reinterpret_cast<float *>(s.C + K * SP * sizeof(T));
+    s.dt = reinterpret_cast<unsigned char *>(s.h + CH * SP);
+    s.z = s.dt + K * CH * dt_size;
+    return s;
+  };
+  const unsigned across = (unsigned)(p.G * p.tiles), tile = blockIdx.x % across;
+  const int64_t worker = blockIdx.x / across, g = tile / p.tiles, c0 = g * p.per + (tile % p.tiles) * CH;
+  const int cn = (int)min((int64_t)CH, (g + 1) * p.per - c0);
+  if (blockIdx.x == 0 && !LOCAL) check_packed(p.p);
+  if (LOCAL) sm100::pdl_trigger();
+  if (worker == p.workers) {
+    zero_tail<T>(p, static_cast<T *>(p.dx), c0, cn);
+    zero_tail<T>(p, static_cast<T *>(p.dz), c0, cn);
+    if (p.dt_f32) zero_tail<float>(p, static_cast<float *>(p.ddt), c0, cn);
+    else zero_tail<T>(p, static_cast<T *>(p.ddt), c0, cn);
+    if (p.piece) sm100::pdl_wait();
+    return;
+  }
+  const bool running = threadIdx.x < RT;
+  float *out = p.over_rows + worker * ssm_sum_cols(p.C, p.S);
+  if (running) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, j = lane % L, rank = lane / L, ch = threadIdx.x / L * 2;
+    const int64_t mine = (c0 + ch) * p.S + j * kQ;
+    const int states = max(0, min(kQ, (int)p.S - j * kQ));
+    int n[2];
+    float2 A[2][2], dA[2][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      n[k] = ch + k < cn ? states : 0;
+      float v[kQ];
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) v[q] = q < n[k] ? p.A[mine + k * p.S + q] * kLog2e : -1.f;
+      A[k][0] = make_float2(v[0], v[1]);
+      A[k][1] = make_float2(v[2], v[3]);
+      dA[k][0] = dA[k][1] = make_float2(0.f, 0.f);
+    }
+    // padded states stay zero, whatever the inputs are
+    auto real = [&](float2 v, int q) { return FULL ? v : make_float2(2 * q < states ? v.x : 0.f, 2 * q + 1 < states ? v.y : 0.f); };
+    auto pairs = [](float4 v, float2 (&o)[2]) {
+      o[0] = make_float2(v.x, v.y);
+      o[1] = make_float2(v.z, v.w);
+    };
+    auto save = [&](float *to, const float2 (&v)[2][2]) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float o[kQ] = {v[k][0].x, v[k][0].y, v[k][1].x, v[k][1].y};
+        store_states(to + k * p.S, n[k], p.quad_states, o);
+      }
+    };
+    if (p.piece && !LOCAL) sm100::pdl_wait();
+    for (int64_t r = worker; r < p.pieces; r += p.workers) {
+      const SsmPiece at_rows(p, r);
+      if (p.piece && (at_rows.b >= at_rows.e || (LOCAL && at_rows.first))) continue;
+      const int chunks = (int)((at_rows.e - at_rows.b + K - 1) / K);
+      float2 back[2][2];  // exp(e A) H of the token after
+      {
+        const float *from = LOCAL ? nullptr : p.piece ? p.enter + r * p.C * p.S : p.dfin ? p.dfin + at_rows.i * p.C * p.S : nullptr;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float v[kQ] = {};
+          if (from) load_states(from + mine + k * p.S, n[k], p.quad_states, v);
+          back[k][0] = make_float2(v[0], v[1]);
+          back[k][1] = make_float2(v[2], v[3]);
+        }
+      }
+      float span[2] = {};
+      __syncthreads();
+      for (int k = 0; k < chunks; ++k) {
+        const int at = (k & 1) * K, rows = k == 0 ? (int)(at_rows.e - at_rows.b) - (chunks - 1) * K : K;
+        if constexpr (LOCAL) {
+#pragma unroll 4
+          for (int t = rows - 1; t >= 0; --t) {
+            const float4 d = *reinterpret_cast<const float4 *>(steps + (at + t) * CH + ch);
+            const float2 gd = *reinterpret_cast<const float2 *>(gs + (at + t) * CH + ch);
+            float2 Cv[2];
+            pairs(*reinterpret_cast<const float4 *>(Cs + (at + t) * SP + j * kQ), Cv);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float e = c ? d.z : d.x;
+              span[c] += e;
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const float2 x = mul2(both(e), A[c][q]);
+                back[c][q] = mul2(make_float2(ex2(x.x), ex2(x.y)), real(fma2(both(c ? gd.y : gd.x), Cv[q], back[c][q]), q));
+              }
+            }
+          }
+        } else {
+          float2 h[2][2];
+          const float *from = stage(k).h + ch * p.S + j * kQ;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float v[kQ];
+            load_states(from + c * p.S, n[c], FULL, v);
+            h[c][0] = make_float2(v[0], v[1]);
+            h[c][1] = make_float2(v[2], v[3]);
+          }
+          // h of the token at t from the one before; `decay` its factor
+          auto forth = [&](int t, float2 (&decay)[2][2]) {
+            const float4 d = *reinterpret_cast<const float4 *>(steps + (at + t) * CH + ch);
+            float2 Bv[2];
+            pairs(*reinterpret_cast<const float4 *>(Bs + (at + t) * SP + j * kQ), Bv);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const float2 x = mul2(both(c ? d.z : d.x), A[c][q]);
+                decay[c][q] = make_float2(ex2(x.x), ex2(x.y));
+                h[c][q] = fma2(decay[c][q], h[c][q], real(mul2(both(c ? d.w : d.y), Bv[q]), q));
+              }
+          };
+          auto copy = [](float2 (&to)[2][2], const float2 (&from)[2][2]) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) to[c][0] = from[c][0], to[c][1] = from[c][1];
+          };
+          auto keep = [&](int q) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) starts[(q * 2 + c) * RT + threadIdx.x] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
+          };
+          float2 unused[2][2];
+          keep(0);
+#pragma unroll 1
+          for (int q = 1; 4 * q < rows; ++q) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) forth(4 * q - 4 + u, unused);
+            keep(q);
+          }
+          // four tokens from t on (m of them exist), there and back
+          auto four = [&](int t, int m, auto whole) {
+            constexpr bool ALL = decltype(whole)::value;
+            float2 before[4][2][2], decay[4][2][2];
+            float u[8], v[8], y[8];
+            float *to = sums + (((k & 1) * W + warp) * K + t) * 2 * SP + j * kQ;
+            constexpr int kept = 2 * kQ / R > 0 ? 2 * kQ / R : 1;  // sums over channels that a lane ends up with
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              if (!ALL && w >= m) break;
+              copy(before[w], h);
+              forth(t + w, decay[w]);
+              if (p.z) {
+                float2 Cv[2];
+                pairs(*reinterpret_cast<const float4 *>(Cs + (at + t + w) * SP + j * kQ), Cv);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  const float2 sum = fma2(Cv[1], h[c][1], mul2(Cv[0], h[c][0]));
+                  y[2 * w + c] = sum.x + sum.y;
+                }
+              }
+            }
+            // (h: after the last of them)
+#pragma unroll
+            for (int w = 3; w >= 0; --w) {
+              if (!ALL && w >= m) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) u[2 * w + c] = v[2 * w + c] = y[2 * w + c] = 0.f;
+                continue;
+              }
+              const float4 d = *reinterpret_cast<const float4 *>(steps + (at + t + w) * CH + ch);
+              const float2 gd = *reinterpret_cast<const float2 *>(gs + (at + t + w) * CH + ch);
+              float2 Bv[2], Cv[2], sB[2], sC[2];
+              pairs(*reinterpret_cast<const float4 *>(Bs + (at + t + w) * SP + j * kQ), Bv);
+              pairs(*reinterpret_cast<const float4 *>(Cs + (at + t + w) * SP + j * kQ), Cv);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const float2 gg = both(c ? gd.y : gd.x), ee = both(c ? d.z : d.x), ex = both(c ? d.w : d.y);
+                float2 uu, vv;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  const float2 H = real(fma2(gg, Cv[q], back[c][q]), q);
+                  sB[q] = c ? fma2(H, ex, sB[q]) : mul2(H, ex);
+                  sC[q] = c ? fma2(gg, h[c][q], sC[q]) : mul2(gg, h[c][q]);
+                  uu = q ? fma2(H, Bv[q], uu) : mul2(H, Bv[q]);
+                  back[c][q] = mul2(H, decay[w][c][q]);
+                  const float2 x = mul2(back[c][q], before[w][c][q]);
+                  vv = q ? fma2(x, A[c][q], vv) : mul2(x, A[c][q]);
+                  dA[c][q] = fma2(x, ee, dA[c][q]);
+                }
+                u[2 * w + c] = uu.x + uu.y;
+                v[2 * w + c] = vv.x + vv.y;
+              }
+              float s[2 * kQ] = {sB[0].x, sB[0].y, sB[1].x, sB[1].y, sC[0].x, sC[0].y, sC[1].x, sC[1].y};
+              sum_scatter<2 * kQ, R, L>(s, rank);
+#pragma unroll
+              for (int q = 0; q < kept; ++q) {
+                const int which = rank * kept + q;  // state of dB, then of dC
+                to[w * 2 * SP + which / kQ * SP + which % kQ] = s[q];
+              }
+              copy(h, before[w]);
+            }
+            auto spread = [&](float (&v)[8], float *to) {
+              sum_scatter<8, L, 1>(v, j);
+              to += (at + t) * YP + ch;
+              if constexpr (L == 4) *reinterpret_cast<float2 *>(to + j * YP) = make_float2(v[0], v[1]);
+              else if (L == 8 || j % 2 == 0) to[(L == 8 ? j : j / 2) / 2 * YP + (L == 8 ? j : j / 2) % 2] = v[0];
+            };
+            spread(u, us);
+            spread(v, vs);
+            if (p.z) spread(y, ys);
+          };
+#pragma unroll 1
+          for (int q = (rows - 1) / 4; q >= 0; --q) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) pairs(starts[(q * 2 + c) * RT + threadIdx.x], h[c]);
+            const int m = rows - 4 * q;
+            if (m >= 4) four(4 * q, 4, std::true_type{});
+            else four(4 * q, m, std::false_type{});
+          }
+        }
+        __syncthreads();
+      }
+      if (LOCAL) {
+        save(p.enter + r * p.C * p.S + mine, back);
+        if (j == 0)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (ch + k < cn) p.spans[r * p.C + c0 + ch + k] = span[k];
+      } else if (p.dinit && at_rows.first) {
+        save(p.dinit + at_rows.i * p.C * p.S + mine, back);
+      }
+    }
+    if (!LOCAL) save(out + mine, dA);
+    return;
+  }
+  // ---- feeding ----
+  const int thread = threadIdx.x - RT, c = thread % CP * 2, t0 = thread / CP;  // first of the thread's two channels, its first token
+  constexpr int STEP = HT / CP, ITEMS = (K + STEP - 1) / STEP;
+  const float bias[2] = {p.bias && c < cn ? p.bias[c0 + c] : 0.f, p.bias && c + 1 < cn ? p.bias[c0 + c + 1] : 0.f};
+  const float2 D = make_float2(p.D && c < cn ? p.D[c0 + c] : 0.f, p.D && c + 1 < cn ? p.D[c0 + c + 1] : 0.f);
+  float2 dD = make_float2(0.f, 0.f), dbias = make_float2(0.f, 0.f);
+  for (int64_t r = worker; r < p.pieces; r += p.workers) {
+    const SsmPiece at_rows(p, r);
+    if (p.piece && (at_rows.b >= at_rows.e || (LOCAL && at_rows.first))) continue;
+    const int chunks = (int)((at_rows.e - at_rows.b + K - 1) / K);
+    // step k goes over chunk chunks - 1 - k
+    auto first_row = [&](int k) { return at_rows.b + (int64_t)(chunks - 1 - k) * K; };
+    auto rows_of = [&](int k) { return k == 0 ? (int)(at_rows.e - at_rows.b) - (chunks - 1) * K : K; };
+    auto bring = [&](int k) {
+      if (k < chunks) {
+        const int64_t row = first_row(k);
+        const int rows = rows_of(k);
+        const Stage s = stage(k);
+        fill<T, CH, HT, K>(s.x, p.x, p.x_st, c0, cn, row, rows, p.fast_rows, thread);
+        fill<T, CH, HT, K>(s.dy, p.dy, p.dy_st, c0, cn, row, rows, p.fast_rows, thread);
+        if (p.dt_f32) fill<float, CH, HT, K>(s.dt, p.dt, p.dt_st, c0, cn, row, rows, p.fast_rows, thread);
+        else fill<T, CH, HT, K>(s.dt, p.dt, p.dt_st, c0, cn, row, rows, p.fast_rows, thread);
+        if (p.z) fill<T, CH, HT, K>(s.z, p.z, p.z_st, c0, cn, row, rows, p.fast_rows, thread);
+        fill<T, SP, HT, K>(s.C, p.Cm, p.C_st, g * p.C_sg, (int)p.S, row, rows, p.fast_vectors, thread);
+        if (!LOCAL) {
+          fill<T, SP, HT, K>(s.B, p.B, p.B_st, g * p.B_sg, (int)p.S, row, rows, p.fast_vectors, thread);
+          const float *from = p.chunks + (at_rows.chunk + chunks - 1 - k) * p.C * p.S + c0 * p.S;
+          if (p.quad_states) {
+            for (int q = thread * kQ; q < cn * (int)p.S; q += HT * kQ) sm100::cp_async16(s.h + q, from + q, 16u);
+          } else {
+            for (int q = thread; q < cn * (int)p.S; q += HT) s.h[q] = from[q];
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto form = [&](int k) {
+      const Stage s = stage(k);
+      const int at = (k & 1) * K, rows = rows_of(k);
+      float2 v[ITEMS], x[ITEMS], d[ITEMS];
+#pragma unroll
+      for (int m = 0; m < ITEMS; ++m) {
+        const int t = t0 + m * STEP, o = (K % STEP == 0 || t < K ? t : 0) * CH + c;
+        v[m] = add2(p.dt_f32 ? load_pair<float>(s.dt, o) : load_pair<T>(s.dt, o), make_float2(bias[0], bias[1]));
+        x[m] = load_pair<T>(s.x, o);
+        d[m] = load_pair<T>(s.dy, o);
+      }
+      if (p.softplus)
+#pragma unroll
+        for (int m = 0; m < ITEMS; ++m) v[m] = softplus2(v[m]);
+      if (p.z)
+#pragma unroll
+        for (int m = 0; m < ITEMS; ++m) {
+          const int t = t0 + m * STEP;
+          const float2 z = load_pair<T>(s.z, (K % STEP == 0 || t < K ? t : 0) * CH + c);
+          d[m] = mul2(d[m], mul2(z, make_float2(sigmoid_fast(z.x), sigmoid_fast(z.y))));
+        }
+#pragma unroll
+      for (int m = 0; m < ITEMS; ++m) {
+        const int t = t0 + m * STEP;
+        if (t >= rows) continue;
+        const float2 in = mul2(v[m], x[m]);
+        *reinterpret_cast<float4 *>(steps + (at + t) * CH + c) = make_float4(v[m].x, in.x, v[m].y, in.y);
+        *reinterpret_cast<float2 *>(gs + (at + t) * CH + c) = d[m];
+      }
+#pragma unroll
+      for (int q = thread * kQ; q < K * SP; q += HT * kQ) {
+        const float2 a0 = load_pair<T>(s.C, q), a1 = load_pair<T>(s.C, q + 2);
+        *reinterpret_cast<float4 *>(Cs + at * SP + q) = make_float4(a0.x, a0.y, a1.x, a1.y);
+        if (!LOCAL) {
+          const float2 b0 = load_pair<T>(s.B, q), b1 = load_pair<T>(s.B, q + 2);
+          *reinterpret_cast<float4 *>(Bs + at * SP + q) = make_float4(b0.x, b0.y, b1.x, b1.y);
+        }
+      }
+    };
+    auto put = [&](void *base, int64_t o, float2 v, auto type) {
+      using V = decltype(type);
+      V *to = static_cast<V *>(base) + o;
+      if (p.pair_out) {
+        if (c < cn) {
+          if constexpr (sizeof(V) == 4) *reinterpret_cast<float2 *>(to) = v;
+          else *reinterpret_cast<uint32_t *>(to) = narrow<V>(v);
+        }
+      } else {
+        if (c < cn) to[0] = from_f32<V>(v.x);
+        if (c + 1 < cn) to[1] = from_f32<V>(v.y);
+      }
+    };
+    auto finish = [&](int k) {
+      const Stage s = stage(k);
+      const int at = (k & 1) * K, rows = rows_of(k);
+      const int64_t row = first_row(k);
+      float2 sum = make_float2(0.f, 0.f), more = sum;
+#pragma unroll
+      for (int m = 0; m < ITEMS; ++m) {
+        const int t = t0 + m * STEP;
+        if (t >= rows) continue;
+        const int o = t * CH + c;
+        const int64_t to = (row + t) * p.C + c0 + c;
+        const float4 d = *reinterpret_cast<const float4 *>(steps + at * CH + o);
+        const float2 gd = *reinterpret_cast<const float2 *>(gs + at * CH + o), x = load_pair<T>(s.x, o);
+        const float2 u = *reinterpret_cast<const float2 *>(us + (at + t) * YP + c), v = *reinterpret_cast<const float2 *>(vs + (at + t) * YP + c);
+        put(p.dx, to, fma2(u, make_float2(d.x, d.z), mul2(gd, D)), T());
+        float2 dt = fma2(v, both(kLn2), mul2(u, x));
+        if (p.softplus) {
+          const float2 w = add2(p.dt_f32 ? load_pair<float>(s.dt, o) : load_pair<T>(s.dt, o), make_float2(bias[0], bias[1]));
+          dt = mul2(dt, make_float2(sigmoid_fast(w.x), sigmoid_fast(w.y)));
+        }
+        if (p.dt_f32) put(p.ddt, to, dt, float());
+        else put(p.ddt, to, dt, T());
+        sum = fma2(gd, x, sum);
+        more = add2(dt, more);
+        if (p.z) {
+          const float2 z = load_pair<T>(s.z, o), dy = load_pair<T>(s.dy, o);
+          const float2 y = fma2(D, x, *reinterpret_cast<const float2 *>(ys + (at + t) * YP + c));
+          const float q0 = sigmoid_fast(z.x), q1 = sigmoid_fast(z.y);
+          put(p.dz, to, mul2(mul2(dy, y), make_float2(q0 * fmaf(z.x, 1.f - q0, 1.f), q1 * fmaf(z.y, 1.f - q1, 1.f))), T());
+        }
+      }
+      dD = add2(dD, sum);
+      dbias = add2(dbias, more);
+      const float *part = sums + (k & 1) * W * K * 2 * SP;
+      float *to = p.over_channels + ((int64_t)tile * p.p.T + row) * (2 * SP);
+      for (int q = thread * kQ; q < rows * 2 * SP; q += HT * kQ) {
+        float4 v = *reinterpret_cast<const float4 *>(part + q);
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+          const float4 o = *reinterpret_cast<const float4 *>(part + w * K * 2 * SP + q);
+          v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+        }
+        *reinterpret_cast<float4 *>(to + q) = v;
+      }
+    };
+    auto meet = [&](bool all) {  // the feeding warps' copies (but the last group) have landed
+      if (all) asm volatile("cp.async.wait_group 0;" ::: "memory");
+      else asm volatile("cp.async.wait_group 1;" ::: "memory");
+      asm volatile("bar.sync 1, %0;" ::"n"(HT) : "memory");
+    };
+    bring(0);
+    bring(1);
+    meet(false);
+    if (chunks > 0) form(0);
+    __syncthreads();
+    for (int k = 0; k < chunks; ++k) {
+      bring(k + 2);
+      if (!LOCAL && k > 0) finish(k - 1);
+      meet(false);
+      if (k + 1 < chunks) form(k + 1);
+      __syncthreads();
+    }
+    if (!LOCAL && chunks > 0) finish(chunks - 1);
+    meet(true);  // before the stages are used again
+  }
+  if (LOCAL) return;
+  // dD and ddt_bias: a channel's rows are spread over the threads that share its number
+  float4 *share = reinterpret_cast<float4 *>(ring);
+  share[thread] = make_float4(dD.x, dD.y, dbias.x, dbias.y);
+  asm volatile("bar.sync 1, %0;" ::"n"(HT) : "memory");
+  if (thread < CP) {
+    float4 v = share[thread];
+    for (int k = 1; k < HT / CP; ++k) {
+      const float4 o = share[k * CP + thread];
+      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+    }
+    float *to = out + p.C * p.S + c0 + c;
+    if (c < cn) to[0] = v.x, to[p.C] = v.z;
+    if (c + 1 < cn) to[1] = v.y, to[p.C + 1] = v.w;
+  }
+}
+
+// The gradients entering every piece of a sequence from behind, from those that the pieces pass on from zero.
+template <int V>
+__global__ void __launch_bounds__(kSsmThreads) gdp_ssm_join_back_kernel(const SsmProblem p) {
+  const int64_t i = blockIdx.x, at = ((int64_t)blockIdx.y * kSsmThreads + threadIdx.x) * V, per = p.C * p.S;
+  sm100::pdl_trigger();
+  sm100::pdl_wait();
+  if (at >= per) return;
+  int64_t b, e;
+  seq_rows(p.p, i, &b, &e);
+  float S[V] = {}, A[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    if (p.dfin) S[k] = p.dfin[i * per + at + k];
+    A[k] = p.A[at + k] * kLog2e;
+  }
+  if (b == e) {  // no piece will write the initial state's
+    if (p.dinit)
+#pragma unroll
+      for (int k = 0; k < V; ++k) p.dinit[i * per + at + k] = S[k];
+    return;
+  }
+  const int64_t r = b / p.piece + i, n = (e - b + p.piece - 1) / p.piece, c = at / p.S;
+  float *enter = p.enter + r * per + at;
+  const float *spans = p.spans + r * p.C + c;
+  constexpr int AHEAD = 16;
+  for (int64_t q = n - 1; q >= 0; q -= AHEAD) {
+    float E[AHEAD][V], span[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (q - u > 0) {
+        span[u] = spans[(q - u) * p.C];
+        const Vec<float, V> v = load_vec<float, V>(enter + (q - u) * per);
+#pragma unroll
+        for (int k = 0; k < V; ++k) E[u][k] = v.v[k];
+      }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (q - u >= 0) {
+        store_vec<float, V>(enter + (q - u) * per, S);
+        if (q - u > 0)
+#pragma unroll
+          for (int k = 0; k < V; ++k) S[k] = carry(S[k], E[u][k], A[k] * span[u]);
+      }
+  }
+}
+
+// dB and dC: the sums over the CTAs that share a group's channels, in their order; padding rows are zeros.
+template <typename T>
+__global__ void __launch_bounds__(256) gdp_ssm_vectors_kernel(const SsmProblem p, int SP) {
+  const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = k / (2 * SP), g = blockIdx.y;
+  if (row >= p.p.T) return;
+  const int s = (int)(k % (2 * SP)), state = s % SP;
+  if (state >= p.S) return;
+  float v = 0.f;
+  if (row < cu_at(p.p, p.p.N)) {
+    const float *from = p.over_channels + (g * p.tiles * p.p.T + row) * (2 * SP) + s;
+#pragma unroll 4
+    for (int64_t i = 0; i < p.tiles; ++i) v += from[i * p.p.T * (2 * SP)];
+  }
+  static_cast<T *>(s < SP ? p.dB : p.dC)[(row * p.G + g) * p.S + state] = from_f32<T>(v);
+}
+
+template <typename T, int L, bool FULL, bool LOCAL>
+cudaError_t ssm_bwd(const SsmProblem &p, cudaStream_t stream) {
+  using Back = SsmBack<T, L>;
+  constexpr int most = Back::bytes(4, true);
+  static_assert(most <= 227 * 1024, "fits an SM");
+  const auto kernel = gdp_ssm_bwd_kernel<T, L, FULL, LOCAL>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e != cudaSuccess) return e;
+  return gdp::launch_kernel(kernel, dim3((unsigned)((p.workers + (LOCAL ? 0 : 1)) * p.G * p.tiles)), dim3(kSsmFeed + kSsmThreads / 2),
+                            Back::bytes(p.dt_f32 ? 4 : (int)sizeof(T), p.z != nullptr), stream, p.piece && !LOCAL, p);
+}
+template <typename T, int L>
+cudaError_t ssm_bwd_by(const SsmProblem &p, cudaStream_t stream) {
+  if (p.piece) {
+    cudaError_t e = ssm_bwd<T, L, false, true>(p, stream);
+    if (e != cudaSuccess) return e;
+    const int64_t per = p.C * p.S, v = p.quad_states ? kQ : 1;
+    const dim3 grid((unsigned)p.p.N, (unsigned)((per / v + kSsmThreads - 1) / kSsmThreads));
+    e = gdp::launch_kernel(p.quad_states ? gdp_ssm_join_back_kernel<kQ> : gdp_ssm_join_back_kernel<1>, grid, dim3(kSsmThreads), 0, stream, true, p);
+    if (e != cudaSuccess) return e;
+  }
+  return p.S == L * kQ ? ssm_bwd<T, L, true, false>(p, stream) : ssm_bwd<T, L, false, false>(p, stream);
+}
+template <typename T>
+cudaError_t launch_ssm_bwd(const SsmProblem &p, cudaStream_t stream) {
+  const int lanes = ssm_lanes(p.S), SP = lanes * kQ;
+  cudaError_t e = lanes == 4 ? ssm_bwd_by<T, 4>(p, stream) : lanes == 8 ? ssm_bwd_by<T, 8>(p, stream) : ssm_bwd_by<T, 16>(p, stream);
+  if (e != cudaSuccess || p.p.T == 0) return e;
+  gdp_ssm_vectors_kernel<T><<<dim3((unsigned)((p.p.T * 2 * SP + 255) / 256), (unsigned)p.G), 256, 0, stream>>>(p, SP);
+  return cudaGetLastError();
+}
+
+}  // namespace layer
+}  // namespace gdp
