@@ -8,42 +8,56 @@ namespace layer {
 
 // Chunk by chunk from a piece's end.  As in the forward pass, feeding warps bring rows (and the states entering the
 // chunks), form e, e x and dy, and finish gradients, while running warps hold two channels by four states a lane.  The
-// states before a chunk's tokens are formed again from the entering one: once through for those before every fourth
-// token, then four tokens at a time into registers, with their decays, which the same four tokens going back use.  A
-// token's sums over the CTA's channels (dB, dC) are made by shuffles in each running warp and added up by the feeding ones.
+// states before a chunk's tokens are formed again from the entering one: once through for those before every second
+// token, then two tokens at a time into registers, with their decays, which the same two going back use (four: 214 registers
+// or spills).  Sums
+// over a channel's lanes and over the CTA's channels are the feeding warps': the running ones, whose chain of dependent
+// steps is what takes the time, leave their parts in shared memory, eight tokens at a time (shuffles in the running
+// warps instead: 3173 against NEWTIME us for the training step of 8 x 4096 x 2048).
 
 template <typename T, int L>
 struct SsmBack {
-  static constexpr int CH = kSsmThreads / L, SP = L * kQ, K = kSsmChunk, RT = kSsmThreads / 2, W = RT / 32, YP = CH + 8;
+  static constexpr int CH = kSsmThreads / L, SP = L * kQ, K = kSsmChunk, HALF = K / 2, RT = kSsmThreads / 2;
+  static constexpr int STAGES = 3;  // chunks whose rows a CTA holds: finished or on their way, run, formed
+  static constexpr int BLK = 2;     // tokens there and back in registers
   __host__ __device__ static constexpr int stage(int dt_size, bool gated) {
     return K * CH * ((int)sizeof(T) * (gated ? 3 : 2) + dt_size) + 2 * K * SP * (int)sizeof(T) + CH * SP * 4;
   }
-  // two tiles of: e and e x, dy, B and C; u, v and y; the running warps' sums
-  static constexpr int formed = K * CH * 12 + 2 * K * SP * 4, made = 3 * K * YP * 4, sums = W * K * 2 * SP * 4, starts = 4 * RT * 8 * 4;
-  __host__ __device__ static constexpr int bytes(int dt_size, bool gated) { return kSsmStages * stage(dt_size, gated) + 2 * (formed + made + sums) + starts; }
+  // two chunks of e and e x, dy, B and C; two halves of the running threads' parts; their states before every BLKth token
+  static constexpr int formed = K * CH * 12 + 2 * K * SP * 4, starts = K / BLK * RT * 8 * 4;
+  __host__ __device__ static constexpr int parts(bool gated) { return HALF * RT * (8 + 2 * (gated ? 3 : 2)) * 4; }
+  __host__ __device__ static constexpr int bytes(int dt_size, bool gated) {
+    return STAGES * stage(dt_size, gated) + 2 * (formed + parts(gated)) + starts;
+  }
 };
 
 template <typename T, int L, bool FULL, bool LOCAL>
 __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_kernel(const SsmProblem p) {
   using Back = SsmBack<T, L>;
-  constexpr int CH = Back::CH, SP = Back::SP, K = Back::K, CP = CH / 2, HT = kSsmFeed, RT = Back::RT, W = Back::W, YP = Back::YP, R = 32 / L;
+  constexpr int CH = Back::CH, SP = Back::SP, K = Back::K, HALF = Back::HALF, CP = CH / 2, HT = kSsmFeed, RT = Back::RT, BLK = Back::BLK;
   constexpr float kLn2 = 0.69314718055994531f;
   extern __shared__ __align__(128) unsigned char smem[];
   const int dt_size = p.dt_f32 ? 4 : (int)sizeof(T), stage_bytes = Back::stage(dt_size, p.z != nullptr);
   float2 *steps = reinterpret_cast<float2 *>(smem);            // [2][K][CH]: e, e x
   float *gs = reinterpret_cast<float *>(steps + 2 * K * CH);   // [2][K][CH]: dy
   float *Bs = gs + 2 * K * CH, *Cs = Bs + 2 * K * SP;          // [2][K][SP]
-  float *us = Cs + 2 * K * SP, *vs = us + 2 * K * YP, *ys = vs + 2 * K * YP;  // [2][K][YP]
-  float *sums = ys + 2 * K * YP;                               // [2][W][K][2 SP]
-  float4 *starts = reinterpret_cast<float4 *>(sums + 2 * W * K * 2 * SP);  // [4][2][RT]: a running thread's states before every fourth token
-  unsigned char *ring = reinterpret_cast<unsigned char *>(starts + 4 * 2 * RT);
+  // Parts of half a chunk: of dB and dC [2][HALF][2][RT], of u, v and y [2][HALF][kinds][L][CP].
+  const int kinds = p.z ? 3 : 2;
+  float4 *sums = reinterpret_cast<float4 *>(Cs + 2 * K * SP);
+  float2 *parts = reinterpret_cast<float2 *>(sums + 2 * HALF * 2 * RT);
+  float4 *starts = reinterpret_cast<float4 *>(parts + 2 * HALF * kinds * RT);  // [K / BLK][2][RT]
+  unsigned char *ring = reinterpret_cast<unsigned char *>(starts + K / BLK * 2 * RT);
+  // (pairs of channels change places by lane, so that half a warp's parts fall on all banks)
+  auto part_of = [&](int t, int kind, int j, int pair) {
+    return ((t * kinds + kind) * L + j) * CP + (pair ^ (j / (L / 4) * (CP / 4)));
+  };
   struct Stage {
     unsigned char *x, *dt, *dy, *z, *B, *C;
     float *h;  // [CH][S]
   };
   auto stage = [&](int k) {
     Stage s;
-    s.x = ring + (k % kSsmStages) * stage_bytes;
+    s.x = ring + (k % Back::STAGES) * stage_bytes;
     s.dy = s.x + K * CH * sizeof(T);
     s.B = s.dy + K * CH * sizeof(T);
     s.C = s.B + K * SP * sizeof(T);
@@ -68,7 +82,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
   const bool running = threadIdx.x < RT;
   float *out = p.over_rows + worker * ssm_sum_cols(p.C, p.S);
   if (running) {
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, j = lane % L, rank = lane / L, ch = threadIdx.x / L * 2;
+    const int j = threadIdx.x % L, ch = threadIdx.x / L * 2;
     const int64_t mine = (c0 + ch) * p.S + j * kQ;
     const int states = max(0, min(kQ, (int)p.S - j * kQ));
     int n[2];
@@ -169,49 +183,59 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
           float2 unused[2][2];
           keep(0);
 #pragma unroll 1
-          for (int q = 1; 4 * q < rows; ++q) {
+          for (int q = 1; BLK * q < rows; ++q) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) forth(4 * q - 4 + u, unused);
+            for (int u = 0; u < BLK; ++u) forth(BLK * (q - 1) + u, unused);
             keep(q);
           }
-          // four tokens from t on (m of them exist), there and back
-          auto four = [&](int t, int m, auto whole) {
+          struct Token {
+            float4 d, B, C;  // e, e x of both channels; the lane's part
+            float2 g;        // dy of both
+          };
+          auto load = [&](int t) {
+            return Token{*reinterpret_cast<const float4 *>(steps + (at + t) * CH + ch), *reinterpret_cast<const float4 *>(Bs + (at + t) * SP + j * kQ),
+                         *reinterpret_cast<const float4 *>(Cs + (at + t) * SP + j * kQ), *reinterpret_cast<const float2 *>(gs + (at + t) * CH + ch)};
+          };
+          // BLK tokens from t on (m of them exist), there and back
+          auto some = [&](int t, int m, auto whole) {
             constexpr bool ALL = decltype(whole)::value;
-            float2 before[4][2][2], decay[4][2][2];
-            float u[8], v[8], y[8];
-            float *to = sums + (((k & 1) * W + warp) * K + t) * 2 * SP + j * kQ;
-            constexpr int kept = 2 * kQ / R > 0 ? 2 * kQ / R : 1;  // sums over channels that a lane ends up with
+            float2 before[BLK][2][2], decay[BLK][2][2];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < BLK; ++w) {
               if (!ALL && w >= m) break;
               copy(before[w], h);
               forth(t + w, decay[w]);
-              if (p.z) {
+            }
+            if (p.z) {
+#pragma unroll
+              for (int w = 0; w < BLK; ++w) {
+                if (!ALL && w >= m) break;
                 float2 Cv[2];
+                float y[2];
                 pairs(*reinterpret_cast<const float4 *>(Cs + (at + t + w) * SP + j * kQ), Cv);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                  const float2 sum = fma2(Cv[1], h[c][1], mul2(Cv[0], h[c][0]));
-                  y[2 * w + c] = sum.x + sum.y;
+                  const bool end = ALL ? w + 1 == BLK : w + 1 >= m;  // (h: after the last of them)
+                  const float2 h0 = end ? h[c][0] : before[w + 1 < BLK ? w + 1 : w][c][0], h1 = end ? h[c][1] : before[w + 1 < BLK ? w + 1 : w][c][1];
+                  const float2 sum = fma2(Cv[1], h1, mul2(Cv[0], h0));
+                  y[c] = sum.x + sum.y;
                 }
+                parts[part_of(t + w, 2, j, ch / 2)] = make_float2(y[0], y[1]);
               }
             }
-            // (h: after the last of them)
+            Token in = load(t + (ALL ? BLK : m) - 1);
 #pragma unroll
-            for (int w = 3; w >= 0; --w) {
-              if (!ALL && w >= m) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) u[2 * w + c] = v[2 * w + c] = y[2 * w + c] = 0.f;
-                continue;
-              }
-              const float4 d = *reinterpret_cast<const float4 *>(steps + (at + t + w) * CH + ch);
-              const float2 gd = *reinterpret_cast<const float2 *>(gs + (at + t + w) * CH + ch);
+            for (int w = BLK - 1; w >= 0; --w) {
+              if (!ALL && w >= m) continue;
+              Token next;
+              if (w > 0) next = load(t + w - 1);
               float2 Bv[2], Cv[2], sB[2], sC[2];
-              pairs(*reinterpret_cast<const float4 *>(Bs + (at + t + w) * SP + j * kQ), Bv);
-              pairs(*reinterpret_cast<const float4 *>(Cs + (at + t + w) * SP + j * kQ), Cv);
+              float u[2], v[2];
+              pairs(in.B, Bv);
+              pairs(in.C, Cv);
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const float2 gg = both(c ? gd.y : gd.x), ee = both(c ? d.z : d.x), ex = both(c ? d.w : d.y);
+                const float2 gg = both(c ? in.g.y : in.g.x), ee = both(c ? in.d.z : in.d.x), ex = both(c ? in.d.w : in.d.y);
                 float2 uu, vv;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -224,38 +248,40 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
                   vv = q ? fma2(x, A[c][q], vv) : mul2(x, A[c][q]);
                   dA[c][q] = fma2(x, ee, dA[c][q]);
                 }
-                u[2 * w + c] = uu.x + uu.y;
-                v[2 * w + c] = vv.x + vv.y;
+                u[c] = uu.x + uu.y;
+                v[c] = vv.x + vv.y;
               }
-              float s[2 * kQ] = {sB[0].x, sB[0].y, sB[1].x, sB[1].y, sC[0].x, sC[0].y, sC[1].x, sC[1].y};
-              sum_scatter<2 * kQ, R, L>(s, rank);
-#pragma unroll
-              for (int q = 0; q < kept; ++q) {
-                const int which = rank * kept + q;  // state of dB, then of dC
-                to[w * 2 * SP + which / kQ * SP + which % kQ] = s[q];
-              }
+              float4 *to = sums + (t + w) * 2 * RT + threadIdx.x;
+              to[0] = make_float4(sB[0].x, sB[0].y, sB[1].x, sB[1].y);
+              to[RT] = make_float4(sC[0].x, sC[0].y, sC[1].x, sC[1].y);
+              parts[part_of(t + w, 0, j, ch / 2)] = make_float2(u[0], u[1]);
+              parts[part_of(t + w, 1, j, ch / 2)] = make_float2(v[0], v[1]);
               copy(h, before[w]);
+              if (w > 0) in = next;
             }
-            auto spread = [&](float (&v)[8], float *to) {
-              sum_scatter<8, L, 1>(v, j);
-              to += (at + t) * YP + ch;
-              if constexpr (L == 4) *reinterpret_cast<float2 *>(to + j * YP) = make_float2(v[0], v[1]);
-              else if (L == 8 || j % 2 == 0) to[(L == 8 ? j : j / 2) / 2 * YP + (L == 8 ? j : j / 2) % 2] = v[0];
-            };
-            spread(u, us);
-            spread(v, vs);
-            if (p.z) spread(y, ys);
           };
+          int q = (rows - 1) / BLK;
 #pragma unroll 1
-          for (int q = (rows - 1) / 4; q >= 0; --q) {
+          for (int half = 1; half >= 0; --half) {
+            auto block = [&](int q, auto whole) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) pairs(starts[(q * 2 + c) * RT + threadIdx.x], h[c]);
-            const int m = rows - 4 * q;
-            if (m >= 4) four(4 * q, 4, std::true_type{});
-            else four(4 * q, m, std::false_type{});
+              for (int c = 0; c < 2; ++c) pairs(starts[(q * 2 + c) * RT + threadIdx.x], h[c]);
+              some(BLK * q, min(BLK, rows - BLK * q), whole);
+            };
+            if (rows == K) {
+#pragma unroll
+              for (int n = HALF / BLK - 1; n >= 0; --n) block(half * (HALF / BLK) + n, std::true_type{});
+            } else {
+#pragma unroll 1
+              for (; q >= half * (HALF / BLK); --q) block(q, std::false_type{});
+            }
+            __syncthreads();
           }
         }
-        __syncthreads();
+        if (LOCAL) {
+          __syncthreads();
+          __syncthreads();
+        }
       }
       if (LOCAL) {
         save(p.enter + r * p.C * p.S + mine, back);
@@ -358,20 +384,23 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
         if (c + 1 < cn) to[1] = from_f32<V>(v.y);
       }
     };
-    auto finish = [&](int k) {
+    // Half a chunk's gradients: the parts of u, v, y and of dB and dC are added up, in a fixed order.
+    auto finish = [&](int k, int half) {
       const Stage s = stage(k);
       const int at = (k & 1) * K, rows = rows_of(k);
       const int64_t row = first_row(k);
-      float2 sum = make_float2(0.f, 0.f), more = sum;
+      const int t = half * HALF + thread / CP;
+      if (thread < HALF * CP && t < rows) {
+        float2 u = make_float2(0.f, 0.f), v = u, y = u;
 #pragma unroll
-      for (int m = 0; m < ITEMS; ++m) {
-        const int t = t0 + m * STEP;
-        if (t >= rows) continue;
+        for (int j = 0; j < L; ++j) {
+          u = add2(u, parts[part_of(t, 0, j, c / 2)]);
+          v = add2(v, parts[part_of(t, 1, j, c / 2)]);
+        }
         const int o = t * CH + c;
         const int64_t to = (row + t) * p.C + c0 + c;
         const float4 d = *reinterpret_cast<const float4 *>(steps + at * CH + o);
         const float2 gd = *reinterpret_cast<const float2 *>(gs + at * CH + o), x = load_pair<T>(s.x, o);
-        const float2 u = *reinterpret_cast<const float2 *>(us + (at + t) * YP + c), v = *reinterpret_cast<const float2 *>(vs + (at + t) * YP + c);
         put(p.dx, to, fma2(u, make_float2(d.x, d.z), mul2(gd, D)), T());
         float2 dt = fma2(v, both(kLn2), mul2(u, x));
         if (p.softplus) {
@@ -380,27 +409,38 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
         }
         if (p.dt_f32) put(p.ddt, to, dt, float());
         else put(p.ddt, to, dt, T());
-        sum = fma2(gd, x, sum);
-        more = add2(dt, more);
+        dD = fma2(gd, x, dD);
+        dbias = add2(dt, dbias);
         if (p.z) {
+#pragma unroll
+          for (int j = 0; j < L; ++j) y = add2(y, parts[part_of(t, 2, j, c / 2)]);
           const float2 z = load_pair<T>(s.z, o), dy = load_pair<T>(s.dy, o);
-          const float2 y = fma2(D, x, *reinterpret_cast<const float2 *>(ys + (at + t) * YP + c));
+          y = fma2(D, x, y);
           const float q0 = sigmoid_fast(z.x), q1 = sigmoid_fast(z.y);
           put(p.dz, to, mul2(mul2(dy, y), make_float2(q0 * fmaf(z.x, 1.f - q0, 1.f), q1 * fmaf(z.y, 1.f - q1, 1.f))), T());
         }
       }
-      dD = add2(dD, sum);
-      dbias = add2(dbias, more);
-      const float *part = sums + (k & 1) * W * K * 2 * SP;
-      float *to = p.over_channels + ((int64_t)tile * p.p.T + row) * (2 * SP);
-      for (int q = thread * kQ; q < rows * 2 * SP; q += HT * kQ) {
-        float4 v = *reinterpret_cast<const float4 *>(part + q);
+      // an item: four states of dB or dC of a token; where there are fewer than threads, two threads share one
+      constexpr int OUT = HALF * 2 * L, SHARE = HT > OUT ? HT / OUT : 1, EACH = RT / L / SHARE;
 #pragma unroll
-        for (int w = 1; w < W; ++w) {
-          const float4 o = *reinterpret_cast<const float4 *>(part + w * K * 2 * SP + q);
-          v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+      for (int m = thread / SHARE; m < OUT; m += HT / SHARE) {
+        const int w = m / (2 * L), j = m % L, share = thread % SHARE;
+        const float4 *from = sums + ((half * HALF + w) * 2 + m / L % 2) * RT + j;
+        float2 a = make_float2(0.f, 0.f), b = a;
+#pragma unroll
+        for (int r = 0; r < EACH; ++r) {
+          const float4 v = from[(share * EACH + ((r + share) & (EACH - 1))) * L];
+          a = add2(a, make_float2(v.x, v.y));
+          b = add2(b, make_float2(v.z, v.w));
         }
-        *reinterpret_cast<float4 *>(to + q) = v;
+#pragma unroll
+        for (int r = 1; r < SHARE; r *= 2) {
+          a = add2(a, make_float2(__shfl_xor_sync(0xffffffffu, a.x, r), __shfl_xor_sync(0xffffffffu, a.y, r)));
+          b = add2(b, make_float2(__shfl_xor_sync(0xffffffffu, b.x, r), __shfl_xor_sync(0xffffffffu, b.y, r)));
+        }
+        if (share == 0 && half * HALF + w < rows)
+          *reinterpret_cast<float4 *>(p.over_channels + ((int64_t)tile * p.p.T + row + half * HALF + w) * (2 * SP) + m % (2 * L) * kQ) =
+              make_float4(a.x, a.y, b.x, b.y);
       }
     };
     auto meet = [&](bool all) {  // the feeding warps' copies (but the last group) have landed
@@ -414,13 +454,15 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
     if (chunks > 0) form(0);
     __syncthreads();
     for (int k = 0; k < chunks; ++k) {
-      bring(k + 2);
-      if (!LOCAL && k > 0) finish(k - 1);
+      if (!LOCAL && k > 0) finish(k - 1, 0);  // while the running warps are at the chunk's second half
+      __syncthreads();
+      bring(k + 2);  // (where chunk k - 1 was)
+      if (!LOCAL) finish(k, 1);
       meet(false);
       if (k + 1 < chunks) form(k + 1);
       __syncthreads();
     }
-    if (!LOCAL && chunks > 0) finish(chunks - 1);
+    if (!LOCAL && chunks > 0) finish(chunks - 1, 0);
     meet(true);  // before the stages are used again
   }
   if (LOCAL) return;
