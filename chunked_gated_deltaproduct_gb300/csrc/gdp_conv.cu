@@ -64,6 +64,7 @@ gdp_status resolve(const gdp_conv_args *a, bool step, ConvProblem *p) {
   p->s = StateModes{a->initial_state, a->output_state, a->state, a->state_indices, a->num_slots};
   p->act = a->activation;
   p->zero_pad = a->zero_padding != 0;
+  p->quad_taps = aligned(a->weight, 16);
   return GDP_OK;
 }
 
@@ -169,7 +170,7 @@ GDP_EXPORT gdp_status gdp_short_convolution_backward(const gdp_conv_backward_arg
   p.p = Packed{a->cu_seqlens, a->cu_seqlens_int64 != 0, a->T, a->N, a->device_status};
   p.C = a->C;
   p.s.init = a->initial_state;
-  p.act = a->activation;
+  p.act = a->activation; p.quad_taps = aligned(a->weight, 16);
   p.dy = a->d_output; p.dy_st = stride_of(a->d_output_stride_t, a->T, a->C);
   p.dfin = a->d_final_state; p.dx = a->dx; p.dinit = a->d_initial_state;
   p.partial = static_cast<float *>(a->workspace);

@@ -10,54 +10,142 @@
 namespace gdp {
 namespace layer {
 
-constexpr int kConvRun = 16;  // rows of a forward run
-constexpr int kConvAhead = 8; // rows whose loads are under way at once
+constexpr int kConvAhead = 4; // rows that are worked on together
+
+// Rows on their way to a thread, S tensors, kConvAhead rows a batch.  Asynchronous copies into places of shared memory
+// that are the thread's own (no barriers) keep two batches under way without registers; values below the copies' least
+// size (four bytes) wait in registers, one batch ahead.
+template <typename R, int S>
+struct RowQueue {
+  static constexpr bool ASYNC = sizeof(R) >= 4;
+  static constexpr int A = kConvAhead, DEEP = ASYNC ? 2 : 1, BYTES = ASYNC ? 3 * A * S * kConvThreads * (int)sizeof(R) : 16;
+  R *own;
+  R now[ASYNC ? 1 : S * A], next[ASYNC ? 1 : S * A];
+  __device__ __forceinline__ explicit RowQueue(unsigned char *smem)
+      : own(reinterpret_cast<R *>(smem) + threadIdx.y * blockDim.x + threadIdx.x) {}
+  // row k of tensor s of the batch in place `at` (0, 1, 2 in turn); every batch is asked for in order, and closed
+  __device__ __forceinline__ void ask(int at, int s, int k, const void *from) {
+    if constexpr (ASYNC) {
+      const uint32_t to = sm100::smem_u32(own + ((at * A + k) * S + s) * kConvThreads);
+      if constexpr (sizeof(R) == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+      else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"((int)sizeof(R)) : "memory");
+    } else {
+      next[s * A + k] = *static_cast<const R *>(from);
+    }
+  }
+  __device__ __forceinline__ void close() {
+    if constexpr (ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void wait() {  // before `ask` of the batch DEEP further on
+    if constexpr (ASYNC) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+#pragma unroll
+      for (int k = 0; k < S * A; ++k) now[k] = next[k];
+  }
+  __device__ __forceinline__ R get(int at, int s, int k) const {
+    if constexpr (ASYNC) return own[((at * A + k) * S + s) * kConvThreads];
+    else return now[s * A + k];
+  }
+};
+
+// V channels as pairs in fp32 (one channel: a pair whose second value is none).
+template <int V>
+struct Pairs {
+  static constexpr int N = V > 1 ? V / 2 : 1;
+  float2 v[N];
+};
+template <typename T, int V>
+__device__ __forceinline__ Pairs<V> pairs_of(const Vec<T, V> &r) {
+  Pairs<V> o;
+  if constexpr (V == 1) o.v[0] = make_float2(to_f32(r.v[0]), 0.f);
+  else
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+      if constexpr (sizeof(T) == 4) o.v[k] = make_float2(r.v[2 * k], r.v[2 * k + 1]);
+      else o.v[k] = widen<T>(reinterpret_cast<const uint32_t *>(r.v)[k]);
+    }
+  return o;
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_pairs(T *at, const Pairs<V> &p) {
+  Vec<T, V> o;
+  if constexpr (V == 1) o.v[0] = from_f32<T>(p.v[0].x);
+  else
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+      if constexpr (sizeof(T) == 4) o.v[2 * k] = p.v[k].x, o.v[2 * k + 1] = p.v[k].y;
+      else reinterpret_cast<uint32_t *>(o.v)[k] = narrow<T>(p.v[k]);
+    }
+  *reinterpret_cast<Vec<T, V> *>(at) = o;
+}
+template <int V>
+__device__ __forceinline__ Pairs<V> no_pairs() {
+  Pairs<V> o;
+#pragma unroll
+  for (int k = 0; k < Pairs<V>::N; ++k) o.v[k] = make_float2(0.f, 0.f);
+  return o;
+}
 
 // x_{t-1-k} of sequence [b, ...) in win[k], from the incoming state where the row lies before b.
 template <typename T, int V, int K>
-__device__ __forceinline__ void load_window(const ConvProblem &p, int64_t t, int64_t b, const T *state, int64_t c, float (&win)[K][V]) {
+__device__ __forceinline__ void load_window(const ConvProblem &p, int64_t t, int64_t b, const T *state, int64_t c, Pairs<V> (&win)[K]) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int64_t row = t - 1 - k;
     const T *at = row >= b ? static_cast<const T *>(p.x) + row * p.x_st + c : state ? state + (K + row - b) * p.C + c : nullptr;
-#pragma unroll
-    for (int i = 0; i < V; ++i) win[k][i] = 0.f;
-    if (at) {
-      const Vec<T, V> v = load_vec<T, V>(at);
-#pragma unroll
-      for (int i = 0; i < V; ++i) win[k][i] = to_f32(v.v[i]);
-    }
+    win[k] = at ? pairs_of<T, V>(load_vec<T, V>(at)) : no_pairs<V>();
   }
 }
 template <int V, int W>
-__device__ __forceinline__ void load_taps(const ConvProblem &p, int64_t c, float (&w)[W][V], float (&b)[V]) {
+__device__ __forceinline__ void load_taps(const ConvProblem &p, int64_t c, Pairs<V> (&w)[W], Pairs<V> &b) {
+  b = no_pairs<V>();
+#pragma unroll
+  for (int j = 0; j < W; ++j) w[j] = no_pairs<V>();
+  float taps[V * W];
+  if (p.quad_taps && V * W % 4 == 0) {
+#pragma unroll
+    for (int k = 0; k < V * W / 4; ++k) {
+      const float4 q = reinterpret_cast<const float4 *>(p.w + c * W)[k];
+      taps[4 * k] = q.x, taps[4 * k + 1] = q.y, taps[4 * k + 2] = q.z, taps[4 * k + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V * W; ++k) taps[k] = p.w[c * W + k];
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][i] = p.w[(c + i) * W + j];
-    b[i] = p.b ? p.b[c + i] : 0.f;
+    for (int j = 0; j < W; ++j) (i % 2 ? w[j].v[i / 2].y : w[j].v[i / 2].x) = taps[i * W + j];
+    if (p.b) (i % 2 ? b.v[i / 2].y : b.v[i / 2].x) = p.b[c + i];
   }
 }
 // p_t of one row: taps oldest first.
 template <int V, int W>
-__device__ __forceinline__ void convolve(const float (&w)[W][V], const float (&b)[V], const float (&win)[W - 1][V], const float (&x)[V],
-                                         float (&y)[V]) {
+__device__ __forceinline__ Pairs<V> convolve(const Pairs<V> (&w)[W], const Pairs<V> &b, const Pairs<V> (&win)[W - 1], const Pairs<V> &x) {
+  Pairs<V> y;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    float s = b[i];
+  for (int i = 0; i < Pairs<V>::N; ++i) {
+    float2 s = b.v[i];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) s = fmaf(w[j][i], win[W - 2 - j][i], s);
-    y[i] = fmaf(w[W - 1][i], x[i], s);
+    for (int j = 0; j < W - 1; ++j) s = fma2(w[j].v[i], win[W - 2 - j].v[i], s);
+    y.v[i] = fma2(w[W - 1].v[i], x.v[i], s);
   }
+  return y;
 }
 template <int V, int K>
-__device__ __forceinline__ void push_window(float (&win)[K][V], const float (&x)[V]) {
+__device__ __forceinline__ void push_window(Pairs<V> (&win)[K], const Pairs<V> &x) {
 #pragma unroll
-  for (int k = K - 1; k > 0; --k)
+  for (int k = K - 1; k > 0; --k) win[k] = win[k - 1];
+  win[0] = x;
+}
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+  const float2 t = mul2(v, both(-kLog2e)), d = add2(make_float2(ex2(t.x), ex2(t.y)), both(1.f));
+  return make_float2(rcp(d.x), rcp(d.y));
+}
+template <int V>
+__device__ __forceinline__ void activate(Pairs<V> &y) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) win[k][i] = win[k - 1][i];
-#pragma unroll
-  for (int i = 0; i < V; ++i) win[0][i] = x[i];
+  for (int i = 0; i < Pairs<V>::N; ++i) y.v[i] = mul2(y.v[i], sigmoid2(y.v[i]));
 }
 
 // Final state of sequence i: the last K rows of the incoming state and the sequence's rows.  All are read before any is
@@ -86,7 +174,7 @@ __device__ __forceinline__ void final_state(const ConvProblem &p, int64_t i, int
 
 template <typename T, int W, int V>
 __global__ void __launch_bounds__(kConvThreads) gdp_conv_fwd_kernel(const ConvProblem p) {
-  constexpr int K = W - 1;
+  constexpr int K = W - 1, A = kConvAhead;
   const int64_t c = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V;
   if (blockIdx.x == 0 && blockIdx.y == 0) check_packed(p.p);
   if (c >= p.C) return;
@@ -95,57 +183,73 @@ __global__ void __launch_bounds__(kConvThreads) gdp_conv_fwd_kernel(const ConvPr
     if (i < p.p.N) final_state<T, V, K>(p, i, c);
     return;
   }
-  int64_t t = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * kConvRun;
-  const int64_t stop = min(t + kConvRun, p.p.T);
-  if (t >= stop) return;
-  float w[W][V], bias[V], win[K][V];
-  load_taps<V, W>(p, c, w, bias);
+  const int64_t t0 = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * p.run, stop = min(t0 + p.run, p.p.T);
+  if (t0 >= stop) return;
   const T *x_at = static_cast<const T *>(p.x) + c;
   T *y_at = static_cast<T *>(p.y) + c;
-  int64_t i = seq_of_row(p.p, t), b, e;
+  using Queue = RowQueue<Vec<T, V>, 1>;
+  __shared__ __align__(16) unsigned char room[Queue::BYTES];
+  Queue queue(room);
+  int left = (int)(stop - t0);  // rows still to be asked for
+  const T *from = x_at + t0 * p.x_st;
+  auto ask = [&](int at) {
+#pragma unroll
+    for (int k = 0; k < A; ++k)
+      if (k < left) queue.ask(at, 0, k, from + k * p.x_st);
+    left -= A;
+    from += A * p.x_st;
+    queue.close();
+  };
+#pragma unroll
+  for (int n = 0; n < Queue::DEEP; ++n) ask(n);
+  Pairs<V> w[W], bias, win[K];
+  load_taps<V, W>(p, c, w, bias);
+  int64_t i = seq_of_row(p.p, t0), b, e;
   seq_rows(p.p, i, &b, &e);
-  bool fresh = true;  // the window is not that of row t
-  while (t < stop) {
-    Vec<T, V> rows[kConvAhead];
+  bool fresh = true;  // the window is not that of the row
+  auto enter = [&](int64_t row) {
+    const T *src;
+    T *dst;
+    state_of<T>(p.s, i, K * p.C, p.p.status, c == 0, &src, &dst);
+    load_window<T, V, K>(p, row, b, src, c, win);
+    fresh = false;
+  };
+  auto one = [&](T *to, const Vec<T, V> &raw) {
+    const Pairs<V> x = pairs_of<T, V>(raw);
+    Pairs<V> y = convolve<V, W>(w, bias, win, x);
+    if (p.act == GDP_ACT_SILU) activate<V>(y);
+    store_pairs<T, V>(to, y);
+    push_window<V, K>(win, x);
+  };
+  T *to = y_at + t0 * p.C;
+  int at = 0;
+  for (int64_t t = t0; t < stop; t += A, to += A * p.C, at = at == 2 ? 0 : at + 1) {
+    queue.wait();
+    ask(at + Queue::DEEP < 3 ? at + Queue::DEEP : at + Queue::DEEP - 3);
+    if (t >= b && t + A <= min(e, stop)) {  // all of one sequence
+      if (fresh) enter(t);
 #pragma unroll
-    for (int k = 0; k < kConvAhead; ++k)
-      if (t + k < stop) rows[k] = load_vec<T, V>(x_at + (t + k) * p.x_st);
+      for (int k = 0; k < A; ++k) one(to + k * p.C, queue.get(at, 0, k));
+    } else {
 #pragma unroll
-    for (int k = 0; k < kConvAhead; ++k) {
-      const int64_t row = t + k;
-      if (row >= stop) break;
-      if (row >= e) {
-        while (row >= e && i + 1 < p.p.N) {
-          ++i;
-          seq_rows(p.p, i, &b, &e);
+      for (int k = 0; k < A; ++k) {
+        const int64_t row = t + k;
+        if (row >= stop) break;
+        if (row >= e) {
+          while (row >= e && i + 1 < p.p.N) {
+            ++i;
+            seq_rows(p.p, i, &b, &e);
+          }
+          fresh = true;
         }
-        fresh = true;
-      }
-      if (row >= e || row < b) {  // padding (or a row that no bounds hold)
-        if (p.zero_pad) {
-          float zero[V] = {};
-          store_vec<T, V>(y_at + row * p.C, zero);
+        if (row >= e || row < b) {  // padding (or a row that no bounds hold)
+          if (p.zero_pad) store_pairs<T, V>(to + k * p.C, no_pairs<V>());
+          continue;
         }
-        continue;
+        if (fresh) enter(row);
+        one(to + k * p.C, queue.get(at, 0, k));
       }
-      if (fresh) {
-        const T *src;
-        T *dst;
-        state_of<T>(p.s, i, K * p.C, p.p.status, c == 0, &src, &dst);
-        load_window<T, V, K>(p, row, b, src, c, win);
-        fresh = false;
-      }
-      float x[V], y[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) x[j] = to_f32(rows[k].v[j]);
-      convolve<V, W>(w, bias, win, x, y);
-      if (p.act == GDP_ACT_SILU)
-#pragma unroll
-        for (int j = 0; j < V; ++j) y[j] *= sigmoid_fast(y[j]);
-      store_vec<T, V>(y_at + row * p.C, y);
-      push_window<V, K>(win, x);
     }
-    t += kConvAhead;
   }
 }
 
@@ -164,7 +268,7 @@ __global__ void __launch_bounds__(kConvThreads) gdp_conv_step_kernel(const ConvP
   const T *src;
   T *dst;
   const Vec<T, V> now = load_vec<T, V>(static_cast<const T *>(p.x) + i * p.x_st + c);
-  float w[W][V], bias[V], x[V], y[V], win[K][V];
+  Pairs<V> w[W], bias, win[K];
   load_taps<V, W>(p, c, w, bias);
   state_of<T>(p.s, i, K * p.C, p.p.status, c == 0, &src, &dst);
   Vec<T, V> old[K];
@@ -176,16 +280,10 @@ __global__ void __launch_bounds__(kConvThreads) gdp_conv_step_kernel(const ConvP
       for (int j = 0; j < V; ++j) old[k].v[j] = from_f32<T>(0.f);
   }
 #pragma unroll
-  for (int j = 0; j < V; ++j) x[j] = to_f32(now.v[j]);
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int j = 0; j < V; ++j) win[K - 1 - k][j] = to_f32(old[k].v[j]);
-  convolve<V, W>(w, bias, win, x, y);
-  if (p.act == GDP_ACT_SILU)
-#pragma unroll
-    for (int j = 0; j < V; ++j) y[j] *= sigmoid_fast(y[j]);
-  store_vec<T, V>(static_cast<T *>(p.y) + i * p.C + c, y);
+  for (int k = 0; k < K; ++k) win[K - 1 - k] = pairs_of<T, V>(old[k]);
+  Pairs<V> y = convolve<V, W>(w, bias, win, pairs_of<T, V>(now));
+  if (p.act == GDP_ACT_SILU) activate<V>(y);
+  store_pairs<T, V>(static_cast<T *>(p.y) + i * p.C + c, y);
   if (dst) {
 #pragma unroll
     for (int k = 0; k + 1 < K; ++k) *reinterpret_cast<Vec<T, V> *>(dst + k * p.C + c) = old[k + 1];
@@ -194,52 +292,56 @@ __global__ void __launch_bounds__(kConvThreads) gdp_conv_step_kernel(const ConvP
 }
 
 // dp = dy act'(p)
-__device__ __forceinline__ float act_slope(float p, int act) {
-  if (act != GDP_ACT_SILU) return 1.f;
-  const float q = sigmoid_fast(p);
-  return q * fmaf(p, 1.f - q, 1.f);
+template <int V>
+__device__ __forceinline__ Pairs<V> through_act(const Pairs<V> &p, const Pairs<V> &dy, int act) {
+  if (act != GDP_ACT_SILU) return dy;
+  Pairs<V> o;
+#pragma unroll
+  for (int i = 0; i < Pairs<V>::N; ++i) {
+    const float2 q = sigmoid2(p.v[i]);
+    const float2 rest = fma2(q, both(-1.f), both(1.f));
+    o.v[i] = mul2(dy.v[i], mul2(q, fma2(p.v[i], rest, both(1.f))));
+  }
+  return o;
 }
 
 // d_initial_state of sequence i: what its first K outputs (and, where it is shorter, its final state) pass back.
 template <typename T, int W, int V>
 __device__ __forceinline__ void initial_gradient(const ConvProblem &p, int64_t i, int64_t c) {
-  constexpr int K = W - 1;
+  constexpr int K = W - 1, N = Pairs<V>::N;
   int64_t b, e;
   seq_rows(p.p, i, &b, &e);
   const T *state = p.s.init ? static_cast<const T *>(p.s.init) + i * K * p.C : nullptr;
-  float w[W][V], bias[V], win[K][V], d[K][V] = {};
+  Pairs<V> w[W], bias, win[K], d[K];
   load_taps<V, W>(p, c, w, bias);
   load_window<T, V, K>(p, b, b, state, c, win);
+#pragma unroll
+  for (int k = 0; k < K; ++k) d[k] = no_pairs<V>();
 #pragma unroll
   for (int k = 0; k < K; ++k) {  // row b + k
     if (b + k >= e) {            // the sequence has k rows: incoming rows k .. K - 1 are final ones 0 .. K - 1 - k
       if (p.dfin && b + k == e)
 #pragma unroll
         for (int r = 0; r + k < K; ++r) {
-          const Vec<T, V> f = load_vec<T, V>(static_cast<const T *>(p.dfin) + (i * K + r) * p.C + c);
+          const Pairs<V> f = pairs_of<T, V>(load_vec<T, V>(static_cast<const T *>(p.dfin) + (i * K + r) * p.C + c));
 #pragma unroll
-          for (int j = 0; j < V; ++j) d[k + r][j] += to_f32(f.v[j]);
+          for (int j = 0; j < N; ++j) d[k + r].v[j] = add2(d[k + r].v[j], f.v[j]);
         }
       continue;
     }
-    const Vec<T, V> xr = load_vec<T, V>(static_cast<const T *>(p.x) + (b + k) * p.x_st + c),
-                    dr = load_vec<T, V>(static_cast<const T *>(p.dy) + (b + k) * p.dy_st + c);
-    float x[V], y[V];
+    const Pairs<V> x = pairs_of<T, V>(load_vec<T, V>(static_cast<const T *>(p.x) + (b + k) * p.x_st + c));
+    const Pairs<V> g = pairs_of<T, V>(load_vec<T, V>(static_cast<const T *>(p.dy) + (b + k) * p.dy_st + c));
+    const Pairs<V> dp = through_act<V>(convolve<V, W>(w, bias, win, x), g, p.act);
 #pragma unroll
-    for (int j = 0; j < V; ++j) x[j] = to_f32(xr.v[j]);
-    convolve<V, W>(w, bias, win, x, y);
+    for (int r = 0; r < K; ++r)
+      if (r >= k)
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float dp = to_f32(dr.v[j]) * act_slope(y[j], p.act);
-#pragma unroll
-      for (int r = 0; r < K; ++r)
-        if (r >= k) d[r][j] = fmaf(w[r - k >= 0 ? r - k : 0][j], dp, d[r][j]);
-    }
+        for (int j = 0; j < N; ++j) d[r].v[j] = fma2(w[r >= k ? r - k : 0].v[j], dp.v[j], d[r].v[j]);
     push_window<V, K>(win, x);
   }
   T *out = static_cast<T *>(p.dinit) + i * K * p.C + c;
 #pragma unroll
-  for (int r = 0; r < K; ++r) store_vec<T, V>(out + r * p.C, d[r]);
+  for (int r = 0; r < K; ++r) store_pairs<T, V>(out + r * p.C, d[r]);
 }
 
 // A part is a run of rows [t0, t1).  A thread walks it in order and K rows beyond, forms p again from its window of
@@ -247,7 +349,7 @@ __device__ __forceinline__ void initial_gradient(const ConvProblem &p, int64_t i
 // part stay in registers too and leave once.
 template <typename T, int W, int V>
 __global__ void __launch_bounds__(kConvThreads) gdp_conv_bwd_kernel(const ConvProblem p) {
-  constexpr int K = W - 1, A = 4;  // rows whose loads are under way at once
+  constexpr int K = W - 1, N = Pairs<V>::N, A = kConvAhead;
   const int64_t c = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V;
   if (blockIdx.x == 0 && blockIdx.y == 0) check_packed(p.p);
   if (c >= p.C) return;
@@ -258,10 +360,31 @@ __global__ void __launch_bounds__(kConvThreads) gdp_conv_bwd_kernel(const ConvPr
   }
   const int64_t part = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int64_t t0 = min(part * p.part_rows, p.p.T), t1 = min(t0 + p.part_rows, p.p.T), last = min(t1 + K, p.p.T);
-  float w[W][V], bias[V], win[K][V], pend[K][V], dw[W][V] = {}, db[V] = {};
+  Pairs<V> w[W], bias, win[K], pend[K], dw[W], db = no_pairs<V>();
+#pragma unroll
+  for (int j = 0; j < W; ++j) dw[j] = no_pairs<V>();
   const T *x_at = static_cast<const T *>(p.x) + c, *dy_at = static_cast<const T *>(p.dy) + c;
   T *dx_at = static_cast<T *>(p.dx) + c;
   if (t0 < t1) {
+    using Queue = RowQueue<Vec<T, V>, 2>;
+    __shared__ __align__(16) unsigned char room[Queue::BYTES];
+    Queue queue(room);
+    int left = (int)(last - t0);  // rows still to be asked for
+    const T *x_from = x_at + t0 * p.x_st, *dy_from = dy_at + t0 * p.dy_st;
+    auto ask = [&](int at) {
+#pragma unroll
+      for (int k = 0; k < A; ++k)
+        if (k < left) {
+          queue.ask(at, 0, k, x_from + k * p.x_st);
+          queue.ask(at, 1, k, dy_from + k * p.dy_st);
+        }
+      left -= A;
+      x_from += A * p.x_st;
+      dy_from += A * p.dy_st;
+      queue.close();
+    };
+#pragma unroll
+    for (int n = 0; n < Queue::DEEP; ++n) ask(n);
     load_taps<V, W>(p, c, w, bias);
     int64_t i = seq_of_row(p.p, t0), b, e;
     seq_rows(p.p, i, &b, &e);
@@ -273,77 +396,75 @@ __global__ void __launch_bounds__(kConvThreads) gdp_conv_bwd_kernel(const ConvPr
         const int64_t row = t - 1 - k;
         if (row < b || row < t0 || row >= t1) continue;
         if (p.dfin) {
-          const Vec<T, V> f = load_vec<T, V>(static_cast<const T *>(p.dfin) + (i * K + (K - 1 - k)) * p.C + c);
+          const Pairs<V> f = pairs_of<T, V>(load_vec<T, V>(static_cast<const T *>(p.dfin) + (i * K + (K - 1 - k)) * p.C + c));
 #pragma unroll
-          for (int j = 0; j < V; ++j) pend[k][j] += to_f32(f.v[j]);
+          for (int j = 0; j < N; ++j) pend[k].v[j] = add2(pend[k].v[j], f.v[j]);
         }
-        store_vec<T, V>(dx_at + row * p.C, pend[k]);
+        store_pairs<T, V>(dx_at + row * p.C, pend[k]);
       }
     };
-    for (int64_t t = t0; t < last && !done; t += A) {
-      Vec<T, V> xs[A], ds[A];
+    auto enter = [&](int64_t row) {
+      const T *state = p.s.init ? static_cast<const T *>(p.s.init) + i * K * p.C : nullptr;
+      load_window<T, V, K>(p, row, b, state, c, win);
 #pragma unroll
-      for (int k = 0; k < A; ++k)
-        if (t + k < last) {
-          xs[k] = load_vec<T, V>(x_at + (t + k) * p.x_st);
-          ds[k] = load_vec<T, V>(dy_at + (t + k) * p.dy_st);
+      for (int r = 0; r < K; ++r) pend[r] = no_pairs<V>();
+      fresh = false;
+    };
+    // One row: `own`: it belongs to the part; the row K before it (at `before`) is complete then, and leaves with `out`.
+    auto one = [&](T *before, const Vec<T, V> &xr, const Vec<T, V> &dr, bool own, bool out) {
+      const Pairs<V> x = pairs_of<T, V>(xr), dp = through_act<V>(convolve<V, W>(w, bias, win, x), pairs_of<T, V>(dr), p.act);
+      Pairs<V> ready;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        ready.v[j] = fma2(w[0].v[j], dp.v[j], pend[K - 1].v[j]);
+#pragma unroll
+        for (int r = K - 1; r > 0; --r) pend[r].v[j] = fma2(w[K - r].v[j], dp.v[j], pend[r - 1].v[j]);
+        pend[0].v[j] = mul2(w[K].v[j], dp.v[j]);
+      }
+      if (own) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          db.v[j] = add2(db.v[j], dp.v[j]);
+          dw[K].v[j] = fma2(dp.v[j], x.v[j], dw[K].v[j]);
+#pragma unroll
+          for (int r = 0; r < K; ++r) dw[r].v[j] = fma2(dp.v[j], win[K - 1 - r].v[j], dw[r].v[j]);
         }
+      }
+      if (out) store_pairs<T, V>(before, ready);
+      push_window<V, K>(win, x);
+    };
+    T *before = dx_at + (t0 - K) * p.C;  // (written where it is a row of the part)
+    int at = 0;
+    for (int64_t t = t0; t < last && !done; t += A, before += A * p.C, at = at == 2 ? 0 : at + 1) {
+      queue.wait();
+      ask(at + Queue::DEEP < 3 ? at + Queue::DEEP : at + Queue::DEEP - 3);
+      if (!fresh && t - K >= max(t0, b) && t + A <= min(e, t1)) {  // all of one sequence and the part
 #pragma unroll
-      for (int k = 0; k < A; ++k) {
-        const int64_t row = t + k;
-        if (row >= last || done) break;
-        if (row >= e) {
-          if (!fresh) flush(row);
-          fresh = true;
-          if (row >= t1) {
-            done = true;
-            break;
+        for (int k = 0; k < A; ++k) one(before + k * p.C, queue.get(at, 0, k), queue.get(at, 1, k), true, true);
+      } else {
+#pragma unroll
+        for (int k = 0; k < A; ++k) {
+          const int64_t row = t + k;
+          if (row >= last || done) break;
+          if (row >= e) {
+            if (!fresh) flush(row);
+            fresh = true;
+            if (row >= t1) {
+              done = true;
+              break;
+            }
+            while (row >= e && i + 1 < p.p.N) {
+              ++i;
+              seq_rows(p.p, i, &b, &e);
+            }
           }
-          while (row >= e && i + 1 < p.p.N) {
-            ++i;
-            seq_rows(p.p, i, &b, &e);
+          if (row >= e || row < b) {
+            if (row < t1) store_pairs<T, V>(dx_at + row * p.C, no_pairs<V>());
+            continue;
           }
+          if (fresh) enter(row);
+          one(before + k * p.C, queue.get(at, 0, k), queue.get(at, 1, k), row < t1, row - K >= b && row - K >= t0);
         }
-        if (row >= e || row < b) {
-          if (row < t1) {
-            float zero[V] = {};
-            store_vec<T, V>(dx_at + row * p.C, zero);
-          }
-          continue;
-        }
-        if (fresh) {
-          const T *state = p.s.init ? static_cast<const T *>(p.s.init) + i * K * p.C : nullptr;
-          load_window<T, V, K>(p, row, b, state, c, win);
-#pragma unroll
-          for (int r = 0; r < K; ++r)
-#pragma unroll
-            for (int j = 0; j < V; ++j) pend[r][j] = 0.f;
-          fresh = false;
-        }
-        float x[V], y[V], dp[V], out[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = to_f32(xs[k].v[j]);
-        convolve<V, W>(w, bias, win, x, y);
-        const float own = row < t1 ? 1.f : 0.f;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          dp[j] = to_f32(ds[k].v[j]) * act_slope(y[j], p.act);
-          out[j] = fmaf(w[0][j], dp[j], pend[K - 1][j]);
-#pragma unroll
-          for (int r = K - 1; r > 0; --r) pend[r][j] = fmaf(w[K - r][j], dp[j], pend[r - 1][j]);
-          pend[0][j] = w[K][j] * dp[j];
-        }
-        if (own != 0.f) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            db[j] += dp[j];
-            dw[K][j] = fmaf(dp[j], x[j], dw[K][j]);
-#pragma unroll
-            for (int r = 0; r < K; ++r) dw[r][j] = fmaf(dp[j], win[K - 1 - r][j], dw[r][j]);
-          }
-        }
-        if (row - K >= b && row - K >= t0) store_vec<T, V>(dx_at + (row - K) * p.C, out);
-        push_window<V, K>(win, x);
       }
     }
     // the tensors end here, and the sequence with them
@@ -353,8 +474,8 @@ __global__ void __launch_bounds__(kConvThreads) gdp_conv_bwd_kernel(const ConvPr
 #pragma unroll
   for (int j = 0; j < V; ++j) {
 #pragma unroll
-    for (int r = 0; r < W; ++r) to[r * p.C + j] = dw[r][j];
-    to[W * p.C + j] = db[j];
+    for (int r = 0; r < W; ++r) to[r * p.C + j] = j % 2 ? dw[r].v[j / 2].y : dw[r].v[j / 2].x;
+    to[W * p.C + j] = j % 2 ? db.v[j / 2].y : db.v[j / 2].x;
   }
 }
 
@@ -362,7 +483,10 @@ template <typename T, int V>
 cudaError_t conv_fwd(ConvProblem &p, int width, bool states, cudaStream_t stream) {
   const int64_t vecs = (p.C + V - 1) / V;
   const dim3 block = conv_block(vecs);
-  p.runs = (p.p.T + kConvRun * block.y - 1) / (kConvRun * block.y);
+  // short batches: sixteen rows a thread, so that there are enough of them; else 64, of which the first three are read twice
+  const int64_t across = (vecs + block.x - 1) / block.x;
+  p.run = p.p.T * across / (64 * block.y) >= 8 * sm_count() ? 64 : 16;
+  p.runs = (p.p.T + p.run * block.y - 1) / (p.run * block.y);
   const dim3 grid((unsigned)(p.runs + (states ? (p.p.N + block.y - 1) / block.y : 0)), (unsigned)((vecs + block.x - 1) / block.x));
   if (grid.x == 0) return cudaSuccess;
   if (width == 2) gdp_conv_fwd_kernel<T, 2, V><<<grid, block, 0, stream>>>(p);
