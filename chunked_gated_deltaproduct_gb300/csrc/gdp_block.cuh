@@ -95,6 +95,11 @@ __device__ __forceinline__ void store_vec(T *at, const float *v) {
 // -87.3 it is 0, as e^-v leaves fp32).
 __device__ __forceinline__ float sigmoid_fast(float v) { return rcp(1.f + exp_fast(-v)); }
 
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+  const float2 t = mul2(v, both(-kLog2e)), d = add2(make_float2(ex2(t.x), ex2(t.y)), both(1.f));
+  return make_float2(rcp(d.x), rcp(d.y));
+}
+
 // ---- host side ----
 // A [T, C] tensor: given where it has elements, aligned to its elements, rows at least C apart.
 inline gdp_status rows_ok(const void *p, int64_t stride, int64_t T, int64_t C, int type, const char *name) {

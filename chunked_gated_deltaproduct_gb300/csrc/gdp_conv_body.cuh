@@ -138,10 +138,6 @@ __device__ __forceinline__ void push_window(Pairs<V> (&win)[K], const Pairs<V> &
   for (int k = K - 1; k > 0; --k) win[k] = win[k - 1];
   win[0] = x;
 }
-__device__ __forceinline__ float2 sigmoid2(float2 v) {
-  const float2 t = mul2(v, both(-kLog2e)), d = add2(make_float2(ex2(t.x), ex2(t.y)), both(1.f));
-  return make_float2(rcp(d.x), rcp(d.y));
-}
 template <int V>
 __device__ __forceinline__ void activate(Pairs<V> &y) {
 #pragma unroll

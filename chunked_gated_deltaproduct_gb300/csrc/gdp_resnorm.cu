@@ -51,6 +51,7 @@ GDP_EXPORT gdp_status gdp_residual_norm(const gdp_residual_norm_args *a, void *s
   p.y = a->y; p.r = a->residual_out;
   p.T = a->T; p.C = a->C; p.eps = a->eps; p.inv_c = 1.f / (float)a->C;
   p.act = a->activation; p.res_f32 = a->residual_dtype == GDP_DTYPE_F32;
+  p.quad_cols = aligned(p.w, 16) && aligned(p.post, 16) && aligned(p.scale, 16);
   const int vec = p.C % kRes == 0 && rows_by(p.res, p.res_st, p.T, a->residual_dtype, 16) && rows_by(p.block, p.block_st, p.T, a->dtype, 16) &&
                   (!p.gate || rows_by(p.gate, p.gate_st, p.T, a->dtype, 16)) && aligned(p.y, 16) && aligned(p.r, 16);
   cudaStream_t s = (cudaStream_t)stream;
@@ -98,6 +99,7 @@ GDP_EXPORT gdp_status gdp_residual_norm_backward(const gdp_residual_norm_backwar
   p.partial = static_cast<float *>(a->workspace);
   p.T = a->T; p.C = a->C; p.eps = a->eps; p.inv_c = 1.f / (float)a->C;
   p.act = a->activation; p.res_f32 = a->residual_dtype == GDP_DTYPE_F32;
+  p.quad_cols = aligned(p.w, 16) && aligned(p.post, 16) && aligned(p.scale, 16);
   const int vec = p.C % kRes == 0 && rows_by(p.res, p.res_st, p.T, a->residual_dtype, 16) && rows_by(p.block, p.block_st, p.T, a->dtype, 16) &&
                   rows_by(p.dy, p.dy_st, p.T, a->dtype, 16) && (!p.gate || (rows_by(p.gate, p.gate_st, p.T, a->dtype, 16) && aligned(p.dgate, 16))) &&
                   (!p.dr || rows_by(p.dr, p.dr_st, p.T, a->residual_dtype, 16)) && aligned(p.dres, 16) && aligned(p.dblock, 16);

@@ -3,7 +3,7 @@
 
 namespace gdp {
 namespace layer {
-template cudaError_t launch_res_fwd<__half>(const ResProblem &, int, cudaStream_t);
-template cudaError_t launch_res_bwd<__half>(const ResProblem &, int, int64_t, cudaStream_t);
+template cudaError_t launch_res_fwd<__half>(ResProblem &, int, cudaStream_t);
+template cudaError_t launch_res_bwd<__half>(ResProblem &, int, int64_t, cudaStream_t);
 }  // namespace layer
 }  // namespace gdp

@@ -3,7 +3,7 @@
 
 namespace gdp {
 namespace layer {
-template cudaError_t launch_res_fwd<float>(const ResProblem &, int, cudaStream_t);
-template cudaError_t launch_res_bwd<float>(const ResProblem &, int, int64_t, cudaStream_t);
+template cudaError_t launch_res_fwd<float>(ResProblem &, int, cudaStream_t);
+template cudaError_t launch_res_bwd<float>(ResProblem &, int, int64_t, cudaStream_t);
 }  // namespace layer
 }  // namespace gdp
