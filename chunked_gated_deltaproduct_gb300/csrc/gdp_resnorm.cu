@@ -1,4 +1,6 @@
 // gdp_resnorm.cu -- the residual norm's C entries and argument checks (gdp_block.h).
+#include <initializer_list>
+
 #include "gdp_resnorm.cuh"
 
 namespace gdp {
@@ -16,6 +18,12 @@ gdp_status res_ok(int64_t T, int64_t C, float eps, int type, int res_type, int a
   if (!w) return fail(GDP_ERR_INVALID_ARG, "weight is required");
   if (!aligned(w, 4) || !aligned(post, 4) || !aligned(scale, 4)) return fail(GDP_ERR_INVALID_ARG, "fp32 buffers must be 4-byte aligned");
   return GDP_OK;
+}
+// Row strides that the kernels take (32 bits).
+bool short_strides(std::initializer_list<int64_t> strides) {
+  for (int64_t s : strides)
+    if (s > INT32_MAX) return false;
+  return true;
 }
 // The same rows exactly, or others.
 bool partly(const void *in, int64_t stride, const void *out, int64_t T, int64_t C, int type) {
@@ -45,6 +53,7 @@ GDP_EXPORT gdp_status gdp_residual_norm(const gdp_residual_norm_args *a, void *s
   p.res = a->residual; p.block = a->block; p.gate = a->gate;
   p.res_st = stride_of(a->residual_stride_t, a->T, a->C); p.block_st = stride_of(a->block_stride_t, a->T, a->C);
   p.gate_st = stride_of(a->gate_stride_t, a->T, a->C);
+  if (!short_strides({p.res_st, p.block_st, p.gate_st})) return fail(GDP_ERR_UNSUPPORTED, "row strides below 2^31 elements");
   if (partly(p.res, p.res_st, a->residual_out, a->T, a->C, a->residual_dtype)) return fail(GDP_ERR_ALIAS, "residual_out partly overlaps residual");
   if (a->T == 0) return GDP_OK;
   p.w = a->weight; p.post = a->post_weight; p.scale = a->scale;
@@ -93,6 +102,7 @@ GDP_EXPORT gdp_status gdp_residual_norm_backward(const gdp_residual_norm_backwar
   p.res_st = stride_of(a->residual_out_stride_t, a->T, a->C); p.block_st = stride_of(a->block_stride_t, a->T, a->C);
   p.gate_st = stride_of(a->gate_stride_t, a->T, a->C); p.dy_st = stride_of(a->d_y_stride_t, a->T, a->C);
   p.dr_st = stride_of(a->d_residual_out_stride_t, a->T, a->C);
+  if (!short_strides({p.res_st, p.block_st, p.gate_st, p.dy_st, p.dr_st})) return fail(GDP_ERR_UNSUPPORTED, "row strides below 2^31 elements");
   if (partly(p.dr, p.dr_st, a->d_residual, a->T, a->C, a->residual_dtype)) return fail(GDP_ERR_ALIAS, "d_residual partly overlaps d_residual_out");
   p.w = a->weight; p.post = a->post_weight; p.scale = a->scale;
   p.dres = a->d_residual; p.dblock = a->d_block; p.dgate = a->d_gate;

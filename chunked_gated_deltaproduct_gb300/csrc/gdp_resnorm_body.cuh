@@ -1,9 +1,11 @@
 // gdp_resnorm_body.cuh -- the residual norm's kernels, instantiated by type in gdp_resnorm_*.cu.
 //
 // A row belongs to a warp (up to 256 channels) or to a CTA; a thread holds eight of its channels in registers, so that
-// every tensor is read once and the norms cost one reduction each (backward: three for the two).  Rows come ahead by
-// asynchronous copies into places of shared memory that are the thread's own.  Bound by memory in the end, and on the way
-// there by instructions: at 57 bytes a channel pair the SM has four issue slots for ... see the figures at the launchers.
+// every tensor is read once and the norms cost one sum over the row each (backward: three for the two).  Rows come ahead by
+// asynchronous copies into places of shared memory that are the thread's own.  Bound by memory at last (57 bytes a channel
+// and pass of a training step with an fp32 stream), but first by instructions and the sums' latency: hence paired
+// arithmetic, weights that stay in registers (forward) or shared memory (backward) instead of an L1 that the places leave
+// too small, and two rows side by side in the forward pass, which share their sums' barriers.
 #pragma once
 
 #include "gdp_resnorm.cuh"
@@ -60,6 +62,15 @@ __device__ __forceinline__ float dot(const Eight &a, const Eight &b) {
 }
 
 // ---- rows in global memory ----
+// The thread's part of row t: one wide multiply, instead of pointers that would take registers (rows and strides are held
+// below 2^31 by the host).
+template <typename T, bool VEC>
+__device__ __forceinline__ const T *row_at(const void *base, int t, int64_t stride) {
+  return static_cast<const T *>(base) + (int64_t)t * (int)stride + (VEC ? threadIdx.x * kRes : 0);
+}
+template <typename T>
+__device__ __forceinline__ T *out_at(void *base, int t, int C) { return static_cast<T *>(base) + (int64_t)t * C; }
+
 template <typename T, bool VEC>
 __device__ __forceinline__ Eight load_row(const void *row, int thread, int threads, int C) {
   const T *at = static_cast<const T *>(row);
@@ -153,38 +164,38 @@ struct RowPlaces {
 // suffices; a buffer's places that no warp has stay zero.
 template <int WARPS>
 struct RowSums {
-  static constexpr int PAIRS = (WARPS + 1) / 2 * 2;
-  float2 (*buffer)[PAIRS];
+  static constexpr int PLACES = WARPS < 4 ? 4 : WARPS;
+  float (*buffer)[3][PLACES];
   int turn;
-  __device__ __forceinline__ explicit RowSums(float2 (*b)[PAIRS]) : buffer(b), turn(0) {
+  __device__ __forceinline__ explicit RowSums(float (*b)[3][PLACES]) : buffer(b), turn(0) {
     if constexpr (WARPS > 1) {
-      for (int i = threadIdx.x; i < 2 * PAIRS; i += blockDim.x) buffer[i / PAIRS][i % PAIRS] = make_float2(0.f, 0.f);
+      for (int i = threadIdx.x; i < 6 * PLACES; i += blockDim.x) (&buffer[0][0][0])[i] = 0.f;
       __syncthreads();
     }
   }
-  __device__ __forceinline__ float one(float v) {
+  // N sums, up to three.  Across warps: four warps' sums a lane, then over the lanes that hold the others.
+  template <int N>
+  __device__ __forceinline__ void over(float (&v)[N]) {
 #pragma unroll
-    for (int k = 16; k > 0; k /= 2) v += __shfl_xor_sync(0xffffffffu, v, k);
-    if constexpr (WARPS > 1) v = across(make_float2(v, 0.f)).x;
-    return v;
-  }
-  __device__ __forceinline__ float2 two(float2 v) {
+    for (int k = 16; k > 0; k /= 2)
 #pragma unroll
-    for (int k = 16; k > 0; k /= 2) v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, k), __shfl_xor_sync(0xffffffffu, v.y, k)));
-    if constexpr (WARPS > 1) v = across(v);
-    return v;
-  }
-  __device__ __forceinline__ float2 across(float2 v) {
-    if (threadIdx.x % 32 == 0) buffer[turn][threadIdx.x / 32] = v;
-    __syncthreads();
-    float2 s = make_float2(0.f, 0.f);
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], k);
+    if constexpr (WARPS > 1) {
+      if (threadIdx.x % 32 == 0)
 #pragma unroll
-    for (int k = 0; k < PAIRS; k += 2) {
-      const float4 q = *reinterpret_cast<const float4 *>(&buffer[turn][k]);
-      s = add2(s, add2(make_float2(q.x, q.y), make_float2(q.z, q.w)));
+        for (int i = 0; i < N; ++i) buffer[turn][i][threadIdx.x / 32] = v[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float4 q = *reinterpret_cast<const float4 *>(&buffer[turn][i][threadIdx.x % (WARPS / 4) * 4]);
+        v[i] = (q.x + q.y) + (q.z + q.w);
+      }
+#pragma unroll
+      for (int k = 1; k < WARPS / 4; k *= 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], k);
+      turn ^= 1;
     }
-    turn ^= 1;
-    return s;
   }
 };
 
@@ -210,172 +221,198 @@ __device__ __forceinline__ Eight gate_slope(const Eight &g, int act, Eight *fact
   return slope;
 }
 
-// TR: the residual's type.
-template <typename T, typename TR, bool VEC, int MOST>
+// TR: the residual's type; RW: rows side by side.
+template <typename T, typename TR, bool VEC, int MOST, int RW>
 __global__ void __launch_bounds__(MOST) gdp_res_fwd_kernel(const ResProblem p) {
   constexpr int WARPS = MOST > 128 ? MOST / 32 : 1, B = kRes * (int)sizeof(T), R = kRes * (int)sizeof(TR);
-  __shared__ __align__(16) float2 buffer[2][RowSums<WARPS>::PAIRS];
+  __shared__ __align__(16) float buffer[2][3][RowSums<WARPS>::PLACES];
   extern __shared__ __align__(16) unsigned char smem[];
   RowSums<WARPS> sums(buffer);
   const int thread = threadIdx.x, threads = blockDim.x, C = (int)p.C;
   const bool mine = thread * kRes < C;
-  const RowPlaces places(smem, B / 16 * (p.gate ? 2 : 1) + R / 16, p.depth);
-  const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, step = (int64_t)gridDim.x * blockDim.y;
-  const T *block = static_cast<const T *>(p.block) + first * p.block_st + (VEC ? thread * kRes : 0),
-          *gate = static_cast<const T *>(p.gate) + (p.gate ? first * p.gate_st + (VEC ? thread * kRes : 0) : 0);
-  const TR *res = static_cast<const TR *>(p.res) + first * p.res_st + (VEC ? thread * kRes : 0);
-  T *y_to = static_cast<T *>(p.y) + first * p.C;
-  TR *r_to = static_cast<TR *>(p.r) + first * p.C;
-  int64_t asked = first;
-  auto ask = [&](int place) {
-    if (mine && asked < p.T) {
-      places.ask<B>(place, 0, block);
-      places.ask<R>(place, B / 16, res);
-      if (p.gate) places.ask<B>(place, B / 16 + R / 16, gate);
-    }
-    asked += step;
-    block += step * p.block_st;
-    res += step * p.res_st;
-    if (p.gate) gate += step * p.gate_st;
+  const int pieces = B / 16 * (p.gate ? 2 : 1) + R / 16;
+  const RowPlaces places(smem, pieces * RW, p.depth);
+  const int first = blockIdx.x * blockDim.y + threadIdx.y, step = gridDim.x * blockDim.y, T_ = (int)p.T;
+  auto ask = [&](int t, int place) {
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+      if (mine && (unsigned)(t + i * step) < (unsigned)T_) {
+        places.ask<B>(place, i * pieces, row_at<T, VEC>(p.block, t + i * step, p.block_st));
+        places.ask<R>(place, i * pieces + B / 16, row_at<TR, VEC>(p.res, t + i * step, p.res_st));
+        if (p.gate) places.ask<B>(place, i * pieces + B / 16 + R / 16, row_at<T, VEC>(p.gate, t + i * step, p.gate_st));
+      }
     places.close();
   };
   if (VEC)
-    for (int k = 0; k + 1 < p.depth; ++k) ask(k);
+    for (int k = 0; k + 1 < p.depth; ++k) ask(first + k * RW * step, k);
+  constexpr bool KEEP = RW > 1;  // weights in registers
+  Eight post, scale, w;
+  if (KEEP) {
+    post = load_columns<VEC>(p.post, thread, threads, C, 0.f, p.quad_cols);
+    scale = load_columns<VEC>(p.scale, thread, threads, C, 0.f, p.quad_cols);
+    w = load_columns<VEC>(p.w, thread, threads, C, 0.f, p.quad_cols);
+  }
   int place = 0;
-  for (int64_t t = first; t < p.T; t += step, place = place + 1 == p.depth ? 0 : place + 1) {
-    Eight m = eight_of(0.f), r = m, g = m;
+  for (int t = first; (unsigned)t < (unsigned)T_; t += RW * step, place = place + 1 == p.depth ? 0 : place + 1) {
+    Eight m[RW], r[RW], g[RW];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) m[i] = r[i] = g[i] = eight_of(0.f);
     if constexpr (VEC) {
-      if (p.depth == 1) ask(0);
+      if (p.depth == 1) ask(t, 0);
       places.wait();
-      if (p.depth > 1) ask(place == 0 ? p.depth - 1 : place - 1);
-      if (mine) {
-        m = places.get<T>(place, 0);
-        r = places.get<TR>(place, B / 16);
-        if (p.gate) g = places.get<T>(place, B / 16 + R / 16);
-      }
+      if (p.depth > 1) ask(t + (p.depth - 1) * RW * step, place == 0 ? p.depth - 1 : place - 1);
+#pragma unroll
+      for (int i = 0; i < RW; ++i)
+        if (mine && (unsigned)(t + i * step) < (unsigned)T_) {
+          m[i] = places.get<T>(place, i * pieces);
+          r[i] = places.get<TR>(place, i * pieces + B / 16);
+          if (p.gate) g[i] = places.get<T>(place, i * pieces + B / 16 + R / 16);
+        }
     } else {
-      m = load_row<T, VEC>(block, thread, threads, C);
-      r = load_row<TR, VEC>(res, thread, threads, C);
-      if (p.gate) g = load_row<T, VEC>(gate, thread, threads, C);
-      block += step * p.block_st;
-      res += step * p.res_st;
-      if (p.gate) gate += step * p.gate_st;
+      m[0] = load_row<T, VEC>(row_at<T, VEC>(p.block, t, p.block_st), thread, threads, C);
+      r[0] = load_row<TR, VEC>(row_at<TR, VEC>(p.res, t, p.res_st), thread, threads, C);
+      if (p.gate) g[0] = load_row<T, VEC>(row_at<T, VEC>(p.gate, t, p.gate_st), thread, threads, C);
     }
+    float s[RW];
     if (p.post) {
-      const Eight post = load_columns<VEC>(p.post, thread, threads, C, 0.f, p.quad_cols);
-      m = m * post * rsqrtf(fmaf(sums.one(dot(m, m)), p.inv_c, p.eps));
+      if (!KEEP) post = load_columns<VEC>(p.post, thread, threads, C, 0.f, p.quad_cols);
+#pragma unroll
+      for (int i = 0; i < RW; ++i) s[i] = dot(m[i], m[i]);
+      sums.over(s);
+#pragma unroll
+      for (int i = 0; i < RW; ++i) m[i] = m[i] * post * rsqrtf(fmaf(s[i], p.inv_c, p.eps));
     }
-    if (p.gate) m = m * gate_of(g, p.act);
-    if (p.scale) m = m * load_columns<VEC>(p.scale, thread, threads, C, 0.f, p.quad_cols);
-    if (VEC ? mine : true) r = add8(r, m);
-    store_row<TR, VEC>(r_to, thread, threads, C, r);
-    const Eight w = load_columns<VEC>(p.w, thread, threads, C, 0.f, p.quad_cols);
-    const float q = rsqrtf(fmaf(sums.one(dot(r, r)), p.inv_c, p.eps));
-    store_row<T, VEC>(y_to, thread, threads, C, r * w * q);
-    r_to += step * p.C;
-    y_to += step * p.C;
+    if (p.gate)
+#pragma unroll
+      for (int i = 0; i < RW; ++i) m[i] = m[i] * gate_of(g[i], p.act);
+    if (p.scale) {
+      if (!KEEP) scale = load_columns<VEC>(p.scale, thread, threads, C, 0.f, p.quad_cols);
+#pragma unroll
+      for (int i = 0; i < RW; ++i) m[i] = m[i] * scale;
+    }
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      if (!VEC || mine) r[i] = add8(r[i], m[i]);
+      s[i] = dot(r[i], r[i]);
+      if ((unsigned)(t + i * step) < (unsigned)T_) store_row<TR, VEC>(out_at<TR>(p.r, t + i * step, C), thread, threads, C, r[i]);
+    }
+    if (!KEEP) w = load_columns<VEC>(p.w, thread, threads, C, 0.f, p.quad_cols);
+    sums.over(s);
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+      if ((unsigned)(t + i * step) < (unsigned)T_)
+        store_row<T, VEC>(out_at<T>(p.y, t + i * step, C), thread, threads, C, r[i] * w * rsqrtf(fmaf(s[i], p.inv_c, p.eps)));
   }
 }
 
 template <typename T, typename TR, bool VEC, int MOST>
 __global__ void __launch_bounds__(MOST) gdp_res_bwd_kernel(const ResProblem p) {
   constexpr int WARPS = MOST > 128 ? MOST / 32 : 1, B = kRes * (int)sizeof(T), R = kRes * (int)sizeof(TR), PB = B / 16, PR = R / 16;
-  __shared__ __align__(16) float2 buffer[2][RowSums<WARPS>::PAIRS];
+  __shared__ __align__(16) float buffer[2][3][RowSums<WARPS>::PLACES];
   extern __shared__ __align__(16) unsigned char smem[];
   RowSums<WARPS> sums(buffer);
-  const int thread = threadIdx.x, threads = blockDim.x, C = (int)p.C, lane = VEC ? thread * kRes : 0;
+  const int thread = threadIdx.x, threads = blockDim.x, C = (int)p.C;
   const bool mine = thread * kRes < C;
   // pieces: dy, block, r, gate, dr
   const int dr_at = PB * (p.gate ? 3 : 2) + PR;
   const RowPlaces places(smem, dr_at + (p.dr ? PR : 0), p.depth);
-  const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, step = (int64_t)gridDim.x * blockDim.y;
-  const T *dy = static_cast<const T *>(p.dy) + first * p.dy_st + lane, *block = static_cast<const T *>(p.block) + first * p.block_st + lane,
-          *gate = static_cast<const T *>(p.gate) + (p.gate ? first * p.gate_st + lane : 0);
-  const TR *res = static_cast<const TR *>(p.res) + first * p.res_st + lane, *dr = static_cast<const TR *>(p.dr) + (p.dr ? first * p.dr_st + lane : 0);
-  TR *dres = static_cast<TR *>(p.dres) + first * p.C;
-  T *dblock = static_cast<T *>(p.dblock) + first * p.C, *dgate = static_cast<T *>(p.dgate) + (p.gate ? first * p.C : 0);
-  int64_t asked = first;
-  auto advance = [&] {
-    dy += step * p.dy_st;
-    block += step * p.block_st;
-    res += step * p.res_st;
-    if (p.gate) gate += step * p.gate_st;
-    if (p.dr) dr += step * p.dr_st;
+  // weights of the thread's channels, behind the rows: two pieces each
+  unsigned char *kept = smem + p.depth * places.place;
+  const RowPlaces columns(kept, 6, 1);
+  auto column = [&](int k) { return columns.get<float>(0, 2 * k); };
+  if (p.keep) {
+    auto put = [&](int k, const Eight &e) {
+      float4 *a = reinterpret_cast<float4 *>(columns.own + 2 * k * columns.piece), *b = reinterpret_cast<float4 *>(columns.own + (2 * k + 1) * columns.piece);
+      *a = make_float4(e.v[0].x, e.v[0].y, e.v[1].x, e.v[1].y);
+      *b = make_float4(e.v[2].x, e.v[2].y, e.v[3].x, e.v[3].y);
+    };
+    put(0, load_columns<VEC>(p.w, thread, threads, C, 0.f, p.quad_cols));
+    put(1, load_columns<VEC>(p.post, thread, threads, C, 1.f, p.quad_cols));
+    put(2, load_columns<VEC>(p.scale, thread, threads, C, 1.f, p.quad_cols));
+  }
+  auto weights = [&](int k, const float *from, float other) {
+    return p.keep ? column(k) : load_columns<VEC>(from, thread, threads, C, other, p.quad_cols);
   };
-  auto ask = [&](int place) {
-    if (mine && asked < p.T) {
-      places.ask<B>(place, 0, dy);
-      places.ask<B>(place, PB, block);
-      places.ask<R>(place, 2 * PB, res);
-      if (p.gate) places.ask<B>(place, 2 * PB + PR, gate);
-      if (p.dr) places.ask<R>(place, dr_at, dr);
+  const int first = blockIdx.x * blockDim.y + threadIdx.y, step = gridDim.x * blockDim.y, T_ = (int)p.T;
+  auto ask = [&](int t, int place) {
+    if (mine && (unsigned)t < (unsigned)T_) {
+      places.ask<B>(place, 0, row_at<T, VEC>(p.dy, t, p.dy_st));
+      places.ask<B>(place, PB, row_at<T, VEC>(p.block, t, p.block_st));
+      places.ask<R>(place, 2 * PB, row_at<TR, VEC>(p.res, t, p.res_st));
+      if (p.gate) places.ask<B>(place, 2 * PB + PR, row_at<T, VEC>(p.gate, t, p.gate_st));
+      if (p.dr) places.ask<R>(place, dr_at, row_at<TR, VEC>(p.dr, t, p.dr_st));
     }
-    asked += step;
-    advance();
     places.close();
   };
   if (VEC)
-    for (int k = 0; k + 1 < p.depth; ++k) ask(k);
+    for (int k = 0; k + 1 < p.depth; ++k) ask(first + k * step, k);
   int place = 0;
   Eight dw = eight_of(0.f), dpost = dw, dscale = dw;
-  for (int64_t t = first; t < p.T; t += step, place = place + 1 == p.depth ? 0 : place + 1) {
+  for (int t = first; (unsigned)t < (unsigned)T_; t += step, place = place + 1 == p.depth ? 0 : place + 1) {
     Eight n = eight_of(0.f), m = n, d = n, g = n, up = n;
     if constexpr (VEC) {
-      if (p.depth == 1) ask(0);
+      if (p.depth == 1) ask(t, 0);
       places.wait();
-      if (p.depth > 1) ask(place == 0 ? p.depth - 1 : place - 1);
+      if (p.depth > 1) ask(t + (p.depth - 1) * step, place == 0 ? p.depth - 1 : place - 1);
       if (mine) {
         d = places.get<T>(place, 0);
         m = places.get<T>(place, PB);
         n = places.get<TR>(place, 2 * PB);
       }
     } else {
-      d = load_row<T, VEC>(dy, thread, threads, C);
-      m = load_row<T, VEC>(block, thread, threads, C);
-      n = load_row<TR, VEC>(res, thread, threads, C);
-      if (p.gate) g = load_row<T, VEC>(gate, thread, threads, C);
-      if (p.dr) up = load_row<TR, VEC>(dr, thread, threads, C);
-      advance();
+      d = load_row<T, VEC>(row_at<T, VEC>(p.dy, t, p.dy_st), thread, threads, C);
+      m = load_row<T, VEC>(row_at<T, VEC>(p.block, t, p.block_st), thread, threads, C);
+      n = load_row<TR, VEC>(row_at<TR, VEC>(p.res, t, p.res_st), thread, threads, C);
+      if (p.gate) g = load_row<T, VEC>(row_at<T, VEC>(p.gate, t, p.gate_st), thread, threads, C);
+      if (p.dr) up = load_row<TR, VEC>(row_at<TR, VEC>(p.dr, t, p.dr_st), thread, threads, C);
     }
-    // the second norm: n becomes its normed values, d the gradient of the stream
-    const Eight w = load_columns<VEC>(p.w, thread, threads, C, 0.f, p.quad_cols);
-    const float2 s = sums.two(make_float2(dot(n, n), dot(m, m)));
-    const float r = rsqrtf(fmaf(s.x, p.inv_c, p.eps)), q = p.post ? rsqrtf(fmaf(s.y, p.inv_c, p.eps)) : 1.f;
+    // The second norm: n its normed values.  The stream's gradient is  d_r = r (d w - n mean(d w n)) + up, and what goes on
+    // to the first norm's values m is d_r k with k = scale act(gate) post.  Its own mean(d_r k m) is linear in the other
+    // mean, so that one pass over the row gives both:  mean((r d w + up) k m) - r mean(d w n) mean(n k m).
+    const Eight w = weights(0, p.w, 0.f);
+    float s[2] = {dot(n, n), dot(m, m)};
+    if (VEC && mine) {
+      if (p.gate) g = places.get<T>(place, 2 * PB + PR);
+      if (p.dr) up = places.get<TR>(place, dr_at);
+    }
+    sums.over(s);
+    const float r = rsqrtf(fmaf(s[0], p.inv_c, p.eps)), q = p.post ? rsqrtf(fmaf(s[1], p.inv_c, p.eps)) : 1.f;
     n = n * r;
+    m = m * q;
     dw = fma8(d, n, dw);
     d = d * w;
-    if (VEC && mine && p.dr) up = places.get<TR>(place, dr_at);
-    const Eight post = load_columns<VEC>(p.post, thread, threads, C, 1.f, p.quad_cols);
-    float mean = sums.one(dot(d, n)) * p.inv_c;
-#pragma unroll
-    for (int k = 0; k < kPairs; ++k) d.v[k] = fma2(fma2(n.v[k], both(-mean), d.v[k]), both(r), up.v[k]);
-    store_row<TR, VEC>(dres, thread, threads, C, d);
-    // the first one, under gate and scale: m its normed values, d becomes their gradient
-    m = m * q;
-    if (p.gate) {
-      if (VEC && mine) g = places.get<T>(place, 2 * PB + PR);
-      Eight a;
-      const Eight slope = gate_slope(g, p.act, &a), u = m * post;
-      Eight through = d;  // of the gated norm
-      if (p.scale) through = d * load_columns<VEC>(p.scale, thread, threads, C, 1.f, p.quad_cols);
-      store_row<T, VEC>(dgate, thread, threads, C, through * u * slope);
-      if (p.scale) dscale = fma8(d * a, u, dscale);
-      d = through * a;
-      dgate += step * p.C;
-    } else if (p.scale) {
-      dscale = fma8(d, m * post, dscale);
-      d = d * load_columns<VEC>(p.scale, thread, threads, C, 1.f, p.quad_cols);
+    Eight a = eight_of(1.f), slope = a;
+    if (p.gate) slope = gate_slope(g, p.act, &a);
+    const Eight post = weights(1, p.post, 1.f), scale = weights(2, p.scale, 1.f);
+    const Eight u = m * post;          // what gate and scale multiply
+    up = fma8(d, eight_of(r), up);     // d_r but for its mean
+    float means[3] = {dot(d, n), 0.f, 0.f};
+    if (p.post) {
+      const Eight ku = a * scale * u;  // k m
+      means[1] = dot(up, ku);
+      means[2] = dot(n, ku);
+      sums.over(means);
+    } else {
+      float first_mean[1] = {means[0]};
+      sums.over(first_mean);
+      means[0] = first_mean[0];
+    }
+    const float back = -r * means[0] * p.inv_c;
+    d = fma8(n, eight_of(back), up);
+    store_row<TR, VEC>(out_at<TR>(p.dres, t, C), thread, threads, C, d);
+    if (p.gate) store_row<T, VEC>(out_at<T>(p.dgate, t, C), thread, threads, C, d * scale * u * slope);
+    d = d * a;
+    if (p.scale) {
+      dscale = fma8(d, u, dscale);
+      d = d * scale;
     }
     if (p.post) {
       dpost = fma8(d, m, dpost);
-      d = d * post;
-      mean = sums.one(dot(d, m)) * p.inv_c;
+      const float mean = fmaf(back, means[2], means[1]) * p.inv_c;
 #pragma unroll
-      for (int k = 0; k < kPairs; ++k) d.v[k] = mul2(fma2(m.v[k], both(-mean), d.v[k]), both(q));
+      for (int k = 0; k < kPairs; ++k) d.v[k] = mul2(fma2(m.v[k], both(-mean), mul2(d.v[k], post.v[k])), both(q));
     }
-    store_row<T, VEC>(dblock, thread, threads, C, d);
-    dres += step * p.C;
-    dblock += step * p.C;
+    store_row<T, VEC>(out_at<T>(p.dblock, t, C), thread, threads, C, d);
   }
   float *out = p.partial + (int64_t)blockIdx.x * 3 * C;
   if constexpr (WARPS == 1) {  // the CTA's warps' sums, one after the other
@@ -412,26 +449,38 @@ __global__ void __launch_bounds__(MOST) gdp_res_bwd_kernel(const ResProblem p) {
 }
 
 // Places of a row in shared memory (see RowPlaces) for `ctas` resident CTAs: three, or as many as there is room for.
-inline int res_depth(int bytes, int ctas) {
-  const int room = 226 * 1024 / ctas - 1024;
+inline int res_depth(int bytes, int ctas, int others) {
+  const int room = 226 * 1024 / ctas - 1024 - others;
   return 3 * bytes <= room ? 3 : 2 * bytes <= room ? 2 : 1;
 }
-template <typename T, typename TR, int MOST>
-cudaError_t res_fwd(ResProblem &p, int vec, cudaStream_t stream) {
-  const dim3 block(res_threads(p.C), res_rows(p.C));
-  const int threads = block.x * block.y, per_sm = 1024 / threads;
-  const int row = threads * kRes * ((int)sizeof(T) * (p.gate ? 2 : 1) + (int)sizeof(TR));
-  p.depth = res_depth(row, per_sm);
-  const int smem = vec ? p.depth * row : 0;
-  const int64_t rows = (p.T + block.y - 1) / block.y, resident = (int64_t)sm_count() * per_sm;
-  const dim3 grid((unsigned)(rows < resident || !vec ? rows : resident));
-  const auto kernel = vec ? gdp_res_fwd_kernel<T, TR, true, MOST> : gdp_res_fwd_kernel<T, TR, false, MOST>;
+template <typename K>
+cudaError_t res_launch(K kernel, const ResProblem &p, int64_t ctas, dim3 block, int smem, cudaStream_t stream) {
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<grid, block, smem, stream>>>(p);
+  kernel<<<(unsigned)ctas, block, smem, stream>>>(p);
   return cudaGetLastError();
+}
+template <typename T, typename TR, int MOST>
+cudaError_t res_fwd(ResProblem &p, int vec, cudaStream_t stream) {
+  const dim3 block(res_threads(p.C), res_rows(p.C));
+  const int threads = block.x * block.y;
+  const int row = threads * kRes * ((int)sizeof(T) * (p.gate ? 2 : 1) + (int)sizeof(TR));
+  const int64_t rows = (p.T + block.y - 1) / block.y;
+  if (!vec) return res_launch(gdp_res_fwd_kernel<T, TR, false, MOST, 1>, p, rows, block, 0, stream);
+  if constexpr (MOST == 512) {  // two rows side by side, where every SM has several pairs of them
+    const int per_sm = 512 / threads > 1 ? 512 / threads : 1;
+    const int64_t resident = (int64_t)sm_count() * per_sm;
+    if (rows >= 8 * resident) {
+      p.depth = res_depth(2 * row, per_sm, 0);
+      return res_launch(gdp_res_fwd_kernel<T, TR, true, MOST, 2>, p, resident, block, p.depth * 2 * row, stream);
+    }
+  }
+  const int per_sm = 1024 / threads;
+  p.depth = res_depth(row, per_sm, 0);
+  const int64_t resident = (int64_t)sm_count() * per_sm;
+  return res_launch(gdp_res_fwd_kernel<T, TR, true, MOST, 1>, p, rows < resident ? rows : resident, block, p.depth * row, stream);
 }
 template <typename T, typename TR>
 cudaError_t res_fwd_by(ResProblem &p, int vec, cudaStream_t stream) {
@@ -445,19 +494,14 @@ cudaError_t launch_res_fwd(ResProblem &p, int vec, cudaStream_t stream) {
 template <typename T, typename TR, int MOST>
 cudaError_t res_bwd(ResProblem &p, int vec, int64_t ctas, cudaStream_t stream) {
   const dim3 block(res_threads(p.C), res_rows(p.C));
-  const int threads = block.x * block.y;
-  const int row = threads * kRes * ((int)sizeof(T) * (p.gate ? 3 : 2) + (int)sizeof(TR) * (p.dr ? 2 : 1));
-  p.depth = res_depth(row, kResResident / threads > 1 ? kResResident / threads : 1);
+  const int threads = block.x * block.y, per_sm = kResResident / threads > 1 ? kResResident / threads : 1;
+  const int row = threads * kRes * ((int)sizeof(T) * (p.gate ? 3 : 2) + (int)sizeof(TR) * (p.dr ? 2 : 1)), kept = threads * kRes * 3 * 4;
+  p.depth = res_depth(row, per_sm, kept);
+  p.keep = vec && p.depth * row + kept <= 226 * 1024 / per_sm - 1024;
   const int sums = block.y > 1 ? (int)block.y * 3 * 256 * (int)sizeof(float) : 0;
-  int smem = vec ? p.depth * row : 0;
+  int smem = vec ? p.depth * row + (p.keep ? kept : 0) : 0;
   if (smem < sums) smem = sums;
-  const auto kernel = vec ? gdp_res_bwd_kernel<T, TR, true, MOST> : gdp_res_bwd_kernel<T, TR, false, MOST>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  kernel<<<(unsigned)ctas, block, smem, stream>>>(p);
-  return cudaGetLastError();
+  return res_launch(vec ? gdp_res_bwd_kernel<T, TR, true, MOST> : gdp_res_bwd_kernel<T, TR, false, MOST>, p, ctas, block, smem, stream);
 }
 template <typename T, typename TR>
 cudaError_t res_bwd_by(ResProblem &p, int vec, int64_t ctas, cudaStream_t stream) {
