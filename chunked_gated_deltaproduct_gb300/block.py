@@ -151,7 +151,7 @@ def _address(t):
 def _output(output, x, shape, dev):
     """(output, its address, whether the call allocated it)."""
     if output is None:
-        output = torch.empty(shape, dtype=x.dtype, device=x.device)
+        output = torch.empty_like(x, memory_format=torch.contiguous_format)
         return output, output.data_ptr(), 1
     return output, _dense("output", output, shape, x.dtype, dev), 0
 
@@ -423,7 +423,7 @@ def residual_norm(residual, block, weight, post_weight=None, gate=None, activati
     code = _activation(_GATE_ACTS, activation)
     output, yp, _ = _output(output, block, shape, dev)
     if output_residual is None:
-        output_residual = torch.empty(shape, dtype=residual.dtype, device=block.device)
+        output_residual = torch.empty_like(residual, memory_format=torch.contiguous_format)
         op = output_residual.data_ptr()
     else:
         op = _dense("output_residual", output_residual, shape, residual.dtype, dev)

@@ -147,10 +147,10 @@ __device__ __forceinline__ void activate(Pairs<V> &y) {
 // Final state of sequence i: the last K rows of the incoming state and the sequence's rows.  All are read before any is
 // written (the cache is updated in place).
 template <typename T, int V, int K>
-__device__ __forceinline__ void final_state(const ConvProblem &p, int64_t i, int64_t c) {
+__device__ __forceinline__ void final_state(const ConvProblem &p, int64_t i, int64_t c) {  // (reports bad slots, an empty sequence's too)
   const T *src;
   T *dst;
-  state_of<T>(p.s, i, K * p.C, p.p.status, false, &src, &dst);
+  state_of<T>(p.s, i, K * p.C, p.p.status, c == 0, &src, &dst);
   if (!dst) return;
   int64_t b, e;
   seq_rows(p.p, i, &b, &e);

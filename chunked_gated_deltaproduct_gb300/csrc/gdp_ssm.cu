@@ -34,7 +34,7 @@ gdp_status common(const Args *a, SsmProblem *p) {
   p->A = a->A; p->D = a->D; p->bias = a->dt_bias;
   p->p = Packed{a->cu_seqlens, a->cu_seqlens_int64 != 0, a->T, a->N, a->device_status};
   p->C = a->C; p->S = a->S; p->G = a->G;
-  p->per = per; p->tiles = tiles;
+  p->per = per; p->tiles = (int)tiles;
   p->dt_f32 = a->dt_dtype == GDP_DTYPE_F32;
   p->softplus = a->dt_softplus != 0;
   p->sms = sm_count();
@@ -44,6 +44,8 @@ gdp_status common(const Args *a, SsmProblem *p) {
                  rows_by(p->dt, p->dt_st, a->T, a->dt_dtype, 16) && (ds == es || per * ds % 16 == 0) && rows_by(p->z, p->z_st, a->T, a->x_dtype, 16);
   p->fast_vectors = a->S * es % 16 == 0 && rows_by(p->B, p->B_st, a->T, a->x_dtype, 16) && rows_by(p->Cm, p->C_st, a->T, a->x_dtype, 16) &&
                     p->B_sg * es % 16 == 0 && p->C_sg * es % 16 == 0;
+  p->quad_vectors = a->S % 4 == 0 && aligned(a->A, 16) && rows_by(p->B, p->B_st, a->T, a->x_dtype, 4 * es) &&
+                    rows_by(p->Cm, p->C_st, a->T, a->x_dtype, 4 * es) && p->B_sg % 4 == 0 && p->C_sg % 4 == 0;
   p->pair_out = a->C % 2 == 0 && per % 2 == 0;
   return GDP_OK;
 }

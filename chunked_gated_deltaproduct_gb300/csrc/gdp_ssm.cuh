@@ -13,13 +13,15 @@ struct SsmProblem {
   void *y;
   Packed p;
   int64_t C, S, G;
-  int64_t per, tiles;  // channels of a group; CTAs that share a group's channels
+  int64_t per;         // channels of a group
+  int tiles;           // CTAs that share a group's channels
   StateModes s;
   float *chunks;       // states entering every chunk, written by the forward and read by the backward pass
   int dt_f32, softplus, zero_pad;
   int sms;             // of the device
   int fast_rows;       // x, dt and z can be copied by 16 bytes from every CTA's first channel on
   int fast_vectors;    // B and C likewise
+  int quad_vectors;    // A, B and C can be read by four states
   int pair_out;        // outputs can be written by two channels
   int quad_states;     // four states at a time: S a multiple of four, every state buffer on 16 bytes
   // Pieces: where whole sequences leave SMs idle, pieces of `piece` tokens (0: whole sequences) run side by side, first

@@ -66,8 +66,8 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
     s.z = s.dt + K * CH * dt_size;
     return s;
   };
-  const unsigned across = (unsigned)(p.G * p.tiles), tile = blockIdx.x % across;
-  const int64_t worker = blockIdx.x / across, g = tile / p.tiles, c0 = g * p.per + (tile % p.tiles) * CH;
+  const unsigned across = (unsigned)(p.G * p.tiles), tile = blockIdx.x % across, group = tile / (unsigned)p.tiles;
+  const int64_t worker = blockIdx.x / across, g = group, c0 = g * p.per + (tile - group * p.tiles) * CH;
   const int cn = (int)min((int64_t)CH, (g + 1) * p.per - c0);
   if (blockIdx.x == 0 && !LOCAL) check_packed(p.p);
   if (LOCAL) sm100::pdl_trigger();

@@ -39,8 +39,8 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, 3) gdp_ssm_fwd_k
   float *Cs = Bs + 2 * kSsmTile * SP;                                      // [2][tile][SP]
   float *ys = Cs + 2 * kSsmTile * SP;                                      // [2][tile][YP]
   unsigned char *ring = reinterpret_cast<unsigned char *>(ys + 2 * kSsmTile * YP);
-  const unsigned across = (unsigned)(p.G * p.tiles), tile = blockIdx.x % across;  // all channels of a piece, then the next one
-  const int64_t r = blockIdx.x / across, g = tile / p.tiles, c0 = g * p.per + (tile % p.tiles) * CH;
+  const unsigned across = (unsigned)(p.G * p.tiles), tile = blockIdx.x % across, group = tile / (unsigned)p.tiles;  // all channels of a piece, then the next one
+  const int64_t r = blockIdx.x / across, g = group, c0 = g * p.per + (tile - group * p.tiles) * CH;
   const int cn = (int)min((int64_t)CH, (g + 1) * p.per - c0);
   if (blockIdx.x == 0 && !LOCAL) check_packed(p.p);
   if (LOCAL) sm100::pdl_trigger();
@@ -372,40 +372,91 @@ __global__ void __launch_bounds__(kSsmThreads) gdp_ssm_join_kernel(const SsmProb
   }
 }
 
-// One token per sequence: the states are read and written once.
-template <typename T, int L>
+// Four values of a vector's states, n of them exist; `quad`: they can be read together.
+template <typename T>
+__device__ __forceinline__ void load_quad(const T *at, int n, int quad, float (&v)[kQ]) {
+  if (quad && n == kQ) {
+    const Vec<T, kQ> q = load_vec<T, kQ>(at);
+#pragma unroll
+    for (int k = 0; k < kQ; ++k) v[k] = to_f32(q.v[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kQ; ++k) v[k] = k < n ? to_f32(at[k]) : 0.f;
+  }
+}
+
+// One token per sequence: the states are read and written once (64 x 4096 x 16: 33.5 MB).  U sequences per CTA: A is read
+// once for them, their loads are under way together, and what a (sequence, channel) pair needs once is formed by one of
+// the channel's lanes for each sequence (64 x 4096 x 16 on the device: 12.5 us with every lane for itself, one sequence).
+template <typename T, int L, int U>
 __global__ void __launch_bounds__(kSsmThreads) gdp_ssm_step_kernel(const SsmProblem p) {
   const SsmPlace<L> at(p, blockIdx.y);
-  const int64_t i = blockIdx.x;
-  const float *src;
-  float *dst;
-  state_of<float>(p.s, i, p.C * p.S, p.p.status, threadIdx.x == 0 && blockIdx.y == 0, &src, &dst);
   const bool real = at.ch < at.cn;
-  const int64_t mine = at.c * p.S + at.j * kQ;
-  float h[kQ] = {}, v = 0.f, x = 0.f, y = 0.f;
-  if (src) load_states(src + mine, at.n, p.quad_states, h);
-  if (real) {
-    v = load_step<T>(p, i, at.c);
-    if (p.softplus) v = softplus(v);
-    x = to_f32(static_cast<const T *>(p.x)[i * p.x_st + at.c]);
-  }
-  const T *B = static_cast<const T *>(p.B) + i * p.B_st + at.g * p.B_sg + at.j * kQ,
-          *Cm = static_cast<const T *>(p.Cm) + i * p.C_st + at.g * p.C_sg + at.j * kQ;
+  const int64_t mine = at.c * p.S + at.j * kQ, first = (int64_t)blockIdx.x * U, per = p.C * p.S;
+  const int own = at.j % U;  // the lane's sequence
+  const int64_t i = first + own;
+  int64_t slot[U];
 #pragma unroll
-  for (int k = 0; k < kQ; ++k)
-    if (k < at.n) {
-      h[k] = fmaf(ex2(v * (p.A[mine + k] * kLog2e)), h[k], v * x * to_f32(B[k]));
-      y = fmaf(to_f32(Cm[k]), h[k], y);
+  for (int u = 0; u < U; ++u) slot[u] = p.s.cache && first + u < p.p.N ? p.s.slots[first + u] : 0;
+  float A[kQ], h[U][kQ], B[U][kQ], Cm[U][kQ], v = 0.f, x = 0.f, z = 0.f;
+  load_quad(p.A + mine, at.n, p.quad_vectors, A);
+  if (real && i < p.p.N) {
+    v = load_step<T>(p, i, at.c);
+    x = to_f32(static_cast<const T *>(p.x)[i * p.x_st + at.c]);
+    if (p.z) z = to_f32(static_cast<const T *>(p.z)[i * p.z_st + at.c]);
+  }
+  const T *B_at = static_cast<const T *>(p.B) + first * p.B_st + at.g * p.B_sg + at.j * kQ,
+          *C_at = static_cast<const T *>(p.Cm) + first * p.C_st + at.g * p.C_sg + at.j * kQ;
+  float *dst[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const bool exists = first + u < p.p.N;
+    load_quad(B_at, exists ? at.n : 0, p.quad_vectors, B[u]);
+    load_quad(C_at, exists ? at.n : 0, p.quad_vectors, Cm[u]);
+    if (first + u + 1 < p.p.N) B_at += p.B_st, C_at += p.C_st;
+    const float *src = nullptr;
+    dst[u] = nullptr;
+    if (p.s.cache) {
+      const bool good = exists && slot[u] >= 0 && slot[u] < p.s.num_slots;
+      if (exists && !good && slot[u] != -1 && threadIdx.x == 0 && blockIdx.y == 0) set_status(p.p.status, GDP_DEV_ERR_SLOT);
+      if (good) src = dst[u] = static_cast<float *>(p.s.cache) + slot[u] * per + mine;
+    } else if (exists) {
+      if (p.s.init) src = static_cast<const float *>(p.s.init) + (first + u) * per + mine;
+      if (p.s.fin) dst[u] = static_cast<float *>(p.s.fin) + (first + u) * per + mine;
     }
-  sum_scatter<1, L, 1>(&y, at.j);
-  if (dst) store_states(dst + mine, at.n, p.quad_states, h);
-  if (real && at.j == 0) {
-    if (p.D) y = fmaf(p.D[at.c], x, y);
-    if (p.z) {
-      const float z = to_f32(static_cast<const T *>(p.z)[i * p.z_st + at.c]);
-      y *= z * sigmoid_fast(z);
-    }
-    static_cast<T *>(p.y)[i * p.C + at.c] = from_f32<T>(y);
+#pragma unroll
+    for (int k = 0; k < kQ; ++k) h[u][k] = 0.f;
+    if (src) load_states(src, at.n, p.quad_states, h[u]);
+  }
+  if (p.softplus) v = softplus(v);
+  const float in = v * x;
+#pragma unroll
+  for (int k = 0; k < kQ; ++k) A[k] *= kLog2e;
+  float y[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float e = U > 1 ? __shfl_sync(0xffffffffu, v, u, L) : v, ex = U > 1 ? __shfl_sync(0xffffffffu, in, u, L) : in;
+    y[u] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kQ; ++k)
+      if (k < at.n) {
+        h[u][k] = fmaf(ex2(e * A[k]), h[u][k], ex * B[u][k]);
+        y[u] = fmaf(Cm[u][k], h[u][k], y[u]);
+      }
+    if (dst[u]) store_states(dst[u], at.n, p.quad_states, h[u]);
+  }
+  // sequence u's readout to the channel's lane u
+  float mine_y = 0.f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int k = L / 2; k > 0; k /= 2) y[u] += __shfl_xor_sync(0xffffffffu, y[u], k);
+    if (own == u) mine_y = y[u];
+  }
+  if (real && at.j < U && i < p.p.N) {
+    if (p.D) mine_y = fmaf(p.D[at.c], x, mine_y);
+    if (p.z) mine_y *= z * sigmoid_fast(z);
+    static_cast<T *>(p.y)[i * p.C + at.c] = from_f32<T>(mine_y);
   }
 }
 
@@ -434,7 +485,7 @@ cudaError_t ssm_fwd_by(const SsmProblem &p, cudaStream_t stream) {
   // A CTA alone on its SM is bound by its warps' own latencies, and twice the warps with half the channels take 16 % off
   // (8192 x 4096: 321 against 384 us); where several share an SM the work counts, and loading B and C once for two
   // channels does (8 x 4096 x 4096: 809 against 836 us).
-  if (FULL && !p.piece && p.pieces * p.G * p.tiles <= p.sms) return ssm_fwd<T, L, FULL ? 1 : 2, FULL, false>(p, stream);
+  if (FULL && !p.piece && p.pieces * p.G * (int64_t)p.tiles <= p.sms) return ssm_fwd<T, L, FULL ? 1 : 2, FULL, false>(p, stream);
   return ssm_fwd<T, L, 2, FULL, false>(p, stream);
 }
 template <typename T>
@@ -445,14 +496,18 @@ cudaError_t launch_ssm_fwd(const SsmProblem &p, cudaStream_t stream) {
   if (lanes == 8) return full ? ssm_fwd_by<T, 8, true>(p, stream) : ssm_fwd_by<T, 8, false>(p, stream);
   return full ? ssm_fwd_by<T, 16, true>(p, stream) : ssm_fwd_by<T, 16, false>(p, stream);
 }
+template <typename T, int L>
+cudaError_t ssm_step(const SsmProblem &p, cudaStream_t stream) {
+  // two sequences a CTA where there are plenty (64 x 4096 x 16: 10.4 us, one 12.8, four 12.3), one for latency
+  const int64_t tiles = p.G * p.tiles;
+  if (p.p.N * tiles >= 16 * p.sms) gdp_ssm_step_kernel<T, L, 2><<<dim3((unsigned)((p.p.N + 1) / 2), (unsigned)tiles), kSsmThreads, 0, stream>>>(p);
+  else gdp_ssm_step_kernel<T, L, 1><<<dim3((unsigned)p.p.N, (unsigned)tiles), kSsmThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
 template <typename T>
 cudaError_t launch_ssm_step(const SsmProblem &p, cudaStream_t stream) {
-  const dim3 grid((unsigned)p.p.N, (unsigned)(p.G * p.tiles));
   const int lanes = ssm_lanes(p.S);
-  if (lanes == 4) gdp_ssm_step_kernel<T, 4><<<grid, kSsmThreads, 0, stream>>>(p);
-  else if (lanes == 8) gdp_ssm_step_kernel<T, 8><<<grid, kSsmThreads, 0, stream>>>(p);
-  else gdp_ssm_step_kernel<T, 16><<<grid, kSsmThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return lanes == 4 ? ssm_step<T, 4>(p, stream) : lanes == 8 ? ssm_step<T, 8>(p, stream) : ssm_step<T, 16>(p, stream);
 }
 
 }  // namespace layer

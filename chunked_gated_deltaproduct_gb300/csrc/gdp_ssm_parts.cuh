@@ -98,9 +98,9 @@ struct SsmPlace {
   int cn;         // the CTA's channels
   int ch, j, n;   // the thread's channel in the CTA, lane of the channel, states that exist
   int64_t c;
-  __device__ __forceinline__ SsmPlace(const SsmProblem &p, int64_t tile) {
+  __device__ __forceinline__ SsmPlace(const SsmProblem &p, int tile) {
     g = tile / p.tiles;
-    c0 = g * p.per + (tile % p.tiles) * CH;
+    c0 = g * p.per + tile % p.tiles * CH;
     cn = (int)min((int64_t)CH, (g + 1) * p.per - c0);
     ch = threadIdx.x / L;
     j = threadIdx.x % L;
