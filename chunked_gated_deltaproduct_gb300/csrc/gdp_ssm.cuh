@@ -27,6 +27,7 @@ struct SsmProblem {
   // Pieces: where whole sequences leave SMs idle, pieces of `piece` tokens (0: whole sequences) run side by side, first
   // from zero for the states they reach, which are then joined to the states entering them.
   int64_t piece, pieces;  // tokens; rows of pieces (or sequences)
+  int ranked;             // whole sequences, the longest first
   float *enter, *spans;   // [pieces][C][S] and [pieces][C]
   // backward
   const void *dy;
@@ -45,9 +46,13 @@ constexpr int kSsmChunk = GDP_SCAN_CHUNK;
 // Lanes that share a channel, four states each.
 inline int ssm_lanes(int64_t S) { return S <= 16 ? 4 : S <= 32 ? 8 : 16; }
 inline int64_t ssm_tiles(int64_t per, int64_t S) { return (per * ssm_lanes(S) + kSsmThreads - 1) / kSsmThreads; }
-// Workers of the backward pass: as many as fill the SMs four times, and no more than there are sequences.
+// Sequences that can be ranked by length: where there are more CTAs than are resident at once, the longest come first, so that
+// none of them is what the last SMs wait for (64 packed requests of 16 to 8192 tokens x 2048: RANKTIMES us).
+constexpr int kSsmRanked = 256;
+inline bool ssm_ranked(int64_t N, int64_t tiles, int sms) { return N > 1 && N <= kSsmRanked && N * tiles > 2 * sms; }
+// Workers of the backward pass: as many as give every SM 16 CTAs, and no more than there are sequences.
 inline int64_t ssm_workers(int64_t N, int64_t tiles, int sms) {
-  int64_t n = (4 * (int64_t)sms + tiles - 1) / tiles;
+  int64_t n = (16 * (int64_t)sms + tiles - 1) / tiles;
   if (n > N) n = N;
   return n < 1 ? 1 : n;
 }

@@ -79,6 +79,9 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
     if (p.piece) sm100::pdl_wait();
     return;
   }
+  __shared__ SsmOrder by_length;
+  if (!LOCAL && p.ranked) by_length.rank(p);
+  auto row_of = [&](int64_t r) { return !LOCAL && p.ranked ? (int64_t)by_length.order[r] : r; };
   const bool running = threadIdx.x < RT;
   float *out = p.over_rows + worker * ssm_sum_cols(p.C, p.S);
   if (running) {
@@ -112,7 +115,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
     };
     if (p.piece && !LOCAL) sm100::pdl_wait();
     for (int64_t r = worker; r < p.pieces; r += p.workers) {
-      const SsmPiece at_rows(p, r);
+      const SsmPiece at_rows(p, row_of(r));
       if (p.piece && (at_rows.b >= at_rows.e || (LOCAL && at_rows.first))) continue;
       const int chunks = (int)((at_rows.e - at_rows.b + K - 1) / K);
       float2 back[2][2];  // exp(e A) H of the token after
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
   const float2 D = make_float2(p.D && c < cn ? p.D[c0 + c] : 0.f, p.D && c + 1 < cn ? p.D[c0 + c + 1] : 0.f);
   float2 dD = make_float2(0.f, 0.f), dbias = make_float2(0.f, 0.f);
   for (int64_t r = worker; r < p.pieces; r += p.workers) {
-    const SsmPiece at_rows(p, r);
+    const SsmPiece at_rows(p, row_of(r));
     if (p.piece && (at_rows.b >= at_rows.e || (LOCAL && at_rows.first))) continue;
     const int chunks = (int)((at_rows.e - at_rows.b + K - 1) / K);
     // step k goes over chunk chunks - 1 - k

@@ -49,7 +49,9 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, 3) gdp_ssm_fwd_k
     zero_tail<T>(p, static_cast<T *>(p.y), c0, cn);
     return;
   }
-  const SsmPiece at_rows(p, r);
+  __shared__ SsmOrder by_length;
+  if (!LOCAL && p.ranked) by_length.rank(p);
+  const SsmPiece at_rows(p, !LOCAL && p.ranked ? by_length.order[r] : r);
   const int64_t b = at_rows.b, e = at_rows.e;
   if (p.piece && (b >= e || (LOCAL && at_rows.last))) {
     if (!LOCAL) sm100::pdl_wait();

@@ -109,6 +109,28 @@ struct SsmPlace {
   }
 };
 
+// A CTA's threads: the sequences by length into `order`, the longest first, ties in their own order.
+struct SsmOrder {
+  int lengths[kSsmRanked];
+  unsigned short order[kSsmRanked];
+  __device__ __forceinline__ void rank(const SsmProblem &p) {
+    const int n = (int)p.p.N;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      int64_t b, e;
+      seq_rows(p.p, i, &b, &e);
+      lengths[i] = (int)(e - b);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const int mine = lengths[i];
+      int before = 0;
+      for (int j = 0; j < n; ++j) before += lengths[j] > mine || (lengths[j] == mine && j < i);
+      order[before] = (unsigned short)i;
+    }
+    __syncthreads();
+  }
+};
+
 // Piece r of the packed sequences: whole sequences, or pieces of p.piece tokens (piece q of sequence i is row
 // cu_seqlens[i] / p.piece + i + q; the rows between are empty).
 struct SsmPiece {
