@@ -18,27 +18,27 @@ template <typename T, int CH, int SP>
 struct SsmStage {
   unsigned char *x, *dt, *z, *B, *C;
 };
-template <typename T, int CH, int SP>
+template <typename T, int CH, int SP, int TILE>
 __host__ __device__ constexpr int ssm_stage_bytes(int dt_size, bool gated) {
-  return kSsmTile * (CH * ((int)sizeof(T) * (gated ? 2 : 1) + dt_size) + 2 * SP * (int)sizeof(T));
+  return TILE * (CH * ((int)sizeof(T) * (gated ? 2 : 1) + dt_size) + 2 * SP * (int)sizeof(T));
 }
-template <typename T, int L, int CPT>
+template <typename T, int L, int CPT, int TILE>
 constexpr int ssm_fwd_bytes(int dt_size, bool gated) {
   constexpr int CH = kSsmThreads / L, SP = L * kQ;
-  return kSsmStages * ssm_stage_bytes<T, CH, SP>(dt_size, gated) + 2 * kSsmTile * (CH * 12 + ssm_skew(CPT) * 4 + SP * 8);
+  return kSsmStages * ssm_stage_bytes<T, CH, SP, TILE>(dt_size, gated) + 2 * TILE * (CH * 12 + ssm_skew(CPT) * 4 + SP * 8);
 }
 
-template <typename T, int L, int CPT, bool FULL, bool LOCAL>
-__global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, 3) gdp_ssm_fwd_kernel(const SsmProblem p) {
+template <typename T, int L, int CPT, int TILE, bool FULL, bool LOCAL>
+__global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, CPT == 1 ? 1 : 3) gdp_ssm_fwd_kernel(const SsmProblem p) {
   constexpr int CH = kSsmThreads / L, SP = L * kQ, CP = CH / 2, HT = kSsmFeed, RT = kSsmThreads / CPT, YP = CH + ssm_skew(CPT);
   extern __shared__ __align__(128) unsigned char smem[];
   const int dt_size = p.dt_f32 ? 4 : (int)sizeof(T);
-  const int stage_bytes = ssm_stage_bytes<T, CH, SP>(dt_size, p.z != nullptr);
+  const int stage_bytes = ssm_stage_bytes<T, CH, SP, TILE>(dt_size, p.z != nullptr);
   float2 *steps = reinterpret_cast<float2 *>(smem);                        // [2][tile][CH]: e, e x
-  float *Bs = reinterpret_cast<float *>(steps + 2 * kSsmTile * CH);        // [2][tile][SP]
-  float *Cs = Bs + 2 * kSsmTile * SP;                                      // [2][tile][SP]
-  float *ys = Cs + 2 * kSsmTile * SP;                                      // [2][tile][YP]
-  unsigned char *ring = reinterpret_cast<unsigned char *>(ys + 2 * kSsmTile * YP);
+  float *Bs = reinterpret_cast<float *>(steps + 2 * TILE * CH);        // [2][tile][SP]
+  float *Cs = Bs + 2 * TILE * SP;                                      // [2][tile][SP]
+  float *ys = Cs + 2 * TILE * SP;                                      // [2][tile][YP]
+  unsigned char *ring = reinterpret_cast<unsigned char *>(ys + 2 * TILE * YP);
   const unsigned across = (unsigned)(p.G * p.tiles), tile = blockIdx.x % across, group = tile / (unsigned)p.tiles;  // all channels of a piece, then the next one
   const int64_t r = blockIdx.x / across, g = group, c0 = g * p.per + (tile - group * p.tiles) * CH;
   const int cn = (int)min((int64_t)CH, (g + 1) * p.per - c0);
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, 3) gdp_ssm_fwd_k
     if (!LOCAL) sm100::pdl_wait();
     return;
   }
-  const int tiles = (int)((e - b + kSsmTile - 1) / kSsmTile);
+  const int tiles = (int)((e - b + TILE - 1) / TILE);
   const int lane = threadIdx.x % 32;
   if (threadIdx.x < RT) {
     const int j = lane % L, ch = threadIdx.x / L * CPT;  // first of CPT channels
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, 3) gdp_ssm_fwd_k
     };
     __syncthreads();
     for (int k = 0; k < tiles; ++k) {
-      const int rows = (int)min((int64_t)kSsmTile, e - b - (int64_t)k * kSsmTile), at = (k & 1) * kSsmTile;
+      const int rows = (int)min((int64_t)TILE, e - b - (int64_t)k * TILE), at = (k & 1) * TILE;
       for (int t = 0; t < rows; t += kSsmChunk) {
         if (chunk) {
           save(chunk);
@@ -207,32 +207,32 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, 3) gdp_ssm_fwd_k
   auto stage = [&](int k) {
     SsmStage<T, CH, SP> s;
     s.x = ring + (k % kSsmStages) * stage_bytes;
-    s.B = s.x + kSsmTile * CH * sizeof(T);
-    s.C = s.B + kSsmTile * SP * sizeof(T);
-    s.dt = s.C + kSsmTile * SP * sizeof(T);
-    s.z = s.dt + kSsmTile * CH * dt_size;
+    s.B = s.x + TILE * CH * sizeof(T);
+    s.C = s.B + TILE * SP * sizeof(T);
+    s.dt = s.C + TILE * SP * sizeof(T);
+    s.z = s.dt + TILE * CH * dt_size;
     return s;
   };
-  auto rows_of = [&](int k) { return (int)min((int64_t)kSsmTile, e - b - (int64_t)k * kSsmTile); };
+  auto rows_of = [&](int k) { return (int)min((int64_t)TILE, e - b - (int64_t)k * TILE); };
   auto bring = [&](int k) {
     if (k < tiles) {
-      const int64_t row = b + (int64_t)k * kSsmTile;
+      const int64_t row = b + (int64_t)k * TILE;
       const int rows = rows_of(k);
       const SsmStage<T, CH, SP> s = stage(k);
-      fill<T, CH, HT, kSsmTile>(s.x, p.x, p.x_st, c0, cn, row, rows, p.fast_rows, thread);
-      if (p.dt_f32) fill<float, CH, HT, kSsmTile>(s.dt, p.dt, p.dt_st, c0, cn, row, rows, p.fast_rows, thread);
-      else fill<T, CH, HT, kSsmTile>(s.dt, p.dt, p.dt_st, c0, cn, row, rows, p.fast_rows, thread);
-      if (!LOCAL && p.z) fill<T, CH, HT, kSsmTile>(s.z, p.z, p.z_st, c0, cn, row, rows, p.fast_rows, thread);
-      fill<T, SP, HT, kSsmTile>(s.B, p.B, p.B_st, g * p.B_sg, (int)p.S, row, rows, p.fast_vectors, thread);
-      if (!LOCAL) fill<T, SP, HT, kSsmTile>(s.C, p.Cm, p.C_st, g * p.C_sg, (int)p.S, row, rows, p.fast_vectors, thread);
+      fill<T, CH, HT, TILE>(s.x, p.x, p.x_st, c0, cn, row, rows, p.fast_rows, thread);
+      if (p.dt_f32) fill<float, CH, HT, TILE>(s.dt, p.dt, p.dt_st, c0, cn, row, rows, p.fast_rows, thread);
+      else fill<T, CH, HT, TILE>(s.dt, p.dt, p.dt_st, c0, cn, row, rows, p.fast_rows, thread);
+      if (!LOCAL && p.z) fill<T, CH, HT, TILE>(s.z, p.z, p.z_st, c0, cn, row, rows, p.fast_rows, thread);
+      fill<T, SP, HT, TILE>(s.B, p.B, p.B_st, g * p.B_sg, (int)p.S, row, rows, p.fast_vectors, thread);
+      if (!LOCAL) fill<T, SP, HT, TILE>(s.C, p.Cm, p.C_st, g * p.C_sg, (int)p.S, row, rows, p.fast_vectors, thread);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   // (Rows behind the sequence's last one hold anything; what is formed of them is not used.)
-  constexpr int ITEMS = kSsmTile * CP / HT, STEP = HT / CP, TOGETHER = ITEMS < 4 ? ITEMS : 4;
+  constexpr int ITEMS = TILE * CP / HT, STEP = HT / CP, TOGETHER = ITEMS < 4 ? ITEMS : 4;
   auto form = [&](int k) {
     const SsmStage<T, CH, SP> s = stage(k);
-    const int at = (k & 1) * kSsmTile, t0 = thread / CP;
+    const int at = (k & 1) * TILE, t0 = thread / CP;
 #pragma unroll
     for (int m = 0; m < ITEMS; m += TOGETHER) {
       float2 v[TOGETHER], x[TOGETHER];
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, 3) gdp_ssm_fwd_k
         *reinterpret_cast<float4 *>(steps + (at + t0 + (m + u) * STEP) * CH + c) = make_float4(v[u].x, in.x, v[u].y, in.y);
       }
     }
-    constexpr int QUADS = kSsmTile * SP / kQ / HT;
+    constexpr int QUADS = TILE * SP / kQ / HT;
     static_assert(QUADS > 0 && ITEMS > 0, "every thread has a part");
 #pragma unroll
     for (int q = 0; q < QUADS; ++q) {
@@ -271,8 +271,8 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, 3) gdp_ssm_fwd_k
   };
   auto finish = [&](int k) {
     const SsmStage<T, CH, SP> s = stage(k);
-    const int rows = rows_of(k), at = (k & 1) * kSsmTile, t0 = thread / CP;
-    T *out = static_cast<T *>(p.y) + (b + (int64_t)k * kSsmTile + t0) * p.C + c0 + c;
+    const int rows = rows_of(k), at = (k & 1) * TILE, t0 = thread / CP;
+    T *out = static_cast<T *>(p.y) + (b + (int64_t)k * TILE + t0) * p.C + c0 + c;
 #pragma unroll
     for (int m = 0; m < ITEMS; m += TOGETHER) {
       float2 x[TOGETHER], y[TOGETHER];
@@ -464,10 +464,13 @@ __global__ void __launch_bounds__(kSsmThreads) gdp_ssm_step_kernel(const SsmProb
 
 template <typename T, int L, int CPT, bool FULL, bool LOCAL>
 cudaError_t ssm_fwd(const SsmProblem &p, cudaStream_t stream) {
-  const int bytes = ssm_fwd_bytes<T, L, CPT>(p.dt_f32 ? 4 : (int)sizeof(T), p.z != nullptr);
-  constexpr int most = ssm_fwd_bytes<T, L, CPT>(4, true);
+  // tokens of a tile: a CTA alone on its SM takes 64 where they fit (8192 x 4096: 282 us, 32: 316), the others 32 (64 leave room
+  // for two CTAs only, 8 x 4096 x 4096: 1280 against 818 us)
+  constexpr int TILE = CPT == 1 && ssm_fwd_bytes<T, L, CPT, 64>(4, true) <= 220 * 1024 ? 64 : 32;
+  const int bytes = ssm_fwd_bytes<T, L, CPT, TILE>(p.dt_f32 ? 4 : (int)sizeof(T), p.z != nullptr);
+  constexpr int most = ssm_fwd_bytes<T, L, CPT, TILE>(4, true);
   static_assert(most <= 227 * 1024, "fits an SM");
-  const auto kernel = gdp_ssm_fwd_kernel<T, L, CPT, FULL, LOCAL>;
+  const auto kernel = gdp_ssm_fwd_kernel<T, L, CPT, TILE, FULL, LOCAL>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
   const int64_t rows = p.pieces + (!LOCAL && p.zero_pad ? 1 : 0);

@@ -8,7 +8,6 @@
 namespace gdp {
 namespace layer {
 
-constexpr int kSsmTile = 32;  // tokens of a forward tile
 // Floats between rows of readouts, so that those of several tokens fall on different banks.
 constexpr int ssm_skew(int cpt) { return cpt == 2 ? 8 : 10; }
 constexpr int kSsmStages = 4; // tiles whose rows a CTA holds: finished, run, formed and on their way
