@@ -23,8 +23,9 @@ struct SsmBack {
   __host__ __device__ static constexpr int stage(int dt_size, bool gated) {
     return K * CH * ((int)sizeof(T) * (gated ? 3 : 2) + dt_size) + 2 * K * SP * (int)sizeof(T) + CH * SP * 4;
   }
-  // two chunks of e and e x, dy, B and C; two halves of the running threads' parts; their states before every BLKth token
-  static constexpr int formed = K * CH * 12 + 2 * K * SP * 4, starts = K / BLK * RT * 8 * 4;
+  // two chunks of e and e x, dy, B and C; two halves of the running threads' parts; their states before every BLKth token, their
+  // sums for dA
+  static constexpr int formed = K * CH * 12 + 2 * K * SP * 4, starts = (K / BLK + 1) * RT * 8 * 4;
   __host__ __device__ static constexpr int parts(bool gated) { return HALF * RT * (8 + 2 * (gated ? 3 : 2)) * 4; }
   __host__ __device__ static constexpr int bytes(int dt_size, bool gated) {
     return STAGES * stage(dt_size, gated) + 2 * (formed + parts(gated)) + starts;
@@ -46,7 +47,8 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
   float4 *sums = reinterpret_cast<float4 *>(Cs + 2 * K * SP);
   float2 *parts = reinterpret_cast<float2 *>(sums + 2 * HALF * 2 * RT);
   float4 *starts = reinterpret_cast<float4 *>(parts + 2 * HALF * kinds * RT);  // [K / BLK][2][RT]
-  unsigned char *ring = reinterpret_cast<unsigned char *>(starts + K / BLK * 2 * RT);
+  float4 *totals = starts + K / BLK * 2 * RT;  // [2][RT]
+  unsigned char *ring = reinterpret_cast<unsigned char *>(totals + 2 * RT);
   // (pairs of channels change places by lane, so that half a warp's parts fall on all banks)
   auto part_of = [&](int t, int kind, int j, int pair) {
     return ((t * kinds + kind) * L + j) * CP + (pair ^ (j / (L / 4) * (CP / 4)));
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
     const int64_t mine = (c0 + ch) * p.S + j * kQ;
     const int states = max(0, min(kQ, (int)p.S - j * kQ));
     int n[2];
-    float2 A[2][2], dA[2][2];
+    float2 A[2][2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       n[k] = ch + k < cn ? states : 0;
@@ -98,7 +100,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
       for (int q = 0; q < kQ; ++q) v[q] = q < n[k] ? p.A[mine + k * p.S + q] * kLog2e : -1.f;
       A[k][0] = make_float2(v[0], v[1]);
       A[k][1] = make_float2(v[2], v[3]);
-      dA[k][0] = dA[k][1] = make_float2(0.f, 0.f);
+      totals[k * RT + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     // padded states stay zero, whatever the inputs are
     auto real = [&](float2 v, int q) { return FULL ? v : make_float2(2 * q < states ? v.x : 0.f, 2 * q + 1 < states ? v.y : 0.f); };
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
             }
           }
         } else {
-          float2 h[2][2];
+          float2 h[2][2], dA[2][2] = {};  // (a chunk's part: sums over many tokens run in two steps)
           const float *from = stage(k).h + ch * p.S + j * kQ;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -278,6 +280,12 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
 #pragma unroll 1
               for (; q >= half * (HALF / BLK); --q) block(q, std::false_type{});
             }
+            if (half == 0)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float4 &sum = totals[c * RT + threadIdx.x];
+                sum = make_float4(sum.x + dA[c][0].x, sum.y + dA[c][0].y, sum.z + dA[c][1].x, sum.w + dA[c][1].y);
+              }
             __syncthreads();
           }
         }
@@ -296,7 +304,12 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
         save(p.dinit + at_rows.i * p.C * p.S + mine, back);
       }
     }
-    if (!LOCAL) save(out + mine, dA);
+    if (!LOCAL) {
+      float2 dA[2][2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) pairs(totals[c * RT + threadIdx.x], dA[c]);
+      save(out + mine, dA);
+    }
     return;
   }
   // ---- feeding ----
