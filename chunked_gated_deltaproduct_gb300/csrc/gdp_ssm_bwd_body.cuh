@@ -325,25 +325,34 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
     // step k goes over chunk chunks - 1 - k
     auto first_row = [&](int k) { return at_rows.b + (int64_t)(chunks - 1 - k) * K; };
     auto rows_of = [&](int k) { return k == 0 ? (int)(at_rows.e - at_rows.b) - (chunks - 1) * K : K; };
-    auto bring = [&](int k) {
+    const int64_t last_row = chunks > 0 ? first_row(0) : 0;
+    TileFeed<T, CH, HT, K> x_feed(static_cast<const T *>(p.x) + c0, p.x_st, last_row, cn, p.fast_rows, thread),
+        dy_feed(static_cast<const T *>(p.dy) + c0, p.dy_st, last_row, cn, p.fast_rows, thread),
+        z_feed(static_cast<const T *>(p.z) + (p.z ? c0 : 0), p.z_st, p.z ? last_row : 0, cn, p.fast_rows && p.z, thread),
+        dt_feed(static_cast<const T *>(p.dt) + (p.dt_f32 ? 0 : c0), p.dt_st, p.dt_f32 ? 0 : last_row, cn, p.fast_rows, thread);
+    TileFeed<float, CH, HT, K> dt32_feed(static_cast<const float *>(p.dt) + (p.dt_f32 ? c0 : 0), p.dt_st, p.dt_f32 ? last_row : 0, cn, p.fast_rows, thread);
+    TileFeed<T, SP, HT, K> B_feed(static_cast<const T *>(p.B) + g * p.B_sg, p.B_st, last_row, (int)p.S, p.fast_vectors, thread),
+        C_feed(static_cast<const T *>(p.Cm) + g * p.C_sg, p.C_st, last_row, (int)p.S, p.fast_vectors, thread);
+    const float *entering = p.chunks + (at_rows.chunk + chunks - 1) * p.C * p.S + c0 * p.S;
+    const int kept = cn * (int)p.S;
+    auto bring = [&](int k) {  // chunk by chunk
       if (k < chunks) {
-        const int64_t row = first_row(k);
         const int rows = rows_of(k);
         const Stage s = stage(k);
-        fill<T, CH, HT, K>(s.x, p.x, p.x_st, c0, cn, row, rows, p.fast_rows, thread);
-        fill<T, CH, HT, K>(s.dy, p.dy, p.dy_st, c0, cn, row, rows, p.fast_rows, thread);
-        if (p.dt_f32) fill<float, CH, HT, K>(s.dt, p.dt, p.dt_st, c0, cn, row, rows, p.fast_rows, thread);
-        else fill<T, CH, HT, K>(s.dt, p.dt, p.dt_st, c0, cn, row, rows, p.fast_rows, thread);
-        if (p.z) fill<T, CH, HT, K>(s.z, p.z, p.z_st, c0, cn, row, rows, p.fast_rows, thread);
-        fill<T, SP, HT, K>(s.C, p.Cm, p.C_st, g * p.C_sg, (int)p.S, row, rows, p.fast_vectors, thread);
+        x_feed.bring(s.x, rows, cn, p.fast_rows, thread, -K);
+        dy_feed.bring(s.dy, rows, cn, p.fast_rows, thread, -K);
+        if (p.dt_f32) dt32_feed.bring(s.dt, rows, cn, p.fast_rows, thread, -K);
+        else dt_feed.bring(s.dt, rows, cn, p.fast_rows, thread, -K);
+        if (p.z) z_feed.bring(s.z, rows, cn, p.fast_rows, thread, -K);
+        C_feed.bring(s.C, rows, (int)p.S, p.fast_vectors, thread, -K);
         if (!LOCAL) {
-          fill<T, SP, HT, K>(s.B, p.B, p.B_st, g * p.B_sg, (int)p.S, row, rows, p.fast_vectors, thread);
-          const float *from = p.chunks + (at_rows.chunk + chunks - 1 - k) * p.C * p.S + c0 * p.S;
+          B_feed.bring(s.B, rows, (int)p.S, p.fast_vectors, thread, -K);
           if (p.quad_states) {
-            for (int q = thread * kQ; q < cn * (int)p.S; q += HT * kQ) sm100::cp_async16(s.h + q, from + q, 16u);
+            for (int q = thread * kQ; q < kept; q += HT * kQ) sm100::cp_async16(s.h + q, entering + q, 16u);
           } else {
-            for (int q = thread; q < cn * (int)p.S; q += HT) s.h[q] = from[q];
+            for (int q = thread; q < kept; q += HT) s.h[q] = entering[q];
           }
+          entering -= p.C * p.S;
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -367,7 +376,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
         for (int m = 0; m < ITEMS; ++m) {
           const int t = t0 + m * STEP;
           const float2 z = load_pair<T>(s.z, (K % STEP == 0 || t < K ? t : 0) * CH + c);
-          d[m] = mul2(d[m], mul2(z, make_float2(sigmoid_fast(z.x), sigmoid_fast(z.y))));
+          d[m] = mul2(d[m], mul2(z, sigmoid2(z)));
         }
 #pragma unroll
       for (int m = 0; m < ITEMS; ++m) {
@@ -421,7 +430,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
         float2 dt = fma2(v, both(kLn2), mul2(u, x));
         if (p.softplus) {
           const float2 w = add2(p.dt_f32 ? load_pair<float>(s.dt, o) : load_pair<T>(s.dt, o), make_float2(bias[0], bias[1]));
-          dt = mul2(dt, make_float2(sigmoid_fast(w.x), sigmoid_fast(w.y)));
+          dt = mul2(dt, sigmoid2(w));
         }
         if (p.dt_f32) put(p.ddt, to, dt, float());
         else put(p.ddt, to, dt, T());
@@ -432,8 +441,8 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_ker
           for (int j = 0; j < L; ++j) y = add2(y, parts[part_of(t, 2, j, c / 2)]);
           const float2 z = load_pair<T>(s.z, o), dy = load_pair<T>(s.dy, o);
           y = fma2(D, x, y);
-          const float q0 = sigmoid_fast(z.x), q1 = sigmoid_fast(z.y);
-          put(p.dz, to, mul2(mul2(dy, y), make_float2(q0 * fmaf(z.x, 1.f - q0, 1.f), q1 * fmaf(z.y, 1.f - q1, 1.f))), T());
+          const float2 q = sigmoid2(z);
+          put(p.dz, to, mul2(mul2(dy, y), mul2(q, fma2(z, fma2(q, both(-1.f), both(1.f)), both(1.f)))), T());
         }
       }
       // an item: four states of dB or dC of a token; where there are fewer than threads, two threads share one

@@ -214,17 +214,22 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, CPT == 1 ? 1 : 3
     return s;
   };
   auto rows_of = [&](int k) { return (int)min((int64_t)TILE, e - b - (int64_t)k * TILE); };
-  auto bring = [&](int k) {
+  TileFeed<T, CH, HT, TILE> x_feed(static_cast<const T *>(p.x) + c0, p.x_st, b, cn, p.fast_rows, thread),
+      z_feed(static_cast<const T *>(p.z) + (p.z ? c0 : 0), p.z_st, p.z ? b : 0, cn, p.fast_rows && p.z, thread),
+      dt_feed(static_cast<const T *>(p.dt) + (p.dt_f32 ? 0 : c0), p.dt_st, p.dt_f32 ? 0 : b, cn, p.fast_rows, thread);
+  TileFeed<float, CH, HT, TILE> dt32_feed(static_cast<const float *>(p.dt) + (p.dt_f32 ? c0 : 0), p.dt_st, p.dt_f32 ? b : 0, cn, p.fast_rows, thread);
+  TileFeed<T, SP, HT, TILE> B_feed(static_cast<const T *>(p.B) + g * p.B_sg, p.B_st, b, (int)p.S, p.fast_vectors, thread),
+      C_feed(static_cast<const T *>(p.Cm) + g * p.C_sg, p.C_st, b, (int)p.S, p.fast_vectors, thread);
+  auto bring = [&](int k) {  // tile by tile
     if (k < tiles) {
-      const int64_t row = b + (int64_t)k * TILE;
       const int rows = rows_of(k);
       const SsmStage<T, CH, SP> s = stage(k);
-      fill<T, CH, HT, TILE>(s.x, p.x, p.x_st, c0, cn, row, rows, p.fast_rows, thread);
-      if (p.dt_f32) fill<float, CH, HT, TILE>(s.dt, p.dt, p.dt_st, c0, cn, row, rows, p.fast_rows, thread);
-      else fill<T, CH, HT, TILE>(s.dt, p.dt, p.dt_st, c0, cn, row, rows, p.fast_rows, thread);
-      if (!LOCAL && p.z) fill<T, CH, HT, TILE>(s.z, p.z, p.z_st, c0, cn, row, rows, p.fast_rows, thread);
-      fill<T, SP, HT, TILE>(s.B, p.B, p.B_st, g * p.B_sg, (int)p.S, row, rows, p.fast_vectors, thread);
-      if (!LOCAL) fill<T, SP, HT, TILE>(s.C, p.Cm, p.C_st, g * p.C_sg, (int)p.S, row, rows, p.fast_vectors, thread);
+      x_feed.bring(s.x, rows, cn, p.fast_rows, thread, TILE);
+      if (p.dt_f32) dt32_feed.bring(s.dt, rows, cn, p.fast_rows, thread, TILE);
+      else dt_feed.bring(s.dt, rows, cn, p.fast_rows, thread, TILE);
+      if (!LOCAL && p.z) z_feed.bring(s.z, rows, cn, p.fast_rows, thread, TILE);
+      B_feed.bring(s.B, rows, (int)p.S, p.fast_vectors, thread, TILE);
+      if (!LOCAL) C_feed.bring(s.C, rows, (int)p.S, p.fast_vectors, thread, TILE);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -288,7 +293,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, CPT == 1 ? 1 : 3
 #pragma unroll
         for (int u = 0; u < TOGETHER; ++u) x[u] = load_pair<T>(s.z, (t0 + (m + u) * STEP) * CH + c);
 #pragma unroll
-        for (int u = 0; u < TOGETHER; ++u) y[u] = mul2(y[u], mul2(x[u], make_float2(sigmoid_fast(x[u].x), sigmoid_fast(x[u].y))));
+        for (int u = 0; u < TOGETHER; ++u) y[u] = mul2(y[u], mul2(x[u], sigmoid2(x[u])));
       }
 #pragma unroll
       for (int u = 0; u < TOGETHER; ++u, out += STEP * p.C) {
@@ -464,8 +469,8 @@ __global__ void __launch_bounds__(kSsmThreads) gdp_ssm_step_kernel(const SsmProb
 
 template <typename T, int L, int CPT, bool FULL, bool LOCAL>
 cudaError_t ssm_fwd(const SsmProblem &p, cudaStream_t stream) {
-  // tokens of a tile: a CTA alone on its SM takes 64 where they fit (8192 x 4096: 282 us, 32: 316), the others 32 (64 leave room
-  // for two CTAs only, 8 x 4096 x 4096: 1280 against 818 us)
+  // tokens of a tile: a CTA alone on its SM takes 64 where they fit (8192 x 4096: 282 us, 32: 316), the others 32 (8 x 4096 x
+  // 4096: 776 us; 64 leave room for two CTAs only, 1280; 16 meet twice as often, 923 with three CTAs, 933 with four)
   constexpr int TILE = CPT == 1 && ssm_fwd_bytes<T, L, CPT, 64>(4, true) <= 220 * 1024 ? 64 : 32;
   const int bytes = ssm_fwd_bytes<T, L, CPT, TILE>(p.dt_f32 ? 4 : (int)sizeof(T), p.z != nullptr);
   constexpr int most = ssm_fwd_bytes<T, L, CPT, TILE>(4, true);

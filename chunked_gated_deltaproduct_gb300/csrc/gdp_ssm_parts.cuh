@@ -36,15 +36,19 @@ __device__ __forceinline__ void sum_scatter(float *v, int rank) {
 }
 
 // e^-|v| of two values, to about 2^-22: the exponent's rounding in base 2 (up to |v| 2^-24, which decays of long memory
-// would notice) is put right to first order.
+// would notice) is put right to first order.  (Below e^-128, nothing in fp32, the exponent stands still, so that infinite
+// steps stay numbers; NaN stays NaN.)
+__device__ __forceinline__ float held(float v) {
+  float a;
+  asm("max.NaN.f32 %0, %1, 0fC3000000;" : "=f"(a) : "f"(-fabsf(v)));
+  return a;
+}
 __device__ __forceinline__ float2 exp_neg_abs2(float2 v) {
-  const float2 a = make_float2(-fabsf(v.x), -fabsf(v.y));
-  const float2 t = mul2(a, both(kLog2e));
+  const float2 a = make_float2(held(v.x), held(v.y)), t = mul2(a, both(kLog2e));
   float2 rest = fma2(a, both(kLog2e), make_float2(-t.x, -t.y));  // what t's rounding left out
   rest = fma2(a, both((float)(1.4426950408889634074 - (double)kLog2e)), rest);
   const float2 w = make_float2(ex2(t.x), ex2(t.y));
-  // (w is 0 where t is -inf and rest is no number)
-  return make_float2(t.x < -126.f ? w.x : fmaf(w.x, 0.6931471806f * rest.x, w.x), t.y < -126.f ? w.y : fmaf(w.y, 0.6931471806f * rest.y, w.y));
+  return fma2(w, mul2(rest, both(0.6931471806f)), w);
 }
 // log(1 + e^v) = max(v, 0) + log(1 + w) with w = e^-|v| in (0, 1]; log(1 + w) = 2 artanh(s), s = w / (2 + w) <= 1/3, by
 // its power series: what is left out is below s^17 / 17 < 2^-30, and small w keep their relative precision.
@@ -183,30 +187,38 @@ __device__ __forceinline__ float2 load_pair(const unsigned char *raw, int i) {
   else return widen<T>(*reinterpret_cast<const uint32_t *>(raw + 2 * i));
 }
 
-// Rows [row, row + rows) of a tensor into a stage [tile][PITCH], columns from c0 on; columns from `real` on become zeros.
+// A tensor's tiles of TILE rows by PITCH columns into stages [TILE][PITCH], one after the other (forwards or, with a negative
+// `tile_step`, backwards) by THREADS threads; columns from `real` on become zeros.  Fast: 16-byte asynchronous copies from a
+// pointer that moves on by itself (finding the rows anew for every tile was 19 of 154 instructions a token).
 template <typename T, int PITCH, int THREADS, int TILE>
-__device__ __forceinline__ void fill(unsigned char *to, const void *base, int64_t stride, int64_t c0, int real, int64_t row, int rows, int fast,
-                                     int thread) {
-  const T *from = static_cast<const T *>(base) + row * stride + c0;
-  if (fast) {
-    constexpr int E = 16 / sizeof(T), PER = PITCH / E, EACH = (TILE * PER + THREADS - 1) / THREADS;
-    static_assert(THREADS % PER == 0, "a thread keeps its columns");
-    const int t0 = thread / PER, c = thread % PER * E;
-    const uint32_t bytes = c < real ? 16u : 0u;
-    const T *at = from + t0 * stride + (c < real ? c : 0);
-    unsigned char *put = to + (t0 * PITCH + c) * sizeof(T);
-#pragma unroll
-    for (int k = 0; k < EACH; ++k, at += THREADS / PER * stride, put += THREADS / PER * PITCH * sizeof(T))
-      if (t0 + k * (THREADS / PER) < rows) sm100::cp_async16(put, at, bytes);
-  } else {
-    T *at = reinterpret_cast<T *>(to);
-#pragma unroll 8
-    for (int i = thread; i < rows * PITCH; i += THREADS) {
-      const int t = i / PITCH, c = i % PITCH;
-      at[i] = c < real ? from[t * stride + c] : from_f32<T>(0.f);
-    }
+struct TileFeed {
+  static constexpr int E = 16 / sizeof(T), PER = PITCH / E, EACH = (TILE * PER + THREADS - 1) / THREADS, APART = THREADS / PER;
+  static_assert(THREADS % PER == 0, "a thread keeps its columns");
+  const T *at;     // fast: the thread's first row and columns of the coming tile; else the tile's first row and column
+  int64_t stride;
+  // base: the tensor's first column; row: the first tile's first row
+  __device__ __forceinline__ TileFeed(const T *base, int64_t stride_, int64_t row, int real, int fast, int thread) : at(base + row * stride_), stride(stride_) {
+    if (fast) at += thread / PER * stride + (thread % PER * E < real ? thread % PER * E : 0);
   }
-}
+  __device__ __forceinline__ void bring(unsigned char *to, int rows, int real, int fast, int thread, int tile_step) {
+    if (fast) {
+      const int t0 = thread / PER, c = thread % PER * E;
+      const uint32_t bytes = c < real ? 16u : 0u;
+      unsigned char *put = to + thread * 16;
+#pragma unroll
+      for (int k = 0; k < EACH; ++k)
+        if (t0 + k * APART < rows) sm100::cp_async16(put + k * THREADS * 16, at + k * APART * stride, bytes);
+    } else {
+      T *put = reinterpret_cast<T *>(to);
+#pragma unroll 8
+      for (int i = thread; i < rows * PITCH; i += THREADS) {
+        const int t = i / PITCH, c = i % PITCH;
+        put[i] = c < real ? at[t * stride + c] : from_f32<T>(0.f);
+      }
+    }
+    at += tile_step * stride;
+  }
+};
 
 }  // namespace layer
 }  // namespace gdp
