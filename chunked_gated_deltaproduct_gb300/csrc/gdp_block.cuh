@@ -115,6 +115,12 @@ inline gdp_status rows_ok(const void *p, int64_t stride, int64_t T, int64_t C, i
 }
 // The stride of a single row means nothing and may be anything in a view.
 inline int64_t stride_of(int64_t stride, int64_t T, int64_t C) { return T > 1 ? stride : C; }
+// Whether T >= 1 rows `stride` apart and T contiguous rows share memory (gaps between the first ones' rows counted).
+inline bool spans_overlap(const void *in, int64_t stride, const void *out, int64_t T, int64_t C, int type) {
+  const size_t es = dtype_size(type), in_bytes = ((size_t)(T - 1) * (size_t)stride + (size_t)C) * es, out_bytes = (size_t)T * (size_t)C * es;
+  const uintptr_t a = (uintptr_t)in, b = (uintptr_t)out;
+  return a < b + out_bytes && b < a + in_bytes;
+}
 // Whether its rows can be read `bytes` at a time.
 inline bool rows_by(const void *p, int64_t stride, int64_t T, int type, size_t bytes) {
   return aligned(p, bytes) && (T <= 1 || stride * dtype_size(type) % bytes == 0);

@@ -56,6 +56,8 @@ gdp_status resolve(const gdp_conv_args *a, bool step, ConvProblem *p) {
   if ((st = states_ok(a->initial_state, a->output_state, a->state, a->state_indices, a->num_slots, es,
                       es * (size_t)a->N * (size_t)(a->width - 1) * (size_t)a->C)) != GDP_OK)
     return st;
+  if (a->T > 0 && spans_overlap(a->x, stride_of(a->x_stride_t, a->T, a->C), a->output, a->T, a->C, a->dtype))
+    return fail(GDP_ERR_ALIAS, "output overlaps x");
   *p = ConvProblem{};
   p->x = a->x; p->x_st = stride_of(a->x_stride_t, a->T, a->C);
   p->w = a->weight; p->b = a->bias; p->y = a->output;

@@ -27,11 +27,7 @@ bool short_strides(std::initializer_list<int64_t> strides) {
 }
 // The same rows exactly, or others.
 bool partly(const void *in, int64_t stride, const void *out, int64_t T, int64_t C, int type) {
-  if (!in || T == 0) return false;
-  const size_t es = dtype_size(type), in_bytes = ((size_t)(T - 1) * (size_t)stride + (size_t)C) * es, out_bytes = (size_t)T * (size_t)C * es;
-  const uintptr_t a = (uintptr_t)in, b = (uintptr_t)out;
-  if (a == b && stride == C) return false;
-  return a < b + out_bytes && b < a + in_bytes;
+  return in && T > 0 && !(in == out && stride == C) && spans_overlap(in, stride, out, T, C, type);
 }
 
 }  // namespace

@@ -59,7 +59,7 @@ inline int64_t ssm_workers(int64_t N, int64_t tiles, int sms) {
 }
 
 // Tokens of a piece, 0 for whole sequences, from the shape alone (the lengths are the device's).  A sequence alone
-// takes 39 ns a token; pieces add a pass of 0.6 of the first one's time and about 13 us, and use the SMs that whole
+// takes 34 ns a token; pieces add a pass of 0.6 of the first one's time and about 13 us, and use the SMs that whole
 // sequences leave idle.  Measured on the device, whole sequences against pieces (bf16, S = 16): 1 x 65536 x 1024 2533 to
 // 697 us, 1 x 4096 x 512 161 to 43, 1 x 1000 x 1024 43 to 27, 2 x 4096 x 1024 162 to 120; equal sequences of half the SMs'
 // CTAs or more lose (4 x 4096 x 1024 162 to 186), ragged ones win (100, 257, 64 and 1000 tokens x 1024: 43 to 27).

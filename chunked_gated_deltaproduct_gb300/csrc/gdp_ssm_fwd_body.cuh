@@ -9,9 +9,15 @@ namespace layer {
 
 // ---- forward: half of the CTA's warps run states, the other half feed them ----
 //
-// Per tile of 32 tokens the feeding warps bring the rows ahead (16-byte asynchronous copies into a ring of shared-memory
+// Per tile of 32 or 64 tokens the feeding warps bring the rows ahead (16-byte asynchronous copies into a ring of shared-memory
 // stages), form e and e x of the next tile, and finish the outputs of the last one, while the running warps take their
-// states over the present one: two channels by four states a lane, so that B and C are loaded once for both.
+// states over the present one: two channels by four states a lane, so that B and C are loaded once for both (or one channel,
+// in twice the warps).
+//
+// Bound by the running warps' latency and issue slots: 41 instructions a warp and token for 32 x 8 states, 16 of them
+// exponentials at 8 lanes a clock.  65536 x 4096 x 16 gated, bf16: 2199 us, 34 ns a token of 128 CTAs alone on their SMs (its
+// exponentials alone would take 452 us, its bytes 317); 64 packed requests, 84086 x 2048 x 16: 958 us at three CTAs per SM; 8 x
+// 4096 x 2048 x 16 with the chunk states: 513 us.
 
 // The raw rows of a tile in shared memory.
 template <typename T, int CH, int SP>
@@ -82,7 +88,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, CPT == 1 ? 1 : 3
       h[k][0] = make_float2(v[0], v[1]);
       h[k][1] = make_float2(v[2], v[3]);
 #pragma unroll
-      for (int q = 0; q < kQ; ++q) v[q] = q < n[k] ? p.A[mine + k * p.S + q] * kLog2e : 0.f;
+      for (int q = 0; q < kQ; ++q) v[q] = q < n[k] ? p.A[mine + k * p.S + q] * kLog2e : -1.f;  // (none: they decay)
       A[k][0] = make_float2(v[0], v[1]);
       A[k][1] = make_float2(v[2], v[3]);
     }
@@ -493,8 +499,8 @@ cudaError_t ssm_fwd_by(const SsmProblem &p, cudaStream_t stream) {
       return e;
   }
   // A CTA alone on its SM is bound by its warps' own latencies, and twice the warps with half the channels take 16 % off
-  // (8192 x 4096: 321 against 384 us); where several share an SM the work counts, and loading B and C once for two
-  // channels does (8 x 4096 x 4096: 809 against 836 us).
+  // (8192 x 4096, both with 32 tokens a tile: 321 against 384 us; with 64 tokens 282); where several share an SM the work
+  // counts, and loading B and C once for two channels does (8 x 4096 x 4096: 809 against 836 us).
   if (FULL && !p.piece && p.pieces * p.G * (int64_t)p.tiles <= p.sms) return ssm_fwd<T, L, FULL ? 1 : 2, FULL, false>(p, stream);
   return ssm_fwd<T, L, 2, FULL, false>(p, stream);
 }

@@ -13,8 +13,8 @@
  * work enqueued on `stream` in order (graph-capturable), a host-side argument error returns a non-zero
  * gdp_status before any launch with the reason in gdp_last_error(), and GDP_DEV_ERR_* bits are OR-ed into
  * *device_status for what only the device can see.  Strides are in elements; the innermost dimension is
- * contiguous.  Any alignment of the elements' own size is served; 16-byte aligned bases and strides take the
- * fast paths.  Outputs must not overlap inputs unless said.  Results do not depend on scheduling: every value
+ * contiguous.  T is below 2^31.  Any alignment of the elements' own size is served; 16-byte aligned bases and strides
+ * take the fast paths.  Outputs must not overlap inputs unless said.  Results do not depend on scheduling: every value
  * is formed by the same operations in the same order.
  *
  * Packed sequences and state modes are those of gdp_linear_recurrence: cu_seqlens that do not ascend from 0 to
@@ -110,7 +110,8 @@ size_t gdp_conv_workspace_bytes(int64_t T, int64_t C, int64_t width); /* 0 for a
  *     h_t[c][s] = exp(e_t A[c][s]) h_{t-1}[c][s] + e_t x_t[c] B_t[s],
  *     y_t[c]    = sum_s C_t[s] h_t[c][s] + D[c] x_t[c],   times z_t sigmoid(z_t) when z is given.
  *
- * B and C are shared by the C / G consecutive channels of a group.  States are fp32 [C, S] per sequence or
+ * B and C are shared by the C / G consecutive channels of a group (C S up to 33 million, or fewer for groups of few
+ * channels, and N times that below 2^40: GDP_ERR_UNSUPPORTED beyond).  States are fp32 [C, S] per sequence or
  * slot, contiguous.  Sums and states are fp32; y is rounded once.
  *
  * chunk_states (optional, what the backward pass reads): the state entering every chunk of GDP_SCAN_CHUNK tokens
@@ -210,7 +211,7 @@ gdp_status gdp_selective_scan_backward(const gdp_scan_backward_args *args, void 
 size_t gdp_scan_workspace_bytes(int64_t T, int64_t N, int64_t C, int64_t S, int64_t G);
 
 /*
- * gdp_residual_norm: for every token, over its C channels (C up to 8192),
+ * gdp_residual_norm: for every token, over its C channels (C up to 8192, row strides below 2^31),
  *
  *     m = block / sqrt(mean(block^2) + eps) post_weight   (m = block without post_weight),
  *     r = residual + scale act(gate) m,   y = r / sqrt(mean(r^2) + eps) weight.

@@ -207,3 +207,26 @@ def test_wrappers_refuse(lib, monkeypatch):
 def test_activations(table, name):
     with pytest.raises(pkg.GdpError, match="activation must be one of"):
         block._activation(table, name)
+
+
+def test_refusals_of_range(lib):
+    """What is documented as out of range or as overlapping is refused before any launch."""
+    far = 1 << 31
+    for name in ("residual", "block", "gate"):
+        a = _norm(gate=FAKE, gate_stride_t=16)
+        _refused(lib, "gdp_residual_norm", _with(a, {name + "_stride_t": far}), UNSUPPORTED)
+    for name in ("d_y", "d_residual_out", "residual_out", "block", "gate"):
+        a = _norm_back(gate=FAKE, gate_stride_t=16, d_gate=FAKE, d_residual_out=1 << 26, d_residual_out_stride_t=16)
+        _refused(lib, "gdp_residual_norm_backward", _with(a, {name + "_stride_t": far}), UNSUPPORTED)
+    for at in (FAKE, FAKE + 2, FAKE + 16 * 8 * 2 - 2, FAKE - 16 * 8 * 2 + 2):
+        _refused(lib, "gdp_short_convolution", _conv(output=at), ALIAS)
+        _refused(lib, "gdp_short_convolution_decode", _conv(output=at, N=8), ALIAS)
+
+
+def test_scan_in_pieces_needs_its_workspace(lib):
+    need = pkg.gdp_scan_forward_workspace_bytes(4096, 1, 64, 16)
+    assert need > 0 and pkg.gdp_scan_forward_workspace_bytes(4096, 1, 64, 16, 3) == 0
+    assert pkg.gdp_scan_forward_workspace_bytes(100, 1, 64, 16) == 0  # (too short for pieces)
+    one = dict(T=4096, N=1, C=64, S=16, x_stride_t=64, dt_stride_t=64, B_stride_t=16, C_stride_t=16, output=1 << 24)
+    for over in (dict(workspace=None), dict(workspace=FAKE + 16, workspace_bytes=need), dict(workspace=FAKE, workspace_bytes=need - 1)):
+        _refused(lib, "gdp_selective_scan", _scan(**one, **over), WORKSPACE)

@@ -436,3 +436,39 @@ def test_a_block_trained_and_served(cuda_device):
     for t in range(new):
         at = torch.tensor([starts[i] + lengths[i] - new + t for i in live], device=dev)
         assert float((rows(at, True) - y[at]).abs().max()) < 1e-3
+
+
+@pytest.mark.parametrize("S", [3, 16, 20, 64])
+@pytest.mark.parametrize("lengths", [[40, 9], [300, 400]])
+def test_an_infinite_step(cuda_device, lengths, S):
+    """A step of +inf forgets what was and takes in what the formula gives, +inf for positive x, B and C, whatever number of
+    states the lanes are padded to; the channel's other sequences and the other channels are as without it."""
+    dev, T, C, at, ch = cuda_device, sum(lengths), 24, 5, 3
+    x, B, Cm = (1 + _rand(shape, i, F32, 1.0).abs().to(dev) for i, shape in enumerate(((T, C), (T, S), (T, S))))
+    dt, A = _rand((T, C), 3, F32, 0.5).to(dev), -torch.exp(_rand((C, S), 4, F32, 0.5)).to(dev)
+    cu = _cu(lengths, dev)
+    clean, fin = pkg.selective_scan(x, dt, A, B, Cm, cu, output_final_state=True)
+    dt[at, ch] = math.inf
+    y, state = pkg.selective_scan(x, dt, A, B, Cm, cu, output_final_state=True)
+    assert bool((y[at:lengths[0], ch] == math.inf).all()) and bool((state[0, ch] == math.inf).all())
+    y[at:lengths[0], ch], state[0, ch] = clean[at:lengths[0], ch], fin[0, ch]
+    assert torch.equal(y, clean) and torch.equal(state, fin)
+    step, after = pkg.selective_scan_decode(x[at:at + 1], dt[at:at + 1], A, B[at:at + 1], Cm[at:at + 1], output_final_state=True)
+    assert bool((step[0, ch] == math.inf).all()) and bool((after[0, ch] == math.inf).all())
+    assert bool(torch.isfinite(step[0, :ch]).all()) and bool(torch.isfinite(after[0, ch + 1:]).all())
+
+
+def test_bounds_of_no_rows(cuda_device):
+    """Bounds are checked where there are no rows too, and the states pass through."""
+    dev = cuda_device
+    b = Block(0, 24, 16, 2, dev)
+    for bounds, bad in (([0, 0, 0], False), ([0, 3, 3], True)):
+        cu = torch.tensor(bounds, dtype=torch.int32, device=dev)
+        for call, state in ((b.conv, b.c0), (b.scan, b.h0)):
+            for how in ({}, {"initial_state": state, "output_final_state": True},
+                        {"state": state.clone(), "state_indices": torch.tensor([1, 0], dtype=torch.int32, device=dev)}):
+                status = torch.zeros(1, dtype=torch.int32, device=dev)
+                got = call(cu, device_status=status, **how)
+                assert bool(int(status) & pkg.GDP_DEV_ERR_CU_SEQLENS) == bad
+                assert "initial_state" not in how or torch.equal(got[1], state)
+                assert "state" not in how or torch.equal(how["state"], state)
