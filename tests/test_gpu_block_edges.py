@@ -472,3 +472,29 @@ def test_bounds_of_no_rows(cuda_device):
                 assert bool(int(status) & pkg.GDP_DEV_ERR_CU_SEQLENS) == bad
                 assert "initial_state" not in how or torch.equal(got[1], state)
                 assert "state" not in how or torch.equal(how["state"], state)
+
+
+@pytest.mark.parametrize("dtype,stream", [(BF16, F32), (BF16, BF16), (F32, F32)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_residual_norm_of_many_rows_at_every_width(cuda_device, dtype, stream, gated):
+    """Every width of CTA and number of rows that it has places for, with rows enough for the widest grids: the first and last
+    rows against the reference."""
+    dev, T, most = cuda_device, 10000, 8192
+    wide = [_rand((T * 2048,), i, F32, 1.0).to(dev).to(t) for i, t in enumerate((dtype, stream, dtype, dtype, stream))]
+    for C in [8, 200, 256] + list(range(264, most, 248)) + [512, 1024, 2048, 4096, 5120, most]:
+        rows = min(T, T * 2048 // C)
+        x, r, g, dy, dr = (v[:rows * C].view(rows, C) for v in wide)
+        w, post, scale = (_rand((C,), 7 + i, F32, 0.2).add(1.0).to(dev) for i in range(3))
+        g = g if gated else None
+        y, out = pkg.residual_norm(r, x, w, post, g, "silu", scale)
+        d = pkg.residual_norm_backward(dy, dr, out, x, w, post, g, "silu", scale)
+        at = torch.tensor([0, 1, rows // 2, rows - 2, rows - 1], device=dev)
+        few = lambda t: None if t is None else t[at].cpu()  # noqa: E731
+        cols = [t.cpu() for t in (w, post)], scale.cpu()
+        want = R.residual_norm(few(r), few(x), *cols[0], few(g), "silu", cols[1])
+        check(few(y), *want["y"], f"y {C}")
+        check(few(out), *want["r"], f"r {C}")
+        want = R.residual_norm_backward(few(dy), few(dr), few(out), few(x), *cols[0], few(g), "silu", cols[1])
+        for name in ("d_residual", "d_block") + (("d_gate",) if gated else ()):
+            check(few(d[name]), *want[name], f"{name} {C}")
+        assert all(bool(torch.isfinite(d[k]).all()) for k in ("dweight", "dpost_weight", "dscale"))
