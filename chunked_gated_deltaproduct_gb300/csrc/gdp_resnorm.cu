@@ -69,7 +69,7 @@ GDP_EXPORT gdp_status gdp_residual_norm(const gdp_residual_norm_args *a, void *s
 GDP_EXPORT size_t gdp_residual_norm_workspace_bytes(int64_t T, int64_t C) {
   using namespace gdp::layer;
   if (T < 0 || C < 1 || C > kResMost || T > INT32_MAX) return 0;
-  return ((size_t)res_ctas(T, C, sm_count()) * 3 * (size_t)C * 4 + 255) / 256 * 256;
+  return ((size_t)res_parts(T, C, sm_count()) * 3 * (size_t)C * 4 + 255) / 256 * 256;
 }
 
 GDP_EXPORT gdp_status gdp_residual_norm_backward(const gdp_residual_norm_backward_args *a, void *stream) {
@@ -109,14 +109,14 @@ GDP_EXPORT gdp_status gdp_residual_norm_backward(const gdp_residual_norm_backwar
   const int vec = p.C % kRes == 0 && rows_by(p.res, p.res_st, p.T, a->residual_dtype, 16) && rows_by(p.block, p.block_st, p.T, a->dtype, 16) &&
                   rows_by(p.dy, p.dy_st, p.T, a->dtype, 16) && (!p.gate || (rows_by(p.gate, p.gate_st, p.T, a->dtype, 16) && aligned(p.dgate, 16))) &&
                   (!p.dr || rows_by(p.dr, p.dr_st, p.T, a->residual_dtype, 16)) && aligned(p.dres, 16) && aligned(p.dblock, 16);
-  const int64_t ctas = res_ctas(p.T, p.C, sm_count());
+  const int64_t parts = res_parts(p.T, p.C, sm_count());
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = a->dtype == GDP_DTYPE_BF16  ? launch_res_bwd<__nv_bfloat16>(p, vec, ctas, s)
-                  : a->dtype == GDP_DTYPE_F16 ? launch_res_bwd<__half>(p, vec, ctas, s)
-                                              : launch_res_bwd<float>(p, vec, ctas, s);
+  cudaError_t e = a->dtype == GDP_DTYPE_BF16  ? launch_res_bwd<__nv_bfloat16>(p, vec, parts, s)
+                  : a->dtype == GDP_DTYPE_F16 ? launch_res_bwd<__half>(p, vec, parts, s)
+                                              : launch_res_bwd<float>(p, vec, parts, s);
   if (e == cudaSuccess) {
     ColumnSums c{};
-    c.from = p.partial; c.parts = ctas; c.cols = 3 * p.C;
+    c.from = p.partial; c.parts = parts; c.cols = 3 * p.C;
     c.to[0] = a->d_weight; c.to[1] = a->d_post_weight; c.to[2] = a->d_scale;
     c.first[1] = p.C; c.first[2] = 2 * p.C; c.first[3] = c.cols;
     e = launch_column_sums(c, s);

@@ -1,7 +1,8 @@
 // gdp_resnorm_body.cuh -- the residual norm's kernels, instantiated by type in gdp_resnorm_*.cu.
 //
-// A row belongs to a warp (up to 256 channels) or to a CTA; a thread holds eight of its channels in registers, so that
-// every tensor is read once and the norms cost one sum over the row each (backward: three for the two).  Rows come ahead by
+// A row belongs to a warp (up to 256 channels) or to a CTA (backward beyond 4096: to a pair of them); a thread holds eight
+// of its channels in registers, so that every tensor is read once and the norms cost one sum over the row each (backward:
+// three for the two).  Rows come ahead by
 // asynchronous copies into places of shared memory that are the thread's own.  Bound by memory at last (57 bytes a channel
 // and pass of a training step with an fp32 stream), but first by instructions and the sums' latency: hence paired
 // arithmetic, weights that stay in registers (forward) or shared memory (backward) instead of an L1 that the places leave
@@ -69,8 +70,8 @@ __device__ __forceinline__ float dot(const Eight &a, const Eight &b) {
 // The thread's part of row t: one wide multiply, instead of pointers that would take registers (rows and strides are held
 // below 2^31 by the host).
 template <typename T, bool VEC>
-__device__ __forceinline__ const T *row_at(const void *base, uint32_t t, int64_t stride) {
-  return static_cast<const T *>(base) + (int64_t)(int)t * (int)stride + (VEC ? threadIdx.x * kRes : 0);
+__device__ __forceinline__ const T *row_at(const void *base, uint32_t t, int64_t stride, int thread = threadIdx.x) {
+  return static_cast<const T *>(base) + (int64_t)(int)t * (int)stride + (VEC ? thread * kRes : 0);
 }
 template <typename T>
 __device__ __forceinline__ T *out_at(void *base, uint32_t t, int C) { return static_cast<T *>(base) + (int64_t)(int)t * C; }
@@ -164,20 +165,32 @@ struct RowPlaces {
 };
 
 // ---- sums over a row ----
-// Over its threads (ONE: one warp), the same bits in all of them.  Two buffers in turn, so that one barrier per sum
-// suffices; a buffer's places that no warp has stay zero.
-template <int WARPS>
+// Over its threads (WARPS 1: one warp), the same bits in all of them.  Two buffers in turn, so that one barrier per sum
+// suffices; a buffer's places that no warp has stay zero.  A pair of CTAs (CL 2) writes its warps' sums into both buffers.
+constexpr int kMostSums = 5;
+template <int WARPS, int CL = 1>
 struct RowSums {
   static constexpr int PLACES = WARPS < 4 ? 4 : WARPS;
-  float (*buffer)[3][PLACES];
+  float (*buffer)[kMostSums][PLACES];
   int turn;
-  __device__ __forceinline__ explicit RowSums(float (*b)[3][PLACES]) : buffer(b), turn(0) {
+  uint32_t peer;  // CL 2: the other CTA's buffer, and the row's warps before this CTA's
+  int before;
+  __device__ __forceinline__ explicit RowSums(float (*b)[kMostSums][PLACES], int rank = 0) : buffer(b), turn(0), peer(0), before(rank * (WARPS / CL)) {
     if constexpr (WARPS > 1) {
-      for (int i = threadIdx.x; i < 6 * PLACES; i += blockDim.x) (&buffer[0][0][0])[i] = 0.f;
+      for (int i = threadIdx.x; i < 2 * kMostSums * PLACES; i += blockDim.x) (&buffer[0][0][0])[i] = 0.f;
+      if constexpr (CL > 1) asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(sm100::smem_u32(buffer)), "r"(rank ^ 1));
+      meet();
+    }
+  }
+  __device__ __forceinline__ void meet() const {
+    if constexpr (CL > 1) {
+      __syncwarp();
+      asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
       __syncthreads();
     }
   }
-  // N sums, up to three.  Across warps: four warps' sums a lane, then over the lanes that hold the others.
+  // N sums, up to kMostSums.  Across warps: four warps' sums a lane, then over the lanes that hold the others.
   template <int N>
   __device__ __forceinline__ void over(float (&v)[N]) {
 #pragma unroll
@@ -187,8 +200,16 @@ struct RowSums {
     if constexpr (WARPS > 1) {
       if (threadIdx.x % 32 == 0)
 #pragma unroll
-        for (int i = 0; i < N; ++i) buffer[turn][i][threadIdx.x / 32] = v[i];
-      __syncthreads();
+        for (int i = 0; i < N; ++i) {
+          if constexpr (CL > 1) {
+            buffer[turn][i][before + threadIdx.x / 32] = v[i];
+            const uint32_t to = peer + ((turn * kMostSums + i) * PLACES + before + threadIdx.x / 32) * 4;
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v[i]) : "memory");
+          } else {
+            buffer[turn][i][threadIdx.x / 32] = v[i];
+          }
+        }
+      meet();
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float4 q = *reinterpret_cast<const float4 *>(&buffer[turn][i][threadIdx.x % (WARPS / 4) * 4]);
@@ -229,7 +250,7 @@ __device__ __forceinline__ Eight gate_slope(const Eight &g, int act, Eight *fact
 template <typename T, typename TR, bool VEC, int MOST, int RW>
 __global__ void __launch_bounds__(MOST) gdp_res_fwd_kernel(const ResProblem p) {
   constexpr int WARPS = MOST > 128 ? MOST / 32 : 1, B = kRes * (int)sizeof(T), R = kRes * (int)sizeof(TR);
-  __shared__ __align__(16) float buffer[2][3][RowSums<WARPS>::PLACES];
+  __shared__ __align__(16) float buffer[2][kMostSums][RowSums<WARPS>::PLACES];
   extern __shared__ __align__(16) unsigned char smem[];
   RowSums<WARPS> sums(buffer);
   const int thread = threadIdx.x, threads = blockDim.x, C = (int)p.C;
@@ -257,14 +278,33 @@ __global__ void __launch_bounds__(MOST) gdp_res_fwd_kernel(const ResProblem p) {
     scale = load_columns<VEC>(p.scale, thread, threads, C, 0.f, p.quad_cols);
     w = load_columns<VEC>(p.w, thread, threads, C, 0.f, p.quad_cols);
   }
+  // MERGED: the block's sums are added up together with the stream's of the row before, so that a row has one barrier (CTAs of
+  // more than 512 threads: 32768 x 8192 1044 to 812 us; where two rows share the barriers it costs: 65536 x 4096 733 to 754).
+  constexpr bool MERGED = VEC && MOST > 512;
+  auto squares = [&](uint32_t t, int at, float *s) {
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      Eight m = eight_of(0.f);
+      if (mine && t + i * step < T_) m = places.get<T>(at, i * pieces);
+      s[i] = dot(m, m);
+    }
+  };
+  float norm[RW];  // the block's sums
+  const bool merged = MERGED && p.post && p.depth > 1;
   int place = 0;
-  for (uint32_t t = first; t < T_; t += RW * step, place = place + 1 == p.depth ? 0 : place + 1) {
+  if (merged) {
+    places.wait();
+    squares(first, 0, norm);
+    sums.over(norm);
+  }
+  for (uint32_t t = first; t < T_; t += RW * step) {
     Eight m[RW], r[RW], g[RW];
+    const int after = place + 1 == p.depth ? 0 : place + 1;
 #pragma unroll
     for (int i = 0; i < RW; ++i) m[i] = r[i] = g[i] = eight_of(0.f);
     if constexpr (VEC) {
       if (p.depth == 1) ask(t, 0);
-      places.wait();
+      if (!merged) places.wait();
       if (p.depth > 1) ask(t + (p.depth - 1) * RW * step, place == 0 ? p.depth - 1 : place - 1);
 #pragma unroll
       for (int i = 0; i < RW; ++i)
@@ -278,14 +318,16 @@ __global__ void __launch_bounds__(MOST) gdp_res_fwd_kernel(const ResProblem p) {
       r[0] = load_row<TR, VEC>(row_at<TR, VEC>(p.res, t, p.res_st), thread, threads, C);
       if (p.gate) g[0] = load_row<T, VEC>(row_at<T, VEC>(p.gate, t, p.gate_st), thread, threads, C);
     }
-    float s[RW];
+    float s[2 * RW];
     if (p.post) {
       if (!KEEP) post = load_columns<VEC>(p.post, thread, threads, C, 0.f, p.quad_cols);
+      if (!merged) {
 #pragma unroll
-      for (int i = 0; i < RW; ++i) s[i] = dot(m[i], m[i]);
-      sums.over(s);
+        for (int i = 0; i < RW; ++i) norm[i] = dot(m[i], m[i]);
+        sums.over(norm);
+      }
 #pragma unroll
-      for (int i = 0; i < RW; ++i) m[i] = m[i] * post * rsqrtf(fmaf(s[i], p.inv_c, p.eps));
+      for (int i = 0; i < RW; ++i) m[i] = m[i] * post * rsqrtf(fmaf(norm[i], p.inv_c, p.eps));
     }
     if (p.gate)
 #pragma unroll
@@ -302,21 +344,36 @@ __global__ void __launch_bounds__(MOST) gdp_res_fwd_kernel(const ResProblem p) {
       if (t + i * step < T_) store_row<TR, VEC>(out_at<TR>(p.r, t + i * step, C), thread, threads, C, r[i]);
     }
     if (!KEEP) w = load_columns<VEC>(p.w, thread, threads, C, 0.f, p.quad_cols);
-    sums.over(s);
+    if (merged) {
+      places.wait();
+      squares(t + RW * step, after, s + RW);
+      sums.over(s);
+#pragma unroll
+      for (int i = 0; i < RW; ++i) norm[i] = s[RW + i];
+    } else {
+      float only[RW];
+#pragma unroll
+      for (int i = 0; i < RW; ++i) only[i] = s[i];
+      sums.over(only);
+#pragma unroll
+      for (int i = 0; i < RW; ++i) s[i] = only[i];
+    }
 #pragma unroll
     for (int i = 0; i < RW; ++i)
       if (t + i * step < T_)
         store_row<T, VEC>(out_at<T>(p.y, t + i * step, C), thread, threads, C, r[i] * w * rsqrtf(fmaf(s[i], p.inv_c, p.eps)));
+    place = after;
   }
 }
 
-template <typename T, typename TR, bool VEC, int MOST>
-__global__ void __launch_bounds__(MOST) gdp_res_bwd_kernel(const ResProblem p) {
-  constexpr int WARPS = MOST > 128 ? MOST / 32 : 1, B = kRes * (int)sizeof(T), R = kRes * (int)sizeof(TR), PB = B / 16, PR = R / 16;
-  __shared__ __align__(16) float buffer[2][3][RowSums<WARPS>::PLACES];
+template <typename T, typename TR, bool VEC, int MOST, int CL>
+__global__ void __launch_bounds__(MOST, MOST == 128 ? kResResident / MOST : 1) gdp_res_bwd_kernel(const ResProblem p) {
+  constexpr int WARPS = MOST > 128 ? CL * MOST / 32 : 1, B = kRes * (int)sizeof(T), R = kRes * (int)sizeof(TR), PB = B / 16, PR = R / 16;
+  __shared__ __align__(16) float buffer[2][kMostSums][RowSums<WARPS, CL>::PLACES];
   extern __shared__ __align__(16) unsigned char smem[];
-  RowSums<WARPS> sums(buffer);
-  const int thread = threadIdx.x, threads = blockDim.x, C = (int)p.C;
+  const int rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;  // (clusters are consecutive CTAs)
+  RowSums<WARPS, CL> sums(buffer, rank);
+  const int thread = rank * blockDim.x + threadIdx.x, threads = CL * blockDim.x, C = (int)p.C;
   const bool mine = thread * kRes < C;
   // pieces: dy, block, r, gate, dr
   const int dr_at = PB * (p.gate ? 3 : 2) + PR;
@@ -339,26 +396,45 @@ __global__ void __launch_bounds__(MOST) gdp_res_bwd_kernel(const ResProblem p) {
     return p.keep ? column(k) : load_columns<VEC>(from, thread, threads, C, other, p.quad_cols);
   };
   // (unsigned: the row behind the last ones may be past 2^31)
-  const uint32_t first = blockIdx.x * blockDim.y + threadIdx.y, step = gridDim.x * blockDim.y, T_ = (uint32_t)p.T;
+  const uint32_t first = blockIdx.x / CL * blockDim.y + threadIdx.y, step = gridDim.x / CL * blockDim.y, T_ = (uint32_t)p.T;
   auto ask = [&](uint32_t t, int place) {
     if (mine && t < T_) {
-      places.ask<B>(place, 0, row_at<T, VEC>(p.dy, t, p.dy_st));
-      places.ask<B>(place, PB, row_at<T, VEC>(p.block, t, p.block_st));
-      places.ask<R>(place, 2 * PB, row_at<TR, VEC>(p.res, t, p.res_st));
-      if (p.gate) places.ask<B>(place, 2 * PB + PR, row_at<T, VEC>(p.gate, t, p.gate_st));
-      if (p.dr) places.ask<R>(place, dr_at, row_at<TR, VEC>(p.dr, t, p.dr_st));
+      places.ask<B>(place, 0, row_at<T, VEC>(p.dy, t, p.dy_st, thread));
+      places.ask<B>(place, PB, row_at<T, VEC>(p.block, t, p.block_st, thread));
+      places.ask<R>(place, 2 * PB, row_at<TR, VEC>(p.res, t, p.res_st, thread));
+      if (p.gate) places.ask<B>(place, 2 * PB + PR, row_at<T, VEC>(p.gate, t, p.gate_st, thread));
+      if (p.dr) places.ask<R>(place, dr_at, row_at<TR, VEC>(p.dr, t, p.dr_st, thread));
     }
     places.close();
   };
   if (VEC)
     for (int k = 0; k + 1 < p.depth; ++k) ask(first + k * step, k);
+  // MERGED: the norms' sums of a row are added up together with the means of the row before, so that a row has one barrier
+  // (pairs of CTAs, whose barriers cost more: 32768 x 8192 2062 to 1554 us; one CTA, 65536 x 4096: 1327 to 1351).
+  constexpr bool MERGED = VEC && CL > 1;
+  auto squares = [&](int at, float *s) {
+    Eight n = eight_of(0.f), m = n;
+    if (mine) {
+      m = places.get<T>(at, PB);
+      n = places.get<TR>(at, 2 * PB);
+    }
+    s[0] = dot(n, n);
+    s[1] = dot(m, m);
+  };
   int place = 0;
+  float s[2] = {0.f, 0.f};
+  if (MERGED && p.depth > 1) {
+    places.wait();
+    if (first < T_) squares(0, s);
+    sums.over(s);
+  }
   Eight dw = eight_of(0.f), dpost = dw, dscale = dw;
-  for (uint32_t t = first; t < T_; t += step, place = place + 1 == p.depth ? 0 : place + 1) {
+  for (uint32_t t = first; t < T_; t += step) {
     Eight n = eight_of(0.f), m = n, d = n, g = n, up = n;
+    const int after = place + 1 == p.depth ? 0 : place + 1;
     if constexpr (VEC) {
       if (p.depth == 1) ask(t, 0);
-      places.wait();
+      if (!MERGED || p.depth == 1) places.wait();
       if (p.depth > 1) ask(t + (p.depth - 1) * step, place == 0 ? p.depth - 1 : place - 1);
       if (mine) {
         d = places.get<T>(place, 0);
@@ -366,22 +442,25 @@ __global__ void __launch_bounds__(MOST) gdp_res_bwd_kernel(const ResProblem p) {
         n = places.get<TR>(place, 2 * PB);
       }
     } else {
-      d = load_row<T, VEC>(row_at<T, VEC>(p.dy, t, p.dy_st), thread, threads, C);
-      m = load_row<T, VEC>(row_at<T, VEC>(p.block, t, p.block_st), thread, threads, C);
-      n = load_row<TR, VEC>(row_at<TR, VEC>(p.res, t, p.res_st), thread, threads, C);
-      if (p.gate) g = load_row<T, VEC>(row_at<T, VEC>(p.gate, t, p.gate_st), thread, threads, C);
-      if (p.dr) up = load_row<TR, VEC>(row_at<TR, VEC>(p.dr, t, p.dr_st), thread, threads, C);
+      d = load_row<T, VEC>(row_at<T, VEC>(p.dy, t, p.dy_st, thread), thread, threads, C);
+      m = load_row<T, VEC>(row_at<T, VEC>(p.block, t, p.block_st, thread), thread, threads, C);
+      n = load_row<TR, VEC>(row_at<TR, VEC>(p.res, t, p.res_st, thread), thread, threads, C);
+      if (p.gate) g = load_row<T, VEC>(row_at<T, VEC>(p.gate, t, p.gate_st, thread), thread, threads, C);
+      if (p.dr) up = load_row<TR, VEC>(row_at<TR, VEC>(p.dr, t, p.dr_st, thread), thread, threads, C);
     }
     // The second norm: n its normed values.  The stream's gradient is  d_r = r (d w - n mean(d w n)) + up, and what goes on
     // to the first norm's values m is d_r k with k = scale act(gate) post.  Its own mean(d_r k m) is linear in the other
     // mean, so that one pass over the row gives both:  mean((r d w + up) k m) - r mean(d w n) mean(n k m).
     const Eight w = weights(0, p.w, 0.f);
-    float s[2] = {dot(n, n), dot(m, m)};
+    if (!MERGED || p.depth == 1) {
+      s[0] = dot(n, n);
+      s[1] = dot(m, m);
+    }
     if (VEC && mine) {
       if (p.gate) g = places.get<T>(place, 2 * PB + PR);
       if (p.dr) up = places.get<TR>(place, dr_at);
     }
-    sums.over(s);
+    if (!MERGED || p.depth == 1) sums.over(s);
     const float r = rsqrtf(fmaf(s[0], p.inv_c, p.eps)), q = p.post ? rsqrtf(fmaf(s[1], p.inv_c, p.eps)) : 1.f;
     n = n * r;
     m = m * q;
@@ -392,17 +471,28 @@ __global__ void __launch_bounds__(MOST) gdp_res_bwd_kernel(const ResProblem p) {
     const Eight post = weights(1, p.post, 1.f), scale = weights(2, p.scale, 1.f);
     const Eight u = m * post;          // what gate and scale multiply
     up = fma8(d, eight_of(r), up);     // d_r but for its mean
-    float means[3] = {dot(d, n), 0.f, 0.f};
+    float means[MERGED ? kMostSums : 3] = {dot(d, n), 0.f, 0.f};
     if (p.post) {
       const Eight ku = a * scale * u;  // k m
       means[1] = dot(up, ku);
       means[2] = dot(n, ku);
+    }
+    if constexpr (MERGED) {
+      if (p.depth > 1) {
+        places.wait();
+        if (t + step < T_) squares(after, means + 3);
+      }
+      sums.over(means);
+      s[0] = means[3];
+      s[1] = means[4];
+    } else if (p.post) {
       sums.over(means);
     } else {
       float first_mean[1] = {means[0]};
       sums.over(first_mean);
       means[0] = first_mean[0];
     }
+    place = after;
     const float back = -r * means[0] * p.inv_c;
     d = fma8(n, eight_of(back), up);
     store_row<TR, VEC>(out_at<TR>(p.dres, t, C), thread, threads, C, d);
@@ -420,7 +510,8 @@ __global__ void __launch_bounds__(MOST) gdp_res_bwd_kernel(const ResProblem p) {
     }
     store_row<T, VEC>(out_at<T>(p.dblock, t, C), thread, threads, C, d);
   }
-  float *out = p.partial + (int64_t)blockIdx.x * 3 * C;
+  if (CL > 1) sums.meet();  // the other CTA may still write here
+  float *out = p.partial + (int64_t)(blockIdx.x / CL) * 3 * C;
   if constexpr (WARPS == 1) {  // the CTA's warps' sums, one after the other
     float *rows = reinterpret_cast<float *>(smem);
     if (VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -460,47 +551,63 @@ inline int res_depth(int bytes, int ctas, int others) {
   const int room = 226 * 1024 / ctas - kResBeside - others;
   return 3 * bytes <= room ? 3 : 2 * bytes <= room ? 2 : 1;
 }
-template <typename K>
-cudaError_t res_launch(K kernel, const ResProblem &p, int64_t ctas, dim3 block, int smem, cudaStream_t stream) {
+// `rows`: CTAs or pairs of them.
+template <int CL>
+cudaError_t res_launch(void (*kernel)(ResProblem), const ResProblem &p, int64_t rows, dim3 block, int smem, cudaStream_t stream) {
   if (smem + kResBeside > 48 * 1024) {  // (what is asked for and the kernel's own count together)
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<(unsigned)ctas, block, smem, stream>>>(p);
-  return cudaGetLastError();
+  if constexpr (CL == 1) {
+    kernel<<<(unsigned)rows, block, smem, stream>>>(p);
+    return cudaGetLastError();
+  } else {
+    cudaLaunchConfig_t how{};
+    how.gridDim = dim3((unsigned)(rows * CL));
+    how.blockDim = block;
+    how.dynamicSmemBytes = smem;
+    how.stream = stream;
+    cudaLaunchAttribute pair[1];
+    pair[0].id = cudaLaunchAttributeClusterDimension;
+    pair[0].val.clusterDim.x = CL;
+    pair[0].val.clusterDim.y = pair[0].val.clusterDim.z = 1;
+    how.attrs = pair;
+    how.numAttrs = 1;
+    return cudaLaunchKernelEx(&how, kernel, p);
+  }
 }
 template <typename T, typename TR, int MOST>
 cudaError_t res_fwd(ResProblem &p, int vec, cudaStream_t stream) {
-  const dim3 block(res_threads(p.C), res_rows(p.C));
+  const dim3 block(res_threads(p.C, 1), res_rows(p.C));
   const int threads = block.x * block.y;
   const int row = threads * kRes * ((int)sizeof(T) * (p.gate ? 2 : 1) + (int)sizeof(TR));
   const int64_t rows = (p.T + block.y - 1) / block.y;
-  if (!vec) return res_launch(gdp_res_fwd_kernel<T, TR, false, MOST, 1>, p, rows, block, 0, stream);
+  if (!vec) return res_launch<1>(gdp_res_fwd_kernel<T, TR, false, MOST, 1>, p, rows, block, 0, stream);
   if constexpr (MOST == 512) {  // two rows side by side, where every SM has several pairs of them
     const int per_sm = 512 / threads > 1 ? 512 / threads : 1;
     const int64_t resident = (int64_t)sm_count() * per_sm;
     if (rows >= 8 * resident) {
       p.depth = res_depth(2 * row, per_sm, 0);
-      return res_launch(gdp_res_fwd_kernel<T, TR, true, MOST, 2>, p, resident, block, p.depth * 2 * row, stream);
+      return res_launch<1>(gdp_res_fwd_kernel<T, TR, true, MOST, 2>, p, resident, block, p.depth * 2 * row, stream);
     }
   }
   const int per_sm = 1024 / threads;
   p.depth = res_depth(row, per_sm, 0);
   const int64_t resident = (int64_t)sm_count() * per_sm;
-  return res_launch(gdp_res_fwd_kernel<T, TR, true, MOST, 1>, p, rows < resident ? rows : resident, block, p.depth * row, stream);
+  return res_launch<1>(gdp_res_fwd_kernel<T, TR, true, MOST, 1>, p, rows < resident ? rows : resident, block, p.depth * row, stream);
 }
 template <typename T, typename TR>
 cudaError_t res_fwd_by(ResProblem &p, int vec, cudaStream_t stream) {
   if (res_rows(p.C) > 1) return res_fwd<T, TR, 128>(p, vec, stream);
-  return res_threads(p.C) <= 512 ? res_fwd<T, TR, 512>(p, vec, stream) : res_fwd<T, TR, 1024>(p, vec, stream);
+  return res_threads(p.C, 1) <= 512 ? res_fwd<T, TR, 512>(p, vec, stream) : res_fwd<T, TR, 1024>(p, vec, stream);
 }
 template <typename T>
 cudaError_t launch_res_fwd(ResProblem &p, int vec, cudaStream_t stream) {
   return p.res_f32 ? res_fwd_by<T, float>(p, vec, stream) : res_fwd_by<T, T>(p, vec, stream);
 }
-template <typename T, typename TR, int MOST>
-cudaError_t res_bwd(ResProblem &p, int vec, int64_t ctas, cudaStream_t stream) {
-  const dim3 block(res_threads(p.C), res_rows(p.C));
+template <typename T, typename TR, int MOST, int CL>
+cudaError_t res_bwd(ResProblem &p, int vec, int64_t parts, cudaStream_t stream) {
+  const dim3 block(res_threads(p.C, CL), res_rows(p.C));
   const int threads = block.x * block.y, per_sm = kResResident / threads > 1 ? kResResident / threads : 1;
   const int row = threads * kRes * ((int)sizeof(T) * (p.gate ? 3 : 2) + (int)sizeof(TR) * (p.dr ? 2 : 1)), kept = threads * kRes * 3 * 4;
   p.depth = res_depth(row, per_sm, kept);
@@ -508,16 +615,16 @@ cudaError_t res_bwd(ResProblem &p, int vec, int64_t ctas, cudaStream_t stream) {
   const int sums = block.y > 1 ? (int)block.y * 3 * 256 * (int)sizeof(float) : 0;
   int smem = vec ? p.depth * row + (p.keep ? kept : 0) : 0;
   if (smem < sums) smem = sums;
-  return res_launch(vec ? gdp_res_bwd_kernel<T, TR, true, MOST> : gdp_res_bwd_kernel<T, TR, false, MOST>, p, ctas, block, smem, stream);
+  return res_launch<CL>(vec ? gdp_res_bwd_kernel<T, TR, true, MOST, CL> : gdp_res_bwd_kernel<T, TR, false, MOST, CL>, p, parts, block, smem, stream);
 }
 template <typename T, typename TR>
-cudaError_t res_bwd_by(ResProblem &p, int vec, int64_t ctas, cudaStream_t stream) {
-  if (res_rows(p.C) > 1) return res_bwd<T, TR, 128>(p, vec, ctas, stream);
-  return res_threads(p.C) <= 512 ? res_bwd<T, TR, 512>(p, vec, ctas, stream) : res_bwd<T, TR, 1024>(p, vec, ctas, stream);
+cudaError_t res_bwd_by(ResProblem &p, int vec, int64_t parts, cudaStream_t stream) {
+  if (res_rows(p.C) > 1) return res_bwd<T, TR, 128, 1>(p, vec, parts, stream);
+  return res_cluster(p.C) == 1 ? res_bwd<T, TR, 512, 1>(p, vec, parts, stream) : res_bwd<T, TR, 512, 2>(p, vec, parts, stream);
 }
 template <typename T>
-cudaError_t launch_res_bwd(ResProblem &p, int vec, int64_t ctas, cudaStream_t stream) {
-  return p.res_f32 ? res_bwd_by<T, float>(p, vec, ctas, stream) : res_bwd_by<T, T>(p, vec, ctas, stream);
+cudaError_t launch_res_bwd(ResProblem &p, int vec, int64_t parts, cudaStream_t stream) {
+  return p.res_f32 ? res_bwd_by<T, float>(p, vec, parts, stream) : res_bwd_by<T, T>(p, vec, parts, stream);
 }
 
 }  // namespace layer
