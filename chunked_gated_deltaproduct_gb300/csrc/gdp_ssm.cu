@@ -84,7 +84,7 @@ int64_t over_rows_bytes(int64_t workers, int64_t C, int64_t S) { return (workers
 GDP_EXPORT size_t gdp_scan_forward_workspace_bytes(int64_t T, int64_t N, int64_t C, int64_t S, int64_t G) {
   using namespace gdp::layer;
   if (!scan_shape(T, N, C, S, G)) return 0;
-  const int64_t piece = ssm_piece(T, N, G * ssm_tiles(C / G, S), sm_count());
+  const int64_t piece = ssm_piece(T, N, G * ssm_tiles(C / G, S), sm_count(), kSsmForward);
   return piece ? (size_t)enter_bytes(T / piece + N, C, S) + (size_t)(T / piece + N) * (size_t)C * 4 : 0;
 }
 
@@ -98,7 +98,7 @@ GDP_EXPORT gdp_status gdp_selective_scan(const gdp_scan_args *args, void *stream
   const size_t need = gdp_scan_forward_workspace_bytes(args->T, args->N, args->C, args->S, args->G);
   if (need && (!args->workspace || !aligned(args->workspace, 256) || args->workspace_bytes < need))
     return fail(GDP_ERR_WORKSPACE, "workspace missing, not 256-byte aligned or smaller than gdp_scan_forward_workspace_bytes");
-  p.piece = ssm_piece(p.p.T, p.p.N, p.G * p.tiles, p.sms);
+  p.piece = ssm_piece(p.p.T, p.p.N, p.G * p.tiles, p.sms, kSsmForward);
   p.pieces = p.piece ? p.p.T / p.piece + p.p.N : p.p.N;
   p.ranked = !p.piece && ssm_ranked(p.p.N, p.G * p.tiles, p.sms);
   if (p.piece) {
@@ -128,7 +128,7 @@ GDP_EXPORT int64_t gdp_scan_chunk_rows(int64_t T, int64_t N) { return T < 0 || N
 GDP_EXPORT size_t gdp_scan_workspace_bytes(int64_t T, int64_t N, int64_t C, int64_t S, int64_t G) {
   using namespace gdp::layer;
   if (!scan_shape(T, N, C, S, G)) return 0;
-  const int64_t tiles = G * ssm_tiles(C / G, S), piece = ssm_piece(T, N, tiles, sm_count()), pieces = piece ? T / piece + N : N;
+  const int64_t tiles = G * ssm_tiles(C / G, S), piece = ssm_piece(T, N, tiles, sm_count(), kSsmBackward), pieces = piece ? T / piece + N : N;
   size_t bytes = (size_t)over_rows_bytes(ssm_workers(pieces, tiles, sm_count()), C, S) + (size_t)tiles * (size_t)T * (size_t)(8 * 4 * ssm_lanes(S));
   if (piece) bytes += (size_t)enter_bytes(pieces, C, S) + (size_t)pieces * (size_t)C * 4;
   return bytes;
@@ -175,7 +175,7 @@ GDP_EXPORT gdp_status gdp_selective_scan_backward(const gdp_scan_backward_args *
   p.quad_states = a->S % 4 == 0 && aligned(a->chunk_states, 16) && aligned(a->d_final_state, 16) && aligned(a->d_initial_state, 16);
   p.fast_rows = p.fast_rows && rows_by(p.dy, p.dy_st, p.p.T, a->x_dtype, 16);
   p.pair_out = p.pair_out && aligned(p.dx, 2 * dtype_size(a->x_dtype)) && aligned(p.dz, 2 * dtype_size(a->x_dtype)) && aligned(p.ddt, 2 * dtype_size(a->dt_dtype));
-  p.piece = ssm_piece(p.p.T, p.p.N, p.G * p.tiles, p.sms);
+  p.piece = ssm_piece(p.p.T, p.p.N, p.G * p.tiles, p.sms, kSsmBackward);
   p.pieces = p.piece ? p.p.T / p.piece + p.p.N : p.p.N;
   p.ranked = !p.piece && ssm_ranked(p.p.N, p.G * p.tiles, p.sms);
   p.workers = ssm_workers(p.pieces, p.G * p.tiles, p.sms);

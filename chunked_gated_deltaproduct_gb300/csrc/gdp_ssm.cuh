@@ -1,6 +1,8 @@
 // gdp_ssm.cuh -- the selective state space scan's problem and launchers.
 #pragma once
 
+#include <cmath>
+
 #include "gdp_block.cuh"
 
 namespace gdp {
@@ -58,19 +60,32 @@ inline int64_t ssm_workers(int64_t N, int64_t tiles, int sms) {
   return n < 1 ? 1 : n;
 }
 
-// Tokens of a piece, 0 for whole sequences, from the shape alone (the lengths are the device's).  A sequence alone
-// takes 34 ns a token; pieces add a pass of 0.6 of the first one's time and about 13 us, and use the SMs that whole
-// sequences leave idle.  Measured on the device, whole sequences against pieces (bf16, S = 16): 1 x 65536 x 1024 2533 to
-// 697 us, 1 x 4096 x 512 161 to 43, 1 x 1000 x 1024 43 to 27, 2 x 4096 x 1024 162 to 120; equal sequences of half the SMs'
-// CTAs or more lose (4 x 4096 x 1024 162 to 186), ragged ones win (100, 257, 64 and 1000 tokens x 1024: 43 to 27).
-inline int64_t ssm_piece(int64_t T, int64_t N, int64_t tiles, int sms) {
-  const int64_t whole = N * tiles;
-  if (N == 1 ? T < 512 || 10 * whole >= 6 * sms : T < 256 * N || 2 * whole >= 3 * sms) return 0;
-  int64_t n = (T * tiles + 6 * sms - 1) / (6 * sms);  // six CTAs per SM
-  if (n < T / 192) n = T / 192;                       // (joining takes the pieces of a sequence one by one)
+// Tokens of a piece, 0 for whole sequences, from the shape alone (the lengths are the device's).  Pieces add a pass and two
+// launches, and use the SMs that whole sequences leave idle: as many pieces as are resident at once (`per_sm` CTAs on an
+// SM), unless they became long; then three waves or more of shorter ones.  Joining takes the pieces of a sequence one by one, 0.18 us
+// each where a piece's token takes 0.06 (backward 0.24): the square root.
+// Measured on the device, whole sequences against pieces, us (bf16, S = 16):
+//   forward   1 x 256 x 256 13.1 to 11.9, 1 x 256 x 1024 13.4 to 14.4, 1 x 512 x 2048 22 to 24, 1 x 1000 x 1024 43 to 24,
+//             1 x 4096 x 512 161 to 36, 1 x 65536 x 1024 2533 to 633; 100, 257, 64 and 1000 x 1024 43 to 31
+//   backward  1 x 96 x 256 27 to 23, 1 x 256 x 256 57 to 24, 1 x 512 x 2048 118 to 68, 1 x 1000 x 4096 223 to 194, two of
+//             100 x 512 32 to 27
+// Equal sequences that fill more than the SMs' half lose by it (forward, 4 x 4096 x 1024 162 to 186), ragged ones win.
+// Shorter pieces than fill the SMs once cost a second wave (backward, 1 x 4096 x 512: 224 tokens 81 us, 192 127).
+inline int64_t ssm_piece(int64_t T, int64_t N, int64_t tiles, int sms, int per_sm) {
+  const bool back = per_sm == 2;
+  const int64_t whole = N * tiles, slots = (int64_t)per_sm * sms;
+  if (T < 96 * N || (N > 1 ? 2 * whole >= 3 * sms || (!back && T < 256 * N) : back ? whole > sms : 10 * whole >= 6 * sms)) return 0;
+  int64_t n = (T * tiles + slots - 1) / slots;
+  if (n > 512) n = (T * tiles + 6 * sms - 1) / (6 * sms);
+  const int64_t least = (int64_t)std::sqrt((back ? 1. : 2.) * (double)T);
+  if (n < least) n = least;
   n = (n + 31) / 32 * 32;
-  return n < 128 ? 128 : n;
+  if (n < 32) n = 32;
+  // (forward, one sequence: a launch's time is that of 150 tokens, a piece's token of 2.1 whole ones, a full SM of 200)
+  if (!back && N == 1 && 150 + 2 * n + 200 * T * tiles / (n * slots) >= T) return 0;
+  return n;
 }
+constexpr int kSsmForward = 3, kSsmBackward = 2;  // CTAs on an SM
 
 // Columns of the backward pass's sums over rows: C S, C and C, and up to a multiple of 16 bytes.
 __host__ __device__ inline int64_t ssm_sum_cols(int64_t C, int64_t S) { return (C * (S + 2) + 3) / 4 * 4; }

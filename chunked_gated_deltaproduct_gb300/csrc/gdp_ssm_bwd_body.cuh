@@ -35,7 +35,7 @@ struct SsmBack {
 };
 
 template <typename T, int L, bool FULL, bool LOCAL>
-__global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, 2) gdp_ssm_bwd_kernel(const SsmProblem p) {
+__global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_ssm_bwd_kernel(const SsmProblem p) {
   using Back = SsmBack<T, L>;
   constexpr int CH = Back::CH, SP = Back::SP, K = Back::K, HALF = Back::HALF, CP = CH / 2, HT = kSsmFeed, RT = Back::RT, BLK = Back::BLK;
   constexpr float kLn2 = 0.69314718055994531f;

@@ -35,7 +35,7 @@ constexpr int ssm_fwd_bytes(int dt_size, bool gated) {
 }
 
 template <typename T, int L, int CPT, int TILE, bool FULL, bool LOCAL>
-__global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, CPT == 1 ? 1 : 3) gdp_ssm_fwd_kernel(const SsmProblem p) {
+__global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, CPT == 1 ? 1 : kSsmForward) gdp_ssm_fwd_kernel(const SsmProblem p) {
   constexpr int CH = kSsmThreads / L, SP = L * kQ, CP = CH / 2, HT = kSsmFeed, RT = kSsmThreads / CPT, YP = CH + ssm_skew(CPT);
   extern __shared__ __align__(128) unsigned char smem[];
   const int dt_size = p.dt_f32 ? 4 : (int)sizeof(T);
