@@ -15,7 +15,9 @@ namespace layer {
 // running warps instead: training step of 8 x 4096 x 2048: 3.17 against 2.54 ms).
 //
 // Bound as the forward pass is, by few warps with dependent work (430 instructions a token of 32 channels, issue slots 36 %
-// busy): 8 x 4096 x 2048 x 16 bf16 in 1905 us, dB and dC's parts added up in 51 more, dA's, dD's and ddt_bias's in 13.
+// busy): 8 x 4096 x 2048 x 16 bf16 in 1880 us, dB and dC's parts added up in 52 more, dA's, dD's and ddt_bias's in 13.  Two CTAs
+// on an SM are what its shared memory is cut to: one takes 1.6 times as long (16384 x 2048 x 16, gated, bf16 with fp32 dt: 1771
+// us by one, 1046 by two; fp32 without a gate 1497 and 886; gated fp32 of 16 states is by one, 1707 us).
 
 template <typename T, int L>
 struct SsmBack {
@@ -25,9 +27,10 @@ struct SsmBack {
   __host__ __device__ static constexpr int stage(int dt_size, bool gated) {
     return K * CH * ((int)sizeof(T) * (gated ? 3 : 2) + dt_size) + 2 * K * SP * (int)sizeof(T) + CH * SP * 4;
   }
-  // two chunks of e and e x, dy, B and C; two halves of the running threads' parts; their states before every BLKth token, their
-  // sums for dA
-  static constexpr int formed = K * CH * 12 + 2 * K * SP * 4, starts = (K / BLK + 1) * RT * 8 * 4;
+  static constexpr bool WIDEN = sizeof(T) == 2;  // B and C have to be widened
+  // two chunks of e and e x, dy, B and C; two halves of the running threads' parts; their states before every BLKth token but the
+  // chunk's first, their sums for dA
+  static constexpr int formed = K * CH * 12 + (WIDEN ? 2 * K * SP * 4 : 0), starts = K / BLK * RT * 8 * 4;
   __host__ __device__ static constexpr int parts(bool gated) { return HALF * RT * (8 + 2 * (gated ? 3 : 2)) * 4; }
   __host__ __device__ static constexpr int bytes(int dt_size, bool gated) {
     return STAGES * stage(dt_size, gated) + 2 * (formed + parts(gated)) + starts;
@@ -43,13 +46,13 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
   const int dt_size = p.dt_f32 ? 4 : (int)sizeof(T), stage_bytes = Back::stage(dt_size, p.z != nullptr);
   float2 *steps = reinterpret_cast<float2 *>(smem);            // [2][K][CH]: e, e x
   float *gs = reinterpret_cast<float *>(steps + 2 * K * CH);   // [2][K][CH]: dy
-  float *Bs = gs + 2 * K * CH, *Cs = Bs + 2 * K * SP;          // [2][K][SP]
+  float *Bs = gs + 2 * K * CH, *Cs = Bs + (Back::WIDEN ? 2 * K * SP : 0);  // [2][K][SP]
   // Parts of half a chunk: of dB and dC [2][HALF][2][RT], of u, v and y [2][HALF][kinds][L][CP].
   const int kinds = p.z ? 3 : 2;
-  float4 *sums = reinterpret_cast<float4 *>(Cs + 2 * K * SP);
+  float4 *sums = reinterpret_cast<float4 *>(Cs + (Back::WIDEN ? 2 * K * SP : 0));
   float2 *parts = reinterpret_cast<float2 *>(sums + 2 * HALF * 2 * RT);
-  float4 *starts = reinterpret_cast<float4 *>(parts + 2 * HALF * kinds * RT);  // [K / BLK][2][RT]
-  float4 *totals = starts + K / BLK * 2 * RT;  // [2][RT]
+  float4 *starts = reinterpret_cast<float4 *>(parts + 2 * HALF * kinds * RT);  // [K / BLK - 1][2][RT]
+  float4 *totals = starts + (K / BLK - 1) * 2 * RT;  // [2][RT]
   unsigned char *ring = reinterpret_cast<unsigned char *>(totals + 2 * RT);
   // (pairs of channels change places by lane, so that half a warp's parts fall on all banks)
   auto part_of = [&](int t, int kind, int j, int pair) {
@@ -84,7 +87,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
     return;
   }
   __shared__ SsmOrder by_length;
-  if (!LOCAL && p.ranked) by_length.rank(p);
+  if (!LOCAL && p.ranked) by_length.rank(p, reinterpret_cast<int *>(smem));
   auto row_of = [&](int64_t r) { return !LOCAL && p.ranked ? (int64_t)by_length.order[r] : r; };
   const bool running = threadIdx.x < RT;
   float *out = p.over_rows + worker * ssm_sum_cols(p.C, p.S);
@@ -137,13 +140,15 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
       __syncthreads();
       for (int k = 0; k < chunks; ++k) {
         const int at = (k & 1) * K, rows = k == 0 ? (int)(at_rows.e - at_rows.b) - (chunks - 1) * K : K;
+        const float *B_at = Back::WIDEN ? Bs + at * SP + j * kQ : reinterpret_cast<const float *>(stage(k).B) + j * kQ;
+        const float *C_at = Back::WIDEN ? Cs + at * SP + j * kQ : reinterpret_cast<const float *>(stage(k).C) + j * kQ;
         if constexpr (LOCAL) {
 #pragma unroll 4
           for (int t = rows - 1; t >= 0; --t) {
             const float4 d = *reinterpret_cast<const float4 *>(steps + (at + t) * CH + ch);
             const float2 gd = *reinterpret_cast<const float2 *>(gs + (at + t) * CH + ch);
             float2 Cv[2];
-            pairs(*reinterpret_cast<const float4 *>(Cs + (at + t) * SP + j * kQ), Cv);
+            pairs(*reinterpret_cast<const float4 *>(C_at + t * SP), Cv);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const float e = c ? d.z : d.x;
@@ -158,18 +163,21 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
         } else {
           float2 h[2][2], dA[2][2] = {};  // (a chunk's part: sums over many tokens run in two steps)
           const float *from = stage(k).h + ch * p.S + j * kQ;
+          auto entering = [&] {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float v[kQ];
-            load_states(from + c * p.S, n[c], FULL, v);
-            h[c][0] = make_float2(v[0], v[1]);
-            h[c][1] = make_float2(v[2], v[3]);
-          }
+            for (int c = 0; c < 2; ++c) {
+              float v[kQ];
+              load_states(from + c * p.S, n[c], FULL, v);
+              h[c][0] = make_float2(v[0], v[1]);
+              h[c][1] = make_float2(v[2], v[3]);
+            }
+          };
+          entering();
           // h of the token at t from the one before; `decay` its factor
           auto forth = [&](int t, float2 (&decay)[2][2]) {
             const float4 d = *reinterpret_cast<const float4 *>(steps + (at + t) * CH + ch);
             float2 Bv[2];
-            pairs(*reinterpret_cast<const float4 *>(Bs + (at + t) * SP + j * kQ), Bv);
+            pairs(*reinterpret_cast<const float4 *>(B_at + t * SP), Bv);
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -185,10 +193,9 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
           };
           auto keep = [&](int q) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) starts[(q * 2 + c) * RT + threadIdx.x] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
+            for (int c = 0; c < 2; ++c) starts[((q - 1) * 2 + c) * RT + threadIdx.x] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
           };
           float2 unused[2][2];
-          keep(0);
 #pragma unroll 1
           for (int q = 1; BLK * q < rows; ++q) {
 #pragma unroll
@@ -200,8 +207,8 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
             float2 g;        // dy of both
           };
           auto load = [&](int t) {
-            return Token{*reinterpret_cast<const float4 *>(steps + (at + t) * CH + ch), *reinterpret_cast<const float4 *>(Bs + (at + t) * SP + j * kQ),
-                         *reinterpret_cast<const float4 *>(Cs + (at + t) * SP + j * kQ), *reinterpret_cast<const float2 *>(gs + (at + t) * CH + ch)};
+            return Token{*reinterpret_cast<const float4 *>(steps + (at + t) * CH + ch), *reinterpret_cast<const float4 *>(B_at + t * SP),
+                         *reinterpret_cast<const float4 *>(C_at + t * SP), *reinterpret_cast<const float2 *>(gs + (at + t) * CH + ch)};
           };
           // BLK tokens from t on (m of them exist), there and back
           auto some = [&](int t, int m, auto whole) {
@@ -219,7 +226,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
                 if (!ALL && w >= m) break;
                 float2 Cv[2];
                 float y[2];
-                pairs(*reinterpret_cast<const float4 *>(Cs + (at + t + w) * SP + j * kQ), Cv);
+                pairs(*reinterpret_cast<const float4 *>(C_at + (t + w) * SP), Cv);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                   const bool end = ALL ? w + 1 == BLK : w + 1 >= m;  // (h: after the last of them)
@@ -271,8 +278,12 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
 #pragma unroll 1
           for (int half = 1; half >= 0; --half) {
             auto block = [&](int q, auto whole) {
+              if (q == 0) {
+                entering();
+              } else {
 #pragma unroll
-              for (int c = 0; c < 2; ++c) pairs(starts[(q * 2 + c) * RT + threadIdx.x], h[c]);
+                for (int c = 0; c < 2; ++c) pairs(starts[((q - 1) * 2 + c) * RT + threadIdx.x], h[c]);
+              }
               some(BLK * q, min(BLK, rows - BLK * q), whole);
             };
             if (rows == K) {
@@ -389,7 +400,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
         *reinterpret_cast<float2 *>(gs + (at + t) * CH + c) = d[m];
       }
 #pragma unroll
-      for (int q = thread * kQ; q < K * SP; q += HT * kQ) {
+      for (int q = Back::WIDEN ? thread * kQ : K * SP; q < K * SP; q += HT * kQ) {
         const float2 a0 = load_pair<T>(s.C, q), a1 = load_pair<T>(s.C, q + 2);
         *reinterpret_cast<float4 *>(Cs + at * SP + q) = make_float4(a0.x, a0.y, a1.x, a1.y);
         if (!LOCAL) {

@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, CPT == 1 ? 1 : k
     return;
   }
   __shared__ SsmOrder by_length;
-  if (!LOCAL && p.ranked) by_length.rank(p);
+  if (!LOCAL && p.ranked) by_length.rank(p, reinterpret_cast<int *>(smem));
   const SsmPiece at_rows(p, !LOCAL && p.ranked ? by_length.order[r] : r);
   const int64_t b = at_rows.b, e = at_rows.e;
   if (p.piece && (b >= e || (LOCAL && at_rows.last))) {

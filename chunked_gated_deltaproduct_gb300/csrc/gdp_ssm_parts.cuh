@@ -112,11 +112,11 @@ struct SsmPlace {
   }
 };
 
-// A CTA's threads: the sequences by length into `order`, the longest first, ties in their own order.
+// A CTA's threads: the sequences by length into `order`, the longest first, ties in their own order.  `lengths`: kSsmRanked
+// places that are free until it returns.
 struct SsmOrder {
-  int lengths[kSsmRanked];
   unsigned short order[kSsmRanked];
-  __device__ __forceinline__ void rank(const SsmProblem &p) {
+  __device__ __forceinline__ void rank(const SsmProblem &p, int *lengths) {
     const int n = (int)p.p.N;
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
       int64_t b, e;
