@@ -100,7 +100,7 @@ GDP_EXPORT gdp_status gdp_selective_scan(const gdp_scan_args *args, void *stream
     return fail(GDP_ERR_WORKSPACE, "workspace missing, not 256-byte aligned or smaller than gdp_scan_forward_workspace_bytes");
   p.piece = ssm_piece(p.p.T, p.p.N, p.G * p.tiles, p.sms, kSsmForward);
   p.pieces = p.piece ? p.p.T / p.piece + p.p.N : p.p.N;
-  p.ranked = !p.piece && ssm_ranked(p.p.N, p.G * p.tiles, p.sms);
+  p.ranked = !p.piece && ssm_ranked(p.p.T, p.p.N, p.G * p.tiles, p.sms);
   if (p.piece) {
     p.enter = static_cast<float *>(args->workspace);
     p.spans = p.enter + enter_bytes(p.pieces, p.C, p.S) / 4;
@@ -177,7 +177,7 @@ GDP_EXPORT gdp_status gdp_selective_scan_backward(const gdp_scan_backward_args *
   p.pair_out = p.pair_out && aligned(p.dx, 2 * dtype_size(a->x_dtype)) && aligned(p.dz, 2 * dtype_size(a->x_dtype)) && aligned(p.ddt, 2 * dtype_size(a->dt_dtype));
   p.piece = ssm_piece(p.p.T, p.p.N, p.G * p.tiles, p.sms, kSsmBackward);
   p.pieces = p.piece ? p.p.T / p.piece + p.p.N : p.p.N;
-  p.ranked = !p.piece && ssm_ranked(p.p.N, p.G * p.tiles, p.sms);
+  p.ranked = !p.piece && ssm_ranked(p.p.T, p.p.N, p.G * p.tiles, p.sms);
   p.workers = ssm_workers(p.pieces, p.G * p.tiles, p.sms);
   p.over_rows = static_cast<float *>(a->workspace);
   p.over_channels = p.over_rows + over_rows_bytes(p.workers, p.C, p.S) / 4;

@@ -48,11 +48,12 @@ constexpr int kSsmChunk = GDP_SCAN_CHUNK;
 // Lanes that share a channel, four states each.
 inline int ssm_lanes(int64_t S) { return S <= 16 ? 4 : S <= 32 ? 8 : 16; }
 inline int64_t ssm_tiles(int64_t per, int64_t S) { return (per * ssm_lanes(S) + kSsmThreads - 1) / kSsmThreads; }
-// Sequences that can be ranked by length: where there are more CTAs than are resident at once, the longest come first, so that
+// Sequences that are ranked by length: where there are more CTAs than are resident at once, the longest come first, so that
 // none of them is what the last SMs wait for (64 packed requests of 16 to 8192 tokens x 2048, forward: 1254 us in
-// their own order, 1011 so).
+// their own order, 1011 so).  Every CTA ranks them, which takes about as long as N / 3 tokens: where the mean sequence is
+// shorter than N they run in their own order (200 of a token x 2048: 83 us, ranked 230; 64 of 30: 61 and 65; 26 of 30: 43 and 41).
 constexpr int kSsmRanked = 256;
-inline bool ssm_ranked(int64_t N, int64_t tiles, int sms) { return N > 1 && N <= kSsmRanked && N * tiles > 2 * sms; }
+inline bool ssm_ranked(int64_t T, int64_t N, int64_t tiles, int sms) { return N > 1 && N <= kSsmRanked && T >= N * N && N * tiles > 2 * sms; }
 // Workers of the backward pass: as many as give every SM 16 CTAs, and no more than there are sequences.
 inline int64_t ssm_workers(int64_t N, int64_t tiles, int sms) {
   int64_t n = (16 * (int64_t)sms + tiles - 1) / tiles;
