@@ -498,3 +498,41 @@ def test_residual_norm_of_many_rows_at_every_width(cuda_device, dtype, stream, g
         for name in ("d_residual", "d_block") + (("d_gate",) if gated else ()):
             check(few(d[name]), *want[name], f"{name} {C}")
         assert all(bool(torch.isfinite(d[k]).all()) for k in ("dweight", "dpost_weight", "dscale"))
+
+
+@pytest.mark.parametrize("widths", [(2200, 70), (33, 4200)])
+def test_two_streams_at_once(cuda_device, widths):
+    """Calls that run beside one another on two streams give the bits that they give alone."""
+    dev, lengths = cuda_device, [100, 0, 290, 400]
+    cu = _cu(lengths, dev)
+    blocks = [Block(sum(lengths), c, 16, 4, dev, seed=c) for c in widths]
+    alone = [b.everything(cu) for b in blocks]
+    streams = [torch.cuda.Stream(dev) for _ in blocks]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for b, s in zip(blocks, streams):
+            with torch.cuda.stream(s):
+                got.append(b.everything(cu))
+        torch.cuda.synchronize()
+        for mine, want in zip(got, alone):
+            for name, v in want.items():
+                assert (v is None and mine[name] is None) or torch.equal(mine[name], v), name
+
+
+def test_wide_rows_captured_and_replayed(cuda_device):
+    """Rows of two CTAs, and pieces, in a graph that is replayed with other inputs."""
+    dev, lengths = cuda_device, [30, 0, 200]
+    cu, b, other = _cu(lengths, dev), Block(230, 4200, 16, 3, dev), Block(230, 4200, 16, 3, dev, seed=50)
+    b.everything(cu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = b.everything(cu)
+    for source in (other, Block(230, 4200, 16, 3, dev, seed=90)):
+        for name, v in vars(b).items():
+            v.copy_(getattr(source, name))
+        graph.replay()
+        torch.cuda.synchronize()
+        for name, v in source.everything(cu).items():
+            assert (v is None and got[name] is None) or torch.equal(got[name], v), name
