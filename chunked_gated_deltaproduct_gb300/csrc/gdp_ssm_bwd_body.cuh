@@ -102,12 +102,12 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
       n[k] = ch + k < cn ? states : 0;
       float v[kQ];
 #pragma unroll
-      for (int q = 0; q < kQ; ++q) v[q] = q < n[k] ? p.A[mine + k * p.S + q] * kLog2e : -1.f;
+      for (int q = 0; q < kQ; ++q) v[q] = q < n[k] ? p.A[mine + k * p.S + q] * kLog2e : 0.f;
       A[k][0] = make_float2(v[0], v[1]);
       A[k][1] = make_float2(v[2], v[3]);
       totals[k * RT + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    // padded states stay zero, whatever the inputs are
+    // padded states and their gradients stay zero, whatever the inputs and the decays are (infinite ones too)
     auto real = [&](float2 v, int q) { return FULL ? v : make_float2(2 * q < states ? v.x : 0.f, 2 * q + 1 < states ? v.y : 0.f); };
     auto pairs = [](float4 v, float2 (&o)[2]) {
       o[0] = make_float2(v.x, v.y);
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
                 const float2 x = mul2(both(e), A[c][q]);
-                back[c][q] = mul2(make_float2(ex2(x.x), ex2(x.y)), real(fma2(both(c ? gd.y : gd.x), Cv[q], back[c][q]), q));
+                back[c][q] = real(mul2(make_float2(ex2(x.x), ex2(x.y)), fma2(both(c ? gd.y : gd.x), Cv[q], back[c][q])), q);
               }
             }
           }
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
               for (int q = 0; q < 2; ++q) {
                 const float2 x = mul2(both(c ? d.z : d.x), A[c][q]);
                 decay[c][q] = make_float2(ex2(x.x), ex2(x.y));
-                h[c][q] = fma2(decay[c][q], h[c][q], real(mul2(both(c ? d.w : d.y), Bv[q]), q));
+                h[c][q] = real(fma2(decay[c][q], h[c][q], mul2(both(c ? d.w : d.y), Bv[q])), q);
               }
           };
           auto copy = [](float2 (&to)[2][2], const float2 (&from)[2][2]) {
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
                   sB[q] = c ? fma2(H, ex, sB[q]) : mul2(H, ex);
                   sC[q] = c ? fma2(gg, h[c][q], sC[q]) : mul2(gg, h[c][q]);
                   uu = q ? fma2(H, Bv[q], uu) : mul2(H, Bv[q]);
-                  back[c][q] = mul2(H, decay[w][c][q]);
+                  back[c][q] = real(mul2(H, decay[w][c][q]), q);
                   const float2 x = mul2(back[c][q], before[w][c][q]);
                   vv = q ? fma2(x, A[c][q], vv) : mul2(x, A[c][q]);
                   dA[c][q] = fma2(x, ee, dA[c][q]);

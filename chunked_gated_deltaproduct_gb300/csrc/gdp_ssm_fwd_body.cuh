@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, CPT == 1 ? 1 : k
       h[k][0] = make_float2(v[0], v[1]);
       h[k][1] = make_float2(v[2], v[3]);
 #pragma unroll
-      for (int q = 0; q < kQ; ++q) v[q] = q < n[k] ? p.A[mine + k * p.S + q] * kLog2e : -1.f;  // (none: they decay)
+      for (int q = 0; q < kQ; ++q) v[q] = q < n[k] ? p.A[mine + k * p.S + q] * kLog2e : 0.f;  // (none)
       A[k][0] = make_float2(v[0], v[1]);
       A[k][1] = make_float2(v[2], v[3]);
     }
@@ -121,12 +121,11 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, CPT == 1 ? 1 : k
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const float2 t = mul2(both(in.d[k].x), A[k][q]);
-          float2 add = mul2(both(in.d[k].y), Bv[q]);
-          if (!FULL) {  // padded states stay zero, whatever the input is
-            add.x = 2 * q < states ? add.x : 0.f;
-            add.y = 2 * q + 1 < states ? add.y : 0.f;
+          h[k][q] = fma2(make_float2(ex2(t.x), ex2(t.y)), h[k][q], mul2(both(in.d[k].y), Bv[q]));
+          if (!FULL) {  // padded states stay zero, whatever the input and the decay are (infinite ones too)
+            h[k][q].x = 2 * q < states ? h[k][q].x : 0.f;
+            h[k][q].y = 2 * q + 1 < states ? h[k][q].y : 0.f;
           }
-          h[k][q] = fma2(make_float2(ex2(t.x), ex2(t.y)), h[k][q], add);
           if (!LOCAL) sum = q ? fma2(Cv[q], h[k][q], sum) : mul2(Cv[q], h[k][q]);
         }
         if (LOCAL) span[k] += in.d[k].x;

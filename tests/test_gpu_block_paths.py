@@ -1,0 +1,58 @@
+"""The block operators' paths that only some shapes take, against the float64 references or against the same calls on
+another path: padded states, several sequences per CTA, longest-first order, long runs of rows, pieces in graphs, on
+given streams, in given workspaces and beside one another, calls from two host threads."""
+import math
+import threading
+
+import pytest
+import torch
+
+import chunked_gated_deltaproduct_gb300 as pkg
+from tests import _block_ref as R
+from tests._layer_ref import TINY, UNIT, check
+from tests.test_gpu_block import _as_laid_out, _close, _cu, _on, _rand
+from tests.test_gpu_block_edges import Block
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def _sms(dev):
+    return torch.cuda.get_device_properties(dev).multi_processor_count
+
+
+def _tiles(C, S, G):
+    """CTAs that share the channels: 128 threads, four states a lane."""
+    lanes = 4 if S <= 16 else 8 if S <= 32 else 16
+    return G * -(-(C // G) * lanes // 128)
+
+
+# ---- padded states -----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("lengths,C", [([40, 0, 9], 24), ([600], 20), ([129, 127, 128, 640], 9)])
+@pytest.mark.parametrize("S", [3, 16, 20, 33])
+def test_large_negative_steps(cuda_device, lengths, C, S):
+    """Steps without softplus may be far below zero: states of slow channels grow by a finite factor, whatever number of
+    states the lanes are padded to, forward and backward, whole and in pieces, and token by token."""
+    dev, T, N = cuda_device, sum(lengths), len(lengths)
+    whole = T < 96 * N
+    assert (pkg.gdp_scan_forward_workspace_bytes(T, N, C, S) == 0) == whole
+    x, B, Cm, dy = (_rand(s, i) for i, s in enumerate(((T, C), (T, S), (T, S), (T, C))))
+    dt, A = _rand((T, C), 4).abs() * 0.5, -0.005 * torch.rand((C, S), generator=torch.Generator().manual_seed(5)) - 0.005
+    dt[5::60], dt[36::120] = -200.0, -1000.0   # factors of up to e^2 and e^10
+    dt[6::60], dt[37::120] = 150.0, 900.0      # and most of the way back
+    D, h0, dfin = _rand((C,), 6), _rand((N, C, S), 7), _rand((N, C, S), 8)
+    ins, (gD, gh0, gdy, gdfin), cu = [t.to(dev) for t in (x, dt, A, B, Cm)], _on(dev, D, h0, dy, dfin), _cu(lengths, dev)
+    y, fin, kept = pkg.selective_scan(*ins, cu, D=gD, dt_softplus=False, initial_state=gh0, output_final_state=True, save_states=True)
+    want = R.scan(x, dt, A, B, Cm, lengths, D=D, softplus=False, init=h0)
+    check(y, *want["y"], "y")
+    check(fin, *want["final"], "final state")
+    got = pkg.selective_scan_backward(*ins, gdy, cu, kept, D=gD, dt_softplus=False, d_final_state=gdfin, output_d_initial_state=True)
+    _close(got, R.scan_backward(x, dt, A, B, Cm, dy, lengths, D=D, softplus=False, init=h0, dfin=dfin))
+    at = torch.tensor([5, 36] if T > 36 else [5])
+    few = [t[at] if t.shape[0] == T else t for t in (x, dt, A, B, Cm)]
+    start = _rand((len(at), C, S), 9)
+    y, fin = pkg.selective_scan_decode(*(t.to(dev) for t in few), D=gD, dt_softplus=False, initial_state=start.to(dev), output_final_state=True)
+    want = R.scan(*few, [1] * len(at), D=D, softplus=False, init=start)
+    check(y, *want["y"], "step")
+    check(fin, *want["final"], "state after the step")
