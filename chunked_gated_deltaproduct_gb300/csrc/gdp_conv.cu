@@ -158,13 +158,10 @@ GDP_EXPORT gdp_status gdp_short_convolution_backward(const gdp_conv_backward_arg
   if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < gdp_conv_workspace_bytes(a->T, a->C, a->width))
     return fail(GDP_ERR_WORKSPACE, "workspace missing, not 256-byte aligned or smaller than gdp_conv_workspace_bytes");
   cudaStream_t s = (cudaStream_t)stream;
-  if (a->N == 0 || a->T == 0) {  // every row is padding, or there are none; an empty sequence passes its state's gradient on
+  if (a->N == 0) {  // every row is padding
     if ((st = zero_out(a->dx, (size_t)(a->T * a->C), a->dtype, s)) != GDP_OK) return st;
     if ((st = zero_out(a->d_weight, (size_t)(a->C * a->width), GDP_DTYPE_F32, s)) != GDP_OK) return st;
-    if ((st = zero_out(a->d_bias, (size_t)a->C, GDP_DTYPE_F32, s)) != GDP_OK) return st;
-    if (!a->d_initial_state || bytes == 0) return GDP_OK;
-    return a->d_final_state ? cuda_status(cudaMemcpyAsync(a->d_initial_state, a->d_final_state, bytes, cudaMemcpyDeviceToDevice, s), "state gradient")
-                            : zero_out(a->d_initial_state, bytes / es, a->dtype, s);
+    return zero_out(a->d_bias, (size_t)a->C, GDP_DTYPE_F32, s);
   }
   ConvProblem p{};
   p.x = a->x; p.x_st = stride_of(a->x_stride_t, a->T, a->C);

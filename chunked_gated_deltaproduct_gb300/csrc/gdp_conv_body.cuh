@@ -527,7 +527,7 @@ cudaError_t conv_bwd(ConvProblem &p, int width, cudaStream_t stream) {
   const dim3 block = conv_block(vecs);
   p.parts = conv_parts(p.p.T, vecs, sm_count());
   p.part_rows = (p.p.T + p.parts - 1) / p.parts;
-  p.runs = p.parts / block.y;
+  p.runs = p.parts / block.y;  // (one at least: the bounds of no rows are checked too)
   const dim3 grid((unsigned)(p.runs + (p.dinit ? (p.p.N + block.y - 1) / block.y : 0)), (unsigned)((vecs + block.x - 1) / block.x));
   if (width == 2) gdp_conv_bwd_kernel<T, 2, V><<<grid, block, 0, stream>>>(p);
   else if (width == 3) gdp_conv_bwd_kernel<T, 3, V><<<grid, block, 0, stream>>>(p);

@@ -56,3 +56,28 @@ def test_large_negative_steps(cuda_device, lengths, C, S):
     want = R.scan(*few, [1] * len(at), D=D, softplus=False, init=start)
     check(y, *want["y"], "step")
     check(fin, *want["final"], "state after the step")
+
+
+# ---- bounds of no rows -------------------------------------------------------------------------------
+
+def test_bounds_of_no_rows_backward(cuda_device):
+    """The backward passes check bounds where there are no rows too; empty sequences pass the states' gradients on."""
+    dev = cuda_device
+    b = Block(0, 24, 16, 2, dev)
+    kept = torch.empty((2, 24, 16), device=dev)
+    for bounds, bad in (([0, 0, 0], False), ([0, 3, 3], True), ([0, 0, 1], True), ([-1, 0, 0], True)):
+        cu = torch.tensor(bounds, dtype=torch.int32, device=dev)
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        d = b.conv_backward(cu, initial_state=b.c0, d_final_state=b.c0, device_status=status)
+        assert bool(int(status) & pkg.GDP_DEV_ERR_CU_SEQLENS) == bad, bounds
+        assert torch.equal(d["d_initial_state"], b.c0) and not d["dweight"].any() and not d["dbias"].any()
+        status.zero_()
+        d = b.conv_backward(cu, device_status=status)
+        assert bool(int(status) & pkg.GDP_DEV_ERR_CU_SEQLENS) == bad and not d["dweight"].any() and not d["dbias"].any()
+        status.zero_()
+        assert not b.conv_backward(cu, initial_state=b.c0, device_status=status)["d_initial_state"].any()
+        assert bool(int(status) & pkg.GDP_DEV_ERR_CU_SEQLENS) == bad
+        status.zero_()
+        d = b.scan_backward(cu, kept, d_final_state=b.h0, output_d_initial_state=True, device_status=status)
+        assert bool(int(status) & pkg.GDP_DEV_ERR_CU_SEQLENS) == bad, bounds
+        assert torch.equal(d["d_initial_state"], b.h0) and not d["dA"].any() and not d["dD"].any()
