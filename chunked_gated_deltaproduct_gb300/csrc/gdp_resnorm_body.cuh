@@ -238,8 +238,8 @@ __device__ __forceinline__ Eight gate_slope(const Eight &g, int act, Eight *fact
   Eight q, slope;
 #pragma unroll
   for (int k = 0; k < kPairs; ++k) {
-    q.v[k] = sigmoid2(g.v[k]);
-    const float2 rest = fma2(q.v[k], both(-1.f), both(1.f));
+    float2 rest;  // 1 - q to its own precision: a sigmoid's slope is q rest, also where the gate is all but open
+    sigmoid_halves(g.v[k], &q.v[k], &rest);
     slope.v[k] = mul2(q.v[k], act == GDP_ACT_SILU ? fma2(g.v[k], rest, both(1.f)) : rest);
   }
   *factor = act == GDP_ACT_SILU ? q * g : q;

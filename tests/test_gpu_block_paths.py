@@ -58,6 +58,28 @@ def test_large_negative_steps(cuda_device, lengths, C, S):
     check(fin, *want["final"], "state after the step")
 
 
+# ---- the gate's slope --------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("C", [64, 61, 520])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_slope_of_an_open_gate(cuda_device, dtype, C):
+    """The gradient of a sigmoid gate keeps its relative precision where the gate is all but open or closed."""
+    dev, most = cuda_device, 80.0 if dtype != F16 else 15.0
+    T = 41
+    gate = torch.linspace(-most, most, T * C).view(T, C).to(dtype)
+    block, dr, w = _rand((T, C), 1).sign().mul(1024.0).to(dtype), 1 + _rand((T, C), 2).abs(), torch.ones(C)
+    r = _rand((T, C), 3)
+    zero = torch.zeros((T, C), dtype=dtype, device=dev)
+    got = pkg.residual_norm_backward(zero, dr.to(dev), r.to(dev), block.to(dev), w.to(dev), gate=gate.to(dev), activation="sigmoid")["d_gate"]
+    v = gate.double()
+    want = dr.double() * block.double() * torch.sigmoid(v) * torch.sigmoid(-v)
+    # (d_gate = dr block q (1 - q): each half off by act_error, three products, one rounding to the type)
+    assert bool((want.abs() > 64 * TINY[dtype]).all())
+    error = (got.cpu().double() - want).abs() / want.abs()
+    bound = 2 * R.act_error(v) + 4 * R.U + UNIT[dtype] + TINY[dtype] / want.abs()
+    assert bool((error <= bound).all()), float((error - bound).max())
+
+
 # ---- bounds of no rows -------------------------------------------------------------------------------
 
 def test_bounds_of_no_rows_backward(cuda_device):
