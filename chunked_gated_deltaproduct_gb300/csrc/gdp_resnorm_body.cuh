@@ -545,17 +545,20 @@ __global__ void __launch_bounds__(MOST, MOST == 128 ? kResResident / MOST : 1) g
   }
 }
 
+constexpr int kResShared = 226 * 1024;  // shared memory of an SM that CTAs' rows, weights and sums may take
 constexpr int kResBeside = 2048;  // shared memory of a CTA besides its rows: the sums' buffers, and 1 KB of the system's
 // Places of a row in shared memory (see RowPlaces) for `ctas` resident CTAs: three, or as many as there is room for.
 inline int res_depth(int bytes, int ctas, int others) {
-  const int room = 226 * 1024 / ctas - kResBeside - others;
+  const int room = kResShared / ctas - kResBeside - others;
   return 3 * bytes <= room ? 3 : 2 * bytes <= room ? 2 : 1;
 }
 // `rows`: CTAs or pairs of them.
 template <int CL>
 cudaError_t res_launch(void (*kernel)(ResProblem), const ResProblem &p, int64_t rows, dim3 block, int smem, cudaStream_t stream) {
-  if (smem + kResBeside > 48 * 1024) {  // (what is asked for and the kernel's own count together)
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (What is asked for and the kernel's own count together.  One limit for all calls: it is the kernel's, not the call's, and
+  // another host thread may launch the same kernel with more.)
+  if (smem + kResBeside > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kResShared - kResBeside);
     if (e != cudaSuccess) return e;
   }
   if constexpr (CL == 1) {
@@ -611,7 +614,7 @@ cudaError_t res_bwd(ResProblem &p, int vec, int64_t parts, cudaStream_t stream) 
   const int threads = block.x * block.y, per_sm = kResResident / threads > 1 ? kResResident / threads : 1;
   const int row = threads * kRes * ((int)sizeof(T) * (p.gate ? 3 : 2) + (int)sizeof(TR) * (p.dr ? 2 : 1)), kept = threads * kRes * 3 * 4;
   p.depth = res_depth(row, per_sm, kept);
-  p.keep = vec && p.depth * row + kept <= 226 * 1024 / per_sm - kResBeside;
+  p.keep = vec && p.depth * row + kept <= kResShared / per_sm - kResBeside;
   const int sums = block.y > 1 ? (int)block.y * 3 * 256 * (int)sizeof(float) : 0;
   int smem = vec ? p.depth * row + (p.keep ? kept : 0) : 0;
   if (smem < sums) smem = sums;

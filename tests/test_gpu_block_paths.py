@@ -1,6 +1,7 @@
 """The block operators' paths that only some shapes take, against the float64 references or against the same calls on
 another path: padded states, several sequences per CTA, longest-first order, long runs of rows, pieces in graphs, on
 given streams, in given workspaces and beside one another, calls from two host threads."""
+import ctypes
 import math
 import threading
 
@@ -8,6 +9,7 @@ import pytest
 import torch
 
 import chunked_gated_deltaproduct_gb300 as pkg
+from chunked_gated_deltaproduct_gb300 import block
 from tests import _block_ref as R
 from tests._layer_ref import TINY, UNIT, check
 from tests.test_gpu_block import _as_laid_out, _close, _cu, _on, _rand
@@ -67,13 +69,13 @@ def test_slope_of_an_open_gate(cuda_device, dtype, C):
     dev, most = cuda_device, 80.0 if dtype != F16 else 15.0
     T = 41
     gate = torch.linspace(-most, most, T * C).view(T, C).to(dtype)
-    block, dr, w = _rand((T, C), 1).sign().mul(1024.0).to(dtype), 1 + _rand((T, C), 2).abs(), torch.ones(C)
+    rows, dr, w = _rand((T, C), 1).sign().mul(1024.0).to(dtype), 1 + _rand((T, C), 2).abs(), torch.ones(C)
     r = _rand((T, C), 3)
     zero = torch.zeros((T, C), dtype=dtype, device=dev)
-    got = pkg.residual_norm_backward(zero, dr.to(dev), r.to(dev), block.to(dev), w.to(dev), gate=gate.to(dev), activation="sigmoid")["d_gate"]
+    got = pkg.residual_norm_backward(zero, dr.to(dev), r.to(dev), rows.to(dev), w.to(dev), gate=gate.to(dev), activation="sigmoid")["d_gate"]
     v = gate.double()
-    want = dr.double() * block.double() * torch.sigmoid(v) * torch.sigmoid(-v)
-    # (d_gate = dr block q (1 - q): each half off by act_error, three products, one rounding to the type)
+    want = dr.double() * rows.double() * torch.sigmoid(v) * torch.sigmoid(-v)
+    # (d_gate = dr rows q (1 - q): each half off by act_error, three products, one rounding to the type)
     assert bool((want.abs() > 64 * TINY[dtype]).all())
     error = (got.cpu().double() - want).abs() / want.abs()
     bound = 2 * R.act_error(v) + 4 * R.U + UNIT[dtype] + TINY[dtype] / want.abs()
@@ -103,3 +105,73 @@ def test_bounds_of_no_rows_backward(cuda_device):
         d = b.scan_backward(cu, kept, d_final_state=b.h0, output_d_initial_state=True, device_status=status)
         assert bool(int(status) & pkg.GDP_DEV_ERR_CU_SEQLENS) == bad, bounds
         assert torch.equal(d["d_initial_state"], b.h0) and not d["dA"].any() and not d["dD"].any()
+
+
+# ---- two host threads --------------------------------------------------------------------------------
+
+def _from_two_threads(calls, times):
+    """Every call `times` times from a host thread of its own, all at once, each thread on its own stream."""
+    failures, start = [], threading.Barrier(len(calls))
+
+    def work(call):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            start.wait()
+            try:
+                for _ in range(times):
+                    call()
+            except Exception as e:  # noqa: BLE001 (what it was is shown below)
+                failures.append(repr(e))
+            torch.cuda.current_stream().synchronize()
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(call,)) for call in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures, failures
+
+
+def _same(got, want):
+    for name, v in want.items():
+        assert (v is None and got[name] is None) or torch.equal(got[name], v), name
+
+
+def _norm_call(name, args, fields):
+    """The C entry with arguments that are filled in once, so that a thread does little else than launch."""
+    lib, a = block._library(), args(**{k: v.data_ptr() if isinstance(v, torch.Tensor) else v for k, v in fields.items()})
+
+    def call():
+        if getattr(lib, name)(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) != pkg.GDP_OK:
+            raise RuntimeError(pkg.gdp_last_error())
+
+    return call
+
+
+def test_residual_norm_from_two_threads(cuda_device):
+    """Calls of one kernel that ask for different amounts of shared memory (with and without a gate), from two host threads
+    at once."""
+    dev, T, C = cuda_device, 6, 4096
+    blocks = [Block(T, C, 1, 1, dev, seed=s) for s in (0, 50)]
+    calls, outs, want = [], [], []
+    for b, gate in zip(blocks, (True, False)):
+        how = dict(post_weight=b.post, gate=b.gate if gate else None, activation="silu")
+        y, r = pkg.residual_norm(b.res, b.x, b.weight, **how)
+        want.append({"y": y, "r": r, **pkg.residual_norm_backward(b.dy, b.dr if gate else None, b.res, b.x, b.weight, **how)})
+        out = {k: None if v is None else torch.empty_like(v) for k, v in want[-1].items()}
+        room = torch.empty(pkg.gdp_residual_norm_workspace_bytes(T, C), dtype=torch.uint8, device=dev)
+        outs.append(out)
+        common = dict(block=b.x, block_stride_t=C, gate=b.gate if gate else 0, gate_stride_t=C, weight=b.weight, post_weight=b.post, T=T,
+                      C=C, eps=1e-5, dtype=pkg.GDP_DTYPE_BF16, residual_dtype=pkg.GDP_DTYPE_F32, activation=block.GDP_ACT_SILU)
+        forward = _norm_call("gdp_residual_norm", pkg.GdpResidualNormArgs,
+                             dict(common, residual=b.res, residual_stride_t=C, y=out["y"], residual_out=out["r"]))
+        backward = _norm_call("gdp_residual_norm_backward", pkg.GdpResidualNormBackwardArgs,
+                              dict(common, d_y=b.dy, d_y_stride_t=C, d_residual_out=b.dr if gate else 0, d_residual_out_stride_t=C,
+                                   residual_out=b.res, residual_out_stride_t=C, d_residual=out["d_residual"], d_block=out["d_block"],
+                                   d_gate=out["d_gate"] if gate else 0, d_weight=out["dweight"], d_post_weight=out["dpost_weight"],
+                                   workspace=room, workspace_bytes=room.numel()))
+        calls.append((forward, backward))
+    for k in range(2):
+        _from_two_threads([c[k] for c in calls], 20000)
+    for got, w in zip(outs, want):
+        _same(got, w)
