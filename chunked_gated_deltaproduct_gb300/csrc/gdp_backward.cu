@@ -705,8 +705,7 @@ int chunk_slice(int d, int qpad) { return ChunkSmem(d, qpad, 16).total <= 227u *
 template <int D, int VSL>
 cudaError_t launch_chunk(const BwdProblem &p, cudaStream_t stream) {
   const size_t smem = ChunkSmem(D, p.qpad, VSL).total;
-  cudaError_t e = cudaFuncSetAttribute(gdp_bwd_chunk_kernel<D, VSL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  cudaError_t e = allow_shared(gdp_bwd_chunk_kernel<D, VSL>);
   if (e != cudaSuccess) return e;
   gdp_bwd_chunk_kernel<D, VSL><<<dim3((unsigned)p.ntdp_pad, (unsigned)p.H), kChunkThreads, smem, stream>>>(p);
   return cudaGetLastError();

@@ -744,8 +744,7 @@ bool bwd_chunk_tc_serves(int d, int qpad) { return d == kCtD && qpad <= 32; }
 
 cudaError_t launch_bwd_chunk_tc(const BwdProblem &p, cudaStream_t stream) {
   const size_t smem = CtLayout(p.qpad).total + 1024u;
-  cudaError_t e =
-      cudaFuncSetAttribute(gdp_bwd_chunk_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(gdp_bwd_chunk_tc_kernel);
   if (e != cudaSuccess) return e;
   // the states entering and the gradients leaving every expanded chunk, [ntdp][H][V][K] fp32, as
   // rows of K in 32 x 32 boxes

@@ -393,8 +393,7 @@ size_t bwd_image_stride(int d, int qpad) { return (BwdImageLayout(d, qpad).bytes
 
 cudaError_t launch_bwd_tc_scan(const BwdProblem &p, cudaStream_t stream) {
   const size_t smem = bt_smem_bytes(p.D, p.qpad);
-  cudaError_t e =
-      cudaFuncSetAttribute(gdp_bwd_tc_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(gdp_bwd_tc_scan_kernel);
   if (e != cudaSuccess) return e;
   alignas(64) CUtensorMap tm_dx, tm_dinit, tm_do;
   // the output gradients [T][H][V] bf16 in boxes of qpad token rows (rows past T read as zero)

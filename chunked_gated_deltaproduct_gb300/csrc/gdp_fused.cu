@@ -855,7 +855,7 @@ size_t fused_smem_bytes(int qpad) { return (size_t)FusedLayout(qpad).total + 102
 cudaError_t launch_fused(const Problem &p, cudaStream_t stream) {
   if (p.N == 0) return cudaSuccess;
   const size_t smem = fused_smem_bytes(p.qpad);
-  cudaError_t e = cudaFuncSetAttribute(gdp_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(gdp_fused_kernel);
   if (e != cudaSuccess) return e;
   alignas(64) CUtensorMap tm_k, tm_q, tm_v, tm_cs, tm_fin, tm_seg, tm_out_a, tm_out_b;
   const int64_t rows = p.T * p.M;

@@ -250,6 +250,18 @@ cudaError_t launch_kernel(void (*kern)(Params...), dim3 grid, dim3 block, size_t
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Args &&>(args)...);
 }
 
+// Lets a kernel be launched with any dynamic shared memory that an SM has beside the kernel's own.  The limit is the
+// kernel's, not the call's, and shared by all host threads: one that followed each call's need would fail the launch of another
+// thread that needs more.
+template <typename Kern>
+cudaError_t allow_shared(Kern kern) {
+  cudaFuncAttributes a;
+  const cudaError_t e = cudaFuncGetAttributes(&a, kern);
+  if (e != cudaSuccess) return e;
+  const int most = 227 * 1024 - (int)a.sharedSizeBytes;
+  return a.maxDynamicSharedSizeBytes == most ? cudaSuccess : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 // Input head h / r of state head h, with m = ceil(2^32 / r): (h m) >> 32 equals h / r for
 // every h < 2^16 and r <= 2^16 (the rounding excess of m stays below 2^-16 <= 1 / r), and it
 // takes one wide multiply instead of a division.

@@ -799,7 +799,7 @@ inline int cluster_size(int slices, int rows, int sms, int per_sm) {
 // Launches slices x cluster CTAs in clusters.
 template <typename... Params, typename... Args>
 cudaError_t launch_clusters(void (*kern)(Params...), int slices, int cluster, int smem, cudaStream_t stream, Args &&...args) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = gdp::allow_shared(kern);
   if (e == cudaSuccess && cluster > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};

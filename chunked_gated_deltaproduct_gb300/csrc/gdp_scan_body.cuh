@@ -621,7 +621,7 @@ __device__ __forceinline__ void scan_body(const Problem &p, const CUtensorMap &t
 template <typename Kern>
 cudaError_t launch_scan_kernel(Kern kern, const Problem &p, cudaStream_t stream) {
   const size_t smem = scan_smem_bytes(p.K, p.qpad, p.V);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(kern);
   if (e != cudaSuccess) return e;
   alignas(64) CUtensorMap tm_cs, tm_fin, tm_seg;
   const int64_t hv = (int64_t)p.H * p.V;

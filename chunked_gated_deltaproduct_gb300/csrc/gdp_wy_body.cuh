@@ -674,7 +674,7 @@ cudaError_t launch_wy_kernel(Kern kern, const Problem &p, cudaStream_t stream) {
   // size: with three, the scan beside them ran 2.5 % slower on the 65536-token sequence than the
   // WY tiles gained (A/B on one GB300)
   const size_t smem = p.seg_rows > 0 ? (size_t)100 * 1024 : WyLayout(p.K).total + 1024;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(kern);
   if (e != cudaSuccess) return e;
   alignas(64) CUtensorMap tm_k, tm_q, tm_v;
   const int64_t rows = p.T * p.M;
