@@ -3,6 +3,7 @@
 #pragma once
 
 #include <climits>
+#include <initializer_list>
 
 #include "../../include/gdp_block.h"
 #include "gdp_layer.cuh"
@@ -115,11 +116,48 @@ inline gdp_status rows_ok(const void *p, int64_t stride, int64_t T, int64_t C, i
 }
 // The stride of a single row means nothing and may be anything in a view.
 inline int64_t stride_of(int64_t stride, int64_t T, int64_t C) { return T > 1 ? stride : C; }
-// Whether T >= 1 rows `stride` apart and T contiguous rows share memory (gaps between the first ones' rows counted).
-inline bool spans_overlap(const void *in, int64_t stride, const void *out, int64_t T, int64_t C, int type) {
-  const size_t es = dtype_size(type), in_bytes = ((size_t)(T - 1) * (size_t)stride + (size_t)C) * es, out_bytes = (size_t)T * (size_t)C * es;
-  const uintptr_t a = (uintptr_t)in, b = (uintptr_t)out;
-  return a < b + out_bytes && b < a + in_bytes;
+// A tensor of T rows as the overlap checks see it: `cols` elements every `stride` (an output's are contiguous), in `groups`
+// that are `stride_g` apart.
+struct Span {
+  const void *p;
+  int64_t stride, cols;
+  int type;
+  const char *name;
+  int64_t groups, stride_g;
+};
+inline Span rows(const void *p, int64_t stride, int64_t cols, int type, const char *name) { return {p, stride, cols, type, name, 1, 0}; }
+inline Span dense(const void *p, int64_t cols, int type, const char *name) { return rows(p, cols, cols, type, name); }
+// Whether T >= 1 rows share memory with T contiguous ones (the gaps between a strided tensor's rows are not its own).
+inline bool spans_overlap(const Span &in, const Span &out, int64_t T) {
+  if (!in.p || !out.p) return false;
+  typedef __int128 Wide;  // (strides may be anything)
+  const Wide es = dtype_size(in.type), row = in.cols * es, apart = in.stride * es, bytes = (Wide)T * out.cols * dtype_size(out.type);
+  const Wide whole = (T - 1) * apart + (in.groups - 1) * in.stride_g * es + row, d = (Wide)(uintptr_t)out.p - (Wide)(uintptr_t)in.p;
+  if (d >= whole || d + bytes <= 0) return false;
+  for (int64_t g = 0; g < in.groups; ++g) {
+    const Wide at = d - g * in.stride_g * es;  // of the output, from the group's first row
+    const Wide t = at < row ? 0 : (at - row) / apart + 1;  // the first row that ends behind the output's begin
+    if (t < T && t * apart < at + bytes) return true;
+  }
+  return false;
+}
+// Outputs share memory with no input and not with one another.
+inline gdp_status apart_ok(int64_t T, std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  if (T == 0) return GDP_OK;
+  const Span *o = outs.begin();
+  for (size_t i = 0; i < outs.size(); ++i) {
+    for (const Span &in : ins)
+      if (spans_overlap(in, o[i], T)) {
+        set_last_error("%s overlaps %s", o[i].name, in.name);
+        return GDP_ERR_ALIAS;
+      }
+    for (size_t k = 0; k < i; ++k)
+      if (spans_overlap(o[k], o[i], T)) {
+        set_last_error("%s overlaps %s", o[i].name, o[k].name);
+        return GDP_ERR_ALIAS;
+      }
+  }
+  return GDP_OK;
 }
 // Whether its rows can be read `bytes` at a time.
 inline bool rows_by(const void *p, int64_t stride, int64_t T, int type, size_t bytes) {

@@ -56,8 +56,8 @@ gdp_status resolve(const gdp_conv_args *a, bool step, ConvProblem *p) {
   if ((st = states_ok(a->initial_state, a->output_state, a->state, a->state_indices, a->num_slots, es,
                       es * (size_t)a->N * (size_t)(a->width - 1) * (size_t)a->C)) != GDP_OK)
     return st;
-  if (a->T > 0 && spans_overlap(a->x, stride_of(a->x_stride_t, a->T, a->C), a->output, a->T, a->C, a->dtype))
-    return fail(GDP_ERR_ALIAS, "output overlaps x");
+  if ((st = apart_ok(a->T, {dense(a->output, a->C, a->dtype, "output")}, {rows(a->x, stride_of(a->x_stride_t, a->T, a->C), a->C, a->dtype, "x")})) != GDP_OK)
+    return st;
   *p = ConvProblem{};
   p->x = a->x; p->x_st = stride_of(a->x_stride_t, a->T, a->C);
   p->w = a->weight; p->b = a->bias; p->y = a->output;
@@ -157,6 +157,10 @@ GDP_EXPORT gdp_status gdp_short_convolution_backward(const gdp_conv_backward_arg
     return fail(GDP_ERR_ALIAS, "d_initial_state overlaps initial_state or d_final_state");
   if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < gdp_conv_workspace_bytes(a->T, a->C, a->width))
     return fail(GDP_ERR_WORKSPACE, "workspace missing, not 256-byte aligned or smaller than gdp_conv_workspace_bytes");
+  if ((st = apart_ok(a->T, {dense(a->dx, a->C, a->dtype, "dx")},
+                     {rows(a->x, stride_of(a->x_stride_t, a->T, a->C), a->C, a->dtype, "x"),
+                      rows(a->d_output, stride_of(a->d_output_stride_t, a->T, a->C), a->C, a->dtype, "d_output")})) != GDP_OK)
+    return st;
   cudaStream_t s = (cudaStream_t)stream;
   if (a->N == 0) {  // every row is padding
     if ((st = zero_out(a->dx, (size_t)(a->T * a->C), a->dtype, s)) != GDP_OK) return st;

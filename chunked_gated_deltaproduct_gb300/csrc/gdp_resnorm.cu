@@ -25,9 +25,9 @@ bool short_strides(std::initializer_list<int64_t> strides) {
     if (s > INT32_MAX) return false;
   return true;
 }
-// The same rows exactly, or others.
+// The stream's rows may be replaced: its own buffer exactly, or others.
 bool partly(const void *in, int64_t stride, const void *out, int64_t T, int64_t C, int type) {
-  return in && T > 0 && !(in == out && stride == C) && spans_overlap(in, stride, out, T, C, type);
+  return T > 0 && !(in == out && stride == C) && spans_overlap(rows(in, stride, C, type, ""), dense(out, C, type, ""), T);
 }
 
 }  // namespace
@@ -51,6 +51,10 @@ GDP_EXPORT gdp_status gdp_residual_norm(const gdp_residual_norm_args *a, void *s
   p.gate_st = stride_of(a->gate_stride_t, a->T, a->C);
   if (!short_strides({p.res_st, p.block_st, p.gate_st})) return fail(GDP_ERR_UNSUPPORTED, "row strides below 2^31 elements");
   if (partly(p.res, p.res_st, a->residual_out, a->T, a->C, a->residual_dtype)) return fail(GDP_ERR_ALIAS, "residual_out partly overlaps residual");
+  const Span residual = rows(p.res, p.res_st, a->C, a->residual_dtype, "residual"), block = rows(p.block, p.block_st, a->C, a->dtype, "block"),
+             gate = rows(p.gate, p.gate_st, a->C, a->dtype, "gate"), y = dense(a->y, a->C, a->dtype, "y"),
+             out = dense(a->residual_out, a->C, a->residual_dtype, "residual_out");
+  if ((st = apart_ok(a->T, {y}, {residual, block, gate, out})) != GDP_OK || (st = apart_ok(a->T, {out}, {block, gate})) != GDP_OK) return st;
   if (a->T == 0) return GDP_OK;
   p.w = a->weight; p.post = a->post_weight; p.scale = a->scale;
   p.y = a->y; p.r = a->residual_out;
@@ -100,6 +104,13 @@ GDP_EXPORT gdp_status gdp_residual_norm_backward(const gdp_residual_norm_backwar
   p.dr_st = stride_of(a->d_residual_out_stride_t, a->T, a->C);
   if (!short_strides({p.res_st, p.block_st, p.gate_st, p.dy_st, p.dr_st})) return fail(GDP_ERR_UNSUPPORTED, "row strides below 2^31 elements");
   if (partly(p.dr, p.dr_st, a->d_residual, a->T, a->C, a->residual_dtype)) return fail(GDP_ERR_ALIAS, "d_residual partly overlaps d_residual_out");
+  const Span dy = rows(p.dy, p.dy_st, a->C, a->dtype, "d_y"), dr = rows(p.dr, p.dr_st, a->C, a->residual_dtype, "d_residual_out"),
+             res = rows(p.res, p.res_st, a->C, a->residual_dtype, "residual_out"), block = rows(p.block, p.block_st, a->C, a->dtype, "block"),
+             gate = rows(p.gate, p.gate_st, a->C, a->dtype, "gate"), dres = dense(a->d_residual, a->C, a->residual_dtype, "d_residual");
+  if ((st = apart_ok(a->T, {dense(a->d_block, a->C, a->dtype, "d_block"), dense(a->gate ? a->d_gate : nullptr, a->C, a->dtype, "d_gate")},
+                     {dy, dr, res, block, gate, dres})) != GDP_OK ||
+      (st = apart_ok(a->T, {dres}, {dy, res, block, gate})) != GDP_OK)
+    return st;
   p.w = a->weight; p.post = a->post_weight; p.scale = a->scale;
   p.dres = a->d_residual; p.dblock = a->d_block; p.dgate = a->d_gate;
   p.partial = static_cast<float *>(a->workspace);

@@ -50,6 +50,14 @@ gdp_status common(const Args *a, SsmProblem *p) {
   return GDP_OK;
 }
 
+// Outputs against the inputs that `common` has resolved, and d_output (`dy`) in the backward pass.
+gdp_status scan_apart(const SsmProblem &p, int type, std::initializer_list<Span> outs, const Span &dy) {
+  const int dt_type = p.dt_f32 ? GDP_DTYPE_F32 : type;
+  return apart_ok(p.p.T, outs,
+                  {rows(p.x, p.x_st, p.C, type, "x"), rows(p.dt, p.dt_st, p.C, dt_type, "dt"), rows(p.z, p.z_st, p.C, type, "z"),
+                   Span{p.B, p.B_st, p.S, type, "B", p.G, p.B_sg}, Span{p.Cm, p.C_st, p.S, type, "C", p.G, p.C_sg}, dy});
+}
+
 gdp_status resolve(const gdp_scan_args *a, bool step, SsmProblem *p) {
   set_last_error("");
   if (!a) return fail(GDP_ERR_INVALID_ARG, "args is NULL");
@@ -62,6 +70,7 @@ gdp_status resolve(const gdp_scan_args *a, bool step, SsmProblem *p) {
                       sizeof(float) * (size_t)a->N * (size_t)a->C * (size_t)a->S)) != GDP_OK)
     return st;
   if (!aligned(a->chunk_states, 4)) return fail(GDP_ERR_INVALID_ARG, "state buffers must be aligned to their elements");
+  if ((st = scan_apart(*p, a->x_dtype, {dense(a->output, a->C, a->x_dtype, "output")}, Span{})) != GDP_OK) return st;
   p->y = a->output;
   p->s = StateModes{a->initial_state, a->output_state, a->state, a->state_indices, a->num_slots};
   p->chunks = step ? nullptr : a->chunk_states;
@@ -158,6 +167,13 @@ GDP_EXPORT gdp_status gdp_selective_scan_backward(const gdp_scan_backward_args *
   if (overlap(a->d_final_state, a->d_initial_state, state_bytes)) return fail(GDP_ERR_ALIAS, "d_initial_state overlaps d_final_state");
   if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < gdp_scan_workspace_bytes(a->T, a->N, a->C, a->S, a->G))
     return fail(GDP_ERR_WORKSPACE, "workspace missing, not 256-byte aligned or smaller than gdp_scan_workspace_bytes");
+  const int type = a->x_dtype;
+  const int64_t vectors = a->G * a->S;
+  if ((st = scan_apart(p, type,
+                       {dense(a->dx, a->C, type, "dx"), dense(a->ddt, a->C, a->dt_dtype, "ddt"), dense(a->z ? a->dz : nullptr, a->C, type, "dz"),
+                        dense(a->dB, vectors, type, "dB"), dense(a->dC, vectors, type, "dC")},
+                       rows(a->d_output, stride_of(a->d_output_stride_t, a->T, a->C), a->C, type, "d_output"))) != GDP_OK)
+    return st;
   cudaStream_t s = (cudaStream_t)stream;
   if (a->N == 0) {  // every row is padding
     const size_t rows = (size_t)(a->T * a->C), vectors = (size_t)(a->T * a->G * a->S);

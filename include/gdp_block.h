@@ -14,7 +14,8 @@
  * gdp_status before any launch with the reason in gdp_last_error(), and GDP_DEV_ERR_* bits are OR-ed into
  * *device_status for what only the device can see.  Strides are in elements; the innermost dimension is
  * contiguous.  T is below 2^31.  Any alignment of the elements' own size is served; 16-byte aligned bases and strides
- * take the fast paths.  Outputs must not overlap inputs unless said.  Results do not depend on scheduling: every value
+ * take the fast paths.  Outputs must not overlap inputs or one another unless said: of the tensors of T rows, an overlap
+ * is GDP_ERR_ALIAS (the gaps between a strided tensor's rows are not its own).  Results do not depend on scheduling: every value
  * is formed by the same operations in the same order.
  *
  * Packed sequences and state modes are those of gdp_linear_recurrence: cu_seqlens that do not ascend from 0 to

@@ -175,3 +175,27 @@ def test_residual_norm_from_two_threads(cuda_device):
         _from_two_threads([c[k] for c in calls], 20000)
     for got, w in zip(outs, want):
         _same(got, w)
+
+
+# ---- outputs between strided rows --------------------------------------------------------------------
+
+def test_outputs_in_the_gaps_of_strided_rows(cuda_device):
+    """An output may lie where a strided input has a gap: no byte is shared, and the call is served."""
+    dev, T, C = cuda_device, 3, 8
+    room = _rand((2, 400), 1).to(dev)
+    x, z = (r[:T * 100].view(T, 100)[:, 4:4 + C] for r in room)
+    gap = lambda r: r[20:20 + T * C].view(T, C)  # noqa: E731
+    B, w, cu = _rand((T, 4), 2).to(dev), _rand((C, 3), 3).to(dev), _cu([T], dev)
+    A, ones = -torch.rand((C, 4), device=dev), torch.ones(C, device=dev)
+    for call in (lambda **k: pkg.short_convolution(x, w, cu, **k), lambda **k: pkg.short_convolution_decode(x, w, **k),
+                 lambda **k: pkg.selective_scan(x, x, A, B, B, cu, z=z, **k), lambda **k: pkg.selective_scan_decode(x, x, A, B, B, z=z, **k),
+                 lambda **k: pkg.residual_norm(x, z, ones, ones, z, **k)[0]):
+        want = call()
+        assert torch.equal(call(output=gap(room[0])), want) and torch.equal(call(output=gap(room[1])), want)
+        for out in (x, z):  # (one row further: an input's)
+            with pytest.raises(pkg.GdpError):
+                call(output=out.as_strided((T, C), (C, 1)))
+            if out is x and "convolution" in str(call.__code__.co_names):
+                break
+    r = pkg.residual_norm(x, z, ones, output_residual=gap(room[0]))[1]
+    assert torch.equal(r, x + z)
