@@ -155,8 +155,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
               span[c] += e;
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
-                const float2 x = mul2(both(e), A[c][q]);
-                back[c][q] = real(mul2(make_float2(ex2(x.x), ex2(x.y)), fma2(both(c ? gd.y : gd.x), Cv[q], back[c][q])), q);
+                back[c][q] = real(mul2(decay2(e, A[c][q]), fma2(both(c ? gd.y : gd.x), Cv[q], back[c][q])), q);
               }
             }
           }
@@ -182,8 +181,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
             for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
-                const float2 x = mul2(both(c ? d.z : d.x), A[c][q]);
-                decay[c][q] = make_float2(ex2(x.x), ex2(x.y));
+                decay[c][q] = decay2(c ? d.z : d.x, A[c][q]);
                 h[c][q] = real(fma2(decay[c][q], h[c][q], mul2(both(c ? d.w : d.y), Bv[q])), q);
               }
           };

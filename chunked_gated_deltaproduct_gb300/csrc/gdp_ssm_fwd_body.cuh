@@ -120,8 +120,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, CPT == 1 ? 1 : k
         float2 sum;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const float2 t = mul2(both(in.d[k].x), A[k][q]);
-          h[k][q] = fma2(make_float2(ex2(t.x), ex2(t.y)), h[k][q], mul2(both(in.d[k].y), Bv[q]));
+          h[k][q] = fma2(decay2(in.d[k].x, A[k][q]), h[k][q], mul2(both(in.d[k].y), Bv[q]));
           if (!FULL) {  // padded states stay zero, whatever the input and the decay are (infinite ones too)
             h[k][q].x = 2 * q < states ? h[k][q].x : 0.f;
             h[k][q].y = 2 * q + 1 < states ? h[k][q].y : 0.f;
@@ -452,7 +451,7 @@ __global__ void __launch_bounds__(kSsmThreads) gdp_ssm_step_kernel(const SsmProb
 #pragma unroll
     for (int k = 0; k < kQ; ++k)
       if (k < at.n) {
-        h[u][k] = fmaf(ex2(e * A[k]), h[u][k], ex * B[u][k]);
+        h[u][k] = fmaf(decay(e, A[k]), h[u][k], ex * B[u][k]);
         y[u] = fmaf(Cm[u][k], h[u][k], y[u]);
       }
     if (dst[u]) store_states(dst[u], at.n, p.quad_states, h[u]);

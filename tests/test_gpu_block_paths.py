@@ -60,6 +60,44 @@ def test_large_negative_steps(cuda_device, lengths, C, S):
     check(fin, *want["final"], "state after the step")
 
 
+# ---- decays ------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("k", range(-14, -2))
+def test_decays_next_to_one(cuda_device, k):
+    """What a state forgets per token has next to no bias: the error of long memory is that times the tokens.  (The hardware's
+    exponential alone is low by up to 0.44 2^-24 here; 0.3 is left, and the mean over 32768 states of 90 tokens' other
+    roundings, each below 2^-24, is below 3 2^-24 / sqrt(90 x 32768) a token.)"""
+    dev, N, n, C, S = cuda_device, 64, 90, 32, 16
+    T, g = N * n, torch.Generator().manual_seed(k + 100)
+    dt = 2.0 ** k * math.log(2) * (1 + torch.rand((T, C), generator=g))  # exponents in base 2 from -2^(k + 1) to -2^k
+    A, h0 = -torch.ones(C, S), 1 + torch.rand((N, C, S), generator=g)
+    zero, cu = torch.zeros((T, C), device=dev), _cu([n] * N, dev)
+    rows = torch.zeros((T, S), device=dev)
+    fin = pkg.selective_scan(zero, dt.to(dev), A.to(dev), rows, rows, cu, dt_softplus=False, initial_state=h0.to(dev), output_final_state=True)[1]
+    want = h0.double() * torch.exp(-dt.double().view(N, n, C).sum(1))[..., None]
+    bias = float((fin.cpu().double() / want - 1).mean()) / n * 2 ** 24
+    assert abs(bias) <= 0.3 + 0.01, bias
+    step = pkg.selective_scan_decode(zero, dt.to(dev), A.to(dev), rows, rows, dt_softplus=False, initial_state=torch.ones((T, C, S), device=dev),
+                                     output_final_state=True)[1]
+    bias = float((step.cpu().double() / torch.exp(-dt.double())[..., None] - 1).mean()) * 2 ** 24
+    assert abs(bias) <= 0.3 + 0.01, bias
+
+
+@pytest.mark.parametrize("S", [5, 16])
+def test_a_step_of_zero_keeps_the_state(cuda_device, S):
+    """To the bit: a step of zero (softplus of the lowest value, too) takes nothing in and forgets nothing."""
+    dev, C, lengths = cuda_device, 24, [70, 0, 33]
+    b, cu = Block(103, C, S, 3, dev, F32), _cu(lengths, dev)
+    for dt, softplus in ((torch.zeros_like(b.dt), False), (torch.full_like(b.dt, torch.finfo(F32).min), True)):
+        y, fin, kept = pkg.selective_scan(b.x, dt, b.A, b.B, b.Cm, cu, dt_softplus=softplus, initial_state=b.h0, output_final_state=True, save_states=True)
+        assert torch.equal(fin, b.h0)
+        d = pkg.selective_scan_backward(b.x, dt, b.A, b.B, b.Cm, torch.zeros_like(b.x), cu, kept, dt_softplus=softplus, d_final_state=b.h0,
+                                        output_d_initial_state=True)
+        assert torch.equal(d["d_initial_state"], b.h0)
+        step = pkg.selective_scan_decode(b.x[:3], dt[:3], b.A, b.B[:3], b.Cm[:3], dt_softplus=softplus, initial_state=b.h0, output_final_state=True)[1]
+        assert torch.equal(step, b.h0)
+
+
 # ---- the gate's slope --------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("C", [64, 61, 520])
