@@ -237,3 +237,254 @@ def test_outputs_in_the_gaps_of_strided_rows(cuda_device):
                 break
     r = pkg.residual_norm(x, z, ones, output_residual=gap(room[0]))[1]
     assert torch.equal(r, x + z)
+
+
+# ---- one token, two sequences a CTA ------------------------------------------------------------------
+# sequences, channels, states, groups, x's type, dt's type, layout: 16 CTAs per SM and more, odd numbers of sequences
+STEPS = [(21, 4096, 16, 1, BF16, BF16, "dense"), (39, 2048, 16, 1, F32, F32, "slice"), (23, 2048, 64, 2, F16, F32, "dense"),
+         (41, 2048, 18, 1, BF16, F32, "odd"), (153, 1000, 5, 2, F16, F16, "odd"), (512, 200, 16, 1, BF16, BF16, "dense"),
+         (2433, 24, 8, 1, BF16, BF16, "dense")]
+
+
+@pytest.mark.parametrize("N,C,S,G,xt,dtt,layout", STEPS)
+def test_steps_of_many_sequences(cuda_device, N, C, S, G, xt, dtt, layout):
+    dev = cuda_device
+    assert N * _tiles(C, S, G) >= 16 * _sms(dev)
+    x, z, dt = _rand((N, C), 1, xt), _rand((N, C), 2, xt), _rand((N, C), 3, dtt, 0.5)
+    A, B, Cm = -torch.exp(_rand((C, S), 4)), _rand((N, G, S), 5, xt), _rand((N, G, S), 6, xt)
+    D, bias, init = _rand((C,), 7), _rand((C,), 8) - 2.0, _rand((N, C, S), 9)
+    lay = lambda t: _as_laid_out(t, layout, dev)  # noqa: E731
+    ins = (lay(x), lay(dt), A.to(dev), lay(B), lay(Cm))
+    how = {"D": D.to(dev), "z": lay(z), "dt_bias": bias.to(dev)}
+    want = R.scan(x, dt, A, B, Cm, [1] * N, D=D, z=z, dt_bias=bias, init=init)
+    y, fin = pkg.selective_scan_decode(*ins, initial_state=init.to(dev), output_final_state=True, **how)
+    check(y, *want["y"], "y")
+    check(fin, *want["final"], "final state")
+    # the cache: slots in another order, one that nobody has, entries of padding, one outside
+    order = torch.randperm(N + 1, generator=torch.Generator().manual_seed(10))[:N].to(torch.int32)
+    off = list(range(3, N, 7)) + [N - 1]
+    cache = torch.empty((N + 1, C, S)).fill_(3.0)
+    cache[order.long()] = init
+    order[off] = -1
+    order[off[0]] = N + 1
+    state, status = cache.to(dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    got = pkg.selective_scan_decode(*ins, state=state, state_indices=order.to(dev), device_status=status, **how)
+    assert int(status) == pkg.GDP_DEV_ERR_SLOT
+    live = [i for i in range(N) if i not in off]
+    assert torch.equal(got[live], y[live]) and torch.equal(state[order[live].long()], fin[live])
+    rest = sorted(set(range(N + 1)) - set(order[live].tolist()))
+    assert torch.equal(state[rest].cpu(), cache[rest])
+    zero = R.scan(*(t[off] if t.shape[0] == N else t for t in (x, dt, A, B, Cm)), [1] * len(off), D=D, z=z[off], dt_bias=bias)
+    check(got[off], *zero["y"], "padding entries")
+
+
+# ---- several sequences per CTA, and the longest first ------------------------------------------------
+
+def _mixed(n, most, seed):
+    """n lengths, short ones in the main, some of them zero, one of `most`."""
+    g = torch.Generator().manual_seed(seed)
+    lengths = torch.randint(0, max(2, most // 8), (n,), generator=g).tolist()
+    lengths[n // 3], lengths[n // 2], lengths[-1] = most, 0, 0
+    return lengths
+
+
+# lengths, channels, states, groups, x's type, dt's type, gated, workers' loops, ranked
+MANY = [
+    (_mixed(90, 30, 1), 2080, 16, 1, BF16, BF16, True, True, False), (_mixed(90, 41, 2), 130, 33, 65, F16, F32, False, True, False),
+    (_mixed(40, 600, 3), 130, 5, 130, F32, F32, True, True, True), (_mixed(12, 200, 4), 832, 16, 1, BF16, F32, True, False, True),
+    (_mixed(200, 60, 5), 96, 64, 8, F32, F32, True, True, False), ([700, 3] * 20, 130, 20, 130, BF16, BF16, True, True, True),
+]
+
+
+@pytest.mark.parametrize("lengths,C,S,G,xt,dtt,gated,loops,ranked", MANY)
+def test_many_sequences(cuda_device, lengths, C, S, G, xt, dtt, gated, loops, ranked):
+    """More sequences than the backward pass has CTAs for, so that each takes several in turn, and sequences that are run by
+    length, against the reference, with rows behind the last one."""
+    dev, N, T, sms = cuda_device, len(lengths), sum(lengths), _sms(cuda_device)
+    tiles, rows = _tiles(C, S, G), sum(lengths) + 5
+    assert loops == (N > -(-16 * sms // tiles)) and ranked == (rows >= N * N and N * tiles > 2 * sms)
+    assert pkg.gdp_scan_forward_workspace_bytes(rows, N, C, S, G) == 0
+    start = torch.exp(_rand((C,), 20) - 3.0)
+    x, z, dy, dt = _rand((T, C), 1, xt), _rand((T, C), 2, xt), _rand((T, C), 3, xt), _rand((T, C), 4, dtt, 0.5)
+    A, B, Cm = -torch.exp(_rand((C, S), 5)) * 2.0, _rand((T, G, S), 6, xt), _rand((T, G, S), 7, xt)
+    D, bias, h0, dfin = _rand((C,), 8), torch.log(torch.expm1(start)), _rand((N, C, S), 9), _rand((N, C, S), 10)
+    z = z if gated else None
+
+    def padded(t):
+        return None if t is None else torch.cat([t, torch.full((5, *t.shape[1:]), math.nan, dtype=t.dtype)]).to(dev)
+
+    ins, how = (padded(x), padded(dt), A.to(dev), padded(B), padded(Cm)), {"D": D.to(dev), "z": padded(z), "dt_bias": bias.to(dev)}
+    cu = _cu(lengths, dev)
+    y, fin, kept = pkg.selective_scan(*ins, cu, initial_state=h0.to(dev), output_final_state=True, save_states=True, **how)
+    want = R.scan(x, dt, A, B, Cm, lengths, D=D, z=z, dt_bias=bias, init=h0)
+    check(y[:T], *want["y"], "y")
+    check(fin, *want["final"], "final state")
+    got = pkg.selective_scan_backward(*ins, padded(dy), cu, kept, d_final_state=dfin.to(dev), output_d_initial_state=True, **how)
+    for name in ("dx", "ddt", "dB", "dC") + (("dz",) if gated else ()):
+        assert not got[name][T:].any(), name
+        got[name] = got[name][:T]
+    assert not y[T:].any()
+    _close(got, R.scan_backward(x, dt, A, B, Cm, dy, lengths, D=D, z=z, dt_bias=bias, init=h0, dfin=dfin))
+
+
+# ---- the convolution's long runs ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("C,W,dtype,bias", [(1024, 4, BF16, True), (127, 3, F16, False), (512, 2, F32, True), (254, 4, BF16, False)])
+def test_convolution_of_many_rows(cuda_device, C, W, dtype, bias):
+    """Rows enough for 64 a thread, bounds on and off the runs' borders; some channels against the reference (channels do not
+    mix), rows behind the last sequence."""
+    dev = cuda_device
+    lengths = [1, 63, 64, 65, 0, 2, 127, 128, 129, 3, 0, 4093, 1, 1, 1, 30000, 61, 60003]
+    T, N = sum(lengths), len(lengths)
+    vecs = C // 8 if C % 8 == 0 and dtype != F32 else C // 4 if C % 4 == 0 and dtype == F32 else C // 2 if C % 2 == 0 else C
+    assert vecs in (127, 128) and T >= 64 * 8 * _sms(dev)  # (128 vectors of channels a CTA, one run of rows)
+    g = torch.Generator(dev).manual_seed(1)
+    x, dy = (torch.randn((T + 70, C), generator=g, device=dev).to(dtype) for _ in range(2))
+    x[T:], dy[T:] = math.nan, math.nan
+    w, b = _rand((C, W), 2, sigma=0.5), _rand((C,), 3) if bias else None
+    s0, dfin = _rand((N, W - 1, C), 4, dtype), _rand((N, W - 1, C), 5, dtype)
+    gw, gb, gs0, gdfin = _on(dev, w, b, s0, dfin)
+    cu = _cu(lengths, dev)
+    y, fin = pkg.short_convolution(x, gw, cu, gb, initial_state=gs0, output_final_state=True)
+    got = pkg.short_convolution_backward(x, gw, dy, cu, gb, initial_state=gs0, d_final_state=gdfin)
+    at = torch.tensor([0, 1, 7, C // 2, C - 2, C - 1])
+    part = lambda t: t[..., at.to(t.device)].cpu()  # noqa: E731
+    args = (part(x[:T]), w[at]), dict(b=None if b is None else b[at], init=s0[..., at])
+    want, err, wfin = R.convolution(*args[0], lengths, act="silu", **args[1])
+    check(part(y[:T]), want, err, "y")
+    assert torch.equal(part(fin).double(), wfin) and not y[T:].any() and bool(torch.isfinite(y).all())
+    back = R.convolution_backward(*args[0], part(dy[:T]), lengths, act="silu", dfin=dfin[..., at], **args[1])
+    check(part(got["dx"][:T]), *back["dx"], "dx")
+    assert not got["dx"][T:].any() and all(bool(torch.isfinite(v).all()) for v in got.values() if v is not None)
+    check(got["dweight"][at.to(dev)], *back["dweight"], "dweight")
+    if bias:
+        check(part(got["dbias"]), *back["dbias"], "dbias")
+    check(part(got["d_initial_state"]), *back["d_initial_state"], "d_initial_state")
+
+
+# ---- pieces ------------------------------------------------------------------------------------------
+
+PIECES = [([1200], 40), ([129, 127, 128, 640], 40)]
+
+
+def _in_pieces(lengths, C, S=16):
+    """Both passes run these sequences in pieces: they need what joins them beside the sums that whole sequences need."""
+    T, N = sum(lengths), len(lengths)
+    lanes = {16: 4}[S]
+    sums = -(-N * 4 * (-(-C * (S + 2) // 4) * 4) // 256) * 256
+    whole = sums + _tiles(C, S, 1) * T * 8 * 4 * lanes
+    return pkg.gdp_scan_forward_workspace_bytes(T, N, C, S) > 0 and pkg.gdp_scan_workspace_bytes(T, N, C, S) > whole + N * C * S * 4
+
+
+@pytest.mark.parametrize("lengths,C", PIECES)
+def test_pieces_captured_and_replayed(cuda_device, lengths, C):
+    """Two graphs of all calls, pieces among them, replayed in turn with other inputs in the same buffers."""
+    dev = cuda_device
+    assert _in_pieces(lengths, C)
+    cu, b, other = _cu(lengths, dev), *(Block(sum(lengths), C, 16, len(lengths), dev, seed=s) for s in (0, 100))
+    want_other, want = other.everything(cu), b.everything(cu)
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(b.everything(cu))
+        graphs.append(g)
+    for g in graphs:
+        g.replay()
+    for o in outs:
+        _same(o, want)
+    for k, v in vars(other).items():
+        getattr(b, k).copy_(v)
+    for g in (*graphs, graphs[0]):
+        g.replay()
+    for o in outs:
+        _same(o, want_other)
+
+
+@pytest.mark.parametrize("lengths,C", PIECES)
+def test_pieces_on_a_given_stream(cuda_device, lengths, C):
+    dev = cuda_device
+    assert _in_pieces(lengths, C)
+    b, cu = Block(sum(lengths), C, 16, len(lengths), dev), _cu(lengths, dev)
+    y, fin, kept = b.scan(cu, initial_state=b.h0, output_final_state=True, save_states=True)
+    want = {"y": y, "fin": fin, **b.scan_backward(cu, kept, d_final_state=b.h0, output_d_initial_state=True)}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # the side stream is busy for a while
+    h = side.cuda_stream
+    y, fin, kept = b.scan(cu, initial_state=b.h0, output_final_state=True, save_states=True, stream=h)
+    got = {"y": y, "fin": fin, **b.scan_backward(cu, kept, d_final_state=b.h0, output_d_initial_state=True, stream=h)}
+    assert not side.query()
+    side.synchronize()
+    _same(got, want)
+
+
+@pytest.mark.parametrize("lengths,C", PIECES)
+def test_pieces_in_given_workspaces(cuda_device, lengths, C):
+    """Workspaces of the stated size, with anything in them; a byte less, or off 256 bytes, is refused."""
+    dev, T, N = cuda_device, sum(lengths), len(lengths)
+    assert _in_pieces(lengths, C)
+    b, cu = Block(T, C, 16, N, dev), _cu(lengths, dev)
+    kept = b.scan(cu, initial_state=b.h0, save_states=True)[1]
+
+    def forward(**k):
+        y, fin, states = b.scan(cu, initial_state=b.h0, output_final_state=True, save_states=True, **k)
+        rows = torch.cat([torch.arange(-(-n // 16)) + sum(lengths[:i]) // 16 + i for i, n in enumerate(lengths)])
+        return {"y": y, "fin": fin, "states": states[rows.to(dev)]}
+
+    def backward(**k):
+        return b.scan_backward(cu, kept, d_final_state=b.h0, output_d_initial_state=True, **k)
+
+    for need, call in ((pkg.gdp_scan_forward_workspace_bytes(T, N, C, 16), forward), (pkg.gdp_scan_workspace_bytes(T, N, C, 16), backward)):
+        assert need > 0
+        want = call()
+        for stale in (255, 127, 0):  # NaN, large and zero values
+            room = torch.full((need + 512,), stale, dtype=torch.uint8, device=dev)
+            _same(call(workspace=room[:need]), want)
+            assert bool((room[need:] == stale).all())
+        with pytest.raises(pkg.GdpError):
+            call(workspace=room[:need - 1])
+        with pytest.raises(pkg.GdpError):
+            call(workspace=room[16:16 + need])
+
+
+def test_pieces_on_two_streams_at_once(cuda_device):
+    """Both streams run pieces, each in workspaces of its own, beside one another."""
+    dev = cuda_device
+    assert all(_in_pieces(*p) for p in PIECES)
+    blocks = [Block(sum(n), c, 16, len(n), dev, seed=i) for i, (n, c) in enumerate(PIECES)]
+    cus = [_cu(n, dev) for n, _ in PIECES]
+    alone = [b.everything(cu) for b, cu in zip(blocks, cus)]
+    streams = [torch.cuda.Stream(dev) for _ in blocks]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        got = []
+        for b, cu, s in zip(blocks, cus, streams):
+            with torch.cuda.stream(s):
+                got.append(b.everything(cu))
+        torch.cuda.synchronize()
+        for mine, want in zip(got, alone):
+            _same(mine, want)
+
+
+def test_pieces_from_two_threads(cuda_device):
+    """The scan in pieces and a wide one that is not, forward and backward, from two host threads at once."""
+    dev = cuda_device
+    blocks = [(Block(1200, 40, 16, 1, dev), _cu([1200], dev)), (Block(230, 2200, 16, 3, dev), _cu([30, 0, 200], dev))]
+    got = [None, None]
+
+    def one(i):
+        b, cu = blocks[i]
+        y, kept = b.scan(cu, save_states=True)
+        return {"y": y, **b.scan_backward(cu, kept)}
+
+    def call(i):
+        def work():
+            got[i] = one(i)
+        return work
+
+    want = [one(0), one(1)]
+    _from_two_threads([call(0), call(1)], 200)
+    for g, w in zip(got, want):
+        _same(g, w)
