@@ -15,7 +15,6 @@ struct ResProblem {
   float eps, inv_c;
   int act, res_f32;
   int quad_cols;  // weights on 16-byte boundaries
-  int keep;       // backward: weights are held in shared memory
   int depth;      // rows that a thread has places for in shared memory
   // backward (res is the forward's residual_out)
   const void *dy, *dr;

@@ -128,7 +128,7 @@ __device__ __forceinline__ Eight load_columns(const float *at, int thread, int t
 }
 
 // ---- rows on their way ----
-// `depth` places per thread, so that depth - 1 rows are under way (depth 1: the row itself, waited for).  A place is some
+// `depth` places per thread, three or two, so that depth - 1 rows are under way.  A place is some
 // pieces of 16 bytes, a CTA's threads side by side in each.
 struct RowPlaces {
   unsigned char *own;
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(MOST) gdp_res_fwd_kernel(const ResProblem p) {
     }
   };
   float norm[RW];  // the block's sums
-  const bool merged = MERGED && p.post && p.depth > 1;
+  const bool merged = MERGED && p.post;
   int place = 0;
   if (merged) {
     places.wait();
@@ -303,9 +303,8 @@ __global__ void __launch_bounds__(MOST) gdp_res_fwd_kernel(const ResProblem p) {
 #pragma unroll
     for (int i = 0; i < RW; ++i) m[i] = r[i] = g[i] = eight_of(0.f);
     if constexpr (VEC) {
-      if (p.depth == 1) ask(t, 0);
       if (!merged) places.wait();
-      if (p.depth > 1) ask(t + (p.depth - 1) * RW * step, place == 0 ? p.depth - 1 : place - 1);
+      ask(t + (p.depth - 1) * RW * step, place == 0 ? p.depth - 1 : place - 1);
 #pragma unroll
       for (int i = 0; i < RW; ++i)
         if (mine && t + i * step < T_) {
@@ -382,7 +381,7 @@ __global__ void __launch_bounds__(MOST, MOST == 128 ? kResResident / MOST : 1) g
   unsigned char *kept = smem + p.depth * places.place;
   const RowPlaces columns(kept, 6, 1);
   auto column = [&](int k) { return columns.get<float>(0, 2 * k); };
-  if (p.keep) {
+  if constexpr (VEC) {
     auto put = [&](int k, const Eight &e) {
       float4 *a = reinterpret_cast<float4 *>(columns.own + 2 * k * columns.piece), *b = reinterpret_cast<float4 *>(columns.own + (2 * k + 1) * columns.piece);
       *a = make_float4(e.v[0].x, e.v[0].y, e.v[1].x, e.v[1].y);
@@ -393,7 +392,7 @@ __global__ void __launch_bounds__(MOST, MOST == 128 ? kResResident / MOST : 1) g
     put(2, load_columns<VEC>(p.scale, thread, threads, C, 1.f, p.quad_cols));
   }
   auto weights = [&](int k, const float *from, float other) {
-    return p.keep ? column(k) : load_columns<VEC>(from, thread, threads, C, other, p.quad_cols);
+    return VEC ? column(k) : load_columns<VEC>(from, thread, threads, C, other, p.quad_cols);
   };
   // (unsigned: the row behind the last ones may be past 2^31)
   const uint32_t first = blockIdx.x / CL * blockDim.y + threadIdx.y, step = gridDim.x / CL * blockDim.y, T_ = (uint32_t)p.T;
@@ -423,7 +422,7 @@ __global__ void __launch_bounds__(MOST, MOST == 128 ? kResResident / MOST : 1) g
   };
   int place = 0;
   float s[2] = {0.f, 0.f};
-  if (MERGED && p.depth > 1) {
+  if constexpr (MERGED) {
     places.wait();
     if (first < T_) squares(0, s);
     sums.over(s);
@@ -433,9 +432,8 @@ __global__ void __launch_bounds__(MOST, MOST == 128 ? kResResident / MOST : 1) g
     Eight n = eight_of(0.f), m = n, d = n, g = n, up = n;
     const int after = place + 1 == p.depth ? 0 : place + 1;
     if constexpr (VEC) {
-      if (p.depth == 1) ask(t, 0);
-      if (!MERGED || p.depth == 1) places.wait();
-      if (p.depth > 1) ask(t + (p.depth - 1) * step, place == 0 ? p.depth - 1 : place - 1);
+      if (!MERGED) places.wait();
+      ask(t + (p.depth - 1) * step, place == 0 ? p.depth - 1 : place - 1);
       if (mine) {
         d = places.get<T>(place, 0);
         m = places.get<T>(place, PB);
@@ -452,7 +450,7 @@ __global__ void __launch_bounds__(MOST, MOST == 128 ? kResResident / MOST : 1) g
     // to the first norm's values m is d_r k with k = scale act(gate) post.  Its own mean(d_r k m) is linear in the other
     // mean, so that one pass over the row gives both:  mean((r d w + up) k m) - r mean(d w n) mean(n k m).
     const Eight w = weights(0, p.w, 0.f);
-    if (!MERGED || p.depth == 1) {
+    if (!MERGED) {
       s[0] = dot(n, n);
       s[1] = dot(m, m);
     }
@@ -460,7 +458,7 @@ __global__ void __launch_bounds__(MOST, MOST == 128 ? kResResident / MOST : 1) g
       if (p.gate) g = places.get<T>(place, 2 * PB + PR);
       if (p.dr) up = places.get<TR>(place, dr_at);
     }
-    if (!MERGED || p.depth == 1) sums.over(s);
+    if (!MERGED) sums.over(s);
     const float r = rsqrtf(fmaf(s[0], p.inv_c, p.eps)), q = p.post ? rsqrtf(fmaf(s[1], p.inv_c, p.eps)) : 1.f;
     n = n * r;
     m = m * q;
@@ -478,10 +476,8 @@ __global__ void __launch_bounds__(MOST, MOST == 128 ? kResResident / MOST : 1) g
       means[2] = dot(n, ku);
     }
     if constexpr (MERGED) {
-      if (p.depth > 1) {
-        places.wait();
-        if (t + step < T_) squares(after, means + 3);
-      }
+      places.wait();
+      if (t + step < T_) squares(after, means + 3);
       sums.over(means);
       s[0] = means[3];
       s[1] = means[4];
@@ -547,10 +543,11 @@ __global__ void __launch_bounds__(MOST, MOST == 128 ? kResResident / MOST : 1) g
 
 constexpr int kResShared = 226 * 1024;  // shared memory of an SM that CTAs' rows, weights and sums may take
 constexpr int kResBeside = 2048;  // shared memory of a CTA besides its rows: the sums' buffers, and 1 KB of the system's
-// Places of a row in shared memory (see RowPlaces) for `ctas` resident CTAs: three, or as many as there is room for.
+// Places of a row in shared memory (see RowPlaces) for `ctas` resident CTAs: three where there is room for them, or two, for
+// which there is at every width, type and set of tensors.
 inline int res_depth(int bytes, int ctas, int others) {
   const int room = kResShared / ctas - kResBeside - others;
-  return 3 * bytes <= room ? 3 : 2 * bytes <= room ? 2 : 1;
+  return 3 * bytes <= room ? 3 : 2;
 }
 // `rows`: CTAs or pairs of them.
 template <int CL>
@@ -614,9 +611,8 @@ cudaError_t res_bwd(ResProblem &p, int vec, int64_t parts, cudaStream_t stream) 
   const int threads = block.x * block.y, per_sm = kResResident / threads > 1 ? kResResident / threads : 1;
   const int row = threads * kRes * ((int)sizeof(T) * (p.gate ? 3 : 2) + (int)sizeof(TR) * (p.dr ? 2 : 1)), kept = threads * kRes * 3 * 4;
   p.depth = res_depth(row, per_sm, kept);
-  p.keep = vec && p.depth * row + kept <= kResShared / per_sm - kResBeside;
   const int sums = block.y > 1 ? (int)block.y * 3 * 256 * (int)sizeof(float) : 0;
-  int smem = vec ? p.depth * row + (p.keep ? kept : 0) : 0;
+  int smem = vec ? p.depth * row + kept : 0;
   if (smem < sums) smem = sums;
   return res_launch<CL>(vec ? gdp_res_bwd_kernel<T, TR, true, MOST, CL> : gdp_res_bwd_kernel<T, TR, false, MOST, CL>, p, parts, block, smem, stream);
 }
