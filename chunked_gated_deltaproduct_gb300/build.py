@@ -34,8 +34,9 @@ def nvcc() -> str:
     return cand
 
 
-# Sources without range checks: their objects are the same in both variants, so that the debug-bounds
-# build links those of the normal one.
+# Sources without the debug-bounds build's range checks: their objects are the same in both variants, so that it links those of
+# the normal one.  (Rows from cu_seqlens and slots of caches, the indices that the device holds, are held to the tensors in
+# every build there: cu_at and slot_of in gdp_block.cuh, clamp_row in gdp_rec_scan.cuh.)
 UNCHECKED = ("gdp_rec", "gdp_norm_", "gdp_group_norm", "gdp_conv", "gdp_ssm", "gdp_resnorm")
 
 

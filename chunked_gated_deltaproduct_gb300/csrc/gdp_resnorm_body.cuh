@@ -1,11 +1,10 @@
 // gdp_resnorm_body.cuh -- the residual norm's kernels, instantiated by type in gdp_resnorm_*.cu.
 //
 // A row belongs to a warp (up to 256 channels) or to a CTA (backward beyond 4096: to a pair of them); a thread holds eight
-// of its channels in registers, so that every tensor is read once and the norms cost one sum over the row each (backward:
-// three for the two).  Rows come ahead by
-// asynchronous copies into places of shared memory that are the thread's own.  Bound by memory at last (57 bytes a channel
-// and pass of a training step with an fp32 stream), but first by instructions and the sums' latency: hence paired
-// arithmetic, weights that stay in registers (forward) or shared memory (backward) instead of an L1 that the places leave
+// of its channels in registers, so that every tensor is read once and the norms cost one reduction over the row each (backward
+// too: the squares of both norms together, then the means of both).  Rows come ahead by asynchronous copies into places of
+// shared memory that are the thread's own.  Bound by memory at last (36 bytes a channel of a training step with an fp32 stream,
+// 14 forward and 22 backward), but first by instructions and the sums' latency: hence paired arithmetic, weights that stay in registers (forward) or shared memory (backward) instead of an L1 that the places leave
 // too small, and two rows side by side in the forward pass, which share their sums' barriers.
 //
 // 65536 x 4096 bf16 with gate, scale and both weights, fp32 stream: forward 728 us, 5.2 TB/s (weights by way of L1, one row at a

@@ -19,7 +19,8 @@
  * is formed by the same operations in the same order.
  *
  * Packed sequences and state modes are those of gdp_linear_recurrence: cu_seqlens that do not ascend from 0 to
- * at most T set GDP_DEV_ERR_CU_SEQLENS (outputs then undefined, nothing outside the buffers touched); an empty
+ * at most T set GDP_DEV_ERR_CU_SEQLENS (outputs then undefined, nothing outside the buffers touched; with N = 0 every row is
+ * padding and they are not read); an empty
  * sequence's final state is its incoming state; output rows at or past cu_seqlens[N] are not written, or with
  * zero_padding written as zeros; the cache `state` is read and written in place at state_indices[i] (-1: start
  * from zero, write nothing; any other value outside [0, num_slots) sets GDP_DEV_ERR_SLOT and is treated as -1; no slot

@@ -239,6 +239,53 @@ def test_outputs_in_the_gaps_of_strided_rows(cuda_device):
     assert torch.equal(r, x + z)
 
 
+# ---- nothing but padding, and long caches -------------------------------------------------------------
+
+@pytest.mark.parametrize("N,T,C", [(1, 1000, 40), (3, 1000, 40), (2, 30, 2200)])
+def test_nothing_but_padding(cuda_device, N, T, C):
+    """Empty sequences before rows that belong to none, in pieces and not: zeros, states as they came, sums of nothing."""
+    dev = cuda_device
+    assert (pkg.gdp_scan_forward_workspace_bytes(T, N, C, 16) > 0) == (C == 40)
+    b, cu = Block(T, C, 16, N, dev), _cu([0] * N, dev)
+    for t in (b.x, b.z, b.dy, b.dt, b.B, b.Cm):
+        t.fill_(math.nan)
+    y, fin = b.conv(cu, initial_state=b.c0, output_final_state=True)
+    assert not y.any() and torch.equal(fin, b.c0)
+    y, fin, kept = b.scan(cu, initial_state=b.h0, output_final_state=True, save_states=True)
+    assert not y.any() and torch.equal(fin, b.h0)
+    d = b.conv_backward(cu, initial_state=b.c0, d_final_state=b.c0)
+    assert torch.equal(d.pop("d_initial_state"), b.c0) and not any(v.any() for v in d.values())
+    d = b.scan_backward(cu, kept, d_final_state=b.h0, output_d_initial_state=True)
+    assert torch.equal(d.pop("d_initial_state"), b.h0) and not any(v.any() for v in d.values())
+
+
+def test_caches_beyond_32_bits(cuda_device):
+    """State caches of more than 2^31 elements, their last slots among those in use."""
+    dev, C, S = cuda_device, 4096, 16
+    for each, lengths in (((C, S), [40, 0, 9]), ((3, C), [5, 2, 70])):
+        elems = each[0] * each[1]
+        many = (1 << 31) // elems + 5
+        b, cu = Block(sum(lengths), C, S, 3, dev), _cu(lengths, dev)
+        cache = torch.empty((many, *each), dtype=F32 if each == (C, S) else BF16, device=dev)
+        slots = torch.tensor([many - 1, 1, many - 3], dtype=torch.int32, device=dev)
+        init = b.h0 if each == (C, S) else b.c0
+        call = b.scan if each == (C, S) else b.conv
+        cache[many - 2] = 7.0
+        cache[slots.long()] = init
+        want, fin = call(cu, initial_state=init, output_final_state=True)
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        assert torch.equal(call(cu, state=cache, state_indices=slots, device_status=status), want)
+        assert torch.equal(cache[slots.long()], fin)
+        if each == (C, S):
+            step = lambda **k: pkg.selective_scan_decode(b.x[:3], b.dt[:3], b.A, b.B[:3], b.Cm[:3], **k)  # noqa: E731
+        else:
+            step = lambda **k: pkg.short_convolution_decode(b.x[:3], b.w, b.b, **k)  # noqa: E731
+        want, fin = step(initial_state=fin, output_final_state=True)
+        assert torch.equal(step(state=cache, state_indices=slots, device_status=status), want)
+        assert torch.equal(cache[slots.long()], fin) and bool((cache[many - 2] == 7.0).all()) and int(status) == 0
+        del cache
+
+
 # ---- one token, two sequences a CTA ------------------------------------------------------------------
 # sequences, channels, states, groups, x's type, dt's type, layout: 16 CTAs per SM and more, odd numbers of sequences
 STEPS = [(21, 4096, 16, 1, BF16, BF16, "dense"), (39, 2048, 16, 1, F32, F32, "slice"), (23, 2048, 64, 2, F16, F32, "dense"),
