@@ -15,6 +15,7 @@ namespace gdp {
 namespace layer {
 
 constexpr int kConvAhead = 4; // rows that are worked on together
+constexpr int kConvSums = 64;  // rows whose products a sum of the backward pass takes in registers
 
 // Rows on their way to a thread, S tensors, kConvAhead rows a batch.  Asynchronous copies into places of shared memory
 // that are the thread's own (no barriers) keep two batches under way without registers; values below the copies' least
@@ -345,8 +346,9 @@ __device__ __forceinline__ void initial_gradient(const ConvProblem &p, int64_t i
 }
 
 // A part is a run of rows [t0, t1).  A thread walks it in order and K rows beyond, forms p again from its window of
-// inputs, and holds the unfinished input gradients of the last K rows in registers; the weights' sums over the
-// part stay in registers too and leave once.
+// inputs, and holds the unfinished input gradients of the last K rows in registers.  The weights' sums run in two steps, so that
+// their roundings grow with kConvSums rows and not with a part's (65536 x 4096, error of dweight: 5.4e-7 to 2.1e-7; the parts of
+// odd widths are four times as long): in registers, and from there into the thread's place of shared memory.
 template <typename T, int W, int V>
 __global__ void __launch_bounds__(kConvThreads) gdp_conv_bwd_kernel(const ConvProblem p) {
   constexpr int K = W - 1, N = Pairs<V>::N, A = kConvAhead;
@@ -361,8 +363,23 @@ __global__ void __launch_bounds__(kConvThreads) gdp_conv_bwd_kernel(const ConvPr
   const int64_t part = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int64_t t0 = min(part * p.part_rows, p.p.T), t1 = min(t0 + p.part_rows, p.p.T), last = min(t1 + K, p.p.T);
   Pairs<V> w[W], bias, win[K], pend[K], dw[W], db = no_pairs<V>();
+  __shared__ float2 sums[(W + 1) * N][kConvThreads];
+  float2 *own_sums = &sums[0][threadIdx.y * blockDim.x + threadIdx.x];
 #pragma unroll
   for (int j = 0; j < W; ++j) dw[j] = no_pairs<V>();
+#pragma unroll
+  for (int k = 0; k < (W + 1) * N; ++k) own_sums[k * kConvThreads] = make_float2(0.f, 0.f);
+  auto add_up = [&] {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+#pragma unroll
+      for (int r = 0; r < W; ++r) own_sums[(r * N + j) * kConvThreads] = add2(own_sums[(r * N + j) * kConvThreads], dw[r].v[j]);
+      own_sums[(W * N + j) * kConvThreads] = add2(own_sums[(W * N + j) * kConvThreads], db.v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j) dw[j] = no_pairs<V>();
+    db = no_pairs<V>();
+  };
   const T *x_at = static_cast<const T *>(p.x) + c, *dy_at = static_cast<const T *>(p.dy) + c;
   T *dx_at = static_cast<T *>(p.dx) + c;
   if (t0 < t1) {
@@ -435,35 +452,38 @@ __global__ void __launch_bounds__(kConvThreads) gdp_conv_bwd_kernel(const ConvPr
     };
     T *before = dx_at + (t0 - K) * p.C;  // (written where it is a row of the part)
     int at = 0;
-    for (int64_t t = t0; t < last && !done; t += A, before += A * p.C, at = at == 2 ? 0 : at + 1) {
-      queue.wait();
-      ask(at + Queue::DEEP < 3 ? at + Queue::DEEP : at + Queue::DEEP - 3);
-      if (!fresh && t - K >= max(t0, b) && t + A <= min(e, t1)) {  // all of one sequence and the part
+    for (int64_t t = t0, stop; t < last && !done; add_up()) {
+      stop = min(t + kConvSums, last);
+      for (; t < stop && !done; t += A, before += A * p.C, at = at == 2 ? 0 : at + 1) {
+        queue.wait();
+        ask(at + Queue::DEEP < 3 ? at + Queue::DEEP : at + Queue::DEEP - 3);
+        if (!fresh && t - K >= max(t0, b) && t + A <= min(e, t1)) {  // all of one sequence and the part
 #pragma unroll
-        for (int k = 0; k < A; ++k) one(before + k * p.C, queue.get(at, 0, k), queue.get(at, 1, k), true, true);
-      } else {
+          for (int k = 0; k < A; ++k) one(before + k * p.C, queue.get(at, 0, k), queue.get(at, 1, k), true, true);
+        } else {
 #pragma unroll
-        for (int k = 0; k < A; ++k) {
-          const int64_t row = t + k;
-          if (row >= last || done) break;
-          if (row >= e) {
-            if (!fresh) flush(row);
-            fresh = true;
-            if (row >= t1) {
-              done = true;
-              break;
+          for (int k = 0; k < A; ++k) {
+            const int64_t row = t + k;
+            if (row >= last || done) break;
+            if (row >= e) {
+              if (!fresh) flush(row);
+              fresh = true;
+              if (row >= t1) {
+                done = true;
+                break;
+              }
+              while (row >= e && i + 1 < p.p.N) {
+                ++i;
+                seq_rows(p.p, i, &b, &e);
+              }
             }
-            while (row >= e && i + 1 < p.p.N) {
-              ++i;
-              seq_rows(p.p, i, &b, &e);
+            if (row >= e || row < b) {
+              if (row < t1) store_pairs<T, V>(dx_at + row * p.C, no_pairs<V>());
+              continue;
             }
+            if (fresh) enter(row);
+            one(before + k * p.C, queue.get(at, 0, k), queue.get(at, 1, k), row < t1, row - K >= b && row - K >= t0);
           }
-          if (row >= e || row < b) {
-            if (row < t1) store_pairs<T, V>(dx_at + row * p.C, no_pairs<V>());
-            continue;
-          }
-          if (fresh) enter(row);
-          one(before + k * p.C, queue.get(at, 0, k), queue.get(at, 1, k), row < t1, row - K >= b && row - K >= t0);
         }
       }
     }
@@ -473,11 +493,12 @@ __global__ void __launch_bounds__(kConvThreads) gdp_conv_bwd_kernel(const ConvPr
   }
   float *to = p.partial + part * (W + 1) * p.C + c;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
+  for (int r = 0; r <= W; ++r)
 #pragma unroll
-    for (int r = 0; r < W; ++r) to[r * p.C + j] = j % 2 ? dw[r].v[j / 2].y : dw[r].v[j / 2].x;
-    to[W * p.C + j] = j % 2 ? db.v[j / 2].y : db.v[j / 2].x;
-  }
+    for (int j = 0; j < V; ++j) {
+      const float2 v = own_sums[(r * N + j / 2) * kConvThreads];
+      to[r * p.C + j] = j % 2 ? v.y : v.x;
+    }
 }
 
 template <typename T, int V>

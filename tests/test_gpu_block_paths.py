@@ -535,3 +535,25 @@ def test_pieces_from_two_threads(cuda_device):
     _from_two_threads([call(0), call(1)], 200)
     for g, w in zip(got, want):
         _same(g, w)
+
+
+# ---- sums over many rows -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("C", [1025, 4095, 4096])
+def test_convolution_sums_of_many_rows(cuda_device, C):
+    """The weights' gradients are sums of exact products over all rows (no activation).  A running sum of n random terms is off by
+    2^-24 sqrt(n / 6) of its size (a rounding's root mean square is 2^-24 / sqrt(3) of what the sum is by then); here 64 rows' are
+    summed, these sums over a part, and P parts' by 32 warps and then over the warps.  (One running sum over a part: 2.7e-7 and
+    5.6e-7 at the odd widths.)"""
+    dev, T = cuda_device, 65536
+    g = torch.Generator(dev).manual_seed(1)
+    x, dy = (torch.randn((T, C), generator=g, device=dev).bfloat16() for _ in range(2))
+    w, b, cu = _rand((C, 4), 2).to(dev), _rand((C,), 3).to(dev), _cu([T], dev)
+    got = pkg.short_convolution_backward(x, w, dy, cu, b, None)
+    xd, dyd = x.double(), dy.double()
+    want = torch.stack([(dyd[3 - j:] * xd[:T - 3 + j]).sum(0) for j in range(4)], 1)
+    parts = 4 * _sms(dev) // -(-(C // 4 if C % 4 == 0 else C) // 128)  # CTAs of 128 vectors of channels, four per SM
+    bound = R.U * math.sqrt((64 + T / parts / 64 + parts / 32 + 32) / 6)
+    for name, ref in (("dweight", want), ("dbias", dyd.sum(0))):
+        error = float((got[name].double() - ref).norm() / ref.norm())
+        assert error <= bound, (name, error, bound)
