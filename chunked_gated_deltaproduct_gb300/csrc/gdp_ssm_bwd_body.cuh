@@ -328,7 +328,14 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
   constexpr int STEP = HT / CP, ITEMS = (K + STEP - 1) / STEP;
   const float bias[2] = {p.bias && c < cn ? p.bias[c0 + c] : 0.f, p.bias && c + 1 < cn ? p.bias[c0 + c + 1] : 0.f};
   const float2 D = make_float2(p.D && c < cn ? p.D[c0 + c] : 0.f, p.D && c + 1 < cn ? p.D[c0 + c + 1] : 0.f);
-  float2 dD = make_float2(0.f, 0.f), dbias = make_float2(0.f, 0.f);
+  // sums over the worker's rows, in two steps: over kSums chunks' and then these (their roundings grow with the shorter of the two)
+  constexpr int kSums = 16;
+  float2 dD = make_float2(0.f, 0.f), dbias = make_float2(0.f, 0.f), total_D = dD, total_bias = dD;
+  auto add_up = [&] {
+    total_D = add2(total_D, dD);
+    total_bias = add2(total_bias, dbias);
+    dD = dbias = make_float2(0.f, 0.f);
+  };
   for (int64_t r = worker; r < p.pieces; r += p.workers) {
     const SsmPiece at_rows(p, row_of(r));
     if (p.piece && (at_rows.b >= at_rows.e || (LOCAL && at_rows.first))) continue;
@@ -496,15 +503,17 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
       if (!LOCAL) finish(k, 1);
       meet(false);
       if (k + 1 < chunks) form(k + 1);
+      if (!LOCAL && k % kSums == kSums - 1) add_up();
       __syncthreads();
     }
     if (!LOCAL && chunks > 0) finish(chunks - 1, 0);
+    if (!LOCAL) add_up();
     meet(true);  // before the stages are used again
   }
   if (LOCAL) return;
   // dD and ddt_bias: a channel's rows are spread over the threads that share its number
   float4 *share = reinterpret_cast<float4 *>(ring);
-  share[thread] = make_float4(dD.x, dD.y, dbias.x, dbias.y);
+  share[thread] = make_float4(total_D.x, total_D.y, total_bias.x, total_bias.y);
   asm volatile("bar.sync 1, %0;" ::"n"(HT) : "memory");
   if (thread < CP) {
     float4 v = share[thread];

@@ -557,3 +557,23 @@ def test_convolution_sums_of_many_rows(cuda_device, C):
     for name, ref in (("dweight", want), ("dbias", dyd.sum(0))):
         error = float((got[name].double() - ref).norm() / ref.norm())
         assert error <= bound, (name, error, bound)
+
+
+@pytest.mark.parametrize("lengths", [[65536], [2000] * 32])
+def test_scan_sums_of_many_rows(cuda_device, lengths):
+    """dD is the sum of products over all rows.  A thread takes every eighth row: 32 products, these sums over its sequences, then
+    eight threads' and the workers' (bound as above; one running sum over the thread's rows: 1.6e-6 and 4.7e-7)."""
+    dev, T, C, S = cuda_device, 65536, 160, 4  # (a group per channel: CTAs enough for whole sequences)
+    N = len(lengths)
+    assert pkg.gdp_scan_forward_workspace_bytes(sum(lengths), N, C, S, C) == 0
+    T = sum(lengths)
+    g = torch.Generator(dev).manual_seed(1)
+    x, dy, dt, B, Cm = (torch.randn(s, generator=g, device=dev) for s in ((T, C), (T, C), (T, C), (T, C, S), (T, C, S)))
+    A, D, cu = -torch.ones((C, S), device=dev), torch.ones(C, device=dev), _cu(lengths, dev)
+    kept = pkg.selective_scan(x, dt, A, B, Cm, cu, D=D, save_states=True)[1]
+    got = pkg.selective_scan_backward(x, dt, A, B, Cm, dy, cu, kept, D=D)["dD"]
+    want = (x.double() * dy.double()).sum(0)
+    each = -(-N // -(-16 * _sms(dev) // C))  # sequences of a worker
+    bound = R.U * math.sqrt((32 + each * max(lengths) / 256 + each + 8 + N) / 6)
+    error = float((got.double() - want).norm() / want.norm())
+    assert error <= bound, (error, bound)
