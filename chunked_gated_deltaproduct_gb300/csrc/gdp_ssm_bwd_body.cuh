@@ -102,12 +102,12 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
       n[k] = ch + k < cn ? states : 0;
       float v[kQ];
 #pragma unroll
-      for (int q = 0; q < kQ; ++q) v[q] = q < n[k] ? p.A[mine + k * p.S + q] * kLog2e : 0.f;
+      for (int q = 0; q < kQ; ++q) v[q] = q < n[k] ? p.A[mine + k * p.S + q] * kLog2e : kNoState;
       A[k][0] = make_float2(v[0], v[1]);
       A[k][1] = make_float2(v[2], v[3]);
       totals[k * RT + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    // padded states and their gradients stay zero, whatever the inputs and the decays are (infinite ones too)
+    // padded states stay zero, whatever the inputs and the decays are, and so do their gradients (kNoState)
     auto real = [&](float2 v, int q) { return FULL ? v : make_float2(2 * q < states ? v.x : 0.f, 2 * q + 1 < states ? v.y : 0.f); };
     auto pairs = [](float4 v, float2 (&o)[2]) {
       o[0] = make_float2(v.x, v.y);
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / 2, kSsmBackward) gdp_
                   sB[q] = c ? fma2(H, ex, sB[q]) : mul2(H, ex);
                   sC[q] = c ? fma2(gg, h[c][q], sC[q]) : mul2(gg, h[c][q]);
                   uu = q ? fma2(H, Bv[q], uu) : mul2(H, Bv[q]);
-                  back[c][q] = real(mul2(H, decay[w][c][q]), q);
+                  back[c][q] = mul2(H, decay[w][c][q]);
                   const float2 x = mul2(back[c][q], before[w][c][q]);
                   vv = q ? fma2(x, A[c][q], vv) : mul2(x, A[c][q]);
                   dA[c][q] = fma2(x, ee, dA[c][q]);

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kSsmFeed + kSsmThreads / CPT, CPT == 1 ? 1 : k
       h[k][0] = make_float2(v[0], v[1]);
       h[k][1] = make_float2(v[2], v[3]);
 #pragma unroll
-      for (int q = 0; q < kQ; ++q) v[q] = q < n[k] ? p.A[mine + k * p.S + q] * kLog2e : 0.f;  // (none)
+      for (int q = 0; q < kQ; ++q) v[q] = q < n[k] ? p.A[mine + k * p.S + q] * kLog2e : kNoState;
       A[k][0] = make_float2(v[0], v[1]);
       A[k][1] = make_float2(v[2], v[3]);
     }

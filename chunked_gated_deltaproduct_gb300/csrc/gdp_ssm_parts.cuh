@@ -67,6 +67,8 @@ __device__ __forceinline__ float2 softplus2(float2 v) {
 }
 __device__ __forceinline__ float softplus(float v) { return softplus2(make_float2(v, v)).x; }
 
+// A of a state that there is none of: every finite step leaves its decay finite (at most 16), so that zero stays zero.
+constexpr float kNoState = -0x1p-126f;
 // e^(e A), the exponent in base 2 (A comes times log2 e).  The hardware's exponential is low on average, in 2^-24 of the result
 // by 0.1 for exponents above -2^-8, 0.3 to 0.45 down to -1/2 and 0.8 below -1, and a state that remembers n tokens is off
 // by n times that, its gradients again.  So the exponent is raised by what makes 0.15 of it: more would take the first of
