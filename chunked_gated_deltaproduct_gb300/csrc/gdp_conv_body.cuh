@@ -4,9 +4,10 @@
 // registers, so that every row is read once (a run's first W - 1 rows twice).  Where a sequence begins, the
 // window is that of its incoming state.
 //
-// 65536 x 4096 bf16, 4 taps, SiLU: forward 169 us, 6.35 TB/s, bound by memory (rows asked for only when they are needed: 389 us;
-// by a double buffer of registers: 389 too); backward 316 us, 5.1 TB/s, bound by the latency of 77 instructions a row and thread at
-// 16 warps per SM.  One token for 64 x 4096: 2.9 us on the device, a launch's latency and three loads' behind one another.
+// 65536 x 4096 bf16, 4 taps, SiLU: forward 168 us, 6.35 TB/s, bound by memory (rows asked for only when they are needed: 389 us;
+// by a double buffer of registers: 389 too); backward 315 us, 5.1 TB/s, bound by the latency of 77 instructions a row and thread at
+// 16 warps per SM; f16 172 and 332 (with the column sums), 32768 rows of fp32 166 and 284.  One token for 64 x 4096: 2.9 us on the
+// device, a launch's latency and three loads' behind one another (512 x 4096: 15 us a call).
 #pragma once
 
 #include "gdp_conv.cuh"

@@ -8,8 +8,9 @@
 // too small, and two rows side by side in the forward pass, which share their sums' barriers.
 //
 // 65536 x 4096 bf16 with gate, scale and both weights, fp32 stream: forward 728 us, 5.2 TB/s (weights by way of L1, one row at a
-// time: 858); backward 1313 us, 4.5 TB/s (weights by way of L1: 1763), bound by the latency of a row's two sums at 16 warps per SM.
-// Rows of no 16-byte alignment go by elements: 1421 x 1601 f16 in 11.6 us, where its bytes take 4.0.
+// time: 858); backward 1300 us, 4.5 TB/s (weights by way of L1: 1763), bound by the latency of a row's two sums at 16 warps per SM.
+// 32768 x 4096 with an fp32 stream: f16 rows 364 and 665 us, fp32 rows 628 (5.1 TB/s) and 1137 (4.2).  Rows of no 16-byte alignment
+// go by elements: 1421 x 1601 f16 in 11.7 us, where its bytes take 4.0.
 #pragma once
 
 #include "gdp_resnorm.cuh"

@@ -15,7 +15,7 @@ namespace layer {
 // running warps instead: training step of 8 x 4096 x 2048: 3.17 against 2.54 ms).
 //
 // Bound as the forward pass is, by few warps with dependent work (430 instructions a token of 32 channels, issue slots 36 %
-// busy): 8 x 4096 x 2048 x 16 bf16 in 1880 us, dB and dC's parts added up in 52 more, dA's, dD's and ddt_bias's in 13.  Two CTAs
+// busy): 8 x 4096 x 2048 x 16 bf16 in 1894 us, dB and dC's parts added up in 52 more, dA's, dD's and ddt_bias's in 13.  Two CTAs
 // on an SM are what its shared memory is cut to: one takes 1.6 times as long (16384 x 2048 x 16, gated, bf16 with fp32 dt: 1771
 // us by one, 1046 by two; fp32 without a gate 1497 and 886; gated fp32 of 16 states is by one, 1707 us).
 
