@@ -1,5 +1,7 @@
 // gdp_recurrence.cu -- the gated linear recurrence (gdp_layer.h): C entries, argument checks, and the
 // one-token step.  The scans over packed sequences are in gdp_rec_fwd_body.cuh and gdp_rec_bwd_body.cuh.
+#include <atomic>
+
 #include "gdp_rec_scan.cuh"
 
 namespace gdp {
@@ -183,11 +185,15 @@ gdp_status dispatch(int x_type, int g_type, P &p, int gate, cudaStream_t stream)
 }  // namespace
 
 int sm_count() {
-  static int counts[64] = {};
+  static std::atomic<int> counts[64];  // (host threads may ask at once)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-  if (counts[dev] == 0 && cudaDeviceGetAttribute(&counts[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
-  return counts[dev];
+  int n = counts[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+    counts[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 }  // namespace layer
