@@ -15,10 +15,10 @@ namespace layer {
 // in twice the warps).
 //
 // Bound by the running warps' latency and issue slots.  Two channels a lane (several CTAs on an SM): 41 instructions a running
-// warp and token for its 256 states, eight a lane, of which 16 are on packed pairs and 8 are exponentials, at 8 lanes a clock; one channel a
-// lane (a CTA alone on its SM): 8 and 4 for half the states, in twice the warps.  65536 x 4096 x 16 gated, bf16, one channel a
-// lane: 2209 us, 34 ns a token of 128 CTAs (its exponentials alone would take 452 us, its bytes 317); two: 64 packed requests, 84086 x 2048 x 16: 959 us at three CTAs per SM; 8 x
-// 4096 x 2048 x 16 with the chunk states: 495 us.
+// warp and token for its 256 states, eight a lane, of which 16 are on packed pairs and 8 are exponentials, at 8 lanes a
+// clock; 64 packed requests, 84086 x 2048 x 16 gated, bf16: 959 us at three CTAs per SM; 8 x 4096 x 2048 x 16 with the chunk
+// states: 495 us.  One channel a lane (a CTA alone on its SM): 8 and 4 for half the states, in twice the warps; 65536 x 4096 x
+// 16: 2209 us, 34 ns a token of 128 CTAs (its exponentials alone would take 452 us, its bytes 317).
 
 // The raw rows of a tile in shared memory.
 template <typename T, int CH, int SP>
